@@ -25,7 +25,10 @@ EXPORTED = ["fftconv_plan_query", "fftconv_plan_create", "fftconv_plan_destroy",
             "fftconv_partial_scratch_bytes", "fftconv_forward_partial", "fftconv_circular_scratch_bytes",
             "fftconv_forward_circular", "fftconv_selftest_wait", "fftconv_plan_create_sparse",
             "fftconv_plan_get_band", "fftconv_sparse_query", "fftconv_circular_query",
-            "fftconv_plan_create_circular",
+            "fftconv_plan_create_circular", "fftconv_delta_create", "fftconv_delta_destroy",
+            "fftconv_delta_status", "fftconv_delta_saved_bytes", "fftconv_delta_scratch_bytes",
+            "fftconv_delta_forward", "fftconv_delta_backward", "fftconv_delta_step", "fftconv_qknorm_forward",
+            "fftconv_qknorm_scratch_bytes", "fftconv_qknorm_backward",
             "fftconv_device_status", "fftconv_status_string", "fftconv_version"]
 
 
@@ -45,6 +48,27 @@ class PlanInfo(ctypes.Structure):
                 "factors": list(self.factors[: self.order]), "path": self.path, "dtype": self.dtype,
                 "kf_bytes_per_channel": self.kf_bytes_per_channel,
                 "workspace_bytes_per_row": self.workspace_bytes_per_row}
+
+
+class View(ctypes.Structure):
+    """fftconv_view_t: a [B, T, H, D] (or [B, T, H]) tensor by its strides."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
+
+
+class DeltaArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hk", ctypes.c_int64), ("Hv", ctypes.c_int64),
+                ("nseq", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("q", View), ("k", View), ("v", View), ("g", View), ("beta", View)]
+
+
+class QKNormArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("norm", ctypes.c_int32), ("D", ctypes.c_int32), ("R", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64),
+                ("q", View), ("k", View), ("wq", ctypes.c_void_p), ("wk", ctypes.c_void_p),
+                ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("table_rows", ctypes.c_int64),
+                ("positions", ctypes.c_void_p)]
 
 
 _lib = None
@@ -98,6 +122,21 @@ def lib(auto_build: bool = True):
         L.fftconv_circular_scratch_bytes.restype = sz
         L.fftconv_forward_circular.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, vp, sz, vp]
         L.fftconv_selftest_wait.argtypes = [vp, ctypes.c_int, vp]
+        da, qa, cint = ctypes.POINTER(DeltaArgs), ctypes.POINTER(QKNormArgs), ctypes.c_int
+        L.fftconv_delta_create.argtypes = [ctypes.POINTER(vp), cint, cint, cint]
+        L.fftconv_delta_destroy.argtypes = [vp]
+        L.fftconv_delta_status.argtypes = [vp, vp, ctypes.POINTER(cint)]
+        L.fftconv_delta_saved_bytes.argtypes = [vp, i64, i64, i64, i64]
+        L.fftconv_delta_saved_bytes.restype = sz
+        L.fftconv_delta_scratch_bytes.argtypes = [vp, i64, i64, i64, i64, i64, cint]
+        L.fftconv_delta_scratch_bytes.restype = sz
+        L.fftconv_delta_forward.argtypes = [vp, da, vp, View, vp, vp, vp, sz, vp]
+        L.fftconv_delta_backward.argtypes = [vp, da, View, vp, vp, View, View, View, View, View, vp, vp, sz, vp]
+        L.fftconv_delta_step.argtypes = [vp, da, vp, vp, i64, vp, View, vp]
+        L.fftconv_qknorm_forward.argtypes = [qa, View, View, vp]
+        L.fftconv_qknorm_scratch_bytes.argtypes = [qa]
+        L.fftconv_qknorm_scratch_bytes.restype = sz
+        L.fftconv_qknorm_backward.argtypes = [qa, View, View, View, View, vp, vp, vp, sz, vp]
         L.fftconv_device_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_int)]
         L.fftconv_status_string.argtypes = [ctypes.c_int]
         L.fftconv_status_string.restype = ctypes.c_char_p
@@ -365,3 +404,221 @@ class Plan:
 
 def status_string(code: int) -> str:
     return lib().fftconv_status_string(code).decode()
+
+
+# ---- token mixers with a state: strided token-major tensors [B, T, H, D]
+
+def _view(t, what: str, dtype, dims: int) -> View:
+    """A tensor's view (None: an empty one), checked against dtype and rank."""
+    if t is None:
+        return View(None, 0, 0, 0)
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dtype != dtype or t.dim() != dims:
+        raise ValueError(f"{what} must be a {dtype} tensor of {dims} dimensions")
+    if dims == 4 and t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return View(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def _dense(t, what: str, dtype, shape) -> Optional[int]:
+    """The address of a contiguous CUDA tensor of the given shape (None: NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _on(stream):
+    """Allocations made inside belong to the stream that the call runs on."""
+    import torch
+    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream())
+
+
+class DeltaRule:
+    """The gated delta rule for head sizes Dk, Dv (64 or 128) and one dtype:
+
+        S~ = exp(g_t) S;  u = beta_t (v_t - S~^T k_t);  S = S~ + k_t u^T;  o_t = scale S^T q_t
+
+    q, k: [B, T, Hk, Dk]; v: [B, T, Hv, Dv]; g (log decay), beta: [B, T, Hv];
+    Hv a multiple of Hk.  States: float32 [sequences, Hv, Dk, Dv].  offsets:
+    int32 [n + 1] on the GPU for n sequences packed into one row (B = 1).
+    scale defaults to Dk ** -0.5."""
+
+    def __init__(self, Dk: int, Dv: int, dtype):
+        self.Dk, self.Dv, self.torch_dtype = int(Dk), int(Dv), dtype
+        h = ctypes.c_void_p()
+        _check(lib().fftconv_delta_create(ctypes.byref(h), self.Dk, self.Dv, _dtype_code(dtype)),
+               "fftconv_delta_create")
+        self._h = h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().fftconv_delta_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _args(self, q, k, v, g, beta, offsets, scale) -> DeltaArgs:
+        import torch
+        dt = self.torch_dtype
+        a = DeltaArgs()
+        a.q, a.k, a.v = _view(q, "q", dt, 4), _view(k, "k", dt, 4), _view(v, "v", dt, 4)
+        a.g, a.beta = _view(g, "g", dt, 3), _view(beta, "beta", dt, 3)
+        a.B, a.T, a.Hk, a.Hv = q.shape[0], q.shape[1], q.shape[2], v.shape[2]
+        if tuple(k.shape) != tuple(q.shape) or q.shape[3] != self.Dk or tuple(v.shape) != (a.B, a.T, a.Hv, self.Dv):
+            raise ValueError("q, k must be [B, T, Hk, Dk] and v [B, T, Hv, Dv]")
+        if tuple(g.shape) != (a.B, a.T, a.Hv) or tuple(beta.shape) != (a.B, a.T, a.Hv):
+            raise ValueError("g and beta must be [B, T, Hv]")
+        a.nseq = a.B
+        if offsets is not None:
+            if offsets.dim() != 1 or offsets.numel() < 1:
+                raise ValueError("offsets must be [n + 1]")
+            a.nseq = offsets.numel() - 1
+            a.offsets = _dense(offsets, "offsets", torch.int32, offsets.shape)
+        a.scale = self.Dk ** -0.5 if scale is None else float(scale)
+        return a
+
+    def _scratch(self, a, backward, device):
+        import torch
+        n = int(lib().fftconv_delta_scratch_bytes(self._h, a.B, a.T, a.Hk, a.Hv, a.nseq, int(backward)))
+        return (torch.empty(n, dtype=torch.uint8, device=device) if n else None), n
+
+    def forward(self, q, k, v, g, beta, state=None, offsets=None, scale=None, save=False, stream=None):
+        """Whole sequences from `state` (None: zero) -> (o, final states), and
+        with save=True also what backward needs: (o, final states, saved)."""
+        import torch
+        a = self._args(q, k, v, g, beta, offsets, scale)
+        shape = (a.nseq, a.Hv, self.Dk, self.Dv)
+        sin = _dense(state, "state", torch.float32, shape)
+        with _on(stream):
+            o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            if offsets is not None:
+                o.zero_()  # tokens outside every sequence
+            out = torch.empty(shape, dtype=torch.float32, device=v.device)
+            saved = None
+            if save:
+                n = int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq))
+                saved = torch.empty(n, dtype=torch.uint8, device=v.device)
+            scratch, n = self._scratch(a, False, v.device)
+            _check(lib().fftconv_delta_forward(self._h, ctypes.byref(a), sin, _view(o, "o", v.dtype, 4), _ptr(out),
+                                               _ptr(saved), _ptr(scratch), n, _stream(stream)),
+                   "fftconv_delta_forward")
+        return (o, out, saved) if save else (o, out)
+
+    def backward(self, do, q, k, v, g, beta, saved, dstate=None, offsets=None, scale=None, stream=None):
+        """Gradients (dq, dk, dv, dg, dbeta, gradient of the initial states)
+        from do [B, T, Hv, Dv] and, if the final states were used, dstate;
+        `saved` and the other arguments as in forward."""
+        import torch
+        a = self._args(q, k, v, g, beta, offsets, scale)
+        dt = self.torch_dtype
+        shape = (a.nseq, a.Hv, self.Dk, self.Dv)
+        dsin = _dense(dstate, "dstate", torch.float32, shape)
+        if tuple(do.shape) != tuple(v.shape):
+            raise ValueError("do must be [B, T, Hv, Dv]")
+        n = int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq))
+        sv = _dense(saved, "saved", torch.uint8, (n,))
+        with _on(stream):
+            dq, dk, dv, dg, dbeta = (torch.empty(t.shape, dtype=dt, device=t.device) for t in (q, k, v, g, beta))
+            dst = torch.empty(shape, dtype=torch.float32, device=v.device)
+            scratch, n = self._scratch(a, True, v.device)
+            _check(lib().fftconv_delta_backward(
+                self._h, ctypes.byref(a), _view(do, "do", dt, 4), dsin, sv, _view(dq, "dq", dt, 4),
+                _view(dk, "dk", dt, 4), _view(dv, "dv", dt, 4), _view(dg, "dg", dt, 3), _view(dbeta, "dbeta", dt, 3),
+                _ptr(dst), _ptr(scratch), n, _stream(stream)), "fftconv_delta_backward")
+        return dq, dk, dv, dg, dbeta, dst
+
+    def step(self, q, k, v, g, beta, state, state_out=None, slots=None, scale=None, stream=None):
+        """The recurrent form: B rows of a few tokens, row b against
+        state[slots[b]] (slots: int32 [B] on the GPU, distinct; None: state[b])
+        -> o.  The updated states go to state_out, by default back to state."""
+        import torch
+        a = self._args(q, k, v, g, beta, None, scale)
+        shape = (state.shape[0], a.Hv, self.Dk, self.Dv)
+        sin = _dense(state, "state", torch.float32, shape)
+        sout = sin if state_out is None else _dense(state_out, "state_out", torch.float32, shape)
+        sl = _dense(slots, "slots", torch.int32, (a.B,))
+        with _on(stream):
+            o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            _check(lib().fftconv_delta_step(self._h, ctypes.byref(a), sin, sout, shape[0], sl,
+                                            _view(o, "o", v.dtype, 4), _stream(stream)), "fftconv_delta_step")
+        return o
+
+    def device_status(self, stream=None) -> int:
+        v = ctypes.c_int()
+        _check(lib().fftconv_delta_status(self._h, _stream(stream), ctypes.byref(v)), "fftconv_delta_status")
+        return v.value
+
+
+class QKNorm:
+    """Norm of queries and keys for each head, with the position rotation of
+    the first `rotary` features in the same pass.  norm: "rms" or "l2"."""
+
+    def __init__(self, D: int, dtype, norm: str = "rms", eps: float = 1e-6, rotary: int = 0, interleaved: bool = False):
+        if norm not in ("rms", "l2"):
+            raise ValueError('norm must be "rms" or "l2"')
+        self.D, self.torch_dtype, self.norm, self.eps = int(D), dtype, norm, float(eps)
+        self.rotary, self.interleaved = int(rotary), bool(interleaved)
+        self._code = _dtype_code(dtype)
+
+    def _args(self, q, k, wq, wk, cos, sin, positions) -> QKNormArgs:
+        import torch
+        a = QKNormArgs()
+        a.dtype, a.norm, a.D, a.R = self._code, int(self.norm == "l2"), self.D, self.rotary
+        a.interleaved, a.eps = int(self.interleaved), self.eps
+        a.q, a.k = _view(q, "q", self.torch_dtype, 4), _view(k, "k", self.torch_dtype, 4)
+        a.B, a.T, a.Hq, a.Hk = q.shape[0], q.shape[1], q.shape[2], k.shape[2]
+        if q.shape[3] != self.D or tuple(k.shape) != (a.B, a.T, a.Hk, self.D):
+            raise ValueError("q must be [B, T, Hq, D] and k [B, T, Hk, D]")
+        a.wq, a.wk = _dense(wq, "wq", torch.float32, (self.D,)), _dense(wk, "wk", torch.float32, (self.D,))
+        if self.rotary:
+            if cos is None or sin is None:
+                raise ValueError("a rotation needs cos and sin")
+            shape = (cos.shape[0], self.rotary // 2)
+            a.cos, a.sin = _dense(cos, "cos", torch.float32, shape), _dense(sin, "sin", torch.float32, shape)
+            a.table_rows = shape[0]
+            a.positions = _dense(positions, "positions", torch.int32, (a.B, a.T))
+        return a
+
+    def forward(self, q, k, wq=None, wk=None, cos=None, sin=None, positions=None, qo=None, ko=None, stream=None):
+        """q: [B, T, Hq, D], k: [B, T, Hk, D] -> the normed and rotated (q, k).
+        wq, wk: float32 [D] or None (ones); cos, sin: float32 [rows, rotary/2];
+        positions: int32 [B, T] (None: the token's index).  qo, ko: where to
+        write (q and k themselves are allowed)."""
+        import torch
+        a = self._args(q, k, wq, wk, cos, sin, positions)
+        with _on(stream):
+            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device) if qo is None else qo
+            ko = torch.empty(k.shape, dtype=k.dtype, device=k.device) if ko is None else ko
+            if qo.shape != q.shape or ko.shape != k.shape:
+                raise ValueError("qo and ko have the shapes of q and k")
+            _check(lib().fftconv_qknorm_forward(ctypes.byref(a), _view(qo, "qo", q.dtype, 4),
+                                                _view(ko, "ko", q.dtype, 4), _stream(stream)),
+                   "fftconv_qknorm_forward")
+        return qo, ko
+
+    def backward(self, dqo, dko, q, k, wq=None, wk=None, cos=None, sin=None, positions=None, stream=None):
+        """Gradients (dq, dk, dwq, dwk) from those of forward's outputs; dwq
+        (dwk) is None where wq (wk) is."""
+        import torch
+        a = self._args(q, k, wq, wk, cos, sin, positions)
+        if dqo.shape != q.shape or dko.shape != k.shape:
+            raise ValueError("dqo and dko have the shapes of q and k")
+        dt = self.torch_dtype
+        with _on(stream):
+            dq, dk = (torch.empty(t.shape, dtype=dt, device=t.device) for t in (q, k))
+            dwq, dwk = (None if w is None else torch.empty(self.D, dtype=torch.float32, device=q.device)
+                        for w in (wq, wk))
+            n = int(lib().fftconv_qknorm_scratch_bytes(ctypes.byref(a))) if (wq is not None or wk is not None) else 0
+            scratch = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+            _check(lib().fftconv_qknorm_backward(ctypes.byref(a), _view(dqo, "dqo", dt, 4), _view(dko, "dko", dt, 4),
+                                                 _view(dq, "dq", dt, 4), _view(dk, "dk", dt, 4), _ptr(dwq),
+                                                 _ptr(dwk), _ptr(scratch), n, _stream(stream)),
+                   "fftconv_qknorm_backward")
+        return dq, dk, dwq, dwk

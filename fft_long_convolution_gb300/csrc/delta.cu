@@ -1,0 +1,608 @@
+// Gated delta rule: C entry points and the token-by-token kernels.
+#include "delta.h"
+
+#include <new>
+
+namespace fftconv {
+namespace {
+
+// ------------------------------------------------------------ token by token
+//
+// S~ = exp(g) S; u = beta (v - S~^T k); S = S~ + k u^T; o = scale S^T q.
+// With o = scale (S~^T q + (q.k) u) a token needs one round of sums over Dk:
+// S~^T k, S~^T q and q.k together, then the rank-one update.
+//
+// A CTA of 128 threads keeps a slice of 32 of the Dv columns of one state in
+// registers: lane % 8 owns 4 columns (16-byte accesses, 128 bytes per row of
+// the slice), the 16 groups of 8 lanes own Dk / 16 rows each.  The sums go over
+// 4 groups by shuffles and over the 4 warps through shared memory, double
+// buffered so that a token costs one barrier.  The state is read and written
+// once per call: for one token that is all the traffic that counts, so the
+// bound is HBM bandwidth for large batches (Dk / 16 independent 16-byte loads
+// in flight per thread) and latency for a few rows.
+struct TokenArgs {
+    DeltaArgs d;
+    const float* sin;   // states [.][Hv][Dk][Dv] or null (zero)
+    float* sout;        // or null
+    const int32_t* slots;
+    int64_t nslots;     // step: size of the pool
+    float* saved;       // forward: states at the chunk starts (float32), or null
+    int step;
+};
+
+template <int DT, int DK, int DV>
+__global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
+    constexpr int RP = DK / 16;
+    __shared__ float4 red[2][4][8][2];
+    __shared__ float redqk[2][4];
+    const DeltaArgs& d = a.d;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int cg = lane % 8, rg = warp * 4 + lane / 8;
+    const int h = blockIdx.y, col = blockIdx.z * 32 + cg * 4, hk = h / d.group;
+    const int i = blockIdx.x;
+    Seq s = locate(d.offsets, d.T, i);
+    int64_t si = i;
+    bool live = true;
+    if (a.step) {
+        si = a.slots ? a.slots[i] : i;
+        live = si >= 0 && si < a.nslots;
+    }
+    const uint16_t* kp = reinterpret_cast<const uint16_t*>(d.k.p) + s.row * d.k.b + s.start * d.k.t + hk * d.k.h + rg * RP;
+    const uint16_t* qp = reinterpret_cast<const uint16_t*>(d.q.p) + s.row * d.q.b + s.start * d.q.t + hk * d.q.h + rg * RP;
+    const uint16_t* vp = reinterpret_cast<const uint16_t*>(d.v.p) + s.row * d.v.b + s.start * d.v.t + h * d.v.h + col;
+    uint16_t* op = reinterpret_cast<uint16_t*>(d.o.p) + s.row * d.o.b + s.start * d.o.t + h * d.o.h + col;
+    const int64_t go = s.row * d.g.b + s.start * d.g.t + h * d.g.h;
+    const int64_t bo = s.row * d.beta.b + s.start * d.beta.t + h * d.beta.h;
+    if (!live) {
+        if (rg == 0)
+            for (int64_t t = 0; t < s.len; ++t) *reinterpret_cast<uint2*>(op + t * d.o.t) = make_uint2(0, 0);
+        return;
+    }
+    const int64_t sbase = ((si * d.Hv + h) * DK + rg * RP) * DV + col;
+    float4 S[RP];
+    #pragma unroll
+    for (int r = 0; r < RP; ++r)
+        S[r] = a.sin ? *reinterpret_cast<const float4*>(a.sin + sbase + r * DV) : make_float4(0, 0, 0, 0);
+    for (int64_t t = 0; t < s.len; ++t) {
+        if (a.saved && (t % kChunk) == 0) {
+            float* p = a.saved + (((s.slot + t / kChunk) * d.Hv + h) * DK + rg * RP) * DV + col;
+            #pragma unroll
+            for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(p + r * DV) = S[r];
+        }
+        float k[RP], q[RP], v[4];
+        #pragma unroll
+        for (int r = 0; r < RP; r += 4) {
+            const uint2 uk = *reinterpret_cast<const uint2*>(kp + t * d.k.t + r);
+            const uint2 uq = *reinterpret_cast<const uint2*>(qp + t * d.q.t + r);
+            const cpx k0 = Op<DT>::unpack(uk.x), k1 = Op<DT>::unpack(uk.y);
+            const cpx q0 = Op<DT>::unpack(uq.x), q1 = Op<DT>::unpack(uq.y);
+            k[r] = k0.r; k[r + 1] = k0.i; k[r + 2] = k1.r; k[r + 3] = k1.i;
+            q[r] = q0.r; q[r + 1] = q0.i; q[r + 2] = q1.r; q[r + 3] = q1.i;
+        }
+        {
+            const uint2 uv = *reinterpret_cast<const uint2*>(vp + t * d.v.t);
+            const cpx v0 = Op<DT>::unpack(uv.x), v1 = Op<DT>::unpack(uv.y);
+            v[0] = v0.r; v[1] = v0.i; v[2] = v1.r; v[3] = v1.i;
+        }
+        const float al = expf(log_decay(load16<DT>(d.g, go + t * d.g.t)));
+        const float be = load16<DT>(d.beta, bo + t * d.beta.t);
+        float ks[4] = {}, qs[4] = {}, qk = 0.0f;
+        #pragma unroll
+        for (int r = 0; r < RP; ++r) {
+            S[r].x *= al; S[r].y *= al; S[r].z *= al; S[r].w *= al;
+            ks[0] = fmaf(k[r], S[r].x, ks[0]); ks[1] = fmaf(k[r], S[r].y, ks[1]);
+            ks[2] = fmaf(k[r], S[r].z, ks[2]); ks[3] = fmaf(k[r], S[r].w, ks[3]);
+            qs[0] = fmaf(q[r], S[r].x, qs[0]); qs[1] = fmaf(q[r], S[r].y, qs[1]);
+            qs[2] = fmaf(q[r], S[r].z, qs[2]); qs[3] = fmaf(q[r], S[r].w, qs[3]);
+            qk = fmaf(q[r], k[r], qk);
+        }
+        #pragma unroll
+        for (int o = 8; o < 32; o <<= 1) {
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                ks[j] += __shfl_xor_sync(0xffffffffu, ks[j], o);
+                qs[j] += __shfl_xor_sync(0xffffffffu, qs[j], o);
+            }
+            qk += __shfl_xor_sync(0xffffffffu, qk, o);
+        }
+        const int pb = int(t & 1);
+        if (lane < 8) {
+            red[pb][warp][lane][0] = make_float4(ks[0], ks[1], ks[2], ks[3]);
+            red[pb][warp][lane][1] = make_float4(qs[0], qs[1], qs[2], qs[3]);
+            if (lane == 0) redqk[pb][warp] = qk;
+        }
+        __syncthreads();
+        float4 K = red[pb][0][cg][0], Q = red[pb][0][cg][1];
+        float QK = redqk[pb][0];
+        #pragma unroll
+        for (int w = 1; w < 4; ++w) {
+            const float4 x = red[pb][w][cg][0], y = red[pb][w][cg][1];
+            K.x += x.x; K.y += x.y; K.z += x.z; K.w += x.w;
+            Q.x += y.x; Q.y += y.y; Q.z += y.z; Q.w += y.w;
+            QK += redqk[pb][w];
+        }
+        const float4 u = make_float4(be * (v[0] - K.x), be * (v[1] - K.y), be * (v[2] - K.z), be * (v[3] - K.w));
+        #pragma unroll
+        for (int r = 0; r < RP; ++r) {
+            S[r].x = fmaf(k[r], u.x, S[r].x); S[r].y = fmaf(k[r], u.y, S[r].y);
+            S[r].z = fmaf(k[r], u.z, S[r].z); S[r].w = fmaf(k[r], u.w, S[r].w);
+        }
+        if (rg == 0) {
+            const float sc = d.scale;
+            *reinterpret_cast<uint2*>(op + t * d.o.t) =
+                make_uint2(Op<DT>::pack(sc * fmaf(QK, u.x, Q.x), sc * fmaf(QK, u.y, Q.y)),
+                           Op<DT>::pack(sc * fmaf(QK, u.z, Q.z), sc * fmaf(QK, u.w, Q.w)));
+        }
+    }
+    if (a.sout) {
+        #pragma unroll
+        for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(a.sout + sbase + r * DV) = S[r];
+    }
+}
+
+// ------------------------------------------------------------ gradients, token by token
+//
+// Reverse recurrence with the states of a chunk recomputed from the saved
+// state at its start:
+//   d1 = dS_t + scale q do^T;  dq = scale S_t do;  du = d1^T k
+//   dk = d1 u - S~ (beta du);  dv = beta du;  dbeta = du.(v - S~^T k)
+//   d2 = d1 - k (beta du)^T;  dg = <d2, S~>;  dS_(t-1) = exp(g) d2
+// One CTA of 256 threads per sequence and value head, S~ and dS in shared
+// memory, everything float32: the simple form.
+struct GradArgs {
+    DeltaArgs d;
+    View dout, dv, dg, dbeta;
+    const float* dsout;  // gradient of the final states, or null
+    float* dsin;         // gradient of the initial states, or null
+    const float* saved;
+    float* states;       // [CTA][64][DK*DV]: the states before each token of a chunk
+    float *dqh, *dkh;    // [B T][Hv][DK] per value head
+};
+
+template <int DT, int DK, int DV>
+__global__ void __launch_bounds__(256) token_grad_kernel(const GradArgs a) {
+    extern __shared__ float sm[];
+    float* S = sm;               // S~ of the current token
+    float* R = S + DK * DV;      // dS
+    float *kq = R + DK * DV, *qq = kq + DK, *vv = qq + DK, *dd = vv + DV, *uu = dd + DV, *du = uu + DV,
+          *part = du + DV;       // [256]
+    const DeltaArgs& d = a.d;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int i = blockIdx.x, h = blockIdx.y, hk = h / d.group;
+    const Seq s = locate(d.offsets, d.T, i);
+    float* st = a.states + (int64_t(i) * d.Hv + h) * kChunk * DK * DV;
+    const int64_t sb = (int64_t(i) * d.Hv + h) * DK * DV;
+    const int c = tid % DV, p0 = tid / DV;
+    constexpr int NP = 256 / DV;
+    for (int x = tid; x < DK * DV; x += 256) R[x] = a.dsout ? a.dsout[sb + x] : 0.0f;
+    const int64_t nch = (s.len + kChunk - 1) / kChunk;
+    auto load = [&](int64_t t) {  // token t of the sequence; returns its decay and beta through part
+        const int64_t tt = s.start + t;
+        for (int x = tid; x < DK; x += 256) {
+            kq[x] = load16<DT>(d.k, s.row * d.k.b + tt * d.k.t + hk * d.k.h + x);
+            qq[x] = load16<DT>(d.q, s.row * d.q.b + tt * d.q.t + hk * d.q.h + x);
+        }
+        for (int x = tid; x < DV; x += 256) {
+            vv[x] = load16<DT>(d.v, s.row * d.v.b + tt * d.v.t + h * d.v.h + x);
+            dd[x] = load16<DT>(a.dout, s.row * a.dout.b + tt * a.dout.t + h * a.dout.h + x);
+        }
+    };
+    // sums over the rows: out[c] = sum_r vec[r] * M[r][c]
+    auto colsum = [&](const float* vec, const float* M) {
+        float v = 0.0f;
+        for (int r = p0; r < DK; r += NP) v = fmaf(vec[r], M[r * DV + c], v);
+        part[tid] = v;
+        __syncthreads();
+        v = 0.0f;
+        for (int j = 0; j < NP; ++j) v += part[j * DV + c];
+        __syncthreads();
+        return v;
+    };
+    for (int64_t ch = nch - 1; ch >= 0; --ch) {
+        const int64_t t0 = ch * kChunk;
+        const int n = int(s.len - t0 < kChunk ? s.len - t0 : kChunk);
+        __syncthreads();
+        const float* sv = a.saved + ((s.slot + ch) * d.Hv + h) * DK * DV;
+        for (int x = tid; x < DK * DV; x += 256) S[x] = sv[x];
+        for (int j = 0; j < n; ++j) {
+            load(t0 + j);
+            const int64_t tt = s.start + t0 + j;
+            const float al = expf(log_decay(load16<DT>(d.g, s.row * d.g.b + tt * d.g.t + h * d.g.h)));
+            const float be = load16<DT>(d.beta, s.row * d.beta.b + tt * d.beta.t + h * d.beta.h);
+            for (int x = tid; x < DK * DV; x += 256) {
+                st[int64_t(j) * DK * DV + x] = S[x];
+                S[x] *= al;
+            }
+            __syncthreads();
+            const float u = be * (vv[c] - colsum(kq, S));
+            for (int r = p0; r < DK; r += NP) S[r * DV + c] = fmaf(kq[r], u, S[r * DV + c]);
+            __syncthreads();
+        }
+        for (int j = n - 1; j >= 0; --j) {
+            load(t0 + j);
+            const int64_t tt = s.start + t0 + j;
+            const float al = expf(log_decay(load16<DT>(d.g, s.row * d.g.b + tt * d.g.t + h * d.g.h)));
+            const float be = load16<DT>(d.beta, s.row * d.beta.b + tt * d.beta.t + h * d.beta.h);
+            __syncthreads();
+            for (int x = tid; x < DK * DV; x += 256) {
+                S[x] = al * st[int64_t(j) * DK * DV + x];
+                R[x] = fmaf(d.scale * qq[x / DV], dd[x % DV], R[x]);
+            }
+            __syncthreads();
+            const float miss = vv[c] - colsum(kq, S);
+            const float dub = colsum(kq, R);
+            if (p0 == 0) {
+                uu[c] = be * miss;
+                du[c] = dub;
+                store16<DT>(a.dv, s.row * a.dv.b + tt * a.dv.t + h * a.dv.h + c, be * dub);
+            }
+            part[tid] = p0 == 0 ? dub * miss : 0.0f;
+            __syncthreads();
+            if (warp == 0) {
+                float v = 0.0f;
+                for (int x = lane; x < 256; x += 32) v += part[x];
+                for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == 0) store16<DT>(a.dbeta, s.row * a.dbeta.b + tt * a.dbeta.t + h * a.dbeta.h, v);
+            }
+            // rows of dq and dk; dg is the sum of <d2, S~> over them
+            float dgp = 0.0f;
+            const int64_t ho = ((s.row * d.T + tt) * d.Hv + h) * DK;
+            for (int r = warp; r < DK; r += 8) {
+                float sdo = 0.0f, ru = 0.0f, sdu = 0.0f, rs = 0.0f, udo = 0.0f;
+                for (int x = lane; x < DV; x += 32) {
+                    const float sx = S[r * DV + x], rx = R[r * DV + x];
+                    sdo = fmaf(sx, dd[x], sdo);
+                    udo = fmaf(uu[x], dd[x], udo);
+                    ru = fmaf(rx, uu[x], ru);
+                    sdu = fmaf(sx, be * du[x], sdu);
+                    rs = fmaf(rx - kq[r] * be * du[x], sx, rs);
+                }
+                for (int o = 16; o; o >>= 1) {
+                    sdo += __shfl_xor_sync(0xffffffffu, sdo, o);
+                    udo += __shfl_xor_sync(0xffffffffu, udo, o);
+                    ru += __shfl_xor_sync(0xffffffffu, ru, o);
+                    sdu += __shfl_xor_sync(0xffffffffu, sdu, o);
+                    rs += __shfl_xor_sync(0xffffffffu, rs, o);
+                }
+                if (lane == 0) {
+                    a.dqh[ho + r] = d.scale * fmaf(kq[r], udo, sdo);
+                    a.dkh[ho + r] = ru - sdu;
+                }
+                dgp += rs;
+            }
+            __syncthreads();
+            if (lane == 0) part[warp] = dgp;
+            __syncthreads();
+            if (tid == 0) {
+                float v = 0.0f;
+                for (int w = 0; w < 8; ++w) v += part[w];
+                store16<DT>(a.dg, s.row * a.dg.b + tt * a.dg.t + h * a.dg.h, v);
+            }
+            for (int x = tid; x < DK * DV; x += 256) R[x] = al * (R[x] - kq[x / DV] * be * du[x % DV]);
+            __syncthreads();
+        }
+    }
+    __syncthreads();
+    if (a.dsin)
+        for (int x = tid; x < DK * DV; x += 256) a.dsin[sb + x] = R[x];
+}
+
+// dq, dk [token][Hk][DK] = the sum over a key head's value heads.
+template <int DT>
+__global__ void head_sum_kernel(const float* x, View y, int64_t B, int64_t T, int Hk, int group, int DK) {
+    const int64_t n = B * T * Hk * DK;
+    for (int64_t e = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += int64_t(gridDim.x) * blockDim.x) {
+        const int r = int(e % DK);
+        const int64_t hk = (e / DK) % Hk, tok = e / DK / Hk, b = tok / T, t = tok - b * T;
+        float v = 0.0f;
+        for (int j = 0; j < group; ++j) v += x[((tok * Hk + hk) * group + j) * DK + r];
+        store16<DT>(y, b * y.b + t * y.t + hk * y.h + r, v);
+    }
+}
+
+template <int DT>
+__global__ void zero_kernel(View y, int64_t B, int64_t T, int64_t H, int D) {
+    const int64_t n = B * T * H * D;
+    for (int64_t e = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += int64_t(gridDim.x) * blockDim.x) {
+        const int64_t r = e % D, h = (e / D) % H, tok = e / D / H, b = tok / T, t = tok - b * T;
+        store16<DT>(y, b * y.b + t * y.t + h * y.h + r, 0.0f);
+    }
+}
+
+template <typename F>
+auto pick(int dt, int dk, int dv, F&& f) {
+    if (dt == FFTCONV_F16) {
+        if (dk == 64) return dv == 64 ? f.template go<0, 64, 64>() : f.template go<0, 64, 128>();
+        return dv == 64 ? f.template go<0, 128, 64>() : f.template go<0, 128, 128>();
+    }
+    if (dk == 64) return dv == 64 ? f.template go<1, 64, 64>() : f.template go<1, 64, 128>();
+    return dv == 64 ? f.template go<1, 128, 64>() : f.template go<1, 128, 128>();
+}
+
+struct LaunchToken {
+    const TokenArgs& a;
+    cudaStream_t st;
+    template <int DT, int DK, int DV>
+    cudaError_t go() {
+        token_kernel<DT, DK, DV><<<dim3(unsigned(a.d.nseq), unsigned(a.d.Hv), DV / 32), 128, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+};
+
+struct LaunchGrad {
+    const GradArgs& a;
+    cudaStream_t st;
+    template <int DT, int DK, int DV>
+    cudaError_t go() {
+        const size_t sm = (2 * DK * DV + 2 * DK + 4 * DV + 256) * 4;
+        cudaError_t e = cudaFuncSetAttribute(token_grad_kernel<DT, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sm));
+        if (e != cudaSuccess) return e;
+        token_grad_kernel<DT, DK, DV><<<dim3(unsigned(a.d.nseq), unsigned(a.d.Hv)), 256, sm, st>>>(a);
+        return cudaGetLastError();
+    }
+};
+
+bool wrong_device(const fftconv_delta_s* p) {
+    int d = -1;
+    if (cudaGetDevice(&d) != cudaSuccess) {
+        cudaGetLastError();
+        return true;
+    }
+    return d != p->device;
+}
+
+// Sizes and input views of every call.
+fftconv_status_t take_args(const fftconv_delta_s* p, const fftconv_delta_args_t* x, DeltaArgs* a) {
+    if (!p || !x || wrong_device(p)) return FFTCONV_ERR_INVALID;
+    if (x->B < 0 || x->T < 0 || x->Hk < 0 || x->Hv < 0 || x->nseq < 0) return FFTCONV_ERR_INVALID;
+    if (x->Hk == 0 ? x->Hv != 0 : x->Hv % x->Hk != 0) return FFTCONV_ERR_INVALID;
+    if (x->offsets ? x->B != 1 : x->nseq != x->B) return FFTCONV_ERR_INVALID;
+    if (reinterpret_cast<uintptr_t>(x->offsets) & 3) return FFTCONV_ERR_ALIGN;
+    const int64_t top = int64_t(1) << 31;
+    if (x->B >= top || x->T >= top || x->Hv > 65535 || x->nseq >= top) return FFTCONV_ERR_UNSUPPORTED;
+    a->offsets = x->offsets;
+    a->B = x->B;
+    a->T = x->T;
+    a->nseq = int(x->nseq);
+    a->Hk = int(x->Hk);
+    a->Hv = int(x->Hv);
+    a->group = x->Hk ? int(x->Hv / x->Hk) : 1;
+    a->scale = x->scale;
+    a->err = p->dev_err;
+    if (x->B == 0 || x->T == 0 || x->Hv == 0) return FFTCONV_OK;
+    fftconv_status_t e;
+    if ((e = take_view(x->q, x->B, x->T, x->Hk, p->Dk, &a->q)) != FFTCONV_OK) return e;
+    if ((e = take_view(x->k, x->B, x->T, x->Hk, p->Dk, &a->k)) != FFTCONV_OK) return e;
+    if ((e = take_view(x->v, x->B, x->T, x->Hv, p->Dv, &a->v)) != FFTCONV_OK) return e;
+    if ((e = take_view(x->g, x->B, x->T, x->Hv, 0, &a->g)) != FFTCONV_OK) return e;
+    return take_view(x->beta, x->B, x->T, x->Hv, 0, &a->beta);
+}
+
+// The address ranges of the inputs.
+void input_spans(const fftconv_delta_s* p, const DeltaArgs& a, Span (&in)[6]) {
+    const bool any = a.B && a.T && a.Hv;
+    in[0] = any ? span_of(a.q, a.B, a.T, a.Hk, p->Dk) : Span{};
+    in[1] = any ? span_of(a.k, a.B, a.T, a.Hk, p->Dk) : Span{};
+    in[2] = any ? span_of(a.v, a.B, a.T, a.Hv, p->Dv) : Span{};
+    in[3] = any ? span_of(a.g, a.B, a.T, a.Hv, 0) : Span{};
+    in[4] = any ? span_of(a.beta, a.B, a.T, a.Hv, 0) : Span{};
+    in[5] = a.offsets ? span_of(a.offsets, size_t(a.nseq + 1) * 4) : Span{};
+}
+
+size_t state_bytes(const fftconv_delta_s* p, int64_t n, int64_t Hv) { return size_t(n) * Hv * p->Dk * p->Dv * 4; }
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+fftconv_status_t done(cudaError_t e) {
+    if (e == cudaSuccess) return FFTCONV_OK;
+    cudaGetLastError();
+    return FFTCONV_ERR_CUDA;
+}
+
+template <int DT>
+cudaError_t zero_view(const View& y, int64_t B, int64_t T, int64_t H, int D, cudaStream_t st) {
+    const int64_t n = B * T * H * D;
+    zero_kernel<DT><<<unsigned(n / 256 + 1 < 4096 ? n / 256 + 1 : 4096), 256, 0, st>>>(y, B, T, H, D);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace fftconv
+
+using namespace fftconv;
+
+extern "C" fftconv_status_t fftconv_delta_create(fftconv_delta_t* out, int Dk, int Dv, fftconv_dtype_t dtype) {
+    if (!out) return FFTCONV_ERR_INVALID;
+    *out = nullptr;
+    if ((Dk != 64 && Dk != 128) || (Dv != 64 && Dv != 128) || (dtype != FFTCONV_F16 && dtype != FFTCONV_BF16))
+        return FFTCONV_ERR_UNSUPPORTED;
+    fftconv_delta_s* p = new (std::nothrow) fftconv_delta_s;
+    if (!p) return FFTCONV_ERR_ALLOC;
+    p->Dk = Dk;
+    p->Dv = Dv;
+    p->dtype = dtype;
+    if (cudaGetDevice(&p->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess) {
+        cudaGetLastError();
+        delete p;
+        return FFTCONV_ERR_CUDA;
+    }
+    if (cudaMalloc(&p->dev_err, sizeof(int)) != cudaSuccess) {
+        cudaGetLastError();
+        delete p;
+        return FFTCONV_ERR_ALLOC;
+    }
+    if (cudaMemset(p->dev_err, 0, sizeof(int)) != cudaSuccess) {
+        cudaGetLastError();
+        cudaFree(p->dev_err);
+        delete p;
+        return FFTCONV_ERR_CUDA;
+    }
+    *out = p;
+    return FFTCONV_OK;
+}
+
+extern "C" fftconv_status_t fftconv_delta_destroy(fftconv_delta_t p) {
+    if (!p) return FFTCONV_OK;
+    cudaFree(p->dev_err);
+    delete p;
+    return FFTCONV_OK;
+}
+
+extern "C" fftconv_status_t fftconv_delta_status(fftconv_delta_t p, fftconv_stream_t stream, int* out) {
+    if (!p || !out || wrong_device(p)) return FFTCONV_ERR_INVALID;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int v = 0;
+    if (cudaMemcpyAsync(&v, p->dev_err, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaMemsetAsync(p->dev_err, 0, sizeof(int), st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess) {
+        cudaGetLastError();
+        return FFTCONV_ERR_CUDA;
+    }
+    *out = v;
+    return FFTCONV_OK;
+}
+
+extern "C" size_t fftconv_delta_saved_bytes(fftconv_delta_t p, int64_t B, int64_t T, int64_t Hv, int64_t nseq) {
+    if (!p || B < 0 || T < 0 || Hv < 0 || nseq < 0) return 0;
+    return size_t(chunk_slots(B, T, nseq)) * Hv * p->Dk * p->Dv * 4;
+}
+
+extern "C" size_t fftconv_delta_scratch_bytes(fftconv_delta_t p, int64_t B, int64_t T, int64_t Hk, int64_t Hv,
+                                              int64_t nseq, int backward) {
+    if (!p || B < 0 || T < 0 || Hk < 0 || Hv < 0 || nseq < 0) return 0;
+    if (!backward) return 0;
+    return up256(size_t(nseq) * Hv * kChunk * p->Dk * p->Dv * 4) + 2 * up256(size_t(B) * T * Hv * p->Dk * 4);
+}
+
+extern "C" fftconv_status_t fftconv_delta_forward(fftconv_delta_t p, const fftconv_delta_args_t* args,
+                                                  const float* state_in, fftconv_view_t o, float* state_out,
+                                                  void* saved, void* scratch, size_t scratch_bytes,
+                                                  fftconv_stream_t stream) {
+    TokenArgs a{};
+    fftconv_status_t e = take_args(p, args, &a.d);
+    if (e != FFTCONV_OK) return e;
+    const DeltaArgs& d = a.d;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (d.nseq == 0 || d.Hv == 0) return FFTCONV_OK;
+    if (off16(state_in) || off16(state_out) || off16(saved) || off16(scratch)) return FFTCONV_ERR_ALIGN;
+    const size_t sb = state_bytes(p, d.nseq, d.Hv);
+    const size_t vb = fftconv_delta_saved_bytes(p, d.B, d.T, d.Hv, d.nseq);
+    const size_t need = fftconv_delta_scratch_bytes(p, d.B, d.T, d.Hk, d.Hv, d.nseq, 0);
+    if (need && (!scratch || scratch_bytes < need)) return FFTCONV_ERR_WORKSPACE;
+    const bool any = d.B && d.T;
+    if (any && (e = take_view(o, d.B, d.T, d.Hv, p->Dv, &a.d.o)) != FFTCONV_OK) return e;
+    Span in[6];
+    input_spans(p, d, in);
+    const Span outs[4] = {any ? span_of(d.o, d.B, d.T, d.Hv, p->Dv) : Span{}, span_of(state_out, sb),
+                          span_of(saved, vb), span_of(scratch, need)};
+    const Span si[1] = {span_of(state_in, sb)};
+    if (any_meet(outs, in) || any_meet(outs, si)) return FFTCONV_ERR_INVALID;
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (meets(outs[i], outs[j])) return FFTCONV_ERR_INVALID;
+    a.sin = state_in;
+    a.sout = state_out;
+    a.saved = static_cast<float*>(saved);
+    if (!any) {  // empty rows: the states pass through
+        if (!state_out) return FFTCONV_OK;
+        return done(state_in ? cudaMemcpyAsync(state_out, state_in, sb, cudaMemcpyDeviceToDevice, st)
+                             : cudaMemsetAsync(state_out, 0, sb, st));
+    }
+    return done(pick(p->dtype, p->Dk, p->Dv, LaunchToken{a, st}));
+}
+
+extern "C" fftconv_status_t fftconv_delta_backward(fftconv_delta_t p, const fftconv_delta_args_t* args,
+                                                   fftconv_view_t d_o, const float* d_state_out, const void* saved,
+                                                   fftconv_view_t dq, fftconv_view_t dk, fftconv_view_t dv,
+                                                   fftconv_view_t dg, fftconv_view_t dbeta, float* d_state_in,
+                                                   void* scratch, size_t scratch_bytes, fftconv_stream_t stream) {
+    GradArgs a{};
+    fftconv_status_t e = take_args(p, args, &a.d);
+    if (e != FFTCONV_OK) return e;
+    const DeltaArgs& d = a.d;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (d.nseq == 0 || d.Hv == 0) return FFTCONV_OK;
+    if (off16(d_state_out) || off16(d_state_in) || off16(saved) || off16(scratch)) return FFTCONV_ERR_ALIGN;
+    const size_t sb = state_bytes(p, d.nseq, d.Hv);
+    const bool any = d.B && d.T;
+    if (!any) {
+        if (!d_state_in) return FFTCONV_OK;
+        if (meets(span_of(d_state_in, sb), span_of(d_state_out, sb))) return FFTCONV_ERR_INVALID;
+        return done(d_state_out ? cudaMemcpyAsync(d_state_in, d_state_out, sb, cudaMemcpyDeviceToDevice, st)
+                                : cudaMemsetAsync(d_state_in, 0, sb, st));
+    }
+    if (!saved) return FFTCONV_ERR_INVALID;
+    const size_t need = fftconv_delta_scratch_bytes(p, d.B, d.T, d.Hk, d.Hv, d.nseq, 1);
+    if (need && (!scratch || scratch_bytes < need)) return FFTCONV_ERR_WORKSPACE;
+    View vdq, vdk;
+    if ((e = take_view(d_o, d.B, d.T, d.Hv, p->Dv, &a.dout)) != FFTCONV_OK) return e;
+    if ((e = take_view(dq, d.B, d.T, d.Hk, p->Dk, &vdq)) != FFTCONV_OK) return e;
+    if ((e = take_view(dk, d.B, d.T, d.Hk, p->Dk, &vdk)) != FFTCONV_OK) return e;
+    if ((e = take_view(dv, d.B, d.T, d.Hv, p->Dv, &a.dv)) != FFTCONV_OK) return e;
+    if ((e = take_view(dg, d.B, d.T, d.Hv, 0, &a.dg)) != FFTCONV_OK) return e;
+    if ((e = take_view(dbeta, d.B, d.T, d.Hv, 0, &a.dbeta)) != FFTCONV_OK) return e;
+    Span in[6];
+    input_spans(p, d, in);
+    const Span more[3] = {span_of(a.dout, d.B, d.T, d.Hv, p->Dv), span_of(d_state_out, sb),
+                          span_of(saved, fftconv_delta_saved_bytes(p, d.B, d.T, d.Hv, d.nseq))};
+    // gradients may be slices of one buffer, so they are not checked against each other
+    const Span outs[7] = {span_of(vdq, d.B, d.T, d.Hk, p->Dk), span_of(vdk, d.B, d.T, d.Hk, p->Dk),
+                          span_of(a.dv, d.B, d.T, d.Hv, p->Dv), span_of(a.dg, d.B, d.T, d.Hv, 0),
+                          span_of(a.dbeta, d.B, d.T, d.Hv, 0), span_of(d_state_in, sb), span_of(scratch, need)};
+    if (any_meet(outs, in) || any_meet(outs, more)) return FFTCONV_ERR_INVALID;
+    a.dsout = d_state_out;
+    a.dsin = d_state_in;
+    a.saved = static_cast<const float*>(saved);
+    char* w = static_cast<char*>(scratch);
+    a.states = reinterpret_cast<float*>(w);
+    w += up256(size_t(d.nseq) * d.Hv * kChunk * p->Dk * p->Dv * 4);
+    const size_t hb = size_t(d.B) * d.T * d.Hv * p->Dk * 4;
+    a.dqh = reinterpret_cast<float*>(w);
+    w += up256(hb);
+    a.dkh = reinterpret_cast<float*>(w);
+    cudaError_t c = cudaSuccess;
+    const bool f16 = p->dtype == FFTCONV_F16;
+    if (d.offsets) {  // tokens outside every sequence have zero gradients
+        c = cudaMemsetAsync(a.dqh, 0, up256(hb) + hb, st);
+        const View zs[3] = {a.dv, a.dg, a.dbeta};
+        for (int i = 0; i < 3 && c == cudaSuccess; ++i)
+            c = f16 ? zero_view<0>(zs[i], d.B, d.T, d.Hv, i == 0 ? p->Dv : 1, st)
+                    : zero_view<1>(zs[i], d.B, d.T, d.Hv, i == 0 ? p->Dv : 1, st);
+    }
+    if (c == cudaSuccess) c = pick(p->dtype, p->Dk, p->Dv, LaunchGrad{a, st});
+    for (int i = 0; i < 2 && c == cudaSuccess; ++i) {
+        const float* x = i ? a.dkh : a.dqh;
+        const View& y = i ? vdk : vdq;
+        if (f16) head_sum_kernel<0><<<4096, 256, 0, st>>>(x, y, d.B, d.T, d.Hk, d.group, p->Dk);
+        else head_sum_kernel<1><<<4096, 256, 0, st>>>(x, y, d.B, d.T, d.Hk, d.group, p->Dk);
+        c = cudaGetLastError();
+    }
+    return done(c);
+}
+
+extern "C" fftconv_status_t fftconv_delta_step(fftconv_delta_t p, const fftconv_delta_args_t* args,
+                                               const float* state_in, float* state_out, int64_t nslots,
+                                               const int32_t* slots, fftconv_view_t o, fftconv_stream_t stream) {
+    TokenArgs a{};
+    fftconv_status_t e = take_args(p, args, &a.d);
+    if (e != FFTCONV_OK) return e;
+    const DeltaArgs& d = a.d;
+    if (d.offsets || nslots < 0 || (!slots && nslots < d.B)) return FFTCONV_ERR_INVALID;
+    if (d.B == 0 || d.T == 0 || d.Hv == 0) return FFTCONV_OK;
+    if (!state_in || !state_out) return FFTCONV_ERR_INVALID;
+    if (off16(state_in) || off16(state_out) || (reinterpret_cast<uintptr_t>(slots) & 3)) return FFTCONV_ERR_ALIGN;
+    if ((e = take_view(o, d.B, d.T, d.Hv, p->Dv, &a.d.o)) != FFTCONV_OK) return e;
+    const size_t sb = state_bytes(p, nslots, d.Hv);
+    Span in[6];
+    input_spans(p, d, in);
+    const Span outs[2] = {span_of(d.o, d.B, d.T, d.Hv, p->Dv), span_of(state_out, sb)};
+    const Span more[2] = {span_of(slots, size_t(d.B) * 4), state_in == state_out ? Span{} : span_of(state_in, sb)};
+    if (any_meet(outs, in) || any_meet(outs, more) || meets(outs[0], outs[1]) || meets(outs[0], span_of(state_in, sb)))
+        return FFTCONV_ERR_INVALID;
+    a.sin = state_in;
+    a.sout = state_out;
+    a.slots = slots;
+    a.nslots = nslots;
+    a.step = 1;
+    return done(pick(p->dtype, p->Dk, p->Dv, LaunchToken{a, static_cast<cudaStream_t>(stream)}));
+}

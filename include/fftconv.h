@@ -426,6 +426,168 @@ fftconv_status_t fftconv_device_status(fftconv_plan_t plan, fftconv_stream_t str
  */
 fftconv_status_t fftconv_selftest_wait(fftconv_plan_t plan, int sleep, fftconv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Token mixers with a state.  The two operators below work on token-major
+ * tensors [B][T][H][D] (the order in which projections write them), given as
+ * strided views; D is contiguous.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A view of a [B][T][H][D] tensor: element (b, t, h, d) at
+ * ptr + (b * batch + t * token + h * head + d) elements.  [B][T][H] tensors
+ * (gates) use the same view without d.  Strides of dimensions of size 1 are
+ * ignored; the others are positive.  Views of [B][T][H][D] tensors start on
+ * a 16-byte boundary and have strides that are multiples of 8 elements
+ * (else ALIGN); gates may start and step anywhere.
+ */
+typedef struct {
+    void *ptr;
+    int64_t batch, token, head;
+} fftconv_view_t;
+
+/*
+ * Gated delta rule.  Per sequence and value head h the state S [Dk][Dv]
+ * (float32) follows, token by token,
+ *   S~  = exp(g_t) S_(t-1)
+ *   u_t = beta_t (v_t - S~^T k_t)
+ *   S_t = S~ + k_t u_t^T
+ *   o_t = scale * S_t^T q_t
+ * q, k: [B][T][Hk][Dk]; v, o: [B][T][Hv][Dv]; g (the log of the decay, <= 0)
+ * and beta: [B][T][Hv]; all in the plan dtype.  Hv is a multiple of Hk: value
+ * head h uses query/key head h / (Hv / Hk).  Dk and Dv are 64 or 128.  g is
+ * taken as max(g, -120): exp(-120) is zero in float32, so a log decay of
+ * -infinity (a reset of the state) needs no special case.  Keys of norm at
+ * most 1 and beta in [0, 1] keep the recurrence bounded; fp16 intermediates
+ * (states and corrected values inside a chunk) have binary16's range.
+ *
+ * Sequences: offsets == NULL: the B rows of T tokens each (nseq = B).  Else
+ * B = 1 and sequence i is tokens offsets[i] .. offsets[i+1] - 1 of the row
+ * (offsets: nseq + 1 non-decreasing int32 on the device, within [0, T];
+ * values outside are clamped; empty sequences are valid).  Tokens outside
+ * every sequence have no output and zero gradients.
+ */
+typedef struct fftconv_delta_s *fftconv_delta_t;
+
+typedef struct {
+    int64_t B, T, Hk, Hv;
+    int64_t nseq;
+    const int32_t *offsets; /* device, or NULL */
+    float scale;
+    fftconv_view_t q, k, v, g, beta;
+} fftconv_delta_args_t;
+
+/*
+ * A plan holds the kernels' launch preparation for one (Dk, Dv, dtype) and a
+ * device error word; it is immutable and may be used from several streams at
+ * once.  Returns OK, INVALID, UNSUPPORTED (Dk, Dv not 64 or 128, dtype),
+ * ALLOC or CUDA.
+ */
+fftconv_status_t fftconv_delta_create(fftconv_delta_t *out, int Dk, int Dv, fftconv_dtype_t dtype);
+fftconv_status_t fftconv_delta_destroy(fftconv_delta_t plan);
+
+/* As fftconv_device_status: read and clear the plan's error word. */
+fftconv_status_t fftconv_delta_status(fftconv_delta_t plan, fftconv_stream_t stream, int *out);
+
+/*
+ * Bytes of `saved` (what the forward keeps for the backward) and of `scratch`
+ * (backward = 0: for the forward; 1: for the backward) for these sizes; 0 if
+ * plan is NULL or a size is negative.
+ */
+size_t fftconv_delta_saved_bytes(fftconv_delta_t plan, int64_t B, int64_t T, int64_t Hv, int64_t nseq);
+size_t fftconv_delta_scratch_bytes(fftconv_delta_t plan, int64_t B, int64_t T, int64_t Hk, int64_t Hv,
+                                   int64_t nseq, int backward);
+
+/*
+ * Whole sequences (training, prompts).  state_in: float32 [nseq][Hv][Dk][Dv]
+ * or NULL (zero); state_out: the same shape, or NULL.  saved: NULL, or
+ * fftconv_delta_saved_bytes bytes for fftconv_delta_backward.  o, state_out,
+ * saved and scratch must not overlap the inputs (checked by address range;
+ * INVALID).  Returns OK, INVALID, UNSUPPORTED (sizes past 32-bit grids), ALIGN,
+ * WORKSPACE (scratch missing or too small) or CUDA.
+ */
+fftconv_status_t fftconv_delta_forward(fftconv_delta_t plan, const fftconv_delta_args_t *args,
+                                       const float *state_in, fftconv_view_t o, float *state_out, void *saved,
+                                       void *scratch, size_t scratch_bytes, fftconv_stream_t stream);
+
+/*
+ * Gradients of fftconv_delta_forward: args as in the forward call, d_o
+ * [B][T][Hv][Dv] the gradient of o, d_state_out float32 [nseq][Hv][Dk][Dv]
+ * the gradient of the final states or NULL (zero), saved from the forward of
+ * the same inputs.  Writes dq, dk [B][T][Hk][Dk], dv [B][T][Hv][Dv], dg, dbeta
+ * [B][T][Hv] (plan dtype) and, unless NULL, d_state_in float32
+ * [nseq][Hv][Dk][Dv].  No atomics: the result is bitwise reproducible.
+ * Returns as fftconv_delta_forward.
+ */
+fftconv_status_t fftconv_delta_backward(fftconv_delta_t plan, const fftconv_delta_args_t *args,
+                                        fftconv_view_t d_o, const float *d_state_out, const void *saved,
+                                        fftconv_view_t dq, fftconv_view_t dk, fftconv_view_t dv,
+                                        fftconv_view_t dg, fftconv_view_t dbeta, float *d_state_in,
+                                        void *scratch, size_t scratch_bytes, fftconv_stream_t stream);
+
+/*
+ * The recurrent form (decoding): B rows of T tokens (few; any T is valid),
+ * each against one state of a pool float32 [nslots][Hv][Dk][Dv].  Row b uses
+ * slot slots[b] (device int32 [B], distinct), or slot b when slots is NULL; a
+ * row whose slot is negative or >= nslots gets zero outputs and touches no
+ * state.  The updated states are written to state_out (the same pool shape;
+ * state_out == state_in updates in place; other overlaps are INVALID); slots
+ * that no row uses are not touched.  args->offsets must be NULL.  Float32
+ * throughout.  Returns OK, INVALID, UNSUPPORTED, ALIGN or CUDA.
+ */
+fftconv_status_t fftconv_delta_step(fftconv_delta_t plan, const fftconv_delta_args_t *args,
+                                    const float *state_in, float *state_out, int64_t nslots,
+                                    const int32_t *slots, fftconv_view_t o, fftconv_stream_t stream);
+
+/*
+ * Norm of queries and keys for each head, with the position rotation in the
+ * same pass:
+ *   r = 1 / sqrt(mean_d x^2 + eps)   (FFTCONV_NORM_RMS)
+ *   r = 1 / sqrt(sum_d x^2 + eps)    (FFTCONV_NORM_L2)
+ *   z = x r w                        (w float32 [D], or NULL: ones)
+ *   y = z with its first R features rotated by the token's position p: the
+ *       pair (a, b) becomes (a c - b s, b c + a s) with c = cos[p][i],
+ *       s = sin[p][i]; pair i is features (i, i + R/2), or (2i, 2i + 1) when
+ *       interleaved.  R = 0: no rotation.
+ * q: [B][T][Hq][D], k: [B][T][Hk][D] (either may have no heads).  D is a
+ * multiple of 8 up to 256, R even and at most D.  cos, sin: float32
+ * [table_rows][R/2] on the device; positions: device int32 [B][T], or NULL for
+ * p = t.  A token whose position is outside the tables gets NaN outputs (and
+ * gradients).  Arithmetic in float32, one rounding at the end.  y may be the
+ * same view as x (in place); other overlaps are INVALID.
+ */
+typedef enum { FFTCONV_NORM_RMS = 0, FFTCONV_NORM_L2 = 1 } fftconv_norm_t;
+
+typedef struct {
+    int32_t dtype; /* fftconv_dtype_t */
+    int32_t norm;  /* fftconv_norm_t */
+    int32_t D, R, interleaved;
+    float eps;
+    int64_t B, T, Hq, Hk;
+    fftconv_view_t q, k;
+    const float *wq, *wk;
+    const float *cos, *sin;
+    int64_t table_rows;
+    const int32_t *positions;
+} fftconv_qknorm_args_t;
+
+/* Returns OK, INVALID, UNSUPPORTED (D, R, dtype, sizes), ALIGN or CUDA. */
+fftconv_status_t fftconv_qknorm_forward(const fftconv_qknorm_args_t *args, fftconv_view_t yq,
+                                        fftconv_view_t yk, fftconv_stream_t stream);
+
+/*
+ * Gradients: dyq, dyk of the outputs give dq, dk (plan dtype) and dwq, dwk
+ * (float32 [D], sums over all tokens and heads, overwritten; NULL: not
+ * wanted; they need wq, wk only through dx).  scratch:
+ * fftconv_qknorm_scratch_bytes(args) bytes, 16-byte aligned; may be NULL when
+ * dwq and dwk are.  Bitwise reproducible.
+ * Returns as the forward, and WORKSPACE.
+ */
+size_t fftconv_qknorm_scratch_bytes(const fftconv_qknorm_args_t *args);
+fftconv_status_t fftconv_qknorm_backward(const fftconv_qknorm_args_t *args, fftconv_view_t dyq,
+                                         fftconv_view_t dyk, fftconv_view_t dq, fftconv_view_t dk,
+                                         float *dwq, float *dwk, void *scratch, size_t scratch_bytes,
+                                         fftconv_stream_t stream);
+
 /* Static English text for a status code (never NULL). */
 const char *fftconv_status_string(fftconv_status_t s);
 
