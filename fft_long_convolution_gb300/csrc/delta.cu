@@ -1,5 +1,6 @@
 // Gated delta rule: C entry points and the token-by-token kernels.
 #include "delta.h"
+#include "delta_chunk.h"
 
 #include <new>
 
@@ -22,12 +23,10 @@ namespace {
 // in flight per thread) and latency for a few rows.
 struct TokenArgs {
     DeltaArgs d;
-    const float* sin;   // states [.][Hv][Dk][Dv] or null (zero)
-    float* sout;        // or null
+    const float* sin;  // pool of states [nslots][Hv][Dk][Dv]
+    float* sout;
     const int32_t* slots;
-    int64_t nslots;     // step: size of the pool
-    float* saved;       // forward: states at the chunk starts (float32), or null
-    int step;
+    int64_t nslots;
 };
 
 template <int DT, int DK, int DV>
@@ -40,13 +39,9 @@ __global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
     const int cg = lane % 8, rg = warp * 4 + lane / 8;
     const int h = blockIdx.y, col = blockIdx.z * 32 + cg * 4, hk = h / d.group;
     const int i = blockIdx.x;
-    Seq s = locate(d.offsets, d.T, i);
-    int64_t si = i;
-    bool live = true;
-    if (a.step) {
-        si = a.slots ? a.slots[i] : i;
-        live = si >= 0 && si < a.nslots;
-    }
+    const Seq s = locate(nullptr, d.T, i);
+    const int64_t si = a.slots ? a.slots[i] : i;
+    const bool live = si >= 0 && si < a.nslots;
     const uint16_t* kp = reinterpret_cast<const uint16_t*>(d.k.p) + s.row * d.k.b + s.start * d.k.t + hk * d.k.h + rg * RP;
     const uint16_t* qp = reinterpret_cast<const uint16_t*>(d.q.p) + s.row * d.q.b + s.start * d.q.t + hk * d.q.h + rg * RP;
     const uint16_t* vp = reinterpret_cast<const uint16_t*>(d.v.p) + s.row * d.v.b + s.start * d.v.t + h * d.v.h + col;
@@ -62,13 +57,8 @@ __global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
     float4 S[RP];
     #pragma unroll
     for (int r = 0; r < RP; ++r)
-        S[r] = a.sin ? *reinterpret_cast<const float4*>(a.sin + sbase + r * DV) : make_float4(0, 0, 0, 0);
+        S[r] = *reinterpret_cast<const float4*>(a.sin + sbase + r * DV);
     for (int64_t t = 0; t < s.len; ++t) {
-        if (a.saved && (t % kChunk) == 0) {
-            float* p = a.saved + (((s.slot + t / kChunk) * d.Hv + h) * DK + rg * RP) * DV + col;
-            #pragma unroll
-            for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(p + r * DV) = S[r];
-        }
         float k[RP], q[RP], v[4];
         #pragma unroll
         for (int r = 0; r < RP; r += 4) {
@@ -134,10 +124,8 @@ __global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
                            Op<DT>::pack(sc * fmaf(QK, u.z, Q.z), sc * fmaf(QK, u.w, Q.w)));
         }
     }
-    if (a.sout) {
-        #pragma unroll
-        for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(a.sout + sbase + r * DV) = S[r];
-    }
+    #pragma unroll
+    for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(a.sout + sbase + r * DV) = S[r];
 }
 
 // ------------------------------------------------------------ gradients, token by token
@@ -154,7 +142,7 @@ struct GradArgs {
     View dout, dv, dg, dbeta;
     const float* dsout;  // gradient of the final states, or null
     float* dsin;         // gradient of the initial states, or null
-    const float* saved;
+    const uint16_t* saved;  // S^T at the chunk starts [slot][Hv][DV][DK]
     float* states;       // [CTA][64][DK*DV]: the states before each token of a chunk
     float *dqh, *dkh;    // [B T][Hv][DK] per value head
 };
@@ -202,8 +190,9 @@ __global__ void __launch_bounds__(256) token_grad_kernel(const GradArgs a) {
         const int64_t t0 = ch * kChunk;
         const int n = int(s.len - t0 < kChunk ? s.len - t0 : kChunk);
         __syncthreads();
-        const float* sv = a.saved + ((s.slot + ch) * d.Hv + h) * DK * DV;
-        for (int x = tid; x < DK * DV; x += 256) S[x] = sv[x];
+        const uint16_t* sv = a.saved + ((s.slot + ch) * d.Hv + h) * DK * DV;
+        for (int x = tid; x < DK * DV; x += 256) S[(x % DK) * DV + x / DK] = Op<DT>::unpack(sv[x]).r;
+        __syncthreads();
         for (int j = 0; j < n; ++j) {
             load(t0 + j);
             const int64_t tt = s.start + t0 + j;
@@ -393,6 +382,18 @@ size_t state_bytes(const fftconv_delta_s* p, int64_t n, int64_t Hv) { return siz
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// What the forward keeps for the backward, per chunk slot and value head: S^T
+// at the chunk's start, Vn^T and T, 16-bit.
+struct SavedLayout {
+    size_t v, t, total;  // byte offsets of Vn^T and T (S^T is first), and the size
+    SavedLayout(const fftconv_delta_s* p, int64_t B, int64_t T, int64_t Hv, int64_t nseq) {
+        const size_t n = size_t(chunk_slots(B, T, nseq)) * Hv * 2;
+        v = up256(n * p->Dk * p->Dv);
+        t = v + up256(n * p->Dv * kChunk);
+        total = t + up256(n * kChunk * kChunk);
+    }
+};
+
 fftconv_status_t done(cudaError_t e) {
     if (e == cudaSuccess) return FFTCONV_OK;
     cudaGetLastError();
@@ -464,7 +465,8 @@ extern "C" fftconv_status_t fftconv_delta_status(fftconv_delta_t p, fftconv_stre
 
 extern "C" size_t fftconv_delta_saved_bytes(fftconv_delta_t p, int64_t B, int64_t T, int64_t Hv, int64_t nseq) {
     if (!p || B < 0 || T < 0 || Hv < 0 || nseq < 0) return 0;
-    return size_t(chunk_slots(B, T, nseq)) * Hv * p->Dk * p->Dv * 4;
+    const SavedLayout l(p, B, T, Hv, nseq);
+    return l.total;
 }
 
 extern "C" size_t fftconv_delta_scratch_bytes(fftconv_delta_t p, int64_t B, int64_t T, int64_t Hk, int64_t Hv,
@@ -478,7 +480,7 @@ extern "C" fftconv_status_t fftconv_delta_forward(fftconv_delta_t p, const fftco
                                                   const float* state_in, fftconv_view_t o, float* state_out,
                                                   void* saved, void* scratch, size_t scratch_bytes,
                                                   fftconv_stream_t stream) {
-    TokenArgs a{};
+    ChunkArgs a{};
     fftconv_status_t e = take_args(p, args, &a.d);
     if (e != FFTCONV_OK) return e;
     const DeltaArgs& d = a.d;
@@ -500,15 +502,24 @@ extern "C" fftconv_status_t fftconv_delta_forward(fftconv_delta_t p, const fftco
     for (int i = 0; i < 4; ++i)
         for (int j = 0; j < i; ++j)
             if (meets(outs[i], outs[j])) return FFTCONV_ERR_INVALID;
-    a.sin = state_in;
-    a.sout = state_out;
-    a.saved = static_cast<float*>(saved);
     if (!any) {  // empty rows: the states pass through
         if (!state_out) return FFTCONV_OK;
         return done(state_in ? cudaMemcpyAsync(state_out, state_in, sb, cudaMemcpyDeviceToDevice, st)
                              : cudaMemsetAsync(state_out, 0, sb, st));
     }
-    return done(pick(p->dtype, p->Dk, p->Dv, LaunchToken{a, st}));
+    a.state_in = state_in;
+    a.state_out = state_out;
+    if (saved) {
+        const SavedLayout l(p, d.B, d.T, d.Hv, d.nseq);
+        a.saved_s = static_cast<uint16_t*>(saved);
+        a.saved_v = reinterpret_cast<uint16_t*>(static_cast<char*>(saved) + l.v);
+        a.saved_t = reinterpret_cast<uint16_t*>(static_cast<char*>(saved) + l.t);
+    }
+    if (!encode_tokens_map(&a.mq, d.q, d.B, d.T, d.Hk, p->Dk, p->dtype) ||
+        !encode_tokens_map(&a.mk, d.k, d.B, d.T, d.Hk, p->Dk, p->dtype) ||
+        !encode_tokens_map(&a.mv, d.v, d.B, d.T, d.Hv, p->Dv, p->dtype))
+        return FFTCONV_ERR_UNSUPPORTED;
+    return done(launch_delta_forward(a, p->dtype, p->Dk, p->Dv, st));
 }
 
 extern "C" fftconv_status_t fftconv_delta_backward(fftconv_delta_t p, const fftconv_delta_args_t* args,
@@ -552,7 +563,7 @@ extern "C" fftconv_status_t fftconv_delta_backward(fftconv_delta_t p, const fftc
     if (any_meet(outs, in) || any_meet(outs, more)) return FFTCONV_ERR_INVALID;
     a.dsout = d_state_out;
     a.dsin = d_state_in;
-    a.saved = static_cast<const float*>(saved);
+    a.saved = static_cast<const uint16_t*>(saved);
     char* w = static_cast<char*>(scratch);
     a.states = reinterpret_cast<float*>(w);
     w += up256(size_t(d.nseq) * d.Hv * kChunk * p->Dk * p->Dv * 4);
@@ -603,6 +614,5 @@ extern "C" fftconv_status_t fftconv_delta_step(fftconv_delta_t p, const fftconv_
     a.sout = state_out;
     a.slots = slots;
     a.nslots = nslots;
-    a.step = 1;
     return done(pick(p->dtype, p->Dk, p->Dv, LaunchToken{a, static_cast<cudaStream_t>(stream)}));
 }

@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "../../include/fftconv.h"
+#include "device.h"
 #include "multipass.cuh"
 #include "otc.cuh"
 #include "otc2.cuh"
@@ -81,19 +82,6 @@ cudaError_t launch_mp_l4k_2level_sparse(const fftconv_plan_s* p, const MPArgs& a
 cudaError_t launch_mp_l4k_circular(const fftconv_plan_s* p, const MPArgs& args, int64_t rows, bool gated,
                                    cudaStream_t st);
 
-// A value per device: kernel attribute opt-ins belong to the context of the
-// device that is current when they are made, so launch preparations are kept
-// per device ordinal (0: not prepared on that device yet).
-constexpr int kDevSlots = 64;
-struct PerDevice {
-    int v[kDevSlots] = {};
-    int* slot() {
-        int d = 0;
-        if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kDevSlots) return nullptr;
-        return &v[d];
-    }
-};
-
 // Dynamic shared memory opt-in and resident blocks per SM of a kernel, once
 // per device; *per_sm receives the block count.
 template <typename K>
@@ -110,26 +98,6 @@ cudaError_t prep_kernel(K fn, size_t smem, int threads, PerDevice& cache, int* p
     }
     *per_sm = *s;
     return cudaSuccess;
-}
-
-// cuTensorMapEncodeTiled, reached through the runtime (once per process;
-// null if the driver does not provide it).
-using TensorMapEncoder = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-inline TensorMapEncoder tensor_map_encoder() {
-    static TensorMapEncoder fn = [] {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            return TensorMapEncoder(nullptr);
-        }
-        return reinterpret_cast<TensorMapEncoder>(ptr);
-    }();
-    return fn;
 }
 
 // A tensor map over rows of `nin` sub-rows of L 32-bit words (row stride

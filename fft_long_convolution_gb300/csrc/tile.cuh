@@ -1,0 +1,111 @@
+// Tiles of token-major tensors on the fifth-generation tensor cores.
+//
+// A tile is 64 tokens x 64 features of 16-bit values: 64 rows of 128 bytes,
+// row r's 16-byte piece c at piece c ^ (r % 8) (the 128-byte swizzle that the
+// TMA engine writes), 8 KB, 1024-byte aligned.  The same bytes serve as an
+// operand whose contraction runs over the features (K-major: the feature is
+// K) and as one whose contraction runs over the tokens (MN-major: the feature
+// is M or N), so no tile is ever transposed:
+// - K-major, R rows (tokens) per 64-feature block: 8-row groups 1024 bytes
+//   apart (SBO), a step of 16 features is 32 bytes.
+// - MN-major: 8-token groups 1024 bytes apart (SBO), 64-feature blocks LBO
+//   bytes apart, a step of 16 tokens is 2048 bytes.
+// The accumulator of an M = 128 contraction has row i in TMEM lane i.
+#pragma once
+#include "mma.cuh"
+#include "tc.cuh"
+
+namespace fftconv {
+namespace tile {
+
+constexpr uint32_t kTile = 8192;
+
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{.reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;}" : "=r"(p));
+    return p != 0;
+}
+
+// Shared-memory descriptor with the 128-byte swizzle.
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo) {
+    return tc::sdesc(addr, lbo, 1024) | (uint64_t(2) << 61);
+}
+
+// Descriptor advanced by `bytes`.
+__device__ __forceinline__ uint64_t adv(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
+constexpr uint32_t kMnA = 1u << 15, kMnB = 1u << 16;  // MN-major A, B in the instruction descriptor
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Whether a phase is over, the same answer in every lane of the warp.
+__device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{.reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;}"
+                 : "=r"(done)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return __all_sync(0xffffffffu, done != 0);
+}
+
+// Bounded wait of a whole warp: gives up after about a second, or sooner when
+// another role of the CTA has (*fail set).  The same answer in every lane.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
+    const uint32_t addr = smem_u32(bar);
+    uint64_t t0 = 0;
+    bool got = false;
+    for (uint32_t it = 0; it < (1u << 24); ++it) {
+        uint32_t done;
+        asm volatile(
+            "{.reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (done) {
+            got = true;
+            break;
+        }
+        if ((it & 31) == 31) {
+            if (*fail) break;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > kWaitNs) break;
+        }
+    }
+    return __all_sync(0xffffffffu, got);
+}
+
+// x = hi + lo in two 16-bit values each (about 16 significant bits for bf16),
+// for a pair packed low half first.
+template <int DT>
+__device__ __forceinline__ void split(float x0, float x1, uint32_t* hi, uint32_t* lo) {
+    const uint32_t h = Op<DT>::pack(x0, x1);
+    const cpx f = Op<DT>::unpack(h);
+    *hi = h;
+    *lo = Op<DT>::pack(x0 - f.r, x1 - f.i);
+}
+
+// Store 32 consecutive columns of this thread's lane.
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+}  // namespace tile
+}  // namespace fftconv
