@@ -394,6 +394,23 @@ struct SavedLayout {
     }
 };
 
+// The forward's scratch.
+struct FwdScratch {
+    ChunkArgs c{};
+    size_t state, trans, total;  // byte offsets (the images are first), and the size
+    FwdScratch(const fftconv_delta_s* p, int64_t B, int64_t T, int64_t Hv, int64_t nseq) {
+        c.d.B = B;
+        c.d.T = T;
+        c.d.Hv = int(Hv);
+        c.d.nseq = int(nseq);
+        plan_segments(&c, p->num_sms);
+        const size_t segs = c.segments > nseq ? size_t(c.segments) * Hv * p->Dk * 4 : 0;
+        state = up256(size_t(c.slots) * Hv * prep_image(p->Dk));
+        trans = state + up256(segs * p->Dv);
+        total = trans + up256(segs * p->Dk);
+    }
+};
+
 fftconv_status_t done(cudaError_t e) {
     if (e == cudaSuccess) return FFTCONV_OK;
     cudaGetLastError();
@@ -472,7 +489,10 @@ extern "C" size_t fftconv_delta_saved_bytes(fftconv_delta_t p, int64_t B, int64_
 extern "C" size_t fftconv_delta_scratch_bytes(fftconv_delta_t p, int64_t B, int64_t T, int64_t Hk, int64_t Hv,
                                               int64_t nseq, int backward) {
     if (!p || B < 0 || T < 0 || Hk < 0 || Hv < 0 || nseq < 0) return 0;
-    if (!backward) return 0;
+    if (!backward) {
+        const FwdScratch l(p, B, T, Hv, nseq);
+        return l.total;
+    }
     return up256(size_t(nseq) * Hv * kChunk * p->Dk * p->Dv * 4) + 2 * up256(size_t(B) * T * Hv * p->Dk * 4);
 }
 
@@ -509,6 +529,15 @@ extern "C" fftconv_status_t fftconv_delta_forward(fftconv_delta_t p, const fftco
     }
     a.state_in = state_in;
     a.state_out = state_out;
+    const FwdScratch w(p, d.B, d.T, d.Hv, d.nseq);
+    if (w.c.slots >= (int64_t(1) << 31)) return FFTCONV_ERR_UNSUPPORTED;
+    a.slots = w.c.slots;
+    a.segments = w.c.segments;
+    a.seg_chunks = w.c.seg_chunks;
+    a.sms = p->num_sms;
+    a.images = static_cast<uint8_t*>(scratch);
+    a.seg_state = reinterpret_cast<float*>(a.images + w.state);
+    a.seg_trans = reinterpret_cast<float*>(a.images + w.trans);
     if (saved) {
         const SavedLayout l(p, d.B, d.T, d.Hv, d.nseq);
         a.saved_s = static_cast<uint16_t*>(saved);

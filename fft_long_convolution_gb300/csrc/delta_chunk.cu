@@ -20,12 +20,16 @@
 // exact.  Products that only feed O (Q S, P Vn) take one 16-bit value: O is
 // rounded to 16 bits anyway.
 //
-// One CTA per sequence and value head; roles by warp, handing tiles over
-// through mbarriers:
-//   warps 0-3   chain: S (float32 -> operands, decayed in place) and Vn
-//   warps 4-7   W^T -> operand in shared memory; O^T -> global memory
-//   warps 8-11  T: A from K K^T, the triangular inverse, P from Q K^T
-//   warp 12     issues every contraction;  warp 13  loads
+// Two kernels.  delta_prep_kernel forms what does not depend on S -- T, W, P
+// and the decays -- for all chunks side by side, and leaves them as images of
+// the shared-memory tiles that delta_fwd_kernel fetches with one bulk copy a
+// chunk (57 KB at Dk = 128, next to the 48 KB of K, Q and V).  delta_fwd_kernel
+// walks the chunks: one CTA per sequence (or segment of one) and value head,
+// roles by warp, handing tiles over through mbarriers:
+//   warps 0-15   chain: S (float32 -> operands, decayed in place), Vn and O^T, a
+//                quarter of the columns for each four warps
+//   warps 16-19  O -> global memory
+//   warp 20      issues every contraction;  warp 21  loads
 #include "delta_chunk.h"
 
 #include "tile.cuh"
@@ -35,614 +39,734 @@ namespace {
 
 using namespace tile;
 
-template <int DK_, int DV_>
-struct FwdCfg {
-    static constexpr int DK = DK_;
-    static constexpr int NKQ = 3;                          // stages of K and Q
-    static constexpr uint32_t KQ = (DK / 64) * 2 * kTile;  // [feature block][K rows | Q rows]
-    static constexpr uint32_t VB = 2 * kTile;              // DV = 64: the same block twice (M = 128)
-    static constexpr uint32_t WB = DK * 128;               // W^T: DK rows of 64 tokens, per part
-    static constexpr int LD = 68;                          // row pitch of the float32 64 x 64 scratch
-    static constexpr uint32_t oKQ = 0, oV = oKQ + NKQ * KQ, oW = oV + VB, oT = oW + 2 * WB, oP = oT + 4 * kTile,
-                              oA = oP + 2 * kTile, oG = oA + 64 * LD * 4, oL = oG + 4 * 132 * 4, oBar = oL + 3 * 64 * 4,
-                              BYTES = oBar + 256;
-    static constexpr int THREADS = 448;
-    // tensor memory columns
-    static constexpr uint32_t cS = 0, cHi = 128, cLo = 128 + DK / 2, cVeH = 128, cVeL = 160, cVnH = 192, cVn = 256,
-                              cOS = 320, cKK = 384, cW = 448;
-};
-
-enum Bar {
-    kKqFull = 0, kKqFree = 3, kVFull = 6, kRaw, kKkDone, kKkFree, kTReady, kUDone, kWtDone, kWReady, kSwDone, kSqDone,
-    kVnReady, kOpRead, kSDone, kSReady, kFinal,
-    kOpDone,             // [2], by chunk parity: T's warps may look back two chunks
-    kGates = kOpDone + 2,  // [4], by ring slot: written up to three chunks ahead of the chain
-    kBars = kGates + 4
-};
-
 constexpr uint32_t kWaitFinal = 1u << 18;  // polls of the waits that end a CTA
 
-// T = (I + A)^-1 in place, A strictly lower triangular 64 x 64 (float32, row
-// pitch LD), by 128 threads.  The four 16 x 16 diagonal blocks by forward
-// substitution (a thread per column), then blocks of 32 and of 64 from
-// T21 = -T22 (A21 T11): exact arithmetic of a triangular solve, no powers of A
-// (which grow like binomials when keys are alike).  Intermediate products sit
-// in the unused blocks above the diagonal, which are left undefined.
-template <int LD, typename Sync>
-__device__ __forceinline__ void inverse64(float* A, int p, Sync sync) {
-    if (p < 64) {
-        float* base = A + (p >> 4) * 16 * (LD + 1);
-        const int col = p & 15;
-        float x[16];
+// What delta_prep_kernel leaves for a chunk of one value head: the tiles P,
+// (T beta) high and low part, then float32 e[64], scale G[64], G_63, then -W^T,
+// DK rows of 64 tokens, high and low part.
+constexpr uint32_t kImgP = 0, kImgT = kTile, kImgE = 3 * kTile, kImgW = kImgE + 1024;
+template <int DK>
+constexpr uint32_t kImage = kImgW + DK * 256;
+
+// One 16 x 8 tile of a float32 product X Y over k0 <= k < k1 (multiples of 8)
+// by one warp, as three products of 10-bit parts (hi hi + hi lo + lo hi: about
+// 2^-20 per product).  X, Y row-major with pitch LD; acc as the MMA's C.
+template <int LD>
+__device__ __forceinline__ void tile_product(float (&acc)[4], const float* X, const float* Y, int k0, int k1, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    for (int k = k0; k < k1; k += 8) {
+        const float x[4] = {X[g * LD + k + t], X[(g + 8) * LD + k + t], X[g * LD + k + t + 4], X[(g + 8) * LD + k + t + 4]};
+        const float y[2] = {Y[(k + t) * LD + g], Y[(k + t + 4) * LD + g]};
+        uint32_t xh[4], xl[4], yh[2], yl[2];
         #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            float s0 = r == col ? 1.0f : 0.0f, s1 = 0.0f;
+        for (int i = 0; i < 4; ++i) {
+            xh[i] = __float_as_uint(x[i]) & 0xffffe000u;
+            xl[i] = __float_as_uint(x[i] - __uint_as_float(xh[i]));
+        }
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            yh[i] = __float_as_uint(y[i]) & 0xffffe000u;
+            yl[i] = __float_as_uint(y[i] - __uint_as_float(yh[i]));
+        }
+        auto mma = [&](const uint32_t (&p)[4], const uint32_t (&q)[2]) {
+            asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+                : "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(q[0]), "r"(q[1]));
+        };
+        mma(xh, yh);
+        mma(xh, yl);
+        mma(xl, yh);
+    }
+}
+
+// Store a 16 x 8 tile, times sgn.
+template <int LD>
+__device__ __forceinline__ void tile_store(float* Z, const float (&acc)[4], float sgn, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    *reinterpret_cast<float2*>(Z + g * LD + 2 * t) = make_float2(sgn * acc[0], sgn * acc[1]);
+    *reinterpret_cast<float2*>(Z + (g + 8) * LD + 2 * t) = make_float2(sgn * acc[2], sgn * acc[3]);
+}
+
+// T = (I + A)^-1 in place, A strictly lower triangular 64 x 64 (float32, row
+// pitch LD), by 256 threads (w: warp, p: thread).  The eight 8 x 8 diagonal
+// blocks by forward substitution (a thread per column), then blocks of 16, 32
+// and 64 from T21 = -T22 (A21 T11): a triangular solve, with no powers of A
+// (which grow like binomials when keys are alike).  The products are small (up
+// to 32 x 32 x 32) and wait on one another, so the larger ones run on the
+// warp-level tensor path with split operands.  Intermediate products sit in
+// the unused blocks above the diagonal, which are left undefined.
+template <int LD, typename Sync>
+__device__ __forceinline__ void inverse64(float* A, int p, int w, int lane, Sync sync) {
+    if (p < 64) {
+        float* base = A + (p >> 3) * 8 * (LD + 1);
+        const int col = p & 7;
+        float x[8];
+        #pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            float s = r == col ? 1.0f : 0.0f;
             #pragma unroll
-            for (int k = 0; k < r; k += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(base + r * LD + k);
-                s0 = fmaf(-v.x, x[k], s0);
-                if (k + 1 < r) s1 = fmaf(-v.y, x[k + 1], s1);
-                if (k + 2 < r) s0 = fmaf(-v.z, x[k + 2], s0);
-                if (k + 3 < r) s1 = fmaf(-v.w, x[k + 3], s1);
-            }
-            x[r] = s0 + s1;
+            for (int k = 0; k < r; ++k) s = fmaf(-base[r * LD + k], x[k], s);
+            x[r] = s;
         }
         __syncwarp();
         #pragma unroll
-        for (int r = 0; r < 16; ++r) base[r * LD + col] = x[r];
+        for (int r = 0; r < 8; ++r) base[r * LD + col] = x[r];
     }
     sync();
     {
-        const int q = (p >> 6) * 32, r = (p & 63) >> 2, c = (p & 3) * 4;
-        const float *A21 = A + (q + 16 + r) * LD + q, *T11 = A + q * LD + q + c;
-        float* M = A + q * LD + q + 16 + c;
-        const float* T22 = A + (q + 16 + r) * LD + q + 16;
-        float4 m = make_float4(0, 0, 0, 0);
+        const int q = (p >> 6) * 16, r = (p >> 3) & 7, c = p & 7;
+        float* T11 = A + q * (LD + 1);
+        const float* A21 = T11 + (8 + r) * LD;
+        float m = 0.0f;
         #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float x = A21[k];
-            const float4 t = *reinterpret_cast<const float4*>(T11 + k * LD);
-            m.x = fmaf(x, t.x, m.x); m.y = fmaf(x, t.y, m.y); m.z = fmaf(x, t.z, m.z); m.w = fmaf(x, t.w, m.w);
-        }
-        *reinterpret_cast<float4*>(M + r * LD) = m;
+        for (int k = 0; k < 8; ++k) m = fmaf(A21[k], T11[k * LD + c], m);
+        T11[r * LD + 8 + c] = m;
         sync();
-        m = make_float4(0, 0, 0, 0);
+        m = 0.0f;
         #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float x = -T22[k];
-            const float4 t = *reinterpret_cast<const float4*>(M + k * LD);
-            m.x = fmaf(x, t.x, m.x); m.y = fmaf(x, t.y, m.y); m.z = fmaf(x, t.z, m.z); m.w = fmaf(x, t.w, m.w);
+        for (int k = 0; k < 8; ++k) m = fmaf(-A21[8 + k], T11[k * LD + 8 + c], m);
+        T11[(8 + r) * LD + c] = m;
+        sync();
+        T11[r * LD + 8 + c] = 0.0f;
+    }
+    sync();
+    {
+        const int q = (w >> 1) * 32, n0 = (w & 1) * 8;
+        float* M = A + q * LD + q + 16 + n0;
+        float* A21 = A + (q + 16) * LD + q;
+        if (w < 4) {
+            float acc[4] = {};
+            tile_product<LD>(acc, A21, A + q * LD + q + n0, 0, 16, lane);
+            tile_store<LD>(M, acc, 1.0f, lane);
         }
-        *reinterpret_cast<float4*>(A + (q + 16 + r) * LD + q + c) = m;
+        sync();
+        if (w < 4) {
+            float acc[4] = {};
+            tile_product<LD>(acc, A21 + 16, M, 0, 16, lane);
+            tile_store<LD>(A21 + n0, acc, -1.0f, lane);
+        }
         sync();
     }
     {
-        const int r = p >> 3, c = (p & 7) * 4, k0 = c & 16;  // T11 is zero above its diagonal blocks
-        const float *A21 = A + (32 + r) * LD, *T11 = A + c, *T22 = A + (32 + r) * LD + 32;
-        float* M = A + 32 + c;
-        float4 m = make_float4(0, 0, 0, 0), n = m;
-        #pragma unroll 8
-        for (int k = k0; k < 32; ++k) {
-            const float x = A21[k], y = A21[16 * LD + k];
-            const float4 t = *reinterpret_cast<const float4*>(T11 + k * LD);
-            m.x = fmaf(x, t.x, m.x); m.y = fmaf(x, t.y, m.y); m.z = fmaf(x, t.z, m.z); m.w = fmaf(x, t.w, m.w);
-            n.x = fmaf(y, t.x, n.x); n.y = fmaf(y, t.y, n.y); n.z = fmaf(y, t.z, n.z); n.w = fmaf(y, t.w, n.w);
-        }
-        *reinterpret_cast<float4*>(M + r * LD) = m;
-        *reinterpret_cast<float4*>(M + (r + 16) * LD) = n;
+        // T11 is zero above its diagonal blocks, T22 too
+        const int m0 = (w & 1) * 16, n0 = (w >> 1) * 8;
+        float* M = A + 32 + n0;
+        float acc[4] = {};
+        tile_product<LD>(acc, A + (32 + m0) * LD, A + n0, n0 & 16, 32, lane);
+        tile_store<LD>(M + m0 * LD, acc, 1.0f, lane);
         sync();
-        m = n = make_float4(0, 0, 0, 0);
-        #pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float x = k < 16 ? -T22[k] : 0.0f, y = -T22[16 * LD + k];
-            const float4 t = *reinterpret_cast<const float4*>(M + k * LD);
-            m.x = fmaf(x, t.x, m.x); m.y = fmaf(x, t.y, m.y); m.z = fmaf(x, t.z, m.z); m.w = fmaf(x, t.w, m.w);
-            n.x = fmaf(y, t.x, n.x); n.y = fmaf(y, t.y, n.y); n.z = fmaf(y, t.z, n.z); n.w = fmaf(y, t.w, n.w);
-        }
-        *reinterpret_cast<float4*>(A + (32 + r) * LD + c) = m;
-        *reinterpret_cast<float4*>(A + (48 + r) * LD + c) = n;
+        float acd[4] = {};
+        tile_product<LD>(acd, A + (32 + m0) * LD + 32, M, 0, m0 + 16, lane);
+        tile_store<LD>(A + (32 + m0) * LD + n0, acd, -1.0f, lane);
         sync();
     }
 }
 
-struct Item {
-    Seq s;
-    int i, h, hk;
-    int n;  // chunks
+
+// Chunk slot -> sequence and chunk: the last sequence whose first slot is not
+// past it.
+__device__ __forceinline__ bool find_chunk(const DeltaArgs& d, int64_t slot, Seq* s, int* i, int64_t* chunk) {
+    int lo = 0, hi = d.nseq - 1;
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (locate(d.offsets, d.T, m).slot <= slot) lo = m;
+        else hi = m - 1;
+    }
+    *s = locate(d.offsets, d.T, lo);
+    *i = lo;
+    *chunk = slot - s->slot;
+    return *chunk >= 0 && *chunk * kChunk < s->len;
+}
+
+// Segment slot -> sequence and segment, by the same rule on the chunk slots.
+__device__ __forceinline__ bool find_segment(const DeltaArgs& d, int64_t L, int64_t slot, Seq* s, int* i, int64_t* seg) {
+    int lo = 0, hi = d.nseq - 1;
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (locate(d.offsets, d.T, m).slot / L + m <= slot) lo = m;
+        else hi = m - 1;
+    }
+    *s = locate(d.offsets, d.T, lo);
+    *i = lo;
+    *seg = slot - (s->slot / L + lo);
+    return *seg == 0 || (*seg > 0 && *seg * L * kChunk < s->len);
+}
+
+template <int DK>
+struct PrepCfg {
+    static constexpr int LD = 68;                          // row pitch of the float32 64 x 64 scratch
+    static constexpr uint32_t KQ = (DK / 64) * 2 * kTile;  // [feature block][K rows | Q rows]; then W^T
+    static constexpr uint32_t oI = KQ, oA = oI + kImgW, oL = oA + 64 * LD * 4, oBar = oL + 224 * 4, BYTES = oBar + 64;
+    static constexpr int PER_SM = 3;
 };
 
-template <int DT, int DK, int DV>
-__global__ void __launch_bounds__(FwdCfg<DK, DV>::THREADS, 1)
-delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
-    using C = FwdCfg<DK, DV>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+// T, W, P and the decays of one chunk and value head at a time.  Bound: the
+// latency of its steps (each waits for the last; the inverse alone has eleven),
+// covered by three CTAs per SM.
+template <int DT, int DK>
+__global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(const __grid_constant__ ChunkArgs a) {
+    using C = PrepCfg<DK>;
+    extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
-    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_fail;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);  // loads, K K^T, W
     const DeltaArgs& d = a.d;
-    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    Item it;
-    it.i = blockIdx.x;
-    it.h = blockIdx.y;
-    it.hk = it.h / d.group;
-    it.s = locate(d.offsets, d.T, it.i);
-    it.n = int((it.s.len + kChunk - 1) / kChunk);
-    const int n = it.n;
-    const int64_t sbase = (int64_t(it.i) * d.Hv + it.h) * DK * DV;
-
-    if (threadIdx.x == 0) {
-        s_fail = 0;
-        for (int i = 0; i < kBars; ++i) {
-            uint32_t cnt = 1;
-            if (i == kKkFree || i == kTReady || i == kWReady || i == kVnReady || i == kOpRead || i == kSReady || i >= kGates)
-                cnt = 4;  // one arrival per warp of the role
-            mbar_init(bar + i, cnt);
-        }
+    const int p = threadIdx.x, w = __shfl_sync(0xffffffffu, p / 32, 0), lane = p % 32;
+    if (sb & 1023) {  // not with the present layout of the window
+        if (p == 0) atomicExch(d.err, 7);
+        return;
+    }
+    if (p == 0) {
+        for (int i = 0; i < 3; ++i) mbar_init(bar + i, 1);
         fence_mbar_init();
     }
-    if (warp == 12) tc::alloc(&s_tmem, 512);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + 3);
+    if (w == 1) tc::alloc(s_tmem, 64);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tm = s_tmem;
-    volatile int* fail = &s_fail;
-    const uint32_t lanes = tm + (uint32_t(32 * (warp & 3)) << 16);  // this warp's tensor-memory lanes
-    const int row = 32 * (warp & 3) + lane;                         // this thread's lane
-
-    float* gates = reinterpret_cast<float*>(sm + C::oG);  // ring of 4: e[64], scale G[64], G_63
-    // one arrival per warp, after every lane's work
-    auto done = [&](Bar b) {
-        __syncwarp();
-        if (lane == 0) arrive(bar + b);
-    };
-
-    if (n == 0) {
-        // an empty sequence: the state passes through
-        if (a.state_out)
-            for (int x = threadIdx.x; x < DK * DV; x += C::THREADS)
-                a.state_out[sbase + x] = a.state_in ? a.state_in[sbase + x] : 0.0f;
-    } else if (warp < 4) {
-        // ---------------------------------------------------------------- chain
-        const int dv = row % DV;
-        const bool mine = row < DV;
-        bool ok = true;
-        for (int c = 0; ok && c < n; ++c) {
-            const float* gt = gates + (c & 3) * 132;
-            if (!(ok = wait(bar + kGates + (c & 3), (c >> 2) & 1, fail))) break;
-            const float gc = gt[128];
-            if (c > 0) {
-                if (!(ok = wait(bar + kSDone, (c - 1) & 1, fail))) break;
-                tc::fence_after();
-            }
-            uint16_t* sv = a.saved_s ? a.saved_s + (((it.s.slot + c) * d.Hv + it.h) * DV + dv) * DK : nullptr;
+    const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(s_tmem);
+    const uint32_t lanes = tm + (uint32_t(32 * (w & 3)) << 16);
+    float* A = reinterpret_cast<float*>(sm + C::oA);
+    // b log2(e), beta; decays between 16-token blocks (below)
+    float *sbv = reinterpret_cast<float*>(sm + C::oL), *sbe = sbv + 64, *sE2 = sbe + 64, *sE1 = sE2 + 64;
+    auto sync = [] { __syncthreads(); };
+    const int64_t items = a.slots * d.Hv;
+    uint32_t par = 0;
+    bool ok = true;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t slot = item / d.Hv;
+        const int h = int(item - slot * d.Hv);
+        Seq s;
+        int si;
+        int64_t ch;
+        if (!find_chunk(d, slot, &s, &si, &ch)) continue;
+        const int64_t left = s.len - ch * kChunk, t0 = s.start + ch * kChunk;
+        const int m = int(left < kChunk ? left : kChunk);
+        if (p == 0) {
+            bulk_wait_read();  // the last images have left shared memory
+            mbar_expect_tx(bar, C::KQ);
             #pragma unroll
-            for (int k0 = 0; k0 < DK; k0 += 32) {
-                uint32_t x[32], hi[16], lo[16];
-                if (c > 0) {
-                    tc::ld32x32b_x32(lanes + C::cS + k0, x);
-                    tc::wait_ld();
-                } else {
-                    #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        x[j] = a.state_in ? __float_as_uint(a.state_in[sbase + (k0 + j) * DV + dv]) : 0u;
-                }
-                #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float x0 = __uint_as_float(x[2 * j]), x1 = __uint_as_float(x[2 * j + 1]);
-                    split<DT>(x0, x1, &hi[j], &lo[j]);
-                    x[2 * j] = __float_as_uint(gc * x0);
-                    x[2 * j + 1] = __float_as_uint(gc * x1);
-                }
-                tc::st16(lanes + C::cHi + k0 / 2, hi);
-                tc::st16(lanes + C::cLo + k0 / 2, lo);
-                st32(lanes + C::cS + k0, x);
-                if (sv && mine) {
-                    #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        *reinterpret_cast<uint4*>(sv + k0 + 2 * j) = make_uint4(hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
-                }
-            }
-            tc::wait_st();
-            tc::fence_before();
-            done(kSReady);
-            // Vn^T = U^T - S^T W^T
-            if (!(ok = wait(bar + kSwDone, c & 1, fail))) break;
-            tc::fence_after();
-            uint32_t vh[32], eh[32], el[32];
-            #pragma unroll
-            for (int j0 = 0; j0 < 64; j0 += 32) {
-                uint32_t x[32];
-                tc::ld32x32b_x32(lanes + C::cVn + j0, x);
-                tc::wait_ld();
-                #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float x0 = __uint_as_float(x[2 * j]), x1 = __uint_as_float(x[2 * j + 1]);
-                    const float2 e = *reinterpret_cast<const float2*>(gt + j0 + 2 * j);
-                    vh[j0 / 2 + j] = Op<DT>::pack(x0, x1);
-                    split<DT>(e.x * x0, e.y * x1, &eh[j0 / 2 + j], &el[j0 / 2 + j]);
-                }
-            }
-            // S's operands are free once Q S is done too
-            if (!(ok = wait(bar + kSqDone, c & 1, fail))) break;
-            st32(lanes + C::cVnH, vh);
-            st32(lanes + C::cVeH, eh);
-            st32(lanes + C::cVeL, el);
-            tc::wait_st();
-            tc::fence_before();
-            done(kVnReady);
-            if (a.saved_v && mine) {
-                uint16_t* p = a.saved_v + (((it.s.slot + c) * d.Hv + it.h) * DV + dv) * 64;
-                #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<uint4*>(p + 2 * j) = make_uint4(vh[j], vh[j + 1], vh[j + 2], vh[j + 3]);
+            for (int f = 0; f < DK / 64; ++f) {
+                tma_load_4d(sb + f * 2 * kTile, &a.mk, f * 64, h / d.group, int(t0), int(s.row), bar);
+                tma_load_4d(sb + f * 2 * kTile + kTile, &a.mq, f * 64, h / d.group, int(t0), int(s.row), bar);
             }
         }
-        if (ok) ok = wait(bar + kSDone, (n - 1) & 1, fail);
-        if (ok && a.state_out) {
-            tc::fence_after();
+        if (w == 2) {
+            // running sum of the log decays, in units of log 2; past the end: no
+            // decay, no update
+            constexpr float kLog2e = 1.44269504088896340736f;
+            float g[2] = {}, e[2] = {};
             #pragma unroll
-            for (int k0 = 0; k0 < DK; k0 += 32) {
-                uint32_t x[32];
-                tc::ld32x32b_x32(lanes + C::cS + k0, x);
-                tc::wait_ld();
-                if (mine) {
-                    #pragma unroll
-                    for (int j = 0; j < 32; ++j) a.state_out[sbase + (k0 + j) * DV + dv] = __uint_as_float(x[j]);
+            for (int u = 0; u < 2; ++u) {
+                const int t = 2 * lane + u;
+                if (t < m) {
+                    g[u] = kLog2e * log_decay(load16<DT>(d.g, s.row * d.g.b + (t0 + t) * d.g.t + h * d.g.h));
+                    e[u] = load16<DT>(d.beta, s.row * d.beta.b + (t0 + t) * d.beta.t + h * d.beta.h);
                 }
             }
+            float x = g[0] + g[1];
+            #pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float v = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += v;
+            }
+            *reinterpret_cast<float2*>(sbv + 2 * lane) = make_float2(x - g[1], x);
+            *reinterpret_cast<float2*>(sbe + 2 * lane) = make_float2(e[0], e[1]);
         }
-        if (!ok) s_fail = 1;
-    } else if (warp < 8) {
-        // ---------------------------------------------------------------- W^T and O^T
-        bool ok = true;
-        auto do_w = [&](int c) {  // W^T of chunk c -> shared memory
-            if (!wait(bar + kWtDone, c & 1, fail)) return false;
-            tc::fence_after();
-            uint32_t hi[32], lo[32];
-            #pragma unroll
-            for (int j0 = 0; j0 < 64; j0 += 32) {
-                uint32_t x[32];
-                tc::ld32x32b_x32(lanes + C::cW + j0, x);
-                tc::wait_ld();
-                #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    split<DT>(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), &hi[j0 / 2 + j], &lo[j0 / 2 + j]);
-            }
-            tc::fence_before();
-            if (c > 0 && !wait(bar + kSwDone, (c - 1) & 1, fail)) return false;
-            if (row < DK) {
-                uint8_t* p = sm + C::oW + row * 128;
-                #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int at = (j ^ (row & 7)) * 16;
-                    *reinterpret_cast<uint4*>(p + at) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-                    *reinterpret_cast<uint4*>(p + C::WB + at) =
-                        make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
-                }
+        sync();
+        // D_ij for i >= 32 > j is E1_i E2_j with both factors at most 1: the decay
+        // from the first token of i's 16-token block, and up to it
+        if (p < 64) {
+            const float b = sbv[p];
+            float* gt = reinterpret_cast<float*>(sm + C::oI + kImgE);
+            gt[p] = exp2_fast(sbv[63] - b);
+            gt[64 + p] = d.scale * exp2_fast(b);
+            if (p == 63) gt[128] = exp2_fast(b);
+        } else if (p < 128) {
+            const int q = p - 64;
+            sE2[q] = exp2_fast(sbv[32 + 16 * (q >> 5)] - sbv[q & 31]);
+        } else if (p < 160) {
+            const int q = p - 128;
+            sE1[q] = exp2_fast(sbv[32 + q] - sbv[32 + (q & 16)]);
+        }
+        ok = mbar_wait_bounded(bar, par, kWaitLimitTile);
+        if (d.offsets && m < kChunk) {
+            // rows past the sequence are the next one's: zero them (past the
+            // tensor's end the TMA engine has)
+            for (int x = p; x < (64 - m) * 8 * (DK / 32); x += 256) {
+                const int f = x / ((64 - m) * 8), y = x % ((64 - m) * 8);
+                *reinterpret_cast<uint4*>(sm + f * kTile + m * 128 + y * 16) = make_uint4(0, 0, 0, 0);
             }
             tc::fence_proxy_async();
-            done(kWReady);
-            return true;
-        };
-        auto do_o = [&](int c) {  // O^T of chunk c -> global memory
-            if (!wait(bar + kOpDone + (c & 1), (c >> 1) & 1, fail)) return false;
-            tc::fence_after();
-            const float* sg = gates + (c & 3) * 132 + 64;
-            uint32_t o[32];
-            #pragma unroll
-            for (int j0 = 0; j0 < 64; j0 += 32) {
-                uint32_t x[32], y[32];
-                tc::ld32x32b_x32(lanes + C::cOS + j0, x);
-                tc::ld32x32b_x32(lanes + C::cVn + j0, y);
-                tc::wait_ld();
-                #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float2 g = *reinterpret_cast<const float2*>(sg + j0 + 2 * j);
-                    o[j0 / 2 + j] = Op<DT>::pack(fmaf(g.x, __uint_as_float(x[2 * j]), __uint_as_float(y[2 * j])),
-                                                 fmaf(g.y, __uint_as_float(x[2 * j + 1]), __uint_as_float(y[2 * j + 1])));
-                }
-            }
-            tc::fence_before();
-            done(kOpRead);
-            if (row < DV) {
-                const int64_t t0 = it.s.start + int64_t(c) * kChunk;
-                const int m = int(it.s.len - int64_t(c) * kChunk < kChunk ? it.s.len - int64_t(c) * kChunk : kChunk);
-                uint16_t* p = reinterpret_cast<uint16_t*>(d.o.p) + it.s.row * d.o.b + t0 * d.o.t + it.h * d.o.h + row;
-                if (m == kChunk) {
-                    #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        p[(2 * j) * d.o.t] = uint16_t(o[j] & 0xffffu);
-                        p[(2 * j + 1) * d.o.t] = uint16_t(o[j] >> 16);
-                    }
-                } else {
-                    #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (2 * j < m) p[(2 * j) * d.o.t] = uint16_t(o[j] & 0xffffu);
-                        if (2 * j + 1 < m) p[(2 * j + 1) * d.o.t] = uint16_t(o[j] >> 16);
-                    }
-                }
-            }
-            return true;
-        };
-        ok = do_w(0);
-        for (int c = 0; ok && c < n; ++c) {
-            bool w = c + 1 >= n;
-            // whichever came first; all four warps see the same completed phases
-            // eventually, and each warp's own order does not matter to the others
-            if (!w && test(bar + kWtDone, (c + 1) & 1)) {
-                if (!(ok = do_w(c + 1))) break;
-                w = true;
-            }
-            if (!(ok = do_o(c))) break;
-            if (!w) ok = do_w(c + 1);
         }
-        if (!ok) s_fail = 1;
-    } else if (warp < 12) {
-        // ---------------------------------------------------------------- T and P
-        const int p = threadIdx.x - 256;
-        float* A = reinterpret_cast<float*>(sm + C::oA);
-        float *sbv = reinterpret_cast<float*>(sm + C::oL), *sbe = sbv + 64, *sbg = sbe + 64;  // b, beta, -beta G
-        auto sync = [&] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-        // the four warps meet in barriers, so they also give up together
-        auto together = [&](bool mine) { return !tc::bar_vote(1, 128, !mine); };
-        bool ok = true;
-        float g_next = 0.0f, b_next = 0.0f;
-        auto fetch = [&](int c) {  // gates of token p of chunk c (p < 64)
-            const int64_t t = int64_t(c) * kChunk + p;
-            if (p < 64 && t < it.s.len) {
-                const int64_t at = it.s.start + t;
-                g_next = load16<DT>(d.g, it.s.row * d.g.b + at * d.g.t + it.h * d.g.h);
-                b_next = load16<DT>(d.beta, it.s.row * d.beta.b + at * d.beta.t + it.h * d.beta.h);
-            } else {
-                g_next = 0.0f;  // past the end: no decay, no update
-                b_next = 0.0f;
-            }
-        };
-        fetch(0);
-        for (int c = 0; ok && c < n; ++c) {
-            float* gt = gates + (c & 3) * 132;
-            // running sum of the log decays over the 64 tokens (warps 8 and 9)
-            float bs = log_decay(g_next);
-            const float be = b_next;
-            if (c + 1 < n) fetch(c + 1);
-            if (p < 64) {
-                #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float v = __shfl_up_sync(0xffffffffu, bs, o);
-                    if (lane >= o) bs += v;
-                }
-                if (p == 31) sbv[0] = bs;
-            }
-            sync();
-            if (p >= 32 && p < 64) bs += sbv[0];
-            sync();
-            if (p < 64) {
-                sbv[p] = bs;
-                sbe[p] = be;
-                const float G = expf(bs);
-                sbg[p] = -be * G;
-                gt[64 + p] = d.scale * G;
-                if (p == 63) gt[128] = G;
-            }
-            sync();
-            if (p < 64) gt[p] = expf(sbv[63] - bs);
-            done(Bar(kGates + (c & 3)));
-            // K K^T (lanes 0-63) and Q K^T (lanes 64-127)
-            ok = wait(bar + kKkDone, c & 1, fail);
-            // P's buffer is free once chunk c - 2's P Vn is done
-            if (ok && c > 1) ok = wait(bar + kOpDone + (c & 1), ((c >> 1) - 1) & 1, fail);
-            if (!(ok = together(ok))) break;
-            tc::fence_after();
-            const int i = row & 63;
-            const bool isp = row >= 64;
-            const float bi = sbv[i], f = isp ? d.scale : sbe[i];
-            #pragma unroll
-            for (int j0 = 0; j0 < 64; j0 += 32) {
-                uint32_t x[32];
-                tc::ld32x32b_x32(lanes + C::cKK + j0, x);
-                tc::wait_ld();
-                #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 bj = *reinterpret_cast<const float4*>(sbv + j0 + j);
-                    const float bb[4] = {bj.x, bj.y, bj.z, bj.w};
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int jj = j0 + j + q;
-                        const bool on = isp ? jj <= i : jj < i;
-                        // off entries take exp(0): no overflow, and the product is dropped
-                        const float D = __expf(on ? bi - bb[q] : 0.0f);
-                        x[j + q] = on ? __float_as_uint(f * D * __uint_as_float(x[j + q])) : 0u;
-                    }
-                }
-                if (isp) {
-                    uint8_t* pp = sm + C::oP + (c & 1) * kTile + i * 128;
-                    #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-                        #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            w[q] = Op<DT>::pack(__uint_as_float(x[8 * j + 2 * q]), __uint_as_float(x[8 * j + 2 * q + 1]));
-                        *reinterpret_cast<uint4*>(pp + (((j0 / 8 + j) ^ (i & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else {
-                    #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<uint4*>(A + i * C::LD + j0 + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-                }
-            }
-            tc::fence_before();
-            done(kKkFree);
-            sync();
-            inverse64<C::LD>(A, p, sync);
-            // the scaled copies of T, as two 16-bit parts; the previous chunk's are
-            // free once its U is done
-            if (c > 0) ok = wait(bar + kUDone, (c - 1) & 1, fail);
-            if (!(ok = together(ok))) break;
-            {
-                const int r = p & 63, h0 = (p >> 6) * 32;
-                #pragma unroll
-                for (int j0 = 0; j0 < 32; j0 += 8) {
-                    uint32_t w[4][4], ts[4];
-                    #pragma unroll
-                    for (int j = 0; j < 8; j += 4) {
-                        const int jj = h0 + j0 + j;
-                        const float4 t = *reinterpret_cast<const float4*>(A + r * C::LD + jj);
-                        const float4 x = *reinterpret_cast<const float4*>(sbe + jj);
-                        const float4 y = *reinterpret_cast<const float4*>(sbg + jj);
-                        // the scratch above the diagonal holds intermediate products
-                        const float t0 = jj <= r ? t.x : 0.0f, t1 = jj + 1 <= r ? t.y : 0.0f,
-                                    t2 = jj + 2 <= r ? t.z : 0.0f, t3 = jj + 3 <= r ? t.w : 0.0f;
-                        split<DT>(t0 * x.x, t1 * x.y, &w[0][j / 2], &w[1][j / 2]);
-                        split<DT>(t2 * x.z, t3 * x.w, &w[0][j / 2 + 1], &w[1][j / 2 + 1]);
-                        split<DT>(t0 * y.x, t1 * y.y, &w[2][j / 2], &w[3][j / 2]);
-                        split<DT>(t2 * y.z, t3 * y.w, &w[2][j / 2 + 1], &w[3][j / 2 + 1]);
-                        ts[j / 2] = Op<DT>::pack(t0, t1);
-                        ts[j / 2 + 1] = Op<DT>::pack(t2, t3);
-                    }
-                    const int at = r * 128 + ((((h0 + j0) / 8) ^ (r & 7)) * 16);
-                    #pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        *reinterpret_cast<uint4*>(sm + C::oT + m * kTile + at) = make_uint4(w[m][0], w[m][1], w[m][2], w[m][3]);
-                    if (a.saved_t)
-                        *reinterpret_cast<uint4*>(a.saved_t + (((it.s.slot + c) * d.Hv + it.h) * 64 + r) * 64 + h0 + j0) =
-                            make_uint4(ts[0], ts[1], ts[2], ts[3]);
-                }
-            }
-            tc::fence_proxy_async();
-            done(kTReady);
-            sync();  // the scratch and the gates are rewritten next
-        }
-        if (!ok) s_fail = 1;
-    } else if (warp == 12) {
-        // ---------------------------------------------------------------- contractions
-        constexpr uint32_t id64 = tc::idesc(DT, 128, 64);
-        constexpr uint32_t idS = tc::idesc(DT, 128, DK) | kMnB;
-        bool ok = true;
-        int kk = 0;  // next chunk of K K^T
-        auto kk_issue = [&] {
-            const uint32_t at = sb + C::oKQ + (kk % C::NKQ) * C::KQ;
-            const uint64_t d0 = sdesc(at, 16);
+        if (!(ok = !__syncthreads_or(!ok))) break;
+        if (w == 0) {
+            constexpr uint32_t id = tc::idesc(DT, 128, 64);
+            const uint64_t d0 = sdesc(sb, 16);
             tc::fence_after();
             if (elect()) {
                 #pragma unroll
                 for (int f = 0; f < DK; f += 16) {
                     const uint64_t x = adv(d0, (f / 64) * 2 * kTile + (f % 64) * 2);
-                    tc::mma_ss(tm + C::cKK, x, x, id64, f > 0);  // A: 128 rows [K; Q], B: the first 64
+                    tc::mma_ss(tm, x, x, id, f > 0);  // A: 128 rows [K; Q], B: the first 64
                 }
-                tc::commit(bar + kKkDone);
+                tc::commit(bar + 1);
             }
-            ++kk;
-        };
-        auto kk_try = [&] {
-            if (kk < n && test(bar + kKqFull + kk % C::NKQ, (kk / C::NKQ) & 1) &&
-                (kk == 0 || test(bar + kKkFree, (kk - 1) & 1)))
-                kk_issue();
-        };
-        auto kk_wait = [&] {
-            if (!wait(bar + kKqFull + kk % C::NKQ, (kk / C::NKQ) & 1, fail)) return false;
-            if (kk > 0 && !wait(bar + kKkFree, (kk - 1) & 1, fail)) return false;
-            kk_issue();
+        }
+        ok = mbar_wait_bounded(bar + 1, par, kWaitLimitTile);
+        if (!(ok = !__syncthreads_or(!ok))) break;
+        tc::fence_after();
+        // K K^T in lanes 0-63, Q K^T in lanes 64-127; warps 0-3 take columns 0-31,
+        // warps 4-7 the others
+        const int row = 32 * (w & 3) + lane, i = row & 63, up = (row >> 5) & 1, half = w >> 2;
+        const bool isp = row >= 64;
+        const float f = isp ? d.scale : sbe[i];
+        uint8_t* prow = sm + C::oI + kImgP + i * 128;
+        if (up || !half) {
+            uint32_t x[32];
+            const int j0 = half * 32;
+            tc::ld32x32b_x32(lanes + j0, x);
+            tc::wait_ld();
+            if (up && !half) {  // whole blocks below the diagonal
+                const float fe = f * sE1[i - 32];
+                const float* e2 = sE2 + (i & 16) * 2;
+                #pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 e = *reinterpret_cast<const float4*>(e2 + j);
+                    const float2 u = mul2(mul2(make_float2(fe, fe), make_float2(e.x, e.y)), pair(x[j], x[j + 1]));
+                    const float2 v = mul2(mul2(make_float2(fe, fe), make_float2(e.z, e.w)), pair(x[j + 2], x[j + 3]));
+                    x[j] = __float_as_uint(u.x); x[j + 1] = __float_as_uint(u.y);
+                    x[j + 2] = __float_as_uint(v.x); x[j + 3] = __float_as_uint(v.y);
+                }
+            } else {  // around the diagonal: entries above it (whatever they hold) become 0
+                const float bi = sbv[i];
+                const int last = (isp ? i : i - 1) - j0;
+                #pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 b = *reinterpret_cast<const float4*>(sbv + j0 + j);
+                    const float bj[4] = {b.x, b.y, b.z, b.w};
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float v = f * exp2_fast(bi - bj[q]) * __uint_as_float(x[j + q]);
+                        x[j + q] = j + q <= last ? __float_as_uint(v) : 0u;
+                    }
+                }
+            }
+            if (isp) {
+                #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t v[4];
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        v[q] = Op<DT>::pack(__uint_as_float(x[8 * j + 2 * q]), __uint_as_float(x[8 * j + 2 * q + 1]));
+                    *reinterpret_cast<uint4*>(prow + (((j0 / 8 + j) ^ (i & 7)) * 16)) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            } else {
+                #pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<uint4*>(A + i * C::LD + j0 + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+            }
+        } else if (isp) {
+            #pragma unroll
+            for (int j = 4; j < 8; ++j) *reinterpret_cast<uint4*>(prow + ((j ^ (i & 7)) * 16)) = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_before();
+        sync();
+        inverse64<C::LD>(A, p, w, lane, sync);
+        // T with its columns times beta, and times -beta G (over the scratch, once
+        // everyone has read it), as two 16-bit parts each
+        const int64_t at = (s.slot + ch) * d.Hv + h;
+        {
+            const int r = p & 63, h0 = (p >> 6) * 16;
+            float4 t[4];
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) t[j] = *reinterpret_cast<const float4*>(A + r * C::LD + h0 + 4 * j);
+            sync();
+            #pragma unroll
+            for (int j0 = 0; j0 < 16; j0 += 8) {
+                uint32_t v[4][4], ts[4];
+                #pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    const int jj = h0 + j0 + j;
+                    const float4 y = t[(j0 + j) / 4];
+                    const float4 x = *reinterpret_cast<const float4*>(sbe + jj), b = *reinterpret_cast<const float4*>(sbv + jj);
+                    // the scratch above the diagonal holds intermediate products
+                    const float2 y0 = make_float2(jj <= r ? y.x : 0.0f, jj + 1 <= r ? y.y : 0.0f);
+                    const float2 y1 = make_float2(jj + 2 <= r ? y.z : 0.0f, jj + 3 <= r ? y.w : 0.0f);
+                    const float2 x0 = mul2(y0, make_float2(x.x, x.y)), x1 = mul2(y1, make_float2(x.z, x.w));
+                    split<DT>(x0, &v[0][j / 2], &v[1][j / 2]);
+                    split<DT>(x1, &v[0][j / 2 + 1], &v[1][j / 2 + 1]);
+                    split<DT>(mul2(x0, make_float2(-exp2_fast(b.x), -exp2_fast(b.y))), &v[2][j / 2], &v[3][j / 2]);
+                    split<DT>(mul2(x1, make_float2(-exp2_fast(b.z), -exp2_fast(b.w))), &v[2][j / 2 + 1], &v[3][j / 2 + 1]);
+                    ts[j / 2] = Op<DT>::pack(y0.x, y0.y);
+                    ts[j / 2 + 1] = Op<DT>::pack(y1.x, y1.y);
+                }
+                const int pos = r * 128 + ((((h0 + j0) / 8) ^ (r & 7)) * 16);
+                #pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4*>(sm + (q < 2 ? C::oI + kImgT + q * kTile : C::oA + (q - 2) * kTile) + pos) =
+                        make_uint4(v[q][0], v[q][1], v[q][2], v[q][3]);
+                if (a.saved_t)
+                    *reinterpret_cast<uint4*>(a.saved_t + (at * 64 + r) * 64 + h0 + j0) = make_uint4(ts[0], ts[1], ts[2], ts[3]);
+            }
+        }
+        tc::fence_proxy_async();
+        sync();
+        if (p == 0) bulk_s2g(a.images + at * kImage<DK>, sb + C::oI, kImgW);
+        if (w == 0) {  // -W^T = K^T (-T beta G)^T
+            constexpr uint32_t id = tc::idesc(DT, 128, 64) | kMnA;
+            const uint64_t da = sdesc(sb, DK == 128 ? 2 * kTile : kTile), db = sdesc(sb + C::oA, 16);
+            tc::fence_after();
+            if (elect()) {
+                #pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    #pragma unroll
+                    for (int t = 0; t < 64; t += 16)
+                        tc::mma_ss(tm, adv(da, t * 128), adv(db, q * kTile + t * 2), id, q + t > 0);
+                tc::commit(bar + 2);
+            }
+        }
+        ok = mbar_wait_bounded(bar + 2, par, kWaitLimitTile);
+        if (!(ok = !__syncthreads_or(!ok))) break;
+        tc::fence_after();
+        if (row < DK) {
+            uint32_t x[32], hi[16], lo[16];
+            tc::ld32x32b_x32(lanes + half * 32, x);
+            tc::wait_ld();
+            #pragma unroll
+            for (int j = 0; j < 16; ++j) split<DT>(pair(x[2 * j], x[2 * j + 1]), &hi[j], &lo[j]);
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint8_t* q = sm + row * 128 + ((half * 4 + j) ^ (row & 7)) * 16;
+                *reinterpret_cast<uint4*>(q) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+                *reinterpret_cast<uint4*>(q + DK * 128) = make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
+            }
+        }
+        tc::fence_proxy_async();
+        tc::fence_before();
+        sync();
+        if (p == 0) bulk_s2g(a.images + at * kImage<DK> + kImgW, sb, DK * 256);
+        par ^= 1;
+    }
+    if (p == 0) {
+        bulk_wait_read();
+        if (!ok) {
+            atomicExch(d.err, 7);
+            mbar_wait_bounded(bar, par, kWaitFinal);  // the copies have landed before the CTA leaves
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (w == 1) tc::dealloc(tm, 64);
+}
+
+template <int DK_, int DV_>
+struct FwdCfg {
+    static constexpr int DK = DK_;
+    static constexpr int NKQ = 2, NI = 2;                  // stages of K and Q, and of the images
+    static constexpr uint32_t KQ = (DK / 64) * 2 * kTile;  // [feature block][K rows | Q rows]
+    static constexpr uint32_t VB = 2 * kTile;              // DV = 64: the same block twice (M = 128)
+    static constexpr uint32_t oKQ = 0, oV = oKQ + NKQ * KQ, oI = oV + VB, oO = oI + NI * kImage<DK_>,
+                              oBar = oO + 64 * DV_ * 2, BYTES = oBar + 256;
+    static constexpr int THREADS = 704;
+    // tensor memory columns.  The two U^T / Vn^T / P Vn accumulators take turns.
+    // Vn's operands take the place of S's parts: Vn that of the low part (dead
+    // after S W), e Vn that of the high part (dead after S Q).
+    static constexpr uint32_t cS = 0, cHi = 128, cLo = 192, cVeH = 128, cVeL = 160, cVnH = 192, cVn = 256, cOS = 384;
+    static __device__ __forceinline__ uint32_t vn(int c) { return cVn + (c & 1) * 64; }
+};
+
+enum Bar {
+    kKqFull = 0, kKqFree = kKqFull + 2, kTFull = kKqFree + 2, kVFull = kTFull + 2, kRaw, kUDone, kSwDone, kSqDone, kVnReady, kSDone, kOReady, kOFree,
+    kSReady, kFinal,
+    kOpDone, kOpRead = kOpDone + 2,  // [2] each, by chunk parity
+    kBars = kOpRead + 2
+};
+
+// STATE: only the state at the end of a segment: from zero (or the initial
+// state) with the segment's values, or (blockIdx.z = 1) from the identity with
+// no values, which gives the segment's transition matrix.
+template <int DT, int DK, int DV, bool STATE>
+__global__ void __launch_bounds__(FwdCfg<DK, DV>::THREADS, 1)
+delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
+    using C = FwdCfg<DK, DV>;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);
+    // no static shared memory: the window starts 1024-byte aligned
+    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 240);
+    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 244);
+    const DeltaArgs& d = a.d;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    const int h = blockIdx.y, hk = h / d.group;
+    if (sb & 1023) {  // not with the present layout of the window
+        if (threadIdx.x == 0) atomicExch(d.err, 7);
+        return;
+    }
+    Seq s;
+    int si;
+    int64_t seg;
+    if (!find_segment(d, a.seg_chunks, blockIdx.x, &s, &si, &seg)) return;
+    const int64_t c_first = seg * a.seg_chunks, c_all = (s.len + kChunk - 1) / kChunk;
+    const bool last = c_first + a.seg_chunks >= c_all;
+    const bool trans = STATE && blockIdx.z == 1;  // the transition matrix
+    if (STATE && (last || (trans && seg == 0))) return;
+    const int n = int(last ? c_all - c_first : a.seg_chunks);
+    const int64_t slot0 = s.slot + c_first, tok0 = s.start + c_first * kChunk, len = s.len - c_first * kChunk;
+    const int64_t hs = int64_t(si) * d.Hv + h, gs = int64_t(blockIdx.x) * d.Hv + h;
+    // where the state starts and where it goes, [DK][lanes] float32
+    const float* sin = seg == 0 ? (a.state_in ? a.state_in + hs * DK * DV : nullptr) : nullptr;
+    if (!STATE && seg > 0) sin = a.seg_state + (gs - d.Hv) * DK * DV;
+    float* sout = last && a.state_out ? a.state_out + hs * DK * DV : nullptr;
+    if (STATE) sout = trans ? a.seg_trans + gs * DK * DK : a.seg_state + gs * DK * DV;
+    const int LV = trans ? DK : DV;  // lanes in use (state columns)
+
+    if (threadIdx.x == 0) {
+        s_fail = 0;
+        for (int i = 0; i < kBars; ++i) {
+            uint32_t cnt = 1;  // else one arrival per warp of the role
+            if (i == kOFree) cnt = 4;
+            if (i == kVnReady || i == kSReady || i == kOReady || i >= kOpRead) cnt = 16;
+            mbar_init(bar + i, cnt);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 20) tc::alloc(&s_tmem, 512);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = *const_cast<volatile uint32_t*>(&s_tmem);
+    volatile int* fail = &s_fail;
+    const uint32_t lanes = tm + (uint32_t(32 * (warp & 3)) << 16);  // this warp's tensor-memory lanes
+    const int row = 32 * (warp & 3) + lane;                         // this thread's lane
+    // one arrival per warp, after every lane's work
+    auto done = [&](int b) {
+        __syncwarp();
+        if (lane == 0) arrive(bar + b);
+    };
+    auto image = [&](int c) { return sm + C::oI + (c % C::NI) * kImage<DK>; };
+
+    if (n == 0) {
+        // an empty sequence: the state passes through
+        if (sout)
+            for (int x = threadIdx.x; x < DK * DV; x += C::THREADS) sout[x] = sin ? sin[x] : 0.0f;
+    } else if (warp < 16) {
+        // ---------------------------------------------------------------- chain
+        const int dv = row % LV, quarter = warp >> 2;
+        const bool mine = row < LV;
+        constexpr int NC = DK / 4;  // columns of S of this warp
+        const int k0 = quarter * NC;
+        const int j0 = quarter * 16;  // and tokens of Vn and O
+        // O^T of chunk c -> shared memory: done while the next chunk's S W runs
+        auto put_o = [&](int c) {
+            const float* gt = reinterpret_cast<const float*>(image(c) + kImgE);
+            if (!wait(bar + kOpDone + (c & 1), (c >> 1) & 1, fail)) return false;
+            if (STATE) {
+                done(kOpRead + (c & 1));
+                return true;
+            }
+            tc::fence_after();
+            uint32_t o[8];
+            {
+                uint32_t y[16], z[16];
+                ld16(lanes + C::cOS + j0, y);
+                ld16(lanes + C::vn(c) + j0, z);
+                tc::wait_ld();
+                #pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 u = fma2(*reinterpret_cast<const float2*>(gt + 64 + j0 + 2 * j), pair(y[2 * j], y[2 * j + 1]),
+                                          pair(z[2 * j], z[2 * j + 1]));
+                    o[j] = Op<DT>::pack(u.x, u.y);
+                }
+            }
+            tc::fence_before();
+            done(kOpRead + (c & 1));
+            // neighbours exchange halves, so that a lane holds two features of one
+            // token; rows of odd tokens are turned by 64 bytes against bank conflicts
+            if (c > 0 && !wait(bar + kOFree, (c - 1) & 1, fail)) return false;
+            if (mine) {
+                uint8_t* p = sm + C::oO + (((row >> 1) * 4) ^ ((row & 1) * 64)) + (j0 + (row & 1)) * (DV * 2);
+                #pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t y = __shfl_xor_sync(0xffffffffu, o[j], 1);
+                    *reinterpret_cast<uint32_t*>(p + 2 * j * (DV * 2)) =
+                        row & 1 ? __byte_perm(y, o[j], 0x7632) : __byte_perm(o[j], y, 0x5410);
+                }
+            }
+            done(kOReady);
             return true;
         };
-        auto wt_issue = [&](int c) {  // W^T = K^T (T beta G)^T
-            const uint64_t da = sdesc(sb + C::oKQ + (c % C::NKQ) * C::KQ, DK == 128 ? 2 * kTile : kTile);
-            const uint64_t db = sdesc(sb + C::oT + 2 * kTile, 16);
-            tc::fence_after();
-            if (elect()) {
+        bool ok = true;
+        for (int c = 0; ok && c < n; ++c) {
+            if (!(ok = wait(bar + kTFull + c % C::NI, (c / C::NI) & 1, fail))) break;
+            const float* gt = reinterpret_cast<const float*>(image(c) + kImgE);
+            const float2 gc = make_float2(gt[128], gt[128]);
+            uint32_t x[NC], hi[NC / 2], lo[NC / 2];
+            if (c > 0) {
+                if (!(ok = wait(bar + kSDone, (c - 1) & 1, fail))) break;
+                tc::fence_after();
+                ld_cols<NC>(lanes + C::cS + k0, x);
+                tc::wait_ld();
+            } else {
                 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    #pragma unroll
-                    for (int t = 0; t < 64; t += 16)
-                        tc::mma_ss(tm + C::cW, adv(da, t * 128), adv(db, m * kTile + t * 2), id64 | kMnA, m + t > 0);
-                tc::commit(bar + kWtDone);
+                for (int j = 0; j < NC; ++j)
+                    x[j] = __float_as_uint(trans ? (k0 + j == dv ? 1.0f : 0.0f) : (sin ? sin[(k0 + j) * DV + dv] : 0.0f));
             }
+            #pragma unroll
+            for (int j = 0; j < NC / 2; ++j) {
+                const float2 v = pair(x[2 * j], x[2 * j + 1]), y = mul2(gc, v);
+                split<DT>(v, &hi[j], &lo[j]);
+                x[2 * j] = __float_as_uint(y.x);
+                x[2 * j + 1] = __float_as_uint(y.y);
+            }
+            st_cols<NC / 2>(lanes + C::cHi + k0 / 2, hi);
+            st_cols<NC / 2>(lanes + C::cLo + k0 / 2, lo);
+            tc::wait_st();
+            tc::fence_before();
+            done(kSReady);
+            st_cols<NC>(lanes + C::cS + k0, x);  // complete before kVnReady
+            if (!STATE && a.saved_s && mine) {
+                uint16_t* sv = a.saved_s + (((slot0 + c) * d.Hv + h) * DV + dv) * DK + k0;
+                #pragma unroll
+                for (int j = 0; j < NC / 2; j += 4)
+                    *reinterpret_cast<uint4*>(sv + 2 * j) = make_uint4(hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
+            }
+            if (c > 0 && !(ok = put_o(c - 1))) break;
+            // Vn^T = U^T - S^T W^T
+            if (!(ok = wait(bar + kSwDone, c & 1, fail))) break;
+            tc::fence_after();
+            uint32_t vh[8], eh[8], el[8];
+            {
+                uint32_t y[16];
+                ld16(lanes + C::vn(c) + j0, y);
+                tc::wait_ld();
+                #pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 v = pair(y[2 * j], y[2 * j + 1]);
+                    vh[j] = Op<DT>::pack(v.x, v.y);
+                    split<DT>(mul2(*reinterpret_cast<const float2*>(gt + j0 + 2 * j), v), &eh[j], &el[j]);
+                }
+            }
+            st_cols<8>(lanes + C::cVnH + j0 / 2, vh);
+            if (!(ok = wait(bar + kSqDone, c & 1, fail))) break;
+            st_cols<8>(lanes + C::cVeH + j0 / 2, eh);
+            st_cols<8>(lanes + C::cVeL + j0 / 2, el);
+            tc::wait_st();
+            tc::fence_before();
+            done(kVnReady);
+            if (!STATE && a.saved_v && mine) {
+                uint16_t* p = a.saved_v + (((slot0 + c) * d.Hv + h) * DV + dv) * 64 + j0;
+                *reinterpret_cast<uint4*>(p) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+                *reinterpret_cast<uint4*>(p + 8) = make_uint4(vh[4], vh[5], vh[6], vh[7]);
+            }
+        }
+        if (ok) ok = put_o(n - 1);
+        if (ok) ok = wait(bar + kSDone, (n - 1) & 1, fail);
+        if (ok && sout) {
+            tc::fence_after();
+            uint32_t x[NC];
+            ld_cols<NC>(lanes + C::cS + k0, x);
+            tc::wait_ld();
+            if (mine) {
+                #pragma unroll
+                for (int j = 0; j < NC; ++j) sout[(k0 + j) * LV + dv] = __uint_as_float(x[j]);
+            }
+        }
+        if (!ok) s_fail = 1;
+    } else if (warp < 20) {
+        // ---------------------------------------------------------------- O
+        bool ok = true;
+        auto copy_o = [&](int c) {  // O of chunk c -> global memory
+            if (!wait(bar + kOReady, c & 1, fail)) return false;
+            constexpr int NP = DV / 8;  // 16-byte pieces of a token
+            const int64_t left = len - int64_t(c) * kChunk;
+            const int piece = row % NP;
+            uint16_t* p = reinterpret_cast<uint16_t*>(d.o.p) + s.row * d.o.b + (tok0 + int64_t(c) * kChunk) * d.o.t +
+                          h * d.o.h + piece * 8;
+            #pragma unroll
+            for (int t = row / NP; t < 64; t += 128 / NP) {
+                const uint4 x = *reinterpret_cast<const uint4*>(sm + C::oO + t * (DV * 2) + ((piece ^ ((t & 1) * 4)) * 16));
+                if (t < left) *reinterpret_cast<uint4*>(p + t * d.o.t) = x;
+            }
+            done(kOFree);
+            return true;
         };
+        for (int c = 0; !STATE && ok && c < n; ++c) ok = copy_o(c);
+        if (!ok) s_fail = 1;
+    } else if (warp == 20) {
+        // ---------------------------------------------------------------- contractions
+        constexpr uint32_t id64 = tc::idesc(DT, 128, 64);
+        constexpr uint32_t idS = tc::idesc(DT, 128, DK) | kMnB;
+        bool ok = true;
         auto u_issue = [&](int c) {  // U^T = V^T (T beta)^T
             const uint64_t da = sdesc(sb + C::oV, kTile);
-            const uint64_t db = sdesc(sb + C::oT, 16);
+            const uint64_t db = sdesc(sb + C::oI + (c % C::NI) * kImage<DK> + kImgT, 16);
             tc::fence_after();
             if (elect()) {
-                #pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    #pragma unroll
-                    for (int t = 0; t < 64; t += 16)
-                        tc::mma_ss(tm + C::cVn, adv(da, t * 128), adv(db, m * kTile + t * 2), id64 | kMnA, m + t > 0);
-                tc::commit(bar + kUDone);
-            }
-        };
-        ok = kk_wait() && wait(bar + kTReady, 0, fail);
-        if (ok) {
-            wt_issue(0);
-            ok = wait(bar + kVFull, 0, fail);
-            if (ok) u_issue(0);
-        }
-        for (int c = 0; ok && c < n; ++c) {
-            kk_try();
-            if (!(ok = wait(bar + kSReady, c & 1, fail) && wait(bar + kWReady, c & 1, fail))) break;
-            tc::fence_after();
-            {
-                const uint64_t dw = sdesc(sb + C::oW, 16);
-                const uint64_t dq = sdesc(sb + C::oKQ + (c % C::NKQ) * C::KQ + kTile, 16);
-                if (elect()) {
-                    #pragma unroll
-                    for (int f = 0; f < DK; f += 16) {  // U^T - S^T W^T (W is stored negated)
-                        tc::mma(tm + C::cVn, tm + C::cHi + f / 2, adv(dw, f * 128), id64 | kMnB, 1);
-                        tc::mma(tm + C::cVn, tm + C::cHi + f / 2, adv(dw, C::WB + f * 128), id64 | kMnB, 1);
-                        tc::mma(tm + C::cVn, tm + C::cLo + f / 2, adv(dw, f * 128), id64 | kMnB, 1);
-                    }
-                    tc::commit(bar + kSwDone);
-                    #pragma unroll
-                    for (int f = 0; f < DK; f += 16)  // S^T Q^T
-                        tc::mma(tm + C::cOS, tm + C::cHi + f / 2, adv(dq, (f / 64) * 2 * kTile + (f % 64) * 2), id64, f > 0);
-                    tc::commit(bar + kSqDone);
-                }
-            }
-            bool wt = c + 1 >= n;
-            // while the chain forms Vn: the next chunks' K K^T and W^T as they get ready
-            uint64_t t0 = 0;
-            for (uint32_t spin = 0; !test(bar + kVnReady, c & 1); ++spin) {
-                kk_try();
-                if (!wt && test(bar + kTReady, (c + 1) & 1)) {
-                    wt_issue(c + 1);
-                    wt = true;
-                }
-                if ((spin & 255) == 255) {
-                    const uint64_t t = globaltimer_ns();
-                    if (t0 == 0) t0 = t;
-                    if (*fail || t - t0 > kWaitNs) {
-                        ok = false;
-                        break;
-                    }
-                }
-            }
-            if (!ok) break;
-            tc::fence_after();
-            {
-                const uint64_t dp = sdesc(sb + C::oP + (c & 1) * kTile, 16);
-                const uint64_t dk = sdesc(sb + C::oKQ + (c % C::NKQ) * C::KQ, 2 * kTile);
-                if (elect()) {
-                    #pragma unroll
-                    for (int t = 0; t < 64; t += 16)  // Vn^T P^T
-                        tc::mma(tm + C::cVn, tm + C::cVnH + t / 2, adv(dp, t * 2), id64, t > 0);
-                    tc::commit(bar + kOpDone + (c & 1));
+                if (!trans) {
                     #pragma unroll
                     for (int m = 0; m < 2; ++m)
                         #pragma unroll
-                        for (int t = 0; t < 64; t += 16)  // S^T += (e Vn)^T K
-                            tc::mma(tm + C::cS, tm + (m ? C::cVeL : C::cVeH) + t / 2, adv(dk, t * 128), idS, 1);
-                    tc::commit(bar + kSDone);
-                    tc::commit(bar + kKqFree + c % C::NKQ);
+                        for (int t = 0; t < 64; t += 16)
+                            tc::mma_ss(tm + C::vn(c), adv(da, t * 128), adv(db, m * kTile + t * 2), id64 | kMnA, m + t > 0);
                 }
+                tc::commit(bar + kUDone);
             }
-            if (c + 1 < n) {
-                while (ok && kk <= c + 1) ok = kk_wait();
-                if (ok && !wt) {
-                    ok = wait(bar + kTReady, (c + 1) & 1, fail);
-                    if (ok) wt_issue(c + 1);
+        };
+        auto u_wait = [&](int c) {
+            return wait(bar + kTFull + c % C::NI, (c / C::NI) & 1, fail) && wait(bar + kVFull, c & 1, fail);
+        };
+        ok = u_wait(0);
+        if (ok) u_issue(0);
+        for (int c = 0; ok && c < n; ++c) {
+            if (!(ok = wait(bar + kSReady, c & 1, fail))) break;
+            tc::fence_after();
+            if (elect()) {
+                const uint64_t dw = sdesc(sb + C::oI + (c % C::NI) * kImage<DK> + kImgW, 16);
+                #pragma unroll
+                for (int f = 0; f < DK; f += 16) {  // U^T - S^T W^T (W is stored negated)
+                    tc::mma(tm + C::vn(c), tm + C::cHi + f / 2, adv(dw, f * 128), id64 | kMnB, !(trans && f == 0));
+                    tc::mma(tm + C::vn(c), tm + C::cHi + f / 2, adv(dw, DK * 128 + f * 128), id64 | kMnB, 1);
+                    tc::mma(tm + C::vn(c), tm + C::cLo + f / 2, adv(dw, f * 128), id64 | kMnB, 1);
                 }
-                if (ok) ok = wait(bar + kOpRead, c & 1, fail) && wait(bar + kVFull, (c + 1) & 1, fail);
+                tc::commit(bar + kSwDone);
+            }
+            // chunk c - 1's O is out of its accumulators
+            if (c > 0 && !(ok = wait(bar + kOpRead + ((c - 1) & 1), ((c - 1) >> 1) & 1, fail))) break;
+            if (!(ok = wait(bar + kKqFull + c % C::NKQ, (c / C::NKQ) & 1, fail))) break;
+            tc::fence_after();
+            if (elect()) {
+                const uint64_t dq = sdesc(sb + C::oKQ + (c % C::NKQ) * C::KQ + kTile, 16);
+                if (!STATE) {
+                    #pragma unroll
+                    for (int f = 0; f < DK; f += 16)  // S^T Q^T
+                        tc::mma(tm + C::cOS, tm + C::cHi + f / 2, adv(dq, (f / 64) * 2 * kTile + (f % 64) * 2), id64, f > 0);
+                }
+                tc::commit(bar + kSqDone);
+            }
+            if (!(ok = wait(bar + kVnReady, c & 1, fail))) break;
+            tc::fence_after();
+            if (elect()) {
+                const uint64_t dp = sdesc(sb + C::oI + (c % C::NI) * kImage<DK> + kImgP, 16);
+                const uint64_t dk = sdesc(sb + C::oKQ + (c % C::NKQ) * C::KQ, 2 * kTile);
+                if (!STATE) {
+                    #pragma unroll
+                    for (int t = 0; t < 64; t += 16)  // Vn^T P^T
+                        tc::mma(tm + C::vn(c), tm + C::cVnH + t / 2, adv(dp, t * 2), id64, t > 0);
+                }
+                tc::commit(bar + kOpDone + (c & 1));
+                #pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    #pragma unroll
+                    for (int t = 0; t < 64; t += 16)  // S^T += (e Vn)^T K
+                        tc::mma(tm + C::cS, tm + (m ? C::cVeL : C::cVeH) + t / 2, adv(dk, t * 128), idS, 1);
+                tc::commit(bar + kSDone);
+                tc::commit(bar + kKqFree + c % C::NKQ);
+            }
+            // while the chain turns S into operands: the next chunk's U^T
+            if (c + 1 < n) {
+                ok = u_wait(c + 1);
                 if (ok) u_issue(c + 1);
             }
         }
@@ -654,48 +778,53 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         // ---------------------------------------------------------------- loads
         bool ok = true;
         int c = 0;
-        const int row0 = int(it.s.row);
         auto fix = [&](uint8_t* t, int m) {  // zero rows m .. 63 of a tile
             for (int x = lane; x < (64 - m) * 8; x += 32) *reinterpret_cast<uint4*>(t + m * 128 + x * 16) = make_uint4(0, 0, 0, 0);
         };
         for (; ok && c < n; ++c) {
             const int st = c % C::NKQ;
             uint8_t* kq = sm + C::oKQ + st * C::KQ;
-            const int t0 = int(it.s.start) + c * kChunk;
-            const int m = int(it.s.len - int64_t(c) * kChunk < kChunk ? it.s.len - int64_t(c) * kChunk : kChunk);
+            const int t0 = int(tok0) + c * kChunk, row0 = int(s.row);
+            const int64_t left = len - int64_t(c) * kChunk;
             // rows past the sequence: the TMA engine writes zeros past the tensor's
             // end; in a packed row they are the next sequence's and are zeroed here
-            const bool tail = d.offsets && m < kChunk;
+            const bool tail = d.offsets && left < kChunk;
             if (c >= C::NKQ && !(ok = wait(bar + kKqFree + st, (c / C::NKQ - 1) & 1, fail))) break;
             uint64_t* full = tail ? bar + kRaw : bar + kKqFull + st;
             if (elect()) {
                 mbar_expect_tx(full, C::KQ);
                 #pragma unroll
                 for (int f = 0; f < DK / 64; ++f) {
-                    tma_load_4d(smem_u32(kq) + f * 2 * kTile, &a.mk, f * 64, it.hk, t0, row0, full);
-                    tma_load_4d(smem_u32(kq) + f * 2 * kTile + kTile, &a.mq, f * 64, it.hk, t0, row0, full);
+                    tma_load_4d(smem_u32(kq) + f * 2 * kTile, &a.mk, f * 64, hk, t0, row0, full);
+                    tma_load_4d(smem_u32(kq) + f * 2 * kTile + kTile, &a.mq, f * 64, hk, t0, row0, full);
                 }
             }
             __syncwarp();
             if (tail) {
                 if (!(ok = wait(bar + kRaw, 0, fail))) break;
-                for (int f = 0; f < 2 * DK / 64; ++f) fix(kq + f * kTile, m);
+                for (int f = 0; f < 2 * DK / 64; ++f) fix(kq + f * kTile, int(left));
                 tc::fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) arrive(bar + kKqFull + st);
             }
+            if (c >= C::NI && !(ok = wait(bar + kOpRead + (c & 1), ((c - 2) >> 1) & 1, fail))) break;
+            if (elect()) {
+                mbar_expect_tx(bar + kTFull + c % C::NI, kImage<DK>);
+                bulk_g2s(image(c), a.images + ((slot0 + c) * d.Hv + h) * kImage<DK>, kImage<DK>, bar + kTFull + c % C::NI);
+            }
+            __syncwarp();
             if (c >= 1 && !(ok = wait(bar + kUDone, (c - 1) & 1, fail))) break;
             full = tail ? bar + kRaw : bar + kVFull;
             if (elect()) {
                 mbar_expect_tx(full, C::VB);
                 #pragma unroll
                 for (int f = 0; f < 2; ++f)
-                    tma_load_4d(sb + C::oV + f * kTile, &a.mv, DV == 128 ? f * 64 : 0, it.h, t0, row0, full);
+                    tma_load_4d(sb + C::oV + f * kTile, &a.mv, DV == 128 ? f * 64 : 0, h, t0, row0, full);
             }
             __syncwarp();
             if (tail) {
                 if (!(ok = wait(bar + kRaw, 1, fail))) break;
-                for (int f = 0; f < 2; ++f) fix(sm + C::oV + f * kTile, m);
+                for (int f = 0; f < 2; ++f) fix(sm + C::oV + f * kTile, int(left));
                 tc::fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) arrive(bar + kVFull);
@@ -706,32 +835,113 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         // is already over returns at once)
         for (int x = c > C::NKQ ? c - C::NKQ : 0; x < c; ++x)
             mbar_wait_bounded(bar + kKqFull + x % C::NKQ, (x / C::NKQ) & 1, kWaitFinal);
+        for (int x = c > C::NI ? c - C::NI : 0; x < c; ++x) mbar_wait_bounded(bar + kTFull + x % C::NI, (x / C::NI) & 1, kWaitFinal);
         if (c > 0) mbar_wait_bounded(bar + kVFull, (c - 1) & 1, kWaitFinal);
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 12) tc::dealloc(tm, 512);
+    if (warp == 20) tc::dealloc(tm, 512);
     if (threadIdx.x == 0 && s_fail) atomicExch(d.err, 7);
+}
+
+// The states at the segments' starts: S_(s+1) = M_s S_s + N_s along a
+// sequence, float32; N_0 already holds the initial state's part.  The result
+// replaces N_s.  A thread owns one column of S and a slice of its rows; 8
+// columns per CTA.
+template <int DK, int DV>
+__global__ void __launch_bounds__(256) delta_join_kernel(const __grid_constant__ ChunkArgs a) {
+    __shared__ float x[2][DK][8];
+    const DeltaArgs& d = a.d;
+    const int i = blockIdx.x, h = blockIdx.y, col = threadIdx.x % 8, r0 = threadIdx.x / 8, v0 = blockIdx.z * 8;
+    const Seq s = locate(d.offsets, d.T, i);
+    const int64_t c_all = (s.len + kChunk - 1) / kChunk, nseg = (c_all + a.seg_chunks - 1) / a.seg_chunks;
+    const int64_t g0 = (s.slot / a.seg_chunks + i) * d.Hv + h;
+    if (nseg < 3) return;
+    const float* N = a.seg_state + g0 * DK * DV + v0 + col;
+    for (int r = r0; r < DK; r += 32) x[0][r][col] = N[r * DV];
+    __syncthreads();
+    for (int64_t g = 1; g + 1 < nseg; ++g) {
+        const float* M = a.seg_trans + (g0 + g * d.Hv) * DK * DK;
+        float* out = a.seg_state + (g0 + g * d.Hv) * DK * DV + v0 + col;
+        const int b = int(g & 1);
+        float acc[DK / 32];
+        #pragma unroll
+        for (int q = 0; q < DK / 32; ++q) acc[q] = out[(r0 + 32 * q) * DV];
+        for (int k = 0; k < DK; k += 4) {
+            #pragma unroll
+            for (int q = 0; q < DK / 32; ++q) {
+                const float4 m = *reinterpret_cast<const float4*>(M + (r0 + 32 * q) * DK + k);
+                acc[q] = fmaf(m.x, x[b ^ 1][k][col], acc[q]);
+                acc[q] = fmaf(m.y, x[b ^ 1][k + 1][col], acc[q]);
+                acc[q] = fmaf(m.z, x[b ^ 1][k + 2][col], acc[q]);
+                acc[q] = fmaf(m.w, x[b ^ 1][k + 3][col], acc[q]);
+            }
+        }
+        #pragma unroll
+        for (int q = 0; q < DK / 32; ++q) {
+            x[b][r0 + 32 * q][col] = acc[q];
+            out[(r0 + 32 * q) * DV] = acc[q];
+        }
+        __syncthreads();
+    }
+}
+
+template <typename K>
+cudaError_t opt_in(K fn, size_t smem, PerDevice& cache) {
+    int* slot = cache.slot();
+    if (!slot) return cudaErrorInvalidDevice;
+    if (!*slot) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+        *slot = 1;
+    }
+    return cudaSuccess;
 }
 
 template <int DT, int DK, int DV>
 cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
-    static PerDevice cache;
-    const size_t smem = FwdCfg<DK, DV>::BYTES + 1024;
-    int* slot = cache.slot();
-    if (!slot) return cudaErrorInvalidDevice;
-    if (!*slot) {
-        cudaError_t e = cudaFuncSetAttribute(delta_fwd_kernel<DT, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(smem));
-        if (e != cudaSuccess) return e;
-        *slot = 1;
+    static PerDevice c0, c1, c2;
+    constexpr size_t sp = PrepCfg<DK>::BYTES, sf = FwdCfg<DK, DV>::BYTES;
+    static_assert(sf <= 232448 && (sp + 1024) * PrepCfg<DK>::PER_SM <= 233472, "shared memory");
+    cudaError_t e = opt_in(delta_prep_kernel<DT, DK>, sp, c0);
+    if (e == cudaSuccess) e = opt_in(delta_fwd_kernel<DT, DK, DV, false>, sf, c1);
+    if (e == cudaSuccess) e = opt_in(delta_fwd_kernel<DT, DK, DV, true>, sf, c2);
+    if (e != cudaSuccess) return e;
+    const unsigned H = unsigned(a.d.Hv);
+    const int64_t items = a.slots * a.d.Hv, most = int64_t(a.sms) * PrepCfg<DK>::PER_SM;
+    delta_prep_kernel<DT, DK><<<unsigned(items < most ? items : most), 256, sp, st>>>(a);
+    if (a.segments > a.d.nseq) {
+        delta_fwd_kernel<DT, DK, DV, true><<<dim3(unsigned(a.segments), H, 2), FwdCfg<DK, DV>::THREADS, sf, st>>>(a);
+        delta_join_kernel<DK, DV><<<dim3(unsigned(a.d.nseq), H, DV / 8), 256, 0, st>>>(a);
     }
-    delta_fwd_kernel<DT, DK, DV><<<dim3(unsigned(a.d.nseq), unsigned(a.d.Hv)), FwdCfg<DK, DV>::THREADS, smem, st>>>(a);
+    delta_fwd_kernel<DT, DK, DV, false><<<dim3(unsigned(a.segments), H), FwdCfg<DK, DV>::THREADS, sf, st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+// Segments.  A sequence's chunks follow one another, so few long sequences
+// leave SMs idle; cut into segments they cost three walks instead of one: the
+// segments' end states from zero and their transition matrices (side by side),
+// a short join, then the outputs from the joined states.  Taken when the rows
+// would fill at most a fifth of the SMs and a segment keeps 16 chunks.
+void plan_segments(ChunkArgs* a, int sms) {
+    const DeltaArgs& d = a->d;
+    a->slots = chunk_slots(d.B, d.T, d.nseq);
+    a->sms = sms;
+    const int64_t rows = int64_t(d.nseq) * d.Hv;
+    int64_t per = rows > 0 ? sms / rows : 1;                         // segments of a row
+    const int64_t chunks = d.nseq ? (d.B * d.T / d.nseq + kChunk - 1) / kChunk : 0;  // of a row (their mean when packed)
+    if (per > chunks / 16) per = chunks / 16;
+    if (per < 5) {
+        a->seg_chunks = a->slots + 1;  // one segment each
+        a->segments = d.nseq;
+        return;
+    }
+    a->seg_chunks = (chunks + per - 1) / per;
+    a->segments = a->slots / a->seg_chunks + d.nseq;
+}
 
 cudaError_t launch_delta_forward(const ChunkArgs& a, int dt, int dk, int dv, cudaStream_t st) {
     if (dt == FFTCONV_F16) {

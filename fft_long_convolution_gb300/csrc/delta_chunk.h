@@ -15,7 +15,19 @@ struct ChunkArgs {
     // what the backward needs, per chunk slot and value head, or null: S^T at
     // the chunk's start [DV][DK], Vn^T [DV][64], T [64][64], all 16-bit
     uint16_t *saved_s, *saved_v, *saved_t;
+    // scratch: an image per chunk slot and value head, and per segment slot and
+    // value head a state [DK][DV] and a transition matrix [DK][DK]
+    uint8_t* images;
+    float *seg_state, *seg_trans;
+    int64_t slots, segments, seg_chunks;
+    int sms;
 };
+
+// Bytes of an image.
+constexpr size_t prep_image(int dk) { return 3 * 8192 + 1024 + size_t(dk) * 256; }
+
+// Sets slots, segments and seg_chunks from the sizes in a->d.
+void plan_segments(ChunkArgs* a, int sms);
 
 cudaError_t launch_delta_forward(const ChunkArgs& a, int dt, int dk, int dv, cudaStream_t st);
 

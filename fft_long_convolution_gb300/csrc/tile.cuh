@@ -85,14 +85,59 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     return __all_sync(0xffffffffu, got);
 }
 
+// Packed float32 pairs.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n sub.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 z, x, y, z;\n mov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) {
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+
+// 2^x; 0 below the normal range.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // x = hi + lo in two 16-bit values each (about 16 significant bits for bf16),
 // for a pair packed low half first.
 template <int DT>
-__device__ __forceinline__ void split(float x0, float x1, uint32_t* hi, uint32_t* lo) {
-    const uint32_t h = Op<DT>::pack(x0, x1);
+__device__ __forceinline__ void split(float2 x, uint32_t* hi, uint32_t* lo) {
+    const uint32_t h = Op<DT>::pack(x.x, x.y);
     const cpx f = Op<DT>::unpack(h);
+    const float2 r = sub2(x, make_float2(f.r, f.i));
     *hi = h;
-    *lo = Op<DT>::pack(x0 - f.r, x1 - f.i);
+    *lo = Op<DT>::pack(r.x, r.y);
+}
+
+// Load 16 consecutive columns of this thread's lane (call wait_ld before use).
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
 // Store 32 consecutive columns of this thread's lane.
@@ -106,6 +151,36 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+
+// Store 4 or 8 consecutive columns of this thread's lane.
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+    if constexpr (N == 8) st8(taddr, r);
+    else if constexpr (N == 16) tc::st16(taddr, r);
+    else st32(taddr, r);
+}
+
+template <int N>
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+    if constexpr (N == 16) ld16(taddr, r);
+    else tc::ld32x32b_x32(taddr, r);
+}
+
+// One-dimensional bulk copy shared -> global, and the wait after which the
+// shared memory may be reused.
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+constexpr uint32_t kWaitLimitTile = 1u << 22;
 
 }  // namespace tile
 }  // namespace fftconv
