@@ -530,7 +530,7 @@ extern "C" fftconv_status_t fftconv_delta_forward(fftconv_delta_t p, const fftco
     a.state_in = state_in;
     a.state_out = state_out;
     const FwdScratch w(p, d.B, d.T, d.Hv, d.nseq);
-    if (w.c.slots >= (int64_t(1) << 31)) return FFTCONV_ERR_UNSUPPORTED;
+    if (w.c.slots >= (int64_t(1) << 30) / d.Hv) return FFTCONV_ERR_UNSUPPORTED;
     a.slots = w.c.slots;
     a.segments = w.c.segments;
     a.seg_chunks = w.c.seg_chunks;

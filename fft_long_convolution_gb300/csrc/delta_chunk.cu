@@ -195,20 +195,30 @@ __device__ __forceinline__ bool find_segment(const DeltaArgs& d, int64_t L, int6
 template <int DK>
 struct PrepCfg {
     static constexpr int LD = 68;                          // row pitch of the float32 64 x 64 scratch
-    static constexpr uint32_t KQ = (DK / 64) * 2 * kTile;  // [feature block][K rows | Q rows]; then W^T
-    static constexpr uint32_t oI = KQ, oA = oI + kImgW, oL = oA + 64 * LD * 4, oBar = oL + 224 * 4, BYTES = oBar + 64;
-    static constexpr int PER_SM = 3;
+    static constexpr uint32_t KQ = (DK / 64) * 2 * kTile;  // [feature block][K rows | Q rows]
+    // T beta is staged where Q was (two tiles), W where the scratch was
+    static constexpr uint32_t oTb = DK == 128 ? kTile : 2 * kTile, sTb = DK == 128 ? 2 * kTile : kTile;
+    static constexpr uint32_t oA = 4 * kTile, oL = oA + 64 * LD * 4, oItem = oL + 288 * 4, oBar = oItem + 64, BYTES = oBar + 64;
+    static constexpr int PER_SM = 4;
+};
+
+// A chunk of a value head: where its tokens are and where its image goes.
+struct PrepItem {
+    int row, t0, m, h;  // m tokens; 0: no more items
+    int64_t at;
 };
 
 // T, W, P and the decays of one chunk and value head at a time.  Bound: the
-// latency of its steps (each waits for the last; the inverse alone has eleven),
-// covered by three CTAs per SM.
+// latency of its steps (each waits for the last, eleven in the inverse alone),
+// covered by four CTAs per SM and by fetching the next chunk's tiles and gates
+// under the current one's last steps.
 template <int DT, int DK>
 __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(const __grid_constant__ ChunkArgs a) {
     using C = PrepCfg<DK>;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);  // loads, K K^T, W
+    PrepItem* items = reinterpret_cast<PrepItem*>(sm + C::oItem);
     const DeltaArgs& d = a.d;
     const int p = threadIdx.x, w = __shfl_sync(0xffffffffu, p / 32, 0), lane = p % 32;
     if (sb & 1023) {  // not with the present layout of the window
@@ -221,78 +231,106 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
     }
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + 3);
     if (w == 1) tc::alloc(s_tmem, 64);
+    const int count = int(a.slots) * d.Hv;
+    int next = blockIdx.x;
+    // the next item that has tokens (warp 3)
+    auto find = [&](PrepItem* to) {
+        PrepItem it{0, 0, 0, 0, 0};
+        for (; next < count; next += gridDim.x) {
+            const int slot = next / d.Hv;
+            Seq s;
+            int si;
+            int64_t ch;
+            if (!find_chunk(d, slot, &s, &si, &ch)) continue;
+            const int64_t left = s.len - ch * kChunk;
+            it = {int(s.row), int(s.start + ch * kChunk), int(left < kChunk ? left : kChunk), next - slot * d.Hv, next};
+            next += gridDim.x;
+            break;
+        }
+        if (lane == 0) *to = it;
+    };
+    auto load = [&](const PrepItem& it) {  // one warp
+        if (elect()) {
+            mbar_expect_tx(bar, C::KQ);
+            #pragma unroll
+            for (int f = 0; f < DK / 64; ++f) {
+                tma_load_4d(sb + f * 2 * kTile, &a.mk, f * 64, it.h / d.group, it.t0, it.row, bar);
+                tma_load_4d(sb + f * 2 * kTile + kTile, &a.mq, f * 64, it.h / d.group, it.t0, it.row, bar);
+            }
+        }
+        __syncwarp();
+    };
+    float g[2], e[2];  // log decays and betas of tokens 2 lane and 2 lane + 1 (warp 2)
+    auto fetch = [&](const PrepItem& it) {
+        #pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t t = it.t0 + 2 * lane + u;
+            g[u] = e[u] = 0.0f;  // past the end: no decay, no update
+            if (2 * lane + u < it.m) {
+                g[u] = load16<DT>(d.g, it.row * d.g.b + t * d.g.t + it.h * d.g.h);
+                e[u] = load16<DT>(d.beta, it.row * d.beta.b + t * d.beta.t + it.h * d.beta.h);
+            }
+        }
+    };
+    if (w == 3) find(items);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(s_tmem);
     const uint32_t lanes = tm + (uint32_t(32 * (w & 3)) << 16);
     float* A = reinterpret_cast<float*>(sm + C::oA);
-    // b log2(e), beta; decays between 16-token blocks (below)
-    float *sbv = reinterpret_cast<float*>(sm + C::oL), *sbe = sbv + 64, *sE2 = sbe + 64, *sE1 = sE2 + 64;
+    // b log2(e), beta, -G; decays between 16-token blocks (below)
+    float *sbv = reinterpret_cast<float*>(sm + C::oL), *sbe = sbv + 64, *sng = sbe + 64, *sE2 = sng + 64, *sE1 = sE2 + 64;
     auto sync = [] { __syncthreads(); };
-    const int64_t items = a.slots * d.Hv;
-    uint32_t par = 0;
+    const int row = 32 * (w & 3) + lane, i = row & 63, up = (row >> 5) & 1, half = w >> 2;
+    const bool isp = row >= 64;
+    if (items[0].m && w == 3) load(items[0]);
+    if (w == 2) fetch(items[0]);
     bool ok = true;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t slot = item / d.Hv;
-        const int h = int(item - slot * d.Hv);
-        Seq s;
-        int si;
-        int64_t ch;
-        if (!find_chunk(d, slot, &s, &si, &ch)) continue;
-        const int64_t left = s.len - ch * kChunk, t0 = s.start + ch * kChunk;
-        const int m = int(left < kChunk ? left : kChunk);
-        if (p == 0) {
-            bulk_wait_read();  // the last images have left shared memory
-            mbar_expect_tx(bar, C::KQ);
-            #pragma unroll
-            for (int f = 0; f < DK / 64; ++f) {
-                tma_load_4d(sb + f * 2 * kTile, &a.mk, f * 64, h / d.group, int(t0), int(s.row), bar);
-                tma_load_4d(sb + f * 2 * kTile + kTile, &a.mq, f * 64, h / d.group, int(t0), int(s.row), bar);
-            }
-        }
+    uint32_t k = 0;
+    for (; items[k & 1].m; ++k) {
+        const PrepItem it = items[k & 1];
+        const uint32_t par = k & 1;
+        uint8_t* image = a.images + it.at * kImage<DK>;
         if (w == 2) {
-            // running sum of the log decays, in units of log 2; past the end: no
-            // decay, no update
+            // running sum of the log decays, in units of log 2
             constexpr float kLog2e = 1.44269504088896340736f;
-            float g[2] = {}, e[2] = {};
-            #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = 2 * lane + u;
-                if (t < m) {
-                    g[u] = kLog2e * log_decay(load16<DT>(d.g, s.row * d.g.b + (t0 + t) * d.g.t + h * d.g.h));
-                    e[u] = load16<DT>(d.beta, s.row * d.beta.b + (t0 + t) * d.beta.t + h * d.beta.h);
-                }
-            }
-            float x = g[0] + g[1];
+            const float g0 = kLog2e * log_decay(g[0]), g1 = kLog2e * log_decay(g[1]);
+            float x = g0 + g1;
             #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const float v = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += v;
             }
-            *reinterpret_cast<float2*>(sbv + 2 * lane) = make_float2(x - g[1], x);
+            *reinterpret_cast<float2*>(sbv + 2 * lane) = make_float2(x - g1, x);
             *reinterpret_cast<float2*>(sbe + 2 * lane) = make_float2(e[0], e[1]);
         }
+        if (p == 0) bulk_wait_read();  // the last W has left the scratch
+        tc::fence_before();
         sync();
         // D_ij for i >= 32 > j is E1_i E2_j with both factors at most 1: the decay
         // from the first token of i's 16-token block, and up to it
         if (p < 64) {
-            const float b = sbv[p];
-            float* gt = reinterpret_cast<float*>(sm + C::oI + kImgE);
+            const float b = sbv[p], G = exp2_fast(b);
+            float* gt = reinterpret_cast<float*>(image + kImgE);
             gt[p] = exp2_fast(sbv[63] - b);
-            gt[64 + p] = d.scale * exp2_fast(b);
-            if (p == 63) gt[128] = exp2_fast(b);
-        } else if (p < 128) {
-            const int q = p - 64;
-            sE2[q] = exp2_fast(sbv[32 + 16 * (q >> 5)] - sbv[q & 31]);
-        } else if (p < 160) {
+            gt[64 + p] = d.scale * G;
+            if (p == 63) gt[128] = G;
+            sng[p] = -G;
+        } else if (w == 3) {
+            find(items + (~k & 1));
+        } else if (p >= 128 && p < 192) {
             const int q = p - 128;
+            sE2[q] = exp2_fast(sbv[32 + 16 * (q >> 5)] - sbv[q & 31]);
+        } else if (p >= 192 && p < 224) {
+            const int q = p - 192;
             sE1[q] = exp2_fast(sbv[32 + q] - sbv[32 + (q & 16)]);
         }
         ok = mbar_wait_bounded(bar, par, kWaitLimitTile);
-        if (d.offsets && m < kChunk) {
+        if (d.offsets && it.m < kChunk) {
             // rows past the sequence are the next one's: zero them (past the
             // tensor's end the TMA engine has)
+            const int m = it.m;
             for (int x = p; x < (64 - m) * 8 * (DK / 32); x += 256) {
                 const int f = x / ((64 - m) * 8), y = x % ((64 - m) * 8);
                 *reinterpret_cast<uint4*>(sm + f * kTile + m * 128 + y * 16) = make_uint4(0, 0, 0, 0);
@@ -318,11 +356,9 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
         tc::fence_after();
         // K K^T in lanes 0-63, Q K^T in lanes 64-127; warps 0-3 take columns 0-31,
         // warps 4-7 the others
-        const int row = 32 * (w & 3) + lane, i = row & 63, up = (row >> 5) & 1, half = w >> 2;
-        const bool isp = row >= 64;
-        const float f = isp ? d.scale : sbe[i];
-        uint8_t* prow = sm + C::oI + kImgP + i * 128;
+        uint8_t* prow = image + kImgP + i * 128;
         if (up || !half) {
+            const float f = isp ? d.scale : sbe[i];
             uint32_t x[32];
             const int j0 = half * 32;
             tc::ld32x32b_x32(lanes + j0, x);
@@ -332,9 +368,9 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
                 const float* e2 = sE2 + (i & 16) * 2;
                 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
-                    const float4 e = *reinterpret_cast<const float4*>(e2 + j);
-                    const float2 u = mul2(mul2(make_float2(fe, fe), make_float2(e.x, e.y)), pair(x[j], x[j + 1]));
-                    const float2 v = mul2(mul2(make_float2(fe, fe), make_float2(e.z, e.w)), pair(x[j + 2], x[j + 3]));
+                    const float4 c = *reinterpret_cast<const float4*>(e2 + j);
+                    const float2 u = mul2(mul2(make_float2(fe, fe), make_float2(c.x, c.y)), pair(x[j], x[j + 1]));
+                    const float2 v = mul2(mul2(make_float2(fe, fe), make_float2(c.z, c.w)), pair(x[j + 2], x[j + 3]));
                     x[j] = __float_as_uint(u.x); x[j + 1] = __float_as_uint(u.y);
                     x[j + 2] = __float_as_uint(v.x); x[j + 3] = __float_as_uint(v.y);
                 }
@@ -370,12 +406,12 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
             #pragma unroll
             for (int j = 4; j < 8; ++j) *reinterpret_cast<uint4*>(prow + ((j ^ (i & 7)) * 16)) = make_uint4(0, 0, 0, 0);
         }
+        if (w == 2) fetch(items[~k & 1]);
         tc::fence_before();
         sync();
         inverse64<C::LD>(A, p, w, lane, sync);
-        // T with its columns times beta, and times -beta G (over the scratch, once
-        // everyone has read it), as two 16-bit parts each
-        const int64_t at = (s.slot + ch) * d.Hv + h;
+        // T with its columns times beta (staged over Q for the image), and times
+        // -beta G (over the scratch, once everyone has read it), as two 16-bit parts
         {
             const int r = p & 63, h0 = (p >> 6) * 16;
             float4 t[4];
@@ -389,30 +425,33 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
                 for (int j = 0; j < 8; j += 4) {
                     const int jj = h0 + j0 + j;
                     const float4 y = t[(j0 + j) / 4];
-                    const float4 x = *reinterpret_cast<const float4*>(sbe + jj), b = *reinterpret_cast<const float4*>(sbv + jj);
+                    const float4 x = *reinterpret_cast<const float4*>(sbe + jj), b = *reinterpret_cast<const float4*>(sng + jj);
                     // the scratch above the diagonal holds intermediate products
                     const float2 y0 = make_float2(jj <= r ? y.x : 0.0f, jj + 1 <= r ? y.y : 0.0f);
                     const float2 y1 = make_float2(jj + 2 <= r ? y.z : 0.0f, jj + 3 <= r ? y.w : 0.0f);
                     const float2 x0 = mul2(y0, make_float2(x.x, x.y)), x1 = mul2(y1, make_float2(x.z, x.w));
                     split<DT>(x0, &v[0][j / 2], &v[1][j / 2]);
                     split<DT>(x1, &v[0][j / 2 + 1], &v[1][j / 2 + 1]);
-                    split<DT>(mul2(x0, make_float2(-exp2_fast(b.x), -exp2_fast(b.y))), &v[2][j / 2], &v[3][j / 2]);
-                    split<DT>(mul2(x1, make_float2(-exp2_fast(b.z), -exp2_fast(b.w))), &v[2][j / 2 + 1], &v[3][j / 2 + 1]);
+                    split<DT>(mul2(x0, make_float2(b.x, b.y)), &v[2][j / 2], &v[3][j / 2]);
+                    split<DT>(mul2(x1, make_float2(b.z, b.w)), &v[2][j / 2 + 1], &v[3][j / 2 + 1]);
                     ts[j / 2] = Op<DT>::pack(y0.x, y0.y);
                     ts[j / 2 + 1] = Op<DT>::pack(y1.x, y1.y);
                 }
                 const int pos = r * 128 + ((((h0 + j0) / 8) ^ (r & 7)) * 16);
                 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<uint4*>(sm + (q < 2 ? C::oI + kImgT + q * kTile : C::oA + (q - 2) * kTile) + pos) =
+                    *reinterpret_cast<uint4*>(sm + (q < 2 ? C::oTb + q * C::sTb : C::oA + (q - 2) * kTile) + pos) =
                         make_uint4(v[q][0], v[q][1], v[q][2], v[q][3]);
                 if (a.saved_t)
-                    *reinterpret_cast<uint4*>(a.saved_t + (at * 64 + r) * 64 + h0 + j0) = make_uint4(ts[0], ts[1], ts[2], ts[3]);
+                    *reinterpret_cast<uint4*>(a.saved_t + (it.at * 64 + r) * 64 + h0 + j0) = make_uint4(ts[0], ts[1], ts[2], ts[3]);
             }
         }
         tc::fence_proxy_async();
         sync();
-        if (p == 0) bulk_s2g(a.images + at * kImage<DK>, sb + C::oI, kImgW);
+        if (p == 96) {
+            bulk_s2g(image + kImgT, sb + C::oTb, kTile);
+            bulk_s2g(image + kImgT + kTile, sb + C::oTb + C::sTb, kTile);
+        }
         if (w == 0) {  // -W^T = K^T (-T beta G)^T
             constexpr uint32_t id = tc::idesc(DT, 128, 64) | kMnA;
             const uint64_t da = sdesc(sb, DK == 128 ? 2 * kTile : kTile), db = sdesc(sb + C::oA, 16);
@@ -429,31 +468,51 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
         ok = mbar_wait_bounded(bar + 2, par, kWaitLimitTile);
         if (!(ok = !__syncthreads_or(!ok))) break;
         tc::fence_after();
+        if (w == 3) {  // K, Q and what was staged over Q have been read
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+            if (items[~k & 1].m) load(items[~k & 1]);
+        }
+        // W^T through the scratch, one part after the other
+        uint32_t lo[16];
+        uint8_t* q = sm + C::oA + row * 128;
         if (row < DK) {
-            uint32_t x[32], hi[16], lo[16];
-            tc::ld32x32b_x32(lanes + half * 32, x);
-            tc::wait_ld();
             #pragma unroll
-            for (int j = 0; j < 16; ++j) split<DT>(pair(x[2 * j], x[2 * j + 1]), &hi[j], &lo[j]);
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint8_t* q = sm + row * 128 + ((half * 4 + j) ^ (row & 7)) * 16;
-                *reinterpret_cast<uint4*>(q) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-                *reinterpret_cast<uint4*>(q + DK * 128) = make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
+            for (int j0 = 0; j0 < 32; j0 += 16) {
+                uint32_t x[16], hi[8];
+                ld16(lanes + half * 32 + j0, x);
+                tc::wait_ld();
+                #pragma unroll
+                for (int j = 0; j < 8; ++j) split<DT>(pair(x[2 * j], x[2 * j + 1]), &hi[j], &lo[j0 / 2 + j]);
+                #pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<uint4*>(q + ((half * 4 + j0 / 8 + j) ^ (row & 7)) * 16) =
+                        make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
             }
         }
         tc::fence_proxy_async();
         tc::fence_before();
         sync();
-        if (p == 0) bulk_s2g(a.images + at * kImage<DK> + kImgW, sb, DK * 256);
-        par ^= 1;
-    }
-    if (p == 0) {
-        bulk_wait_read();
-        if (!ok) {
-            atomicExch(d.err, 7);
-            mbar_wait_bounded(bar, par, kWaitFinal);  // the copies have landed before the CTA leaves
+        if (p == 0) {
+            bulk_s2g(image + kImgW, sb + C::oA, DK * 128);
+            bulk_wait_read();
         }
+        sync();
+        if (row < DK) {
+            #pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(q + ((half * 4 + j) ^ (row & 7)) * 16) =
+                    make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
+        }
+        tc::fence_proxy_async();
+        sync();
+        if (p == 0) bulk_s2g(image + kImgW + DK * 128, sb + C::oA, DK * 128);
+    }
+    if (p == 0) bulk_wait_read();
+    if (p == 96) bulk_wait_read();
+    if (p == 0 && !ok) {
+        atomicExch(d.err, 7);
+        mbar_wait_bounded(bar, k & 1, kWaitFinal);  // the copies have landed before the CTA leaves
     }
     tc::fence_before();
     __syncthreads();
