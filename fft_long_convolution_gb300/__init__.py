@@ -484,9 +484,9 @@ class DeltaRule:
         a.scale = self.Dk ** -0.5 if scale is None else float(scale)
         return a
 
-    def _scratch(self, a, backward, device):
+    def _scratch(self, a, which, device):
         import torch
-        n = int(lib().fftconv_delta_scratch_bytes(self._h, a.B, a.T, a.Hk, a.Hv, a.nseq, int(backward)))
+        n = int(lib().fftconv_delta_scratch_bytes(self._h, a.B, a.T, a.Hk, a.Hv, a.nseq, which))
         return (torch.empty(n, dtype=torch.uint8, device=device) if n else None), n
 
     def forward(self, q, k, v, g, beta, state=None, offsets=None, scale=None, save=False, stream=None):
@@ -505,7 +505,7 @@ class DeltaRule:
             if save:
                 n = int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq))
                 saved = torch.empty(n, dtype=torch.uint8, device=v.device)
-            scratch, n = self._scratch(a, False, v.device)
+            scratch, n = self._scratch(a, 2 if save else 0, v.device)
             _check(lib().fftconv_delta_forward(self._h, ctypes.byref(a), sin, _view(o, "o", v.dtype, 4), _ptr(out),
                                                _ptr(saved), _ptr(scratch), n, _stream(stream)),
                    "fftconv_delta_forward")
@@ -527,7 +527,7 @@ class DeltaRule:
         with _on(stream):
             dq, dk, dv, dg, dbeta = (torch.empty(t.shape, dtype=dt, device=t.device) for t in (q, k, v, g, beta))
             dst = torch.empty(shape, dtype=torch.float32, device=v.device)
-            scratch, n = self._scratch(a, True, v.device)
+            scratch, n = self._scratch(a, 1, v.device)
             _check(lib().fftconv_delta_backward(
                 self._h, ctypes.byref(a), _view(do, "do", dt, 4), dsin, sv, _view(dq, "dq", dt, 4),
                 _view(dk, "dk", dt, 4), _view(dv, "dv", dt, 4), _view(dg, "dg", dt, 3), _view(dbeta, "dbeta", dt, 3),

@@ -128,167 +128,6 @@ __global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
     for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(a.sout + sbase + r * DV) = S[r];
 }
 
-// ------------------------------------------------------------ gradients, token by token
-//
-// Reverse recurrence with the states of a chunk recomputed from the saved
-// state at its start:
-//   d1 = dS_t + scale q do^T;  dq = scale S_t do;  du = d1^T k
-//   dk = d1 u - S~ (beta du);  dv = beta du;  dbeta = du.(v - S~^T k)
-//   d2 = d1 - k (beta du)^T;  dg = <d2, S~>;  dS_(t-1) = exp(g) d2
-// One CTA of 256 threads per sequence and value head, S~ and dS in shared
-// memory, everything float32: the simple form.
-struct GradArgs {
-    DeltaArgs d;
-    View dout, dv, dg, dbeta;
-    const float* dsout;  // gradient of the final states, or null
-    float* dsin;         // gradient of the initial states, or null
-    const uint16_t* saved;  // S^T at the chunk starts [slot][Hv][DV][DK]
-    float* states;       // [CTA][64][DK*DV]: the states before each token of a chunk
-    float *dqh, *dkh;    // [B T][Hv][DK] per value head
-};
-
-template <int DT, int DK, int DV>
-__global__ void __launch_bounds__(256) token_grad_kernel(const GradArgs a) {
-    extern __shared__ float sm[];
-    float* S = sm;               // S~ of the current token
-    float* R = S + DK * DV;      // dS
-    float *kq = R + DK * DV, *qq = kq + DK, *vv = qq + DK, *dd = vv + DV, *uu = dd + DV, *du = uu + DV,
-          *part = du + DV;       // [256]
-    const DeltaArgs& d = a.d;
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int i = blockIdx.x, h = blockIdx.y, hk = h / d.group;
-    const Seq s = locate(d.offsets, d.T, i);
-    float* st = a.states + (int64_t(i) * d.Hv + h) * kChunk * DK * DV;
-    const int64_t sb = (int64_t(i) * d.Hv + h) * DK * DV;
-    const int c = tid % DV, p0 = tid / DV;
-    constexpr int NP = 256 / DV;
-    for (int x = tid; x < DK * DV; x += 256) R[x] = a.dsout ? a.dsout[sb + x] : 0.0f;
-    const int64_t nch = (s.len + kChunk - 1) / kChunk;
-    auto load = [&](int64_t t) {  // token t of the sequence; returns its decay and beta through part
-        const int64_t tt = s.start + t;
-        for (int x = tid; x < DK; x += 256) {
-            kq[x] = load16<DT>(d.k, s.row * d.k.b + tt * d.k.t + hk * d.k.h + x);
-            qq[x] = load16<DT>(d.q, s.row * d.q.b + tt * d.q.t + hk * d.q.h + x);
-        }
-        for (int x = tid; x < DV; x += 256) {
-            vv[x] = load16<DT>(d.v, s.row * d.v.b + tt * d.v.t + h * d.v.h + x);
-            dd[x] = load16<DT>(a.dout, s.row * a.dout.b + tt * a.dout.t + h * a.dout.h + x);
-        }
-    };
-    // sums over the rows: out[c] = sum_r vec[r] * M[r][c]
-    auto colsum = [&](const float* vec, const float* M) {
-        float v = 0.0f;
-        for (int r = p0; r < DK; r += NP) v = fmaf(vec[r], M[r * DV + c], v);
-        part[tid] = v;
-        __syncthreads();
-        v = 0.0f;
-        for (int j = 0; j < NP; ++j) v += part[j * DV + c];
-        __syncthreads();
-        return v;
-    };
-    for (int64_t ch = nch - 1; ch >= 0; --ch) {
-        const int64_t t0 = ch * kChunk;
-        const int n = int(s.len - t0 < kChunk ? s.len - t0 : kChunk);
-        __syncthreads();
-        const uint16_t* sv = a.saved + ((s.slot + ch) * d.Hv + h) * DK * DV;
-        for (int x = tid; x < DK * DV; x += 256) S[(x % DK) * DV + x / DK] = Op<DT>::unpack(sv[x]).r;
-        __syncthreads();
-        for (int j = 0; j < n; ++j) {
-            load(t0 + j);
-            const int64_t tt = s.start + t0 + j;
-            const float al = expf(log_decay(load16<DT>(d.g, s.row * d.g.b + tt * d.g.t + h * d.g.h)));
-            const float be = load16<DT>(d.beta, s.row * d.beta.b + tt * d.beta.t + h * d.beta.h);
-            for (int x = tid; x < DK * DV; x += 256) {
-                st[int64_t(j) * DK * DV + x] = S[x];
-                S[x] *= al;
-            }
-            __syncthreads();
-            const float u = be * (vv[c] - colsum(kq, S));
-            for (int r = p0; r < DK; r += NP) S[r * DV + c] = fmaf(kq[r], u, S[r * DV + c]);
-            __syncthreads();
-        }
-        for (int j = n - 1; j >= 0; --j) {
-            load(t0 + j);
-            const int64_t tt = s.start + t0 + j;
-            const float al = expf(log_decay(load16<DT>(d.g, s.row * d.g.b + tt * d.g.t + h * d.g.h)));
-            const float be = load16<DT>(d.beta, s.row * d.beta.b + tt * d.beta.t + h * d.beta.h);
-            __syncthreads();
-            for (int x = tid; x < DK * DV; x += 256) {
-                S[x] = al * st[int64_t(j) * DK * DV + x];
-                R[x] = fmaf(d.scale * qq[x / DV], dd[x % DV], R[x]);
-            }
-            __syncthreads();
-            const float miss = vv[c] - colsum(kq, S);
-            const float dub = colsum(kq, R);
-            if (p0 == 0) {
-                uu[c] = be * miss;
-                du[c] = dub;
-                store16<DT>(a.dv, s.row * a.dv.b + tt * a.dv.t + h * a.dv.h + c, be * dub);
-            }
-            part[tid] = p0 == 0 ? dub * miss : 0.0f;
-            __syncthreads();
-            if (warp == 0) {
-                float v = 0.0f;
-                for (int x = lane; x < 256; x += 32) v += part[x];
-                for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane == 0) store16<DT>(a.dbeta, s.row * a.dbeta.b + tt * a.dbeta.t + h * a.dbeta.h, v);
-            }
-            // rows of dq and dk; dg is the sum of <d2, S~> over them
-            float dgp = 0.0f;
-            const int64_t ho = ((s.row * d.T + tt) * d.Hv + h) * DK;
-            for (int r = warp; r < DK; r += 8) {
-                float sdo = 0.0f, ru = 0.0f, sdu = 0.0f, rs = 0.0f, udo = 0.0f;
-                for (int x = lane; x < DV; x += 32) {
-                    const float sx = S[r * DV + x], rx = R[r * DV + x];
-                    sdo = fmaf(sx, dd[x], sdo);
-                    udo = fmaf(uu[x], dd[x], udo);
-                    ru = fmaf(rx, uu[x], ru);
-                    sdu = fmaf(sx, be * du[x], sdu);
-                    rs = fmaf(rx - kq[r] * be * du[x], sx, rs);
-                }
-                for (int o = 16; o; o >>= 1) {
-                    sdo += __shfl_xor_sync(0xffffffffu, sdo, o);
-                    udo += __shfl_xor_sync(0xffffffffu, udo, o);
-                    ru += __shfl_xor_sync(0xffffffffu, ru, o);
-                    sdu += __shfl_xor_sync(0xffffffffu, sdu, o);
-                    rs += __shfl_xor_sync(0xffffffffu, rs, o);
-                }
-                if (lane == 0) {
-                    a.dqh[ho + r] = d.scale * fmaf(kq[r], udo, sdo);
-                    a.dkh[ho + r] = ru - sdu;
-                }
-                dgp += rs;
-            }
-            __syncthreads();
-            if (lane == 0) part[warp] = dgp;
-            __syncthreads();
-            if (tid == 0) {
-                float v = 0.0f;
-                for (int w = 0; w < 8; ++w) v += part[w];
-                store16<DT>(a.dg, s.row * a.dg.b + tt * a.dg.t + h * a.dg.h, v);
-            }
-            for (int x = tid; x < DK * DV; x += 256) R[x] = al * (R[x] - kq[x / DV] * be * du[x % DV]);
-            __syncthreads();
-        }
-    }
-    __syncthreads();
-    if (a.dsin)
-        for (int x = tid; x < DK * DV; x += 256) a.dsin[sb + x] = R[x];
-}
-
-// dq, dk [token][Hk][DK] = the sum over a key head's value heads.
-template <int DT>
-__global__ void head_sum_kernel(const float* x, View y, int64_t B, int64_t T, int Hk, int group, int DK) {
-    const int64_t n = B * T * Hk * DK;
-    for (int64_t e = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += int64_t(gridDim.x) * blockDim.x) {
-        const int r = int(e % DK);
-        const int64_t hk = (e / DK) % Hk, tok = e / DK / Hk, b = tok / T, t = tok - b * T;
-        float v = 0.0f;
-        for (int j = 0; j < group; ++j) v += x[((tok * Hk + hk) * group + j) * DK + r];
-        store16<DT>(y, b * y.b + t * y.t + hk * y.h + r, v);
-    }
-}
-
 template <int DT>
 __global__ void zero_kernel(View y, int64_t B, int64_t T, int64_t H, int D) {
     const int64_t n = B * T * H * D;
@@ -314,19 +153,6 @@ struct LaunchToken {
     template <int DT, int DK, int DV>
     cudaError_t go() {
         token_kernel<DT, DK, DV><<<dim3(unsigned(a.d.nseq), unsigned(a.d.Hv), DV / 32), 128, 0, st>>>(a);
-        return cudaGetLastError();
-    }
-};
-
-struct LaunchGrad {
-    const GradArgs& a;
-    cudaStream_t st;
-    template <int DT, int DK, int DV>
-    cudaError_t go() {
-        const size_t sm = (2 * DK * DV + 2 * DK + 4 * DV + 256) * 4;
-        cudaError_t e = cudaFuncSetAttribute(token_grad_kernel<DT, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sm));
-        if (e != cudaSuccess) return e;
-        token_grad_kernel<DT, DK, DV><<<dim3(unsigned(a.d.nseq), unsigned(a.d.Hv)), 256, sm, st>>>(a);
         return cudaGetLastError();
     }
 };
@@ -382,15 +208,30 @@ size_t state_bytes(const fftconv_delta_s* p, int64_t n, int64_t Hv) { return siz
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// What the forward keeps for the backward, per chunk slot and value head: S^T
-// at the chunk's start, Vn^T and T, 16-bit.
+// What the forward keeps for the backward, per chunk slot and value head: the
+// prep kernel's images, S^T at the chunk's start, Vn^T and T.
 struct SavedLayout {
-    size_t v, t, total;  // byte offsets of Vn^T and T (S^T is first), and the size
+    size_t s, v, t, total;  // byte offsets (the images are first), and the size
     SavedLayout(const fftconv_delta_s* p, int64_t B, int64_t T, int64_t Hv, int64_t nseq) {
-        const size_t n = size_t(chunk_slots(B, T, nseq)) * Hv * 2;
-        v = up256(n * p->Dk * p->Dv);
-        t = v + up256(n * p->Dv * kChunk);
-        total = t + up256(n * kChunk * kChunk);
+        const size_t n = size_t(chunk_slots(B, T, nseq)) * Hv;
+        s = n * prep_image(p->Dk);
+        v = s + n * p->Dk * p->Dv * 2;
+        t = v + n * p->Dv * kChunk * 2;
+        total = t + n * kChunk * kChunk * 2;
+    }
+};
+
+// The backward's scratch: dS'^T and dR (two parts) per chunk slot and value head, and dq, dk
+// per value head where value heads share a key head.
+struct BwdScratch {
+    size_t r, q, k, total;  // byte offsets (dS'^T is first), and the size
+    BwdScratch(const fftconv_delta_s* p, int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t nseq) {
+        const size_t n = size_t(chunk_slots(B, T, nseq)) * Hv;
+        const size_t h = Hk < Hv ? up256(size_t(B) * T * Hv * p->Dk * 4) : 0;
+        r = up256(n * p->Dk * p->Dv * 2);
+        q = r + up256(n * p->Dv * kChunk * 4);
+        k = q + h;
+        total = k + h;
     }
 };
 
@@ -398,14 +239,14 @@ struct SavedLayout {
 struct FwdScratch {
     ChunkArgs c{};
     size_t state, trans, total;  // byte offsets (the images are first), and the size
-    FwdScratch(const fftconv_delta_s* p, int64_t B, int64_t T, int64_t Hv, int64_t nseq) {
+    FwdScratch(const fftconv_delta_s* p, int64_t B, int64_t T, int64_t Hv, int64_t nseq, bool saved) {
         c.d.B = B;
         c.d.T = T;
         c.d.Hv = int(Hv);
         c.d.nseq = int(nseq);
         plan_segments(&c, p->num_sms);
         const size_t segs = c.segments > nseq ? size_t(c.segments) * Hv * p->Dk * 4 : 0;
-        state = up256(size_t(c.slots) * Hv * prep_image(p->Dk));
+        state = saved ? 0 : up256(size_t(c.slots) * Hv * prep_image(p->Dk));
         trans = state + up256(segs * p->Dv);
         total = trans + up256(segs * p->Dk);
     }
@@ -487,13 +328,14 @@ extern "C" size_t fftconv_delta_saved_bytes(fftconv_delta_t p, int64_t B, int64_
 }
 
 extern "C" size_t fftconv_delta_scratch_bytes(fftconv_delta_t p, int64_t B, int64_t T, int64_t Hk, int64_t Hv,
-                                              int64_t nseq, int backward) {
+                                              int64_t nseq, int pass) {
     if (!p || B < 0 || T < 0 || Hk < 0 || Hv < 0 || nseq < 0) return 0;
-    if (!backward) {
-        const FwdScratch l(p, B, T, Hv, nseq);
+    if (pass != 1) {
+        const FwdScratch l(p, B, T, Hv, nseq, pass == 2);
         return l.total;
     }
-    return up256(size_t(nseq) * Hv * kChunk * p->Dk * p->Dv * 4) + 2 * up256(size_t(B) * T * Hv * p->Dk * 4);
+    const BwdScratch l(p, B, T, Hk, Hv, nseq);
+    return l.total;
 }
 
 extern "C" fftconv_status_t fftconv_delta_forward(fftconv_delta_t p, const fftconv_delta_args_t* args,
@@ -509,7 +351,9 @@ extern "C" fftconv_status_t fftconv_delta_forward(fftconv_delta_t p, const fftco
     if (off16(state_in) || off16(state_out) || off16(saved) || off16(scratch)) return FFTCONV_ERR_ALIGN;
     const size_t sb = state_bytes(p, d.nseq, d.Hv);
     const size_t vb = fftconv_delta_saved_bytes(p, d.B, d.T, d.Hv, d.nseq);
-    const size_t need = fftconv_delta_scratch_bytes(p, d.B, d.T, d.Hk, d.Hv, d.nseq, 0);
+    // with `saved` the images stay there
+    const FwdScratch w(p, d.B, d.T, d.Hv, d.nseq, saved != nullptr);
+    const size_t need = w.total;
     if (need && (!scratch || scratch_bytes < need)) return FFTCONV_ERR_WORKSPACE;
     const bool any = d.B && d.T;
     if (any && (e = take_view(o, d.B, d.T, d.Hv, p->Dv, &a.d.o)) != FFTCONV_OK) return e;
@@ -529,20 +373,19 @@ extern "C" fftconv_status_t fftconv_delta_forward(fftconv_delta_t p, const fftco
     }
     a.state_in = state_in;
     a.state_out = state_out;
-    const FwdScratch w(p, d.B, d.T, d.Hv, d.nseq);
     if (w.c.slots >= (int64_t(1) << 30) / d.Hv) return FFTCONV_ERR_UNSUPPORTED;
     a.slots = w.c.slots;
     a.segments = w.c.segments;
     a.seg_chunks = w.c.seg_chunks;
     a.sms = p->num_sms;
-    a.images = static_cast<uint8_t*>(scratch);
-    a.seg_state = reinterpret_cast<float*>(a.images + w.state);
-    a.seg_trans = reinterpret_cast<float*>(a.images + w.trans);
+    a.images = static_cast<uint8_t*>(saved ? saved : scratch);
+    a.seg_state = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + w.state);
+    a.seg_trans = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + w.trans);
     if (saved) {
         const SavedLayout l(p, d.B, d.T, d.Hv, d.nseq);
-        a.saved_s = static_cast<uint16_t*>(saved);
-        a.saved_v = reinterpret_cast<uint16_t*>(static_cast<char*>(saved) + l.v);
-        a.saved_t = reinterpret_cast<uint16_t*>(static_cast<char*>(saved) + l.t);
+        a.saved_s = a.images + l.s;
+        a.saved_v = a.images + l.v;
+        a.saved_t = a.images + l.t;
     }
     if (!encode_tokens_map(&a.mq, d.q, d.B, d.T, d.Hk, p->Dk, p->dtype) ||
         !encode_tokens_map(&a.mk, d.k, d.B, d.T, d.Hk, p->Dk, p->dtype) ||
@@ -574,49 +417,58 @@ extern "C" fftconv_status_t fftconv_delta_backward(fftconv_delta_t p, const fftc
     if (!saved) return FFTCONV_ERR_INVALID;
     const size_t need = fftconv_delta_scratch_bytes(p, d.B, d.T, d.Hk, d.Hv, d.nseq, 1);
     if (need && (!scratch || scratch_bytes < need)) return FFTCONV_ERR_WORKSPACE;
-    View vdq, vdk;
-    if ((e = take_view(d_o, d.B, d.T, d.Hv, p->Dv, &a.dout)) != FFTCONV_OK) return e;
-    if ((e = take_view(dq, d.B, d.T, d.Hk, p->Dk, &vdq)) != FFTCONV_OK) return e;
-    if ((e = take_view(dk, d.B, d.T, d.Hk, p->Dk, &vdk)) != FFTCONV_OK) return e;
+    View vdo;
+    if ((e = take_view(d_o, d.B, d.T, d.Hv, p->Dv, &vdo)) != FFTCONV_OK) return e;
+    if ((e = take_view(dq, d.B, d.T, d.Hk, p->Dk, &a.dq)) != FFTCONV_OK) return e;
+    if ((e = take_view(dk, d.B, d.T, d.Hk, p->Dk, &a.dk)) != FFTCONV_OK) return e;
     if ((e = take_view(dv, d.B, d.T, d.Hv, p->Dv, &a.dv)) != FFTCONV_OK) return e;
     if ((e = take_view(dg, d.B, d.T, d.Hv, 0, &a.dg)) != FFTCONV_OK) return e;
     if ((e = take_view(dbeta, d.B, d.T, d.Hv, 0, &a.dbeta)) != FFTCONV_OK) return e;
     Span in[6];
     input_spans(p, d, in);
-    const Span more[3] = {span_of(a.dout, d.B, d.T, d.Hv, p->Dv), span_of(d_state_out, sb),
+    const Span more[3] = {span_of(vdo, d.B, d.T, d.Hv, p->Dv), span_of(d_state_out, sb),
                           span_of(saved, fftconv_delta_saved_bytes(p, d.B, d.T, d.Hv, d.nseq))};
     // gradients may be slices of one buffer, so they are not checked against each other
-    const Span outs[7] = {span_of(vdq, d.B, d.T, d.Hk, p->Dk), span_of(vdk, d.B, d.T, d.Hk, p->Dk),
+    const Span outs[7] = {span_of(a.dq, d.B, d.T, d.Hk, p->Dk), span_of(a.dk, d.B, d.T, d.Hk, p->Dk),
                           span_of(a.dv, d.B, d.T, d.Hv, p->Dv), span_of(a.dg, d.B, d.T, d.Hv, 0),
                           span_of(a.dbeta, d.B, d.T, d.Hv, 0), span_of(d_state_in, sb), span_of(scratch, need)};
     if (any_meet(outs, in) || any_meet(outs, more)) return FFTCONV_ERR_INVALID;
-    a.dsout = d_state_out;
-    a.dsin = d_state_in;
-    a.saved = static_cast<const uint16_t*>(saved);
-    char* w = static_cast<char*>(scratch);
-    a.states = reinterpret_cast<float*>(w);
-    w += up256(size_t(d.nseq) * d.Hv * kChunk * p->Dk * p->Dv * 4);
-    const size_t hb = size_t(d.B) * d.T * d.Hv * p->Dk * 4;
-    a.dqh = reinterpret_cast<float*>(w);
-    w += up256(hb);
-    a.dkh = reinterpret_cast<float*>(w);
+    a.d_state_out = d_state_out;
+    a.d_state_in = d_state_in;
+    const SavedLayout l(p, d.B, d.T, d.Hv, d.nseq);
+    a.images = static_cast<const uint8_t*>(saved);
+    a.saved_s = a.images + l.s;
+    a.saved_v = a.images + l.v;
+    a.saved_t = a.images + l.t;
+    const BwdScratch w(p, d.B, d.T, d.Hk, d.Hv, d.nseq);
+    a.ds = static_cast<uint8_t*>(scratch);
+    a.dr = a.ds + w.r;
+    if (d.group > 1) {
+        a.dqh = reinterpret_cast<float*>(a.ds + w.q);
+        a.dkh = reinterpret_cast<float*>(a.ds + w.k);
+    }
+    a.slots = chunk_slots(d.B, d.T, d.nseq);
+    a.sms = p->num_sms;
+    if (a.slots >= (int64_t(1) << 30) / d.Hv) return FFTCONV_ERR_UNSUPPORTED;
+    if (!encode_tokens_map(&a.mq, d.q, d.B, d.T, d.Hk, p->Dk, p->dtype) ||
+        !encode_tokens_map(&a.mk, d.k, d.B, d.T, d.Hk, p->Dk, p->dtype) ||
+        !encode_tokens_map(&a.mv, d.v, d.B, d.T, d.Hv, p->Dv, p->dtype) ||
+        !encode_tokens_map(&a.mo, vdo, d.B, d.T, d.Hv, p->Dv, p->dtype) ||
+        !encode_tokens_map(&a.mdq, a.dq, d.B, d.T, d.Hk, p->Dk, p->dtype) ||
+        !encode_tokens_map(&a.mdk, a.dk, d.B, d.T, d.Hk, p->Dk, p->dtype) ||
+        !encode_tokens_map(&a.mdv, a.dv, d.B, d.T, d.Hv, p->Dv, p->dtype))
+        return FFTCONV_ERR_UNSUPPORTED;
     cudaError_t c = cudaSuccess;
-    const bool f16 = p->dtype == FFTCONV_F16;
     if (d.offsets) {  // tokens outside every sequence have zero gradients
-        c = cudaMemsetAsync(a.dqh, 0, up256(hb) + hb, st);
-        const View zs[3] = {a.dv, a.dg, a.dbeta};
-        for (int i = 0; i < 3 && c == cudaSuccess; ++i)
-            c = f16 ? zero_view<0>(zs[i], d.B, d.T, d.Hv, i == 0 ? p->Dv : 1, st)
-                    : zero_view<1>(zs[i], d.B, d.T, d.Hv, i == 0 ? p->Dv : 1, st);
+        const View zs[5] = {a.dq, a.dk, a.dv, a.dg, a.dbeta};
+        const int64_t zh[5] = {d.Hk, d.Hk, d.Hv, d.Hv, d.Hv};
+        const int zd[5] = {p->Dk, p->Dk, p->Dv, 1, 1};
+        for (int i = 0; i < 5 && c == cudaSuccess; ++i)
+            c = p->dtype == FFTCONV_F16 ? zero_view<0>(zs[i], d.B, d.T, zh[i], zd[i], st)
+                                        : zero_view<1>(zs[i], d.B, d.T, zh[i], zd[i], st);
+        if (c == cudaSuccess && a.dqh) c = cudaMemsetAsync(a.dqh, 0, w.total - w.q, st);
     }
-    if (c == cudaSuccess) c = pick(p->dtype, p->Dk, p->Dv, LaunchGrad{a, st});
-    for (int i = 0; i < 2 && c == cudaSuccess; ++i) {
-        const float* x = i ? a.dkh : a.dqh;
-        const View& y = i ? vdk : vdq;
-        if (f16) head_sum_kernel<0><<<4096, 256, 0, st>>>(x, y, d.B, d.T, d.Hk, d.group, p->Dk);
-        else head_sum_kernel<1><<<4096, 256, 0, st>>>(x, y, d.B, d.T, d.Hk, d.group, p->Dk);
-        c = cudaGetLastError();
-    }
+    if (c == cudaSuccess) c = launch_delta_backward(a, p->dtype, p->Dk, p->Dv, st);
     return done(c);
 }
 

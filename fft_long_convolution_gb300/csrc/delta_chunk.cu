@@ -32,21 +32,12 @@
 //   warp 20      issues every contraction;  warp 21  loads
 #include "delta_chunk.h"
 
-#include "tile.cuh"
+#include "chunk.cuh"
 
 namespace fftconv {
 namespace {
 
 using namespace tile;
-
-constexpr uint32_t kWaitFinal = 1u << 18;  // polls of the waits that end a CTA
-
-// What delta_prep_kernel leaves for a chunk of one value head: the tiles P,
-// (T beta) high and low part, then float32 e[64], scale G[64], G_63, then -W^T,
-// DK rows of 64 tokens, high and low part.
-constexpr uint32_t kImgP = 0, kImgT = kTile, kImgE = 3 * kTile, kImgW = kImgE + 1024;
-template <int DK>
-constexpr uint32_t kImage = kImgW + DK * 256;
 
 // One 16 x 8 tile of a float32 product X Y over k0 <= k < k1 (multiples of 8)
 // by one warp, as three products of 10-bit parts (hi hi + hi lo + lo hi: about
@@ -163,21 +154,6 @@ __device__ __forceinline__ void inverse64(float* A, int p, int w, int lane, Sync
 }
 
 
-// Chunk slot -> sequence and chunk: the last sequence whose first slot is not
-// past it.
-__device__ __forceinline__ bool find_chunk(const DeltaArgs& d, int64_t slot, Seq* s, int* i, int64_t* chunk) {
-    int lo = 0, hi = d.nseq - 1;
-    while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (locate(d.offsets, d.T, m).slot <= slot) lo = m;
-        else hi = m - 1;
-    }
-    *s = locate(d.offsets, d.T, lo);
-    *i = lo;
-    *chunk = slot - s->slot;
-    return *chunk >= 0 && *chunk * kChunk < s->len;
-}
-
 // Segment slot -> sequence and segment, by the same rule on the chunk slots.
 __device__ __forceinline__ bool find_segment(const DeltaArgs& d, int64_t L, int64_t slot, Seq* s, int* i, int64_t* seg) {
     int lo = 0, hi = d.nseq - 1;
@@ -202,12 +178,6 @@ struct PrepCfg {
     static constexpr int PER_SM = 4;
 };
 
-// A chunk of a value head: where its tokens are and where its image goes.
-struct PrepItem {
-    int row, t0, m, h;  // m tokens; 0: no more items
-    int64_t at;
-};
-
 // T, W, P and the decays of one chunk and value head at a time.  Bound: the
 // latency of its steps (each waits for the last, eleven in the inverse alone),
 // covered by four CTAs per SM and by fetching the next chunk's tiles and gates
@@ -218,7 +188,7 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);  // loads, K K^T, W
-    PrepItem* items = reinterpret_cast<PrepItem*>(sm + C::oItem);
+    ChunkItem* items = reinterpret_cast<ChunkItem*>(sm + C::oItem);
     const DeltaArgs& d = a.d;
     const int p = threadIdx.x, w = __shfl_sync(0xffffffffu, p / 32, 0), lane = p % 32;
     if (sb & 1023) {  // not with the present layout of the window
@@ -231,25 +201,9 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
     }
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + 3);
     if (w == 1) tc::alloc(s_tmem, 64);
-    const int count = int(a.slots) * d.Hv;
     int next = blockIdx.x;
-    // the next item that has tokens (warp 3)
-    auto find = [&](PrepItem* to) {
-        PrepItem it{0, 0, 0, 0, 0};
-        for (; next < count; next += gridDim.x) {
-            const int slot = next / d.Hv;
-            Seq s;
-            int si;
-            int64_t ch;
-            if (!find_chunk(d, slot, &s, &si, &ch)) continue;
-            const int64_t left = s.len - ch * kChunk;
-            it = {int(s.row), int(s.start + ch * kChunk), int(left < kChunk ? left : kChunk), next - slot * d.Hv, next};
-            next += gridDim.x;
-            break;
-        }
-        if (lane == 0) *to = it;
-    };
-    auto load = [&](const PrepItem& it) {  // one warp
+    auto find = [&](ChunkItem* to) { find_item(d, int(a.slots), &next, to); };  // warp 3
+    auto load = [&](const ChunkItem& it) {  // one warp
         if (elect()) {
             mbar_expect_tx(bar, C::KQ);
             #pragma unroll
@@ -261,7 +215,7 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
         __syncwarp();
     };
     float g[2], e[2];  // log decays and betas of tokens 2 lane and 2 lane + 1 (warp 2)
-    auto fetch = [&](const PrepItem& it) {
+    auto fetch = [&](const ChunkItem& it) {
         #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int64_t t = it.t0 + 2 * lane + u;
@@ -289,7 +243,7 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
     bool ok = true;
     uint32_t k = 0;
     for (; items[k & 1].m; ++k) {
-        const PrepItem it = items[k & 1];
+        const ChunkItem it = items[k & 1];
         const uint32_t par = k & 1;
         uint8_t* image = a.images + it.at * kImage<DK>;
         if (w == 2) {
@@ -315,7 +269,8 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
             float* gt = reinterpret_cast<float*>(image + kImgE);
             gt[p] = exp2_fast(sbv[63] - b);
             gt[64 + p] = d.scale * G;
-            if (p == 63) gt[128] = G;
+            gt[128 + p] = b;
+            gt[192 + p] = sbe[p];
             sng[p] = -G;
         } else if (w == 3) {
             find(items + (~k & 1));
@@ -443,7 +398,7 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
                     *reinterpret_cast<uint4*>(sm + (q < 2 ? C::oTb + q * C::sTb : C::oA + (q - 2) * kTile) + pos) =
                         make_uint4(v[q][0], v[q][1], v[q][2], v[q][3]);
                 if (a.saved_t)
-                    *reinterpret_cast<uint4*>(a.saved_t + (it.at * 64 + r) * 64 + h0 + j0) = make_uint4(ts[0], ts[1], ts[2], ts[3]);
+                    *reinterpret_cast<uint4*>(a.saved_t + it.at * kTile + pos) = make_uint4(ts[0], ts[1], ts[2], ts[3]);
             }
         }
         tc::fence_proxy_async();
@@ -660,7 +615,8 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         for (int c = 0; ok && c < n; ++c) {
             if (!(ok = wait(bar + kTFull + c % C::NI, (c / C::NI) & 1, fail))) break;
             const float* gt = reinterpret_cast<const float*>(image(c) + kImgE);
-            const float2 gc = make_float2(gt[128], gt[128]);
+            const float g63 = exp2_fast(gt[128 + 63]);
+            const float2 gc = make_float2(g63, g63);
             uint32_t x[NC], hi[NC / 2], lo[NC / 2];
             if (c > 0) {
                 if (!(ok = wait(bar + kSDone, (c - 1) & 1, fail))) break;
@@ -686,10 +642,11 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             done(kSReady);
             st_cols<NC>(lanes + C::cS + k0, x);  // complete before kVnReady
             if (!STATE && a.saved_s && mine) {
-                uint16_t* sv = a.saved_s + (((slot0 + c) * d.Hv + h) * DV + dv) * DK + k0;
+                uint8_t* sv = a.saved_s + ((slot0 + c) * d.Hv + h) * (DV * DK * 2) + (k0 >> 6) * (DV * 128) + dv * 128;
                 #pragma unroll
                 for (int j = 0; j < NC / 2; j += 4)
-                    *reinterpret_cast<uint4*>(sv + 2 * j) = make_uint4(hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
+                    *reinterpret_cast<uint4*>(sv + ((((k0 & 63) / 8 + j / 4) ^ (dv & 7)) * 16)) =
+                        make_uint4(hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
             }
             if (c > 0 && !(ok = put_o(c - 1))) break;
             // Vn^T = U^T - S^T W^T
@@ -715,9 +672,9 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             tc::fence_before();
             done(kVnReady);
             if (!STATE && a.saved_v && mine) {
-                uint16_t* p = a.saved_v + (((slot0 + c) * d.Hv + h) * DV + dv) * 64 + j0;
-                *reinterpret_cast<uint4*>(p) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
-                *reinterpret_cast<uint4*>(p + 8) = make_uint4(vh[4], vh[5], vh[6], vh[7]);
+                uint8_t* p = a.saved_v + ((slot0 + c) * d.Hv + h) * (DV * 128) + dv * 128;
+                *reinterpret_cast<uint4*>(p + ((j0 / 8) ^ (dv & 7)) * 16) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+                *reinterpret_cast<uint4*>(p + ((j0 / 8 + 1) ^ (dv & 7)) * 16) = make_uint4(vh[4], vh[5], vh[6], vh[7]);
             }
         }
         if (ok) ok = put_o(n - 1);
@@ -944,18 +901,6 @@ __global__ void __launch_bounds__(256) delta_join_kernel(const __grid_constant__
         }
         __syncthreads();
     }
-}
-
-template <typename K>
-cudaError_t opt_in(K fn, size_t smem, PerDevice& cache) {
-    int* slot = cache.slot();
-    if (!slot) return cudaErrorInvalidDevice;
-    if (!*slot) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) return e;
-        *slot = 1;
-    }
-    return cudaSuccess;
 }
 
 template <int DT, int DK, int DV>

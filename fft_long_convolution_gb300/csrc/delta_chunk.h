@@ -12,10 +12,11 @@ struct ChunkArgs {
     DeltaArgs d;
     const float* state_in;
     float* state_out;
-    // what the backward needs, per chunk slot and value head, or null: S^T at
-    // the chunk's start [DV][DK], Vn^T [DV][64], T [64][64], all 16-bit
-    uint16_t *saved_s, *saved_v, *saved_t;
-    // scratch: an image per chunk slot and value head, and per segment slot and
+    // what the backward needs, per chunk slot and value head, or null: S^T at the
+    // chunk's start ([DK / 64] blocks of DV rows of 64), Vn^T (DV rows of 64) and
+    // T (64 rows of 64), 16-bit, rows of 128 bytes in the tiles' swizzled order
+    uint8_t *saved_s, *saved_v, *saved_t;
+    // an image per chunk slot and value head, and per segment slot and
     // value head a state [DK][DV] and a transition matrix [DK][DK]
     uint8_t* images;
     float *seg_state, *seg_trans;
@@ -28,6 +29,26 @@ constexpr size_t prep_image(int dk) { return 3 * 8192 + 1024 + size_t(dk) * 256;
 
 // Sets slots, segments and seg_chunks from the sizes in a->d.
 void plan_segments(ChunkArgs* a, int sms);
+
+// The gradients' kernels (delta_grad.cu).  d.o is not used; images, saved_s,
+// saved_v and saved_t come from the forward.
+struct GradArgs {
+    CUtensorMap mq, mk, mv, mo, mdq, mdk, mdv;  // mo: the gradient of o
+    DeltaArgs d;
+    View dq, dk, dv, dg, dbeta;
+    const float* d_state_out;
+    float* d_state_in;
+    const uint8_t *images, *saved_s, *saved_v, *saved_t;
+    // scratch, per chunk slot and value head: dS^T at the chunk's end (as saved_s)
+    // and dR (tiles of 64 tokens x 64 features; high parts, then low); per token and value head, when
+    // value heads share a key head, dq and dk in float32, else null
+    uint8_t *ds, *dr;
+    float *dqh, *dkh;
+    int64_t slots;
+    int sms;
+};
+
+cudaError_t launch_delta_backward(const GradArgs& a, int dt, int dk, int dv, cudaStream_t st);
 
 cudaError_t launch_delta_forward(const ChunkArgs& a, int dt, int dk, int dv, cudaStream_t st);
 

@@ -490,12 +490,13 @@ fftconv_status_t fftconv_delta_status(fftconv_delta_t plan, fftconv_stream_t str
 
 /*
  * Bytes of `saved` (what the forward keeps for the backward) and of `scratch`
- * (backward = 0: for the forward; 1: for the backward) for these sizes; 0 if
- * plan is NULL or a size is negative.
+ * for these sizes (pass = 0: a forward without saved; 1: a backward; 2: a
+ * forward with saved, which needs less); 0 if plan is NULL or a size is
+ * negative.
  */
 size_t fftconv_delta_saved_bytes(fftconv_delta_t plan, int64_t B, int64_t T, int64_t Hv, int64_t nseq);
 size_t fftconv_delta_scratch_bytes(fftconv_delta_t plan, int64_t B, int64_t T, int64_t Hk, int64_t Hv,
-                                   int64_t nseq, int backward);
+                                   int64_t nseq, int pass);
 
 /*
  * Whole sequences (training, prompts).  state_in: float32 [nseq][Hv][Dk][Dv]
