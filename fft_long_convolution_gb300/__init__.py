@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 from .build import LIB_PATH, build as build_library
@@ -186,9 +187,10 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    from torch import _C  # torch.cuda.current_stream() takes 12 us
+    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
 
 
 class Plan:
@@ -407,33 +409,58 @@ def status_string(code: int) -> str:
 
 
 # ---- token mixers with a state: strided token-major tensors [B, T, H, D]
+#
+# A decoding step is a few microseconds of GPU work, so these calls keep their
+# own work small: each tensor is looked at once, and the argument structures
+# are packed in one go.
+
+_DELTA_ARGS = struct.Struct("=5qQf4x" + "Q3q" * 5)
+_NORM_ARGS = struct.Struct("=5if4q" + "Q3q" * 2 + "4QqQ")
+
+
+def _strides(t, what: str, dtype, shape):
+    """A tensor's address and its first three strides, checked against dtype and shape."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA {dtype} tensor of shape {tuple(shape)}")
+    st = t.stride()
+    if len(st) == 4 and st[3] != 1 and shape[3] > 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t.data_ptr(), st[0], st[1], st[2]
+
 
 def _view(t, what: str, dtype, dims: int) -> View:
-    """A tensor's view (None: an empty one), checked against dtype and rank."""
-    if t is None:
-        return View(None, 0, 0, 0)
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype != dtype or t.dim() != dims:
-        raise ValueError(f"{what} must be a {dtype} tensor of {dims} dimensions")
-    if dims == 4 and t.shape[3] > 1 and t.stride(3) != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    return View(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    """A tensor as a view, checked against dtype and rank."""
+    if t.dim() != dims:
+        raise ValueError(f"{what} must have {dims} dimensions")
+    return View(*_strides(t, what, dtype, t.shape))
 
 
-def _dense(t, what: str, dtype, shape) -> Optional[int]:
-    """The address of a contiguous CUDA tensor of the given shape (None: NULL)."""
+def _dense(t, what: str, dtype, shape) -> int:
+    """The address of a contiguous CUDA tensor of the given shape (None: 0)."""
     if t is None:
-        return None
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        return 0
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
+class _Same:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_SAME = _Same()
+
+
 def _on(stream):
     """Allocations made inside belong to the stream that the call runs on."""
+    if stream is None:
+        return _SAME
     import torch
-    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream())
+    return torch.cuda.stream(stream)
 
 
 class DeltaRule:
@@ -448,6 +475,7 @@ class DeltaRule:
 
     def __init__(self, Dk: int, Dv: int, dtype):
         self.Dk, self.Dv, self.torch_dtype = int(Dk), int(Dv), dtype
+        self._scale = self.Dk ** -0.5
         h = ctypes.c_void_p()
         _check(lib().fftconv_delta_create(ctypes.byref(h), self.Dk, self.Dv, _dtype_code(dtype)),
                "fftconv_delta_create")
@@ -467,22 +495,21 @@ class DeltaRule:
     def _args(self, q, k, v, g, beta, offsets, scale) -> DeltaArgs:
         import torch
         dt = self.torch_dtype
-        a = DeltaArgs()
-        a.q, a.k, a.v = _view(q, "q", dt, 4), _view(k, "k", dt, 4), _view(v, "v", dt, 4)
-        a.g, a.beta = _view(g, "g", dt, 3), _view(beta, "beta", dt, 3)
-        a.B, a.T, a.Hk, a.Hv = q.shape[0], q.shape[1], q.shape[2], v.shape[2]
-        if tuple(k.shape) != tuple(q.shape) or q.shape[3] != self.Dk or tuple(v.shape) != (a.B, a.T, a.Hv, self.Dv):
+        if q.dim() != 4 or v.dim() != 4 or q.shape[3] != self.Dk:
             raise ValueError("q, k must be [B, T, Hk, Dk] and v [B, T, Hv, Dv]")
-        if tuple(g.shape) != (a.B, a.T, a.Hv) or tuple(beta.shape) != (a.B, a.T, a.Hv):
-            raise ValueError("g and beta must be [B, T, Hv]")
-        a.nseq = a.B
+        B, T, Hk, _ = qs = q.shape
+        Hv = v.shape[2]
+        gs = (B, T, Hv)
+        nseq, off = B, 0
         if offsets is not None:
             if offsets.dim() != 1 or offsets.numel() < 1:
                 raise ValueError("offsets must be [n + 1]")
-            a.nseq = offsets.numel() - 1
-            a.offsets = _dense(offsets, "offsets", torch.int32, offsets.shape)
-        a.scale = self.Dk ** -0.5 if scale is None else float(scale)
-        return a
+            nseq = offsets.numel() - 1
+            off = _dense(offsets, "offsets", torch.int32, offsets.shape)
+        return DeltaArgs.from_buffer_copy(_DELTA_ARGS.pack(
+            B, T, Hk, Hv, nseq, off, self._scale if scale is None else scale, *_strides(q, "q", dt, qs),
+            *_strides(k, "k", dt, qs), *_strides(v, "v", dt, (B, T, Hv, self.Dv)), *_strides(g, "g", dt, gs),
+            *_strides(beta, "beta", dt, gs)))
 
     def _scratch(self, a, which, device):
         import torch
@@ -497,17 +524,16 @@ class DeltaRule:
         shape = (a.nseq, a.Hv, self.Dk, self.Dv)
         sin = _dense(state, "state", torch.float32, shape)
         with _on(stream):
-            o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-            if offsets is not None:
-                o.zero_()  # tokens outside every sequence
+            # tokens outside every sequence are zero
+            o = (torch.empty if offsets is None else torch.zeros)(v.shape, dtype=v.dtype, device=v.device)
             out = torch.empty(shape, dtype=torch.float32, device=v.device)
             saved = None
             if save:
                 n = int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq))
                 saved = torch.empty(n, dtype=torch.uint8, device=v.device)
             scratch, n = self._scratch(a, 2 if save else 0, v.device)
-            _check(lib().fftconv_delta_forward(self._h, ctypes.byref(a), sin, _view(o, "o", v.dtype, 4), _ptr(out),
-                                               _ptr(saved), _ptr(scratch), n, _stream(stream)),
+            _check(lib().fftconv_delta_forward(self._h, ctypes.byref(a), sin, _view(o, "o", v.dtype, 4),
+                                               out.data_ptr(), _ptr(saved), _ptr(scratch), n, _stream(stream)),
                    "fftconv_delta_forward")
         return (o, out, saved) if save else (o, out)
 
@@ -520,19 +546,17 @@ class DeltaRule:
         dt = self.torch_dtype
         shape = (a.nseq, a.Hv, self.Dk, self.Dv)
         dsin = _dense(dstate, "dstate", torch.float32, shape)
-        if tuple(do.shape) != tuple(v.shape):
-            raise ValueError("do must be [B, T, Hv, Dv]")
-        n = int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq))
-        sv = _dense(saved, "saved", torch.uint8, (n,))
+        vdo = View(*_strides(do, "do", dt, v.shape))
+        sv = _dense(saved, "saved", torch.uint8,
+                    (int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq)),))
         with _on(stream):
-            dq, dk, dv, dg, dbeta = (torch.empty(t.shape, dtype=dt, device=t.device) for t in (q, k, v, g, beta))
+            grads = [torch.empty(t.shape, dtype=dt, device=t.device) for t in (q, k, v, g, beta)]
             dst = torch.empty(shape, dtype=torch.float32, device=v.device)
             scratch, n = self._scratch(a, 1, v.device)
-            _check(lib().fftconv_delta_backward(
-                self._h, ctypes.byref(a), _view(do, "do", dt, 4), dsin, sv, _view(dq, "dq", dt, 4),
-                _view(dk, "dk", dt, 4), _view(dv, "dv", dt, 4), _view(dg, "dg", dt, 3), _view(dbeta, "dbeta", dt, 3),
-                _ptr(dst), _ptr(scratch), n, _stream(stream)), "fftconv_delta_backward")
-        return dq, dk, dv, dg, dbeta, dst
+            views = [View(*_strides(t, "gradient", dt, t.shape)) for t in grads]
+            _check(lib().fftconv_delta_backward(self._h, ctypes.byref(a), vdo, dsin, sv, *views, dst.data_ptr(), _ptr(scratch), n,
+                                                _stream(stream)), "fftconv_delta_backward")
+        return (*grads, dst)
 
     def step(self, q, k, v, g, beta, state, state_out=None, slots=None, scale=None, stream=None):
         """The recurrent form: B rows of a few tokens, row b against
@@ -540,14 +564,15 @@ class DeltaRule:
         -> o.  The updated states go to state_out, by default back to state."""
         import torch
         a = self._args(q, k, v, g, beta, None, scale)
-        shape = (state.shape[0], a.Hv, self.Dk, self.Dv)
+        shape = (state.shape[0], v.shape[2], self.Dk, self.Dv)
         sin = _dense(state, "state", torch.float32, shape)
         sout = sin if state_out is None else _dense(state_out, "state_out", torch.float32, shape)
-        sl = _dense(slots, "slots", torch.int32, (a.B,))
+        sl = _dense(slots, "slots", torch.int32, (q.shape[0],))
         with _on(stream):
             o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
             _check(lib().fftconv_delta_step(self._h, ctypes.byref(a), sin, sout, shape[0], sl,
-                                            _view(o, "o", v.dtype, 4), _stream(stream)), "fftconv_delta_step")
+                                            _view(o, "o", v.dtype, 4), _stream(stream)),
+                   "fftconv_delta_step")
         return o
 
     def device_status(self, stream=None) -> int:
@@ -565,26 +590,26 @@ class QKNorm:
             raise ValueError('norm must be "rms" or "l2"')
         self.D, self.torch_dtype, self.norm, self.eps = int(D), dtype, norm, float(eps)
         self.rotary, self.interleaved = int(rotary), bool(interleaved)
-        self._code = _dtype_code(dtype)
+        self._code, self._norm = _dtype_code(dtype), int(norm == "l2")
 
     def _args(self, q, k, wq, wk, cos, sin, positions) -> QKNormArgs:
         import torch
-        a = QKNormArgs()
-        a.dtype, a.norm, a.D, a.R = self._code, int(self.norm == "l2"), self.D, self.rotary
-        a.interleaved, a.eps = int(self.interleaved), self.eps
-        a.q, a.k = _view(q, "q", self.torch_dtype, 4), _view(k, "k", self.torch_dtype, 4)
-        a.B, a.T, a.Hq, a.Hk = q.shape[0], q.shape[1], q.shape[2], k.shape[2]
-        if q.shape[3] != self.D or tuple(k.shape) != (a.B, a.T, a.Hk, self.D):
+        dt, D, R, f32 = self.torch_dtype, self.D, self.rotary, torch.float32
+        if q.dim() != 4 or k.dim() != 4:
             raise ValueError("q must be [B, T, Hq, D] and k [B, T, Hk, D]")
-        a.wq, a.wk = _dense(wq, "wq", torch.float32, (self.D,)), _dense(wk, "wk", torch.float32, (self.D,))
-        if self.rotary:
+        B, T, Hq, _ = q.shape
+        Hk = k.shape[2]
+        pc = ps = pp = rows = 0
+        if R:
             if cos is None or sin is None:
                 raise ValueError("a rotation needs cos and sin")
-            shape = (cos.shape[0], self.rotary // 2)
-            a.cos, a.sin = _dense(cos, "cos", torch.float32, shape), _dense(sin, "sin", torch.float32, shape)
-            a.table_rows = shape[0]
-            a.positions = _dense(positions, "positions", torch.int32, (a.B, a.T))
-        return a
+            rows = cos.shape[0]
+            pc, ps = _dense(cos, "cos", f32, (rows, R // 2)), _dense(sin, "sin", f32, (rows, R // 2))
+            pp = _dense(positions, "positions", torch.int32, (B, T))
+        return QKNormArgs.from_buffer_copy(_NORM_ARGS.pack(
+            self._code, self._norm, D, R, self.interleaved, self.eps, B, T, Hq, Hk,
+            *_strides(q, "q", dt, (B, T, Hq, D)), *_strides(k, "k", dt, (B, T, Hk, D)),
+            _dense(wq, "wq", f32, (D,)), _dense(wk, "wk", f32, (D,)), pc, ps, rows, pp))
 
     def forward(self, q, k, wq=None, wk=None, cos=None, sin=None, positions=None, qo=None, ko=None, stream=None):
         """q: [B, T, Hq, D], k: [B, T, Hk, D] -> the normed and rotated (q, k).
@@ -592,14 +617,13 @@ class QKNorm:
         positions: int32 [B, T] (None: the token's index).  qo, ko: where to
         write (q and k themselves are allowed)."""
         import torch
-        a = self._args(q, k, wq, wk, cos, sin, positions)
+        args = ctypes.byref(self._args(q, k, wq, wk, cos, sin, positions))
+        dt = self.torch_dtype
         with _on(stream):
-            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device) if qo is None else qo
-            ko = torch.empty(k.shape, dtype=k.dtype, device=k.device) if ko is None else ko
-            if qo.shape != q.shape or ko.shape != k.shape:
-                raise ValueError("qo and ko have the shapes of q and k")
-            _check(lib().fftconv_qknorm_forward(ctypes.byref(a), _view(qo, "qo", q.dtype, 4),
-                                                _view(ko, "ko", q.dtype, 4), _stream(stream)),
+            qo = torch.empty(q.shape, dtype=dt, device=q.device) if qo is None else qo
+            ko = torch.empty(k.shape, dtype=dt, device=k.device) if ko is None else ko
+            _check(lib().fftconv_qknorm_forward(args, View(*_strides(qo, "qo", dt, q.shape)),
+                                                View(*_strides(ko, "ko", dt, k.shape)), _stream(stream)),
                    "fftconv_qknorm_forward")
         return qo, ko
 
@@ -607,18 +631,16 @@ class QKNorm:
         """Gradients (dq, dk, dwq, dwk) from those of forward's outputs; dwq
         (dwk) is None where wq (wk) is."""
         import torch
-        a = self._args(q, k, wq, wk, cos, sin, positions)
-        if dqo.shape != q.shape or dko.shape != k.shape:
-            raise ValueError("dqo and dko have the shapes of q and k")
+        args = ctypes.byref(self._args(q, k, wq, wk, cos, sin, positions))
         dt = self.torch_dtype
+        vdq, vdk = View(*_strides(dqo, "dqo", dt, q.shape)), View(*_strides(dko, "dko", dt, k.shape))
         with _on(stream):
             dq, dk = (torch.empty(t.shape, dtype=dt, device=t.device) for t in (q, k))
             dwq, dwk = (None if w is None else torch.empty(self.D, dtype=torch.float32, device=q.device)
                         for w in (wq, wk))
-            n = int(lib().fftconv_qknorm_scratch_bytes(ctypes.byref(a))) if (wq is not None or wk is not None) else 0
+            n = int(lib().fftconv_qknorm_scratch_bytes(args)) if (wq is not None or wk is not None) else 0
             scratch = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-            _check(lib().fftconv_qknorm_backward(ctypes.byref(a), _view(dqo, "dqo", dt, 4), _view(dko, "dko", dt, 4),
-                                                 _view(dq, "dq", dt, 4), _view(dk, "dk", dt, 4), _ptr(dwq),
-                                                 _ptr(dwk), _ptr(scratch), n, _stream(stream)),
-                   "fftconv_qknorm_backward")
+            _check(lib().fftconv_qknorm_backward(args, vdq, vdk, View(*_strides(dq, "dq", dt, q.shape)),
+                                                 View(*_strides(dk, "dk", dt, k.shape)), _ptr(dwq), _ptr(dwk),
+                                                 _ptr(scratch), n, _stream(stream)), "fftconv_qknorm_backward")
         return dq, dk, dwq, dwk

@@ -10,9 +10,9 @@
 // latency for single tokens.  Split: a row (one head of one token) belongs to
 // G = 8, 16 or 32 lanes that hold 8 consecutive features (one 16-byte load)
 // each; the row's sums are shuffles within the group and nothing is staged.
-// A group takes HB consecutive heads of its token at once, so HB (times two in
-// the backward) loads are in flight before the first is used and the token's
-// cos and sin are read once for all of them.
+// A group takes a token's heads three at a time, so three (six in the backward)
+// loads are in flight before the first is used, the token's cos and sin are
+// read once for all its heads, and the weights once for all tokens.
 #include "views.h"
 
 #include <cuda_bf16.h>
@@ -31,9 +31,9 @@ struct NormArgs {
     const float *wq, *wk, *cos, *sin;
     const int32_t* pos;
     int64_t rows;  // table rows
-    int64_t T, tokens, items;
-    int Hq, Hk, D, R, inter;
-    int nbq, nbk;  // blocks of HB heads of q and of k per token
+    uint32_t T, items;
+    int parts, per;  // a token's heads (q's, then k's) in parts of `per`; an item is a part
+    int Hq, Hk, D, R;
     float eps, c;
     float* part;  // [grid][2][D] partial weight gradients, or null
 };
@@ -55,60 +55,114 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                       Op<DT>::pack(x[6], x[7]));
 }
 
-// The cos and sin that belong to a lane's 8 features: feature j < R turns with
-// entry j mod (R/2) (halves) or j / 2 (interleaved).  Features at R or beyond
-// get (1, 0).
-__device__ __forceinline__ void load_turn(const NormArgs& a, int64_t p, int d0, float (&c)[8], float (&s)[8]) {
+// A lane's 8 features are two runs of 4, at d[0] and d[1].  With halves that
+// rotate against each other (MODE 2, R a multiple of 8) the first R / 8 lanes
+// hold features 4 l .. and R/2 + 4 l .., so that every pair sits in one lane;
+// otherwise a lane holds 8 consecutive features.
+template <int MODE>
+__device__ __forceinline__ void features(int lane, int R, int (&d)[2]) {
+    const bool halves = MODE == 2 && lane * 8 < R;
+    d[0] = halves ? lane * 4 : lane * 8;
+    d[1] = halves ? R / 2 + lane * 4 : lane * 8 + 4;
+}
+
+template <int MODE>
+__device__ __forceinline__ uint4 load_row(const uint16_t* p, const int (&d)[2]) {
+    if constexpr (MODE == 2) {
+        const uint2 a = *reinterpret_cast<const uint2*>(p + d[0]), b = *reinterpret_cast<const uint2*>(p + d[1]);
+        return make_uint4(a.x, a.y, b.x, b.y);
+    }
+    return *reinterpret_cast<const uint4*>(p + d[0]);
+}
+
+template <int MODE>
+__device__ __forceinline__ void store_row(uint16_t* p, const int (&d)[2], const uint4& v) {
+    if constexpr (MODE == 2) {
+        *reinterpret_cast<uint2*>(p + d[0]) = make_uint2(v.x, v.y);
+        *reinterpret_cast<uint2*>(p + d[1]) = make_uint2(v.z, v.w);
+    } else {
+        *reinterpret_cast<uint4*>(p + d[0]) = v;
+    }
+}
+
+// 4 consecutive floats, by one 16-byte load where VEC.
+template <bool VEC>
+__device__ __forceinline__ void load4(const float* p, float* x) {
+    if constexpr (VEC) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+    } else {
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __ldg(p + j);
+    }
+}
+
+// The cos and sin of a lane's features: one entry per pair (MODE 1, 2) or per
+// feature (MODE 3).  Features at R or beyond get (1, 0).
+template <int MODE, bool VEC, int N>
+__device__ __forceinline__ void load_turn(const NormArgs& a, int64_t p, int lane, float (&c)[N], float (&s)[N]) {
     const int half = a.R >> 1;
     const float *cp = a.cos + p * half, *sp = a.sin + p * half;
     #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int d = d0 + j, i = a.inter ? d >> 1 : (d < half ? d : d - half);
-        const bool on = d < a.R;
-        c[j] = on ? __ldg(cp + i) : 1.0f;
-        s[j] = on ? __ldg(sp + i) : 0.0f;
+    for (int j = 0; j < N; ++j) {
+        c[j] = 1.0f;
+        s[j] = 0.0f;
+    }
+    if constexpr (MODE == 3) {
+        #pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int d = lane * 8 + j, i = d < half ? d : d - half;
+            if (d < a.R) {
+                c[j] = __ldg(cp + i);
+                s[j] = __ldg(sp + i);
+            }
+        }
+    } else {
+        const int i = lane * 4;  // the lane's first pair
+        if (MODE == 2 || VEC) {
+            if (i + 4 <= half) {
+                load4<VEC>(cp + i, c);
+                load4<VEC>(sp + i, s);
+            }
+        } else {
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (i + j < half) {
+                    c[j] = __ldg(cp + i + j);
+                    s[j] = __ldg(sp + i + j);
+                }
+            }
+        }
     }
 }
 
 // Rotate a row spread over the group's lanes; dir = +1 forward, -1 inverse.
-// MODE 1: pairs are neighbours in the lane; 2: halves whose distance R/2 is a
-// multiple of 8 (the partner sits in one other lane); 3: other halves, through
-// the group's row buffer in shared memory.
-template <int G, int MODE>
-__device__ __forceinline__ void turn(float (&z)[8], const float (&c)[8], const float (&s)[8], float dir, int lane,
-                                     int R, float* row, unsigned mask) {
-    if constexpr (MODE == 1) {
-        #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const float x = z[j], y = z[j + 1], sj = dir * s[j];
-            z[j] = x * c[j] - y * sj;
-            z[j + 1] = y * c[j] + x * sj;
-        }
-    } else {
+// MODE 1: pairs are neighbours; 2: pairs are features j and 4 + j of a lane; 3:
+// halves of another length, through the group's row buffer in shared memory.
+template <int MODE, int N>
+__device__ __forceinline__ void turn(float (&z)[8], const float (&c)[N], const float (&s)[N], float dir, int lane, int R,
+                                     float* row, unsigned mask) {
+    if constexpr (MODE == 3) {
         const int half = R >> 1;
-        float o[8];
-        if constexpr (MODE == 2) {
-            const int step = half >> 3;
-            const bool low = lane < step;
-            const int other = lane < 2 * step ? (low ? lane + step : lane - step) : lane;
-            #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(mask, z[j], other, G);
-            const float sg = low ? -dir : dir;
-            #pragma unroll
-            for (int j = 0; j < 8; ++j) z[j] = z[j] * c[j] + sg * o[j] * s[j];
-        } else {
-            #pragma unroll
-            for (int j = 0; j < 8; ++j) row[lane * 8 + j] = z[j];
-            __syncwarp(mask);
-            #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int d = lane * 8 + j;
-                if (d < R) {
-                    const bool low = d < half;
-                    z[j] = z[j] * c[j] + (low ? -dir : dir) * row[low ? d + half : d - half] * s[j];
-                }
+        #pragma unroll
+        for (int j = 0; j < 8; ++j) row[lane * 8 + j] = z[j];
+        __syncwarp(mask);
+        #pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int d = lane * 8 + j;
+            if (d < R) {
+                const bool low = d < half;
+                z[j] = z[j] * c[j] + (low ? -dir : dir) * row[low ? d + half : d - half] * s[j];
             }
-            __syncwarp(mask);
+        }
+        __syncwarp(mask);
+    } else {
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float &x = z[MODE == 1 ? 2 * j : j], &y = z[MODE == 1 ? 2 * j + 1 : j + 4];
+            const float u = x, v = y, sj = dir * s[j];
+            x = u * c[j] - v * sj;
+            y = v * c[j] + u * sj;
         }
     }
 }
@@ -120,84 +174,94 @@ __device__ __forceinline__ float group_sum(float v, unsigned mask) {
     return v;
 }
 
-// MODE 0: no rotation; 1, 2, 3 as turn().
-template <int DT, int G, int HB, int MODE, bool BWD>
+// MODE 0: no rotation; 1, 2, 3 as turn().  HB: heads taken at a time.  VEC:
+// weights and tables by 16-byte loads.
+template <int DT, int G, int HB, int MODE, bool VEC, bool BWD>
 __global__ void __launch_bounds__(kThreads) qknorm_kernel(const NormArgs a) {
     __shared__ float rows[MODE == 3 ? kThreads / G : 1][MODE == 3 ? 8 * G : 1];
     const int lane = threadIdx.x % G, grp = threadIdx.x / G;
-    const int d0 = lane * 8;
-    const bool on = d0 < a.D;
+    const bool on = lane * 8 < a.D;
+    int d[2];
+    features<MODE>(lane, a.R, d);
     const unsigned mask = G == 32 ? 0xffffffffu : ((1u << G) - 1u) << ((threadIdx.x % 32) / G * G);
     constexpr int NG = kThreads / G;
-    const int nb = a.nbq + a.nbk;
-    float acc[BWD ? 2 : 1][8] = {};  // weight gradients of this lane's features, q and k
-    for (int64_t it = int64_t(blockIdx.x) * NG + grp; it < a.items; it += int64_t(gridDim.x) * NG) {
-        const int64_t tok = it / nb;
-        const int blk = int(it - tok * nb);
-        const bool isk = blk >= a.nbq;
-        const int h0 = (isk ? blk - a.nbq : blk) * HB, H = isk ? a.Hk : a.Hq;
-        const int64_t b = tok / a.T, t = tok - b * a.T;
-        const View& vx = isk ? a.k : a.q;
-        const View& vy = isk ? a.yk : a.yq;
-        const uint16_t* px = reinterpret_cast<const uint16_t*>(vx.p) + b * vx.b + t * vx.t + d0;
-        uint16_t* py = reinterpret_cast<uint16_t*>(vy.p) + b * vy.b + t * vy.t + d0;
-        uint4 ux[HB], ud[BWD ? HB : 1];
+    float w[2][8];
+    #pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const float* p = m ? a.wk : a.wq;
         #pragma unroll
-        for (int i = 0; i < HB; ++i)
-            ux[i] = on && h0 + i < H ? *reinterpret_cast<const uint4*>(px + (h0 + i) * vx.h) : make_uint4(0, 0, 0, 0);
-        if constexpr (BWD) {
-            const View& vd = isk ? a.dyk : a.dyq;
-            const uint16_t* pd = reinterpret_cast<const uint16_t*>(vd.p) + b * vd.b + t * vd.t + d0;
-            #pragma unroll
-            for (int i = 0; i < HB; ++i)
-                ud[i] = on && h0 + i < H ? *reinterpret_cast<const uint4*>(pd + (h0 + i) * vd.h) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 8; ++j) w[m][j] = 1.0f;
+        if (p && on) {
+            load4<VEC>(p + d[0], w[m]);
+            load4<VEC>(p + d[1], w[m] + 4);
         }
-        float c[8], s[8];
+    }
+    float acc[BWD ? 2 : 1][8] = {};  // weight gradients of this lane's features, q and k
+    constexpr int NT = MODE == 3 ? 8 : 4;
+    for (uint32_t it = blockIdx.x * NG + grp; it < a.items; it += gridDim.x * NG) {
+        const uint32_t tok = it / uint32_t(a.parts);
+        const int lo = int(it - tok * a.parts) * a.per, hi = min(lo + a.per, a.Hq + a.Hk);
+        const int64_t b = tok / a.T, t = tok - uint32_t(b) * a.T;
+        float c[NT], s[NT];
         bool lost = false;
         if constexpr (MODE != 0) {
             const int64_t p = a.pos ? a.pos[tok] : t;
             lost = p < 0 || p >= a.rows;
-            load_turn(a, lost ? 0 : p, d0, c, s);
+            load_turn<MODE, VEC>(a, lost ? 0 : p, lane, c, s);
         }
-        const float* wp = isk ? a.wk : a.wq;
-        float w[8];
         #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = wp && on ? __ldg(wp + d0 + j) : 1.0f;
-        #pragma unroll
-        for (int i = 0; i < HB; ++i) {
-            if (h0 + i >= H) break;  // the same for every lane of the group
-            float x[8], z[8];
-            unpack8<DT>(ux[i], x);
-            float ss = 0.0f;
-            #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-            ss = group_sum<G>(ss, mask);
-            const float r = rsqrtf(fmaf(a.c, ss, a.eps));
-            if constexpr (!BWD) {
+        for (int m = 0; m < 2; ++m) {
+            const View& vx = m ? a.k : a.q;
+            const View& vy = m ? a.yk : a.yq;
+            const View& vd = m ? a.dyk : a.dyq;
+            const int first = m ? max(lo - a.Hq, 0) : lo, end = m ? hi - a.Hq : min(hi, a.Hq);
+            if (first >= end) continue;
+            const uint16_t* px = reinterpret_cast<const uint16_t*>(vx.p) + b * vx.b + t * vx.t;
+            uint16_t* py = reinterpret_cast<uint16_t*>(vy.p) + b * vy.b + t * vy.t;
+            const uint16_t* pd = BWD ? reinterpret_cast<const uint16_t*>(vd.p) + b * vd.b + t * vd.t : nullptr;
+            for (int h0 = first; h0 < end; h0 += HB) {
+                uint4 ux[HB], ud[BWD ? HB : 1];
                 #pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = x[j] * r * w[j];
-                if constexpr (MODE != 0) turn<G, MODE>(z, c, s, 1.0f, lane, a.R, rows[grp], mask);
-            } else {
-                unpack8<DT>(ud[i], z);
-                if constexpr (MODE != 0) turn<G, MODE>(z, c, s, -1.0f, lane, a.R, rows[grp], mask);
-                float dot = 0.0f;
-                #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float g = z[j] * x[j] * r;
-                    if (isk) acc[1][j] += g;
-                    else acc[0][j] += g;
-                    z[j] *= w[j];
-                    dot = fmaf(z[j], x[j], dot);
+                for (int i = 0; i < HB; ++i) {
+                    const bool in = on && h0 + i < end;
+                    ux[i] = in ? load_row<MODE>(px + (h0 + i) * vx.h, d) : make_uint4(0, 0, 0, 0);
+                    if constexpr (BWD) ud[i] = in ? load_row<MODE>(pd + (h0 + i) * vd.h, d) : make_uint4(0, 0, 0, 0);
                 }
-                dot = group_sum<G>(dot, mask) * a.c * r * r;
                 #pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = r * fmaf(-dot, x[j], z[j]);
+                for (int i = 0; i < HB; ++i) {
+                    if (h0 + i >= end) break;  // the same for every lane of the group
+                    float x[8], z[8];
+                    unpack8<DT>(ux[i], x);
+                    float ss = 0.0f;
+                    #pragma unroll
+                    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+                    ss = group_sum<G>(ss, mask);
+                    const float r = rsqrtf(fmaf(a.c, ss, a.eps));
+                    if constexpr (!BWD) {
+                        #pragma unroll
+                        for (int j = 0; j < 8; ++j) z[j] = x[j] * r * w[m][j];
+                        if constexpr (MODE != 0) turn<MODE>(z, c, s, 1.0f, lane, a.R, rows[grp], mask);
+                    } else {
+                        unpack8<DT>(ud[i], z);
+                        if constexpr (MODE != 0) turn<MODE>(z, c, s, -1.0f, lane, a.R, rows[grp], mask);
+                        float dot = 0.0f;
+                        #pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            acc[m][j] = fmaf(z[j] * r, x[j], acc[m][j]);
+                            z[j] *= w[m][j];
+                            dot = fmaf(z[j], x[j], dot);
+                        }
+                        dot = group_sum<G>(dot, mask) * a.c * r * r;
+                        #pragma unroll
+                        for (int j = 0; j < 8; ++j) z[j] = r * fmaf(-dot, x[j], z[j]);
+                    }
+                    if (lost) {
+                        #pragma unroll
+                        for (int j = 0; j < 8; ++j) z[j] = CUDART_NAN_F;
+                    }
+                    if (on) store_row<MODE>(py + (h0 + i) * vy.h, d, pack8<DT>(z));
+                }
             }
-            if (lost) {
-                #pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = CUDART_NAN_F;
-            }
-            if (on) *reinterpret_cast<uint4*>(py + (h0 + i) * vy.h) = pack8<DT>(z);
         }
     }
     if constexpr (BWD) {
@@ -208,12 +272,12 @@ __global__ void __launch_bounds__(kThreads) qknorm_kernel(const NormArgs a) {
         for (int m = 0; m < 2; ++m) {
             __syncthreads();
             #pragma unroll
-            for (int j = 0; j < 8; ++j) red[grp][d0 + j] = acc[m][j];
+            for (int j = 0; j < 8; ++j) red[grp][on ? d[j >> 2] + (j & 3) : lane * 8 + j] = acc[m][j];
             __syncthreads();
-            for (int d = threadIdx.x; d < a.D; d += kThreads) {
+            for (int f = threadIdx.x; f < a.D; f += kThreads) {
                 float v = 0.0f;
-                for (int g = 0; g < NG; ++g) v += red[g][d];
-                a.part[(int64_t(blockIdx.x) * 2 + m) * a.D + d] = v;
+                for (int g = 0; g < NG; ++g) v += red[g][f];
+                a.part[(int64_t(blockIdx.x) * 2 + m) * a.D + f] = v;
             }
         }
     }
@@ -234,29 +298,42 @@ __global__ void __launch_bounds__(kThreads) qknorm_dw_kernel(const float* part, 
 int lanes_of(int D) { return D <= 64 ? 8 : (D <= 128 ? 16 : 32); }
 
 template <int DT, int G, int HB, bool BWD>
-void launch_mode(const NormArgs& a, int mode, int grid, cudaStream_t st) {
+void launch_mode(const NormArgs& a, int mode, bool vec, int grid, cudaStream_t st) {
     switch (mode) {
-        case 0: qknorm_kernel<DT, G, HB, 0, BWD><<<grid, kThreads, 0, st>>>(a); break;
-        case 1: qknorm_kernel<DT, G, HB, 1, BWD><<<grid, kThreads, 0, st>>>(a); break;
-        case 2: qknorm_kernel<DT, G, HB, 2, BWD><<<grid, kThreads, 0, st>>>(a); break;
-        default: qknorm_kernel<DT, G, HB, 3, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 0:
+            if (vec) qknorm_kernel<DT, G, HB, 0, true, BWD><<<grid, kThreads, 0, st>>>(a);
+            else qknorm_kernel<DT, G, HB, 0, false, BWD><<<grid, kThreads, 0, st>>>(a);
+            break;
+        case 1:
+            if (vec) qknorm_kernel<DT, G, HB, 1, true, BWD><<<grid, kThreads, 0, st>>>(a);
+            else qknorm_kernel<DT, G, HB, 1, false, BWD><<<grid, kThreads, 0, st>>>(a);
+            break;
+        case 2:
+            if (vec) qknorm_kernel<DT, G, HB, 2, true, BWD><<<grid, kThreads, 0, st>>>(a);
+            else qknorm_kernel<DT, G, HB, 2, false, BWD><<<grid, kThreads, 0, st>>>(a);
+            break;
+        default: qknorm_kernel<DT, G, HB, 3, false, BWD><<<grid, kThreads, 0, st>>>(a); break;
     }
 }
 
 template <int DT, bool BWD>
-void launch_dt(const NormArgs& a, int mode, int G, int HB, int grid, cudaStream_t st) {
+void launch_dt(const NormArgs& a, int mode, bool vec, int G, int HB, int grid, cudaStream_t st) {
     if (HB == 1) {
-        if (G == 8) launch_mode<DT, 8, 1, BWD>(a, mode, grid, st);
-        else if (G == 16) launch_mode<DT, 16, 1, BWD>(a, mode, grid, st);
-        else launch_mode<DT, 32, 1, BWD>(a, mode, grid, st);
+        if (G == 8) launch_mode<DT, 8, 1, BWD>(a, mode, vec, grid, st);
+        else if (G == 16) launch_mode<DT, 16, 1, BWD>(a, mode, vec, grid, st);
+        else launch_mode<DT, 32, 1, BWD>(a, mode, vec, grid, st);
     } else {
-        if (G == 8) launch_mode<DT, 8, 3, BWD>(a, mode, grid, st);
-        else if (G == 16) launch_mode<DT, 16, 3, BWD>(a, mode, grid, st);
-        else launch_mode<DT, 32, 3, BWD>(a, mode, grid, st);
+        if (G == 8) launch_mode<DT, 8, 3, BWD>(a, mode, vec, grid, st);
+        else if (G == 16) launch_mode<DT, 16, 3, BWD>(a, mode, vec, grid, st);
+        else launch_mode<DT, 32, 3, BWD>(a, mode, vec, grid, st);
     }
 }
 
-constexpr int kMaxGrid = 152 * 8;  // CTAs of the persistent grid; bounds the partial sums
+// CTAs at most.  The forward takes a CTA per few tokens (16 x 16384 tokens of
+// 12 heads of 128: 146 us, 5.5 TB/s; a resident grid that fetches ahead took
+// 225 us); the backward keeps its grid small, as each CTA leaves a partial sum of
+// the weights' gradients (236 us, 5.1 TB/s).
+constexpr int kMaxGrid = 152 * 4, kMaxGridForward = 1 << 24;
 
 fftconv_status_t check_args(const fftconv_qknorm_args_t* p) {
     if (!p) return FFTCONV_ERR_INVALID;
@@ -264,8 +341,8 @@ fftconv_status_t check_args(const fftconv_qknorm_args_t* p) {
     if (p->dtype != FFTCONV_F16 && p->dtype != FFTCONV_BF16) return FFTCONV_ERR_UNSUPPORTED;
     if (p->norm != FFTCONV_NORM_RMS && p->norm != FFTCONV_NORM_L2) return FFTCONV_ERR_UNSUPPORTED;
     if (p->D < 8 || p->D > 256 || p->D % 8 || p->R < 0 || p->R > p->D || p->R % 2) return FFTCONV_ERR_UNSUPPORTED;
-    if (p->Hq > 65535 || p->Hk > 65535 || p->T > (int64_t(1) << 40) || p->B > (int64_t(1) << 40) ||
-        (p->T && p->B > (int64_t(1) << 40) / p->T))
+    // items and two steps of the grid beyond them in 32 bits
+    if (p->Hq > 1023 || p->Hk > 1023 || p->T >= (int64_t(1) << 30) || (p->T && p->B >= (int64_t(1) << 30) / p->T))
         return FFTCONV_ERR_UNSUPPORTED;
     if (p->R && (!p->cos || !p->sin || p->table_rows < 1)) return FFTCONV_ERR_INVALID;
     if ((reinterpret_cast<uintptr_t>(p->cos) | reinterpret_cast<uintptr_t>(p->sin) |
@@ -338,34 +415,37 @@ fftconv_status_t run(const fftconv_qknorm_args_t* p, const fftconv_view_t* dy, c
     a.sin = p->sin;
     a.pos = p->positions;
     a.rows = p->table_rows;
-    a.T = p->T;
-    a.tokens = tokens;
+    a.T = uint32_t(p->T);
     a.Hq = int(p->Hq);
     a.Hk = int(p->Hk);
     a.D = p->D;
     a.R = p->R;
-    a.inter = p->interleaved != 0;
     a.eps = p->eps;
     a.c = p->norm == FFTCONV_NORM_RMS ? 1.0f / float(p->D) : 1.0f;
     const int G = lanes_of(p->D);
-    // Heads per group: three when the call still fills the GPU that way, else
-    // one (more groups for calls of few tokens).
-    const int64_t rows = tokens * (p->Hq + p->Hk);
-    const int HB = rows * G >= int64_t(3) * 152 * 2048 ? 3 : 1;
-    a.nbq = (a.Hq + HB - 1) / HB;
-    a.nbk = (a.Hk + HB - 1) / HB;
-    a.items = tokens * (a.nbq + a.nbk);
+    // As few parts of a token's heads as fill the GPU's threads twice over: one
+    // for whole batches, one per head for single tokens.
+    const int total = a.Hq + a.Hk;
+    const int64_t want_parts = (int64_t(2) * 152 * 2048 + tokens * G - 1) / (tokens * G);
+    a.per = int((total + want_parts - 1) / want_parts);
+    a.parts = (total + a.per - 1) / a.per;
+    a.items = uint32_t(tokens * a.parts);
+    const int HB = a.per > 1 ? 3 : 1;
     const int64_t per = kThreads / G, need = (a.items + per - 1) / per;
-    const int grid = int(need < kMaxGrid ? need : kMaxGrid);
+    const int most = BWD ? kMaxGrid : kMaxGridForward;
+    const int grid = int(need < most ? need : most);
     if (want) {
         if (!scratch || scratch_bytes < size_t(grid) * 2 * wb) return FFTCONV_ERR_WORKSPACE;
         if (off16(scratch)) return FFTCONV_ERR_ALIGN;
         a.part = static_cast<float*>(scratch);
     }
     int mode = 0;
-    if (p->R) mode = a.inter ? 1 : ((p->R / 2) % 8 == 0 ? 2 : 3);
-    if (p->dtype == FFTCONV_F16) launch_dt<0, BWD>(a, mode, G, HB, grid, st);
-    else launch_dt<1, BWD>(a, mode, G, HB, grid, st);
+    if (p->R) mode = p->interleaved ? 1 : (p->R % 8 == 0 ? 2 : 3);
+    // 16-byte loads of weights and tables: rows of tables start on 16 bytes when
+    // R/2 is a multiple of 4
+    const bool vec = !(off16(p->wq) || off16(p->wk) || (p->R && (off16(p->cos) || off16(p->sin) || p->R % 8)));
+    if (p->dtype == FFTCONV_F16) launch_dt<0, BWD>(a, mode, vec, G, HB, grid, st);
+    else launch_dt<1, BWD>(a, mode, vec, G, HB, grid, st);
     if (want) qknorm_dw_kernel<<<(2 * p->D + 7) / 8, kThreads, 0, st>>>(a.part, grid, p->D, dwq, dwk);
     return cudaGetLastError() == cudaSuccess ? FFTCONV_OK : FFTCONV_ERR_CUDA;
 }
