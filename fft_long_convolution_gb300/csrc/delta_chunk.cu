@@ -29,7 +29,8 @@
 //   warps 0-15   chain: S (float32 -> operands, decayed in place), Vn and O^T, a
 //                quarter of the columns for each four warps
 //   warps 16-19  O -> global memory
-//   warp 20      issues every contraction;  warp 21  loads
+//   warp 20      issues every contraction;  warp 21  loads;  warp 22  stores what
+//                the backward needs
 #include "delta_chunk.h"
 
 #include "chunk.cuh"
@@ -478,12 +479,13 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
 template <int DK_, int DV_>
 struct FwdCfg {
     static constexpr int DK = DK_;
-    static constexpr int NKQ = 2, NI = 2;                  // stages of K and Q, and of the images
+    static constexpr int NKQ = 2, NI = 2;                  // stages of K and Q, and of the images (W: one)
     static constexpr uint32_t KQ = (DK / 64) * 2 * kTile;  // [feature block][K rows | Q rows]
     static constexpr uint32_t VB = 2 * kTile;              // DV = 64: the same block twice (M = 128)
-    static constexpr uint32_t oKQ = 0, oV = oKQ + NKQ * KQ, oI = oV + VB, oO = oI + NI * kImage<DK_>,
-                              oBar = oO + 64 * DV_ * 2, BYTES = oBar + 256;
-    static constexpr int THREADS = 704;
+    static constexpr uint32_t oKQ = 0, oV = oKQ + NKQ * KQ, oI = oV + VB, oW = oI + NI * kImgW,
+                              oO = oW + DK * 256, oSv = oO + 64 * DV_ * 2,
+                              oBar = oSv + (DK / 64 + 1) * DV_ * 128, BYTES = oBar + 256;
+    static constexpr int THREADS = 736;
     // tensor memory columns.  The two U^T / Vn^T / P Vn accumulators take turns.
     // Vn's operands take the place of S's parts: Vn that of the low part (dead
     // after S W), e Vn that of the high part (dead after S Q).
@@ -492,8 +494,10 @@ struct FwdCfg {
 };
 
 enum Bar {
-    kKqFull = 0, kKqFree = kKqFull + 2, kTFull = kKqFree + 2, kVFull = kTFull + 2, kRaw, kUDone, kSwDone, kSqDone, kVnReady, kSDone, kOReady, kOFree,
-    kSReady, kFinal,
+    kKqFull = 0, kKqFree = kKqFull + 2, kTFull = kKqFree + 2, kVFull = kTFull + 2, kWFull, kRaw, kUDone, kSwDone, kSqDone, kVnReady, kSDone, kOReady, kOFree,
+    kSv,                 // [3]: S (two blocks) and Vn are in their staging buffers
+    kSvFree = kSv + 3,   // [3]: and out of them
+    kSReady = kSvFree + 3, kFinal,
     kOpDone, kOpRead = kOpDone + 2,  // [2] each, by chunk parity
     kBars = kOpRead + 2
 };
@@ -541,7 +545,8 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         for (int i = 0; i < kBars; ++i) {
             uint32_t cnt = 1;  // else one arrival per warp of the role
             if (i == kOFree) cnt = 4;
-            if (i == kVnReady || i == kSReady || i == kOReady || i >= kOpRead) cnt = 16;
+            if (i == kVnReady || i == kSReady || i == kOReady || i == kSv + 2 || i >= kOpRead) cnt = 16;
+            if (i == kSv || i == kSv + 1) cnt = DK == 128 ? 8 : 16;
             mbar_init(bar + i, cnt);
         }
         fence_mbar_init();
@@ -559,7 +564,7 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         __syncwarp();
         if (lane == 0) arrive(bar + b);
     };
-    auto image = [&](int c) { return sm + C::oI + (c % C::NI) * kImage<DK>; };
+    auto image = [&](int c) { return sm + C::oI + (c % C::NI) * kImgW; };
 
     if (n == 0) {
         // an empty sequence: the state passes through
@@ -641,12 +646,19 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             tc::fence_before();
             done(kSReady);
             st_cols<NC>(lanes + C::cS + k0, x);  // complete before kVnReady
-            if (!STATE && a.saved_s && mine) {
-                uint8_t* sv = a.saved_s + ((slot0 + c) * d.Hv + h) * (DV * DK * 2) + (k0 >> 6) * (DV * 128) + dv * 128;
-                #pragma unroll
-                for (int j = 0; j < NC / 2; j += 4)
-                    *reinterpret_cast<uint4*>(sv + ((((k0 & 63) / 8 + j / 4) ^ (dv & 7)) * 16)) =
-                        make_uint4(hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
+            if (!STATE && a.saved_s) {
+                // a staging buffer for each block of 64 features of S, and for Vn
+                const int blk = k0 >> 6;
+                if (c > 0 && !(ok = wait(bar + kSvFree + blk, (c - 1) & 1, fail))) break;
+                if (mine) {
+                    uint8_t* sv = sm + C::oSv + blk * (DV * 128) + dv * 128;
+                    #pragma unroll
+                    for (int j = 0; j < NC / 2; j += 4)
+                        *reinterpret_cast<uint4*>(sv + ((((k0 & 63) / 8 + j / 4) ^ (dv & 7)) * 16)) =
+                            make_uint4(hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
+                }
+                tc::fence_proxy_async();
+                done(kSv + blk);
             }
             if (c > 0 && !(ok = put_o(c - 1))) break;
             // Vn^T = U^T - S^T W^T
@@ -671,10 +683,15 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             tc::wait_st();
             tc::fence_before();
             done(kVnReady);
-            if (!STATE && a.saved_v && mine) {
-                uint8_t* p = a.saved_v + ((slot0 + c) * d.Hv + h) * (DV * 128) + dv * 128;
-                *reinterpret_cast<uint4*>(p + ((j0 / 8) ^ (dv & 7)) * 16) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
-                *reinterpret_cast<uint4*>(p + ((j0 / 8 + 1) ^ (dv & 7)) * 16) = make_uint4(vh[4], vh[5], vh[6], vh[7]);
+            if (!STATE && a.saved_s) {
+                if (c > 0 && !(ok = wait(bar + kSvFree + 2, (c - 1) & 1, fail))) break;
+                if (mine) {
+                    uint8_t* sv = sm + C::oSv + (DK / 64) * (DV * 128) + dv * 128;
+                    *reinterpret_cast<uint4*>(sv + ((j0 / 8) ^ (dv & 7)) * 16) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+                    *reinterpret_cast<uint4*>(sv + ((j0 / 8 + 1) ^ (dv & 7)) * 16) = make_uint4(vh[4], vh[5], vh[6], vh[7]);
+                }
+                tc::fence_proxy_async();
+                done(kSv + 2);
             }
         }
         if (ok) ok = put_o(n - 1);
@@ -717,7 +734,7 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         bool ok = true;
         auto u_issue = [&](int c) {  // U^T = V^T (T beta)^T
             const uint64_t da = sdesc(sb + C::oV, kTile);
-            const uint64_t db = sdesc(sb + C::oI + (c % C::NI) * kImage<DK> + kImgT, 16);
+            const uint64_t db = sdesc(sb + C::oI + (c % C::NI) * kImgW + kImgT, 16);
             tc::fence_after();
             if (elect()) {
                 if (!trans) {
@@ -736,10 +753,10 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         ok = u_wait(0);
         if (ok) u_issue(0);
         for (int c = 0; ok && c < n; ++c) {
-            if (!(ok = wait(bar + kSReady, c & 1, fail))) break;
+            if (!(ok = wait(bar + kWFull, c & 1, fail) && wait(bar + kSReady, c & 1, fail))) break;
             tc::fence_after();
             if (elect()) {
-                const uint64_t dw = sdesc(sb + C::oI + (c % C::NI) * kImage<DK> + kImgW, 16);
+                const uint64_t dw = sdesc(sb + C::oW, 16);
                 #pragma unroll
                 for (int f = 0; f < DK; f += 16) {  // U^T - S^T W^T (W is stored negated)
                     tc::mma(tm + C::vn(c), tm + C::cHi + f / 2, adv(dw, f * 128), id64 | kMnB, !(trans && f == 0));
@@ -764,7 +781,7 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             if (!(ok = wait(bar + kVnReady, c & 1, fail))) break;
             tc::fence_after();
             if (elect()) {
-                const uint64_t dp = sdesc(sb + C::oI + (c % C::NI) * kImage<DK> + kImgP, 16);
+                const uint64_t dp = sdesc(sb + C::oI + (c % C::NI) * kImgW + kImgP, 16);
                 const uint64_t dk = sdesc(sb + C::oKQ + (c % C::NKQ) * C::KQ, 2 * kTile);
                 if (!STATE) {
                     #pragma unroll
@@ -790,6 +807,25 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         // everything issued is done before tensor memory is given back
         if (elect()) tc::commit(bar + kFinal);
         mbar_wait_bounded(bar + kFinal, 0, kWaitFinal);
+    } else if (warp == 22) {
+        // ---------------------------------------------------------------- S, Vn -> global
+        bool ok = true;
+        for (int c = 0; !STATE && a.saved_s && ok && c < n; ++c) {
+            const int64_t at = (slot0 + c) * d.Hv + h;
+            #pragma unroll
+            for (int b = 0; ok && b <= DK / 64; ++b) {
+                const bool v = b == DK / 64;
+                const int x = v ? 2 : b;
+                if (!(ok = wait(bar + kSv + x, c & 1, fail))) break;
+                if (elect()) {
+                    bulk_s2g(v ? a.saved_v + at * (DV * 128) : a.saved_s + at * (DV * DK * 2) + b * (DV * 128),
+                             sb + C::oSv + b * (DV * 128), DV * 128);
+                    bulk_wait_read();
+                }
+                done(kSvFree + x);
+            }
+        }
+        if (!ok) s_fail = 1;
     } else {
         // ---------------------------------------------------------------- loads
         bool ok = true;
@@ -825,8 +861,8 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             }
             if (c >= C::NI && !(ok = wait(bar + kOpRead + (c & 1), ((c - 2) >> 1) & 1, fail))) break;
             if (elect()) {
-                mbar_expect_tx(bar + kTFull + c % C::NI, kImage<DK>);
-                bulk_g2s(image(c), a.images + ((slot0 + c) * d.Hv + h) * kImage<DK>, kImage<DK>, bar + kTFull + c % C::NI);
+                mbar_expect_tx(bar + kTFull + c % C::NI, kImgW);
+                bulk_g2s(image(c), a.images + ((slot0 + c) * d.Hv + h) * kImage<DK>, kImgW, bar + kTFull + c % C::NI);
             }
             __syncwarp();
             if (c >= 1 && !(ok = wait(bar + kUDone, (c - 1) & 1, fail))) break;
@@ -845,6 +881,12 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
                 __syncwarp();
                 if (lane == 0) arrive(bar + kVFull);
             }
+            if (c >= 1 && !(ok = wait(bar + kSwDone, (c - 1) & 1, fail))) break;
+            if (elect()) {
+                mbar_expect_tx(bar + kWFull, DK * 256);
+                bulk_g2s(sm + C::oW, a.images + ((slot0 + c) * d.Hv + h) * kImage<DK> + kImgW, DK * 256, bar + kWFull);
+            }
+            __syncwarp();
         }
         if (!ok) s_fail = 1;
         // every copy has landed before the CTA leaves (bounded waits; a phase that
@@ -852,7 +894,10 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         for (int x = c > C::NKQ ? c - C::NKQ : 0; x < c; ++x)
             mbar_wait_bounded(bar + kKqFull + x % C::NKQ, (x / C::NKQ) & 1, kWaitFinal);
         for (int x = c > C::NI ? c - C::NI : 0; x < c; ++x) mbar_wait_bounded(bar + kTFull + x % C::NI, (x / C::NI) & 1, kWaitFinal);
-        if (c > 0) mbar_wait_bounded(bar + kVFull, (c - 1) & 1, kWaitFinal);
+        if (c > 0) {
+            mbar_wait_bounded(bar + kVFull, (c - 1) & 1, kWaitFinal);
+            mbar_wait_bounded(bar + kWFull, (c - 1) & 1, kWaitFinal);
+        }
     }
     tc::fence_before();
     __syncthreads();

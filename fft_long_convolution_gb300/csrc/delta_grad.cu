@@ -29,25 +29,27 @@ using namespace tile;
 // Roles by warp, as in delta_fwd_kernel:
 //   warps 0-15   chain: dS^T (float32 -> operands, decayed in place), dVn^T, dR^T
 //   warps 16-19  scale G dO -> operand
-//   warp 20      issues every contraction;  warp 21  loads;  warp 22  stores
+//   warp 20      issues every contraction;  warp 21  loads;  warp 22  stores dR and
+//                dV;  warp 23  stores dS'
 template <int DK_, int DV_>
 struct BwdCfg {
     static constexpr int DK = DK_;
     static constexpr uint32_t KQ = (DK / 64) * 2 * kTile;  // [feature block][K rows | Q rows]
     static constexpr uint32_t DO = 2 * kTile;              // DV = 64: the same block twice (M = 128)
     static constexpr uint32_t WB = DK * 128;
-    // of an image: P, the decays, -W^T (high part); then T
-    static constexpr uint32_t iE = kTile, iW = iE + 1024, iT = iW + WB, IM = iT + kTile;
-    static constexpr uint32_t oKQ = 0, oDO = oKQ + 2 * KQ, oDS = oDO + DO, oI = oDS + DO, oR = oI + 2 * IM,
-                              oV = oR + 2 * DV_ * 128, oBar = oV + DV_ * 128, BYTES = oBar + 256;
-    static constexpr int THREADS = 736;
+    // of an image, two stages: P, the decays; then T.  -W^T (high part): one
+    static constexpr uint32_t iE = kTile, iT = iE + 1024, IM = iT + kTile;
+    static constexpr uint32_t oKQ = 0, oDO = oKQ + 2 * KQ, oDS = oDO + DO, oI = oDS + DO, oW = oI + 2 * IM, oR = oW + WB,
+                              oV = oR + 2 * DV_ * 128, oSv = oV + DV_ * 128, oBar = oSv + (DK / 64) * DV_ * 128, BYTES = oBar + 256;
+    static constexpr int THREADS = 768;
     // tensor memory columns
     static constexpr uint32_t cS = 0, cHi = 128, cLo = 192, cC2 = 256, cC1 = 320, cVn = 384, cVl = 416, cR = 448;
 };
 
 enum BBar {
     bKqFull = 0, bKqFree = 2, bImFull = 4, bRead = 6,  // [2] each, by step parity
-    bDoFull = 8, bRaw, bDosReady, bDosFree, bC1, bC2, bSReady, bVnReady, bSDone, bR, bStReady, bStFree, bFinal, bBars
+    bDoFull = 8, bRaw, bDosReady, bDosFree, bC1, bC2, bSReady, bVnReady, bSDone, bR, bStReady, bStFree, bFinal, bWFull, bSvFree, bSv = bSvFree + 2,  // [2] each, by block
+    bBars = bSv + 2
 };
 
 template <int DT, int DK, int DV>
@@ -75,6 +77,7 @@ delta_dstate_kernel(const __grid_constant__ GradArgs a) {
             uint32_t cnt = 1;  // else one arrival per warp of the role
             if (i == bDosReady) cnt = 4;
             if (i == bSReady || i == bVnReady || i == bStReady || i == bRead || i == bRead + 1) cnt = 16;
+            if (i >= bSv) cnt = DK == 128 ? 8 : 16;
             mbar_init(bar + i, cnt);
         }
         fence_mbar_init();
@@ -175,12 +178,18 @@ delta_dstate_kernel(const __grid_constant__ GradArgs a) {
             tc::wait_st();
             tc::fence_before();
             done(bSReady);
-            if (mine) {
-                uint8_t* p = a.ds + at(c) * (DV * DK * 2) + (k0 >> 6) * (DV * 128) + dv * 128;
-                #pragma unroll
-                for (int j = 0; j < NC / 2; j += 4)
-                    *reinterpret_cast<uint4*>(p + ((((k0 & 63) / 8 + j / 4) ^ (dv & 7)) * 16)) =
-                        make_uint4(hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
+            {  // dS'^T -> global memory, a block of 64 features at a time
+                const int blk = k0 >> 6;
+                if (c > 0 && !(ok = wait(bar + bSvFree + blk, (c - 1) & 1, fail))) break;
+                if (mine) {
+                    uint8_t* p = sm + C::oSv + blk * (DV * 128) + dv * 128;
+                    #pragma unroll
+                    for (int j = 0; j < NC / 2; j += 4)
+                        *reinterpret_cast<uint4*>(p + ((((k0 & 63) / 8 + j / 4) ^ (dv & 7)) * 16)) =
+                            make_uint4(hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
+                }
+                tc::fence_proxy_async();
+                done(bSv + blk);
             }
             if (c > 0 && !(ok = put_r(c - 1))) break;
             // dVn^T = dO^T P + e (dS'^T K^T)
@@ -290,10 +299,10 @@ delta_dstate_kernel(const __grid_constant__ GradArgs a) {
                     tc::mma_ss(tm + C::cS, adv(da, t * 128), adv(dq, t * 128), idK | kMnA | kMnB, 1);
                 tc::commit(bar + bDosFree);
             }
-            if (!(ok = wait(bar + bVnReady, c & 1, fail))) break;
+            if (!(ok = wait(bar + bWFull, c & 1, fail) && wait(bar + bVnReady, c & 1, fail))) break;
             tc::fence_after();
             if (elect()) {
-                const uint64_t dw = sdesc(im + C::iW, 16);
+                const uint64_t dw = sdesc(sb + C::oW, 16);
                 #pragma unroll
                 for (int t = 0; t < 64; t += 16) {  // dS^T -= dVn^T W (W is stored negated)
                     tc::mma(tm + C::cS, tm + C::cVn + t / 2, adv(dw, t * 2), idK, 1);
@@ -358,7 +367,7 @@ delta_dstate_kernel(const __grid_constant__ GradArgs a) {
                 const uint8_t* src = a.images + at(c) * kImage<DK>;
                 mbar_expect_tx(b, C::IM);
                 bulk_g2s(image(c), src + kImgP, kTile, b);
-                bulk_g2s(image(c) + C::iE, src + kImgE, 1024 + C::WB, b);
+                bulk_g2s(image(c) + C::iE, src + kImgE, 1024, b);
                 bulk_g2s(image(c) + C::iT, a.saved_t + at(c) * kTile, kTile, b);
             }
             __syncwarp();
@@ -378,13 +387,37 @@ delta_dstate_kernel(const __grid_constant__ GradArgs a) {
                 __syncwarp();
                 if (lane == 0) arrive(bar + bDoFull);
             }
+            if (c >= 1 && !(ok = wait(bar + bSDone, (c - 1) & 1, fail))) break;
+            if (elect()) {
+                mbar_expect_tx(bar + bWFull, C::WB);
+                bulk_g2s(sm + C::oW, a.images + at(c) * kImage<DK> + kImgW, C::WB, bar + bWFull);
+            }
+            __syncwarp();
         }
         if (!ok) s_fail = 1;
         for (int x = c > 2 ? c - 2 : 0; x < c; ++x) {  // every copy has landed before the CTA leaves
             mbar_wait_bounded(bar + bKqFull + (x & 1), (x >> 1) & 1, kWaitFinal);
             mbar_wait_bounded(bar + bImFull + (x & 1), (x >> 1) & 1, kWaitFinal);
         }
-        if (c > 0) mbar_wait_bounded(bar + bDoFull, (c - 1) & 1, kWaitFinal);
+        if (c > 0) {
+            mbar_wait_bounded(bar + bDoFull, (c - 1) & 1, kWaitFinal);
+            mbar_wait_bounded(bar + bWFull, (c - 1) & 1, kWaitFinal);
+        }
+    } else if (warp == 23) {
+        // ---------------------------------------------------------------- dS' -> global
+        bool ok = true;
+        for (int c = 0; ok && c < n; ++c) {
+            #pragma unroll
+            for (int b = 0; ok && b < DK / 64; ++b) {
+                if (!(ok = wait(bar + bSv + b, c & 1, fail))) break;
+                if (elect()) {
+                    bulk_s2g(a.ds + at(c) * (DV * DK * 2) + b * (DV * 128), sb + C::oSv + b * (DV * 128), DV * 128);
+                    bulk_wait_read();
+                }
+                done(bSvFree + b);
+            }
+        }
+        if (!ok) s_fail = 1;
     } else {
         // ---------------------------------------------------------------- dR, dV -> global
         bool ok = true;
