@@ -457,7 +457,7 @@ delta_dstate_kernel(const __grid_constant__ GradArgs a) {
 
 // ------------------------------------------------------------ dQ, dK, dbeta, dg
 //
-// One chunk of one value head at a time, one CTA per SM.  Rows 0-63 of the
+// One chunk of one value head at a time, one CTA per SM (two for heads of 64).  Rows 0-63 of the
 // M = 128 products belong to dO (and X), rows 64-127 to dR (and H); the
 // products whose rows are keys are placed at rows 64-127 too (their A operand
 // starts one block early: rows 0-63 are never used), so dK's parts meet in one
@@ -465,32 +465,33 @@ delta_dstate_kernel(const __grid_constant__ GradArgs a) {
 template <int DK, int DV>
 struct GradCfg {
     static constexpr uint32_t oA = 0;                      // [feature block][dO rows | dR rows]
-    static constexpr uint32_t oB = oA + 4 * kTile;         // [feature block][Q rows | K rows]
-    static constexpr uint32_t oV = oB + 4 * kTile;         // V
-    static constexpr uint32_t oN = oV + 2 * kTile;         // Vn^T: DV rows of 64 tokens
-    static constexpr uint32_t oS = oN + 2 * kTile;         // S^T: [DK / 64] blocks of DV rows
-    static constexpr uint32_t oD = oS + 4 * kTile;         // dS'^T
-    static constexpr uint32_t oX = oD + 4 * kTile;         // [X; H], then dQ
+    static constexpr uint32_t oB = oA + (DV / 64) * 2 * kTile;  // [feature block][Q rows | K rows]
+    static constexpr uint32_t oV = oB + (DK / 64) * 2 * kTile;  // V
+    static constexpr uint32_t oN = oV + DV * 128;          // Vn^T: DV rows of 64 tokens
+    static constexpr uint32_t oS = oN + DV * 128;          // S^T: [DK / 64] blocks of DV rows
+    static constexpr uint32_t oD = oS + DK * DV * 2;       // dS'^T
+    static constexpr uint32_t oX = oD + DK * DV * 2;       // [X; H], then dQ
     static constexpr uint32_t oG = oX + 2 * kTile;         // [X; beta H], then dK
     static constexpr uint32_t oR = oG + 2 * kTile;         // dR's low part
-    static constexpr uint32_t oE = oR + DV * 128;          // the image's decays
-    static constexpr uint32_t oL = oE + 1024;              // row sums: [4][2][64], dR.V [4][64], <S, dS'> [8]
+    static constexpr uint32_t oE = oR + DV * 128;          // the image's decays, two stages
+    static constexpr uint32_t oL = oE + 2048;              // row sums: [4][2][64], dR.V [4][64], <S, dS'> [8]
     static constexpr uint32_t oItem = oL + (8 * 64 + 4 * 64 + 8) * 4, oBar = oItem + 64, BYTES = oBar + 128;
+    // small heads: two CTAs per SM
+    static constexpr int PER_SM = (BYTES + 1024) * 2 <= 233472 && DK == 64 ? 2 : 1;
     // bytes of the three groups of loads
     static constexpr uint32_t B0 = 4 * DV * 128 + 1024, B1 = 2 * DV * DK * 2, B2 = DK * 256 + DV * 128;
     // tensor memory columns; the scores' 64 columns are taken over by E2
-    static constexpr uint32_t cE1 = 0, cE2 = 128, cSc = 128, cD1 = 256, cD2 = 384;
+    static constexpr uint32_t cE1 = 0, cE2 = DK, cSc = DK, cD1 = 2 * DK, cD2 = 3 * DK, COLS = 4 * DK;
 };
 
 template <int DT, int DK, int DV>
-__global__ void __launch_bounds__(256, 1) delta_grad_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(256, GradCfg<DK, DV>::PER_SM) delta_grad_kernel(const __grid_constant__ GradArgs a) {
     using C = GradCfg<DK, DV>;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);  // loads 0-2, scores, D1 and E1, D2 and E2
     ChunkItem* items = reinterpret_cast<ChunkItem*>(sm + C::oItem);
     float *red = reinterpret_cast<float*>(sm + C::oL), *rv = red + 512, *sd = rv + 256;
-    const float* gt = reinterpret_cast<const float*>(sm + C::oE);
     const DeltaArgs& d = a.d;
     const int p = threadIdx.x, w = __shfl_sync(0xffffffffu, p / 32, 0), lane = p % 32;
     if (sb & 1023) {  // not with the present layout of the window
@@ -502,10 +503,10 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const __grid_constan
         fence_mbar_init();
     }
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + 8);
-    if (w == 1) tc::alloc(s_tmem, 512);
+    if (w == 1) tc::alloc(s_tmem, C::COLS);
     int next = blockIdx.x;
     // dO, dR, Vn and the decays; S and dS'; Q, K and V (one thread)
-    auto load0 = [&](const ChunkItem& it) {
+    auto load0 = [&](const ChunkItem& it, uint32_t stage) {
         mbar_expect_tx(bar, C::B0);
         #pragma unroll
         for (int f = 0; f < DV / 64; ++f) {
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const __grid_constan
         }
         bulk_g2s(sm + C::oR, a.dr + it.at * (2 * DV * 128) + DV * 128, DV * 128, bar);
         bulk_g2s(sm + C::oN, a.saved_v + it.at * (DV * 128), DV * 128, bar);
-        bulk_g2s(sm + C::oE, a.images + it.at * kImage<DK> + kImgE, 1024, bar);
+        bulk_g2s(sm + C::oE + stage * 1024, a.images + it.at * kImage<DK> + kImgE, 1024, bar);
     };
     auto load1 = [&](const ChunkItem& it) {
         mbar_expect_tx(bar + 1, C::B1);
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const __grid_constan
     const int row = 32 * (w & 3) + lane, i = row & 63, half = w >> 2;
     const bool lower = row >= 64;  // dR, H, Y, dK
     if (p == 96 && items[0].m) {
-        load0(items[0]);
+        load0(items[0], 0);
         load1(items[0]);
         load2(items[0]);
     }
@@ -558,6 +559,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const __grid_constan
         const ChunkItem it = items[k & 1];
         const uint32_t par = k & 1;
         const bool tail = d.offsets && it.m < kChunk;
+        const float* gt = reinterpret_cast<const float*>(sm + C::oE + par * 1024);
         // scores [dO; dR] Vn^T, then D1 = [dO; dR] S^T and E1 = Vn dS'^T
         ok = mbar_wait_bounded(bar, par, kWaitLimitTile);
         if (tail) {
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const __grid_constan
         if (w == 0) {
             constexpr uint32_t id = tc::idesc(DT, 128, DK) | kMnB;
             const uint64_t da = sdesc(sb + C::oA, 16), ds = sdesc(sb + C::oS, DV * 128);
-            const uint64_t dn = sdesc(sb + C::oN - 2 * kTile, 2 * kTile), dd = sdesc(sb + C::oD, DV * 128);
+            const uint64_t dn = sdesc(sb + C::oV, DV * 128), dd = sdesc(sb + C::oD, DV * 128);
             if (elect()) {
                 #pragma unroll
                 for (int f = 0; f < DV; f += 16)
@@ -695,6 +697,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const __grid_constan
         ok = ok && mbar_wait_bounded(bar + 5, par, kWaitLimitTile);
         if (!(ok = !__syncthreads_or(!ok))) break;
         tc::fence_after();
+        if (p == 96 && items[~k & 1].m) load0(items[~k & 1], ~k & 1);  // dO, dR and Vn have been read
         // rows of dQ (upper) and of Y and dK (lower), a half of the features per thread
         {
             const float sg = lower ? -exp2_fast(gt[128 + i]) : gt[64 + i];
@@ -763,10 +766,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const __grid_constan
         tc::fence_proxy_async();
         tc::fence_before();
         __syncthreads();
-        if (p == 96 && items[~k & 1].m) {
-            // everything of this chunk but the decays has been read
-            load2(items[~k & 1]);
-        }
+        if (p == 96 && items[~k & 1].m) load2(items[~k & 1]);  // and Q, K, V
         if (!a.dqh) {
             if (!tail) {
                 if (p == 0) {  // tokens past the tensor's end are not written
@@ -823,7 +823,6 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const __grid_constan
             }
         }
         __syncthreads();
-        if (p == 96 && items[~k & 1].m) load0(items[~k & 1]);
     }
     if (p == 0) bulk_wait_read();
     if (p == 0 && !ok) {
@@ -833,7 +832,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(const __grid_constan
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (w == 1) tc::dealloc(tm, 512);
+    if (w == 1) tc::dealloc(tm, C::COLS);
 }
 
 // dq, dk [token][Hk][DK] = the sum over a key head's value heads, 8 features a thread.
@@ -870,7 +869,8 @@ cudaError_t launch(const GradArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     delta_dstate_kernel<DT, DK, DV><<<dim3(unsigned(a.d.nseq), unsigned(a.d.Hv)), BwdCfg<DK, DV>::THREADS, sb, st>>>(a);
     const int64_t items = a.slots * a.d.Hv;
-    delta_grad_kernel<DT, DK, DV><<<unsigned(items < a.sms ? items : a.sms), 256, sg, st>>>(a);
+    const int64_t most = int64_t(a.sms) * GradCfg<DK, DV>::PER_SM;
+    delta_grad_kernel<DT, DK, DV><<<unsigned(items < most ? items : most), 256, sg, st>>>(a);
     if (a.dqh) {
         const int64_t n = (a.d.B * a.d.T * a.d.Hk * (DK / 8) * 2 + 255) / 256;
         head_sum_kernel<DT><<<unsigned(n < 152 * 32 ? n : 152 * 32), 256, 0, st>>>(a.dqh, a.dkh, a.dq, a.dk, a.d.B * a.d.T,
