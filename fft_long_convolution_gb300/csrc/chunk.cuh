@@ -37,10 +37,8 @@ struct ChunkItem {
     int64_t at;
 };
 
-// The next item from *next on (a stride of the grid apart) that has tokens, by
-// one warp.
-__device__ __forceinline__ void find_item(const DeltaArgs& d, int slots, int* next, ChunkItem* to) {
-    ChunkItem it{0, 0, 0, 0, 0};
+// The next item from *next on (a stride of the grid apart) that has tokens.
+__device__ __forceinline__ ChunkItem find_item(const DeltaArgs& d, int slots, int* next) {
     const int count = slots * d.Hv;
     while (*next < count) {
         const int x = *next, slot = x / d.Hv;
@@ -50,10 +48,9 @@ __device__ __forceinline__ void find_item(const DeltaArgs& d, int slots, int* ne
         *next = count - x > int(gridDim.x) ? x + int(gridDim.x) : count;
         if (!find_chunk(d, slot, &s, &si, &ch)) continue;
         const int64_t left = s.len - ch * kChunk;
-        it = {int(s.row), int(s.start + ch * kChunk), int(left < kChunk ? left : kChunk), x - slot * d.Hv, x};
-        break;
+        return {int(s.row), int(s.start + ch * kChunk), int(left < kChunk ? left : kChunk), x - slot * d.Hv, x};
     }
-    if (threadIdx.x % 32 == 0) *to = it;
+    return {0, 0, 0, 0, 0};
 }
 
 template <typename K>

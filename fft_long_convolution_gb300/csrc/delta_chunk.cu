@@ -203,7 +203,10 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + 3);
     if (w == 1) tc::alloc(s_tmem, 64);
     int next = blockIdx.x;
-    auto find = [&](ChunkItem* to) { find_item(d, int(a.slots), &next, to); };  // warp 3
+    auto find = [&](ChunkItem* to) {  // warp 3
+        const ChunkItem x = find_item(d, int(a.slots), &next);
+        if (lane == 0) *to = x;
+    };
     auto load = [&](const ChunkItem& it) {  // one warp
         if (elect()) {
             mbar_expect_tx(bar, C::KQ);

@@ -461,7 +461,10 @@ delta_dstate_kernel(const __grid_constant__ GradArgs a) {
 // M = 128 products belong to dO (and X), rows 64-127 to dR (and H); the
 // products whose rows are keys are placed at rows 64-127 too (their A operand
 // starts one block early: rows 0-63 are never used), so dK's parts meet in one
-// thread.  Bound: HBM, 160 KB read and 32 KB written per chunk at Dk = Dv = 128.
+// thread.  Roles: warps 0-7 form X and H and the gradients' rows, warp 8 stores
+// them and forms the gates' gradients, warp 9 loads (a chunk ahead, each buffer as
+// soon as it has been read) and issues the products.  Bound: HBM, 193 KB read and
+// 32 KB written per chunk at Dk = Dv = 128.
 template <int DK, int DV>
 struct GradCfg {
     static constexpr uint32_t oA = 0;                      // [feature block][dO rows | dR rows]
@@ -474,8 +477,10 @@ struct GradCfg {
     static constexpr uint32_t oG = oX + 2 * kTile;         // [X; beta H], then dK
     static constexpr uint32_t oR = oG + 2 * kTile;         // dR's low part
     static constexpr uint32_t oE = oR + DV * 128;          // the image's decays, two stages
-    static constexpr uint32_t oL = oE + 2048;              // row sums: [4][2][64], dR.V [4][64], <S, dS'> [8]
-    static constexpr uint32_t oItem = oL + (8 * 64 + 4 * 64 + 8) * 4, oBar = oItem + 64, BYTES = oBar + 128;
+    // two stages of row sums: [4][2][64], dR.V [4][64], <S, dS'> [8]
+    static constexpr uint32_t oL = oE + 2048, LB = (8 * 64 + 4 * 64 + 8) * 4;
+    static constexpr uint32_t oItem = oL + 2 * LB, oBar = oItem + 64, BYTES = oBar + 128;
+    static constexpr int THREADS = 320;
     // small heads: two CTAs per SM
     static constexpr int PER_SM = (BYTES + 1024) * 2 <= 233472 && DK == 64 ? 2 : 1;
     // bytes of the three groups of loads
@@ -484,14 +489,22 @@ struct GradCfg {
     static constexpr uint32_t cE1 = 0, cE2 = DK, cSc = DK, cD1 = 2 * DK, cD2 = 3 * DK, COLS = 4 * DK;
 };
 
+enum GBar {
+    gLoad = 0,  // [3] groups of loads
+    gScores = 3, gD1, gD2,                    // scores; D1 and E1; D2 and E2 are done
+    gIn, gX, gRv, gRows, gItem, gStFree, gBars  // dO is in order; X, H, Q, K are; dR.V is done; the rows are out
+};
+
 template <int DT, int DK, int DV>
-__global__ void __launch_bounds__(256, GradCfg<DK, DV>::PER_SM) delta_grad_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(GradCfg<DK, DV>::THREADS, GradCfg<DK, DV>::PER_SM)
+delta_grad_kernel(const __grid_constant__ GradArgs a) {
     using C = GradCfg<DK, DV>;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
-    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);  // loads 0-2, scores, D1 and E1, D2 and E2
-    ChunkItem* items = reinterpret_cast<ChunkItem*>(sm + C::oItem);
-    float *red = reinterpret_cast<float*>(sm + C::oL), *rv = red + 512, *sd = rv + 256;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);
+    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 112);
+    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 116);
+    ChunkItem* items = reinterpret_cast<ChunkItem*>(sm + C::oItem);  // [2]
     const DeltaArgs& d = a.d;
     const int p = threadIdx.x, w = __shfl_sync(0xffffffffu, p / 32, 0), lane = p % 32;
     if (sb & 1023) {  // not with the present layout of the window
@@ -499,296 +512,245 @@ __global__ void __launch_bounds__(256, GradCfg<DK, DV>::PER_SM) delta_grad_kerne
         return;
     }
     if (p == 0) {
-        for (int i = 0; i < 6; ++i) mbar_init(bar + i, 1);
+        s_fail = 0;
+        for (int i = 0; i < gBars; ++i) mbar_init(bar + i, i == gIn || i == gX || i == gRv || i == gRows ? 8 : 1);
         fence_mbar_init();
     }
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + 8);
-    if (w == 1) tc::alloc(s_tmem, C::COLS);
-    int next = blockIdx.x;
-    // dO, dR, Vn and the decays; S and dS'; Q, K and V (one thread)
-    auto load0 = [&](const ChunkItem& it, uint32_t stage) {
-        mbar_expect_tx(bar, C::B0);
-        #pragma unroll
-        for (int f = 0; f < DV / 64; ++f) {
-            tma_load_4d(sb + C::oA + f * 2 * kTile, &a.mo, f * 64, it.h, it.t0, it.row, bar);
-            bulk_g2s(sm + C::oA + f * 2 * kTile + kTile, a.dr + it.at * (2 * DV * 128) + f * kTile, kTile, bar);
-        }
-        bulk_g2s(sm + C::oR, a.dr + it.at * (2 * DV * 128) + DV * 128, DV * 128, bar);
-        bulk_g2s(sm + C::oN, a.saved_v + it.at * (DV * 128), DV * 128, bar);
-        bulk_g2s(sm + C::oE + stage * 1024, a.images + it.at * kImage<DK> + kImgE, 1024, bar);
-    };
-    auto load1 = [&](const ChunkItem& it) {
-        mbar_expect_tx(bar + 1, C::B1);
-        bulk_g2s(sm + C::oS, a.saved_s + it.at * (DV * DK * 2), DV * DK * 2, bar + 1);
-        bulk_g2s(sm + C::oD, a.ds + it.at * (DV * DK * 2), DV * DK * 2, bar + 1);
-    };
-    auto load2 = [&](const ChunkItem& it) {
-        mbar_expect_tx(bar + 2, C::B2);
-        #pragma unroll
-        for (int f = 0; f < DK / 64; ++f) {
-            tma_load_4d(sb + C::oB + f * 2 * kTile, &a.mq, f * 64, it.h / d.group, it.t0, it.row, bar + 2);
-            tma_load_4d(sb + C::oB + f * 2 * kTile + kTile, &a.mk, f * 64, it.h / d.group, it.t0, it.row, bar + 2);
-        }
-        #pragma unroll
-        for (int f = 0; f < DV / 64; ++f) tma_load_4d(sb + C::oV + f * kTile, &a.mv, f * 64, it.h, it.t0, it.row, bar + 2);
-    };
-    // zero rows m .. 63 of `n` tiles `step` bytes apart: in a packed row they are
-    // the next sequence's (past the tensor's end the TMA engine writes zeros)
-    auto fix = [&](uint32_t off, int n, uint32_t step, int m) {
-        for (int x = p; x < (64 - m) * 8 * n; x += 256) {
-            const int f = x / ((64 - m) * 8), y = x % ((64 - m) * 8);
-            *reinterpret_cast<uint4*>(sm + off + f * step + m * 128 + y * 16) = make_uint4(0, 0, 0, 0);
-        }
-    };
-    if (w == 3) find_item(d, int(a.slots), &next, items);
+    if (w == 9) tc::alloc(&s_tmem, C::COLS);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(s_tmem);
-    const uint32_t lanes = tm + (uint32_t(32 * (w & 3)) << 16);
-    const int row = 32 * (w & 3) + lane, i = row & 63, half = w >> 2;
-    const bool lower = row >= 64;  // dR, H, Y, dK
-    if (p == 96 && items[0].m) {
-        load0(items[0], 0);
-        load1(items[0]);
-        load2(items[0]);
-    }
+    const uint32_t tm = *const_cast<volatile uint32_t*>(&s_tmem);
+    volatile int* fail = &s_fail;
+    auto done = [&](int b) {
+        __syncwarp();
+        if (lane == 0) arrive(bar + b);
+    };
     bool ok = true;
     uint32_t k = 0;
-    for (; items[k & 1].m; ++k) {
-        const ChunkItem it = items[k & 1];
-        const uint32_t par = k & 1;
-        const bool tail = d.offsets && it.m < kChunk;
-        const float* gt = reinterpret_cast<const float*>(sm + C::oE + par * 1024);
-        // scores [dO; dR] Vn^T, then D1 = [dO; dR] S^T and E1 = Vn dS'^T
-        ok = mbar_wait_bounded(bar, par, kWaitLimitTile);
-        if (tail) {
-            fix(C::oA, DV / 64, 2 * kTile, it.m);
-            tc::fence_proxy_async();
-        }
-        if (p == 0) bulk_wait_read();  // the last dQ and dK have left shared memory
-        if (!(ok = !__syncthreads_or(!ok))) break;
-        if (w == 0) {
-            tc::fence_after();
-            const uint64_t da = sdesc(sb + C::oA, 16), dn = sdesc(sb + C::oN, 16);
-            if (elect()) {
-                #pragma unroll
-                for (int f = 0; f < DV; f += 16)
-                    tc::mma_ss(tm + C::cSc, adv(da, (f / 64) * 2 * kTile + (f % 64) * 2), adv(dn, f * 128),
-                               tc::idesc(DT, 128, 64) | kMnB, f > 0);
-                tc::commit(bar + 3);
+    if (w < 8) {
+        // ---------------------------------------------------------------- rows
+        const uint32_t lanes = tm + (uint32_t(32 * (w & 3)) << 16);
+        const int row = 32 * (w & 3) + lane, i = row & 63, half = w >> 2;
+        const bool lower = row >= 64;  // dR, H, Y, dK
+        // zero rows m .. 63 of `n` tiles `step` bytes apart: in a packed row they are
+        // the next sequence's (past the tensor's end the TMA engine writes zeros)
+        auto fix = [&](uint32_t off, int n, uint32_t step, int m) {
+            for (int x = p; x < (64 - m) * 8 * n; x += 256) {
+                const int f = x / ((64 - m) * 8), y = x % ((64 - m) * 8);
+                *reinterpret_cast<uint4*>(sm + off + f * step + m * 128 + y * 16) = make_uint4(0, 0, 0, 0);
             }
-        }
-        if (w == 3) find_item(d, int(a.slots), &next, items + (~k & 1));
-        ok = mbar_wait_bounded(bar + 1, par, kWaitLimitTile);
-        if (!(ok = !__syncthreads_or(!ok))) break;
-        if (w == 0) {
-            constexpr uint32_t id = tc::idesc(DT, 128, DK) | kMnB;
-            const uint64_t da = sdesc(sb + C::oA, 16), ds = sdesc(sb + C::oS, DV * 128);
-            const uint64_t dn = sdesc(sb + C::oV, DV * 128), dd = sdesc(sb + C::oD, DV * 128);
-            if (elect()) {
-                #pragma unroll
-                for (int f = 0; f < DV; f += 16)
-                    tc::mma_ss(tm + C::cD1, adv(da, (f / 64) * 2 * kTile + (f % 64) * 2), adv(ds, f * 128), id, f > 0);
-                #pragma unroll
-                for (int f = 0; f < DV; f += 16)
-                    tc::mma_ss(tm + C::cE1, adv(dn, f * 128), adv(dd, f * 128), id | kMnA, f > 0);
-                tc::commit(bar + 4);
+        };
+        for (;; ++k) {
+            const uint32_t par = k & 1;
+            if (!(ok = wait(bar + gItem, par, fail))) break;
+            const ChunkItem it = items[k & 1];
+            if (!it.m) break;
+            const bool tail = d.offsets && it.m < kChunk;
+            const float* gt = reinterpret_cast<const float*>(sm + C::oE + par * 1024);
+            float *red = reinterpret_cast<float*>(sm + C::oL + par * C::LB), *rv = red + 512, *sd = rv + 256;
+            if (!(ok = wait(bar + gLoad, par, fail))) break;
+            if (tail) {
+                fix(C::oA, DV / 64, 2 * kTile, it.m);
+                tc::fence_proxy_async();
             }
-        }
-        // <S, dS'> meanwhile
-        {
-            float v = 0.0f;
-            #pragma unroll 4
-            for (int x = p; x < DV * DK / 8; x += 256) {
-                const uint4 y = *reinterpret_cast<const uint4*>(sm + C::oS + x * 16);
-                const uint4 z = *reinterpret_cast<const uint4*>(sm + C::oD + x * 16);
-                const uint32_t ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w};
-                #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const cpx u = Op<DT>::unpack(ys[q]), t = Op<DT>::unpack(zs[q]);
-                    v = fmaf(u.r, t.r, fmaf(u.i, t.i, v));
-                }
-            }
-            #pragma unroll
-            for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0) sd[w] = v;
-        }
-        ok = mbar_wait_bounded(bar + 3, par, kWaitLimitTile);
-        if (!(ok = !__syncthreads_or(!ok))) break;
-        tc::fence_after();
-        // X and H: the scores times the decays; warps 0-3 columns 0-31, 4-7 the others
-        {
-            uint32_t x[32];
-            const int j0 = half * 32;
-            tc::ld32x32b_x32(lanes + C::cSc + j0, x);
-            tc::wait_ld();
-            const float bi = gt[128 + i], f = lower ? -1.0f : d.scale, be = lower ? gt[192 + i] : 1.0f;
-            const int last = (lower ? i - 1 : i) - j0;
-            uint8_t *px = sm + C::oX + row * 128, *pg = sm + C::oG + row * 128;
-            #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-                uint32_t u[4], g[4];
-                #pragma unroll
-                for (int q = 0; q < 8; q += 4) {
-                    const float4 b = *reinterpret_cast<const float4*>(gt + 128 + j0 + j + q);
-                    const float bj[4] = {b.x, b.y, b.z, b.w};
-                    float v[4];
+            done(gIn);
+            // <S, dS'> while the scores are formed
+            if (!(ok = wait(bar + gLoad + 1, par, fail))) break;
+            {
+                float v = 0.0f, u = 0.0f;
+                #pragma unroll 4
+                for (int x = p; x < DV * DK / 8; x += 256) {
+                    const uint4 y = *reinterpret_cast<const uint4*>(sm + C::oS + x * 16);
+                    const uint4 z = *reinterpret_cast<const uint4*>(sm + C::oD + x * 16);
+                    const uint32_t ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w};
                     #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float y = f * exp2_fast(bi - bj[r]) * __uint_as_float(x[j + q + r]);
-                        v[r] = j + q + r <= last ? y : 0.0f;  // above the diagonal, whatever it holds
+                    for (int q = 0; q < 4; ++q) {
+                        const cpx e = Op<DT>::unpack(ys[q]), t = Op<DT>::unpack(zs[q]);
+                        v = fmaf(e.r, t.r, v);
+                        u = fmaf(e.i, t.i, u);
                     }
-                    u[q / 2] = Op<DT>::pack(v[0], v[1]);
-                    u[q / 2 + 1] = Op<DT>::pack(v[2], v[3]);
-                    g[q / 2] = Op<DT>::pack(be * v[0], be * v[1]);
-                    g[q / 2 + 1] = Op<DT>::pack(be * v[2], be * v[3]);
                 }
-                const int pos = (((j0 + j) / 8) ^ (row & 7)) * 16;
-                *reinterpret_cast<uint4*>(px + pos) = make_uint4(u[0], u[1], u[2], u[3]);
-                *reinterpret_cast<uint4*>(pg + pos) = make_uint4(g[0], g[1], g[2], g[3]);
+                v += u;
+                #pragma unroll
+                for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == 0) sd[w] = v;
             }
-        }
-        ok = mbar_wait_bounded(bar + 2, par, kWaitLimitTile);
-        if (tail) {
-            fix(C::oB, 2 * (DK / 64), kTile, it.m);
-            fix(C::oV, DV / 64, kTile, it.m);
-        }
-        tc::fence_proxy_async();
-        tc::fence_before();
-        if (!(ok = !__syncthreads_or(!ok))) break;
-        if (w == 0) {
+            ok = wait(bar + gScores, par, fail);
+            if (ok && k > 0) ok = wait(bar + gStFree, par ^ 1, fail);  // the last dQ and dK have left shared memory
+            if (!ok) break;
             tc::fence_after();
-            constexpr uint32_t id = tc::idesc(DT, 128, DK) | kMnB;
-            const uint64_t dx = sdesc(sb + C::oX, 16), dk = sdesc(sb + C::oB + kTile, 2 * kTile);
-            const uint64_t dg = sdesc(sb + C::oG - 2 * kTile, 2 * kTile), dq = sdesc(sb + C::oB, 2 * kTile);
-            if (elect()) {
-                #pragma unroll
-                for (int t = 0; t < 64; t += 16)  // [X; H] K
-                    tc::mma_ss(tm + C::cD2, adv(dx, t * 2), adv(dk, t * 128), id, t > 0);
-                #pragma unroll
-                for (int t = 0; t < 128; t += 16)  // [X; beta H]^T [Q; K]
-                    tc::mma_ss(tm + C::cE2, adv(dg, t * 128), adv(dq, t * 128), id | kMnA, t > 0);
-                tc::commit(bar + 5);
-            }
-        }
-        // dR.V meanwhile, with both parts of dR (dbeta is small where it cancels
-        // against k.Y): a thread per row and quarter of the features
-        {
-            const int r = p & 63, q0 = (p >> 6) * (DV / 32);
-            float v = 0.0f;
-            #pragma unroll
-            for (int q = q0; q < q0 + DV / 32; ++q) {
-                const int pos = r * 128 + (((q & 7) ^ (r & 7)) * 16);
-                const uint4 y = *reinterpret_cast<const uint4*>(sm + C::oA + (q >> 3) * 2 * kTile + kTile + pos);
-                const uint4 z = *reinterpret_cast<const uint4*>(sm + C::oV + (q >> 3) * kTile + pos);
-                const uint4 l = *reinterpret_cast<const uint4*>(sm + C::oR + (q >> 3) * kTile + pos);
-                const uint32_t ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w}, ls[4] = {l.x, l.y, l.z, l.w};
-                #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const cpx u = Op<DT>::unpack(ys[t]), x = Op<DT>::unpack(zs[t]), c = Op<DT>::unpack(ls[t]);
-                    v = fmaf(u.r + c.r, x.r, fmaf(u.i + c.i, x.i, v));
-                }
-            }
-            rv[p] = v;
-        }
-        ok = mbar_wait_bounded(bar + 4, par, kWaitLimitTile);
-        if (ok && p == 96 && items[~k & 1].m) load1(items[~k & 1]);  // S and dS' have been read
-        ok = ok && mbar_wait_bounded(bar + 5, par, kWaitLimitTile);
-        if (!(ok = !__syncthreads_or(!ok))) break;
-        tc::fence_after();
-        if (p == 96 && items[~k & 1].m) load0(items[~k & 1], ~k & 1);  // dO, dR and Vn have been read
-        // rows of dQ (upper) and of Y and dK (lower), a half of the features per thread
-        {
-            const float sg = lower ? -exp2_fast(gt[128 + i]) : gt[64 + i];
-            const float ej = gt[i], be = gt[192 + i];
-            float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f;
-            const int64_t tok = int64_t(it.row) * d.T + it.t0 + i;
-            float* part = a.dqh ? (lower ? a.dkh : a.dqh) + (tok * d.Hv + it.h) * DK : nullptr;
-            #pragma unroll 1
-            for (int f0 = half * (DK / 2); f0 < (half + 1) * (DK / 2); f0 += 16) {
-                uint32_t x[16], y[16], z[16], u[16];
-                ld16(lanes + C::cD1 + f0, x);
-                ld16(lanes + C::cD2 + f0, y);
-                if (lower) {
-                    ld16(lanes + C::cE1 + f0, z);
-                    ld16(lanes + C::cE2 + f0, u);
-                }
+            // X and H: the scores times the decays; warps 0-3 columns 0-31, 4-7 the others
+            {
+                uint32_t x[32];
+                const int j0 = half * 32;
+                tc::ld32x32b_x32(lanes + C::cSc + j0, x);
                 tc::wait_ld();
-                // this row of Q (upper) or K (lower)
-                const uint8_t* src = sm + C::oB + (f0 >> 6) * 2 * kTile + row * 128;
-                float o[16];
+                const float bi = gt[128 + i], f = lower ? -1.0f : d.scale, be = lower ? gt[192 + i] : 1.0f;
+                const int last = (lower ? i - 1 : i) - j0;
+                uint8_t *px = sm + C::oX + row * 128, *pg = sm + C::oG + row * 128;
                 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint4 t = *reinterpret_cast<const uint4*>(src + ((((f0 & 63) / 8 + q) ^ (i & 7)) * 16));
-                    const uint32_t ts[4] = {t.x, t.y, t.z, t.w};
+                for (int j = 0; j < 32; j += 8) {
+                    uint32_t u[4], g[4];
                     #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const cpx c2 = Op<DT>::unpack(ts[r / 2]);
-                        const float c = r & 1 ? c2.i : c2.r;
-                        const int e = 8 * q + r;
-                        const float v = fmaf(sg, __uint_as_float(x[e]), __uint_as_float(y[e]));
-                        s0 = fmaf(c, v, s0);
-                        if (lower) {
-                            const float em = ej * __uint_as_float(z[e]), dm = __uint_as_float(u[e]) + em;
-                            s1 = fmaf(c, dm, s1);
-                            s2 = fmaf(c, em, s2);
-                            o[e] = fmaf(be, v, dm);
-                        } else {
-                            o[e] = v;
+                    for (int q = 0; q < 8; q += 4) {
+                        const float4 b = *reinterpret_cast<const float4*>(gt + 128 + j0 + j + q);
+                        const float bj[4] = {b.x, b.y, b.z, b.w};
+                        float v[4];
+                        #pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float y = f * exp2_fast(bi - bj[r]) * __uint_as_float(x[j + q + r]);
+                            v[r] = j + q + r <= last ? y : 0.0f;  // above the diagonal, whatever it holds
+                        }
+                        u[q / 2] = Op<DT>::pack(v[0], v[1]);
+                        u[q / 2 + 1] = Op<DT>::pack(v[2], v[3]);
+                        g[q / 2] = Op<DT>::pack(be * v[0], be * v[1]);
+                        g[q / 2 + 1] = Op<DT>::pack(be * v[2], be * v[3]);
+                    }
+                    const int pos = (((j0 + j) / 8) ^ (row & 7)) * 16;
+                    *reinterpret_cast<uint4*>(px + pos) = make_uint4(u[0], u[1], u[2], u[3]);
+                    *reinterpret_cast<uint4*>(pg + pos) = make_uint4(g[0], g[1], g[2], g[3]);
+                }
+            }
+            if (!(ok = wait(bar + gLoad + 2, par, fail))) break;
+            if (tail) {
+                fix(C::oB, 2 * (DK / 64), kTile, it.m);
+            }
+            tc::fence_proxy_async();
+            tc::fence_before();
+            done(gX);
+            // dR.V meanwhile, with both parts of dR (dbeta is small where it cancels
+            // against k.Y): a thread per row and quarter of the features
+            {
+                const int r = p & 63, q0 = (p >> 6) * (DV / 32);
+                float v = 0.0f;
+                #pragma unroll
+                for (int q = q0; q < q0 + DV / 32; ++q) {
+                    const int pos = r * 128 + (((q & 7) ^ (r & 7)) * 16);
+                    const uint4 y = *reinterpret_cast<const uint4*>(sm + C::oA + (q >> 3) * 2 * kTile + kTile + pos);
+                    const uint4 z = *reinterpret_cast<const uint4*>(sm + C::oV + (q >> 3) * kTile + pos);
+                    const uint4 l = *reinterpret_cast<const uint4*>(sm + C::oR + (q >> 3) * kTile + pos);
+                    const uint32_t ys[4] = {y.x, y.y, y.z, y.w}, zs[4] = {z.x, z.y, z.z, z.w}, ls[4] = {l.x, l.y, l.z, l.w};
+                    #pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const cpx u = Op<DT>::unpack(ys[t]), x = Op<DT>::unpack(zs[t]), c = Op<DT>::unpack(ls[t]);
+                        v = fmaf(u.r + c.r, x.r, fmaf(u.i + c.i, x.i, v));
+                    }
+                }
+                rv[p] = v;
+            }
+            done(gRv);
+            if (!(ok = wait(bar + gD1, par, fail) && wait(bar + gD2, par, fail))) break;
+            tc::fence_after();
+            // rows of dQ (upper) and of Y and dK (lower), a half of the features per thread
+            {
+                const float sg = lower ? -exp2_fast(gt[128 + i]) : gt[64 + i];
+                const float ej = gt[i], be = gt[192 + i];
+                float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f;
+                const int64_t tok = int64_t(it.row) * d.T + it.t0 + i;
+                float* part = a.dqh ? (lower ? a.dkh : a.dqh) + (tok * d.Hv + it.h) * DK : nullptr;
+                #pragma unroll 1
+                for (int f0 = half * (DK / 2); f0 < (half + 1) * (DK / 2); f0 += 16) {
+                    uint32_t x[16], y[16], z[16], u[16];
+                    ld16(lanes + C::cD1 + f0, x);
+                    ld16(lanes + C::cD2 + f0, y);
+                    if (lower) {
+                        ld16(lanes + C::cE1 + f0, z);
+                        ld16(lanes + C::cE2 + f0, u);
+                    }
+                    tc::wait_ld();
+                    // this row of Q (upper) or K (lower)
+                    const uint8_t* src = sm + C::oB + (f0 >> 6) * 2 * kTile + row * 128;
+                    float o[16];
+                    #pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint4 t = *reinterpret_cast<const uint4*>(src + ((((f0 & 63) / 8 + q) ^ (i & 7)) * 16));
+                        const uint32_t ts[4] = {t.x, t.y, t.z, t.w};
+                        #pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const cpx c2 = Op<DT>::unpack(ts[r / 2]);
+                            const float c = r & 1 ? c2.i : c2.r;
+                            const int e = 8 * q + r;
+                            const float v = fmaf(sg, __uint_as_float(x[e]), __uint_as_float(y[e]));
+                            s0 = fmaf(c, v, s0);
+                            if (lower) {
+                                const float em = ej * __uint_as_float(z[e]), dm = __uint_as_float(u[e]) + em;
+                                s1 = fmaf(c, dm, s1);
+                                s2 = fmaf(c, em, s2);
+                                o[e] = fmaf(be, v, dm);
+                            } else {
+                                o[e] = v;
+                            }
                         }
                     }
-                }
-                if (part) {
-                    if (i < it.m) {
+                    if (part) {
+                        if (i < it.m) {
+                            #pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<float4*>(part + f0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        }
+                    } else {
+                        uint8_t* dst = sm + (lower ? C::oG : C::oX) + (f0 >> 6) * kTile + i * 128;
                         #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<float4*>(part + f0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int q = 0; q < 2; ++q)
+                            *reinterpret_cast<uint4*>(dst + ((((f0 & 63) / 8 + q) ^ (i & 7)) * 16)) =
+                                make_uint4(Op<DT>::pack(o[8 * q], o[8 * q + 1]), Op<DT>::pack(o[8 * q + 2], o[8 * q + 3]),
+                                           Op<DT>::pack(o[8 * q + 4], o[8 * q + 5]), Op<DT>::pack(o[8 * q + 6], o[8 * q + 7]));
                     }
+                }
+                float* r = red + half * 64 + i;
+                if (lower) {
+                    r[128] = s0;
+                    r[256] = s1;
+                    r[384] = s2;
                 } else {
-                    uint8_t* dst = sm + (lower ? C::oG : C::oX) + (f0 >> 6) * kTile + i * 128;
-                    #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        *reinterpret_cast<uint4*>(dst + ((((f0 & 63) / 8 + q) ^ (i & 7)) * 16)) =
-                            make_uint4(Op<DT>::pack(o[8 * q], o[8 * q + 1]), Op<DT>::pack(o[8 * q + 2], o[8 * q + 3]),
-                                       Op<DT>::pack(o[8 * q + 4], o[8 * q + 5]), Op<DT>::pack(o[8 * q + 6], o[8 * q + 7]));
+                    r[0] = s0;
                 }
             }
-            float* r = red + half * 64 + i;
-            if (lower) {
-                r[128] = s0;
-                r[256] = s1;
-                r[384] = s2;
-            } else {
-                r[0] = s0;
-            }
+            tc::fence_proxy_async();
+            tc::fence_before();
+            done(gRows);
         }
-        tc::fence_proxy_async();
-        tc::fence_before();
-        __syncthreads();
-        if (p == 96 && items[~k & 1].m) load2(items[~k & 1]);  // and Q, K, V
-        if (!a.dqh) {
-            if (!tail) {
-                if (p == 0) {  // tokens past the tensor's end are not written
-                    #pragma unroll
-                    for (int f = 0; f < DK / 64; ++f) {
-                        tma_store_4d(&a.mdq, sb + C::oX + f * kTile, f * 64, it.h, it.t0, it.row);
-                        tma_store_4d(&a.mdk, sb + C::oG + f * kTile, f * 64, it.h, it.t0, it.row);
+    } else if (w == 8) {
+        // ---------------------------------------------------------------- dq, dk, dbeta, dg -> global
+        int next = blockIdx.x;
+        for (;; ++k) {
+            const uint32_t par = k & 1;
+            const ChunkItem it = find_item(d, int(a.slots), &next);
+            if (!it.m) break;
+            const bool tail = d.offsets && it.m < kChunk;
+            // a decay below the least one is a constant
+            bool reset[2] = {};
+            #pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (2 * lane + u < it.m)
+                    reset[u] = load16<DT>(d.g, it.row * d.g.b + (it.t0 + int64_t(2 * lane + u)) * d.g.t + it.h * d.g.h) <
+                               kMinLogDecay;
+            if (!(ok = wait(bar + gRows, par, fail))) break;
+            if (!a.dqh) {
+                if (!tail) {
+                    if (elect()) {  // tokens past the tensor's end are not written
+                        #pragma unroll
+                        for (int f = 0; f < DK / 64; ++f) {
+                            tma_store_4d(&a.mdq, sb + C::oX + f * kTile, f * 64, it.h, it.t0, it.row);
+                            tma_store_4d(&a.mdk, sb + C::oG + f * kTile, f * 64, it.h, it.t0, it.row);
+                        }
+                    }
+                    __syncwarp();
+                } else {
+                    constexpr int NP = DK / 8;
+                    for (int x = lane; x < it.m * NP; x += 32) {
+                        const int t = x / NP, y = x % NP, pos = (y >> 3) * kTile + t * 128 + (((y & 7) ^ (t & 7)) * 16);
+                        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.dq.p) + it.row * a.dq.b + (it.t0 + int64_t(t)) * a.dq.t +
+                                                  it.h * a.dq.h + y * 8) = *reinterpret_cast<const uint4*>(sm + C::oX + pos);
+                        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.dk.p) + it.row * a.dk.b + (it.t0 + int64_t(t)) * a.dk.t +
+                                                  it.h * a.dk.h + y * 8) = *reinterpret_cast<const uint4*>(sm + C::oG + pos);
                     }
                 }
-            } else {
-                constexpr int NP = DK / 8;
-                for (int x = p; x < it.m * NP; x += 256) {
-                    const int t = x / NP, y = x % NP, pos = (y >> 3) * kTile + t * 128 + (((y & 7) ^ (t & 7)) * 16);
-                    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.dq.p) + it.row * a.dq.b + (it.t0 + int64_t(t)) * a.dq.t +
-                                              it.h * a.dq.h + y * 8) = *reinterpret_cast<const uint4*>(sm + C::oX + pos);
-                    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.dk.p) + it.row * a.dk.b + (it.t0 + int64_t(t)) * a.dk.t +
-                                              it.h * a.dk.h + y * 8) = *reinterpret_cast<const uint4*>(sm + C::oG + pos);
-                }
             }
-        }
-        if (w == 2) {
             // dbeta, and db summed from the end: tokens 2 lane and 2 lane + 1
+            const float* gt = reinterpret_cast<const float*>(sm + C::oE + par * 1024);
+            const float *red = reinterpret_cast<const float*>(sm + C::oL + par * C::LB), *rv = red + 512, *sd = rv + 256;
             float db[2], last = 0.0f;
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -814,25 +776,134 @@ __global__ void __launch_bounds__(256, GradCfg<DK, DV>::PER_SM) delta_grad_kerne
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int j = 2 * lane + u;
-                if (j < it.m) {
-                    const int64_t t = it.t0 + int64_t(j);
-                    // a decay below the least one is a constant
-                    const bool reset = load16<DT>(d.g, it.row * d.g.b + t * d.g.t + it.h * d.g.h) < kMinLogDecay;
-                    store16<DT>(a.dg, it.row * a.dg.b + t * a.dg.t + it.h * a.dg.h, reset ? 0.0f : dg[u]);
-                }
+                if (j < it.m)
+                    store16<DT>(a.dg, it.row * a.dg.b + (it.t0 + int64_t(j)) * a.dg.t + it.h * a.dg.h, reset[u] ? 0.0f : dg[u]);
             }
+            if (elect()) bulk_wait_read();
+            done(gStFree);
         }
-        __syncthreads();
+    } else {
+        // ---------------------------------------------------------------- loads and products
+        int next = blockIdx.x;
+        uint32_t loads = 0;  // items whose loads are under way or done
+        auto load0 = [&](const ChunkItem& it, uint32_t stage) {  // dO, dR, Vn and the decays
+            if (elect()) {
+                mbar_expect_tx(bar, C::B0);
+                #pragma unroll
+                for (int f = 0; f < DV / 64; ++f) {
+                    tma_load_4d(sb + C::oA + f * 2 * kTile, &a.mo, f * 64, it.h, it.t0, it.row, bar);
+                    bulk_g2s(sm + C::oA + f * 2 * kTile + kTile, a.dr + it.at * (2 * DV * 128) + f * kTile, kTile, bar);
+                }
+                bulk_g2s(sm + C::oR, a.dr + it.at * (2 * DV * 128) + DV * 128, DV * 128, bar);
+                bulk_g2s(sm + C::oN, a.saved_v + it.at * (DV * 128), DV * 128, bar);
+                bulk_g2s(sm + C::oE + stage * 1024, a.images + it.at * kImage<DK> + kImgE, 1024, bar);
+            }
+            __syncwarp();
+        };
+        auto load1 = [&](const ChunkItem& it) {  // S and dS'
+            if (elect()) {
+                mbar_expect_tx(bar + 1, C::B1);
+                bulk_g2s(sm + C::oS, a.saved_s + it.at * (DV * DK * 2), DV * DK * 2, bar + 1);
+                bulk_g2s(sm + C::oD, a.ds + it.at * (DV * DK * 2), DV * DK * 2, bar + 1);
+            }
+            __syncwarp();
+        };
+        auto load2 = [&](const ChunkItem& it) {  // Q, K and V
+            if (elect()) {
+                mbar_expect_tx(bar + 2, C::B2);
+                #pragma unroll
+                for (int f = 0; f < DK / 64; ++f) {
+                    tma_load_4d(sb + C::oB + f * 2 * kTile, &a.mq, f * 64, it.h / d.group, it.t0, it.row, bar + 2);
+                    tma_load_4d(sb + C::oB + f * 2 * kTile + kTile, &a.mk, f * 64, it.h / d.group, it.t0, it.row, bar + 2);
+                }
+                #pragma unroll
+                for (int f = 0; f < DV / 64; ++f) tma_load_4d(sb + C::oV + f * kTile, &a.mv, f * 64, it.h, it.t0, it.row, bar + 2);
+            }
+            __syncwarp();
+        };
+        auto find = [&](uint32_t to) {  // the next item, also for the rows' warps
+            const ChunkItem x = find_item(d, int(a.slots), &next);
+            if (lane == 0) items[to & 1] = x;
+            done(gItem);
+            return x;
+        };
+        ChunkItem it = find(0);
+        if (it.m) {
+            load0(it, 0);
+            load1(it);
+            load2(it);
+            loads = 1;
+        }
+        for (; it.m; ++k) {
+            const uint32_t par = k & 1;
+            // scores [dO; dR] Vn^T; the last rows are out of tensor memory
+            ok = wait(bar + gIn, par, fail);
+            if (ok && k > 0) ok = wait(bar + gRows, par ^ 1, fail);
+            if (!ok) break;
+            const ChunkItem nx = find(k + 1);
+            tc::fence_after();
+            const uint64_t da = sdesc(sb + C::oA, 16);
+            if (elect()) {
+                const uint64_t dn = sdesc(sb + C::oN, 16);
+                #pragma unroll
+                for (int f = 0; f < DV; f += 16)
+                    tc::mma_ss(tm + C::cSc, adv(da, (f / 64) * 2 * kTile + (f % 64) * 2), adv(dn, f * 128),
+                               tc::idesc(DT, 128, 64) | kMnB, f > 0);
+                tc::commit(bar + gScores);
+            }
+            // D1 = [dO; dR] S^T and E1 = Vn dS'^T
+            if (!(ok = wait(bar + gLoad + 1, par, fail))) break;
+            tc::fence_after();
+            constexpr uint32_t id = tc::idesc(DT, 128, DK) | kMnB;
+            if (elect()) {
+                const uint64_t ds = sdesc(sb + C::oS, DV * 128);
+                const uint64_t dn = sdesc(sb + C::oV, DV * 128), dd = sdesc(sb + C::oD, DV * 128);
+                #pragma unroll
+                for (int f = 0; f < DV; f += 16)
+                    tc::mma_ss(tm + C::cD1, adv(da, (f / 64) * 2 * kTile + (f % 64) * 2), adv(ds, f * 128), id, f > 0);
+                #pragma unroll
+                for (int f = 0; f < DV; f += 16)
+                    tc::mma_ss(tm + C::cE1, adv(dn, f * 128), adv(dd, f * 128), id | kMnA, f > 0);
+                tc::commit(bar + gD1);
+            }
+            // D2 = [X; H] K and E2 = [X; beta H]^T [Q; K]
+            if (!(ok = wait(bar + gX, par, fail))) break;
+            tc::fence_after();
+            if (elect()) {
+                const uint64_t dx = sdesc(sb + C::oX, 16), dk = sdesc(sb + C::oB + kTile, 2 * kTile);
+                const uint64_t dg = sdesc(sb + C::oX, 2 * kTile), dq = sdesc(sb + C::oB, 2 * kTile);
+                #pragma unroll
+                for (int t = 0; t < 64; t += 16)
+                    tc::mma_ss(tm + C::cD2, adv(dx, t * 2), adv(dk, t * 128), id, t > 0);
+                #pragma unroll
+                for (int t = 0; t < 128; t += 16)
+                    tc::mma_ss(tm + C::cE2, adv(dg, t * 128), adv(dq, t * 128), id | kMnA, t > 0);
+                tc::commit(bar + gD2);
+            }
+            if (nx.m) {
+                // S and dS' (all have formed <S, dS'> before gX); dO, dR and Vn; Q, K, V
+                if (!(ok = wait(bar + gD1, par, fail))) break;
+                loads = k + 2;
+                load1(nx);
+                if (!(ok = wait(bar + gRv, par, fail))) break;
+                load0(nx, par ^ 1);
+                if (!(ok = wait(bar + gRows, par, fail))) break;
+                load2(nx);
+            }
+            it = nx;
+        }
+        // everything issued is done and landed before the CTA leaves (bounded waits;
+        // a phase that is already over returns at once)
+        if (!ok && loads)
+            for (int x = 0; x < 3; ++x) mbar_wait_bounded(bar + gLoad + x, (loads - 1) & 1, kWaitFinal);
+        if (!ok && k > 0) mbar_wait_bounded(bar + gD2, k & 1, kWaitFinal);
     }
-    if (p == 0) bulk_wait_read();
-    if (p == 0 && !ok) {
-        atomicExch(d.err, 7);
-        for (int x = 0; x < 3; ++x) mbar_wait_bounded(bar + x, k & 1, kWaitFinal);  // the copies have landed
-    }
+    if (!ok) s_fail = 1;
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (w == 1) tc::dealloc(tm, C::COLS);
+    if (w == 9) tc::dealloc(tm, C::COLS);
+    if (p == 0 && s_fail) atomicExch(d.err, 7);
 }
 
 // dq, dk [token][Hk][DK] = the sum over a key head's value heads, 8 features a thread.
@@ -870,7 +941,7 @@ cudaError_t launch(const GradArgs& a, cudaStream_t st) {
     delta_dstate_kernel<DT, DK, DV><<<dim3(unsigned(a.d.nseq), unsigned(a.d.Hv)), BwdCfg<DK, DV>::THREADS, sb, st>>>(a);
     const int64_t items = a.slots * a.d.Hv;
     const int64_t most = int64_t(a.sms) * GradCfg<DK, DV>::PER_SM;
-    delta_grad_kernel<DT, DK, DV><<<unsigned(items < most ? items : most), 256, sg, st>>>(a);
+    delta_grad_kernel<DT, DK, DV><<<unsigned(items < most ? items : most), GradCfg<DK, DV>::THREADS, sg, st>>>(a);
     if (a.dqh) {
         const int64_t n = (a.d.B * a.d.T * a.d.Hk * (DK / 8) * 2 + 255) / 256;
         head_sum_kernel<DT><<<unsigned(n < 152 * 32 ? n : 152 * 32), 256, 0, st>>>(a.dqh, a.dkh, a.dq, a.dk, a.d.B * a.d.T,
