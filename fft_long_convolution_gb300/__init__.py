@@ -524,8 +524,7 @@ class DeltaRule:
         shape = (a.nseq, a.Hv, self.Dk, self.Dv)
         sin = _dense(state, "state", torch.float32, shape)
         with _on(stream):
-            # tokens outside every sequence are zero
-            o = (torch.empty if offsets is None else torch.zeros)(v.shape, dtype=v.dtype, device=v.device)
+            o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
             out = torch.empty(shape, dtype=torch.float32, device=v.device)
             saved = None
             if save:

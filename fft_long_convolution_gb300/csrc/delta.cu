@@ -128,12 +128,28 @@ __global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
     for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(a.sout + sbase + r * DV) = S[r];
 }
 
-template <int DT>
-__global__ void zero_kernel(View y, int64_t B, int64_t T, int64_t H, int D) {
-    const int64_t n = B * T * H * D;
-    for (int64_t e = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += int64_t(gridDim.x) * blockDim.x) {
-        const int64_t r = e % D, h = (e / D) % H, tok = e / D / H, b = tok / T, t = tok - b * T;
-        store16<DT>(y, b * y.b + t * y.t + h * y.h + r, 0.0f);
+// Zero the tokens of a packed row that belong to no sequence: those before the
+// first offset and from the last one on (offsets do not decrease).
+struct GapArgs {
+    View v[5];
+    int H[5], D[5];
+    int n;
+    const int32_t* offsets;
+    int nseq;
+    int64_t T;
+};
+
+__global__ void __launch_bounds__(256) gap_kernel(const GapArgs a) {
+    int64_t lo = a.nseq ? a.offsets[0] : a.T, hi = a.nseq ? a.offsets[a.nseq] : a.T;
+    lo = lo < 0 ? 0 : (lo > a.T ? a.T : lo);
+    hi = hi < lo ? lo : (hi > a.T ? a.T : hi);
+    const int64_t tokens = lo + a.T - hi;
+    for (int i = 0; i < a.n; ++i) {
+        const int64_t per = int64_t(a.H[i]) * a.D[i], n = tokens * per;
+        for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < n; e += int64_t(gridDim.x) * 256) {
+            const int64_t t = e / per, r = e - t * per;
+            reinterpret_cast<uint16_t*>(a.v[i].p)[(t < lo ? t : hi + t - lo) * a.v[i].t + r / a.D[i] * a.v[i].h + r % a.D[i]] = 0;
+        }
     }
 }
 
@@ -258,10 +274,18 @@ fftconv_status_t done(cudaError_t e) {
     return FFTCONV_ERR_CUDA;
 }
 
-template <int DT>
-cudaError_t zero_view(const View& y, int64_t B, int64_t T, int64_t H, int D, cudaStream_t st) {
-    const int64_t n = B * T * H * D;
-    zero_kernel<DT><<<unsigned(n / 256 + 1 < 4096 ? n / 256 + 1 : 4096), 256, 0, st>>>(y, B, T, H, D);
+cudaError_t zero_gaps(const DeltaArgs& d, int n, const View* v, const int* H, const int* D, cudaStream_t st) {
+    GapArgs a{};
+    for (int i = 0; i < n; ++i) {
+        a.v[i] = v[i];
+        a.H[i] = H[i];
+        a.D[i] = D[i];
+    }
+    a.n = n;
+    a.offsets = d.offsets;
+    a.nseq = d.nseq;
+    a.T = d.T;
+    gap_kernel<<<64, 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -347,7 +371,7 @@ extern "C" fftconv_status_t fftconv_delta_forward(fftconv_delta_t p, const fftco
     if (e != FFTCONV_OK) return e;
     const DeltaArgs& d = a.d;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (d.nseq == 0 || d.Hv == 0) return FFTCONV_OK;
+    if ((d.nseq == 0 && !d.offsets) || d.Hv == 0) return FFTCONV_OK;
     if (off16(state_in) || off16(state_out) || off16(saved) || off16(scratch)) return FFTCONV_ERR_ALIGN;
     const size_t sb = state_bytes(p, d.nseq, d.Hv);
     const size_t vb = fftconv_delta_saved_bytes(p, d.B, d.T, d.Hv, d.nseq);
@@ -391,7 +415,10 @@ extern "C" fftconv_status_t fftconv_delta_forward(fftconv_delta_t p, const fftco
         !encode_tokens_map(&a.mk, d.k, d.B, d.T, d.Hk, p->Dk, p->dtype) ||
         !encode_tokens_map(&a.mv, d.v, d.B, d.T, d.Hv, p->Dv, p->dtype))
         return FFTCONV_ERR_UNSUPPORTED;
-    return done(launch_delta_forward(a, p->dtype, p->Dk, p->Dv, st));
+    cudaError_t c = cudaSuccess;
+    if (d.offsets) c = zero_gaps(d, 1, &d.o, &d.Hv, &p->Dv, st);
+    if (c == cudaSuccess && d.nseq) c = launch_delta_forward(a, p->dtype, p->Dk, p->Dv, st);
+    return done(c);
 }
 
 extern "C" fftconv_status_t fftconv_delta_backward(fftconv_delta_t p, const fftconv_delta_args_t* args,
@@ -404,7 +431,7 @@ extern "C" fftconv_status_t fftconv_delta_backward(fftconv_delta_t p, const fftc
     if (e != FFTCONV_OK) return e;
     const DeltaArgs& d = a.d;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (d.nseq == 0 || d.Hv == 0) return FFTCONV_OK;
+    if ((d.nseq == 0 && !d.offsets) || d.Hv == 0) return FFTCONV_OK;
     if (off16(d_state_out) || off16(d_state_in) || off16(saved) || off16(scratch)) return FFTCONV_ERR_ALIGN;
     const size_t sb = state_bytes(p, d.nseq, d.Hv);
     const bool any = d.B && d.T;
@@ -459,16 +486,14 @@ extern "C" fftconv_status_t fftconv_delta_backward(fftconv_delta_t p, const fftc
         !encode_tokens_map(&a.mdv, a.dv, d.B, d.T, d.Hv, p->Dv, p->dtype))
         return FFTCONV_ERR_UNSUPPORTED;
     cudaError_t c = cudaSuccess;
-    if (d.offsets) {  // tokens outside every sequence have zero gradients
+    if (d.offsets) {
         const View zs[5] = {a.dq, a.dk, a.dv, a.dg, a.dbeta};
-        const int64_t zh[5] = {d.Hk, d.Hk, d.Hv, d.Hv, d.Hv};
-        const int zd[5] = {p->Dk, p->Dk, p->Dv, 1, 1};
-        for (int i = 0; i < 5 && c == cudaSuccess; ++i)
-            c = p->dtype == FFTCONV_F16 ? zero_view<0>(zs[i], d.B, d.T, zh[i], zd[i], st)
-                                        : zero_view<1>(zs[i], d.B, d.T, zh[i], zd[i], st);
-        if (c == cudaSuccess && a.dqh) c = cudaMemsetAsync(a.dqh, 0, w.total - w.q, st);
+        const int zh[5] = {d.Hk, d.Hk, d.Hv, d.Hv, d.Hv}, zd[5] = {p->Dk, p->Dk, p->Dv, 1, 1};
+        // with shared heads dq and dk are summed from float32 parts, zero in the gaps
+        if (a.dqh) c = cudaMemsetAsync(a.dqh, 0, w.total - w.q, st);
+        if (c == cudaSuccess) c = zero_gaps(d, 5, zs, zh, zd, st);
     }
-    if (c == cudaSuccess) c = launch_delta_backward(a, p->dtype, p->Dk, p->Dv, st);
+    if (c == cudaSuccess && d.nseq) c = launch_delta_backward(a, p->dtype, p->Dk, p->Dv, st);
     return done(c);
 }
 

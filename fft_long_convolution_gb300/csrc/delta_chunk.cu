@@ -846,12 +846,12 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             const bool tail = d.offsets && left < kChunk;
             if (c >= C::NKQ && !(ok = wait(bar + kKqFree + st, (c / C::NKQ - 1) & 1, fail))) break;
             uint64_t* full = tail ? bar + kRaw : bar + kKqFull + st;
-            if (elect()) {
-                mbar_expect_tx(full, C::KQ);
+            if (elect()) {  // the state alone needs neither Q nor P
+                mbar_expect_tx(full, STATE ? C::KQ / 2 : C::KQ);
                 #pragma unroll
                 for (int f = 0; f < DK / 64; ++f) {
                     tma_load_4d(smem_u32(kq) + f * 2 * kTile, &a.mk, f * 64, hk, t0, row0, full);
-                    tma_load_4d(smem_u32(kq) + f * 2 * kTile + kTile, &a.mq, f * 64, hk, t0, row0, full);
+                    if (!STATE) tma_load_4d(smem_u32(kq) + f * 2 * kTile + kTile, &a.mq, f * 64, hk, t0, row0, full);
                 }
             }
             __syncwarp();
@@ -864,25 +864,32 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             }
             if (c >= C::NI && !(ok = wait(bar + kOpRead + (c & 1), ((c - 2) >> 1) & 1, fail))) break;
             if (elect()) {
-                mbar_expect_tx(bar + kTFull + c % C::NI, kImgW);
-                bulk_g2s(image(c), a.images + ((slot0 + c) * d.Hv + h) * kImage<DK>, kImgW, bar + kTFull + c % C::NI);
+                // and the transition matrix no values: only the decays
+                const uint32_t from = STATE ? (trans ? kImgE : kImgT) : 0;
+                mbar_expect_tx(bar + kTFull + c % C::NI, kImgW - from);
+                bulk_g2s(image(c) + from, a.images + ((slot0 + c) * d.Hv + h) * kImage<DK> + from, kImgW - from,
+                         bar + kTFull + c % C::NI);
             }
             __syncwarp();
             if (c >= 1 && !(ok = wait(bar + kUDone, (c - 1) & 1, fail))) break;
-            full = tail ? bar + kRaw : bar + kVFull;
-            if (elect()) {
-                mbar_expect_tx(full, C::VB);
-                #pragma unroll
-                for (int f = 0; f < 2; ++f)
-                    tma_load_4d(sb + C::oV + f * kTile, &a.mv, DV == 128 ? f * 64 : 0, h, t0, row0, full);
-            }
-            __syncwarp();
-            if (tail) {
-                if (!(ok = wait(bar + kRaw, 1, fail))) break;
-                for (int f = 0; f < 2; ++f) fix(sm + C::oV + f * kTile, int(left));
-                tc::fence_proxy_async();
-                __syncwarp();
+            if (trans) {
                 if (lane == 0) arrive(bar + kVFull);
+            } else {
+                full = tail ? bar + kRaw : bar + kVFull;
+                if (elect()) {
+                    mbar_expect_tx(full, C::VB);
+                    #pragma unroll
+                    for (int f = 0; f < 2; ++f)
+                        tma_load_4d(sb + C::oV + f * kTile, &a.mv, DV == 128 ? f * 64 : 0, h, t0, row0, full);
+                }
+                __syncwarp();
+                if (tail) {
+                    if (!(ok = wait(bar + kRaw, 1, fail))) break;
+                    for (int f = 0; f < 2; ++f) fix(sm + C::oV + f * kTile, int(left));
+                    tc::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) arrive(bar + kVFull);
+                }
             }
             if (c >= 1 && !(ok = wait(bar + kSwDone, (c - 1) & 1, fail))) break;
             if (elect()) {
@@ -911,27 +918,48 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
 
 // The states at the segments' starts: S_(s+1) = M_s S_s + N_s along a
 // sequence, float32; N_0 already holds the initial state's part.  The result
-// replaces N_s.  A thread owns one column of S and a slice of its rows; 8
-// columns per CTA.
+// replaces N_s.  A CTA takes 8 columns of S; the next M arrives by a bulk copy
+// while the current one is applied (8 us a segment without, 2 us with it at
+// 128 x 128).
 template <int DK, int DV>
 __global__ void __launch_bounds__(256) delta_join_kernel(const __grid_constant__ ChunkArgs a) {
+    extern __shared__ __align__(128) float join_sm[];  // M, two stages
     __shared__ float x[2][DK][8];
+    __shared__ uint64_t bar[2];
     const DeltaArgs& d = a.d;
     const int i = blockIdx.x, h = blockIdx.y, col = threadIdx.x % 8, r0 = threadIdx.x / 8, v0 = blockIdx.z * 8;
     const Seq s = locate(d.offsets, d.T, i);
     const int64_t c_all = (s.len + kChunk - 1) / kChunk, nseg = (c_all + a.seg_chunks - 1) / a.seg_chunks;
     const int64_t g0 = (s.slot / a.seg_chunks + i) * d.Hv + h;
     if (nseg < 3) return;
+    auto load = [&](int64_t g) {
+        mbar_expect_tx(&bar[g & 1], DK * DK * 4);
+        bulk_g2s(join_sm + (g & 1) * DK * DK, a.seg_trans + (g0 + g * d.Hv) * DK * DK, DK * DK * 4, &bar[g & 1]);
+    };
+    if (threadIdx.x == 0) {
+        mbar_init(&bar[0], 1);
+        mbar_init(&bar[1], 1);
+        fence_mbar_init();
+        load(1);
+    }
     const float* N = a.seg_state + g0 * DK * DV + v0 + col;
     for (int r = r0; r < DK; r += 32) x[0][r][col] = N[r * DV];
     __syncthreads();
+    bool ok = true;
     for (int64_t g = 1; g + 1 < nseg; ++g) {
-        const float* M = a.seg_trans + (g0 + g * d.Hv) * DK * DK;
-        float* out = a.seg_state + (g0 + g * d.Hv) * DK * DV + v0 + col;
         const int b = int(g & 1);
+        if (threadIdx.x == 0 && g + 2 < nseg) load(g + 1);
+        float* out = a.seg_state + (g0 + g * d.Hv) * DK * DV + v0 + col;
         float acc[DK / 32];
         #pragma unroll
         for (int q = 0; q < DK / 32; ++q) acc[q] = out[(r0 + 32 * q) * DV];
+        ok = mbar_wait_bounded(&bar[b], uint32_t((g - 1) >> 1) & 1, kWaitLimitTile);
+        if (__syncthreads_or(!ok)) {
+            ok = false;
+            break;
+        }
+        const float* M = join_sm + b * DK * DK;
+        #pragma unroll 4
         for (int k = 0; k < DK; k += 4) {
             #pragma unroll
             for (int q = 0; q < DK / 32; ++q) {
@@ -949,23 +977,31 @@ __global__ void __launch_bounds__(256) delta_join_kernel(const __grid_constant__
         }
         __syncthreads();
     }
+    if (!ok && threadIdx.x == 0) {
+        atomicExch(d.err, 7);
+        for (int b = 0; b < 2; ++b) {  // copies have landed before the CTA leaves
+            mbar_wait_bounded(&bar[b], 0, kWaitFinal);
+            mbar_wait_bounded(&bar[b], 1, kWaitFinal);
+        }
+    }
 }
 
 template <int DT, int DK, int DV>
 cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
-    static PerDevice c0, c1, c2;
+    static PerDevice c0, c1, c2, c3;
     constexpr size_t sp = PrepCfg<DK>::BYTES, sf = FwdCfg<DK, DV>::BYTES;
     static_assert(sf <= 232448 && (sp + 1024) * PrepCfg<DK>::PER_SM <= 233472, "shared memory");
     cudaError_t e = opt_in(delta_prep_kernel<DT, DK>, sp, c0);
     if (e == cudaSuccess) e = opt_in(delta_fwd_kernel<DT, DK, DV, false>, sf, c1);
     if (e == cudaSuccess) e = opt_in(delta_fwd_kernel<DT, DK, DV, true>, sf, c2);
+    if (e == cudaSuccess) e = opt_in(delta_join_kernel<DK, DV>, 2 * DK * DK * 4, c3);
     if (e != cudaSuccess) return e;
     const unsigned H = unsigned(a.d.Hv);
     const int64_t items = a.slots * a.d.Hv, most = int64_t(a.sms) * PrepCfg<DK>::PER_SM;
     delta_prep_kernel<DT, DK><<<unsigned(items < most ? items : most), 256, sp, st>>>(a);
     if (a.segments > a.d.nseq) {
         delta_fwd_kernel<DT, DK, DV, true><<<dim3(unsigned(a.segments), H, 2), FwdCfg<DK, DV>::THREADS, sf, st>>>(a);
-        delta_join_kernel<DK, DV><<<dim3(unsigned(a.d.nseq), H, DV / 8), 256, 0, st>>>(a);
+        delta_join_kernel<DK, DV><<<dim3(unsigned(a.d.nseq), H, DV / 8), 256, 2 * DK * DK * 4, st>>>(a);
     }
     delta_fwd_kernel<DT, DK, DV, false><<<dim3(unsigned(a.segments), H), FwdCfg<DK, DV>::THREADS, sf, st>>>(a);
     return cudaGetLastError();

@@ -464,7 +464,7 @@ typedef struct {
  * B = 1 and sequence i is tokens offsets[i] .. offsets[i+1] - 1 of the row
  * (offsets: nseq + 1 non-decreasing int32 on the device, within [0, T];
  * values outside are clamped; empty sequences are valid).  Tokens outside
- * every sequence have no output and zero gradients.
+ * every sequence have zero outputs and gradients.
  */
 typedef struct fftconv_delta_s *fftconv_delta_t;
 

@@ -358,6 +358,43 @@ def test_offsets_outside_the_row_are_clamped():
 
 
 @pytest.mark.gpu
+def test_no_sequences_and_tokens_before_the_first():
+    """A packed row without sequences is all zeros; so are tokens before the
+    first sequence."""
+    dt, Hk, Hv, Dk, Dv, T = torch.float16, 1, 2, 64, 64, 90
+    ins = cuda(*delta_inputs(1, T, Hk, Hv, Dk, Dv, dt, seed=42))
+    plan = F.DeltaRule(Dk, Dv, dt)
+    for off in ([0], [20, 50]):
+        off = torch.tensor(off, dtype=torch.int32).cuda()
+        torch.full((1, T, Hv, Dv), 3.0, dtype=dt, device="cuda")  # what the allocator hands out next is not zero
+        o, s, saved = plan.forward(*ins, offsets=off, save=True)
+        got = plan.backward(ins[2], *ins, saved, offsets=off)
+        live = torch.zeros(T, dtype=torch.bool)
+        if off.numel() > 1:
+            live[20:50] = True
+            ref, sref = delta_rule(*[x.cpu()[:, 20:50] for x in ins], scale=Dk ** -0.5)
+            assert rel(o[:, 20:50], ref) < tol_o(dt) and rel(s, sref) < TOL_STATE
+        for x in [o] + list(got[:5]):
+            assert not bool(x.cpu()[:, ~live].any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("B,T,Hk,Hv,Dk,Dv", [(1, 12000, 1, 1, 64, 64), (1, 8200, 1, 2, 128, 64), (2, 6500, 1, 1, 64, 128)])
+def test_long_rows_in_segments(B, T, Hk, Hv, Dk, Dv, dt):
+    """Rows long and few enough to be cut into segments, with and without an
+    initial state; compared at the end and on a sample of the outputs, so that
+    the 64-bit side stays small."""
+    ins = delta_inputs(B, T, Hk, Hv, Dk, Dv, dt, seed=51)
+    s0 = states(B, Hv, Dk, Dv)
+    plan = F.DeltaRule(Dk, Dv, dt)
+    ref, sref = delta_rule(*ins, state=s0, scale=Dk ** -0.5)
+    o, s = plan.forward(*cuda(*ins), state=s0.cuda())
+    assert rel(o, ref) < tol_o(dt) and rel(s, sref) < TOL_STATE
+    assert plan.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_refusals():
     dt = torch.bfloat16
     B, T, Hk, Hv, Dk, Dv = 2, 70, 1, 2, 64, 64

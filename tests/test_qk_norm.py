@@ -96,6 +96,24 @@ def test_zero_rows_missing_weights_and_default_positions(dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("norm,inter", [("rms", False), ("l2", True)])
+def test_weights_and_tables_off_16_bytes(norm, inter):
+    """float32 weights and tables need their own alignment only."""
+    dt, B, T, H, D, R = torch.bfloat16, 2, 9, 3, 64, 32
+    q, k, wq, wk, dq, dk, pos = [x.cuda() for x in inputs(B, T, H, H, D, dt, seed=5)]
+    cos, sin = (x.cuda() for x in tables(40, R))
+    plan = F.QKNorm(D, dt, norm=norm, rotary=R, interleaved=inter)
+
+    def shifted(x):
+        return torch.cat([x.new_zeros(1), x.flatten()])[1:].view(x.shape)
+
+    sets = [dict(wq=wq, wk=wk, cos=cos, sin=sin, positions=pos)]
+    sets.append({n: x if n == "positions" else shifted(x) for n, x in sets[0].items()})
+    res = [list(plan.forward(q, k, **kw)) + list(plan.backward(dq, dk, q, k, **kw)) for kw in sets]
+    assert all(torch.equal(x, y) for x, y in zip(*res))
+
+
+@pytest.mark.gpu
 def test_positions_outside_the_tables_give_nan():
     dt, B, T, H, D, R = torch.bfloat16, 1, 4, 2, 64, 32
     q, k, *_ = inputs(B, T, H, H, D, dt, seed=3)
