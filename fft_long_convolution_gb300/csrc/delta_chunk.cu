@@ -29,8 +29,11 @@
 //   warps 0-15   chain: S (float32 -> operands, decayed in place), Vn and O^T, a
 //                quarter of the columns for each four warps
 //   warps 16-19  O -> global memory
-//   warp 20      issues every contraction;  warp 21  loads;  warp 22  stores what
-//                the backward needs
+//   warp 20      issues S W and the update of S, the two products that the walk
+//                waits for;  warp 23  the others;  warp 21  loads;  warp 22
+//                stores what the backward needs
+// A step is a chain of waits (S's operands, S W, Vn, the update), and a wait costs
+// some 200 cycles even when it is over, so what S W needs arrives on one barrier.
 #include "delta_chunk.h"
 
 #include "chunk.cuh"
@@ -488,20 +491,21 @@ struct FwdCfg {
     static constexpr uint32_t oKQ = 0, oV = oKQ + NKQ * KQ, oI = oV + VB, oW = oI + NI * kImgW,
                               oO = oW + DK * 256, oSv = oO + 64 * DV_ * 2,
                               oBar = oSv + (DK / 64 + 1) * DV_ * 128, BYTES = oBar + 256;
-    static constexpr int THREADS = 736;
+    static constexpr int THREADS = 768;
     // tensor memory columns.  The two U^T / Vn^T / P Vn accumulators take turns.
-    // Vn's operands take the place of S's parts: Vn that of the low part (dead
-    // after S W), e Vn that of the high part (dead after S Q).
-    static constexpr uint32_t cS = 0, cHi = 128, cLo = 192, cVeH = 128, cVeL = 160, cVnH = 192, cVn = 256, cOS = 384;
+    // Vn's operand for O takes the place of S's low part (dead after S W).
+    static constexpr uint32_t cS = 0, cHi = 128, cLo = 192, cVnH = 192, cVn = 256, cOS = 384, cVeH = 448, cVeL = 480;
     static __device__ __forceinline__ uint32_t vn(int c) { return cVn + (c & 1) * 64; }
 };
 
 enum Bar {
-    kKqFull = 0, kKqFree = kKqFull + 2, kTFull = kKqFree + 2, kVFull = kTFull + 2, kWFull, kRaw, kUDone, kSwDone, kSqDone, kVnReady, kSDone, kOReady, kOFree,
+    kGo = 0,              // [2]: S's operands, K and Q, W and U are there: S W can go
+    kKqFree = kGo + 2, kTFull = kKqFree + 2, kVFull = kTFull + 2, kRaw, kUDone, kSwDone, kVnReady, kSDone,
+    kOReady, kOFree,
     kSv,                 // [3]: S (two blocks) and Vn are in their staging buffers
     kSvFree = kSv + 3,   // [3]: and out of them
-    kSReady = kSvFree + 3, kFinal,
-    kOpDone, kOpRead = kOpDone + 2,  // [2] each, by chunk parity
+    kFinal = kSvFree + 3,  // [2]
+    kOpDone = kFinal + 2, kOpRead = kOpDone + 2,  // [2] each, by chunk parity
     kBars = kOpRead + 2
 };
 
@@ -548,8 +552,10 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         for (int i = 0; i < kBars; ++i) {
             uint32_t cnt = 1;  // else one arrival per warp of the role
             if (i == kOFree) cnt = 4;
-            if (i == kVnReady || i == kSReady || i == kOReady || i == kSv + 2 || i >= kOpRead) cnt = 16;
+            if (i == kVnReady || i == kOReady || i == kSv + 2 || i >= kOpRead) cnt = 16;
             if (i == kSv || i == kSv + 1) cnt = DK == 128 ? 8 : 16;
+            if (i < kGo + 2) cnt = 16 + 3;                   // the chain, K and Q, W, U
+            if (i == kKqFree || i == kKqFree + 1) cnt = 2;   // S Q and the update
             mbar_init(bar + i, cnt);
         }
         fence_mbar_init();
@@ -583,7 +589,6 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         // O^T of chunk c -> shared memory: done while the next chunk's S W runs
         auto put_o = [&](int c) {
             const float* gt = reinterpret_cast<const float*>(image(c) + kImgE);
-            if (!wait(bar + kOpDone + (c & 1), (c >> 1) & 1, fail)) return false;
             if (STATE) {
                 done(kOpRead + (c & 1));
                 return true;
@@ -643,11 +648,14 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
                 x[2 * j] = __float_as_uint(y.x);
                 x[2 * j + 1] = __float_as_uint(y.y);
             }
+            // the places of S's operands are free after S Q and (the last) P Vn
+            if (c > 0 && !(ok = wait(bar + kOpDone + ((c - 1) & 1), ((c - 1) >> 1) & 1, fail))) break;
+            tc::fence_after();
             st_cols<NC / 2>(lanes + C::cHi + k0 / 2, hi);
             st_cols<NC / 2>(lanes + C::cLo + k0 / 2, lo);
             tc::wait_st();
             tc::fence_before();
-            done(kSReady);
+            done(kGo + (c & 1));
             st_cols<NC>(lanes + C::cS + k0, x);  // complete before kVnReady
             if (!STATE && a.saved_s) {
                 // a staging buffer for each block of 64 features of S, and for Vn
@@ -680,7 +688,6 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
                 }
             }
             st_cols<8>(lanes + C::cVnH + j0 / 2, vh);
-            if (!(ok = wait(bar + kSqDone, c & 1, fail))) break;
             st_cols<8>(lanes + C::cVeH + j0 / 2, eh);
             st_cols<8>(lanes + C::cVeL + j0 / 2, el);
             tc::wait_st();
@@ -697,7 +704,7 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
                 done(kSv + 2);
             }
         }
-        if (ok) ok = put_o(n - 1);
+        if (ok) ok = wait(bar + kOpDone + ((n - 1) & 1), ((n - 1) >> 1) & 1, fail) && put_o(n - 1);
         if (ok) ok = wait(bar + kSDone, (n - 1) & 1, fail);
         if (ok && sout) {
             tc::fence_after();
@@ -731,67 +738,26 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         for (int c = 0; !STATE && ok && c < n; ++c) ok = copy_o(c);
         if (!ok) s_fail = 1;
     } else if (warp == 20) {
-        // ---------------------------------------------------------------- contractions
-        constexpr uint32_t id64 = tc::idesc(DT, 128, 64);
-        constexpr uint32_t idS = tc::idesc(DT, 128, DK) | kMnB;
+        // ---------------------------------------------------------------- S W and the update of S
+        constexpr uint32_t id64 = tc::idesc(DT, 128, 64) | kMnB, idS = tc::idesc(DT, 128, DK) | kMnB;
         bool ok = true;
-        auto u_issue = [&](int c) {  // U^T = V^T (T beta)^T
-            const uint64_t da = sdesc(sb + C::oV, kTile);
-            const uint64_t db = sdesc(sb + C::oI + (c % C::NI) * kImgW + kImgT, 16);
-            tc::fence_after();
-            if (elect()) {
-                if (!trans) {
-                    #pragma unroll
-                    for (int m = 0; m < 2; ++m)
-                        #pragma unroll
-                        for (int t = 0; t < 64; t += 16)
-                            tc::mma_ss(tm + C::vn(c), adv(da, t * 128), adv(db, m * kTile + t * 2), id64 | kMnA, m + t > 0);
-                }
-                tc::commit(bar + kUDone);
-            }
-        };
-        auto u_wait = [&](int c) {
-            return wait(bar + kTFull + c % C::NI, (c / C::NI) & 1, fail) && wait(bar + kVFull, c & 1, fail);
-        };
-        ok = u_wait(0);
-        if (ok) u_issue(0);
-        for (int c = 0; ok && c < n; ++c) {
-            if (!(ok = wait(bar + kWFull, c & 1, fail) && wait(bar + kSReady, c & 1, fail))) break;
+        for (int c = 0; c < n; ++c) {
+            if (!(ok = wait(bar + kGo + (c & 1), (c >> 1) & 1, fail))) break;
             tc::fence_after();
             if (elect()) {
                 const uint64_t dw = sdesc(sb + C::oW, 16);
                 #pragma unroll
                 for (int f = 0; f < DK; f += 16) {  // U^T - S^T W^T (W is stored negated)
-                    tc::mma(tm + C::vn(c), tm + C::cHi + f / 2, adv(dw, f * 128), id64 | kMnB, !(trans && f == 0));
-                    tc::mma(tm + C::vn(c), tm + C::cHi + f / 2, adv(dw, DK * 128 + f * 128), id64 | kMnB, 1);
-                    tc::mma(tm + C::vn(c), tm + C::cLo + f / 2, adv(dw, f * 128), id64 | kMnB, 1);
+                    tc::mma(tm + C::vn(c), tm + C::cHi + f / 2, adv(dw, f * 128), id64, !(trans && f == 0));
+                    tc::mma(tm + C::vn(c), tm + C::cHi + f / 2, adv(dw, DK * 128 + f * 128), id64, 1);
+                    tc::mma(tm + C::vn(c), tm + C::cLo + f / 2, adv(dw, f * 128), id64, 1);
                 }
                 tc::commit(bar + kSwDone);
-            }
-            // chunk c - 1's O is out of its accumulators
-            if (c > 0 && !(ok = wait(bar + kOpRead + ((c - 1) & 1), ((c - 1) >> 1) & 1, fail))) break;
-            if (!(ok = wait(bar + kKqFull + c % C::NKQ, (c / C::NKQ) & 1, fail))) break;
-            tc::fence_after();
-            if (elect()) {
-                const uint64_t dq = sdesc(sb + C::oKQ + (c % C::NKQ) * C::KQ + kTile, 16);
-                if (!STATE) {
-                    #pragma unroll
-                    for (int f = 0; f < DK; f += 16)  // S^T Q^T
-                        tc::mma(tm + C::cOS, tm + C::cHi + f / 2, adv(dq, (f / 64) * 2 * kTile + (f % 64) * 2), id64, f > 0);
-                }
-                tc::commit(bar + kSqDone);
             }
             if (!(ok = wait(bar + kVnReady, c & 1, fail))) break;
             tc::fence_after();
             if (elect()) {
-                const uint64_t dp = sdesc(sb + C::oI + (c % C::NI) * kImgW + kImgP, 16);
                 const uint64_t dk = sdesc(sb + C::oKQ + (c % C::NKQ) * C::KQ, 2 * kTile);
-                if (!STATE) {
-                    #pragma unroll
-                    for (int t = 0; t < 64; t += 16)  // Vn^T P^T
-                        tc::mma(tm + C::vn(c), tm + C::cVnH + t / 2, adv(dp, t * 2), id64, t > 0);
-                }
-                tc::commit(bar + kOpDone + (c & 1));
                 #pragma unroll
                 for (int m = 0; m < 2; ++m)
                     #pragma unroll
@@ -800,16 +766,67 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
                 tc::commit(bar + kSDone);
                 tc::commit(bar + kKqFree + c % C::NKQ);
             }
-            // while the chain turns S into operands: the next chunk's U^T
-            if (c + 1 < n) {
-                ok = u_wait(c + 1);
-                if (ok) u_issue(c + 1);
-            }
         }
         if (!ok) s_fail = 1;
         // everything issued is done before tensor memory is given back
         if (elect()) tc::commit(bar + kFinal);
         mbar_wait_bounded(bar + kFinal, 0, kWaitFinal);
+    } else if (warp == 23) {
+        // ---------------------------------------------------------------- U, S Q and P Vn
+        constexpr uint32_t id64 = tc::idesc(DT, 128, 64);
+        bool ok = true;
+        auto u_wait = [&](int c) {
+            return wait(bar + kTFull + c % C::NI, (c / C::NI) & 1, fail) && wait(bar + kVFull, c & 1, fail);
+        };
+        auto u_issue = [&](int c) {  // U^T = V^T (T beta)^T; by one thread
+            const uint64_t da = sdesc(sb + C::oV, kTile);
+            const uint64_t db = sdesc(sb + C::oI + (c % C::NI) * kImgW + kImgT, 16);
+            if (!trans) {
+                #pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    #pragma unroll
+                    for (int t = 0; t < 64; t += 16)
+                        tc::mma_ss(tm + C::vn(c), adv(da, t * 128), adv(db, m * kTile + t * 2), id64 | kMnA, m + t > 0);
+            }
+            tc::commit(bar + kUDone);
+            tc::commit(bar + kGo + (c & 1));
+        };
+        ok = u_wait(0);
+        tc::fence_after();
+        if (ok && elect()) u_issue(0);
+        for (int c = 0; ok && c < n; ++c) {
+            // S Q after S W, once chunk c - 1's O is out of its accumulators
+            ok = wait(bar + kSwDone, c & 1, fail);
+            if (ok && c > 0) ok = wait(bar + kOpRead + ((c - 1) & 1), ((c - 1) >> 1) & 1, fail);
+            if (!ok) break;
+            tc::fence_after();
+            if (elect()) {
+                const uint64_t dq = sdesc(sb + C::oKQ + (c % C::NKQ) * C::KQ + kTile, 16);
+                if (!STATE) {
+                    #pragma unroll
+                    for (int f = 0; f < DK; f += 16)  // S^T Q^T
+                        tc::mma(tm + C::cOS, tm + C::cHi + f / 2, adv(dq, (f / 64) * 2 * kTile + (f % 64) * 2), id64, f > 0);
+                }
+                tc::commit(bar + kKqFree + c % C::NKQ);
+            }
+            if (c + 1 < n && !(ok = u_wait(c + 1))) break;
+            // P Vn and the next U after the update of S, while the chain turns S into operands
+            if (!(ok = wait(bar + kSDone, c & 1, fail))) break;
+            tc::fence_after();
+            if (elect()) {
+                const uint64_t dp = sdesc(sb + C::oI + (c % C::NI) * kImgW + kImgP, 16);
+                if (!STATE) {
+                    #pragma unroll
+                    for (int t = 0; t < 64; t += 16)  // Vn^T P^T
+                        tc::mma(tm + C::vn(c), tm + C::cVnH + t / 2, adv(dp, t * 2), id64, t > 0);
+                }
+                tc::commit(bar + kOpDone + (c & 1));
+                if (c + 1 < n) u_issue(c + 1);
+            }
+        }
+        if (!ok) s_fail = 1;
+        if (elect()) tc::commit(bar + kFinal + 1);
+        mbar_wait_bounded(bar + kFinal + 1, 0, kWaitFinal);
     } else if (warp == 22) {
         // ---------------------------------------------------------------- S, Vn -> global
         bool ok = true;
@@ -845,7 +862,7 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             // end; in a packed row they are the next sequence's and are zeroed here
             const bool tail = d.offsets && left < kChunk;
             if (c >= C::NKQ && !(ok = wait(bar + kKqFree + st, (c / C::NKQ - 1) & 1, fail))) break;
-            uint64_t* full = tail ? bar + kRaw : bar + kKqFull + st;
+            uint64_t* full = tail ? bar + kRaw : bar + kGo + st;
             if (elect()) {  // the state alone needs neither Q nor P
                 mbar_expect_tx(full, STATE ? C::KQ / 2 : C::KQ);
                 #pragma unroll
@@ -860,7 +877,7 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
                 for (int f = 0; f < 2 * DK / 64; ++f) fix(kq + f * kTile, int(left));
                 tc::fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) arrive(bar + kKqFull + st);
+                if (lane == 0) arrive(bar + kGo + st);
             }
             if (c >= C::NI && !(ok = wait(bar + kOpRead + (c & 1), ((c - 2) >> 1) & 1, fail))) break;
             if (elect()) {
@@ -893,21 +910,19 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             }
             if (c >= 1 && !(ok = wait(bar + kSwDone, (c - 1) & 1, fail))) break;
             if (elect()) {
-                mbar_expect_tx(bar + kWFull, DK * 256);
-                bulk_g2s(sm + C::oW, a.images + ((slot0 + c) * d.Hv + h) * kImage<DK> + kImgW, DK * 256, bar + kWFull);
+                mbar_expect_tx(bar + kGo + (c & 1), DK * 256);
+                bulk_g2s(sm + C::oW, a.images + ((slot0 + c) * d.Hv + h) * kImage<DK> + kImgW, DK * 256, bar + kGo + (c & 1));
             }
             __syncwarp();
         }
         if (!ok) s_fail = 1;
         // every copy has landed before the CTA leaves (bounded waits; a phase that
         // is already over returns at once)
-        for (int x = c > C::NKQ ? c - C::NKQ : 0; x < c; ++x)
-            mbar_wait_bounded(bar + kKqFull + x % C::NKQ, (x / C::NKQ) & 1, kWaitFinal);
-        for (int x = c > C::NI ? c - C::NI : 0; x < c; ++x) mbar_wait_bounded(bar + kTFull + x % C::NI, (x / C::NI) & 1, kWaitFinal);
-        if (c > 0) {
-            mbar_wait_bounded(bar + kVFull, (c - 1) & 1, kWaitFinal);
-            mbar_wait_bounded(bar + kWFull, (c - 1) & 1, kWaitFinal);
+        for (int x = c > 2 ? c - 2 : 0; x < c; ++x) {
+            mbar_wait_bounded(bar + kGo + (x & 1), (x >> 1) & 1, kWaitFinal);
+            mbar_wait_bounded(bar + kTFull + x % C::NI, (x / C::NI) & 1, kWaitFinal);
         }
+        if (c > 0) mbar_wait_bounded(bar + kVFull, (c - 1) & 1, kWaitFinal);
     }
     tc::fence_before();
     __syncthreads();
