@@ -420,12 +420,10 @@ _NORM_ARGS = struct.Struct("=5if4q" + "Q3q" * 2 + "4QqQ")
 
 def _strides(t, what: str, dtype, shape):
     """A tensor's address and its first three strides, checked against dtype and shape."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA {dtype} tensor of shape {tuple(shape)}")
     st = t.stride()
-    if len(st) == 4 and st[3] != 1 and shape[3] > 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), st[0], st[1], st[2]
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or (len(st) == 4 and st[3] != 1 and shape[3] > 1):
+        raise ValueError(f"{what} must be a CUDA {dtype} tensor of shape {tuple(shape)}, contiguous in its features")
+    return (t.data_ptr(), *st[:3])
 
 
 def _view(t, what: str, dtype, dims: int) -> View:
@@ -444,21 +442,8 @@ def _dense(t, what: str, dtype, shape) -> int:
     return t.data_ptr()
 
 
-class _Same:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
-
-
-_SAME = _Same()
-
-
 def _on(stream):
     """Allocations made inside belong to the stream that the call runs on."""
-    if stream is None:
-        return _SAME
     import torch
     return torch.cuda.stream(stream)
 
@@ -520,20 +505,22 @@ class DeltaRule:
         """Whole sequences from `state` (None: zero) -> (o, final states), and
         with save=True also what backward needs: (o, final states, saved)."""
         import torch
+        if stream is not None:
+            with _on(stream):
+                return self.forward(q, k, v, g, beta, state, offsets, scale, save)
         a = self._args(q, k, v, g, beta, offsets, scale)
         shape = (a.nseq, a.Hv, self.Dk, self.Dv)
         sin = _dense(state, "state", torch.float32, shape)
-        with _on(stream):
-            o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-            out = torch.empty(shape, dtype=torch.float32, device=v.device)
-            saved = None
-            if save:
-                n = int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq))
-                saved = torch.empty(n, dtype=torch.uint8, device=v.device)
-            scratch, n = self._scratch(a, 2 if save else 0, v.device)
-            _check(lib().fftconv_delta_forward(self._h, ctypes.byref(a), sin, _view(o, "o", v.dtype, 4),
-                                               out.data_ptr(), _ptr(saved), _ptr(scratch), n, _stream(stream)),
-                   "fftconv_delta_forward")
+        o = v.new_empty(v.shape)
+        out = torch.empty(shape, dtype=torch.float32, device=v.device)
+        saved = None
+        if save:
+            n = int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq))
+            saved = torch.empty(n, dtype=torch.uint8, device=v.device)
+        scratch, n = self._scratch(a, 2 if save else 0, v.device)
+        _check(lib().fftconv_delta_forward(self._h, ctypes.byref(a), sin, _view(o, "o", v.dtype, 4),
+                                           out.data_ptr(), _ptr(saved), _ptr(scratch), n, _stream(None)),
+               "fftconv_delta_forward")
         return (o, out, saved) if save else (o, out)
 
     def backward(self, do, q, k, v, g, beta, saved, dstate=None, offsets=None, scale=None, stream=None):
@@ -541,6 +528,9 @@ class DeltaRule:
         from do [B, T, Hv, Dv] and, if the final states were used, dstate;
         `saved` and the other arguments as in forward."""
         import torch
+        if stream is not None:
+            with _on(stream):
+                return self.backward(do, q, k, v, g, beta, saved, dstate, offsets, scale)
         a = self._args(q, k, v, g, beta, offsets, scale)
         dt = self.torch_dtype
         shape = (a.nseq, a.Hv, self.Dk, self.Dv)
@@ -548,13 +538,12 @@ class DeltaRule:
         vdo = View(*_strides(do, "do", dt, v.shape))
         sv = _dense(saved, "saved", torch.uint8,
                     (int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq)),))
-        with _on(stream):
-            grads = [torch.empty(t.shape, dtype=dt, device=t.device) for t in (q, k, v, g, beta)]
-            dst = torch.empty(shape, dtype=torch.float32, device=v.device)
-            scratch, n = self._scratch(a, 1, v.device)
-            views = [View(*_strides(t, "gradient", dt, t.shape)) for t in grads]
-            _check(lib().fftconv_delta_backward(self._h, ctypes.byref(a), vdo, dsin, sv, *views, dst.data_ptr(), _ptr(scratch), n,
-                                                _stream(stream)), "fftconv_delta_backward")
+        grads = [t.new_empty(t.shape) for t in (q, k, v, g, beta)]
+        dst = torch.empty(shape, dtype=torch.float32, device=v.device)
+        scratch, n = self._scratch(a, 1, v.device)
+        views = [View(*_strides(t, "gradient", dt, t.shape)) for t in grads]
+        _check(lib().fftconv_delta_backward(self._h, ctypes.byref(a), vdo, dsin, sv, *views, dst.data_ptr(), _ptr(scratch), n,
+                                            _stream(None)), "fftconv_delta_backward")
         return (*grads, dst)
 
     def step(self, q, k, v, g, beta, state, state_out=None, slots=None, scale=None, stream=None):
@@ -562,16 +551,18 @@ class DeltaRule:
         state[slots[b]] (slots: int32 [B] on the GPU, distinct; None: state[b])
         -> o.  The updated states go to state_out, by default back to state."""
         import torch
+        if stream is not None:
+            with _on(stream):
+                return self.step(q, k, v, g, beta, state, state_out, slots, scale)
         a = self._args(q, k, v, g, beta, None, scale)
         shape = (state.shape[0], v.shape[2], self.Dk, self.Dv)
         sin = _dense(state, "state", torch.float32, shape)
         sout = sin if state_out is None else _dense(state_out, "state_out", torch.float32, shape)
         sl = _dense(slots, "slots", torch.int32, (q.shape[0],))
-        with _on(stream):
-            o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-            _check(lib().fftconv_delta_step(self._h, ctypes.byref(a), sin, sout, shape[0], sl,
-                                            _view(o, "o", v.dtype, 4), _stream(stream)),
-                   "fftconv_delta_step")
+        o = v.new_empty(v.shape)
+        _check(lib().fftconv_delta_step(self._h, ctypes.byref(a), sin, sout, shape[0], sl,
+                                        _view(o, "o", v.dtype, 4), _stream(None)),
+               "fftconv_delta_step")
         return o
 
     def device_status(self, stream=None) -> int:
@@ -616,30 +607,34 @@ class QKNorm:
         positions: int32 [B, T] (None: the token's index).  qo, ko: where to
         write (q and k themselves are allowed)."""
         import torch
+        if stream is not None:
+            with _on(stream):
+                return self.forward(q, k, wq, wk, cos, sin, positions, qo, ko)
         args = ctypes.byref(self._args(q, k, wq, wk, cos, sin, positions))
         dt = self.torch_dtype
-        with _on(stream):
-            qo = torch.empty(q.shape, dtype=dt, device=q.device) if qo is None else qo
-            ko = torch.empty(k.shape, dtype=dt, device=k.device) if ko is None else ko
-            _check(lib().fftconv_qknorm_forward(args, View(*_strides(qo, "qo", dt, q.shape)),
-                                                View(*_strides(ko, "ko", dt, k.shape)), _stream(stream)),
-                   "fftconv_qknorm_forward")
+        qo = q.new_empty(q.shape) if qo is None else qo
+        ko = k.new_empty(k.shape) if ko is None else ko
+        _check(lib().fftconv_qknorm_forward(args, View(*_strides(qo, "qo", dt, q.shape)),
+                                            View(*_strides(ko, "ko", dt, k.shape)), _stream(None)),
+               "fftconv_qknorm_forward")
         return qo, ko
 
     def backward(self, dqo, dko, q, k, wq=None, wk=None, cos=None, sin=None, positions=None, stream=None):
         """Gradients (dq, dk, dwq, dwk) from those of forward's outputs; dwq
         (dwk) is None where wq (wk) is."""
         import torch
+        if stream is not None:
+            with _on(stream):
+                return self.backward(dqo, dko, q, k, wq, wk, cos, sin, positions)
         args = ctypes.byref(self._args(q, k, wq, wk, cos, sin, positions))
         dt = self.torch_dtype
         vdq, vdk = View(*_strides(dqo, "dqo", dt, q.shape)), View(*_strides(dko, "dko", dt, k.shape))
-        with _on(stream):
-            dq, dk = (torch.empty(t.shape, dtype=dt, device=t.device) for t in (q, k))
-            dwq, dwk = (None if w is None else torch.empty(self.D, dtype=torch.float32, device=q.device)
-                        for w in (wq, wk))
-            n = int(lib().fftconv_qknorm_scratch_bytes(args)) if (wq is not None or wk is not None) else 0
-            scratch = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-            _check(lib().fftconv_qknorm_backward(args, vdq, vdk, View(*_strides(dq, "dq", dt, q.shape)),
-                                                 View(*_strides(dk, "dk", dt, k.shape)), _ptr(dwq), _ptr(dwk),
-                                                 _ptr(scratch), n, _stream(stream)), "fftconv_qknorm_backward")
+        dq, dk = (t.new_empty(t.shape) for t in (q, k))
+        dwq, dwk = (None if w is None else torch.empty(self.D, dtype=torch.float32, device=q.device)
+                    for w in (wq, wk))
+        n = int(lib().fftconv_qknorm_scratch_bytes(args)) if (wq is not None or wk is not None) else 0
+        scratch = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        _check(lib().fftconv_qknorm_backward(args, vdq, vdk, View(*_strides(dq, "dq", dt, q.shape)),
+                                             View(*_strides(dk, "dk", dt, k.shape)), _ptr(dwq), _ptr(dwk),
+                                             _ptr(scratch), n, _stream(None)), "fftconv_qknorm_backward")
         return dq, dk, dwq, dwk
