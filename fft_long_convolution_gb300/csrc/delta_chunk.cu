@@ -1025,25 +1025,33 @@ cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
 }  // namespace
 
 // Segments.  A sequence's chunks follow one another, so few long sequences
-// leave SMs idle; cut into segments they cost three walks instead of one: the
-// segments' end states from zero and their transition matrices (side by side),
-// a short join, then the outputs from the joined states.  Taken when the rows
-// would fill at most a fifth of the SMs and a segment keeps 16 chunks.
+// leave SMs idle.  Cut into m segments a row costs two walks of 1/m of its
+// chunks instead of one of all: the segments' end states from zero and their
+// transition matrices (side by side: m - 1 and m - 2 CTAs a row; the last
+// segment needs neither, the first no matrix), a join, then the outputs from the
+// joined states.  The rule counts waves of CTAs over the SMs in chunks of a walk
+// (2 us; 2.6 us when all SMs walk and share the bandwidth), takes a join's step as
+// one more and 12 for the rest of it, and cuts when that saves a tenth.  One row
+// of 262144 tokens, 6 heads of 128: 25 segments, 1.1 ms in walks and join instead
+// of 8.3 ms; 8 rows of 4096: 3 segments took 148 us against 130 us uncut, and stay
+// uncut.  Packed rows are taken at their mean length.
 void plan_segments(ChunkArgs* a, int sms) {
     const DeltaArgs& d = a->d;
     a->slots = chunk_slots(d.B, d.T, d.nseq);
     a->sms = sms;
     const int64_t rows = int64_t(d.nseq) * d.Hv;
-    int64_t per = rows > 0 ? sms / rows : 1;                         // segments of a row
-    const int64_t chunks = d.nseq ? (d.B * d.T / d.nseq + kChunk - 1) / kChunk : 0;  // of a row (their mean when packed)
-    if (per > chunks / 16) per = chunks / 16;
-    if (per < 5) {
-        a->seg_chunks = a->slots + 1;  // one segment each
-        a->segments = d.nseq;
-        return;
+    const int64_t chunks = d.nseq ? (d.B * d.T / d.nseq + kChunk - 1) / kChunk : 0;
+    int64_t best = 1, cost = chunks - chunks / 10;
+    for (int64_t m = 3; rows > 0 && m * rows <= sms && m * 8 <= chunks; ++m) {
+        const int64_t w1 = ((2 * m - 3) * rows + sms - 1) / sms, len = (chunks + m - 1) / m;
+        const int64_t c = 13 * (w1 + 1) * len / 10 + m + 12;
+        if (c < cost) {
+            cost = c;
+            best = m;
+        }
     }
-    a->seg_chunks = (chunks + per - 1) / per;
-    a->segments = a->slots / a->seg_chunks + d.nseq;
+    a->seg_chunks = best == 1 ? a->slots + 1 : (chunks + best - 1) / best;
+    a->segments = best == 1 ? d.nseq : a->slots / a->seg_chunks + d.nseq;
 }
 
 cudaError_t launch_delta_forward(const ChunkArgs& a, int dt, int dk, int dv, cudaStream_t st) {
