@@ -20,7 +20,8 @@ namespace {
 // buffered so that a token costs one barrier.  The state is read and written
 // once per call: for one token that is all the traffic that counts, so the
 // bound is HBM bandwidth for large batches (Dk / 16 independent 16-byte loads
-// in flight per thread) and latency for a few rows.
+// in flight per thread; 256 rows of 12 heads of 128 x 128: 63 us, 6.4 TB/s) and
+// latency for a few rows (one row: 2.2 us).
 struct TokenArgs {
     DeltaArgs d;
     const float* sin;  // pool of states [nslots][Hv][Dk][Dv]

@@ -34,6 +34,12 @@
 //                stores what the backward needs
 // A step is a chain of waits (S's operands, S W, Vn, the update), and a wait costs
 // some 200 cycles even when it is over, so what S W needs arrives on one barrier.
+// That chain bounds the walk: 2 us a chunk at Dk = Dv = 128 while few CTAs walk
+// (8 x 4096 tokens, 6 heads, 48 CTAs: 130 us; 149 us when it also stores what the
+// backward needs), of which the products take 1 us and the conversions of S, two
+// parts of 16384 values, 0.3 us of the four schedulers.  Where segments fill the SMs
+// the bound is HBM (262144 tokens, 6 heads: the outputs' walks 445 us, 105 KB a chunk,
+// 5.8 TB/s; the states' 592 us, 123 KB, 5.1 TB/s).
 #include "delta_chunk.h"
 
 #include "chunk.cuh"
@@ -182,10 +188,12 @@ struct PrepCfg {
     static constexpr int PER_SM = 4;
 };
 
-// T, W, P and the decays of one chunk and value head at a time.  Bound: the
-// latency of its steps (each waits for the last, eleven in the inverse alone),
-// covered by four CTAs per SM and by fetching the next chunk's tiles and gates
-// under the current one's last steps.
+// T, W, P and the decays of one chunk and value head at a time.  Bound: HBM at
+// Dk = 128 (32 KB of K and Q in, 57 KB of images out; 8 x 4096 tokens, 6 heads:
+// 53 us, 5.2 TB/s, 76 % of a plain copy's rate), the latency of its steps at
+// Dk = 64 (each waits for the last, the inverse's levels most of all).  Hence four
+// CTAs per SM, and the next chunk's tiles and gates fetched under the current
+// one's last steps.
 template <int DT, int DK>
 __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(const __grid_constant__ ChunkArgs a) {
     using C = PrepCfg<DK>;
@@ -850,6 +858,10 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
         // ---------------------------------------------------------------- loads
         bool ok = true;
         int c = 0;
+        // images are asked into L2 two chunks ahead (8 x 4096 tokens with what the
+        // backward needs: 149 us, 161 us without); not by the walks of segments, which
+        // fill the SMs and are at HBM's rate without it (445 us, 483 us with it)
+        const bool ahead = a.seg_chunks > a.slots;
         auto fix = [&](uint8_t* t, int m) {  // zero rows m .. 63 of a tile
             for (int x = lane; x < (64 - m) * 8; x += 32) *reinterpret_cast<uint4*>(t + m * 128 + x * 16) = make_uint4(0, 0, 0, 0);
         };
@@ -861,6 +873,9 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             // rows past the sequence: the TMA engine writes zeros past the tensor's
             // end; in a packed row they are the next sequence's and are zeroed here
             const bool tail = d.offsets && left < kChunk;
+            if (!STATE && ahead && c + 2 < n && elect())
+                bulk_prefetch(a.images + ((slot0 + c + 2) * d.Hv + h) * kImage<DK>, kImage<DK>);
+            __syncwarp();
             if (c >= C::NKQ && !(ok = wait(bar + kKqFree + st, (c / C::NKQ - 1) & 1, fail))) break;
             uint64_t* full = tail ? bar + kRaw : bar + kGo + st;
             if (elect()) {  // the state alone needs neither Q nor P
@@ -935,7 +950,8 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
 // sequence, float32; N_0 already holds the initial state's part.  The result
 // replaces N_s.  A CTA takes 8 columns of S; the next M arrives by a bulk copy
 // while the current one is applied (8 us a segment without, 2 us with it at
-// 128 x 128).
+// 128 x 128; 25 segments: 76 us).  Bound: the 64 KB of M that each CTA pulls from L2
+// a segment, which nothing but the chain of segments can overlap.
 template <int DK, int DV>
 __global__ void __launch_bounds__(256) delta_join_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(128) float join_sm[];  // M, two stages

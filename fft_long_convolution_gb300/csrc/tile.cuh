@@ -36,6 +36,11 @@ __device__ __forceinline__ uint64_t adv(uint64_t d, uint32_t bytes) { return d +
 
 constexpr uint32_t kMnA = 1u << 15, kMnB = 1u << 16;  // MN-major A, B in the instruction descriptor
 
+// Bring n bytes (a multiple of 16, from a 16-byte boundary) into L2.
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t n) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(src)), "r"(n) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "

@@ -458,7 +458,10 @@ typedef struct {
  * taken as max(g, -120): exp(-120) is zero in float32, so a log decay of
  * -infinity (a reset of the state) needs no special case.  Keys of norm at
  * most 1 and beta in [0, 1] keep the recurrence bounded; fp16 intermediates
- * (states and corrected values inside a chunk) have binary16's range.
+ * (states and corrected values inside a chunk) have binary16's range.  Whole
+ * sequences are worked in chunks of 64 tokens: a NaN or an infinity in a token
+ * may reach every output of its chunk, those before it included, and every
+ * later one of its sequence and head; other sequences and heads are not reached.
  *
  * Sequences: offsets == NULL: the B rows of T tokens each (nseq = B).  Else
  * B = 1 and sequence i is tokens offsets[i] .. offsets[i+1] - 1 of the row
