@@ -426,11 +426,11 @@ def _strides(t, what: str, dtype, shape):
     return (t.data_ptr(), *st[:3])
 
 
-def _view(t, what: str, dtype, dims: int) -> View:
-    """A tensor as a view, checked against dtype and rank."""
-    if t.dim() != dims:
-        raise ValueError(f"{what} must have {dims} dimensions")
-    return View(*_strides(t, what, dtype, t.shape))
+def _new(t):
+    """An uninitialised contiguous tensor like t, and its view."""
+    import torch
+    o = torch.empty_like(t, memory_format=torch.contiguous_format)
+    return o, View(o.data_ptr(), *o.stride()[:3])
 
 
 def _dense(t, what: str, dtype, shape) -> int:
@@ -511,16 +511,15 @@ class DeltaRule:
         a = self._args(q, k, v, g, beta, offsets, scale)
         shape = (a.nseq, a.Hv, self.Dk, self.Dv)
         sin = _dense(state, "state", torch.float32, shape)
-        o = v.new_empty(v.shape)
+        o, vo = _new(v)
         out = torch.empty(shape, dtype=torch.float32, device=v.device)
         saved = None
         if save:
             n = int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq))
             saved = torch.empty(n, dtype=torch.uint8, device=v.device)
         scratch, n = self._scratch(a, 2 if save else 0, v.device)
-        _check(lib().fftconv_delta_forward(self._h, ctypes.byref(a), sin, _view(o, "o", v.dtype, 4),
-                                           out.data_ptr(), _ptr(saved), _ptr(scratch), n, _stream(None)),
-               "fftconv_delta_forward")
+        _check(lib().fftconv_delta_forward(self._h, ctypes.byref(a), sin, vo, out.data_ptr(), _ptr(saved),
+                                           _ptr(scratch), n, _stream(None)), "fftconv_delta_forward")
         return (o, out, saved) if save else (o, out)
 
     def backward(self, do, q, k, v, g, beta, saved, dstate=None, offsets=None, scale=None, stream=None):
@@ -538,10 +537,9 @@ class DeltaRule:
         vdo = View(*_strides(do, "do", dt, v.shape))
         sv = _dense(saved, "saved", torch.uint8,
                     (int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq)),))
-        grads = [t.new_empty(t.shape) for t in (q, k, v, g, beta)]
+        grads, views = zip(*(_new(t) for t in (q, k, v, g, beta)))
         dst = torch.empty(shape, dtype=torch.float32, device=v.device)
         scratch, n = self._scratch(a, 1, v.device)
-        views = [View(*_strides(t, "gradient", dt, t.shape)) for t in grads]
         _check(lib().fftconv_delta_backward(self._h, ctypes.byref(a), vdo, dsin, sv, *views, dst.data_ptr(), _ptr(scratch), n,
                                             _stream(None)), "fftconv_delta_backward")
         return (*grads, dst)
@@ -559,9 +557,8 @@ class DeltaRule:
         sin = _dense(state, "state", torch.float32, shape)
         sout = sin if state_out is None else _dense(state_out, "state_out", torch.float32, shape)
         sl = _dense(slots, "slots", torch.int32, (q.shape[0],))
-        o = v.new_empty(v.shape)
-        _check(lib().fftconv_delta_step(self._h, ctypes.byref(a), sin, sout, shape[0], sl,
-                                        _view(o, "o", v.dtype, 4), _stream(None)),
+        o, vo = _new(v)
+        _check(lib().fftconv_delta_step(self._h, ctypes.byref(a), sin, sout, shape[0], sl, vo, _stream(None)),
                "fftconv_delta_step")
         return o
 
@@ -612,11 +609,9 @@ class QKNorm:
                 return self.forward(q, k, wq, wk, cos, sin, positions, qo, ko)
         args = ctypes.byref(self._args(q, k, wq, wk, cos, sin, positions))
         dt = self.torch_dtype
-        qo = q.new_empty(q.shape) if qo is None else qo
-        ko = k.new_empty(k.shape) if ko is None else ko
-        _check(lib().fftconv_qknorm_forward(args, View(*_strides(qo, "qo", dt, q.shape)),
-                                            View(*_strides(ko, "ko", dt, k.shape)), _stream(None)),
-               "fftconv_qknorm_forward")
+        qo, vq = _new(q) if qo is None else (qo, View(*_strides(qo, "qo", dt, q.shape)))
+        ko, vk = _new(k) if ko is None else (ko, View(*_strides(ko, "ko", dt, k.shape)))
+        _check(lib().fftconv_qknorm_forward(args, vq, vk, _stream(None)), "fftconv_qknorm_forward")
         return qo, ko
 
     def backward(self, dqo, dko, q, k, wq=None, wk=None, cos=None, sin=None, positions=None, stream=None):
@@ -629,12 +624,11 @@ class QKNorm:
         args = ctypes.byref(self._args(q, k, wq, wk, cos, sin, positions))
         dt = self.torch_dtype
         vdq, vdk = View(*_strides(dqo, "dqo", dt, q.shape)), View(*_strides(dko, "dko", dt, k.shape))
-        dq, dk = (t.new_empty(t.shape) for t in (q, k))
+        (dq, oq), (dk, ok) = _new(q), _new(k)
         dwq, dwk = (None if w is None else torch.empty(self.D, dtype=torch.float32, device=q.device)
                     for w in (wq, wk))
         n = int(lib().fftconv_qknorm_scratch_bytes(args)) if (wq is not None or wk is not None) else 0
         scratch = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-        _check(lib().fftconv_qknorm_backward(args, vdq, vdk, View(*_strides(dq, "dq", dt, q.shape)),
-                                             View(*_strides(dk, "dk", dt, k.shape)), _ptr(dwq), _ptr(dwk),
-                                             _ptr(scratch), n, _stream(None)), "fftconv_qknorm_backward")
+        _check(lib().fftconv_qknorm_backward(args, vdq, vdk, oq, ok, _ptr(dwq), _ptr(dwk), _ptr(scratch), n,
+                                             _stream(None)), "fftconv_qknorm_backward")
         return dq, dk, dwq, dwk

@@ -429,12 +429,12 @@ def test_refusals():
     # outputs over inputs
     L = F.lib()
     a = plan._args(q, k, v, g, beta, None, None)
-    vo = F._view(v, "v", dt, 4)
+    vo = F.View(*F._strides(v, "v", dt, v.shape))
     need = L.fftconv_delta_scratch_bytes(plan._h, B, T, Hk, Hv, B, 0)
     scratch = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
     assert L.fftconv_delta_forward(plan._h, ctypes.byref(a), None, vo, None, None, scratch.data_ptr(), need, None) == 1
     o = torch.empty_like(v)
-    ov = F._view(o, "o", dt, 4)
+    ov = F.View(*F._strides(o, "o", dt, o.shape))
     if need:
         assert L.fftconv_delta_forward(plan._h, ctypes.byref(a), None, ov, None, None, None, 0, None) == 4
     assert L.fftconv_delta_backward(plan._h, ctypes.byref(a), ov, None, None, ov, ov, ov, ov, ov, None, None, 0, None) == 1
