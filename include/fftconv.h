@@ -553,7 +553,8 @@ fftconv_status_t fftconv_delta_step(fftconv_delta_t plan, const fftconv_delta_ar
  *       s = sin[p][i]; pair i is features (i, i + R/2), or (2i, 2i + 1) when
  *       interleaved.  R = 0: no rotation.
  * q: [B][T][Hq][D], k: [B][T][Hk][D] (either may have no heads).  D is a
- * multiple of 8 up to 256, R even and at most D.  cos, sin: float32
+ * multiple of 8 up to 256, R even and at most D; at most 1023 heads each and
+ * fewer than 2^30 tokens.  cos, sin: float32
  * [table_rows][R/2] on the device; positions: device int32 [B][T], or NULL for
  * p = t.  A token whose position is outside the tables gets NaN outputs (and
  * gradients).  Arithmetic in float32, one rounding at the end.  y may be the
