@@ -53,16 +53,6 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Whether a phase is over, the same answer in every lane of the warp.
-__device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{.reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;}"
-                 : "=r"(done)
-                 : "r"(smem_u32(bar)), "r"(parity)
-                 : "memory");
-    return __all_sync(0xffffffffu, done != 0);
-}
-
 // Bounded wait of a whole warp: gives up after about a second, or sooner when
 // another role of the CTA has (*fail set).  The same answer in every lane.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
