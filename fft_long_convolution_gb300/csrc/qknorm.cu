@@ -372,7 +372,8 @@ fftconv_status_t run(const fftconv_qknorm_args_t* p, const fftconv_view_t* dy, c
     const int64_t heads[2] = {p->Hq, p->Hk};
     const fftconv_view_t* xs[2] = {&p->q, &p->k};
     View *vx[2] = {&a.q, &a.k}, *vd[2] = {&a.dyq, &a.dyk}, *vy[2] = {&a.yq, &a.yk};
-    Span outs[4] = {}, ins[9] = {};
+    // two outputs, both weights' gradients, scratch; inputs and given gradients, weights, tables, positions
+    Span outs[5] = {}, ins[9] = {};
     int no = 0, ni = 0;
     for (int i = 0; i < 2; ++i) {
         if (!heads[i]) continue;
@@ -382,24 +383,17 @@ fftconv_status_t run(const fftconv_qknorm_args_t* p, const fftconv_view_t* dy, c
     }
     for (int i = 0; i < 2; ++i) {
         if (!heads[i]) continue;
-        const Span o = span_of(*vy[i], p->B, p->T, heads[i], p->D);
         // in place on its own input is fine (a lane reads its elements before it writes them)
         for (int j = 0; j < 2; ++j) {
             if (!heads[j]) continue;
-            if (!(i == j && same_view(*vx[j], *vy[i])) && meets(o, span_of(*vx[j], p->B, p->T, heads[j], p->D))) {
-                // heads of q and k may be interleaved slices of one buffer; two
-                // slices updated in place never share an element
-                const bool both = heads[0] && heads[1] && same_view(a.q, a.yq) && same_view(a.k, a.yk);
-                if (!both) return FFTCONV_ERR_INVALID;
-            }
-            if (BWD && !(i == j && same_view(*vd[j], *vy[i])) &&
-                meets(o, span_of(*vd[j], p->B, p->T, heads[j], p->D))) {
-                const bool both = heads[0] && heads[1] && same_view(a.dyq, a.yq) && same_view(a.dyk, a.yk);
-                if (!both) return FFTCONV_ERR_INVALID;
+            for (const View* x : {vx[j], vd[j]}) {
+                if (!x->p || (i == j && same_view(*x, *vy[i]))) continue;
+                if (share(*x, heads[j], *vy[i], heads[i], p->B, p->T, p->D)) return FFTCONV_ERR_INVALID;
             }
         }
-        outs[no++] = o;
+        outs[no++] = span_of(*vy[i], p->B, p->T, heads[i], p->D);
     }
+    if (heads[0] && heads[1] && share(a.yq, heads[0], a.yk, heads[1], p->B, p->T, p->D)) return FFTCONV_ERR_INVALID;
     const size_t wb = size_t(p->D) * 4, tb = size_t(p->table_rows) * (p->R / 2) * 4;
     ins[ni++] = span_of(p->wq, wb);
     ins[ni++] = span_of(p->wk, wb);
@@ -409,6 +403,13 @@ fftconv_status_t run(const fftconv_qknorm_args_t* p, const fftconv_view_t* dy, c
         ins[ni++] = span_of(p->positions, size_t(tokens) * 4);
     }
     if (any_meet(outs, ins)) return FFTCONV_ERR_INVALID;
+    const int first = no;
+    outs[no++] = span_of(dwq, wb);
+    outs[no++] = span_of(dwk, wb);
+    for (int j = 0; j < 2; ++j) {
+        if (vx[j]->p) ins[ni++] = span_of(*vx[j], p->B, p->T, heads[j], p->D);
+        if (vd[j]->p) ins[ni++] = span_of(*vd[j], p->B, p->T, heads[j], p->D);
+    }
     a.wq = p->wq;
     a.wk = p->wk;
     a.cos = p->cos;
@@ -441,6 +442,13 @@ fftconv_status_t run(const fftconv_qknorm_args_t* p, const fftconv_view_t* dy, c
         if (!scratch || scratch_bytes < size_t(grid) * 2 * wb) return FFTCONV_ERR_WORKSPACE;
         if (off16(scratch)) return FFTCONV_ERR_ALIGN;
         a.part = static_cast<float*>(scratch);
+        outs[no++] = span_of(scratch, size_t(grid) * 2 * wb);
+    }
+    for (int i = first; i < no; ++i) {
+        for (const Span& x : ins)
+            if (meets(outs[i], x)) return FFTCONV_ERR_INVALID;
+        for (int j = 0; j < i; ++j)
+            if (meets(outs[i], outs[j])) return FFTCONV_ERR_INVALID;
     }
     int mode = 0;
     if (p->R) mode = p->interleaved ? 1 : (p->R % 8 == 0 ? 2 : 3);

@@ -47,6 +47,52 @@ inline Span span_of(const void* p, size_t bytes) {
 
 inline bool meets(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
 
+// Whether two boxes of D elements, repeated along the dimensions k .. n - 1
+// (strides descending; na and nb repetitions), have an element in common; b's
+// first element is off elements after a's.  Only repetitions whose remaining
+// dimensions' ranges meet are looked at: one or two of each dimension where these
+// lie inside the stride, as in every permuted slice of one buffer.  Strides that
+// overlap themselves count as shared.
+struct Level {
+    int64_t s, na, nb;
+};
+inline bool boxes_meet(const Level* lv, int k, int n, int64_t off, int64_t D) {
+    if (k == n) return off < D && -off < D;
+    int64_t ea = D, eb = D;
+    for (int i = k + 1; i < n; ++i) {
+        ea += (lv[i].na - 1) * lv[i].s;
+        eb += (lv[i].nb - 1) * lv[i].s;
+    }
+    auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+    const int64_t s = lv[k].s;
+    int64_t lo = floor_div(-eb - off, s) + 1, hi = -floor_div(off - ea, s) - 1;
+    if (lo < 1 - lv[k].na) lo = 1 - lv[k].na;
+    if (hi > lv[k].nb - 1) hi = lv[k].nb - 1;
+    if (hi - lo > 3) return true;
+    for (int64_t m = lo; m <= hi; ++m)
+        if (boxes_meet(lv, k + 1, n, off + m * s, D)) return true;
+    return false;
+}
+
+// Whether two views [B][T][Ha or Hb][D] have an element in common: exact for
+// slices of one buffer (equal strides), else by their address ranges.
+inline bool share(const View& a, int64_t Ha, const View& b, int64_t Hb, int64_t B, int64_t T, int64_t D) {
+    if (!meets(span_of(a, B, T, Ha, D), span_of(b, B, T, Hb, D))) return false;
+    if ((B > 1 && a.b != b.b) || (T > 1 && a.t != b.t) || (Ha > 1 && Hb > 1 && a.h != b.h)) return true;
+    Level lv[3];
+    int n = 0;
+    if (B > 1) lv[n++] = {a.b, B, B};
+    if (T > 1) lv[n++] = {a.t, T, T};
+    if (Ha > 1 || Hb > 1) lv[n++] = {Ha > 1 ? a.h : b.h, Ha, Hb};
+    for (int i = 1; i < n; ++i)
+        for (int j = i; j > 0 && lv[j].s > lv[j - 1].s; --j) {
+            const Level t = lv[j];
+            lv[j] = lv[j - 1];
+            lv[j - 1] = t;
+        }
+    return boxes_meet(lv, 0, n, (b.p - a.p) / 2, D);
+}
+
 // Whether any of `outs` meets any of `ins`.
 template <int NO, int NI>
 bool any_meet(const Span (&outs)[NO], const Span (&ins)[NI]) {

@@ -558,7 +558,9 @@ fftconv_status_t fftconv_delta_step(fftconv_delta_t plan, const fftconv_delta_ar
  * [table_rows][R/2] on the device; positions: device int32 [B][T], or NULL for
  * p = t.  A token whose position is outside the tables gets NaN outputs (and
  * gradients).  Arithmetic in float32, one rounding at the end.  y may be the
- * same view as x (in place); other overlaps are INVALID.
+ * same view as x (in place).  Otherwise no output shares an element with an
+ * input or with the other output (INVALID): slices of one buffer with equal
+ * strides are told apart element by element, other views by address range.
  */
 typedef enum { FFTCONV_NORM_RMS = 0, FFTCONV_NORM_L2 = 1 } fftconv_norm_t;
 
@@ -584,7 +586,8 @@ fftconv_status_t fftconv_qknorm_forward(const fftconv_qknorm_args_t *args, fftco
  * (float32 [D], sums over all tokens and heads, overwritten; NULL: not
  * wanted; they need wq, wk only through dx).  scratch:
  * fftconv_qknorm_scratch_bytes(args) bytes, 16-byte aligned; may be NULL when
- * dwq and dwk are.  Bitwise reproducible.
+ * dwq and dwk are.  dq (dk) may be the same view as q or dyq (k or dyk); dwq,
+ * dwk and scratch overlap nothing.  Bitwise reproducible.
  * Returns as the forward, and WORKSPACE.
  */
 size_t fftconv_qknorm_scratch_bytes(const fftconv_qknorm_args_t *args);

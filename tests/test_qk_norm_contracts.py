@@ -1,0 +1,93 @@
+"""What the norm of queries and keys promises beside its values: overlaps."""
+import ctypes
+
+import pytest
+import torch
+
+import fft_long_convolution_gb300 as F
+from _mixers import qk_norm, rel
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+B, T, D, WIDE = 2, 4, 64, 8  # views below are heads of one [B, T, WIDE, D] buffer
+BUF, OTHER, GRAD = 1 << 20, 1 << 24, 1 << 28  # addresses that nothing reads: every call here is refused
+
+
+def view(base, head):
+    return F.View(base + head * D * 2, T * WIDE * D, WIDE * D, D)
+
+
+def args(q, k, Hq, Hk):
+    a = F.QKNormArgs()
+    a.dtype, a.norm, a.D, a.R, a.interleaved, a.eps = 1, 0, D, 0, 0, 1e-6
+    a.B, a.T, a.Hq, a.Hk, a.q, a.k = B, T, Hq, Hk, q, k
+    return a
+
+
+@pytest.mark.parametrize("hq,hk", [((0, 4), (2, 4)), ((0, 2), (0, 2)), ((3, 2), (0, 4)), ((0, 8), (7, 1)), ((5, 1), (0, 8))])
+def test_shared_heads_in_place_are_refused(hq, hk):
+    """Queries and keys in place (forward on themselves, backward on their
+    gradients) while they have heads in common."""
+    L = F.lib()
+    q, k = view(BUF, hq[0]), view(BUF, hk[0])
+    a = args(q, k, hq[1], hk[1])
+    assert L.fftconv_qknorm_forward(ctypes.byref(a), q, k, None) == 1
+    b = args(view(OTHER, 0), view(2 * OTHER, 0), hq[1], hk[1])
+    assert L.fftconv_qknorm_backward(ctypes.byref(b), q, k, q, k, None, None, None, 0, None) == 1
+
+
+@pytest.mark.parametrize("hq,hk", [((0, 4), (2, 4)), ((0, 2), (0, 2)), ((0, 8), (7, 1))])
+def test_outputs_over_each_other_are_refused(hq, hk):
+    L = F.lib()
+    yq, yk = view(GRAD, hq[0]), view(GRAD, hk[0])
+    a = args(view(BUF, 0), view(OTHER, 0), hq[1], hk[1])
+    assert L.fftconv_qknorm_forward(ctypes.byref(a), yq, yk, None) == 1
+    assert L.fftconv_qknorm_backward(ctypes.byref(a), view(2 * OTHER, 0), view(4 * OTHER, 0), yq, yk, None, None, None, 0,
+                                     None) == 1
+
+
+def test_one_output_in_place_over_the_other_input_is_refused():
+    L = F.lib()
+    a = args(view(BUF, 0), view(BUF, 2), 4, 4)
+    assert L.fftconv_qknorm_forward(ctypes.byref(a), a.q, view(OTHER, 0), None) == 1
+
+
+@pytest.mark.parametrize("dwq,dwk,scratch", [
+    (BUF, None, 4 * GRAD), (None, OTHER, 4 * GRAD), (2 * GRAD, None, 4 * GRAD), (5 * GRAD, 5 * GRAD, 4 * GRAD),
+    (5 * GRAD, 5 * GRAD + 128, 4 * GRAD), (4 * GRAD, None, 4 * GRAD), (5 * GRAD, None, BUF), (5 * GRAD, None, 3 * GRAD),
+    (6 * GRAD, None, 4 * GRAD), (GRAD, None, 4 * GRAD)])
+def test_weight_gradients_and_scratch_over_other_buffers_are_refused(dwq, dwk, scratch):
+    """Over an input (BUF, OTHER), a given gradient (GRAD), an output (2 and 3
+    GRAD), a weight (6 GRAD), each other."""
+    L = F.lib()
+    a = args(view(BUF, 0), view(OTHER, 0), 4, 4)
+    a.wq = 6 * GRAD
+    n = L.fftconv_qknorm_scratch_bytes(ctypes.byref(a))
+    st = L.fftconv_qknorm_backward(ctypes.byref(a), view(GRAD, 0), view(GRAD, 4), view(2 * GRAD, 0), view(3 * GRAD, 0), dwq, dwk,
+                                   scratch, n, None)
+    assert st == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["token-major", "head-major", "batch-inside"])
+def test_slices_of_one_buffer(layout):
+    """Disjoint heads of one buffer, in whatever order it is stored: both in
+    place, one of them, and written to other slices of it."""
+    dt, Hq, Hk = torch.bfloat16, 3, 2
+    order = {"token-major": (0, 1, 2, 3), "head-major": (0, 2, 1, 3), "batch-inside": (1, 0, 2, 3)}[layout]
+    back = [order.index(i) for i in range(4)]
+    gen = torch.Generator().manual_seed(1)
+    x = torch.randn(B, T, 2 * (Hq + Hk), D, generator=gen).to(dt)
+    plan = F.QKNorm(D, dt)
+    ref = qk_norm(x, None, "rms", 1e-6)
+
+    def fresh():
+        y = x.permute(order).contiguous().cuda().permute(back)
+        return y, y[:, :, :Hq], y[:, :, Hq:Hq + Hk], y[:, :, Hq + Hk:2 * Hq + Hk], y[:, :, 2 * Hq + Hk:]
+
+    for way in range(4):
+        y, q, k, sq, sk = fresh()
+        to = [(q, k), (q, None), (None, k), (sq, sk)][way]
+        qo, ko = plan.forward(q, k, qo=to[0], ko=to[1])
+        assert rel(qo, ref[:, :, :Hq]) < U[dt] and rel(ko, ref[:, :, Hq:Hq + Hk]) < U[dt]
+        untouched = {0: slice(Hq + Hk, None), 1: slice(Hq, None), 2: slice(Hq + Hk, None), 3: slice(0, Hq + Hk)}[way]
+        assert torch.equal(y[:, :, untouched].cpu(), x[:, :, untouched])
