@@ -360,6 +360,7 @@ fftconv_status_t run(const fftconv_qknorm_args_t* p, const fftconv_view_t* dy, c
                      float* dwk, void* scratch, size_t scratch_bytes, fftconv_stream_t stream) {
     fftconv_status_t e = check_args(p);
     if (e != FFTCONV_OK) return e;
+    if ((reinterpret_cast<uintptr_t>(dwq) | reinterpret_cast<uintptr_t>(dwk)) & 3) return FFTCONV_ERR_ALIGN;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t tokens = p->B * p->T;
     const bool want = BWD && (dwq || dwk);

@@ -91,3 +91,14 @@ def test_slices_of_one_buffer(layout):
         assert rel(qo, ref[:, :, :Hq]) < U[dt] and rel(ko, ref[:, :, Hq:Hq + Hk]) < U[dt]
         untouched = {0: slice(Hq + Hk, None), 1: slice(Hq, None), 2: slice(Hq + Hk, None), 3: slice(0, Hq + Hk)}[way]
         assert torch.equal(y[:, :, untouched].cpu(), x[:, :, untouched])
+
+
+@pytest.mark.parametrize("dwq,dwk", [(5 * GRAD + 2, None), (None, 5 * GRAD + 1)])
+def test_weight_gradients_off_their_alignment_are_refused(dwq, dwk):
+    L = F.lib()
+    a = args(view(BUF, 0), view(OTHER, 0), 4, 4)
+    n = L.fftconv_qknorm_scratch_bytes(ctypes.byref(a))
+    for T_ in (T, 0):
+        a.T = T_
+        assert L.fftconv_qknorm_backward(ctypes.byref(a), view(GRAD, 0), view(GRAD, 4), view(2 * GRAD, 0), view(3 * GRAD, 0), dwq,
+                                         dwk, 4 * GRAD, n, None) == 3
