@@ -190,7 +190,7 @@ def _stream(stream) -> Optional[int]:
     if stream is not None:
         return stream.cuda_stream
     from torch import _C  # torch.cuda.current_stream() takes 12 us
-    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+    return _C._cuda_getCurrentRawStream(_current_device())
 
 
 class Plan:
@@ -412,17 +412,33 @@ def status_string(code: int) -> str:
 #
 # A decoding step is a few microseconds of GPU work, so these calls keep their
 # own work small: each tensor is looked at once, and the argument structures
-# are packed in one go.
+# are packed in one go.  All tensors of a call are on the current GPU (checked).
 
 _DELTA_ARGS = struct.Struct("=5qQf4x" + "Q3q" * 5)
 _NORM_ARGS = struct.Struct("=5if4q" + "Q3q" * 2 + "4QqQ")
 
 
-def _strides(t, what: str, dtype, shape):
-    """A tensor's address and its first three strides, checked against dtype and shape."""
+def _current_device() -> int:
+    from torch import _C
+    return _C._cuda_getDevice()
+
+
+def _device(t, what: str) -> int:
+    """The GPU of a call's first tensor, which has to be the current one: that is
+    where the call's stream, its outputs and its scratch are."""
+    dev = t.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"{what} must be a CUDA tensor on the current GPU")
+    return dev
+
+
+def _strides(t, what: str, dtype, shape, dev=None):
+    """A tensor's address and its first three strides, checked against dtype, shape and (if given) GPU."""
     st = t.stride()
     if t.shape != shape or t.dtype is not dtype or not t.is_cuda or (len(st) == 4 and st[3] != 1 and shape[3] > 1):
         raise ValueError(f"{what} must be a CUDA {dtype} tensor of shape {tuple(shape)}, contiguous in its features")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{what} is on another GPU than the call's first tensor")
     return (t.data_ptr(), *st[:3])
 
 
@@ -433,12 +449,14 @@ def _new(t):
     return o, View(o.data_ptr(), *o.stride()[:3])
 
 
-def _dense(t, what: str, dtype, shape) -> int:
+def _dense(t, what: str, dtype, shape, dev=None) -> int:
     """The address of a contiguous CUDA tensor of the given shape (None: 0)."""
     if t is None:
         return 0
     if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{what} is on another GPU than the call's first tensor")
     return t.data_ptr()
 
 
@@ -485,16 +503,17 @@ class DeltaRule:
         B, T, Hk, _ = qs = q.shape
         Hv = v.shape[2]
         gs = (B, T, Hv)
+        dev = _device(q, "q")
         nseq, off = B, 0
         if offsets is not None:
             if offsets.dim() != 1 or offsets.numel() < 1:
                 raise ValueError("offsets must be [n + 1]")
             nseq = offsets.numel() - 1
-            off = _dense(offsets, "offsets", torch.int32, offsets.shape)
+            off = _dense(offsets, "offsets", torch.int32, offsets.shape, dev)
         return DeltaArgs.from_buffer_copy(_DELTA_ARGS.pack(
             B, T, Hk, Hv, nseq, off, self._scale if scale is None else scale, *_strides(q, "q", dt, qs),
-            *_strides(k, "k", dt, qs), *_strides(v, "v", dt, (B, T, Hv, self.Dv)), *_strides(g, "g", dt, gs),
-            *_strides(beta, "beta", dt, gs)))
+            *_strides(k, "k", dt, qs, dev), *_strides(v, "v", dt, (B, T, Hv, self.Dv), dev),
+            *_strides(g, "g", dt, gs, dev), *_strides(beta, "beta", dt, gs, dev)))
 
     def _scratch(self, a, which, device):
         import torch
@@ -510,7 +529,7 @@ class DeltaRule:
                 return self.forward(q, k, v, g, beta, state, offsets, scale, save)
         a = self._args(q, k, v, g, beta, offsets, scale)
         shape = (a.nseq, a.Hv, self.Dk, self.Dv)
-        sin = _dense(state, "state", torch.float32, shape)
+        sin = _dense(state, "state", torch.float32, shape, q.get_device())
         o, vo = _new(v)
         out = torch.empty(shape, dtype=torch.float32, device=v.device)
         saved = None
@@ -531,12 +550,12 @@ class DeltaRule:
             with _on(stream):
                 return self.backward(do, q, k, v, g, beta, saved, dstate, offsets, scale)
         a = self._args(q, k, v, g, beta, offsets, scale)
-        dt = self.torch_dtype
+        dt, dev = self.torch_dtype, q.get_device()
         shape = (a.nseq, a.Hv, self.Dk, self.Dv)
-        dsin = _dense(dstate, "dstate", torch.float32, shape)
-        vdo = View(*_strides(do, "do", dt, v.shape))
+        dsin = _dense(dstate, "dstate", torch.float32, shape, dev)
+        vdo = View(*_strides(do, "do", dt, v.shape, dev))
         sv = _dense(saved, "saved", torch.uint8,
-                    (int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq)),))
+                    (int(lib().fftconv_delta_saved_bytes(self._h, a.B, a.T, a.Hv, a.nseq)),), dev)
         grads, views = zip(*(_new(t) for t in (q, k, v, g, beta)))
         dst = torch.empty(shape, dtype=torch.float32, device=v.device)
         scratch, n = self._scratch(a, 1, v.device)
@@ -554,9 +573,9 @@ class DeltaRule:
                 return self.step(q, k, v, g, beta, state, state_out, slots, scale)
         a = self._args(q, k, v, g, beta, None, scale)
         shape = (state.shape[0], v.shape[2], self.Dk, self.Dv)
-        sin = _dense(state, "state", torch.float32, shape)
-        sout = sin if state_out is None else _dense(state_out, "state_out", torch.float32, shape)
-        sl = _dense(slots, "slots", torch.int32, (q.shape[0],))
+        sin = _dense(state, "state", torch.float32, shape, q.get_device())
+        sout = sin if state_out is None else _dense(state_out, "state_out", torch.float32, shape, q.get_device())
+        sl = _dense(slots, "slots", torch.int32, (q.shape[0],), q.get_device())
         o, vo = _new(v)
         _check(lib().fftconv_delta_step(self._h, ctypes.byref(a), sin, sout, shape[0], sl, vo, _stream(None)),
                "fftconv_delta_step")
@@ -587,16 +606,17 @@ class QKNorm:
         B, T, Hq, _ = q.shape
         Hk = k.shape[2]
         pc = ps = pp = rows = 0
+        dev = _device(q, "q")
         if R:
             if cos is None or sin is None:
                 raise ValueError("a rotation needs cos and sin")
             rows = cos.shape[0]
-            pc, ps = _dense(cos, "cos", f32, (rows, R // 2)), _dense(sin, "sin", f32, (rows, R // 2))
-            pp = _dense(positions, "positions", torch.int32, (B, T))
+            pc, ps = _dense(cos, "cos", f32, (rows, R // 2), dev), _dense(sin, "sin", f32, (rows, R // 2), dev)
+            pp = _dense(positions, "positions", torch.int32, (B, T), dev)
         return QKNormArgs.from_buffer_copy(_NORM_ARGS.pack(
             self._code, self._norm, D, R, self.interleaved, self.eps, B, T, Hq, Hk,
-            *_strides(q, "q", dt, (B, T, Hq, D)), *_strides(k, "k", dt, (B, T, Hk, D)),
-            _dense(wq, "wq", f32, (D,)), _dense(wk, "wk", f32, (D,)), pc, ps, rows, pp))
+            *_strides(q, "q", dt, (B, T, Hq, D)), *_strides(k, "k", dt, (B, T, Hk, D), dev),
+            _dense(wq, "wq", f32, (D,), dev), _dense(wk, "wk", f32, (D,), dev), pc, ps, rows, pp))
 
     def forward(self, q, k, wq=None, wk=None, cos=None, sin=None, positions=None, qo=None, ko=None, stream=None):
         """q: [B, T, Hq, D], k: [B, T, Hk, D] -> the normed and rotated (q, k).
@@ -608,9 +628,9 @@ class QKNorm:
             with _on(stream):
                 return self.forward(q, k, wq, wk, cos, sin, positions, qo, ko)
         args = ctypes.byref(self._args(q, k, wq, wk, cos, sin, positions))
-        dt = self.torch_dtype
-        qo, vq = _new(q) if qo is None else (qo, View(*_strides(qo, "qo", dt, q.shape)))
-        ko, vk = _new(k) if ko is None else (ko, View(*_strides(ko, "ko", dt, k.shape)))
+        dt, dev = self.torch_dtype, q.get_device()
+        qo, vq = _new(q) if qo is None else (qo, View(*_strides(qo, "qo", dt, q.shape, dev)))
+        ko, vk = _new(k) if ko is None else (ko, View(*_strides(ko, "ko", dt, k.shape, dev)))
         _check(lib().fftconv_qknorm_forward(args, vq, vk, _stream(None)), "fftconv_qknorm_forward")
         return qo, ko
 
@@ -622,8 +642,9 @@ class QKNorm:
             with _on(stream):
                 return self.backward(dqo, dko, q, k, wq, wk, cos, sin, positions)
         args = ctypes.byref(self._args(q, k, wq, wk, cos, sin, positions))
-        dt = self.torch_dtype
-        vdq, vdk = View(*_strides(dqo, "dqo", dt, q.shape)), View(*_strides(dko, "dko", dt, k.shape))
+        dt, dev = self.torch_dtype, q.get_device()
+        vdq = View(*_strides(dqo, "dqo", dt, q.shape, dev))
+        vdk = View(*_strides(dko, "dko", dt, k.shape, dev))
         (dq, oq), (dk, ok) = _new(q), _new(k)
         dwq, dwk = (None if w is None else torch.empty(self.D, dtype=torch.float32, device=q.device)
                     for w in (wq, wk))
