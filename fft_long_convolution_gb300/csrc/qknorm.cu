@@ -255,9 +255,13 @@ __global__ void __launch_bounds__(kThreads) qknorm_kernel(const NormArgs a) {
                         #pragma unroll
                         for (int j = 0; j < 8; ++j) z[j] = r * fmaf(-dot, x[j], z[j]);
                     }
-                    if (lost) {
+                    if (lost) {  // the weights' gradients are sums over it, too
                         #pragma unroll
                         for (int j = 0; j < 8; ++j) z[j] = CUDART_NAN_F;
+                        if constexpr (BWD) {
+                            #pragma unroll
+                            for (int j = 0; j < 8; ++j) acc[m][j] = CUDART_NAN_F;
+                        }
                     }
                     if (on) store_row<MODE>(py + (h0 + i) * vy.h, d, pack8<DT>(z));
                 }

@@ -556,8 +556,9 @@ fftconv_status_t fftconv_delta_step(fftconv_delta_t plan, const fftconv_delta_ar
  * multiple of 8 up to 256, R even and at most D; at most 1023 heads each and
  * fewer than 2^30 tokens.  cos, sin: float32
  * [table_rows][R/2] on the device; positions: device int32 [B][T], or NULL for
- * p = t.  A token whose position is outside the tables gets NaN outputs (and
- * gradients).  Arithmetic in float32, one rounding at the end.  y may be the
+ * p = t.  A token whose position is outside the tables gets NaN outputs and
+ * gradients, and the weights' gradients, sums over all tokens, become NaN.
+ * Arithmetic in float32, one rounding at the end.  y may be the
  * same view as x (in place).  Otherwise no output shares an element with an
  * input or with the other output (INVALID): slices of one buffer with equal
  * strides are told apart element by element, other views by address range.

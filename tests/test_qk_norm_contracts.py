@@ -1,4 +1,5 @@
-"""What the norm of queries and keys promises beside its values: overlaps."""
+"""What the norm of queries and keys promises beside its values: overlaps,
+positions outside the tables."""
 import ctypes
 
 import pytest
@@ -102,3 +103,33 @@ def test_weight_gradients_off_their_alignment_are_refused(dwq, dwk):
         a.T = T_
         assert L.fftconv_qknorm_backward(ctypes.byref(a), view(GRAD, 0), view(GRAD, 4), view(2 * GRAD, 0), view(3 * GRAD, 0), dwq,
                                          dwk, 4 * GRAD, n, None) == 3
+
+
+def tables(rows, R):
+    ang = torch.arange(rows, dtype=torch.float64)[:, None] * 100.0 ** (-torch.arange(R // 2, dtype=torch.float64) / max(R // 2, 1))
+    return ang.cos().float().cuda(), ang.sin().float().cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+def test_positions_outside_the_tables_reach_every_gradient(inter):
+    """A token without a table row has NaN outputs and gradients; the weights'
+    gradients are sums over all tokens, so it reaches them too.  Other tokens
+    keep their values."""
+    dt, b, t, Hq, Hk, d, R = torch.bfloat16, 1, 4, 2, 1, 64, 32
+    gen = torch.Generator().manual_seed(3)
+    q, k, dq, dk = (torch.randn(b, t, h, d, generator=gen).to(dt).cuda() for h in (Hq, Hk, Hq, Hk))
+    wq, wk = torch.ones(d).cuda(), torch.ones(d).cuda()
+    cos, sin = tables(10, R)
+    plan = F.QKNorm(d, dt, rotary=R, interleaved=inter)
+
+    def both(pos):
+        kw = dict(wq=wq, wk=wk, cos=cos, sin=sin, positions=torch.tensor([pos], dtype=torch.int32).cuda())
+        return plan.forward(q, k, **kw) + plan.backward(dq, dk, q, k, **kw)
+
+    good, bad = both([0, 3, 4, 9]), both([0, -1, 10, 9])
+    for x, y in zip(good[:4], bad[:4]):
+        assert bool(torch.isfinite(x).all()) and bool(torch.isnan(y[:, 1:3]).all())
+        assert torch.equal(x[:, [0, 3]], y[:, [0, 3]])
+    for x, y in zip(good[4:], bad[4:]):
+        assert bool(torch.isfinite(x).all()) and bool(torch.isnan(y).all())
