@@ -139,7 +139,12 @@ __device__ __forceinline__ void load_turn(const NormArgs& a, int64_t p, int lane
 // Rotate a row spread over the group's lanes; dir = +1 forward, -1 inverse.
 // MODE 1: pairs are neighbours; 2: pairs are features j and 4 + j of a lane; 3:
 // halves of another length, through the group's row buffer in shared memory.
-template <int MODE, int N>
+// Features at R or beyond are not mixed: turned by (1, 0), a NaN or an infinity in
+// one would reach another, so the other's part is dropped, not multiplied by 0 (8 x
+// 16384 tokens of 12 heads of 128: forward 153 us, 151 by multiplying; choosing
+// between the results took 177).
+// WHOLE: R is a multiple of 8, so a lane's pairs are all rotated or none.
+template <int MODE, bool WHOLE, int N>
 __device__ __forceinline__ void turn(float (&z)[8], const float (&c)[N], const float (&s)[N], float dir, int lane, int R,
                                      float* row, unsigned mask) {
     if constexpr (MODE == 3) {
@@ -159,10 +164,11 @@ __device__ __forceinline__ void turn(float (&z)[8], const float (&c)[N], const f
     } else {
         #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            const bool on = lane * 8 + (MODE == 1 && !WHOLE ? 2 * j : 0) < R;
             float &x = z[MODE == 1 ? 2 * j : j], &y = z[MODE == 1 ? 2 * j + 1 : j + 4];
             const float u = x, v = y, sj = dir * s[j];
-            x = u * c[j] - v * sj;
-            y = v * c[j] + u * sj;
+            x = u * c[j] - (on ? v : 0.0f) * sj;
+            y = v * c[j] + (on ? u : 0.0f) * sj;
         }
     }
 }
@@ -175,7 +181,7 @@ __device__ __forceinline__ float group_sum(float v, unsigned mask) {
 }
 
 // MODE 0: no rotation; 1, 2, 3 as turn().  HB: heads taken at a time.  VEC:
-// weights and tables by 16-byte loads.
+// weights and tables by 16-byte loads (R a multiple of 8).
 template <int DT, int G, int HB, int MODE, bool VEC, bool BWD>
 __global__ void __launch_bounds__(kThreads) qknorm_kernel(const NormArgs a) {
     __shared__ float rows[MODE == 3 ? kThreads / G : 1][MODE == 3 ? 8 * G : 1];
@@ -240,10 +246,10 @@ __global__ void __launch_bounds__(kThreads) qknorm_kernel(const NormArgs a) {
                     if constexpr (!BWD) {
                         #pragma unroll
                         for (int j = 0; j < 8; ++j) z[j] = x[j] * r * w[m][j];
-                        if constexpr (MODE != 0) turn<MODE>(z, c, s, 1.0f, lane, a.R, rows[grp], mask);
+                        if constexpr (MODE != 0) turn<MODE, VEC>(z, c, s, 1.0f, lane, a.R, rows[grp], mask);
                     } else {
                         unpack8<DT>(ud[i], z);
-                        if constexpr (MODE != 0) turn<MODE>(z, c, s, -1.0f, lane, a.R, rows[grp], mask);
+                        if constexpr (MODE != 0) turn<MODE, VEC>(z, c, s, -1.0f, lane, a.R, rows[grp], mask);
                         float dot = 0.0f;
                         #pragma unroll
                         for (int j = 0; j < 8; ++j) {

@@ -558,10 +558,12 @@ fftconv_status_t fftconv_delta_step(fftconv_delta_t plan, const fftconv_delta_ar
  * [table_rows][R/2] on the device; positions: device int32 [B][T], or NULL for
  * p = t.  A token whose position is outside the tables gets NaN outputs and
  * gradients, and the weights' gradients, sums over all tokens, become NaN.
- * Arithmetic in float32, one rounding at the end.  y may be the
- * same view as x (in place).  Otherwise no output shares an element with an
- * input or with the other output (INVALID): slices of one buffer with equal
- * strides are told apart element by element, other views by address range.
+ * A NaN or an infinity in q or k reaches its own row only (and the weights' gradients);
+ * features past R are mixed with no other.
+ * Arithmetic in float32, one rounding at the end.  y may be the same view
+ * as x (in place).  Otherwise no output shares an element with an input or with
+ * the other output (INVALID): slices of one buffer with equal strides are told
+ * apart element by element, other views by address range.
  */
 typedef enum { FFTCONV_NORM_RMS = 0, FFTCONV_NORM_L2 = 1 } fftconv_norm_t;
 

@@ -1,5 +1,5 @@
 """What the norm of queries and keys promises beside its values: overlaps,
-positions outside the tables."""
+positions outside the tables, the reach of non-finite values."""
 import ctypes
 
 import pytest
@@ -133,3 +133,37 @@ def test_positions_outside_the_tables_reach_every_gradient(inter):
         assert torch.equal(x[:, [0, 3]], y[:, [0, 3]])
     for x, y in zip(good[4:], bad[4:]):
         assert bool(torch.isfinite(x).all()) and bool(torch.isnan(y).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["weight", "input", "gradient"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("d,R,inter", [(64, 32, False), (64, 32, True), (24, 6, True), (24, 6, False), (96, 40, False), (80, 4, True)])
+def test_unrotated_features_stay_by_themselves(d, R, inter, bad, what):
+    """A NaN or an infinity in a feature past the rotated ones is mixed with no
+    other feature: in a weight it is seen in that feature's output alone, in an
+    input as the norm carries it, in a gradient in that weight's gradient alone."""
+    dt, b, t, H, f = torch.bfloat16, 1, 3, 2, R
+    gen = torch.Generator().manual_seed(4)
+    q, k, dq, dk = (torch.randn(b, t, H, d, generator=gen).to(dt).cuda() for _ in range(4))
+    wq, wk = torch.ones(d).cuda(), torch.ones(d).cuda()
+    cos, sin = tables(10, R)
+    plan = F.QKNorm(d, dt, rotary=R, interleaved=inter)
+    kw = dict(cos=cos, sin=sin)
+    others = [i for i in range(d) if i != f]
+    if what == "weight":
+        want, _ = plan.forward(q, k, wq=wq, wk=wk, **kw)
+        wq[f] = bad
+        got, _ = plan.forward(q, k, wq=wq, wk=wk, **kw)
+        assert not bool(torch.isfinite(got[..., f]).any()) and torch.equal(got[..., others], want[..., others])
+    elif what == "input":
+        q[0, 1, 0, f] = bad
+        got, _ = plan.forward(q, k, wq=wq, wk=wk, **kw)
+        pos = torch.arange(t)[None].expand(b, t)
+        ref = qk_norm(q.cpu(), wq.cpu(), "rms", 1e-6, cos.cpu(), sin.cpu(), pos, inter)
+        assert torch.equal(torch.isnan(got).cpu(), torch.isnan(ref))
+    else:
+        want = plan.backward(dq, dk, q, k, wq=wq, wk=wk, **kw)[2]
+        dq[0, 1, 0, f] = bad
+        got = plan.backward(dq, dk, q, k, wq=wq, wk=wk, **kw)[2]
+        assert not bool(torch.isfinite(got[f])) and torch.equal(got[others], want[others])
