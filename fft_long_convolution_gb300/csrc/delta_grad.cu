@@ -9,7 +9,11 @@
 //   dK = beta Y + X^T Q + (beta H)^T K + e (Vn dS'^T),   dbeta = dR.V + k.Y
 //   db_i = q.dQ + k.(beta Y) - k.(dK - beta Y), and at the last token also
 //          sum_j k_j.(e Vn dS'^T)_j + G_63 <S, dS'>;  dg: db summed from the end
-// (rows dotted; every term of db is a row of a product that is formed anyway.)
+// (rows dotted; every term of db is a row of a product that is formed anyway).  A
+// pair of tokens (i, j) adds X_ij q_i.k_j and beta_i H_ij k_i.k_j to db_i and takes them
+// from db_j; both sides use the same rounded X, H and beta H, or what should cancel
+// in dg for pairs on one side of a token would stay as rounding (keys with a cosine of
+// 0.9, beta = 0.9: dg 1.5 to 2.5 u off, 4 to 6 u with beta H rounded by itself).
 //
 // Two kernels, as in the forward.  delta_dstate_kernel walks the chunks from
 // the last to the first with dS^T as its accumulator and leaves dS'^T and dR
@@ -466,8 +470,9 @@ delta_dstate_kernel(const __grid_constant__ GradArgs a) {
 // starts one block early: rows 0-63 are never used), so dK's parts meet in one
 // thread.  Roles: warps 0-7 form X and H and the gradients' rows, warp 8 stores
 // them and forms the gates' gradients, warp 9 loads (a chunk ahead, each buffer as
-// soon as it has been read) and issues the products.  Bound: HBM, 193 KB read and
-// 32 KB written per chunk at Dk = Dv = 128 (8 x 4096 tokens, 6 heads: 108 us, 6.4 TB/s).
+// soon as it has been read) and issues the products.  Bound: HBM, 181 kB read and
+// 33 kB written per chunk at Dk = Dv = 128 (8 x 4096 tokens, 6 heads, 3072 chunks:
+// 114 us, 5.8 TB/s; beta H as one 16-bit part, which dg does not stand, took 109).
 template <int DK, int DV>
 struct GradCfg {
     static constexpr uint32_t oA = 0;                      // [feature block][dO rows | dR rows]
@@ -477,7 +482,7 @@ struct GradCfg {
     static constexpr uint32_t oS = oN + DV * 128;          // S^T: [DK / 64] blocks of DV rows
     static constexpr uint32_t oD = oS + DK * DV * 2;       // dS'^T
     static constexpr uint32_t oX = oD + DK * DV * 2;       // [X; H], then dQ
-    static constexpr uint32_t oG = oX + 2 * kTile;         // [X; beta H], then dK
+    static constexpr uint32_t oG = oX + 2 * kTile;         // beta H, high and low part, then dK
     static constexpr uint32_t oR = oG + 2 * kTile;         // dR's low part
     static constexpr uint32_t oE = oR + DV * 128;          // the image's decays, two stages
     // two stages of row sums: [4][2][64], dR.V [4][64], <S, dS'> [8]
@@ -589,12 +594,12 @@ delta_grad_kernel(const __grid_constant__ GradArgs a) {
                 const int j0 = half * 32;
                 tc::ld32x32b_x32(lanes + C::cSc + j0, x);
                 tc::wait_ld();
-                const float bi = gt[128 + i], f = lower ? -1.0f : d.scale, be = lower ? gt[192 + i] : 1.0f;
+                const float bi = gt[128 + i], f = lower ? -1.0f : d.scale, be = gt[192 + i];
                 const int last = (lower ? i - 1 : i) - j0;
-                uint8_t *px = sm + C::oX + row * 128, *pg = sm + C::oG + row * 128;
+                uint8_t *px = sm + C::oX + row * 128, *pg = sm + C::oG + i * 128;
                 #pragma unroll
                 for (int j = 0; j < 32; j += 8) {
-                    uint32_t u[4], g[4];
+                    uint32_t u[4];
                     #pragma unroll
                     for (int q = 0; q < 8; q += 4) {
                         const float4 b = *reinterpret_cast<const float4*>(gt + 128 + j0 + j + q);
@@ -607,12 +612,21 @@ delta_grad_kernel(const __grid_constant__ GradArgs a) {
                         }
                         u[q / 2] = Op<DT>::pack(v[0], v[1]);
                         u[q / 2 + 1] = Op<DT>::pack(v[2], v[3]);
-                        g[q / 2] = Op<DT>::pack(be * v[0], be * v[1]);
-                        g[q / 2 + 1] = Op<DT>::pack(be * v[2], be * v[3]);
                     }
                     const int pos = (((j0 + j) / 8) ^ (row & 7)) * 16;
                     *reinterpret_cast<uint4*>(px + pos) = make_uint4(u[0], u[1], u[2], u[3]);
-                    *reinterpret_cast<uint4*>(pg + pos) = make_uint4(g[0], g[1], g[2], g[3]);
+                    if (lower) {
+                        // beta times the rounded H, whole in two parts: a pair's term in db's
+                        // row and its term in db's column cancel where neither is after t
+                        uint32_t hi[4], lo[4];
+                        #pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const cpx c = Op<DT>::unpack(u[q]);
+                            split<DT>(mul2(make_float2(be, be), make_float2(c.r, c.i)), &hi[q], &lo[q]);
+                        }
+                        *reinterpret_cast<uint4*>(pg + pos) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(pg + kTile + pos) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
             }
             if (!(ok = wait(bar + gLoad + 2, par, fail))) break;
@@ -869,18 +883,23 @@ delta_grad_kernel(const __grid_constant__ GradArgs a) {
                     tc::mma_ss(tm + C::cE1, adv(dn, f * 128), adv(dd, f * 128), id | kMnA, f > 0);
                 tc::commit(bar + gD1);
             }
-            // D2 = [X; H] K and E2 = [X; beta H]^T [Q; K]
+            // D2 = [X; H] K and E2 = X^T Q + (beta H)^T K
             if (!(ok = wait(bar + gX, par, fail))) break;
             tc::fence_after();
             if (elect()) {
                 const uint64_t dx = sdesc(sb + C::oX, 16), dk = sdesc(sb + C::oB + kTile, 2 * kTile);
-                const uint64_t dg = sdesc(sb + C::oX, 2 * kTile), dq = sdesc(sb + C::oB, 2 * kTile);
+                // A's first 64 rows are never used and come from Q's tile
+                const uint64_t du = sdesc(sb + C::oB, C::oX - C::oB), dq = sdesc(sb + C::oB, 2 * kTile);
+                const uint64_t dh = sdesc(sb + C::oB, C::oG - C::oB), dl = sdesc(sb + C::oB, C::oG + kTile - C::oB);
                 #pragma unroll
                 for (int t = 0; t < 64; t += 16)
                     tc::mma_ss(tm + C::cD2, adv(dx, t * 2), adv(dk, t * 128), id, t > 0);
                 #pragma unroll
-                for (int t = 0; t < 128; t += 16)
-                    tc::mma_ss(tm + C::cE2, adv(dg, t * 128), adv(dq, t * 128), id | kMnA, t > 0);
+                for (int t = 0; t < 64; t += 16) {
+                    tc::mma_ss(tm + C::cE2, adv(du, t * 128), adv(dq, t * 128), id | kMnA, t > 0);
+                    tc::mma_ss(tm + C::cE2, adv(dh, t * 128), adv(dk, t * 128), id | kMnA, 1);
+                    tc::mma_ss(tm + C::cE2, adv(dl, t * 128), adv(dk, t * 128), id | kMnA, 1);
+                }
                 tc::commit(bar + gD2);
             }
             if (nx.m) {
