@@ -11,10 +11,13 @@ constexpr uint32_t kWaitFinal = 1u << 18;  // polls of the waits that end a CTA
 
 // What delta_prep_kernel leaves for a chunk of one value head: the tiles P,
 // (T beta) high and low part, then float32 e[64], scale G[64], b log2(e)[64],
-// beta[64], then -W^T, DK rows of 64 tokens, high and low part.
+// beta[64], then -W^T, DK rows of 64 tokens, high and low part, then what rounding
+// b log2(e) left, float32 [64].
 constexpr uint32_t kImgP = 0, kImgT = tile::kTile, kImgE = 3 * tile::kTile, kImgW = kImgE + 1024;
 template <int DK>
-constexpr uint32_t kImage = kImgW + DK * 256;
+constexpr uint32_t kImgR = kImgW + DK * 256;
+template <int DK>
+constexpr uint32_t kImage = kImgR<DK> + 256;
 
 // Chunk slot -> sequence and chunk: the last sequence whose first slot is not
 // past it.

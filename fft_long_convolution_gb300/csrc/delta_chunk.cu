@@ -184,7 +184,7 @@ struct PrepCfg {
     static constexpr uint32_t KQ = (DK / 64) * 2 * kTile;  // [feature block][K rows | Q rows]
     // T beta is staged where Q was (two tiles), W where the scratch was
     static constexpr uint32_t oTb = DK == 128 ? kTile : 2 * kTile, sTb = DK == 128 ? 2 * kTile : kTile;
-    static constexpr uint32_t oA = 4 * kTile, oL = oA + 64 * LD * 4, oItem = oL + 288 * 4, oBar = oItem + 64, BYTES = oBar + 64;
+    static constexpr uint32_t oA = 4 * kTile, oL = oA + 64 * LD * 4, oItem = oL + 352 * 4, oBar = oItem + 64, BYTES = oBar + 64;
     static constexpr int PER_SM = 4;
 };
 
@@ -248,8 +248,10 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
     const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(s_tmem);
     const uint32_t lanes = tm + (uint32_t(32 * (w & 3)) << 16);
     float* A = reinterpret_cast<float*>(sm + C::oA);
-    // b log2(e), beta, -G; decays between 16-token blocks (below)
-    float *sbv = reinterpret_cast<float*>(sm + C::oL), *sbe = sbv + 64, *sng = sbe + 64, *sE2 = sng + 64, *sE1 = sE2 + 64;
+    // b log2(e) and what rounding it left, beta, -G; decays between 16-token blocks (below)
+    float *sbv = reinterpret_cast<float*>(sm + C::oL), *sbr = sbv + 64, *sbe = sbr + 64, *sng = sbe + 64, *sE2 = sng + 64,
+          *sE1 = sE2 + 64;
+    auto decay = [&](int i, int j) { return exp2_fast((sbv[i] - sbv[j]) + (sbr[i] - sbr[j])); };
     auto sync = [] { __syncthreads(); };
     const int row = 32 * (w & 3) + lane, i = row & 63, up = (row >> 5) & 1, half = w >> 2;
     const bool isp = row >= 64;
@@ -262,16 +264,27 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
         const uint32_t par = k & 1;
         uint8_t* image = a.images + it.at * kImage<DK>;
         if (w == 2) {
-            // running sum of the log decays, in units of log 2
+            // running sum of the log decays, in units of log 2, as two floats: whole
+            // numbers (exact) and fractions are summed apart, so that tokens that empty
+            // the state (-173 each) cost later ratios of decays no digits
             constexpr float kLog2e = 1.44269504088896340736f;
             const float g0 = kLog2e * log_decay(g[0]), g1 = kLog2e * log_decay(g[1]);
-            float x = g0 + g1;
+            const float h1 = rintf(g1), f1 = g1 - h1;
+            float h = rintf(g0) + h1, f = (g0 - rintf(g0)) + f1;
             #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float v = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += v;
+                const float v = __shfl_up_sync(0xffffffffu, h, o), y = __shfl_up_sync(0xffffffffu, f, o);
+                if (lane >= o) {
+                    h += v;
+                    f += y;
+                }
             }
-            *reinterpret_cast<float2*>(sbv + 2 * lane) = make_float2(x - g1, x);
+            #pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float a = u ? h : h - h1, c = u ? f : f - f1, s = a + c, t = s - a;
+                sbv[2 * lane + u] = s;
+                sbr[2 * lane + u] = (a - (s - t)) + (c - t);  // a + c - s, exactly
+            }
             *reinterpret_cast<float2*>(sbe + 2 * lane) = make_float2(e[0], e[1]);
         }
         if (p == 0) bulk_wait_read();  // the last W has left the scratch
@@ -282,19 +295,20 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
         if (p < 64) {
             const float b = sbv[p], G = exp2_fast(b);
             float* gt = reinterpret_cast<float*>(image + kImgE);
-            gt[p] = exp2_fast(sbv[63] - b);
+            gt[p] = decay(63, p);
             gt[64 + p] = d.scale * G;
             gt[128 + p] = b;
             gt[192 + p] = sbe[p];
+            reinterpret_cast<float*>(image + kImgR<DK>)[p] = sbr[p];
             sng[p] = -G;
         } else if (w == 3) {
             find(items + (~k & 1));
         } else if (p >= 128 && p < 192) {
             const int q = p - 128;
-            sE2[q] = exp2_fast(sbv[32 + 16 * (q >> 5)] - sbv[q & 31]);
+            sE2[q] = decay(32 + 16 * (q >> 5), q & 31);
         } else if (p >= 192 && p < 224) {
             const int q = p - 192;
-            sE1[q] = exp2_fast(sbv[32 + q] - sbv[32 + (q & 16)]);
+            sE1[q] = decay(32 + q, 32 + (q & 16));
         }
         ok = mbar_wait_bounded(bar, par, kWaitLimitTile);
         if (d.offsets && it.m < kChunk) {
@@ -345,15 +359,16 @@ __global__ void __launch_bounds__(256, PrepCfg<DK>::PER_SM) delta_prep_kernel(co
                     x[j + 2] = __float_as_uint(v.x); x[j + 3] = __float_as_uint(v.y);
                 }
             } else {  // around the diagonal: entries above it (whatever they hold) become 0
-                const float bi = sbv[i];
+                const float bi = sbv[i], ri = sbr[i];
                 const int last = (isp ? i : i - 1) - j0;
                 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 b = *reinterpret_cast<const float4*>(sbv + j0 + j);
-                    const float bj[4] = {b.x, b.y, b.z, b.w};
+                    const float4 r = *reinterpret_cast<const float4*>(sbr + j0 + j);
+                    const float bj[4] = {b.x, b.y, b.z, b.w}, rj[4] = {r.x, r.y, r.z, r.w};
                     #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float v = f * exp2_fast(bi - bj[q]) * __uint_as_float(x[j + q]);
+                        const float v = f * exp2_fast((bi - bj[q]) + (ri - rj[q])) * __uint_as_float(x[j + q]);
                         x[j + q] = j + q <= last ? __float_as_uint(v) : 0u;
                     }
                 }
@@ -874,7 +889,7 @@ delta_fwd_kernel(const __grid_constant__ ChunkArgs a) {
             // end; in a packed row they are the next sequence's and are zeroed here
             const bool tail = d.offsets && left < kChunk;
             if (!STATE && ahead && c + 2 < n && elect())
-                bulk_prefetch(a.images + ((slot0 + c + 2) * d.Hv + h) * kImage<DK>, kImage<DK>);
+                bulk_prefetch(a.images + ((slot0 + c + 2) * d.Hv + h) * kImage<DK>, kImgR<DK>);
             __syncwarp();
             if (c >= C::NKQ && !(ok = wait(bar + kKqFree + st, (c / C::NKQ - 1) & 1, fail))) break;
             uint64_t* full = tail ? bar + kRaw : bar + kGo + st;

@@ -25,7 +25,7 @@ struct ChunkArgs {
 };
 
 // Bytes of an image.
-constexpr size_t prep_image(int dk) { return 3 * 8192 + 1024 + size_t(dk) * 256; }
+constexpr size_t prep_image(int dk) { return 3 * 8192 + 1024 + size_t(dk) * 256 + 256; }
 
 // Sets slots, segments and seg_chunks from the sizes in a->d.
 void plan_segments(ChunkArgs* a, int sms);

@@ -484,15 +484,15 @@ struct GradCfg {
     static constexpr uint32_t oX = oD + DK * DV * 2;       // [X; H], then dQ
     static constexpr uint32_t oG = oX + 2 * kTile;         // beta H, high and low part, then dK
     static constexpr uint32_t oR = oG + 2 * kTile;         // dR's low part
-    static constexpr uint32_t oE = oR + DV * 128;          // the image's decays, two stages
+    static constexpr uint32_t oE = oR + DV * 128, EB = 1024 + 256;  // the image's decays, two stages
     // two stages of row sums: [4][2][64], dR.V [4][64], <S, dS'> [8]
-    static constexpr uint32_t oL = oE + 2048, LB = (8 * 64 + 4 * 64 + 8) * 4;
+    static constexpr uint32_t oL = oE + 2 * EB, LB = (8 * 64 + 4 * 64 + 8) * 4;
     static constexpr uint32_t oItem = oL + 2 * LB, oBar = oItem + 64, BYTES = oBar + 128;
     static constexpr int THREADS = 320;
     // small heads: two CTAs per SM
     static constexpr int PER_SM = (BYTES + 1024) * 2 <= 233472 && DK == 64 ? 2 : 1;
     // bytes of the three groups of loads
-    static constexpr uint32_t B0 = 4 * DV * 128 + 1024, B1 = 2 * DV * DK * 2, B2 = DK * 256 + DV * 128;
+    static constexpr uint32_t B0 = 4 * DV * 128 + EB, B1 = 2 * DV * DK * 2, B2 = DK * 256 + DV * 128;
     // tensor memory columns; the scores' 64 columns are taken over by E2
     static constexpr uint32_t cE1 = 0, cE2 = DK, cSc = DK, cD1 = 2 * DK, cD2 = 3 * DK, COLS = 4 * DK;
 };
@@ -555,7 +555,7 @@ delta_grad_kernel(const __grid_constant__ GradArgs a) {
             const ChunkItem it = items[k & 1];
             if (!it.m) break;
             const bool tail = d.offsets && it.m < kChunk;
-            const float* gt = reinterpret_cast<const float*>(sm + C::oE + par * 1024);
+            const float* gt = reinterpret_cast<const float*>(sm + C::oE + par * C::EB);
             float *red = reinterpret_cast<float*>(sm + C::oL + par * C::LB), *rv = red + 512, *sd = rv + 256;
             if (!(ok = wait(bar + gLoad, par, fail))) break;
             if (tail) {
@@ -594,7 +594,7 @@ delta_grad_kernel(const __grid_constant__ GradArgs a) {
                 const int j0 = half * 32;
                 tc::ld32x32b_x32(lanes + C::cSc + j0, x);
                 tc::wait_ld();
-                const float bi = gt[128 + i], f = lower ? -1.0f : d.scale, be = gt[192 + i];
+                const float bi = gt[128 + i], ri = gt[256 + i], f = lower ? -1.0f : d.scale, be = gt[192 + i];
                 const int last = (lower ? i - 1 : i) - j0;
                 uint8_t *px = sm + C::oX + row * 128, *pg = sm + C::oG + i * 128;
                 #pragma unroll
@@ -603,11 +603,12 @@ delta_grad_kernel(const __grid_constant__ GradArgs a) {
                     #pragma unroll
                     for (int q = 0; q < 8; q += 4) {
                         const float4 b = *reinterpret_cast<const float4*>(gt + 128 + j0 + j + q);
-                        const float bj[4] = {b.x, b.y, b.z, b.w};
+                        const float4 s = *reinterpret_cast<const float4*>(gt + 256 + j0 + j + q);
+                        const float bj[4] = {b.x, b.y, b.z, b.w}, rj[4] = {s.x, s.y, s.z, s.w};
                         float v[4];
                         #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const float y = f * exp2_fast(bi - bj[r]) * __uint_as_float(x[j + q + r]);
+                            const float y = f * exp2_fast((bi - bj[r]) + (ri - rj[r])) * __uint_as_float(x[j + q + r]);
                             v[r] = j + q + r <= last ? y : 0.0f;  // above the diagonal, whatever it holds
                         }
                         u[q / 2] = Op<DT>::pack(v[0], v[1]);
@@ -766,7 +767,7 @@ delta_grad_kernel(const __grid_constant__ GradArgs a) {
                 }
             }
             // dbeta, and db summed from the end: tokens 2 lane and 2 lane + 1
-            const float* gt = reinterpret_cast<const float*>(sm + C::oE + par * 1024);
+            const float* gt = reinterpret_cast<const float*>(sm + C::oE + par * C::EB);
             const float *red = reinterpret_cast<const float*>(sm + C::oL + par * C::LB), *rv = red + 512, *sd = rv + 256;
             float db[2], last = 0.0f;
             #pragma unroll
@@ -813,7 +814,8 @@ delta_grad_kernel(const __grid_constant__ GradArgs a) {
                 }
                 bulk_g2s(sm + C::oR, a.dr + it.at * (2 * DV * 128) + DV * 128, DV * 128, bar);
                 bulk_g2s(sm + C::oN, a.saved_v + it.at * (DV * 128), DV * 128, bar);
-                bulk_g2s(sm + C::oE + stage * 1024, a.images + it.at * kImage<DK> + kImgE, 1024, bar);
+                bulk_g2s(sm + C::oE + stage * C::EB, a.images + it.at * kImage<DK> + kImgE, 1024, bar);
+                bulk_g2s(sm + C::oE + stage * C::EB + 1024, a.images + it.at * kImage<DK> + kImgR<DK>, 256, bar);
             }
             __syncwarp();
         };

@@ -1,7 +1,8 @@
 """Gated delta rule where its intermediate sums are far larger than its results.
 
 The tolerances are those of the ordinary inputs (u = 2^-8 for bf16, 2^-11 for
-fp16): states 2e-5, outputs 1.25 u, gradients 1.5 u, of the gates 3 u.
+fp16): states 2e-5, outputs 1.25 u, gradients 1.5 u, of the gates 3 u; heads are
+compared one by one where their decays matter.
 """
 import pytest
 import torch
@@ -11,12 +12,40 @@ from _mixers import delta_inputs, delta_rule, rel
 
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 DTYPES = [torch.bfloat16, torch.float16]
+NAMES = ("dq", "dk", "dv", "dg", "dbeta")
 
 
 def gradients(ins, do, scale):
     xs = [x.double().requires_grad_() for x in ins]
     o, _ = delta_rule(*xs, scale=scale)
     return torch.autograd.grad((o * do.double()).sum(), xs)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("low", [float("-inf"), -60.0, -20.0])
+@pytest.mark.parametrize("n", [16, 40])
+def test_many_resets_in_one_chunk(n, low, dt):
+    """n tokens in a row that empty the state (or nearly), then weak decays in
+    the same chunk: the decays between the latter do not feel the former."""
+    B, T, H, D = 1, 192, 3, 128
+    q, k, v, g, beta = delta_inputs(B, T, H, H, D, D, dt, seed=n)
+    g[:, 128:128 + n] = low
+    ins = (q, k, v, g, beta)
+    do = delta_inputs(B, T, H, H, D, D, dt, seed=n + 1)[2]
+    plan = F.DeltaRule(D, D, dt)
+    dins = [x.cuda() for x in ins]
+    o, s, saved = plan.forward(*dins, save=True)
+    got = plan.backward(do.cuda(), *dins, saved)
+    fin = [x.double() for x in ins]
+    fin[3] = fin[3].clamp(min=-200.0)
+    ref, sref = delta_rule(*fin, scale=D ** -0.5)
+    r = gradients(fin, do, D ** -0.5)
+    for h in range(H):
+        assert rel(s[:, h], sref[:, h]) < 2e-5
+        assert rel(o[:, :, h], ref[:, :, h]) < 1.25 * U[dt]
+        for name, x, y in zip(NAMES, got, r):
+            assert rel(x[:, :, h], y[:, :, h]) < (3 if name in ("dg", "dbeta") else 1.5) * U[dt], name
 
 
 @pytest.mark.gpu
