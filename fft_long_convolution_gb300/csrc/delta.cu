@@ -456,11 +456,14 @@ extern "C" fftconv_status_t fftconv_delta_backward(fftconv_delta_t p, const fftc
     input_spans(p, d, in);
     const Span more[3] = {span_of(vdo, d.B, d.T, d.Hv, p->Dv), span_of(d_state_out, sb),
                           span_of(saved, fftconv_delta_saved_bytes(p, d.B, d.T, d.Hv, d.nseq))};
-    // gradients may be slices of one buffer, so they are not checked against each other
+    // tokens' gradients may be slices of one buffer, so they are not checked against each other
     const Span outs[7] = {span_of(a.dq, d.B, d.T, d.Hk, p->Dk), span_of(a.dk, d.B, d.T, d.Hk, p->Dk),
                           span_of(a.dv, d.B, d.T, d.Hv, p->Dv), span_of(a.dg, d.B, d.T, d.Hv, 0),
                           span_of(a.dbeta, d.B, d.T, d.Hv, 0), span_of(d_state_in, sb), span_of(scratch, need)};
     if (any_meet(outs, in) || any_meet(outs, more)) return FFTCONV_ERR_INVALID;
+    for (int i = 5; i < 7; ++i)  // the state's gradient and scratch overlap nothing
+        for (int j = 0; j < i; ++j)
+            if (meets(outs[i], outs[j])) return FFTCONV_ERR_INVALID;
     a.d_state_out = d_state_out;
     a.d_state_in = d_state_in;
     const SavedLayout l(p, d.B, d.T, d.Hv, d.nseq);

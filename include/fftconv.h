@@ -520,6 +520,9 @@ fftconv_status_t fftconv_delta_forward(fftconv_delta_t plan, const fftconv_delta
  * the same inputs.  Writes dq, dk [B][T][Hk][Dk], dv [B][T][Hv][Dv], dg, dbeta
  * [B][T][Hv] (plan dtype) and, unless NULL, d_state_in float32
  * [nseq][Hv][Dk][Dv].  No atomics: the result is bitwise reproducible.
+ * Outputs and scratch must not overlap the inputs, d_state_in and scratch no
+ * output either (checked by address range; INVALID); the tokens' gradients may be
+ * slices of one buffer, and that they are disjoint is not checked.
  * Returns as fftconv_delta_forward.
  */
 fftconv_status_t fftconv_delta_backward(fftconv_delta_t plan, const fftconv_delta_args_t *args,
