@@ -130,14 +130,15 @@ __global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
 }
 
 // Zero the tokens of a packed row that belong to no sequence: those before the
-// first offset and from the last one on (offsets do not decrease).
+// first offset and from the last one on (offsets do not decrease); without
+// sequences, every token of every row.
 struct GapArgs {
     View v[5];
     int H[5], D[5];
     int n;
     const int32_t* offsets;
     int nseq;
-    int64_t T;
+    int64_t B, T;
 };
 
 __global__ void __launch_bounds__(256) gap_kernel(const GapArgs a) {
@@ -146,10 +147,11 @@ __global__ void __launch_bounds__(256) gap_kernel(const GapArgs a) {
     hi = hi < lo ? lo : (hi > a.T ? a.T : hi);
     const int64_t tokens = lo + a.T - hi;
     for (int i = 0; i < a.n; ++i) {
-        const int64_t per = int64_t(a.H[i]) * a.D[i], n = tokens * per;
+        const int64_t per = int64_t(a.H[i]) * a.D[i], row = tokens * per, n = a.B * row;
         for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < n; e += int64_t(gridDim.x) * 256) {
-            const int64_t t = e / per, r = e - t * per;
-            reinterpret_cast<uint16_t*>(a.v[i].p)[(t < lo ? t : hi + t - lo) * a.v[i].t + r / a.D[i] * a.v[i].h + r % a.D[i]] = 0;
+            const int64_t b = e / row, t = (e - b * row) / per, r = e - b * row - t * per;
+            reinterpret_cast<uint16_t*>(a.v[i].p)[b * a.v[i].b + (t < lo ? t : hi + t - lo) * a.v[i].t + r / a.D[i] * a.v[i].h +
+                                                  r % a.D[i]] = 0;
         }
     }
 }
@@ -285,6 +287,7 @@ cudaError_t zero_gaps(const DeltaArgs& d, int n, const View* v, const int* H, co
     a.n = n;
     a.offsets = d.offsets;
     a.nseq = d.nseq;
+    a.B = d.B;
     a.T = d.T;
     gap_kernel<<<64, 256, 0, st>>>(a);
     return cudaGetLastError();
@@ -432,7 +435,16 @@ extern "C" fftconv_status_t fftconv_delta_backward(fftconv_delta_t p, const fftc
     if (e != FFTCONV_OK) return e;
     const DeltaArgs& d = a.d;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((d.nseq == 0 && !d.offsets) || d.Hv == 0) return FFTCONV_OK;
+    if (d.Hv == 0) {  // no value head uses the queries and keys
+        if (!d.B || !d.T || !d.Hk) return FFTCONV_OK;
+        View v[2];
+        if ((e = take_view(dq, d.B, d.T, d.Hk, p->Dk, &v[0])) != FFTCONV_OK) return e;
+        if ((e = take_view(dk, d.B, d.T, d.Hk, p->Dk, &v[1])) != FFTCONV_OK) return e;
+        const int H[2] = {d.Hk, d.Hk}, D[2] = {p->Dk, p->Dk};
+        a.d.nseq = 0;
+        return done(zero_gaps(d, 2, v, H, D, st));
+    }
+    if (d.nseq == 0 && !d.offsets) return FFTCONV_OK;
     if (off16(d_state_out) || off16(d_state_in) || off16(saved) || off16(scratch)) return FFTCONV_ERR_ALIGN;
     const size_t sb = state_bytes(p, d.nseq, d.Hv);
     const bool any = d.B && d.T;

@@ -453,8 +453,9 @@ typedef struct {
  *   S_t = S~ + k_t u_t^T
  *   o_t = scale * S_t^T q_t
  * q, k: [B][T][Hk][Dk]; v, o: [B][T][Hv][Dv]; g (the log of the decay, <= 0)
- * and beta: [B][T][Hv]; all in the plan dtype.  Hv is a multiple of Hk: value
- * head h uses query/key head h / (Hv / Hk).  Dk and Dv are 64 or 128.  g is
+ * and beta: [B][T][Hv]; all in the plan dtype.  Hv is a multiple of Hk (0: no
+ * outputs, and gradients of q and k that are zero): value head h uses query/key
+ * head h / (Hv / Hk).  Dk and Dv are 64 or 128.  g is
  * taken as max(g, -120): exp(-120) is zero in float32, so a log decay of
  * -infinity (a reset of the state) needs no special case.  Keys of norm at
  * most 1 and beta in [0, 1] keep the recurrence bounded; fp16 intermediates

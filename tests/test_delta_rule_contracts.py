@@ -1,4 +1,5 @@
-"""What the gated delta rule promises beside its values: overlaps."""
+"""What the gated delta rule promises beside its values: overlaps, calls without
+value heads."""
 import ctypes
 
 import pytest
@@ -38,3 +39,22 @@ def test_scratch_and_state_gradient_over_outputs_are_refused(over):
         scratch = torch.zeros(need, dtype=torch.uint8, device="cuda")
         assert call(scratch.data_ptr(), at[:-16].data_ptr() - 64) == 1
         torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,offsets", [(2, None), (1, None), (1, [3, 20])])
+def test_no_value_heads(B, offsets):
+    """Queries and keys that no value head uses have zero gradients."""
+    dt, T, Hk, D = torch.bfloat16, 30, 2, 64
+    q, k, v, g, beta = (x.cuda() for x in delta_inputs(B, T, Hk, Hk, D, D, dt))
+    v, g, beta = v[:, :, :0], g[:, :, :0], beta[:, :, :0]
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32).cuda()
+    plan = F.DeltaRule(D, D, dt)
+    o, s, saved = plan.forward(q, k, v, g, beta, offsets=off, save=True)
+    assert o.shape == v.shape and s.shape == (B, 0, D, D)
+    for _ in range(2):
+        # what the allocator hands out next is not zero
+        keep = [torch.full((B, T, Hk, D), 3.0, dtype=dt, device="cuda") for _ in range(4)]
+        del keep
+        got = plan.backward(o, q, k, v, g, beta, saved, offsets=off)
+        assert got[0].shape == q.shape and not bool(got[0].any()) and not bool(got[1].any())
