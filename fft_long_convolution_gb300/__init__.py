@@ -432,13 +432,16 @@ def _device(t, what: str) -> int:
     return dev
 
 
+def _elsewhere(t, dev) -> bool:
+    """Whether t is not on GPU dev (None: any)."""
+    return not t.is_cuda if dev is None else t.get_device() != dev
+
+
 def _strides(t, what: str, dtype, shape, dev=None):
-    """A tensor's address and its first three strides, checked against dtype, shape and (if given) GPU."""
+    """A tensor's address and its first three strides, checked against dtype, shape and GPU."""
     st = t.stride()
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or (len(st) == 4 and st[3] != 1 and shape[3] > 1):
-        raise ValueError(f"{what} must be a CUDA {dtype} tensor of shape {tuple(shape)}, contiguous in its features")
-    if dev is not None and t.get_device() != dev:
-        raise ValueError(f"{what} is on another GPU than the call's first tensor")
+    if t.shape != shape or t.dtype is not dtype or _elsewhere(t, dev) or (len(st) == 4 and st[3] != 1 and shape[3] > 1):
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} on the call's GPU, contiguous in its features")
     return (t.data_ptr(), *st[:3])
 
 
@@ -450,13 +453,11 @@ def _new(t):
 
 
 def _dense(t, what: str, dtype, shape, dev=None) -> int:
-    """The address of a contiguous CUDA tensor of the given shape (None: 0)."""
+    """The address of a contiguous tensor of the given shape and GPU (None: 0)."""
     if t is None:
         return 0
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
-    if dev is not None and t.get_device() != dev:
-        raise ValueError(f"{what} is on another GPU than the call's first tensor")
+    if t.shape != shape or t.dtype is not dtype or _elsewhere(t, dev) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the call's GPU")
     return t.data_ptr()
 
 
@@ -511,7 +512,7 @@ class DeltaRule:
             nseq = offsets.numel() - 1
             off = _dense(offsets, "offsets", torch.int32, offsets.shape, dev)
         return DeltaArgs.from_buffer_copy(_DELTA_ARGS.pack(
-            B, T, Hk, Hv, nseq, off, self._scale if scale is None else scale, *_strides(q, "q", dt, qs),
+            B, T, Hk, Hv, nseq, off, self._scale if scale is None else scale, *_strides(q, "q", dt, qs, dev),
             *_strides(k, "k", dt, qs, dev), *_strides(v, "v", dt, (B, T, Hv, self.Dv), dev),
             *_strides(g, "g", dt, gs, dev), *_strides(beta, "beta", dt, gs, dev)))
 
@@ -615,7 +616,7 @@ class QKNorm:
             pp = _dense(positions, "positions", torch.int32, (B, T), dev)
         return QKNormArgs.from_buffer_copy(_NORM_ARGS.pack(
             self._code, self._norm, D, R, self.interleaved, self.eps, B, T, Hq, Hk,
-            *_strides(q, "q", dt, (B, T, Hq, D)), *_strides(k, "k", dt, (B, T, Hk, D), dev),
+            *_strides(q, "q", dt, (B, T, Hq, D), dev), *_strides(k, "k", dt, (B, T, Hk, D), dev),
             _dense(wq, "wq", f32, (D,), dev), _dense(wk, "wk", f32, (D,), dev), pc, ps, rows, pp))
 
     def forward(self, q, k, wq=None, wk=None, cos=None, sin=None, positions=None, qo=None, ko=None, stream=None):
