@@ -16,14 +16,16 @@
 //
 // Precision: the state is float32; products that feed it take it, W, T and
 // (e Vn) as two 16-bit values each (high and low part; the low x low product
-// is dropped), so the state is good to about 2^-17 per chunk while K and V are
-// exact.  Products that only feed O (Q S, P Vn) take one 16-bit value: O is
-// rounded to 16 bits anyway.
+// is dropped), so the state is good to about 2^-17 per chunk (fp16: 2^-19) while K
+// and V are exact.  In fp16 a low part below 2^-14 is subnormal: an entry of size x is
+// good to 2^-25 / x at best (values of 1e-3: states 1e-4, outputs 2 roundings off).
+// Products that only feed O (Q S, P Vn) take one 16-bit value: O is rounded to 16 bits
+// anyway.
 //
 // Two kernels.  delta_prep_kernel forms what does not depend on S -- T, W, P
 // and the decays -- for all chunks side by side, and leaves them as images of
 // the shared-memory tiles that delta_fwd_kernel fetches with one bulk copy a
-// chunk (57 KB at Dk = 128, next to the 48 KB of K, Q and V).  delta_fwd_kernel
+// chunk (58 kB at Dk = 128, next to the 49 kB of K, Q and V).  delta_fwd_kernel
 // walks the chunks: one CTA per sequence (or segment of one) and value head,
 // roles by warp, handing tiles over through mbarriers:
 //   warps 0-15   chain: S (float32 -> operands, decayed in place), Vn and O^T, a
@@ -38,8 +40,11 @@
 // (8 x 4096 tokens, 6 heads, 48 CTAs: 130 us; 149 us when it also stores what the
 // backward needs), of which the products take 1 us and the conversions of S, two
 // parts of 16384 values, 0.3 us of the four schedulers.  Where segments fill the SMs
-// the bound is HBM (262144 tokens, 6 heads: the outputs' walks 445 us, 105 KB a chunk,
-// 5.8 TB/s; the states' 592 us, 123 KB, 5.1 TB/s).
+// (262144 tokens, 6 heads of 128, 24576 chunks) the outputs' walks are bound by HBM: 450
+// us, 108 kB read and 16 kB written a chunk, 6.8 TB/s, a copy's rate.  The states' walks
+// are bound by both: 282 CTAs take two waves of 164 chunks, 1.8 us a chunk, and move
+// 126 kB a chunk (83 the state, 50 the transition, none for the last segments) in 592
+// us, 5.2 TB/s.
 #include "delta_chunk.h"
 
 #include "chunk.cuh"
@@ -189,8 +194,8 @@ struct PrepCfg {
 };
 
 // T, W, P and the decays of one chunk and value head at a time.  Bound: HBM at
-// Dk = 128 (32 KB of K and Q in, 57 KB of images out; 8 x 4096 tokens, 6 heads:
-// 53 us, 5.2 TB/s, 76 % of a plain copy's rate), the latency of its steps at
+// Dk = 128 (33 kB of K and Q in, 59 kB of images out; 8 x 4096 tokens, 6 heads:
+// 54 us, 5.2 TB/s, 76 % of a plain copy's rate), the latency of its steps at
 // Dk = 64 (each waits for the last, the inverse's levels most of all).  Hence four
 // CTAs per SM, and the next chunk's tiles and gates fetched under the current
 // one's last steps.
@@ -1065,7 +1070,9 @@ cudaError_t launch(const ChunkArgs& a, cudaStream_t st) {
 // one more and 12 for the rest of it, and cuts when that saves a tenth.  One row
 // of 262144 tokens, 6 heads of 128: 25 segments, 1.1 ms in walks and join instead
 // of 8.3 ms; 8 rows of 4096: 3 segments took 148 us against 130 us uncut, and stay
-// uncut.  Packed rows are taken at their mean length.
+// uncut.  Packed rows are taken at their mean length, as the host does not know their
+// offsets: one prompt of 60000 tokens among 31 of 178 stays uncut, 1.93 ms where it
+// takes 0.45 ms alone.
 void plan_segments(ChunkArgs* a, int sms) {
     const DeltaArgs& d = a->d;
     a->slots = chunk_slots(d.B, d.T, d.nseq);

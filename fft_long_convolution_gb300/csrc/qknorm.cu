@@ -340,9 +340,9 @@ void launch_dt(const NormArgs& a, int mode, bool vec, int G, int HB, int grid, c
 }
 
 // CTAs at most.  The forward takes a CTA per few tokens (8 x 16384 tokens of
-// 12 heads of 128: 151 us, 5.3 TB/s; a resident grid that fetches ahead took
+// 12 heads of 128: 153 us, 5.3 TB/s; a resident grid that fetches ahead took
 // 225 us); the backward keeps its grid small, as each CTA leaves a partial sum of
-// the weights' gradients (236 us, 5.1 TB/s).
+// the weights' gradients (240 us, 5.0 TB/s).
 constexpr int kMaxGrid = 152 * 4, kMaxGridForward = 1 << 24;
 
 fftconv_status_t check_args(const fftconv_qknorm_args_t* p) {
@@ -438,8 +438,8 @@ fftconv_status_t run(const fftconv_qknorm_args_t* p, const fftconv_view_t* dy, c
     // As few parts of a token's heads as fill a quarter of the GPU's threads: one for
     // whole batches, one per head for single tokens.  A part waits for the weights, the
     // position and its table rows before its first row: 8 x 4096 tokens of 18 heads of
-    // 64 in three parts took 51.6 us, in one 35.5 us; 5115 tokens of 12 heads of 80 in
-    // six parts 11.3 us, in one 8.6 us.
+    // 64 in three parts took 1.45 times as long as in one (30.0 us); 5115 tokens of 12
+    // heads of 80 in six parts 1.3 times as long as in one (8.9 us).
     const int total = a.Hq + a.Hk;
     const int64_t want_parts = (int64_t(1) * 152 * 512 + tokens * G - 1) / (tokens * G);
     a.per = int((total + want_parts - 1) / want_parts);
