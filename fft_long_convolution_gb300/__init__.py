@@ -29,7 +29,10 @@ EXPORTED = ["fftconv_plan_query", "fftconv_plan_create", "fftconv_plan_destroy",
             "fftconv_plan_create_circular", "fftconv_delta_create", "fftconv_delta_destroy",
             "fftconv_delta_status", "fftconv_delta_saved_bytes", "fftconv_delta_scratch_bytes",
             "fftconv_delta_forward", "fftconv_delta_backward", "fftconv_delta_step", "fftconv_qknorm_forward",
-            "fftconv_qknorm_scratch_bytes", "fftconv_qknorm_backward",
+            "fftconv_qknorm_scratch_bytes", "fftconv_qknorm_backward", "fftconv_linattn_create",
+            "fftconv_linattn_destroy", "fftconv_linattn_status", "fftconv_linattn_scratch_bytes",
+            "fftconv_linattn_forward", "fftconv_linattn_backward", "fftconv_linattn_step",
+            "fftconv_layernorm_forward", "fftconv_layernorm_scratch_bytes", "fftconv_layernorm_backward",
             "fftconv_device_status", "fftconv_status_string", "fftconv_version"]
 
 
@@ -70,6 +73,18 @@ class QKNormArgs(ctypes.Structure):
                 ("q", View), ("k", View), ("wq", ctypes.c_void_p), ("wk", ctypes.c_void_p),
                 ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("table_rows", ctypes.c_int64),
                 ("positions", ctypes.c_void_p)]
+
+
+class LinAttnArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hk", ctypes.c_int64), ("Hv", ctypes.c_int64),
+                ("nseq", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("decay", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("q", View), ("k", View), ("v", View)]
+
+
+class LayerNormArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("D", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int64), ("x", View),
+                ("w", ctypes.c_void_p), ("b", ctypes.c_void_p)]
 
 
 _lib = None
@@ -138,6 +153,19 @@ def lib(auto_build: bool = True):
         L.fftconv_qknorm_scratch_bytes.argtypes = [qa]
         L.fftconv_qknorm_scratch_bytes.restype = sz
         L.fftconv_qknorm_backward.argtypes = [qa, View, View, View, View, vp, vp, vp, sz, vp]
+        la, ln = ctypes.POINTER(LinAttnArgs), ctypes.POINTER(LayerNormArgs)
+        L.fftconv_linattn_create.argtypes = [ctypes.POINTER(vp), cint, cint, cint]
+        L.fftconv_linattn_destroy.argtypes = [vp]
+        L.fftconv_linattn_status.argtypes = [vp, vp, ctypes.POINTER(cint)]
+        L.fftconv_linattn_scratch_bytes.argtypes = [vp, i64, i64, i64, i64, i64, cint]
+        L.fftconv_linattn_scratch_bytes.restype = sz
+        L.fftconv_linattn_forward.argtypes = [vp, la, vp, View, vp, vp, sz, vp]
+        L.fftconv_linattn_backward.argtypes = [vp, la, vp, View, vp, View, View, View, vp, vp, sz, vp]
+        L.fftconv_linattn_step.argtypes = [vp, la, vp, vp, i64, vp, View, vp]
+        L.fftconv_layernorm_forward.argtypes = [ln, View, vp]
+        L.fftconv_layernorm_scratch_bytes.argtypes = [ln]
+        L.fftconv_layernorm_scratch_bytes.restype = sz
+        L.fftconv_layernorm_backward.argtypes = [ln, View, View, vp, vp, vp, sz, vp]
         L.fftconv_device_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_int)]
         L.fftconv_status_string.argtypes = [ctypes.c_int]
         L.fftconv_status_string.restype = ctypes.c_char_p
@@ -416,6 +444,8 @@ def status_string(code: int) -> str:
 
 _DELTA_ARGS = struct.Struct("=5qQf4x" + "Q3q" * 5)
 _NORM_ARGS = struct.Struct("=5if4q" + "Q3q" * 2 + "4QqQ")
+_LINATTN_ARGS = struct.Struct("=5qQQf4x" + "Q3q" * 3)
+_LAYERNORM_ARGS = struct.Struct("=2if4x3q" + "Q3q" + "2Q")
 
 
 def _current_device() -> int:
@@ -654,3 +684,189 @@ class QKNorm:
         _check(lib().fftconv_qknorm_backward(args, vdq, vdk, oq, ok, _ptr(dwq), _ptr(dwk), _ptr(scratch), n,
                                              _stream(None)), "fftconv_qknorm_backward")
         return dq, dk, dwq, dwk
+
+
+class LinearAttention:
+    """Linear attention with a fixed decay for each head, for head sizes Dk, Dv
+    (64 or 128) and one dtype:
+
+        S = exp(decay) S + k_t v_t^T;  o_t = scale S^T q_t
+
+    q, k: [B, T, Hk, Dk]; v: [B, T, Hv, Dv]; decay: float32 [Hv], logarithms
+    (taken as at most 0; constants of the layer, without a gradient); Hv a
+    multiple of Hk.  States: float32 [sequences, Hv, Dk, Dv].  offsets: int32
+    [n + 1] on the GPU for n sequences packed into one row (B = 1).  scale
+    defaults to Dk ** -0.5."""
+
+    def __init__(self, Dk: int, Dv: int, dtype):
+        self.Dk, self.Dv, self.torch_dtype = int(Dk), int(Dv), dtype
+        self._scale = self.Dk ** -0.5
+        h = ctypes.c_void_p()
+        _check(lib().fftconv_linattn_create(ctypes.byref(h), self.Dk, self.Dv, _dtype_code(dtype)),
+               "fftconv_linattn_create")
+        self._h = h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().fftconv_linattn_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _args(self, q, k, v, decay, offsets, scale) -> LinAttnArgs:
+        import torch
+        dt = self.torch_dtype
+        if q.dim() != 4 or v.dim() != 4 or q.shape[3] != self.Dk:
+            raise ValueError("q, k must be [B, T, Hk, Dk] and v [B, T, Hv, Dv]")
+        B, T, Hk, _ = qs = q.shape
+        Hv = v.shape[2]
+        dev = _device(q, "q")
+        nseq, off = B, 0
+        if offsets is not None:
+            if offsets.dim() != 1 or offsets.numel() < 1:
+                raise ValueError("offsets must be [n + 1]")
+            nseq = offsets.numel() - 1
+            off = _dense(offsets, "offsets", torch.int32, offsets.shape, dev)
+        if decay is None:
+            raise ValueError("decay must be float32 [Hv]")
+        return LinAttnArgs.from_buffer_copy(_LINATTN_ARGS.pack(
+            B, T, Hk, Hv, nseq, off, _dense(decay, "decay", torch.float32, (Hv,), dev),
+            self._scale if scale is None else scale, *_strides(q, "q", dt, qs, dev), *_strides(k, "k", dt, qs, dev),
+            *_strides(v, "v", dt, (B, T, Hv, self.Dv), dev)))
+
+    def _scratch(self, a, backward, device):
+        import torch
+        n = int(lib().fftconv_linattn_scratch_bytes(self._h, a.B, a.T, a.Hk, a.Hv, a.nseq, backward))
+        return (torch.empty(n, dtype=torch.uint8, device=device) if n else None), n
+
+    def forward(self, q, k, v, decay, state=None, offsets=None, scale=None, stream=None):
+        """Whole sequences from `state` (None: zero) -> (o, final states)."""
+        import torch
+        if stream is not None:
+            with _on(stream):
+                return self.forward(q, k, v, decay, state, offsets, scale)
+        a = self._args(q, k, v, decay, offsets, scale)
+        shape = (a.nseq, a.Hv, self.Dk, self.Dv)
+        sin = _dense(state, "state", torch.float32, shape, q.get_device())
+        o, vo = _new(v)
+        out = torch.empty(shape, dtype=torch.float32, device=v.device)
+        scratch, n = self._scratch(a, 0, v.device)
+        _check(lib().fftconv_linattn_forward(self._h, ctypes.byref(a), sin, vo, out.data_ptr(), _ptr(scratch), n,
+                                             _stream(None)), "fftconv_linattn_forward")
+        return o, out
+
+    def backward(self, do, q, k, v, decay, state=None, dstate=None, offsets=None, scale=None, stream=None):
+        """Gradients (dq, dk, dv, gradient of the initial states) from do
+        [B, T, Hv, Dv] and, if the final states were used, dstate; the other
+        arguments as in forward, which keeps nothing for this call."""
+        import torch
+        if stream is not None:
+            with _on(stream):
+                return self.backward(do, q, k, v, decay, state, dstate, offsets, scale)
+        a = self._args(q, k, v, decay, offsets, scale)
+        dev = q.get_device()
+        shape = (a.nseq, a.Hv, self.Dk, self.Dv)
+        sin = _dense(state, "state", torch.float32, shape, dev)
+        dsin = _dense(dstate, "dstate", torch.float32, shape, dev)
+        vdo = View(*_strides(do, "do", self.torch_dtype, v.shape, dev))
+        (dq, oq), (dk, ok), (dv, ov) = _new(q), _new(k), _new(v)
+        dst = torch.empty(shape, dtype=torch.float32, device=v.device)
+        scratch, n = self._scratch(a, 1, v.device)
+        _check(lib().fftconv_linattn_backward(self._h, ctypes.byref(a), sin, vdo, dsin, oq, ok, ov, dst.data_ptr(),
+                                              _ptr(scratch), n, _stream(None)), "fftconv_linattn_backward")
+        return dq, dk, dv, dst
+
+    def step(self, q, k, v, decay, state, state_out=None, slots=None, scale=None, stream=None):
+        """The recurrent form: B rows of a few tokens, row b against
+        state[slots[b]] (slots: int32 [B] on the GPU, distinct; None: state[b])
+        -> o.  The updated states go to state_out, by default back to state."""
+        import torch
+        if stream is not None:
+            with _on(stream):
+                return self.step(q, k, v, decay, state, state_out, slots, scale)
+        a = self._args(q, k, v, decay, None, scale)
+        shape, dev = (state.shape[0], v.shape[2], self.Dk, self.Dv), q.get_device()
+        sin = _dense(state, "state", torch.float32, shape, dev)
+        sout = sin if state_out is None else _dense(state_out, "state_out", torch.float32, shape, dev)
+        sl = _dense(slots, "slots", torch.int32, (q.shape[0],), dev)
+        o, vo = _new(v)
+        _check(lib().fftconv_linattn_step(self._h, ctypes.byref(a), sin, sout, shape[0], sl, vo, _stream(None)),
+               "fftconv_linattn_step")
+        return o
+
+    def device_status(self, stream=None) -> int:
+        v = ctypes.c_int()
+        _check(lib().fftconv_linattn_status(self._h, _stream(stream), ctypes.byref(v)), "fftconv_linattn_status")
+        return v.value
+
+
+class LayerNorm:
+    """Layer norm of rows of D features:
+
+        y = (x - mean) / sqrt(var + eps) * w + b
+
+    x: [N, D] or [B, T, D] (rows of a hidden state) with w, b float32 [D], or
+    [B, T, H, D] (a mixer's heads, normed one by one) with w, b float32 [H, D];
+    either may be None (ones, zeros)."""
+
+    def __init__(self, D: int, dtype, eps: float = 1e-5):
+        self.D, self.torch_dtype, self.eps = int(D), dtype, float(eps)
+        self._code = _dtype_code(dtype)
+
+    def _view(self, t, what, shape, dev):
+        """A tensor's address and its batch, token and head strides."""
+        st = t.stride()
+        if t.shape != shape or t.dtype is not self.torch_dtype or t.get_device() != dev or (st[-1] != 1 and shape[-1] > 1):
+            raise ValueError(f"{what} must be a {self.torch_dtype} tensor of shape {tuple(shape)} on the call's GPU, "
+                             "contiguous in its features")
+        n = len(st)
+        if n == 4:
+            return t.data_ptr(), st[0], st[1], st[2]
+        return (t.data_ptr(), st[0], st[1], self.D) if n == 3 else (t.data_ptr(), self.D, st[0], self.D)
+
+    def _args(self, x, w, b) -> LayerNormArgs:
+        import torch
+        shape, n, D = x.shape, x.dim(), self.D
+        if n < 2 or n > 4 or shape[-1] != D:
+            raise ValueError("x must be [N, D], [B, T, D] or [B, T, H, D]")
+        dev = _device(x, "x")
+        B, T, H = (1, shape[0], 1) if n == 2 else (shape[0], shape[1], shape[2] if n == 4 else 1)
+        ws = (H, D) if n == 4 else (D,)
+        return LayerNormArgs.from_buffer_copy(_LAYERNORM_ARGS.pack(
+            self._code, D, self.eps, B, T, H, *self._view(x, "x", shape, dev),
+            _dense(w, "w", torch.float32, ws, dev), _dense(b, "b", torch.float32, ws, dev)))
+
+    def forward(self, x, w=None, b=None, y=None, stream=None):
+        """The normed rows.  y: where to write (x itself is allowed)."""
+        import torch
+        if stream is not None:
+            with _on(stream):
+                return self.forward(x, w, b, y)
+        a = self._args(x, w, b)
+        if y is None:
+            y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        vy = View(*self._view(y, "y", x.shape, x.get_device()))
+        _check(lib().fftconv_layernorm_forward(ctypes.byref(a), vy, _stream(None)), "fftconv_layernorm_forward")
+        return y
+
+    def backward(self, dy, x, w=None, b=None, stream=None):
+        """Gradients (dx, dw, db) from that of forward's output; dw (db) is
+        None where w (b) is."""
+        import torch
+        if stream is not None:
+            with _on(stream):
+                return self.backward(dy, x, w, b)
+        a = self._args(x, w, b)
+        vdy = View(*self._view(dy, "dy", x.shape, x.get_device()))
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+        vdx = View(*self._view(dx, "dx", x.shape, x.get_device()))
+        dw, db = (None if t is None else torch.empty_like(t) for t in (w, b))
+        n = int(lib().fftconv_layernorm_scratch_bytes(ctypes.byref(a))) if (w is not None or b is not None) else 0
+        scratch = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+        _check(lib().fftconv_layernorm_backward(ctypes.byref(a), vdy, vdx, _ptr(dw), _ptr(db), _ptr(scratch), n,
+                                                _stream(None)), "fftconv_layernorm_backward")
+        return dx, dw, db

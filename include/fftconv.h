@@ -427,7 +427,7 @@ fftconv_status_t fftconv_device_status(fftconv_plan_t plan, fftconv_stream_t str
 fftconv_status_t fftconv_selftest_wait(fftconv_plan_t plan, int sleep, fftconv_stream_t stream);
 
 /* ------------------------------------------------------------------------
- * Token mixers with a state.  The two operators below work on token-major
+ * Token mixers with a state, and norms.  The operators below work on token-major
  * tensors [B][T][H][D] (the order in which projections write them), given as
  * strided views; D is contiguous.
  * ------------------------------------------------------------------------ */
@@ -613,6 +613,127 @@ fftconv_status_t fftconv_qknorm_backward(const fftconv_qknorm_args_t *args, fftc
                                          fftconv_view_t dyk, fftconv_view_t dq, fftconv_view_t dk,
                                          float *dwq, float *dwk, void *scratch, size_t scratch_bytes,
                                          fftconv_stream_t stream);
+
+/*
+ * Linear attention with a fixed decay for each head.  Per sequence and value
+ * head h, with l = exp(decay[h]), the state S [Dk][Dv] (float32) follows, token
+ * by token,
+ *   S_t = l S_(t-1) + k_t v_t^T
+ *   o_t = scale * S_t^T q_t
+ * q, k: [B][T][Hk][Dk]; v, o: [B][T][Hv][Dv], in the plan dtype.  Hv is a
+ * multiple of Hk (0: no outputs, and gradients of q and k that are zero): value
+ * head h uses query/key head h / (Hv / Hk).  Dk and Dv are 64 or 128.  decay:
+ * float32 [Hv] on the device, logarithms, taken as min(max(x, -120), 0): 0 keeps
+ * everything, -infinity only the token itself.  It is a constant of the layer
+ * and has no gradient (fftconv_delta_* has decays for each token, with theirs).
+ * Sequences and offsets as for the gated delta rule.
+ */
+typedef struct fftconv_linattn_s *fftconv_linattn_t;
+
+typedef struct {
+    int64_t B, T, Hk, Hv;
+    int64_t nseq;
+    const int32_t *offsets; /* device, or NULL */
+    const float *decay;     /* device */
+    float scale;
+    fftconv_view_t q, k, v;
+} fftconv_linattn_args_t;
+
+/*
+ * A plan holds the kernels' launch preparation for one (Dk, Dv, dtype) and a
+ * device error word; it is immutable and may be used from several streams at
+ * once.  Returns OK, INVALID, UNSUPPORTED (Dk, Dv not 64 or 128, dtype),
+ * ALLOC or CUDA.
+ */
+fftconv_status_t fftconv_linattn_create(fftconv_linattn_t *out, int Dk, int Dv, fftconv_dtype_t dtype);
+fftconv_status_t fftconv_linattn_destroy(fftconv_linattn_t plan);
+
+/* As fftconv_device_status: read and clear the plan's error word. */
+fftconv_status_t fftconv_linattn_status(fftconv_linattn_t plan, fftconv_stream_t stream, int *out);
+
+/* Bytes of scratch of a forward (backward = 0) or a backward (1) of these
+ * sizes; 0 if plan is NULL or a size is negative. */
+size_t fftconv_linattn_scratch_bytes(fftconv_linattn_t plan, int64_t B, int64_t T, int64_t Hk, int64_t Hv,
+                                     int64_t nseq, int backward);
+
+/*
+ * Whole sequences (training, prompts).  state_in: float32 [nseq][Hv][Dk][Dv]
+ * or NULL (zero); state_out: the same shape, or NULL.  o, state_out and scratch
+ * must not overlap the inputs or one another (checked by address range;
+ * INVALID).  Returns OK, INVALID, UNSUPPORTED (sizes past 32-bit grids), ALIGN,
+ * WORKSPACE (scratch missing or too small) or CUDA.
+ */
+fftconv_status_t fftconv_linattn_forward(fftconv_linattn_t plan, const fftconv_linattn_args_t *args,
+                                         const float *state_in, fftconv_view_t o, float *state_out, void *scratch,
+                                         size_t scratch_bytes, fftconv_stream_t stream);
+
+/*
+ * Gradients of fftconv_linattn_forward with the same args and state_in; d_o
+ * [B][T][Hv][Dv] is the gradient of o, d_state_out float32 [nseq][Hv][Dk][Dv]
+ * that of the final states or NULL (zero).  Nothing is kept by the forward.
+ * Writes dq, dk [B][T][Hk][Dk], dv [B][T][Hv][Dv] (plan dtype) and, unless NULL,
+ * d_state_in float32 [nseq][Hv][Dk][Dv].  No atomics: the result is bitwise
+ * reproducible.  Outputs and scratch must not overlap the inputs, d_state_in and
+ * scratch no output either (checked by address range; INVALID); the tokens'
+ * gradients may be slices of one buffer, and that they are disjoint is not
+ * checked.  Returns as fftconv_linattn_forward.
+ */
+fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t plan, const fftconv_linattn_args_t *args,
+                                          const float *state_in, fftconv_view_t d_o, const float *d_state_out,
+                                          fftconv_view_t dq, fftconv_view_t dk, fftconv_view_t dv,
+                                          float *d_state_in, void *scratch, size_t scratch_bytes,
+                                          fftconv_stream_t stream);
+
+/*
+ * The recurrent form (decoding): B rows of T tokens (few; any T is valid),
+ * each against one state of a pool float32 [nslots][Hv][Dk][Dv], as
+ * fftconv_delta_step: row b uses slot slots[b] (device int32 [B], distinct), or
+ * slot b when slots is NULL; a row whose slot is negative or >= nslots gets zero
+ * outputs and touches no state; state_out == state_in updates in place, other
+ * overlaps are INVALID; slots that no row uses are not touched.  args->offsets
+ * must be NULL.  Float32 throughout.  Returns OK, INVALID, UNSUPPORTED, ALIGN or
+ * CUDA.
+ */
+fftconv_status_t fftconv_linattn_step(fftconv_linattn_t plan, const fftconv_linattn_args_t *args,
+                                      const float *state_in, float *state_out, int64_t nslots,
+                                      const int32_t *slots, fftconv_view_t o, fftconv_stream_t stream);
+
+/*
+ * Layer norm of rows of D features:
+ *   m = mean_d x, r = 1 / sqrt(mean_d (x - m)^2 + eps), y = (x - m) r w + b
+ * x, y: [B][T][H][D] in the plan dtype (H = 1: rows of a hidden state; else the
+ * heads of a mixer, normed one by one); w, b: float32 [H][D], or NULL (ones,
+ * zeros).  D is a multiple of 8 up to 8192; at most 65535 heads and fewer than
+ * 2^30 rows.  Arithmetic in float32 (the variance from differences to the mean),
+ * one rounding at the end.  A NaN or an infinity reaches its own row only (and
+ * the weights' gradients).  y may be the same view as x (in place); otherwise it
+ * shares no element with x, told apart as in fftconv_qknorm_forward, and
+ * overlaps no weight.
+ */
+typedef struct {
+    int32_t dtype; /* fftconv_dtype_t */
+    int32_t D;
+    float eps;
+    int64_t B, T, H;
+    fftconv_view_t x;
+    const float *w, *b;
+} fftconv_layernorm_args_t;
+
+/* Returns OK, INVALID, UNSUPPORTED (D, dtype, sizes), ALIGN or CUDA. */
+fftconv_status_t fftconv_layernorm_forward(const fftconv_layernorm_args_t *args, fftconv_view_t y,
+                                           fftconv_stream_t stream);
+
+/*
+ * Gradients: dy of y gives dx (plan dtype; may be the same view as x or dy) and
+ * dw, db (float32 [H][D], sums over all tokens, overwritten; NULL: not wanted).
+ * b is not read.  scratch: fftconv_layernorm_scratch_bytes(args) bytes, 16-byte
+ * aligned; may be NULL when dw and db are.  dw, db and scratch overlap nothing.
+ * Bitwise reproducible.  Returns as the forward, and WORKSPACE.
+ */
+size_t fftconv_layernorm_scratch_bytes(const fftconv_layernorm_args_t *args);
+fftconv_status_t fftconv_layernorm_backward(const fftconv_layernorm_args_t *args, fftconv_view_t dy,
+                                            fftconv_view_t dx, float *dw, float *db, void *scratch,
+                                            size_t scratch_bytes, fftconv_stream_t stream);
 
 /* Static English text for a status code (never NULL). */
 const char *fftconv_status_string(fftconv_status_t s);
