@@ -14,7 +14,7 @@ LIB_NAME = "libfftconv_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 SOURCES = ["fftconv.cu", "mp_l16k.cu", "mp_l4k.cu", "mp_l16k_sparse.cu", "mp_l4k_sparse.cu", "mp_circ.cu",
            "delta.cu", "delta_chunk.cu", "delta_grad.cu", "qknorm.cu", "linattn.cu",
-           "layernorm.cu"]  # compiled in parallel, then linked
+           "linattn_chunk.cu", "layernorm.cu"]  # compiled in parallel, then linked
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 _lock = threading.Lock()
 

@@ -1,6 +1,6 @@
 // Linear attention with a fixed decay for each head: C entry points and the
 // token-by-token kernels.
-#include "linattn.h"
+#include "linattn_chunk.h"
 
 #include <new>
 
@@ -103,91 +103,6 @@ __global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
     for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(a.sout + sbase + r * DV) = S[r];
 }
 
-// Whole sequences token by token, a CTA per sequence, head and 32 columns.
-template <int DT, int DK, int DV>
-__global__ void __launch_bounds__(128) walk_kernel(const Walk a) {
-    constexpr int RP = DK / 16;
-    __shared__ float4 red[2][4][8];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int cg = lane % 8, rg = warp * 4 + lane / 8;
-    const int h = blockIdx.y, col = blockIdx.z * 32 + cg * 4;
-    const int i = blockIdx.x;
-    const Seq s = locate(a.offsets, a.T, i);
-    auto at = [&](const View& x, int hh) { return reinterpret_cast<uint16_t*>(x.p) + s.row * x.b + s.start * x.t + hh * x.h; };
-    const uint16_t* kp = at(a.k, h / a.gk) + rg * RP;
-    const uint16_t* qp = at(a.q, h / a.gq) + rg * RP;
-    const uint16_t* vp = at(a.v, h / a.gv) + col;
-    uint16_t* op = a.o32 ? nullptr : at(a.o, h) + col;
-    const int64_t sb = (int64_t(i) * a.H + h) * DK * DV;
-    float4 S[RP];
-    #pragma unroll
-    for (int r = 0; r < RP; ++r) {
-        const int row = rg * RP + r;
-        S[r] = make_float4(0, 0, 0, 0);
-        if (!a.state_in) continue;
-        const float* p = a.state_in + sb;
-        S[r] = a.turned ? make_float4(p[col * DK + row], p[(col + 1) * DK + row], p[(col + 2) * DK + row], p[(col + 3) * DK + row])
-                        : *reinterpret_cast<const float4*>(p + row * DV + col);
-    }
-    const Decay al = decay_over(head_decay(a.decay, h), 1.0f);
-    auto lose = [&](const float4& x) {
-        return make_float4(decayed(al, x.x, 0), decayed(al, x.y, 0), decayed(al, x.z, 0), decayed(al, x.w, 0));
-    };
-    for (int64_t n = 0; n < s.len; ++n) {
-        const int64_t t = a.reverse ? s.len - 1 - n : n;
-        float k[RP], q[RP], v[4], qk = 0.0f;
-        #pragma unroll
-        for (int r = 0; r < RP; r += 4) {
-            unpack4<DT>(*reinterpret_cast<const uint2*>(kp + t * a.k.t + r), k + r);
-            unpack4<DT>(*reinterpret_cast<const uint2*>(qp + t * a.q.t + r), q + r);
-        }
-        unpack4<DT>(*reinterpret_cast<const uint2*>(vp + t * a.v.t), v);
-        float4 y = make_float4(0, 0, 0, 0);
-        #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-            if (!a.reverse) S[r] = lose(S[r]);
-            const float qs = q[r] * a.s_in;
-            qk = fmaf(q[r], k[r], qk);
-            y.x = fmaf(qs, S[r].x, y.x);
-            y.y = fmaf(qs, S[r].y, y.y);
-            y.z = fmaf(qs, S[r].z, y.z);
-            y.w = fmaf(qs, S[r].w, y.w);
-            const float ku = k[r] * a.s_up;
-            S[r].x = fmaf(ku, v[0], S[r].x);
-            S[r].y = fmaf(ku, v[1], S[r].y);
-            S[r].z = fmaf(ku, v[2], S[r].z);
-            S[r].w = fmaf(ku, v[3], S[r].w);
-            if (a.reverse) S[r] = lose(S[r]);
-        }
-        qk *= a.s_p;
-        y.x = fmaf(qk, v[0], y.x); y.y = fmaf(qk, v[1], y.y); y.z = fmaf(qk, v[2], y.z); y.w = fmaf(qk, v[3], y.w);
-        #pragma unroll
-        for (int o = 8; o < 32; o <<= 1) {
-            y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
-            y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
-            y.z += __shfl_xor_sync(0xffffffffu, y.z, o);
-            y.w += __shfl_xor_sync(0xffffffffu, y.w, o);
-        }
-        const int pb = int(n & 1);
-        if (lane < 8) red[pb][warp][lane] = y;
-        __syncthreads();
-        if (rg == 0) {
-            #pragma unroll
-            for (int w = 1; w < 4; ++w) {
-                const float4 x = red[pb][w][cg];
-                y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
-            }
-            if (a.o32)
-                *reinterpret_cast<float4*>(a.o32 + ((s.row * a.T + s.start + t) * a.H + h) * DV + col) = y;
-            else
-                *reinterpret_cast<uint2*>(op + t * a.o.t) = make_uint2(Op<DT>::pack(y.x, y.y), Op<DT>::pack(y.z, y.w));
-        }
-    }
-    if (!a.state_out) return;
-    #pragma unroll
-    for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(a.state_out + sb + (rg * RP + r) * DV + col) = S[r];
-}
-
 // dq, dk [token][Hk][DK] = the sum over a key head's value heads, 8 features a thread, in the
 // heads' order.
 template <int DT>
@@ -260,16 +175,6 @@ struct LaunchToken {
     }
 };
 
-struct LaunchWalk {
-    const Walk& a;
-    cudaStream_t st;
-    template <int DT, int DK, int DV>
-    cudaError_t go() {
-        walk_kernel<DT, DK, DV><<<dim3(unsigned(a.nseq), unsigned(a.H), DV / 32), 128, 0, st>>>(a);
-        return cudaGetLastError();
-    }
-};
-
 bool wrong_device(const fftconv_linattn_s* p) {
     int d = -1;
     if (cudaGetDevice(&d) != cudaSuccess) {
@@ -330,29 +235,57 @@ size_t state_bytes(const fftconv_linattn_s* p, int64_t n, int64_t Hv) { return s
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Scratch: for a backward whose value heads share key heads, dq and dk per
-// value head in float32.
+// Scratch.  Forward: the segments' end states.  Backward: those of S and of its
+// gradient, and, where value heads share key heads, dq and dk per value head in
+// float32.
 struct Scratch {
-    size_t q, k, total;  // byte offsets, and the size
-    Scratch(const fftconv_linattn_s* p, int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t, bool backward) {
+    Segments seg;
+    size_t s, r, q, k, total;  // byte offsets, and the size
+    Scratch(const fftconv_linattn_s* p, int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t nseq, bool backward) {
+        plan_segments(&seg, B, T, nseq, Hv, backward ? 3 : 1, p->num_sms);
+        const size_t n = seg.count > nseq ? up256(state_bytes(p, seg.count, Hv)) : 0;
         const size_t h = backward && Hk < Hv ? up256(size_t(B) * T * Hv * p->Dk * 4) : 0;
-        q = 0;
-        k = h;
-        total = 2 * h;
+        s = 0;
+        r = n;
+        q = backward ? 2 * n : n;
+        k = q + h;
+        total = k + h;
     }
+    bool cut(int nseq) const { return seg.count > nseq; }
 };
 
-Walk walk_of(const fftconv_linattn_args_t* x, const Call& c) {
+// A walk of a call, its sizes and constants.
+Walk walk_of(const fftconv_linattn_args_t* x, const Call& c, bool reverse) {
     Walk w{};
     w.decay = x->decay;
     w.offsets = x->offsets;
-    w.B = c.B;
     w.T = c.T;
     w.nseq = c.nseq;
     w.H = c.Hv;
     w.gq = w.gk = w.gv = 1;
     w.s_p = x->scale;
+    w.s_in = reverse ? 1.0f : x->scale;
+    w.s_up = reverse ? x->scale : 1.0f;
+    w.reverse = reverse;
     return w;
+}
+
+// A walk's tensors: their views, heads and features.
+struct Tensor {
+    View v;
+    int heads, D;
+};
+
+bool encode(const fftconv_linattn_s* p, const Call& c, CUtensorMap* m, const Tensor& t) {
+    return encode_tokens_map(m, t.v, c.B, c.T, t.heads, t.D, p->dtype);
+}
+
+Passes passes_of(const fftconv_linattn_s* p, const Scratch& l) {
+    Passes a{};
+    a.seg_chunks = l.seg.chunks;
+    a.segments = l.seg.count;
+    a.err = p->dev_err;
+    return a;
 }
 
 cudaError_t zero_gaps(const fftconv_linattn_args_t* x, const Call& c, int n, const View* v, const int* H, const int* D,
@@ -461,19 +394,23 @@ extern "C" fftconv_status_t fftconv_linattn_forward(fftconv_linattn_t p, const f
         return done(state_in ? cudaMemcpyAsync(state_out, state_in, sb, cudaMemcpyDeviceToDevice, st)
                              : cudaMemsetAsync(state_out, 0, sb, st));
     }
-    Walk w = walk_of(args, c);
-    w.q = c.q;
-    w.k = c.k;
-    w.v = c.v;
-    w.o = vo;
-    w.gq = w.gk = c.group;
-    w.s_in = args->scale;
-    w.s_up = 1.0f;
-    w.state_in = state_in;
-    w.state_out = state_out;
+    if (l.seg.count >= (int64_t(1) << 30) / c.Hv) return FFTCONV_ERR_UNSUPPORTED;
+    Passes a = passes_of(p, l);
+    Pass& x = a.p[0];
+    x.w = walk_of(args, c, false);
+    x.w.gq = x.w.gk = c.group;
+    x.w.o = vo;
+    x.w.state_in = state_in;
+    x.w.state_out = state_out;
+    x.seg_state = static_cast<float*>(scratch);
+    const Tensor q{c.q, c.Hk, p->Dk}, k{c.k, c.Hk, p->Dk}, v{c.v, c.Hv, p->Dv}, y{vo, c.Hv, p->Dv};
+    if (!encode(p, c, &x.mq, q) || !encode(p, c, &x.mk, k) || !encode(p, c, &x.mv, v) || !encode(p, c, &x.mo, y))
+        return FFTCONV_ERR_UNSUPPORTED;
     cudaError_t r = cudaSuccess;
     if (args->offsets) r = zero_gaps(args, c, 1, &vo, &c.Hv, &p->Dv, st);
-    if (r == cudaSuccess && c.nseq) r = pick(p->dtype, p->Dk, p->Dv, LaunchWalk{w, st});
+    if (!c.nseq) return done(r);
+    if (r == cudaSuccess && l.cut(c.nseq)) r = launch_linattn(a, 1, true, p->dtype, p->Dk, p->Dv, st);
+    if (r == cudaSuccess) r = launch_linattn(a, 1, false, p->dtype, p->Dk, p->Dv, st);
     return done(r);
 }
 
@@ -521,36 +458,64 @@ extern "C" fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t p, const 
     for (int i = 3; i < 5; ++i)  // the state's gradient and scratch overlap nothing
         for (int j = 0; j < i; ++j)
             if (meets(outs[i], outs[j])) return FFTCONV_ERR_INVALID;
+    if (l.seg.count >= (int64_t(1) << 30) / c.Hv) return FFTCONV_ERR_UNSUPPORTED;
     const bool shared = c.group > 1;
-    float* dq32 = shared ? reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + l.q) : nullptr;
-    float* dk32 = shared ? reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + l.k) : nullptr;
-    Walk wq = walk_of(args, c), wv = wq, wk = wq;
-    wq.q = vdo, wq.k = c.v, wq.v = c.k, wq.o = vdq, wq.o32 = dq32;
-    wq.gv = c.group;
-    wq.s_in = args->scale, wq.s_up = 1.0f;
-    wq.state_in = state_in, wq.turned = true;
-    wv.q = c.k, wv.k = c.q, wv.v = vdo, wv.o = vdv;
-    wv.gq = wv.gk = c.group;
-    wv.reverse = true;
-    wv.s_in = 1.0f, wv.s_up = args->scale;
-    wv.state_in = d_state_out, wv.state_out = d_state_in;
-    wk.q = c.v, wk.k = vdo, wk.v = c.q, wk.o = vdk, wk.o32 = dk32;
-    wk.gv = c.group;
-    wk.reverse = true;
-    wk.s_in = 1.0f, wk.s_up = args->scale;
-    wk.state_in = d_state_out, wk.turned = true;
+    uint8_t* at = static_cast<uint8_t*>(scratch);
+    float* dq32 = shared ? reinterpret_cast<float*>(at + l.q) : nullptr;
+    float* dk32 = shared ? reinterpret_cast<float*>(at + l.k) : nullptr;
+    // dQ and dK in tensors of Dv x Dk, dV of Dk x Dv: one launch where that is the same
+    Passes a = passes_of(p, l);
+    Pass &xq = a.p[0], &xk = a.p[1], &xv = a.p[2];
+    xq.w = walk_of(args, c, false);
+    xq.w.gv = c.group;
+    xq.w.o = vdq;
+    xq.w.o32 = dq32;
+    xq.w.state_in = state_in;
+    xq.w.turned = true;
+    xk.w = walk_of(args, c, true);
+    xk.w.gv = c.group;
+    xk.w.o = vdk;
+    xk.w.o32 = dk32;
+    xk.w.state_in = d_state_out;
+    xk.w.turned = true;
+    xv.w = walk_of(args, c, true);
+    xv.w.gq = xv.w.gk = c.group;
+    xv.w.o = vdv;
+    xv.w.state_in = d_state_out;
+    xv.w.state_out = d_state_in;
+    xq.seg_state = reinterpret_cast<float*>(at + l.s);
+    xk.seg_state = xv.seg_state = reinterpret_cast<float*>(at + l.r);
+    const Tensor q{c.q, c.Hk, p->Dk}, k{c.k, c.Hk, p->Dk}, v{c.v, c.Hv, p->Dv}, d{vdo, c.Hv, p->Dv};
+    const Tensor yq{vdq, c.Hk, p->Dk}, yk{vdk, c.Hk, p->Dk}, yv{vdv, c.Hv, p->Dv};
+    if (!encode(p, c, &xq.mq, d) || !encode(p, c, &xq.mk, v) || !encode(p, c, &xq.mv, k) || !encode(p, c, &xq.mo, yq) ||
+        !encode(p, c, &xk.mq, v) || !encode(p, c, &xk.mk, d) || !encode(p, c, &xk.mv, q) || !encode(p, c, &xk.mo, yk) ||
+        !encode(p, c, &xv.mq, k) || !encode(p, c, &xv.mk, q) || !encode(p, c, &xv.mv, d) || !encode(p, c, &xv.mo, yv))
+        return FFTCONV_ERR_UNSUPPORTED;
+    // the segments' states: S as the forward forms it, its gradient as dV's walk does
+    Passes b = a;
+    b.p[0] = xv;
+    b.p[1] = xv;
+    b.p[1].w.reverse = false;
+    b.p[1].w.s_up = 1.0f;
+    b.p[1].w.state_in = state_in;
+    b.p[1].mk = xq.mv;
+    b.p[1].mv = xq.mk;
+    b.p[1].seg_state = xq.seg_state;
+    Passes only_dv = a;
+    only_dv.p[0] = xv;
     cudaError_t r = cudaSuccess;
     if (args->offsets) {
         const View zs[3] = {vdq, vdk, vdv};
         const int zh[3] = {c.Hk, c.Hk, c.Hv}, zd[3] = {p->Dk, p->Dk, p->Dv};
         // with shared heads dq and dk are summed from float32 parts, zero in the gaps
-        if (shared) r = cudaMemsetAsync(scratch, 0, l.total, st);
+        if (shared) r = cudaMemsetAsync(at + l.q, 0, l.total - l.q, st);
         if (r == cudaSuccess) r = zero_gaps(args, c, 3, zs, zh, zd, st);
     }
     if (c.nseq) {
-        if (r == cudaSuccess) r = pick(p->dtype, p->Dv, p->Dk, LaunchWalk{wq, st});
-        if (r == cudaSuccess) r = pick(p->dtype, p->Dk, p->Dv, LaunchWalk{wv, st});
-        if (r == cudaSuccess) r = pick(p->dtype, p->Dv, p->Dk, LaunchWalk{wk, st});
+        const bool same = p->Dk == p->Dv;
+        if (r == cudaSuccess && l.cut(c.nseq)) r = launch_linattn(b, 2, true, p->dtype, p->Dk, p->Dv, st);
+        if (r == cudaSuccess) r = launch_linattn(a, same ? 3 : 2, false, p->dtype, p->Dv, p->Dk, st);
+        if (r == cudaSuccess && !same) r = launch_linattn(only_dv, 1, false, p->dtype, p->Dk, p->Dv, st);
         if (r == cudaSuccess && shared) {
             const int64_t n = (c.B * c.T * c.Hk * (p->Dk / 8) * 2 + 255) / 256;
             const unsigned grid = unsigned(n < 152 * 32 ? n : 152 * 32);

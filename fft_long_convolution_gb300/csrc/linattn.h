@@ -24,7 +24,7 @@ struct Walk {
     int gq, gk, gv;  // head h uses head h / g of q, k, v
     const float* decay;
     const int32_t* offsets;
-    int64_t B, T;
+    int64_t T;
     int nseq, H;
     float s_in, s_up, s_p;
     bool reverse;

@@ -1,0 +1,35 @@
+// Launch of the linear attention's chunked kernels (linattn_chunk.cu).
+#pragma once
+#include "delta_chunk.h"
+#include "linattn.h"
+
+namespace fftconv {
+
+// A walk over sequences (linattn.h), its tensors as boxes of 64 tokens x 64 features,
+// and where the segments' states are: float32 [segment slot][H][DK][DV] of the walk
+// that formed them; they are read as w.turned says.
+struct Pass {
+    CUtensorMap mq, mk, mv, mo;
+    Walk w;
+    float* seg_state;
+};
+
+// Up to three walks of the same sizes, side by side.
+struct Passes {
+    Pass p[3];
+    int64_t seg_chunks;
+    int64_t segments;
+    int* err;
+};
+
+// Chunks of a segment, and how many segment slots there are (nseq: no sequence is cut),
+// for `walks` walks at once.
+struct Segments {
+    int64_t chunks, count;
+};
+void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int sms);
+
+// states: the end states of all segments but the walks' last, joined along each sequence.
+cudaError_t launch_linattn(const Passes& a, int n, bool states, int dt, int dk, int dv, cudaStream_t st);
+
+}  // namespace fftconv
