@@ -20,12 +20,14 @@
 //
 // One CTA per sequence (or segment of one) and value head, roles by warp, handing
 // over through mbarriers:
-//   warps 0-7    S: float32 += KV, and its 16-bit parts for S Q
-//   warps 8-11   w V in parts
-//   warps 12-15  scores -> P, then O -> shared memory
-//   warp 16      loads, three chunks deep;  warp 17  issues every contraction;  warp 18  stores O
-// The contractions of a chunk are issued as KV, scores, S Q, P V: while KV runs the
-// last O is read out, while S Q runs the scores become P.
+//   warps 0-15   S: float32 += KV, and its 16-bit parts for S Q
+//   warps 16-19  w V in parts, and V, -> tensor memory
+//   warps 20-23  scores -> P;  warps 24-27  O -> shared memory
+//   warp 28      loads, three chunks deep;  warp 29  issues every contraction
+//   warp 30      O -> global memory
+// The contractions of a chunk are issued as KV (its first 64 columns), scores, KV (the
+// others), S Q, P V, so that every result is read, and every operand formed, while
+// others run.
 #include "linattn_chunk.h"
 
 #include "chunk.cuh"
@@ -48,23 +50,40 @@ __device__ __forceinline__ void stsm_t(uint32_t addr, uint32_t a, uint32_t b, ui
                  : "memory");
 }
 
-// Store 16 lanes x 32 columns: thread t holds, for every 4 columns, column t % 4 of
+// Store 16 lanes x 8 columns: thread t holds, for every 4 columns, column t % 4 of
 // lanes t / 4 and t / 4 + 8.
-__device__ __forceinline__ void st16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+__device__ __forceinline__ void st16x128b_x2(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
+                 : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void more_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+// Bounded wait of a whole warp that sleeps until the phase is over, so that the roles
+// that wait leave the issue slots to those that work.  Gives up after about a second,
+// or when another role has (*fail set).  The first poll nearly always suffices (it may
+// suspend the warp for kWaitHintNs); what follows it is kept out of the roles' loops.
+__device__ __forceinline__ bool poll(uint32_t addr, uint32_t parity) {
+    uint32_t over;
+    asm volatile(
+        "{.reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;}"
+        : "=r"(over)
+        : "r"(addr), "r"(parity), "r"(kWaitHintNs)
+        : "memory");
+    return __all_sync(0xffffffffu, over);
 }
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+
+__device__ __noinline__ bool rest_on(uint32_t addr, uint32_t parity, volatile int* fail) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 0; it < (1u << 20); ++it) {
+        if (poll(addr, parity)) return true;
+        if (__any_sync(0xffffffffu, *fail || globaltimer_ns() - t0 > kWaitNs)) return false;
+    }
+    return false;
+}
+
+__device__ __forceinline__ bool rest(uint64_t* bar, uint32_t parity, volatile int* fail) {
+    const uint32_t addr = smem_u32(bar);
+    return poll(addr, parity) || rest_on(addr, parity, fail);
 }
 
 // A power of two that takes a row's largest size x into [2^14, 2^15), and its
@@ -80,21 +99,28 @@ struct Cfg {
     static constexpr int NST = 3;
     static constexpr uint32_t sK = 0, sQ = KT * kTile, sV = 2 * KT * kTile, STAGE = sV + 2 * kTile;  // V: M = 128 lanes
     static constexpr uint32_t oP = NST * STAGE, oO = oP + 2 * kTile, oT = oO + (DV_ / 64) * kTile;
-    // float tables: w and u for a whole chunk and for a last one, the scales of V, S and P
-    static constexpr uint32_t tW = 0, tU = 128, tV = 256, tS = 768, tP = 1024, tM = 1088, TABLE = (1088 + 256) * 4;
-    static constexpr uint32_t oBar = oT + TABLE, BYTES = oBar + 256;
-    static constexpr int THREADS = 640;
-    // tensor memory columns: S in two parts, KV, S Q, scores and then P V, w V in parts.
-    // Where only the states are wanted KV and w V take turns.
-    static constexpr uint32_t cHi = 0, cLo = DK_ / 2, cKV = DK_, cOi = 2 * DK_, cX = cOi + 64, cW = cX + 64;
+    // float tables: w and u for a whole chunk and for a last one, the decays between a
+    // chunk's tokens (pairs), the scales of w V [4][128], S [2][128] and P [2][64], and
+    // the rows' sizes of S [2][4][128]
+    static constexpr uint32_t tW = 0, tU = 128, tD = 256, tV = 512, tS = 1024, tP = 1280, tM = 1408, TABLE = (1408 + 1024) * 4;
+    static constexpr uint32_t oBar = oT + TABLE, BYTES = oBar + 272;
+    static constexpr int THREADS = 1024;
+    // tensor memory columns: S in two parts; KV, 64 columns at a time; S Q; scores and
+    // then P V, two buffers; w V in parts; V.  512 in all at Dk = 128.  Where only the
+    // states are wanted KV and w V have two buffers.
+    static constexpr uint32_t cHi = 0, cLo = DK_ / 2, cKV = DK_, cOi = DK_ + 64, cX = cOi + 64, cW = cX + 128, cV = cW + 96;
+    static_assert(cV + 32 <= 512, "tensor memory");
     static __device__ __forceinline__ uint32_t kv(bool state, int c) { return state ? (c & 1) * DK_ : cKV; }
     static __device__ __forceinline__ uint32_t w(bool state, int c) { return state ? 2 * DK_ + (c & 1) * 96 : cW; }
+    static __device__ __forceinline__ uint32_t x(int c) { return cX + (c & 1) * 64; }
 };
 
 enum Bar {
-    kFull = 0, kFree = 3, kParts = 6, kKvDone = 8, kKvRead = 10,  // three stages; by chunk parity
-    kRaw = 12, kSop, kSqDone, kScDone, kPReady, kPvDone, kORead, kOReady, kOFree, kFinal,
-    kMax, kBars = kMax + 4  // the two warps of 32 lanes of S
+    kFull = 0, kFree = 3,                       // by stage
+    kParts = 6, kKvDone = 8, kKvRead = 10,      // by chunk parity where only states are wanted, else by half of KV
+    kScDone = 12, kORead = 14,                  // by chunk parity
+    kRaw = 16, kSop, kSqDone, kPReady, kVReady, kPvDone, kOReady, kOFree, kFinal,
+    kMax, kBars = kMax + 4  // the four warps of 32 lanes of S
 };
 
 // Where a CTA's part of a sequence is.
@@ -131,20 +157,23 @@ __device__ __forceinline__ bool find_part(const Walk& w, int64_t L, int64_t slot
 template <int DT, int DK, int DV, bool STATE>
 __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(const __grid_constant__ Passes a) {
     using C = Cfg<DK, DV>;
-    constexpr int NP = DT == 0 ? 2 : 3;      // parts of w V
-    constexpr int NB = STATE ? 2 : 1;        // buffers of KV and w V
-    constexpr int NC = DK / 2;               // columns of S of a thread
+    constexpr int NP = DT == 0 ? 2 : 3;                 // parts of w V
+    constexpr int NH = !STATE && DK == 128 ? 2 : 1;     // halves of KV, one after the other in the same columns
+    constexpr int NC = DK / 4;                          // columns of S of a thread
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);
     // no static shared memory: the window starts 1024-byte aligned
-    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 240);
-    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 244);
+    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 256);
+    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 260);
     float* tab = reinterpret_cast<float*>(sm + C::oT);
     const Pass& x = a.p[blockIdx.z];
     const Walk& wk = x.w;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int h = blockIdx.y;
+    // out of the indexed parameter once, not at every use
+    const bool reverse = wk.reverse, packed = wk.offsets != nullptr;
+    float* o32 = wk.o32;
     if (sb & 1023) {  // not with the present layout of the window
         if (threadIdx.x == 0) atomicExch(a.err, 7);
         return;
@@ -155,7 +184,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     const int n = p.n;
     const int64_t hs = int64_t(p.i) * wk.H + h, gs = int64_t(blockIdx.x) * wk.H + h;
     const float* sin = wk.state_in ? wk.state_in + hs * DK * DV : nullptr;
-    if (!p.first) sin = STATE ? nullptr : x.seg_state + (gs + (wk.reverse ? wk.H : -wk.H)) * DK * DV;
+    if (!p.first) sin = STATE ? nullptr : x.seg_state + (gs + (reverse ? wk.H : -wk.H)) * DK * DV;
     float* sout = p.last && wk.state_out ? wk.state_out + hs * DK * DV : nullptr;
     if (STATE) sout = x.seg_state + gs * DK * DV;
 
@@ -163,9 +192,11 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         s_fail = 0;
         for (int i = 0; i < kBars; ++i) {
             uint32_t cnt = 1;  // else one arrival per warp of the role
-            if (i == kParts || i == kParts + 1 || i == kPReady || i == kORead || i == kOReady) cnt = 4;
-            if (i == kKvRead || i == kKvRead + 1 || i == kSop) cnt = 8;
-            if (i >= kMax) cnt = 2;
+            if (i == kParts || i == kParts + 1 || i == kPReady || i == kVReady || i == kOReady || i >= kMax) cnt = 4;
+            if (i == kORead || i == kORead + 1) cnt = 4;
+            if (i == kKvRead || i == kKvRead + 1) cnt = 16 / NH;
+            if (i == kSop) cnt = 16;
+            if (i >= kFree && i < kFree + 3 && !STATE) cnt = 5;  // S Q, and V has been read
             mbar_init(bar + i, cnt);
         }
         fence_mbar_init();
@@ -175,29 +206,37 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         const int j = threadIdx.x & 63;
         const int m = threadIdx.x < 64 ? 64 : int((p.s.len - 1) % kChunk) + 1;
         const int back = m - 1 - j, on = j + 1;
-        tab[C::tW + threadIdx.x] = back >= 0 ? wk.s_up * expf(g * float(wk.reverse ? on : back)) : 0.0f;
-        tab[C::tU + threadIdx.x] = back >= 0 ? wk.s_in * expf(g * float(wk.reverse ? back : on)) : 0.0f;
+        tab[C::tW + threadIdx.x] = back >= 0 ? wk.s_up * expf(g * float(reverse ? on : back)) : 0.0f;
+        tab[C::tU + threadIdx.x] = back >= 0 ? wk.s_in * expf(g * float(reverse ? back : on)) : 0.0f;
+    } else if (threadIdx.x < 384) {
+        // entry 64 + i - j: the decays of (i, j) and (i, j + 1)
+        const int e = threadIdx.x - 128, d = (e >> 1) - 64 - (e & 1), t = reverse ? -d : d;
+        tab[C::tD + e] = t >= 0 ? wk.s_p * expf(g * float(t)) : 0.0f;
     }
-    if (warp == 17) tc::alloc(&s_tmem, 512);
+    if (warp == 29) tc::alloc(&s_tmem, 512);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = *const_cast<volatile uint32_t*>(&s_tmem);
     volatile int* fail = &s_fail;
-    const uint32_t lanes = tm + (uint32_t(32 * (warp & 3)) << 16);  // this warp's tensor-memory lanes
-    const int row = 32 * (warp & 3) + lane;                         // this thread's lane
+    const int sp = warp & 3;
+    const uint32_t lanes = tm + (uint32_t(32 * sp) << 16);  // this warp's tensor-memory lanes
+    const int row = 32 * sp + lane;                         // this thread's lane
     // one arrival per warp, after every lane's work
     auto done = [&](int b) {
         __syncwarp();
         if (lane == 0) arrive(bar + b);
     };
-    // step c's chunk, its tokens, and whether they are fewer than 64
-    auto chunk = [&](int c) { return wk.reverse ? n - 1 - c : c; };
-    auto tokens = [&](int c) {
-        const int64_t l = p.left - int64_t(chunk(c)) * kChunk;
-        return int(l < kChunk ? l : kChunk);
-    };
+    // step c's chunk, and its tokens
+    auto chunk = [&](int c) { return reverse ? n - 1 - c : c; };
+    const int all = int(p.left < int64_t(n) * kChunk ? p.left : int64_t(n) * kChunk);
+    auto tokens = [&](int c) { return min(all - chunk(c) * kChunk, kChunk); };
+    bool ok = true;
+    int c = 0;
 
+    // The roles' loops are kept short and rolled: they share the instruction cache, and
+    // straight code that runs once a chunk is fetched once a chunk (unrolled, 90 KB of
+    // code, a chunk of 64 tokens took 6100 cycles).
     if (n == 0) {
         // an empty sequence: the state passes through
         if (sout)
@@ -206,10 +245,9 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                 if (sin) v = wk.turned ? sin[(e % DV) * DK + e / DV] : sin[e];
                 sout[e] = v;
             }
-    } else if (warp < 8) {
+    } else if (warp < 16) {
         // ---------------------------------------------------------------- S
-        more_registers<128>();
-        const int dv = row % DV, k0 = (warp >> 2) * NC;
+        const int dv = row % DV, quarter = warp >> 2, k0 = quarter * NC, half = NH == 2 ? quarter >> 1 : 0;
         float2 S[NC / 2];
         #pragma unroll
         for (int j = 0; j < NC / 2; ++j) {
@@ -219,59 +257,63 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                 S[j] = wk.turned ? *reinterpret_cast<const float2*>(sin + dv * DK + k)
                                  : make_float2(sin[k * DV + dv], sin[(k + 1) * DV + dv]);
         }
-        auto put = [&](int c) {  // S's parts for step c
-            float2 sc = make_float2(1.0f, 1.0f);
-            if constexpr (DT == 0) {
-                float m = 0.0f;
+        const Decay whole = decay_over(g, float(kChunk));
+        const Decay last = decay_over(g, float(tokens(reverse ? 0 : n - 1)));
+        // S in parts for step c, then KV of step c
+        #pragma unroll 1
+        for (; ok && c < n; ++c) {
+            if constexpr (!STATE) {
+                float2 sc = make_float2(1.0f, 1.0f);
+                if constexpr (DT == 0) {
+                    float m = 0.0f;
+                    #pragma unroll
+                    for (int j = 0; j < NC / 2; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
+                    float* size = tab + C::tM + (c & 1) * 512 + row;
+                    size[quarter * 128] = m;
+                    done(kMax + sp);
+                    if (!(ok = rest(bar + kMax + sp, c & 1, fail))) break;
+                    #pragma unroll
+                    for (int j = 1; j < 4; ++j) m = fmaxf(m, size[((quarter + j) & 3) * 128]);
+                    sc = row_scale(m);
+                }
+                if (c > 0 && !(ok = rest(bar + kSqDone, (c - 1) & 1, fail))) break;
+                tc::fence_after();
+                if (DT == 0 && quarter == 0) tab[C::tS + (c & 1) * 128 + row] = sc.y;
                 #pragma unroll
-                for (int j = 0; j < NC / 2; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
-                tab[C::tM + (warp >> 2) * 128 + row] = m;
-                done(kMax + (warp & 3));
-                if (!wait(bar + kMax + (warp & 3), c & 1, fail)) return false;
-                sc = row_scale(fmaxf(m, tab[C::tM + (~warp >> 2 & 1) * 128 + row]));
-                if (warp < 4) tab[C::tS + (c & 1) * 128 + row] = sc.y;
+                for (int b = 0; b < NC; b += 16) {
+                    uint32_t hi[8], lo[8];
+                    #pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        split<DT>(DT == 0 ? mul2(S[b / 2 + j], make_float2(sc.x, sc.x)) : S[b / 2 + j], &hi[j], &lo[j]);
+                    st_cols<8>(lanes + C::cHi + (k0 + b) / 2, hi);
+                    st_cols<8>(lanes + C::cLo + (k0 + b) / 2, lo);
+                }
+                tc::wait_st();
+                tc::fence_before();
+                done(kSop);
             }
-            #pragma unroll
-            for (int b = 0; b < NC; b += 16) {
-                uint32_t hi[8], lo[8];
-                #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    split<DT>(DT == 0 ? mul2(S[b / 2 + j], make_float2(sc.x, sc.x)) : S[b / 2 + j], &hi[j], &lo[j]);
-                st_cols<8>(lanes + C::cHi + (k0 + b) / 2, hi);
-                st_cols<8>(lanes + C::cLo + (k0 + b) / 2, lo);
-            }
-            tc::wait_st();
-            tc::fence_before();
-            done(kSop);
-            return true;
-        };
-        bool ok = STATE || put(0);
-        for (int c = 0; ok && c < n; ++c) {
-            const Decay l = decay_over(g, float(tokens(c)));
-            if (!(ok = wait(bar + kKvDone + (c & 1), (c >> 1) & 1, fail))) break;
+            const int b0 = STATE ? c & 1 : half;
+            if (!(ok = rest(bar + kKvDone + b0, STATE ? (c >> 1) & 1 : c & 1, fail))) break;
             tc::fence_after();
+            const Decay l = tokens(c) < kChunk ? last : whole;
+            const float2 part = make_float2(l.part, l.part), keep = make_float2(l.keep, l.keep);
             float inv = 1.0f;
             if constexpr (DT == 0) inv = tab[C::tV + (c & 3) * 128 + row];
             #pragma unroll
-            for (int b = 0; b < NC; b += 32) {
-                uint32_t y[32];
-                tc::ld32x32b_x32(lanes + C::kv(STATE, c) + k0 + b, y);
+            for (int b = 0; b < NC; b += 16) {
+                uint32_t y[16];
+                ld16(lanes + C::kv(STATE, c) + k0 - half * 64 + b, y);
                 tc::wait_ld();
                 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     float2& s = S[b / 2 + j];
-                    const float2 kv = pair(y[2 * j], y[2 * j + 1]), part = make_float2(l.part, l.part);
+                    const float2 kv = pair(y[2 * j], y[2 * j + 1]);
                     const float2 t = DT == 0 ? fma2(kv, make_float2(inv, inv), mul2(part, s)) : fma2(part, s, kv);
-                    s = fma2(make_float2(l.keep, l.keep), s, t);
+                    s = fma2(keep, s, t);
                 }
             }
             tc::fence_before();
-            done(kKvRead + (c & 1));
-            if (!STATE && c + 1 < n) {
-                if (!(ok = wait(bar + kSqDone, c & 1, fail))) break;
-                tc::fence_after();
-                ok = put(c + 1);
-            }
+            done(kKvRead + b0);
         }
         if (ok && sout && row < DV) {
             #pragma unroll
@@ -280,218 +322,246 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                 sout[(k0 + 2 * j + 1) * DV + dv] = S[j].y;
             }
         }
-        if (!ok) s_fail = 1;
-    } else if (warp < 12) {
-        // ---------------------------------------------------------------- w V
-        fewer_registers<88>();
-        const int sp = warp & 3;
-        bool ok = true;
-        for (int c = 0; ok && c < n; ++c) {
-            const uint32_t tile_v = sb + (c % C::NST) * C::STAGE + C::sV + (sp >> 1) * kTile;
-            ok = wait(bar + kFull + c % C::NST, (c / C::NST) & 1, fail);
-            if (ok && c >= NB) ok = wait(bar + kKvDone + ((c - NB) & 1), ((c - NB) >> 1) & 1, fail);
+    } else if (warp < 20) {
+        // ---------------------------------------------------------------- w V and V
+        // A block of 16 features x 16 tokens at a time: its rows of 8 features x 8 tokens
+        // come transposed from ldmatrix in the order in which tensor memory takes them.
+        auto block = [&](uint32_t tile_v, int b, uint32_t (&v)[4]) {
+            const int tok = 16 * (b & 3) + (lane >> 4) * 8 + (lane & 7);
+            const int piece = (sp & 1) * 4 + (b >> 2) * 2 + ((lane >> 3) & 1);
+            ldsm_t(tile_v + tok * 128 + ((piece ^ (tok & 7)) * 16), v[0], v[1], v[2], v[3]);
+        };
+        // where the block's 16 lanes x 8 columns go
+        auto place = [&](int b) { return lanes + (uint32_t(16 * (b >> 2)) << 16) + 8 * (b & 3); };
+        #pragma unroll 1
+        for (; c < n; ++c) {
+            const int st = c % C::NST;
+            const uint32_t tile_v = sb + st * C::STAGE + C::sV + (sp >> 1) * kTile;
+            ok = rest(bar + kFull + st, (c / C::NST) & 1, fail);
+            if (STATE) {
+                if (ok && c >= 2) ok = rest(bar + kKvDone + (c & 1), ((c - 2) >> 1) & 1, fail);
+            } else {
+                if (ok && c >= 1) ok = rest(bar + kKvDone + NH - 1, (c - 1) & 1, fail);
+            }
             if (!ok) break;
             tc::fence_after();
             const float* wt = tab + C::tW + (tokens(c) < kChunk ? 64 : 0) + 2 * (lane & 3);
-            #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {  // 16 features each
-                uint32_t v[16];
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = 16 * i + (lane >> 4) * 8 + (lane & 7), piece = (sp & 1) * 4 + hf * 2 + ((lane >> 3) & 1);
-                    ldsm_t(tile_v + tok * 128 + ((piece ^ (tok & 7)) * 16), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                }
-                const uint32_t to = lanes + (uint32_t(16 * hf) << 16) + C::w(STATE, c);
-                uint32_t hi[16], lo[16];
+            float2 s0 = make_float2(1.0f, 1.0f), s1 = s0;
+            #pragma unroll 1
+            for (int b = 0; b < 8; ++b) {
+                uint32_t v[4], hi[4], lo[4];
                 if constexpr (DT == 0) {
-                    float2 y[16];
-                    float m0 = 0.0f, m1 = 0.0f;
-                    #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const cpx u = Op<DT>::unpack(v[i]);
-                        y[i] = mul2(make_float2(u.r, u.i), *reinterpret_cast<const float2*>(wt + 8 * (i >> 1)));
-                        float& m = i & 1 ? m1 : m0;
-                        m = fmaxf(m, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
-                    }
-                    #pragma unroll
-                    for (int o = 1; o < 4; o <<= 1) {
-                        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-                        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-                    }
-                    const float2 s0 = row_scale(m0), s1 = row_scale(m1);
-                    if ((lane & 3) == 0) {
-                        float* inv = tab + C::tV + (c & 3) * 128 + 32 * sp + 16 * hf + (lane >> 2);
-                        inv[0] = s0.y;
-                        inv[8] = s1.y;
-                    }
-                    #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float s = i & 1 ? s1.x : s0.x;
-                        split<DT>(mul2(y[i], make_float2(s, s)), &hi[i], &lo[i]);
-                    }
-                } else {
-                    uint32_t l2[16];
-                    #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const cpx u = Op<DT>::unpack(v[i]);
-                        const float2 y = mul2(make_float2(u.r, u.i), *reinterpret_cast<const float2*>(wt + 8 * (i >> 1)));
-                        hi[i] = Op<DT>::pack(y.x, y.y);
-                        const cpx e = Op<DT>::unpack(hi[i]);
-                        split<DT>(sub2(y, make_float2(e.r, e.i)), &lo[i], &l2[i]);
-                    }
-                    st16x128b_x8(to + 64, l2);
-                }
-                st16x128b_x8(to, hi);
-                st16x128b_x8(to + 32, lo);
-            }
-            tc::wait_st();
-            tc::fence_before();
-            done(kParts + (c & 1));
-        }
-        if (!ok) s_fail = 1;
-    } else if (warp < 16) {
-        // ---------------------------------------------------------------- P and O
-        const int sp = warp & 3, q = lane >> 2, r = lane & 3;
-        if constexpr (!STATE) {
-            const bool mine = 32 * sp < DV;
-            // decays between the chunk's tokens: rows i = 16 sp + q and i + 8, columns 8 n + 2 r and the next
-            float dd[32];
-            #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int i = 16 * sp + q + (e & 2) * 4, j = 8 * (e >> 2) + 2 * r + (e & 1);
-                const int d = wk.reverse ? j - i : i - j;
-                dd[e] = d >= 0 ? wk.s_p * expf(g * float(d)) : 0.0f;
-            }
-            bool ok = true;
-            for (int c = 0; ok && c < n; ++c) {
-                if (!(ok = wait(bar + kScDone, c & 1, fail))) break;
-                tc::fence_after();
-                {
-                    uint32_t y[32];
-                    tc::ld16x256b_x8(lanes + C::cX, y);
-                    tc::wait_ld();
-                    float2 z0 = make_float2(1.0f, 1.0f), z1 = z0;
-                    if constexpr (DT == 0) {
+                    if ((b & 3) == 0) {  // the sizes of the block's rows
                         float m0 = 0.0f, m1 = 0.0f;
-                        #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float& m = e & 2 ? m1 : m0;
-                            m = fmaxf(m, fabsf(__uint_as_float(y[e]) * dd[e]));
+                        #pragma unroll 1
+                        for (int e = b; e < b + 4; ++e) {
+                            block(tile_v, e, v);
+                            #pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const cpx u = Op<DT>::unpack(v[i]);
+                                const float2 y = mul2(make_float2(u.r, u.i), *reinterpret_cast<const float2*>(wt + 16 * (e & 3) + 8 * (i >> 1)));
+                                float& m = i & 1 ? m1 : m0;
+                                m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
+                            }
                         }
                         #pragma unroll
                         for (int o = 1; o < 4; o <<= 1) {
                             m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
                             m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
                         }
-                        z0 = row_scale(m0);
-                        z1 = row_scale(m1);
-                        if (r == 0) {
-                            tab[C::tP + 16 * sp + q] = z0.y;
-                            tab[C::tP + 16 * sp + q + 8] = z1.y;
+                        s0 = row_scale(m0);
+                        s1 = row_scale(m1);
+                        if ((lane & 3) == 0) {
+                            float* inv = tab + C::tV + (c & 3) * 128 + 32 * sp + 4 * b + (lane >> 2);
+                            inv[0] = s0.y;
+                            inv[8] = s1.y;
                         }
                     }
-                    uint8_t* to = sm + C::oP + (16 * sp + q) * 128 + r * 4;
-                    #pragma unroll
-                    for (int b = 0; b < 8; ++b)
-                        #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            float2 v = mul2(pair(y[4 * b + 2 * u], y[4 * b + 2 * u + 1]),
-                                            make_float2(dd[4 * b + 2 * u], dd[4 * b + 2 * u + 1]));
-                            if constexpr (DT == 0) v = mul2(v, u ? make_float2(z1.x, z1.x) : make_float2(z0.x, z0.x));
-                            uint32_t hi, lo;
-                            split<DT>(v, &hi, &lo);
-                            uint8_t* at = to + u * 1024 + ((b ^ q) * 16);  // rows i and i + 8 turn alike
-                            *reinterpret_cast<uint32_t*>(at) = hi;
-                            *reinterpret_cast<uint32_t*>(at + kTile) = lo;
-                        }
                 }
-                tc::fence_proxy_async();
-                tc::fence_before();
-                done(kPReady);
-                // O of this chunk
-                if (!(ok = wait(bar + kPvDone, c & 1, fail))) break;
-                tc::fence_after();
-                const int m = tokens(c);
-                const float* ut = tab + C::tU + (m < kChunk ? 64 : 0) + 2 * r;
-                if (!wk.o32 && c > 0 && !(ok = wait(bar + kOFree, (c - 1) & 1, fail))) break;  // the last O has left shared memory
-                const int64_t t0 = p.tok0 + int64_t(chunk(c)) * kChunk;
+                block(tile_v, b, v);
+                uint32_t l2[4];
                 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    #pragma unroll
-                    for (int b0 = 0; b0 < 8; b0 += 4) {
-                        uint32_t y[16], z[16];
-                        const uint32_t from = lanes + (uint32_t(16 * hf) << 16) + 8 * b0;
-                        tc::ld16x256b_x4(from + C::cOi, y);
-                        tc::ld16x256b_x4(from + C::cX, z);
-                        tc::wait_ld();
-                        const int f = mine ? 32 * sp + 16 * hf + q : 0;
-                        float s0 = 1.0f, s1 = 1.0f;
-                        if constexpr (DT == 0) {
-                            s0 = tab[C::tS + (c & 1) * 128 + f];
-                            s1 = tab[C::tS + (c & 1) * 128 + f + 8];
-                        }
-                        uint32_t o[8];
-                        #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const float2 u = *reinterpret_cast<const float2*>(ut + 8 * (b0 + b));
-                            float2 e0 = pair(z[4 * b], z[4 * b + 1]), e1 = pair(z[4 * b + 2], z[4 * b + 3]);
-                            float2 u0 = u, u1 = u;
-                            if constexpr (DT == 0) {
-                                const float2 ps = *reinterpret_cast<const float2*>(tab + C::tP + 8 * (b0 + b) + 2 * r);
-                                e0 = mul2(e0, ps);
-                                e1 = mul2(e1, ps);
-                                u0 = mul2(u, make_float2(s0, s0));
-                                u1 = mul2(u, make_float2(s1, s1));
-                            }
-                            e0 = fma2(u0, pair(y[4 * b], y[4 * b + 1]), e0);
-                            e1 = fma2(u1, pair(y[4 * b + 2], y[4 * b + 3]), e1);
-                            if (wk.o32 && mine) {
-                                const int t = 8 * (b0 + b) + 2 * r;
-                                float* to = wk.o32 + ((p.s.row * wk.T + t0 + t) * wk.H + h) * DV + f;
-                                if (t < m) to[0] = e0.x, to[8] = e1.x;
-                                if (t + 1 < m) to[int64_t(wk.H) * DV] = e0.y, to[int64_t(wk.H) * DV + 8] = e1.y;
-                            }
-                            o[2 * b] = Op<DT>::pack(e0.x, e0.y);
-                            o[2 * b + 1] = Op<DT>::pack(e1.x, e1.y);
-                        }
-                        if (hf == 1 && b0 == 4) {  // the accumulators and the scales have been read
-                            tc::fence_before();
-                            done(kORead);
-                        }
-                        if (!wk.o32 && mine) {
-                            const int piece = (sp & 1) * 4 + hf * 2 + ((lane >> 3) & 1);
-                            #pragma unroll
-                            for (int b = 0; b < 4; b += 2) {
-                                const int tok = 8 * (b0 + b) + (lane >> 4) * 8 + (lane & 7);
-                                stsm_t(sb + C::oO + (sp >> 1) * kTile + tok * 128 + ((piece ^ (tok & 7)) * 16), o[2 * b],
-                                       o[2 * b + 1], o[2 * b + 2], o[2 * b + 3]);
-                            }
-                        }
+                for (int i = 0; i < 4; ++i) {
+                    const cpx u = Op<DT>::unpack(v[i]);
+                    float2 y = mul2(make_float2(u.r, u.i), *reinterpret_cast<const float2*>(wt + 16 * (b & 3) + 8 * (i >> 1)));
+                    if constexpr (DT == 0) {
+                        const float s = i & 1 ? s1.x : s0.x;
+                        split<DT>(mul2(y, make_float2(s, s)), &hi[i], &lo[i]);
+                    } else {
+                        hi[i] = Op<DT>::pack(y.x, y.y);
+                        const cpx e = Op<DT>::unpack(hi[i]);
+                        split<DT>(sub2(y, make_float2(e.r, e.i)), &lo[i], &l2[i]);
                     }
                 }
-                if (wk.o32) continue;
-                tc::fence_proxy_async();
-                done(kOReady);
+                const uint32_t to = place(b) + C::w(STATE, c);
+                st16x128b_x2(to, hi);
+                st16x128b_x2(to + 32, lo);
+                if constexpr (DT != 0) st16x128b_x2(to + 64, l2);
             }
-            if (!ok) s_fail = 1;
+            tc::wait_st();
+            tc::fence_before();
+            done(kParts + (STATE ? c & 1 : 0));
+            if (STATE) continue;
+            if (c > 0 && !(ok = rest(bar + kPvDone, (c - 1) & 1, fail))) break;
+            tc::fence_after();
+            #pragma unroll 1
+            for (int b = 0; b < 8; ++b) {
+                uint32_t v[4];
+                block(tile_v, b, v);
+                st16x128b_x2(place(b) + C::cV, v);
+            }
+            tc::wait_st();
+            tc::fence_before();
+            done(kVReady);
+            done(kFree + st);
         }
-    } else {
-        fewer_registers<40>();
-        bool ok = true;
-        int c = 0;
-        if (warp == 16) {
+    } else if (warp < 24) {
+        // ---------------------------------------------------------------- P
+        const int q = lane >> 2, r = lane & 3;
+        // rows i = 16 sp + q and i + 8, columns j = 8 b + 2 r and the next
+        const float2* dt = reinterpret_cast<const float2*>(tab + C::tD) + 64 + 16 * sp + q - 2 * r;
+        uint8_t* to = sm + C::oP + (16 * sp + q) * 128 + r * 4;
+        #pragma unroll 1
+        for (; !STATE && c < n; ++c) {
+            if (!(ok = rest(bar + kScDone + (c & 1), (c >> 1) & 1, fail))) break;
+            tc::fence_after();
+            float2 z0 = make_float2(1.0f, 1.0f), z1 = z0;
+            if constexpr (DT == 0) {
+                float m0 = 0.0f, m1 = 0.0f;
+                #pragma unroll 1
+                for (int b = 0; b < 8; b += 2) {
+                    uint32_t y[8];
+                    tc::ld16x256b_x2(lanes + C::x(c) + 8 * b, y);
+                    tc::wait_ld();
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 v = mul2(pair(y[2 * e], y[2 * e + 1]), dt[(e & 1) * 8 - 8 * (b + (e >> 1))]);
+                        float& m = e & 1 ? m1 : m0;
+                        m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
+                }
+                #pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                }
+                z0 = row_scale(m0);
+                z1 = row_scale(m1);
+                if (r == 0) {
+                    tab[C::tP + (c & 1) * 64 + 16 * sp + q] = z0.y;
+                    tab[C::tP + (c & 1) * 64 + 16 * sp + q + 8] = z1.y;
+                }
+            }
+            #pragma unroll 1
+            for (int b = 0; b < 8; b += 2) {
+                uint32_t y[8];
+                tc::ld16x256b_x2(lanes + C::x(c) + 8 * b, y);
+                tc::wait_ld();
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 v = mul2(pair(y[2 * e], y[2 * e + 1]), dt[(e & 1) * 8 - 8 * (b + (e >> 1))]);
+                    if constexpr (DT == 0) v = mul2(v, e & 1 ? make_float2(z1.x, z1.x) : make_float2(z0.x, z0.x));
+                    uint32_t hi, lo;
+                    split<DT>(v, &hi, &lo);
+                    uint8_t* at = to + (e & 1) * 1024 + (((b + (e >> 1)) ^ q) * 16);  // rows i and i + 8 turn alike
+                    *reinterpret_cast<uint32_t*>(at) = hi;
+                    *reinterpret_cast<uint32_t*>(at + kTile) = lo;
+                }
+            }
+            tc::fence_proxy_async();
+            tc::fence_before();
+            done(kPReady);
+        }
+    } else if (warp < 28) {
+        // ---------------------------------------------------------------- O
+        const int q = lane >> 2, r = lane & 3;
+        const bool mine = 32 * sp < DV;
+        const int o32_token = wk.H * DV;
+        if (o32) o32 += (p.s.row * wk.T + p.tok0) * o32_token + h * DV;
+        #pragma unroll 1
+        for (; !STATE && c < n; ++c) {
+            ok = rest(bar + kPvDone, c & 1, fail);
+            if (ok && !o32 && c > 0) ok = rest(bar + kOFree, (c - 1) & 1, fail);  // the last O has left shared memory
+            if (!ok) break;
+            tc::fence_after();
+            const int m = tokens(c);
+            const float* ut = tab + C::tU + (m < kChunk ? 64 : 0) + 2 * r;
+            const float* pt = tab + C::tP + (c & 1) * 64 + 2 * r;
+            // 16 features x 32 tokens at a time
+            #pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                const int hf = b >> 1, t0 = (b & 1) * 32;
+                uint32_t y[16], z[16];
+                const uint32_t from = lanes + (uint32_t(16 * hf) << 16) + t0;
+                tc::ld16x256b_x4(from + C::cOi, y);
+                tc::ld16x256b_x4(from + C::x(c), z);
+                const int f = mine ? 32 * sp + 16 * hf + q : 0;
+                float s0 = 1.0f, s1 = 1.0f;
+                if constexpr (DT == 0) {
+                    s0 = tab[C::tS + (c & 1) * 128 + f];
+                    s1 = tab[C::tS + (c & 1) * 128 + f + 8];
+                }
+                tc::wait_ld();
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 u = *reinterpret_cast<const float2*>(ut + t0 + 8 * e);
+                    float2 e0 = pair(z[4 * e], z[4 * e + 1]), e1 = pair(z[4 * e + 2], z[4 * e + 3]);
+                    float2 u0 = u, u1 = u;
+                    if constexpr (DT == 0) {
+                        const float2 ps = *reinterpret_cast<const float2*>(pt + t0 + 8 * e);
+                        e0 = mul2(e0, ps);
+                        e1 = mul2(e1, ps);
+                        u0 = mul2(u, make_float2(s0, s0));
+                        u1 = mul2(u, make_float2(s1, s1));
+                    }
+                    e0 = fma2(u0, pair(y[4 * e], y[4 * e + 1]), e0);
+                    e1 = fma2(u1, pair(y[4 * e + 2], y[4 * e + 3]), e1);
+                    y[4 * e] = __float_as_uint(e0.x), y[4 * e + 1] = __float_as_uint(e0.y);
+                    y[4 * e + 2] = __float_as_uint(e1.x), y[4 * e + 3] = __float_as_uint(e1.y);
+                }
+                if (b == 3) {  // the accumulators and the scales have been read
+                    tc::fence_before();
+                    done(kORead + (c & 1));
+                }
+                if (!mine) continue;
+                if (o32) {
+                    float* to = o32 + int64_t(chunk(c)) * kChunk * o32_token + f;
+                    #pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int t = t0 + 8 * (e >> 2) + 2 * r + (e & 1);
+                        if (t < m) to[int64_t(t) * o32_token + (e & 2) * 4] = __uint_as_float(y[e]);
+                    }
+                    continue;
+                }
+                const int piece = (sp & 1) * 4 + hf * 2 + ((lane >> 3) & 1);
+                #pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int tok = t0 + 8 * e + (lane >> 4) * 8 + (lane & 7);
+                    uint32_t o[4];
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[i] = Op<DT>::pack(__uint_as_float(y[4 * e + 2 * i]), __uint_as_float(y[4 * e + 2 * i + 1]));
+                    stsm_t(sb + C::oO + (sp >> 1) * kTile + tok * 128 + ((piece ^ (tok & 7)) * 16), o[0], o[1], o[2], o[3]);
+                }
+            }
+            if (o32) continue;
+            tc::fence_proxy_async();
+            done(kOReady);
+        }
+    } else if (warp == 28) {
         // ---------------------------------------------------------------- loads
         const int row0 = int(p.s.row);
         auto fix = [&](uint8_t* t, int m) {  // zero rows m .. 63 of a tile
             for (int e = lane; e < (64 - m) * 8; e += 32) *reinterpret_cast<uint4*>(t + m * 128 + e * 16) = make_uint4(0, 0, 0, 0);
         };
-        for (; ok && c < n; ++c) {
+        #pragma unroll 1
+        for (; c < n; ++c) {
             const int st = c % C::NST, t0 = int(p.tok0) + chunk(c) * kChunk, m = tokens(c);
             // rows past the sequence: the TMA engine writes zeros past the tensor's
             // end; in a packed row they are the next sequence's and are zeroed here
-            const bool tail = wk.offsets && m < kChunk;  // one chunk at most
+            const bool tail = packed && m < kChunk;  // one chunk at most
             uint8_t* to = sm + st * C::STAGE;
-            if (c >= C::NST && !(ok = wait(bar + kFree + st, (c / C::NST - 1) & 1, fail))) break;
+            if (c >= C::NST && !(ok = rest(bar + kFree + st, (c / C::NST - 1) & 1, fail))) break;
             uint64_t* full = tail ? bar + kRaw : bar + kFull + st;
             if (elect()) {
                 mbar_expect_tx(full, STATE ? C::STAGE - C::KT * kTile : C::STAGE);
@@ -506,7 +576,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             }
             __syncwarp();
             if (tail) {
-                if (!(ok = wait(bar + kRaw, 0, fail))) break;
+                if (!(ok = rest(bar + kRaw, 0, fail))) break;
                 for (int f = 0; f < 2 * C::KT + 2; ++f)
                     if (!STATE || f < C::KT || f >= 2 * C::KT) fix(to + f * kTile, m);
                 tc::fence_proxy_async();
@@ -518,69 +588,90 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         // is already over returns at once)
         for (int y = c > C::NST ? c - C::NST : 0; y < c; ++y)
             mbar_wait_bounded(bar + kFull + y % C::NST, (y / C::NST) & 1, kWaitFinal);
-        } else if (warp == 17) {
+    } else if (warp == 29) {
         // ---------------------------------------------------------------- contractions
-        constexpr uint32_t idX = tc::idesc(DT, 64, 64), idO = tc::idesc(DT, 128, 64), idS = tc::idesc(DT, 128, DK) | kMnB;
-        for (; ok && c < n; ++c) {
-            const uint32_t from = sb + (c % C::NST) * C::STAGE;
-            ok = wait(bar + kFull + c % C::NST, (c / C::NST) & 1, fail) && wait(bar + kParts + (c & 1), (c >> 1) & 1, fail);
-            if (ok && c >= NB) ok = wait(bar + kKvRead + ((c - NB) & 1), ((c - NB) >> 1) & 1, fail);
+        constexpr uint32_t idX = tc::idesc(DT, 64, 64), idO = tc::idesc(DT, 128, 64);
+        constexpr uint32_t idS = tc::idesc(DT, 128, DK / NH) | kMnB;
+        #pragma unroll 1
+        for (; c < n; ++c) {
+            const int st = c % C::NST;
+            const uint32_t from = sb + st * C::STAGE;
+            const int b0 = STATE ? c & 1 : 0;
+            ok = rest(bar + kFull + st, (c / C::NST) & 1, fail) && rest(bar + kParts + b0, STATE ? (c >> 1) & 1 : c & 1, fail);
+            if (STATE) {
+                if (ok && c >= 2) ok = rest(bar + kKvRead + b0, ((c - 2) >> 1) & 1, fail);
+            } else {
+                if (ok && c >= 1) ok = rest(bar + kKvRead + NH - 1, (c - 1) & 1, fail);
+            }
+            if (!ok) break;
+            tc::fence_after();
+            auto kv = [&](int half) {  // (w V)^T K; by one thread
+                const uint64_t dk = sdesc(from + C::sK + half * kTile, kTile);
+                #pragma unroll 1
+                for (int q = 0; q < NP; ++q)
+                    #pragma unroll
+                    for (int t = 0; t < 64; t += 16)
+                        tc::mma(tm + C::kv(STATE, c), tm + C::w(STATE, c) + q * 32 + t / 2, adv(dk, t * 128), idS, q + t > 0);
+                tc::commit(bar + kKvDone + b0 + half);
+            };
+            if (elect()) {
+                kv(0);
+                if (STATE) tc::commit(bar + kFree + st);
+            }
+            if (STATE) continue;
+            if (c >= 2 && !(ok = rest(bar + kORead + (c & 1), ((c - 2) >> 1) & 1, fail))) break;
+            tc::fence_after();
+            const uint64_t dq = sdesc(from + C::sQ, 16);
+            if (elect()) {
+                const uint64_t dk = sdesc(from + C::sK, 16);
+                #pragma unroll 1
+                for (int f = 0; f < C::KT; ++f)
+                    #pragma unroll
+                    for (int t = 0; t < 128; t += 32)  // Q K^T
+                        tc::mma_ss(tm + C::x(c), adv(dq, f * kTile + t), adv(dk, f * kTile + t), idX, f + t > 0);
+                tc::commit(bar + kScDone + (c & 1));
+            }
+            if constexpr (NH == 2) {
+                if (!(ok = rest(bar + kKvRead, c & 1, fail))) break;
+                tc::fence_after();
+                if (elect()) kv(1);
+            }
+            ok = rest(bar + kSop, c & 1, fail);
+            if (ok && c >= 1) ok = rest(bar + kORead + (~c & 1), ((c - 1) >> 1) & 1, fail);
             if (!ok) break;
             tc::fence_after();
             if (elect()) {
-                const uint64_t dk = sdesc(from + C::sK, kTile);
-                #pragma unroll
-                for (int q = 0; q < NP; ++q)
+                #pragma unroll 1
+                for (int f = 0; f < 2 * C::KT; ++f)  // S^T Q^T: the high part, then the low part
                     #pragma unroll
-                    for (int t = 0; t < 64; t += 16)  // (w V)^T K
-                        tc::mma(tm + C::kv(STATE, c), tm + C::w(STATE, c) + q * 32 + t / 2, adv(dk, t * 128), idS, q + t > 0);
-                tc::commit(bar + kKvDone + (c & 1));
-                if (STATE) tc::commit(bar + kFree + c % C::NST);
-            }
-            if (STATE) continue;
-            if (c > 0 && !(ok = wait(bar + kORead, (c - 1) & 1, fail))) break;
-            tc::fence_after();
-            if (elect()) {
-                const uint64_t dq = sdesc(from + C::sQ, 16), dk = sdesc(from + C::sK, 16);
-                #pragma unroll
-                for (int f = 0; f < DK; f += 16)  // Q K^T
-                    tc::mma_ss(tm + C::cX, adv(dq, (f / 64) * kTile + (f % 64) * 2), adv(dk, (f / 64) * kTile + (f % 64) * 2), idX, f > 0);
-                tc::commit(bar + kScDone);
-            }
-            if (!(ok = wait(bar + kSop, c & 1, fail))) break;
-            tc::fence_after();
-            if (elect()) {
-                const uint64_t dq = sdesc(from + C::sQ, 16);
-                #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    #pragma unroll
-                    for (int f = 0; f < DK; f += 16)  // S^T Q^T
-                        tc::mma(tm + C::cOi, tm + (q ? C::cLo : C::cHi) + f / 2, adv(dq, (f / 64) * kTile + (f % 64) * 2), idO, q + f > 0);
+                    for (int t = 0; t < 4; ++t)
+                        tc::mma(tm + C::cOi, tm + C::cHi + f * 32 + t * 8, adv(dq, (f & (C::KT - 1)) * kTile + t * 32), idO, f + t > 0);
                 tc::commit(bar + kSqDone);
+                tc::commit(bar + kFree + st);
             }
-            if (!(ok = wait(bar + kPReady, c & 1, fail))) break;
+            if (!(ok = rest(bar + kPReady, c & 1, fail) && rest(bar + kVReady, c & 1, fail))) break;
             tc::fence_after();
             if (elect()) {
-                const uint64_t dv = sdesc(from + C::sV, kTile), dp = sdesc(sb + C::oP, 16);
-                #pragma unroll
+                const uint64_t dp = sdesc(sb + C::oP, 16);
+                #pragma unroll 1
                 for (int q = 0; q < 2; ++q)
                     #pragma unroll
-                    for (int t = 0; t < 64; t += 16)  // V^T P^T
-                        tc::mma_ss(tm + C::cX, adv(dv, t * 128), adv(dp, q * kTile + t * 2), idO | kMnA, q + t > 0);
+                    for (int t = 0; t < 4; ++t)  // V^T P^T
+                        tc::mma(tm + C::x(c), tm + C::cV + t * 8, adv(dp, q * kTile + t * 32), idO, q + t > 0);
                 tc::commit(bar + kPvDone);
-                tc::commit(bar + kFree + c % C::NST);
             }
         }
         // everything issued is done before tensor memory is given back
         if (elect()) tc::commit(bar + kFinal);
         mbar_wait_bounded(bar + kFinal, 0, kWaitFinal);
-        } else if (warp == 18 && !STATE && !wk.o32) {
+    } else if (warp == 30 && !STATE && !o32) {
         // ---------------------------------------------------------------- O -> global
+        #pragma unroll 1
         for (; c < n; ++c) {
-            if (!(ok = wait(bar + kOReady, c & 1, fail))) break;
+            if (!(ok = rest(bar + kOReady, c & 1, fail))) break;
             const int m = tokens(c);
             const int64_t t0 = p.tok0 + int64_t(chunk(c)) * kChunk;
-            if (!(wk.offsets && m < kChunk)) {  // tokens past the tensor's end are not written
+            if (!(packed && m < kChunk)) {  // tokens past the tensor's end are not written
                 if (elect()) {
                     #pragma unroll
                     for (int f = 0; f < DV / 64; ++f)
@@ -598,13 +689,12 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             }
             done(kOFree);
         }
-        }
-        if (!ok) s_fail = 1;
     }
+    if (!ok) s_fail = 1;
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 17) tc::dealloc(tm, 512);
+    if (warp == 29) tc::dealloc(tm, 512);
     if (threadIdx.x == 0 && s_fail) atomicExch(a.err, 7);
 }
 
@@ -643,7 +733,7 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
     static PerDevice c0, c1;
     constexpr size_t bytes = Cfg<DK, DV>::BYTES;
     static_assert(bytes <= 232448, "shared memory");
-    static_assert(kBars * 8 <= 240, "barriers");
+    static_assert(kBars * 8 <= 256, "barriers");
     cudaError_t e = opt_in(linattn_walk_kernel<DT, DK, DV, false>, bytes, c0);
     if (e == cudaSuccess) e = opt_in(linattn_walk_kernel<DT, DK, DV, true>, bytes, c1);
     if (e != cudaSuccess) return e;
