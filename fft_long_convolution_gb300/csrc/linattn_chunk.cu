@@ -11,23 +11,25 @@
 // KV^T and O^T are accumulators, S^T and the weighted V^T come back as A operands in
 // tensor memory, and K, Q, V stay the tiles that the TMA engine wrote (tile.cuh).
 //
-// Precision: S is float32, in the registers of the warps that update it.  Operands
-// that are not inputs are taken in 16-bit parts: w V as three for bf16 (24 bits) or
-// two for fp16 (22 bits), so that S keeps float32's digits; S and P as two, so that
-// O is as good as its one rounding to 16 bits.  In fp16 a row of each of them is
-// first scaled by a power of two to a largest value in [2^14, 2^15), and the
-// accumulator scaled back: neither small values nor large states leave fp16's range.
+// Precision: S is float32, in the registers of the warps that update it.  What feeds it,
+// w V, is taken in 16-bit parts: three for bf16 (24 bits) and two for fp16 (22 bits)
+// where the state at the end of the walk is an output, so that it keeps float32's
+// digits; two for bf16 (17 bits) where S only feeds O.  S and P enter O as one 16-bit
+// value each: their roundings are as large as O's own and fall on the two terms of its
+// sum, so that O is off by about sqrt(2) times its rounding alone at most (two parts
+// each, built and measured, gave the rounding alone and took 1.3 times as long).  In
+// fp16 a row of each of them is first scaled by a power of two to a largest value in
+// [2^14, 2^15), and the accumulator scaled back: neither small values nor large states
+// leave fp16's range.
 //
 // One CTA per sequence (or segment of one) and value head, roles by warp, handing
 // over through mbarriers:
-//   warps 0-15   S: float32 += KV, and its 16-bit parts for S Q
-//   warps 16-19  w V in parts, and V, -> tensor memory
-//   warps 20-23  scores -> P;  warps 24-27  O -> shared memory
+//   warps 0-15   w V in parts -> tensor memory; S: float32 += KV, and in 16 bits for S Q
+//   warps 16-19  scores -> P;  warps 20-27  O -> shared memory
 //   warp 28      loads, three chunks deep;  warp 29  issues every contraction
 //   warp 30      O -> global memory
-// The contractions of a chunk are issued as KV (its first 64 columns), scores, KV (the
-// others), S Q, P V, so that every result is read, and every operand formed, while
-// others run.
+// The contractions of a step are issued as scores of the next chunk, KV, S Q, P V, so
+// that every result is read, and every operand formed, while others run.
 #include "linattn_chunk.h"
 
 #include "chunk.cuh"
@@ -86,6 +88,27 @@ __device__ __forceinline__ bool rest(uint64_t* bar, uint32_t parity, volatile in
     return poll(addr, parity) || rest_on(addr, parity, fail);
 }
 
+// Pairs of 16-bit values: products, fused products, a b - c, and the larger sizes.
+template <int DT>
+struct Pair {
+    static __device__ __forceinline__ uint32_t mul(uint32_t a, uint32_t b) {
+        uint32_t r;
+        if (DT == 0) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        if (DT == 0) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t fma_less(uint32_t a, uint32_t b, uint32_t c) { return fma(a, b, c ^ 0x80008000u); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {  // |a|, |b| as integers
+        return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
+    }
+};
+
 // A power of two that takes a row's largest size x into [2^14, 2^15), and its
 // inverse; for sizes below 2^-112 that of 2^-112.
 __device__ __forceinline__ float2 row_scale(float x) {
@@ -99,27 +122,28 @@ struct Cfg {
     static constexpr int NST = 3;
     static constexpr uint32_t sK = 0, sQ = KT * kTile, sV = 2 * KT * kTile, STAGE = sV + 2 * kTile;  // V: M = 128 lanes
     static constexpr uint32_t oP = NST * STAGE, oO = oP + 2 * kTile, oT = oO + (DV_ / 64) * kTile;
-    // float tables: w and u for a whole chunk and for a last one, the decays between a
-    // chunk's tokens (pairs), the scales of w V [4][128], S [2][128] and P [2][64], and
-    // the rows' sizes of S [2][4][128]
-    static constexpr uint32_t tW = 0, tU = 128, tD = 256, tV = 512, tS = 1024, tP = 1280, tM = 1408, TABLE = (1408 + 1024) * 4;
-    static constexpr uint32_t oBar = oT + TABLE, BYTES = oBar + 272;
+    // float tables: w and u for a whole chunk and for a last one; w of two tokens in two
+    // 16-bit parts, packed [2][32][2]; the decays between a chunk's tokens (pairs); the
+    // scales of w V [4][128], S [2][128] and P [2][64]; the rows' sizes of S [2][4][128]
+    static constexpr uint32_t tW = 0, tU = 128, tH = 256, tD = 384, tV = 640, tS = 1152, tP = 1408, tM = 1536, TABLE = (1536 + 1024) * 4;
+    static constexpr uint32_t oBar = oT + TABLE, BYTES = oBar + 256;
     static constexpr int THREADS = 1024;
-    // tensor memory columns: S in two parts; KV, 64 columns at a time; S Q; scores and
-    // then P V, two buffers; w V in parts; V.  512 in all at Dk = 128.  Where only the
-    // states are wanted KV and w V have two buffers.
-    static constexpr uint32_t cHi = 0, cLo = DK_ / 2, cKV = DK_, cOi = DK_ + 64, cX = cOi + 64, cW = cX + 128, cV = cW + 96;
-    static_assert(cV + 32 <= 512, "tensor memory");
+    // tensor memory columns: S; KV; S Q; scores and then P V, two buffers; w V: two buffers
+    // of two parts, or one of three.  512 in all at Dk = 128.  Where only the states are
+    // wanted: KV and w V of three parts, two buffers each.
+    static constexpr uint32_t cS = 0, cKV = DK_ / 2, cOi = cKV + DK_, cX = cOi + 64, cW = cX + 128;
+    static_assert(cW + 128 <= 512 && 2 * DK_ + 192 <= 512, "tensor memory");
     static __device__ __forceinline__ uint32_t kv(bool state, int c) { return state ? (c & 1) * DK_ : cKV; }
-    static __device__ __forceinline__ uint32_t w(bool state, int c) { return state ? 2 * DK_ + (c & 1) * 96 : cW; }
+    static __device__ __forceinline__ uint32_t w(bool state, bool fine, int c) {
+        return state ? 2 * DK_ + (c & 1) * 96 : cW + (fine ? 0 : (c & 1) * 64);
+    }
     static __device__ __forceinline__ uint32_t x(int c) { return cX + (c & 1) * 64; }
 };
 
 enum Bar {
-    kFull = 0, kFree = 3,                       // by stage
-    kParts = 6, kKvDone = 8, kKvRead = 10,      // by chunk parity where only states are wanted, else by half of KV
-    kScDone = 12, kORead = 14,                  // by chunk parity
-    kRaw = 16, kSop, kSqDone, kPReady, kVReady, kPvDone, kOReady, kOFree, kFinal,
+    kFull = 0, kFree = 3,                                                        // by stage
+    kKvDone = 6, kKvRead = 8, kParts = 10, kScDone = 12, kORead = 14, kPReady = 16,  // by chunk parity
+    kRaw = 18, kSop, kSqDone, kPvDone, kOReady, kOFree, kFinal,
     kMax, kBars = kMax + 4  // the four warps of 32 lanes of S
 };
 
@@ -157,15 +181,13 @@ __device__ __forceinline__ bool find_part(const Walk& w, int64_t L, int64_t slot
 template <int DT, int DK, int DV, bool STATE>
 __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(const __grid_constant__ Passes a) {
     using C = Cfg<DK, DV>;
-    constexpr int NP = DT == 0 ? 2 : 3;                 // parts of w V
-    constexpr int NH = !STATE && DK == 128 ? 2 : 1;     // halves of KV, one after the other in the same columns
-    constexpr int NC = DK / 4;                          // columns of S of a thread
+    constexpr int NC = DK / 4;  // columns of S of a thread
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);
     // no static shared memory: the window starts 1024-byte aligned
-    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 256);
-    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 260);
+    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 240);
+    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 244);
     float* tab = reinterpret_cast<float*>(sm + C::oT);
     const Pass& x = a.p[blockIdx.z];
     const Walk& wk = x.w;
@@ -187,16 +209,17 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     if (!p.first) sin = STATE ? nullptr : x.seg_state + (gs + (reverse ? wk.H : -wk.H)) * DK * DV;
     float* sout = p.last && wk.state_out ? wk.state_out + hs * DK * DV : nullptr;
     if (STATE) sout = x.seg_state + gs * DK * DV;
+    // w V in three parts (bf16) where the state at the end is wanted for itself
+    const bool fine = DT == 1 && sout;
+    const int parts = fine ? 3 : 2;
 
     if (threadIdx.x == 0) {
         s_fail = 0;
         for (int i = 0; i < kBars; ++i) {
             uint32_t cnt = 1;  // else one arrival per warp of the role
-            if (i == kParts || i == kParts + 1 || i == kPReady || i == kVReady || i == kOReady || i >= kMax) cnt = 4;
-            if (i == kORead || i == kORead + 1) cnt = 4;
-            if (i == kKvRead || i == kKvRead + 1) cnt = 16 / NH;
-            if (i == kSop) cnt = 16;
-            if (i >= kFree && i < kFree + 3 && !STATE) cnt = 5;  // S Q, and V has been read
+            if (i == kPReady || i == kPReady + 1 || i >= kMax) cnt = 4;
+            if (i == kORead || i == kORead + 1 || i == kOReady) cnt = 8;
+            if (i == kParts || i == kParts + 1 || i == kSop || i == kKvRead || i == kKvRead + 1) cnt = 16;
             mbar_init(bar + i, cnt);
         }
         fence_mbar_init();
@@ -206,7 +229,13 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         const int j = threadIdx.x & 63;
         const int m = threadIdx.x < 64 ? 64 : int((p.s.len - 1) % kChunk) + 1;
         const int back = m - 1 - j, on = j + 1;
-        tab[C::tW + threadIdx.x] = back >= 0 ? wk.s_up * expf(g * float(reverse ? on : back)) : 0.0f;
+        // fp16 holds weights of at most 1: what is common to them goes with the rows' scales
+        const float w = back >= 0 ? (DT == 0 ? expf(g * float(reverse ? j : back)) : wk.s_up * expf(g * float(reverse ? on : back))) : 0.0f;
+        tab[C::tW + threadIdx.x] = w;
+        const float wh = Op<DT>::unpack(Op<DT>::pack(w, 0.0f)).r;
+        uint16_t* half = reinterpret_cast<uint16_t*>(tab + C::tH) + (threadIdx.x >> 1) * 4 + (threadIdx.x & 1);
+        half[0] = uint16_t(Op<DT>::pack(wh, 0.0f));
+        half[2] = uint16_t(Op<DT>::pack(w - wh, 0.0f));
         tab[C::tU + threadIdx.x] = back >= 0 ? wk.s_in * expf(g * float(reverse ? back : on)) : 0.0f;
     } else if (threadIdx.x < 384) {
         // entry 64 + i - j: the decays of (i, j) and (i, j + 1)
@@ -247,7 +276,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             }
     } else if (warp < 16) {
         // ---------------------------------------------------------------- S
-        const int dv = row % DV, quarter = warp >> 2, k0 = quarter * NC, half = NH == 2 ? quarter >> 1 : 0;
+        const int dv = row % DV, quarter = warp >> 2, k0 = quarter * NC;
         float2 S[NC / 2];
         #pragma unroll
         for (int j = 0; j < NC / 2; ++j) {
@@ -259,50 +288,132 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         }
         const Decay whole = decay_over(g, float(kChunk));
         const Decay last = decay_over(g, float(tokens(reverse ? 0 : n - 1)));
-        // S in parts for step c, then KV of step c
-        #pragma unroll 1
-        for (; ok && c < n; ++c) {
-            if constexpr (!STATE) {
-                float2 sc = make_float2(1.0f, 1.0f);
-                if constexpr (DT == 0) {
-                    float m = 0.0f;
-                    #pragma unroll
-                    for (int j = 0; j < NC / 2; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
-                    float* size = tab + C::tM + (c & 1) * 512 + row;
-                    size[quarter * 128] = m;
-                    done(kMax + sp);
-                    if (!(ok = rest(bar + kMax + sp, c & 1, fail))) break;
-                    #pragma unroll
-                    for (int j = 1; j < 4; ++j) m = fmaxf(m, size[((quarter + j) & 3) * 128]);
-                    sc = row_scale(m);
-                }
-                if (c > 0 && !(ok = rest(bar + kSqDone, (c - 1) & 1, fail))) break;
-                tc::fence_after();
-                if (DT == 0 && quarter == 0) tab[C::tS + (c & 1) * 128 + row] = sc.y;
-                #pragma unroll
-                for (int b = 0; b < NC; b += 16) {
-                    uint32_t hi[8], lo[8];
-                    #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        split<DT>(DT == 0 ? mul2(S[b / 2 + j], make_float2(sc.x, sc.x)) : S[b / 2 + j], &hi[j], &lo[j]);
-                    st_cols<8>(lanes + C::cHi + (k0 + b) / 2, hi);
-                    st_cols<8>(lanes + C::cLo + (k0 + b) / 2, lo);
-                }
-                tc::wait_st();
-                tc::fence_before();
-                done(kSop);
-            }
-            const int b0 = STATE ? c & 1 : half;
-            if (!(ok = rest(bar + kKvDone + b0, STATE ? (c >> 1) & 1 : c & 1, fail))) break;
+        // A block of 16 features x 16 tokens (this warp's quarter of the chunk): its rows of
+        // 8 features x 8 tokens come transposed from ldmatrix in the order in which
+        // tensor memory takes them.
+        const uint32_t v_at = sb + C::sV + (sp >> 1) * kTile + ((lane >> 4) * 8 + (lane & 7)) * 128;
+        auto rows = [&](int st, int hf, int b, uint32_t (&v)[4]) {
+            const int piece = (sp & 1) * 4 + hf * 2 + ((lane >> 3) & 1);
+            ldsm_t(v_at + st * C::STAGE + b * 2048 + ((piece ^ (lane & 7)) * 16), v[0], v[1], v[2], v[3]);
+        };
+        auto block = [&](int st, int hf, uint32_t (&v)[4]) { rows(st, hf, quarter, v); };
+        const float s_up = reverse ? wk.s_up * expf(g) : wk.s_up;  // fp16 (see the weights)
+        auto place = [&](int hf) { return lanes + (uint32_t(16 * hf) << 16) + 8 * quarter; };
+        // w V of step e in parts.  Two parts without leaving 16 bits: with w = wh + wm, the
+        // product v wh rounds to hi and leaves an error that 16 bits hold exactly, which
+        // a fused multiply-add gives: lo = v wm + (v wh - hi).
+        auto weigh = [&](int e) {
+            const int st = e % C::NST;
+            if (!rest(bar + kFull + st, (e / C::NST) & 1, fail)) return false;
+            if (!STATE && fine && e > 0 && !rest(bar + kKvDone + (~e & 1), ((e - 1) >> 1) & 1, fail)) return false;
             tc::fence_after();
-            const Decay l = tokens(c) < kChunk ? last : whole;
+            const int at = (tokens(e) < kChunk ? 64 : 0) + 16 * quarter + 2 * (lane & 3);  // the first of this thread's tokens
+            const uint32_t to = C::w(STATE, fine, e);
+            if (fine) {
+                const float2 w0 = *reinterpret_cast<const float2*>(tab + C::tW + at), w1 = *reinterpret_cast<const float2*>(tab + C::tW + at + 8);
+                #pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t v[4], hi[4], lo[4], l2[4];
+                    block(st, hf, v);
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const cpx u = Op<DT>::unpack(v[i]);
+                        const float2 y = mul2(make_float2(u.r, u.i), i < 2 ? w0 : w1);
+                        hi[i] = Op<DT>::pack(y.x, y.y);
+                        const cpx z = Op<DT>::unpack(hi[i]);
+                        split<DT>(sub2(y, make_float2(z.r, z.i)), &lo[i], &l2[i]);
+                    }
+                    st16x128b_x2(place(hf) + to, hi);
+                    st16x128b_x2(place(hf) + to + 32, lo);
+                    st16x128b_x2(place(hf) + to + 64, l2);
+                }
+            } else {
+                const uint2 w0 = *reinterpret_cast<const uint2*>(tab + C::tH + at), w1 = *reinterpret_cast<const uint2*>(tab + C::tH + at + 8);
+                #pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t v[4], hi[4], lo[4], sc[2];
+                    if constexpr (DT == 0) {  // the sizes of V's rows
+                        uint32_t m[2] = {};
+                        #pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            rows(st, hf, b, v);
+                            #pragma unroll
+                            for (int i = 0; i < 4; ++i) m[i & 1] = Pair<DT>::larger(m[i & 1], v[i]);
+                        }
+                        #pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            m[i] = Pair<DT>::larger(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
+                            m[i] = Pair<DT>::larger(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
+                            m[i] = max(m[i] & 0x7fffu, m[i] >> 16 & 0x7fffu);
+                            // a power of two that takes the largest to [2^14, 2^15) (at most 2^15 itself)
+                            const uint32_t x = min(44u - (m[i] >> 10), 30u);
+                            sc[i] = x << 10 | x << 26;
+                            if (quarter == 0 && (lane & 3) == 0)
+                                tab[C::tV + (e & 3) * 128 + 32 * sp + 16 * hf + 8 * i + (lane >> 2)] = s_up * __uint_as_float((142u - x) << 23);
+                        }
+                    }
+                    block(st, hf, v);
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 w = i < 2 ? w0 : w1;
+                        if constexpr (DT == 0) v[i] = Pair<DT>::mul(v[i], sc[i & 1]);
+                        hi[i] = Pair<DT>::mul(v[i], w.x);
+                        lo[i] = Pair<DT>::fma(v[i], w.y, Pair<DT>::fma_less(v[i], w.x, hi[i]));
+                    }
+                    st16x128b_x2(place(hf) + to, hi);
+                    st16x128b_x2(place(hf) + to + 32, lo);
+                }
+            }
+            tc::wait_st();
+            tc::fence_before();
+            done(kParts + (e & 1));
+            return true;
+        };
+        // S for step e, after S Q of the step before
+        auto put = [&](int e) {
+            float2 sc = make_float2(1.0f, 1.0f);
+            if constexpr (DT == 0) {
+                float m = 0.0f;
+                #pragma unroll
+                for (int j = 0; j < NC / 2; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
+                float* size = tab + C::tM + (e & 1) * 512 + row;
+                size[quarter * 128] = m;
+                done(kMax + sp);
+                if (!rest(bar + kMax + sp, e & 1, fail)) return false;
+                #pragma unroll
+                for (int j = 1; j < 4; ++j) m = fmaxf(m, size[((quarter + j) & 3) * 128]);
+                sc = row_scale(m);
+            }
+            if (e > 0 && !rest(bar + kSqDone, (e - 1) & 1, fail)) return false;
+            tc::fence_after();
+            if (DT == 0 && quarter == 0) tab[C::tS + (e & 1) * 128 + row] = sc.y;
+            #pragma unroll
+            for (int b = 0; b < NC; b += 16) {
+                uint32_t y[8];
+                #pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 v = DT == 0 ? mul2(S[b / 2 + j], make_float2(sc.x, sc.x)) : S[b / 2 + j];
+                    y[j] = Op<DT>::pack(v.x, v.y);
+                }
+                st_cols<8>(lanes + C::cS + (k0 + b) / 2, y);
+            }
+            tc::wait_st();
+            tc::fence_before();
+            done(kSop);
+            return true;
+        };
+        // S += KV of step e
+        auto add = [&](int e) {
+            if (!rest(bar + kKvDone + (e & 1), (e >> 1) & 1, fail)) return false;
+            tc::fence_after();
+            const Decay l = tokens(e) < kChunk ? last : whole;
             const float2 part = make_float2(l.part, l.part), keep = make_float2(l.keep, l.keep);
             float inv = 1.0f;
-            if constexpr (DT == 0) inv = tab[C::tV + (c & 3) * 128 + row];
+            if constexpr (DT == 0) inv = tab[C::tV + (e & 3) * 128 + row];
             #pragma unroll
             for (int b = 0; b < NC; b += 16) {
                 uint32_t y[16];
-                ld16(lanes + C::kv(STATE, c) + k0 - half * 64 + b, y);
+                ld16(lanes + C::kv(STATE, e) + k0 + b, y);
                 tc::wait_ld();
                 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -313,7 +424,16 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                 }
             }
             tc::fence_before();
-            done(kKvRead + b0);
+            done(kKvRead + (e & 1));
+            return true;
+        };
+        // w V of the next step before KV of this one is added: it has two buffers (the
+        // products of the step before have been waited for), or waits for that KV
+        #pragma unroll 1
+        for (; ok && c <= n; ++c) {
+            if (c < n) ok = weigh(c);
+            if (ok && c > 0) ok = add(c - 1);
+            if (!STATE && ok && c < n) ok = put(c);
         }
         if (ok && sout && row < DV) {
             #pragma unroll
@@ -323,118 +443,25 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             }
         }
     } else if (warp < 20) {
-        // ---------------------------------------------------------------- w V and V
-        // A block of 16 features x 16 tokens at a time: its rows of 8 features x 8 tokens
-        // come transposed from ldmatrix in the order in which tensor memory takes them.
-        auto block = [&](uint32_t tile_v, int b, uint32_t (&v)[4]) {
-            const int tok = 16 * (b & 3) + (lane >> 4) * 8 + (lane & 7);
-            const int piece = (sp & 1) * 4 + (b >> 2) * 2 + ((lane >> 3) & 1);
-            ldsm_t(tile_v + tok * 128 + ((piece ^ (tok & 7)) * 16), v[0], v[1], v[2], v[3]);
-        };
-        // where the block's 16 lanes x 8 columns go
-        auto place = [&](int b) { return lanes + (uint32_t(16 * (b >> 2)) << 16) + 8 * (b & 3); };
-        #pragma unroll 1
-        for (; c < n; ++c) {
-            const int st = c % C::NST;
-            const uint32_t tile_v = sb + st * C::STAGE + C::sV + (sp >> 1) * kTile;
-            ok = rest(bar + kFull + st, (c / C::NST) & 1, fail);
-            if (STATE) {
-                if (ok && c >= 2) ok = rest(bar + kKvDone + (c & 1), ((c - 2) >> 1) & 1, fail);
-            } else {
-                if (ok && c >= 1) ok = rest(bar + kKvDone + NH - 1, (c - 1) & 1, fail);
-            }
-            if (!ok) break;
-            tc::fence_after();
-            const float* wt = tab + C::tW + (tokens(c) < kChunk ? 64 : 0) + 2 * (lane & 3);
-            float2 s0 = make_float2(1.0f, 1.0f), s1 = s0;
-            #pragma unroll 1
-            for (int b = 0; b < 8; ++b) {
-                uint32_t v[4], hi[4], lo[4];
-                if constexpr (DT == 0) {
-                    if ((b & 3) == 0) {  // the sizes of the block's rows
-                        float m0 = 0.0f, m1 = 0.0f;
-                        #pragma unroll 1
-                        for (int e = b; e < b + 4; ++e) {
-                            block(tile_v, e, v);
-                            #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const cpx u = Op<DT>::unpack(v[i]);
-                                const float2 y = mul2(make_float2(u.r, u.i), *reinterpret_cast<const float2*>(wt + 16 * (e & 3) + 8 * (i >> 1)));
-                                float& m = i & 1 ? m1 : m0;
-                                m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
-                            }
-                        }
-                        #pragma unroll
-                        for (int o = 1; o < 4; o <<= 1) {
-                            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-                            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-                        }
-                        s0 = row_scale(m0);
-                        s1 = row_scale(m1);
-                        if ((lane & 3) == 0) {
-                            float* inv = tab + C::tV + (c & 3) * 128 + 32 * sp + 4 * b + (lane >> 2);
-                            inv[0] = s0.y;
-                            inv[8] = s1.y;
-                        }
-                    }
-                }
-                block(tile_v, b, v);
-                uint32_t l2[4];
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const cpx u = Op<DT>::unpack(v[i]);
-                    float2 y = mul2(make_float2(u.r, u.i), *reinterpret_cast<const float2*>(wt + 16 * (b & 3) + 8 * (i >> 1)));
-                    if constexpr (DT == 0) {
-                        const float s = i & 1 ? s1.x : s0.x;
-                        split<DT>(mul2(y, make_float2(s, s)), &hi[i], &lo[i]);
-                    } else {
-                        hi[i] = Op<DT>::pack(y.x, y.y);
-                        const cpx e = Op<DT>::unpack(hi[i]);
-                        split<DT>(sub2(y, make_float2(e.r, e.i)), &lo[i], &l2[i]);
-                    }
-                }
-                const uint32_t to = place(b) + C::w(STATE, c);
-                st16x128b_x2(to, hi);
-                st16x128b_x2(to + 32, lo);
-                if constexpr (DT != 0) st16x128b_x2(to + 64, l2);
-            }
-            tc::wait_st();
-            tc::fence_before();
-            done(kParts + (STATE ? c & 1 : 0));
-            if (STATE) continue;
-            if (c > 0 && !(ok = rest(bar + kPvDone, (c - 1) & 1, fail))) break;
-            tc::fence_after();
-            #pragma unroll 1
-            for (int b = 0; b < 8; ++b) {
-                uint32_t v[4];
-                block(tile_v, b, v);
-                st16x128b_x2(place(b) + C::cV, v);
-            }
-            tc::wait_st();
-            tc::fence_before();
-            done(kVReady);
-            done(kFree + st);
-        }
-    } else if (warp < 24) {
         // ---------------------------------------------------------------- P
-        const int q = lane >> 2, r = lane & 3;
         // rows i = 16 sp + q and i + 8, columns j = 8 b + 2 r and the next
+        const int q = lane >> 2, r = lane & 3;
         const float2* dt = reinterpret_cast<const float2*>(tab + C::tD) + 64 + 16 * sp + q - 2 * r;
-        uint8_t* to = sm + C::oP + (16 * sp + q) * 128 + r * 4;
         #pragma unroll 1
         for (; !STATE && c < n; ++c) {
             if (!(ok = rest(bar + kScDone + (c & 1), (c >> 1) & 1, fail))) break;
             tc::fence_after();
+            uint8_t* to = sm + C::oP + (c & 1) * kTile + (16 * sp + q) * 128 + r * 4;
             float2 z0 = make_float2(1.0f, 1.0f), z1 = z0;
             if constexpr (DT == 0) {
                 float m0 = 0.0f, m1 = 0.0f;
                 #pragma unroll 1
-                for (int b = 0; b < 8; b += 2) {
-                    uint32_t y[8];
-                    tc::ld16x256b_x2(lanes + C::x(c) + 8 * b, y);
+                for (int b = 0; b < 8; b += 4) {
+                    uint32_t y[16];
+                    tc::ld16x256b_x4(lanes + C::x(c) + 8 * b, y);
                     tc::wait_ld();
                     #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         const float2 v = mul2(pair(y[2 * e], y[2 * e + 1]), dt[(e & 1) * 8 - 8 * (b + (e >> 1))]);
                         float& m = e & 1 ? m1 : m0;
                         m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
@@ -453,31 +480,31 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                 }
             }
             #pragma unroll 1
-            for (int b = 0; b < 8; b += 2) {
-                uint32_t y[8];
-                tc::ld16x256b_x2(lanes + C::x(c) + 8 * b, y);
+            for (int b = 0; b < 8; b += 4) {
+                uint32_t y[16];
+                tc::ld16x256b_x4(lanes + C::x(c) + 8 * b, y);
                 tc::wait_ld();
                 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 8; ++e) {
                     float2 v = mul2(pair(y[2 * e], y[2 * e + 1]), dt[(e & 1) * 8 - 8 * (b + (e >> 1))]);
                     if constexpr (DT == 0) v = mul2(v, e & 1 ? make_float2(z1.x, z1.x) : make_float2(z0.x, z0.x));
-                    uint32_t hi, lo;
-                    split<DT>(v, &hi, &lo);
-                    uint8_t* at = to + (e & 1) * 1024 + (((b + (e >> 1)) ^ q) * 16);  // rows i and i + 8 turn alike
-                    *reinterpret_cast<uint32_t*>(at) = hi;
-                    *reinterpret_cast<uint32_t*>(at + kTile) = lo;
+                    // rows i and i + 8 turn alike
+                    *reinterpret_cast<uint32_t*>(to + (e & 1) * 1024 + (((b + (e >> 1)) ^ q) * 16)) = Op<DT>::pack(v.x, v.y);
                 }
             }
             tc::fence_proxy_async();
             tc::fence_before();
-            done(kPReady);
+            done(kPReady + (c & 1));
         }
     } else if (warp < 28) {
         // ---------------------------------------------------------------- O
-        const int q = lane >> 2, r = lane & 3;
+        // 16 features a warp, 32 tokens at a time
+        const int q = lane >> 2, r = lane & 3, hf = (warp >> 2) & 1, f = 32 * sp + 16 * hf + q;
         const bool mine = 32 * sp < DV;
+        const int piece = (sp & 1) * 4 + hf * 2 + ((lane >> 3) & 1);
+        const uint32_t stage = sb + C::oO + (sp >> 1) * kTile + ((lane >> 4) * 8 + (lane & 7)) * 128 + ((piece ^ (lane & 7)) * 16);
         const int o32_token = wk.H * DV;
-        if (o32) o32 += (p.s.row * wk.T + p.tok0) * o32_token + h * DV;
+        if (o32) o32 += (p.s.row * wk.T + p.tok0) * o32_token + h * DV + f;
         #pragma unroll 1
         for (; !STATE && c < n; ++c) {
             ok = rest(bar + kPvDone, c & 1, fail);
@@ -487,21 +514,22 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             const int m = tokens(c);
             const float* ut = tab + C::tU + (m < kChunk ? 64 : 0) + 2 * r;
             const float* pt = tab + C::tP + (c & 1) * 64 + 2 * r;
-            // 16 features x 32 tokens at a time
+            float s0 = 1.0f, s1 = 1.0f;
+            if constexpr (DT == 0) {
+                s0 = tab[C::tS + (c & 1) * 128 + f];
+                s1 = tab[C::tS + (c & 1) * 128 + f + 8];
+            }
             #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                const int hf = b >> 1, t0 = (b & 1) * 32;
+            for (int t0 = 0; t0 < 64; t0 += 32) {
                 uint32_t y[16], z[16];
                 const uint32_t from = lanes + (uint32_t(16 * hf) << 16) + t0;
                 tc::ld16x256b_x4(from + C::cOi, y);
                 tc::ld16x256b_x4(from + C::x(c), z);
-                const int f = mine ? 32 * sp + 16 * hf + q : 0;
-                float s0 = 1.0f, s1 = 1.0f;
-                if constexpr (DT == 0) {
-                    s0 = tab[C::tS + (c & 1) * 128 + f];
-                    s1 = tab[C::tS + (c & 1) * 128 + f + 8];
-                }
                 tc::wait_ld();
+                if (DT != 0 && t0) {  // the accumulators have been read
+                    tc::fence_before();
+                    done(kORead + (c & 1));
+                }
                 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 u = *reinterpret_cast<const float2*>(ut + t0 + 8 * e);
@@ -519,13 +547,13 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                     y[4 * e] = __float_as_uint(e0.x), y[4 * e + 1] = __float_as_uint(e0.y);
                     y[4 * e + 2] = __float_as_uint(e1.x), y[4 * e + 3] = __float_as_uint(e1.y);
                 }
-                if (b == 3) {  // the accumulators and the scales have been read
+                if (DT == 0 && t0) {  // the accumulators and the scales have been read
                     tc::fence_before();
                     done(kORead + (c & 1));
                 }
                 if (!mine) continue;
                 if (o32) {
-                    float* to = o32 + int64_t(chunk(c)) * kChunk * o32_token + f;
+                    float* to = o32 + int64_t(chunk(c)) * kChunk * o32_token;
                     #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int t = t0 + 8 * (e >> 2) + 2 * r + (e & 1);
@@ -533,15 +561,13 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                     }
                     continue;
                 }
-                const int piece = (sp & 1) * 4 + hf * 2 + ((lane >> 3) & 1);
                 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
-                    const int tok = t0 + 8 * e + (lane >> 4) * 8 + (lane & 7);
                     uint32_t o[4];
                     #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         o[i] = Op<DT>::pack(__uint_as_float(y[4 * e + 2 * i]), __uint_as_float(y[4 * e + 2 * i + 1]));
-                    stsm_t(sb + C::oO + (sp >> 1) * kTile + tok * 128 + ((piece ^ (tok & 7)) * 16), o[0], o[1], o[2], o[3]);
+                    stsm_t(stage + (t0 + 8 * e) * 128, o[0], o[1], o[2], o[3]);
                 }
             }
             if (o32) continue;
@@ -590,75 +616,69 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             mbar_wait_bounded(bar + kFull + y % C::NST, (y / C::NST) & 1, kWaitFinal);
     } else if (warp == 29) {
         // ---------------------------------------------------------------- contractions
-        constexpr uint32_t idX = tc::idesc(DT, 64, 64), idO = tc::idesc(DT, 128, 64);
-        constexpr uint32_t idS = tc::idesc(DT, 128, DK / NH) | kMnB;
-        #pragma unroll 1
-        for (; c < n; ++c) {
-            const int st = c % C::NST;
-            const uint32_t from = sb + st * C::STAGE;
-            const int b0 = STATE ? c & 1 : 0;
-            ok = rest(bar + kFull + st, (c / C::NST) & 1, fail) && rest(bar + kParts + b0, STATE ? (c >> 1) & 1 : c & 1, fail);
-            if (STATE) {
-                if (ok && c >= 2) ok = rest(bar + kKvRead + b0, ((c - 2) >> 1) & 1, fail);
-            } else {
-                if (ok && c >= 1) ok = rest(bar + kKvRead + NH - 1, (c - 1) & 1, fail);
-            }
-            if (!ok) break;
+        constexpr uint32_t idX = tc::idesc(DT, 64, 64), idO = tc::idesc(DT, 128, 64), idS = tc::idesc(DT, 128, DK) | kMnB;
+        // The scores go one step ahead, so that P is ready when its turn comes.
+        auto scores = [&](int e) {
+            const int st = e % C::NST;
+            if (!rest(bar + kFull + st, (e / C::NST) & 1, fail)) return false;
+            if (e >= 2 && !rest(bar + kORead + (e & 1), ((e - 2) >> 1) & 1, fail)) return false;
             tc::fence_after();
-            auto kv = [&](int half) {  // (w V)^T K; by one thread
-                const uint64_t dk = sdesc(from + C::sK + half * kTile, kTile);
-                #pragma unroll 1
-                for (int q = 0; q < NP; ++q)
-                    #pragma unroll
-                    for (int t = 0; t < 64; t += 16)
-                        tc::mma(tm + C::kv(STATE, c), tm + C::w(STATE, c) + q * 32 + t / 2, adv(dk, t * 128), idS, q + t > 0);
-                tc::commit(bar + kKvDone + b0 + half);
-            };
             if (elect()) {
-                kv(0);
-                if (STATE) tc::commit(bar + kFree + st);
-            }
-            if (STATE) continue;
-            if (c >= 2 && !(ok = rest(bar + kORead + (c & 1), ((c - 2) >> 1) & 1, fail))) break;
-            tc::fence_after();
-            const uint64_t dq = sdesc(from + C::sQ, 16);
-            if (elect()) {
-                const uint64_t dk = sdesc(from + C::sK, 16);
+                const uint64_t dq = sdesc(sb + st * C::STAGE + C::sQ, 16), dk = sdesc(sb + st * C::STAGE + C::sK, 16);
                 #pragma unroll 1
                 for (int f = 0; f < C::KT; ++f)
                     #pragma unroll
                     for (int t = 0; t < 128; t += 32)  // Q K^T
-                        tc::mma_ss(tm + C::x(c), adv(dq, f * kTile + t), adv(dk, f * kTile + t), idX, f + t > 0);
-                tc::commit(bar + kScDone + (c & 1));
+                        tc::mma_ss(tm + C::x(e), adv(dq, f * kTile + t), adv(dk, f * kTile + t), idX, f + t > 0);
+                tc::commit(bar + kScDone + (e & 1));
             }
-            if constexpr (NH == 2) {
-                if (!(ok = rest(bar + kKvRead, c & 1, fail))) break;
-                tc::fence_after();
-                if (elect()) kv(1);
+            __syncwarp();
+            return true;
+        };
+        if (!STATE) ok = scores(0);
+        #pragma unroll 1
+        for (; ok && c < n; ++c) {
+            const int st = c % C::NST;
+            const uint32_t from = sb + st * C::STAGE;
+            if (!STATE && c + 1 < n && !(ok = scores(c + 1))) break;
+            ok = (!STATE || rest(bar + kFull + st, (c / C::NST) & 1, fail)) && rest(bar + kParts + (c & 1), (c >> 1) & 1, fail);
+            constexpr int NB = STATE ? 2 : 1;  // buffers of KV
+            if (ok && c >= NB) ok = rest(bar + kKvRead + ((c - NB) & 1), ((c - NB) >> 1) & 1, fail);
+            if (!ok) break;
+            tc::fence_after();
+            if (elect()) {
+                const uint64_t dk = sdesc(from + C::sK, kTile);
+                #pragma unroll 1
+                for (int q = 0; q < parts; ++q)
+                    #pragma unroll
+                    for (int t = 0; t < 64; t += 16)  // (w V)^T K
+                        tc::mma(tm + C::kv(STATE, c), tm + C::w(STATE, fine, c) + q * 32 + t / 2, adv(dk, t * 128), idS, q + t > 0);
+                tc::commit(bar + kKvDone + (c & 1));
+                if (STATE) tc::commit(bar + kFree + st);
             }
+            if (STATE) continue;
             ok = rest(bar + kSop, c & 1, fail);
             if (ok && c >= 1) ok = rest(bar + kORead + (~c & 1), ((c - 1) >> 1) & 1, fail);
             if (!ok) break;
             tc::fence_after();
             if (elect()) {
+                const uint64_t dq = sdesc(from + C::sQ, 16);
                 #pragma unroll 1
-                for (int f = 0; f < 2 * C::KT; ++f)  // S^T Q^T: the high part, then the low part
+                for (int f = 0; f < C::KT; ++f)  // S^T Q^T
                     #pragma unroll
                     for (int t = 0; t < 4; ++t)
-                        tc::mma(tm + C::cOi, tm + C::cHi + f * 32 + t * 8, adv(dq, (f & (C::KT - 1)) * kTile + t * 32), idO, f + t > 0);
+                        tc::mma(tm + C::cOi, tm + C::cS + f * 32 + t * 8, adv(dq, f * kTile + t * 32), idO, f + t > 0);
                 tc::commit(bar + kSqDone);
-                tc::commit(bar + kFree + st);
             }
-            if (!(ok = rest(bar + kPReady, c & 1, fail) && rest(bar + kVReady, c & 1, fail))) break;
+            if (!(ok = rest(bar + kPReady + (c & 1), (c >> 1) & 1, fail))) break;
             tc::fence_after();
             if (elect()) {
-                const uint64_t dp = sdesc(sb + C::oP, 16);
-                #pragma unroll 1
-                for (int q = 0; q < 2; ++q)
-                    #pragma unroll
-                    for (int t = 0; t < 4; ++t)  // V^T P^T
-                        tc::mma(tm + C::x(c), tm + C::cV + t * 8, adv(dp, q * kTile + t * 32), idO, q + t > 0);
+                const uint64_t dv = sdesc(from + C::sV, kTile), dp = sdesc(sb + C::oP + (c & 1) * kTile, 16);
+                #pragma unroll
+                for (int t = 0; t < 4; ++t)  // V^T P^T
+                    tc::mma_ss(tm + C::x(c), adv(dv, t * 2048), adv(dp, t * 32), idO | kMnA, t > 0);
                 tc::commit(bar + kPvDone);
+                tc::commit(bar + kFree + st);
             }
         }
         // everything issued is done before tensor memory is given back
@@ -733,7 +753,7 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
     static PerDevice c0, c1;
     constexpr size_t bytes = Cfg<DK, DV>::BYTES;
     static_assert(bytes <= 232448, "shared memory");
-    static_assert(kBars * 8 <= 256, "barriers");
+    static_assert(kBars * 8 <= 240, "barriers");
     cudaError_t e = opt_in(linattn_walk_kernel<DT, DK, DV, false>, bytes, c0);
     if (e == cudaSuccess) e = opt_in(linattn_walk_kernel<DT, DK, DV, true>, bytes, c1);
     if (e != cudaSuccess) return e;
