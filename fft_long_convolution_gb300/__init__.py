@@ -761,8 +761,9 @@ class LinearAttention:
 
     def backward(self, do, q, k, v, decay, state=None, dstate=None, offsets=None, scale=None, stream=None):
         """Gradients (dq, dk, dv, gradient of the initial states) from do
-        [B, T, Hv, Dv] and, if the final states were used, dstate; the other
-        arguments as in forward, which keeps nothing for this call."""
+        [B, T, Hv, Dv] and, if the final states were used, dstate; the last is
+        None where state is.  The other arguments as in forward, which keeps
+        nothing for this call."""
         import torch
         if stream is not None:
             with _on(stream):
@@ -774,9 +775,9 @@ class LinearAttention:
         dsin = _dense(dstate, "dstate", torch.float32, shape, dev)
         vdo = View(*_strides(do, "do", self.torch_dtype, v.shape, dev))
         (dq, oq), (dk, ok), (dv, ov) = _new(q), _new(k), _new(v)
-        dst = torch.empty(shape, dtype=torch.float32, device=v.device)
+        dst = None if state is None else torch.empty(shape, dtype=torch.float32, device=v.device)
         scratch, n = self._scratch(a, 1, v.device)
-        _check(lib().fftconv_linattn_backward(self._h, ctypes.byref(a), sin, vdo, dsin, oq, ok, ov, dst.data_ptr(),
+        _check(lib().fftconv_linattn_backward(self._h, ctypes.byref(a), sin, vdo, dsin, oq, ok, ov, _ptr(dst),
                                               _ptr(scratch), n, _stream(None)), "fftconv_linattn_backward")
         return dq, dk, dv, dst
 

@@ -409,7 +409,10 @@ extern "C" fftconv_status_t fftconv_linattn_forward(fftconv_linattn_t p, const f
     cudaError_t r = cudaSuccess;
     if (args->offsets) r = zero_gaps(args, c, 1, &vo, &c.Hv, &p->Dv, st);
     if (!c.nseq) return done(r);
-    if (r == cudaSuccess && l.cut(c.nseq)) r = launch_linattn(a, 1, true, p->dtype, p->Dk, p->Dv, st);
+    if (r == cudaSuccess && l.cut(c.nseq)) {
+        r = launch_linattn(a, 1, true, p->dtype, p->Dk, p->Dv, st);
+        x.w.state_out = nullptr;  // the segments' walk has written them
+    }
     if (r == cudaSuccess) r = launch_linattn(a, 1, false, p->dtype, p->Dk, p->Dv, st);
     return done(r);
 }
@@ -498,6 +501,7 @@ extern "C" fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t p, const 
     b.p[1].w.reverse = false;
     b.p[1].w.s_up = 1.0f;
     b.p[1].w.state_in = state_in;
+    b.p[1].w.state_out = nullptr;
     b.p[1].mk = xq.mv;
     b.p[1].mv = xq.mk;
     b.p[1].seg_state = xq.seg_state;
@@ -513,7 +517,10 @@ extern "C" fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t p, const 
     }
     if (c.nseq) {
         const bool same = p->Dk == p->Dv;
-        if (r == cudaSuccess && l.cut(c.nseq)) r = launch_linattn(b, 2, true, p->dtype, p->Dk, p->Dv, st);
+        if (r == cudaSuccess && l.cut(c.nseq)) {
+            r = launch_linattn(b, 2, true, p->dtype, p->Dk, p->Dv, st);
+            xv.w.state_out = only_dv.p[0].w.state_out = nullptr;  // the segments' walk has written them
+        }
         if (r == cudaSuccess) r = launch_linattn(a, same ? 3 : 2, false, p->dtype, p->Dv, p->Dk, st);
         if (r == cudaSuccess && !same) r = launch_linattn(only_dv, 1, false, p->dtype, p->Dk, p->Dv, st);
         if (r == cudaSuccess && shared) {

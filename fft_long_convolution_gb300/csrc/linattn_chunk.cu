@@ -26,10 +26,8 @@
 // over through mbarriers:
 //   warps 0-15   w V in parts -> tensor memory; S: float32 += KV, and in 16 bits for S Q
 //   warps 16-19  scores -> P;  warps 20-27  O -> shared memory
-//   warp 28      loads, three chunks deep;  warp 29  issues every contraction
-//   warp 30      O -> global memory
-// The contractions of a step are issued as scores of the next chunk, KV, S Q, P V, so
-// that every result is read, and every operand formed, while others run.
+//   warp 28      loads, three chunks deep;  warp 30  O -> global memory
+//   warp 29      issues KV and the next chunk's scores;  warp 31  S Q and P V
 #include "linattn_chunk.h"
 
 #include "chunk.cuh"
@@ -52,11 +50,17 @@ __device__ __forceinline__ void stsm_t(uint32_t addr, uint32_t a, uint32_t b, ui
                  : "memory");
 }
 
-// Store 16 lanes x 8 columns: thread t holds, for every 4 columns, column t % 4 of
+// Store 16 lanes x 8 or 16 columns: thread t holds, for every 4 columns, column t % 4 of
 // lanes t / 4 and t / 4 + 8.
 __device__ __forceinline__ void st16x128b_x2(uint32_t taddr, const uint32_t (&r)[4]) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3])
+                 : "memory");
+}
+
+__device__ __forceinline__ void st16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 
@@ -103,9 +107,16 @@ struct Pair {
         else asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
         return r;
     }
-    static __device__ __forceinline__ uint32_t fma_less(uint32_t a, uint32_t b, uint32_t c) { return fma(a, b, c ^ 0x80008000u); }
-    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {  // |a|, |b| as integers
-        return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
+    static __device__ __forceinline__ uint32_t fma_less(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        if (DT == 0) asm("{.reg .b32 n;\n neg.f16x2 n, %3;\n fma.rn.f16x2 %0, %1, %2, n;}" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        else asm("{.reg .b32 n;\n neg.bf16x2 n, %3;\n fma.rn.bf16x2 %0, %1, %2, n;}" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {  // |a|, |b|; DT 0
+        uint32_t r;
+        asm("{.reg .b32 x, y;\n abs.f16x2 x, %1;\n abs.f16x2 y, %2;\n max.f16x2 %0, x, y;}" : "=r"(r) : "r"(a), "r"(b));
+        return r;
     }
 };
 
@@ -126,7 +137,7 @@ struct Cfg {
     // 16-bit parts, packed [2][32][2]; the decays between a chunk's tokens (pairs); the
     // scales of w V [4][128], S [2][128] and P [2][64]; the rows' sizes of S [2][4][128]
     static constexpr uint32_t tW = 0, tU = 128, tH = 256, tD = 384, tV = 640, tS = 1152, tP = 1408, tM = 1536, TABLE = (1536 + 1024) * 4;
-    static constexpr uint32_t oBar = oT + TABLE, BYTES = oBar + 256;
+    static constexpr uint32_t oBar = oT + TABLE, BYTES = oBar + 272;
     static constexpr int THREADS = 1024;
     // tensor memory columns: S; KV; S Q; scores and then P V, two buffers; w V: two buffers
     // of two parts, or one of three.  512 in all at Dk = 128.  Where only the states are
@@ -142,9 +153,23 @@ struct Cfg {
 
 enum Bar {
     kFull = 0, kFree = 3,                                                        // by stage
-    kKvDone = 6, kKvRead = 8, kParts = 10, kScDone = 12, kORead = 14, kPReady = 16,  // by chunk parity
-    kRaw = 18, kSop, kSqDone, kPvDone, kOReady, kOFree, kFinal,
-    kMax, kBars = kMax + 4  // the four warps of 32 lanes of S
+    kKvDone = 6, kKvRead = 8, kParts = 10, kScDone = 12, kORead = 14, kPReady = 16, kPvDone = 18,  // by chunk parity
+    kRaw = 20, kSop, kSqDone, kOReady, kOFree,
+    kFinal,            // [2]
+    kMax = kFinal + 2, kBars = kMax + 4  // the four warps of 32 lanes of S
+};
+
+// A stage of the loads and the parity of its barriers, step after step.
+template <int N>
+struct Ring {
+    int st = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++st == N) {
+            st = 0;
+            parity ^= 1;
+        }
+    }
 };
 
 // Where a CTA's part of a sequence is.
@@ -177,7 +202,8 @@ __device__ __forceinline__ bool find_part(const Walk& w, int64_t L, int64_t slot
     return true;
 }
 
-// STATE: only the state at the end of a segment (from zero, or from the initial state).
+// STATE: only the state at the end of a segment (from zero, or from the initial state);
+// a walk's last one, if the final state is wanted, to where that goes.
 template <int DT, int DK, int DV, bool STATE>
 __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(const __grid_constant__ Passes a) {
     using C = Cfg<DK, DV>;
@@ -186,8 +212,8 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     const uint32_t sb = smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);
     // no static shared memory: the window starts 1024-byte aligned
-    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 240);
-    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 244);
+    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 256);
+    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 260);
     float* tab = reinterpret_cast<float*>(sm + C::oT);
     const Pass& x = a.p[blockIdx.z];
     const Walk& wk = x.w;
@@ -202,13 +228,13 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     }
     Part p;
     if (!find_part(wk, a.seg_chunks, blockIdx.x, &p)) return;
-    if (STATE && p.last) return;
+    if (STATE && p.last && !wk.state_out) return;
     const int n = p.n;
     const int64_t hs = int64_t(p.i) * wk.H + h, gs = int64_t(blockIdx.x) * wk.H + h;
     const float* sin = wk.state_in ? wk.state_in + hs * DK * DV : nullptr;
     if (!p.first) sin = STATE ? nullptr : x.seg_state + (gs + (reverse ? wk.H : -wk.H)) * DK * DV;
     float* sout = p.last && wk.state_out ? wk.state_out + hs * DK * DV : nullptr;
-    if (STATE) sout = x.seg_state + gs * DK * DV;
+    if (STATE && !p.last) sout = x.seg_state + gs * DK * DV;
     // w V in three parts (bf16) where the state at the end is wanted for itself
     const bool fine = DT == 1 && sout;
     const int parts = fine ? 3 : 2;
@@ -219,7 +245,9 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             uint32_t cnt = 1;  // else one arrival per warp of the role
             if (i == kPReady || i == kPReady + 1 || i >= kMax) cnt = 4;
             if (i == kORead || i == kORead + 1 || i == kOReady) cnt = 8;
-            if (i == kParts || i == kParts + 1 || i == kSop || i == kKvRead || i == kKvRead + 1) cnt = 16;
+            if (i >= kFree && i < kFree + 3 && !STATE) cnt = 2;  // both warps that issue products
+            if (i == kParts || i == kParts + 1) cnt = DT == 1 && (STATE || (p.last && wk.state_out)) ? 16 : 8;
+            if (i == kSop || i == kKvRead || i == kKvRead + 1) cnt = 16;
             mbar_init(bar + i, cnt);
         }
         fence_mbar_init();
@@ -288,82 +316,91 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         }
         const Decay whole = decay_over(g, float(kChunk));
         const Decay last = decay_over(g, float(tokens(reverse ? 0 : n - 1)));
-        // A block of 16 features x 16 tokens (this warp's quarter of the chunk): its rows of
-        // 8 features x 8 tokens come transposed from ldmatrix in the order in which
-        // tensor memory takes them.
-        const uint32_t v_at = sb + C::sV + (sp >> 1) * kTile + ((lane >> 4) * 8 + (lane & 7)) * 128;
-        auto rows = [&](int st, int hf, int b, uint32_t (&v)[4]) {
-            const int piece = (sp & 1) * 4 + hf * 2 + ((lane >> 3) & 1);
-            ldsm_t(v_at + st * C::STAGE + b * 2048 + ((piece ^ (lane & 7)) * 16), v[0], v[1], v[2], v[3]);
-        };
-        auto block = [&](int st, int hf, uint32_t (&v)[4]) { rows(st, hf, quarter, v); };
+        // w V in parts.  A warp takes 16 features; a block of 16 tokens of them comes
+        // transposed from ldmatrix, as 8 features x 8 tokens four times, in the order in
+        // which tensor memory takes them.
+        const int hf = quarter >> 1, side = quarter & 1;
+        const uint32_t v_at = sb + C::sV + (sp >> 1) * kTile + ((lane >> 4) * 8 + (lane & 7)) * 128 +
+                              ((((sp & 1) * 4 + hf * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) * 16);
+        auto block = [&](int st, int b, uint32_t* v) { ldsm_t(v_at + st * C::STAGE + b * 2048, v[0], v[1], v[2], v[3]); };
+        const uint32_t w_at = lanes + (uint32_t(16 * hf) << 16);
         const float s_up = reverse ? wk.s_up * expf(g) : wk.s_up;  // fp16 (see the weights)
-        auto place = [&](int hf) { return lanes + (uint32_t(16 * hf) << 16) + 8 * quarter; };
-        // w V of step e in parts.  Two parts without leaving 16 bits: with w = wh + wm, the
-        // product v wh rounds to hi and leaves an error that 16 bits hold exactly, which
-        // a fused multiply-add gives: lo = v wm + (v wh - hi).
-        auto weigh = [&](int e) {
-            const int st = e % C::NST;
-            if (!rest(bar + kFull + st, (e / C::NST) & 1, fail)) return false;
-            if (!STATE && fine && e > 0 && !rest(bar + kKvDone + (~e & 1), ((e - 1) >> 1) & 1, fail)) return false;
+        Ring<C::NST> full;
+        // Three parts: a warp half of the tokens of every step, as KV waits for it.
+        auto weigh_fine = [&](int e) {
+            if (!rest(bar + kFull + full.st, full.parity, fail)) return false;
             tc::fence_after();
-            const int at = (tokens(e) < kChunk ? 64 : 0) + 16 * quarter + 2 * (lane & 3);  // the first of this thread's tokens
-            const uint32_t to = C::w(STATE, fine, e);
-            if (fine) {
-                const float2 w0 = *reinterpret_cast<const float2*>(tab + C::tW + at), w1 = *reinterpret_cast<const float2*>(tab + C::tW + at + 8);
-                #pragma unroll 1
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t v[4], hi[4], lo[4], l2[4];
-                    block(st, hf, v);
-                    #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const cpx u = Op<DT>::unpack(v[i]);
-                        const float2 y = mul2(make_float2(u.r, u.i), i < 2 ? w0 : w1);
-                        hi[i] = Op<DT>::pack(y.x, y.y);
-                        const cpx z = Op<DT>::unpack(hi[i]);
-                        split<DT>(sub2(y, make_float2(z.r, z.i)), &lo[i], &l2[i]);
-                    }
-                    st16x128b_x2(place(hf) + to, hi);
-                    st16x128b_x2(place(hf) + to + 32, lo);
-                    st16x128b_x2(place(hf) + to + 64, l2);
-                }
-            } else {
-                const uint2 w0 = *reinterpret_cast<const uint2*>(tab + C::tH + at), w1 = *reinterpret_cast<const uint2*>(tab + C::tH + at + 8);
+            const float* wt = tab + C::tW + (tokens(e) < kChunk ? 64 : 0) + 32 * side + 2 * (lane & 3);
+            const uint32_t to = w_at + C::w(STATE, true, e) + 16 * side;
+            #pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                uint32_t v[4], hi[4], lo[4], l2[4];
+                block(full.st, 2 * side + b, v);
                 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t v[4], hi[4], lo[4], sc[2];
-                    if constexpr (DT == 0) {  // the sizes of V's rows
-                        uint32_t m[2] = {};
-                        #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            rows(st, hf, b, v);
-                            #pragma unroll
-                            for (int i = 0; i < 4; ++i) m[i & 1] = Pair<DT>::larger(m[i & 1], v[i]);
-                        }
-                        #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            m[i] = Pair<DT>::larger(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
-                            m[i] = Pair<DT>::larger(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
-                            m[i] = max(m[i] & 0x7fffu, m[i] >> 16 & 0x7fffu);
-                            // a power of two that takes the largest to [2^14, 2^15) (at most 2^15 itself)
-                            const uint32_t x = min(44u - (m[i] >> 10), 30u);
-                            sc[i] = x << 10 | x << 26;
-                            if (quarter == 0 && (lane & 3) == 0)
-                                tab[C::tV + (e & 3) * 128 + 32 * sp + 16 * hf + 8 * i + (lane >> 2)] = s_up * __uint_as_float((142u - x) << 23);
-                        }
-                    }
-                    block(st, hf, v);
+                for (int i = 0; i < 4; ++i) {
+                    const cpx u = Op<DT>::unpack(v[i]);
+                    const float2 y = mul2(make_float2(u.r, u.i), *reinterpret_cast<const float2*>(wt + 16 * b + 8 * (i >> 1)));
+                    hi[i] = Op<DT>::pack(y.x, y.y);
+                    const cpx z = Op<DT>::unpack(hi[i]);
+                    split<DT>(sub2(y, make_float2(z.r, z.i)), &lo[i], &l2[i]);
+                }
+                st16x128b_x2(to + 8 * b, hi);
+                st16x128b_x2(to + 8 * b + 32, lo);
+                st16x128b_x2(to + 8 * b + 64, l2);
+            }
+            full.next();
+            tc::wait_st();
+            tc::fence_before();
+            done(kParts + (e & 1));
+            return true;
+        };
+        // Two parts, without leaving 16 bits: with w = wh + wm, the product v wh rounds to hi
+        // and leaves an error that 16 bits hold exactly, which a fused multiply-add gives:
+        // lo = v wm + (v wh - hi).  A warp all tokens of every other step, a step ahead.
+        auto weigh = [&](int e) {
+            if (!rest(bar + kFull + full.st, full.parity, fail)) return false;
+            tc::fence_after();
+            const float* wt = tab + C::tH + (tokens(e) < kChunk ? 64 : 0) + 2 * (lane & 3);
+            const uint32_t to = w_at + C::w(STATE, false, e);
+            uint32_t sc[2] = {};
+            if constexpr (DT == 0) {  // the sizes of V's rows
+                uint32_t m[2] = {};
+                #pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t v[4];
+                    block(full.st, b, v);
                     #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint2 w = i < 2 ? w0 : w1;
-                        if constexpr (DT == 0) v[i] = Pair<DT>::mul(v[i], sc[i & 1]);
-                        hi[i] = Pair<DT>::mul(v[i], w.x);
-                        lo[i] = Pair<DT>::fma(v[i], w.y, Pair<DT>::fma_less(v[i], w.x, hi[i]));
-                    }
-                    st16x128b_x2(place(hf) + to, hi);
-                    st16x128b_x2(place(hf) + to + 32, lo);
+                    for (int i = 0; i < 4; ++i) m[i & 1] = Pair<DT>::larger(m[i & 1], v[i]);
+                }
+                #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    m[i] = Pair<DT>::larger(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
+                    m[i] = Pair<DT>::larger(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
+                    m[i] = max(m[i] & 0x7fffu, m[i] >> 16);
+                    // a power of two that takes the largest to [2^14, 2^15) (at most 2^15 itself)
+                    const uint32_t x = min(44u - (m[i] >> 10), 30u);
+                    sc[i] = x << 10 | x << 26;
+                    if ((lane & 3) == 0)
+                        tab[C::tV + (e & 3) * 128 + 32 * sp + 16 * hf + 8 * i + (lane >> 2)] = s_up * __uint_as_float((142u - x) << 23);
                 }
             }
+            #pragma unroll 1
+            for (int b = 0; b < 4; b += 2) {
+                uint32_t v[8], hi[8], lo[8];
+                block(full.st, b, v);
+                block(full.st, b + 1, v + 4);
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(wt + 16 * b + 8 * (i >> 1));
+                    if constexpr (DT == 0) v[i] = Pair<DT>::mul(v[i], sc[i & 1]);
+                    hi[i] = Pair<DT>::mul(v[i], w.x);
+                    lo[i] = Pair<DT>::fma(v[i], w.y, Pair<DT>::fma_less(v[i], w.x, hi[i]));
+                }
+                st16x128b_x4(to + 8 * b, hi);
+                st16x128b_x4(to + 8 * b + 32, lo);
+            }
+            full.next();
+            full.next();
             tc::wait_st();
             tc::fence_before();
             done(kParts + (e & 1));
@@ -427,13 +464,26 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             done(kKvRead + (e & 1));
             return true;
         };
-        // w V of the next step before KV of this one is added: it has two buffers (the
-        // products of the step before have been waited for), or waits for that KV
-        #pragma unroll 1
-        for (; ok && c <= n; ++c) {
-            if (c < n) ok = weigh(c);
-            if (ok && c > 0) ok = add(c - 1);
-            if (!STATE && ok && c < n) ok = put(c);
+        if (fine) {
+            // where only the states are wanted w V has two buffers, else KV has to be over
+            #pragma unroll 1
+            for (; ok && c <= n; ++c) {
+                if (STATE && c < n) ok = weigh_fine(c);
+                if (ok && c > 0) ok = add(c - 1);
+                if (!STATE && ok && c < n) ok = weigh_fine(c) && put(c);
+            }
+        } else {
+            // w V of step c goes into the buffer of step c - 2, whose products add() has
+            // waited for: the warps of one side take the even steps, those of the other
+            // the odd ones
+            if (side) full.next();
+            else ok = weigh(0);
+            #pragma unroll 1
+            for (; ok && c <= n; ++c) {
+                if (c > 0) ok = add(c - 1);
+                if (!STATE && ok && c < n) ok = put(c);
+                if (ok && c + 1 < n && ((c + 1) & 1) == side) ok = weigh(c + 1);
+            }
         }
         if (ok && sout && row < DV) {
             #pragma unroll
@@ -449,12 +499,41 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         const float2* dt = reinterpret_cast<const float2*>(tab + C::tD) + 64 + 16 * sp + q - 2 * r;
         #pragma unroll 1
         for (; !STATE && c < n; ++c) {
-            if (!(ok = rest(bar + kScDone + (c & 1), (c >> 1) & 1, fail))) break;
+            ok = rest(bar + kScDone + (c & 1), (c >> 1) & 1, fail);
+            if (ok && c >= 2) ok = rest(bar + kPvDone + (c & 1), ((c - 2) >> 1) & 1, fail);  // the buffer's last P has been used
+            if (!ok) break;
             tc::fence_after();
             uint8_t* to = sm + C::oP + (c & 1) * kTile + (16 * sp + q) * 128 + r * 4;
-            float2 z0 = make_float2(1.0f, 1.0f), z1 = z0;
             if constexpr (DT == 0) {
+                uint32_t y[32];
+                tc::ld16x256b_x8(lanes + C::x(c), y);
+                tc::wait_ld();
                 float m0 = 0.0f, m1 = 0.0f;
+                #pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 v = mul2(pair(y[2 * e], y[2 * e + 1]), dt[(e & 1) * 8 - 8 * (e >> 1)]);
+                    y[2 * e] = __float_as_uint(v.x);
+                    y[2 * e + 1] = __float_as_uint(v.y);
+                    float& m = e & 1 ? m1 : m0;
+                    m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+                }
+                #pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                }
+                const float2 z0 = row_scale(m0), z1 = row_scale(m1);
+                if (r == 0) {
+                    tab[C::tP + (c & 1) * 64 + 16 * sp + q] = z0.y;
+                    tab[C::tP + (c & 1) * 64 + 16 * sp + q + 8] = z1.y;
+                }
+                #pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float z = e & 1 ? z1.x : z0.x;
+                    const float2 v = mul2(pair(y[2 * e], y[2 * e + 1]), make_float2(z, z));
+                    *reinterpret_cast<uint32_t*>(to + (e & 1) * 1024 + (((e >> 1) ^ q) * 16)) = Op<DT>::pack(v.x, v.y);
+                }
+            } else {
                 #pragma unroll 1
                 for (int b = 0; b < 8; b += 4) {
                     uint32_t y[16];
@@ -463,33 +542,9 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 v = mul2(pair(y[2 * e], y[2 * e + 1]), dt[(e & 1) * 8 - 8 * (b + (e >> 1))]);
-                        float& m = e & 1 ? m1 : m0;
-                        m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+                        // rows i and i + 8 turn alike
+                        *reinterpret_cast<uint32_t*>(to + (e & 1) * 1024 + (((b + (e >> 1)) ^ q) * 16)) = Op<DT>::pack(v.x, v.y);
                     }
-                }
-                #pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-                    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-                }
-                z0 = row_scale(m0);
-                z1 = row_scale(m1);
-                if (r == 0) {
-                    tab[C::tP + (c & 1) * 64 + 16 * sp + q] = z0.y;
-                    tab[C::tP + (c & 1) * 64 + 16 * sp + q + 8] = z1.y;
-                }
-            }
-            #pragma unroll 1
-            for (int b = 0; b < 8; b += 4) {
-                uint32_t y[16];
-                tc::ld16x256b_x4(lanes + C::x(c) + 8 * b, y);
-                tc::wait_ld();
-                #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float2 v = mul2(pair(y[2 * e], y[2 * e + 1]), dt[(e & 1) * 8 - 8 * (b + (e >> 1))]);
-                    if constexpr (DT == 0) v = mul2(v, e & 1 ? make_float2(z1.x, z1.x) : make_float2(z0.x, z0.x));
-                    // rows i and i + 8 turn alike
-                    *reinterpret_cast<uint32_t*>(to + (e & 1) * 1024 + (((b + (e >> 1)) ^ q) * 16)) = Op<DT>::pack(v.x, v.y);
                 }
             }
             tc::fence_proxy_async();
@@ -507,7 +562,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         if (o32) o32 += (p.s.row * wk.T + p.tok0) * o32_token + h * DV + f;
         #pragma unroll 1
         for (; !STATE && c < n; ++c) {
-            ok = rest(bar + kPvDone, c & 1, fail);
+            ok = rest(bar + kPvDone + (c & 1), (c >> 1) & 1, fail);
             if (ok && !o32 && c > 0) ok = rest(bar + kOFree, (c - 1) & 1, fail);  // the last O has left shared memory
             if (!ok) break;
             tc::fence_after();
@@ -580,14 +635,15 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         auto fix = [&](uint8_t* t, int m) {  // zero rows m .. 63 of a tile
             for (int e = lane; e < (64 - m) * 8; e += 32) *reinterpret_cast<uint4*>(t + m * 128 + e * 16) = make_uint4(0, 0, 0, 0);
         };
+        Ring<C::NST> ring;
         #pragma unroll 1
-        for (; c < n; ++c) {
-            const int st = c % C::NST, t0 = int(p.tok0) + chunk(c) * kChunk, m = tokens(c);
+        for (; c < n; ++c, ring.next()) {
+            const int st = ring.st, t0 = int(p.tok0) + chunk(c) * kChunk, m = tokens(c);
             // rows past the sequence: the TMA engine writes zeros past the tensor's
             // end; in a packed row they are the next sequence's and are zeroed here
             const bool tail = packed && m < kChunk;  // one chunk at most
             uint8_t* to = sm + st * C::STAGE;
-            if (c >= C::NST && !(ok = rest(bar + kFree + st, (c / C::NST - 1) & 1, fail))) break;
+            if (c >= C::NST && !(ok = rest(bar + kFree + st, ring.parity ^ 1, fail))) break;
             uint64_t* full = tail ? bar + kRaw : bar + kFull + st;
             if (elect()) {
                 mbar_expect_tx(full, STATE ? C::STAGE - C::KT * kTile : C::STAGE);
@@ -615,75 +671,88 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         for (int y = c > C::NST ? c - C::NST : 0; y < c; ++y)
             mbar_wait_bounded(bar + kFull + y % C::NST, (y / C::NST) & 1, kWaitFinal);
     } else if (warp == 29) {
-        // ---------------------------------------------------------------- contractions
-        constexpr uint32_t idX = tc::idesc(DT, 64, 64), idO = tc::idesc(DT, 128, 64), idS = tc::idesc(DT, 128, DK) | kMnB;
-        // The scores go one step ahead, so that P is ready when its turn comes.
-        auto scores = [&](int e) {
-            const int st = e % C::NST;
-            if (!rest(bar + kFull + st, (e / C::NST) & 1, fail)) return false;
-            if (e >= 2 && !rest(bar + kORead + (e & 1), ((e - 2) >> 1) & 1, fail)) return false;
+        // ---------------------------------------------------------------- KV and scores
+        // The scores go one step ahead, so that P is ready when its turn comes; they and KV
+        // run while O is read, which S Q waits for.
+        constexpr uint32_t idX = tc::idesc(DT, 64, 64), idS = tc::idesc(DT, 128, DK) | kMnB;
+        const uint64_t dk_mn = sdesc(sb + C::sK, kTile), dk = sdesc(sb + C::sK, 16), dq = sdesc(sb + C::sQ, 16);
+        Ring<C::NST> ring, ahead;
+        #pragma unroll 1
+        for (int e = STATE ? 0 : -1; ok && e < n; ++e) {
+            c = e;
+            if (c >= 0) {
+                constexpr int NB = STATE ? 2 : 1;  // buffers of KV
+                if (STATE) ok = rest(bar + kFull + ring.st, ring.parity, fail);
+                ok = ok && rest(bar + kParts + (c & 1), (c >> 1) & 1, fail);
+                if (ok && c >= NB) ok = rest(bar + kKvRead + ((c - NB) & 1), ((c - NB) >> 1) & 1, fail);
+                if (!ok) break;
+                tc::fence_after();
+                if (elect()) {
+                    const uint64_t d = adv(dk_mn, ring.st * C::STAGE);
+                    #pragma unroll 1
+                    for (int q = 0; q < parts; ++q)
+                        #pragma unroll
+                        for (int t = 0; t < 64; t += 16)  // (w V)^T K
+                            tc::mma(tm + C::kv(STATE, c), tm + C::w(STATE, fine, c) + q * 32 + t / 2, adv(d, t * 128), idS, q + t > 0);
+                    tc::commit(bar + kKvDone + (c & 1));
+                    tc::commit(bar + kFree + ring.st);
+                }
+                __syncwarp();
+                ring.next();
+            }
+            if (STATE || c + 1 >= n) continue;
+            ok = rest(bar + kFull + ahead.st, ahead.parity, fail);
+            if (ok && c >= 1) ok = rest(bar + kORead + (~c & 1), ((c - 1) >> 1) & 1, fail);  // the buffer's last O has been read
+            if (!ok) break;
             tc::fence_after();
             if (elect()) {
-                const uint64_t dq = sdesc(sb + st * C::STAGE + C::sQ, 16), dk = sdesc(sb + st * C::STAGE + C::sK, 16);
+                const uint32_t off = ahead.st * C::STAGE;
                 #pragma unroll 1
                 for (int f = 0; f < C::KT; ++f)
                     #pragma unroll
                     for (int t = 0; t < 128; t += 32)  // Q K^T
-                        tc::mma_ss(tm + C::x(e), adv(dq, f * kTile + t), adv(dk, f * kTile + t), idX, f + t > 0);
-                tc::commit(bar + kScDone + (e & 1));
+                        tc::mma_ss(tm + C::x(c + 1), adv(dq, off + f * kTile + t), adv(dk, off + f * kTile + t), idX, f + t > 0);
+                tc::commit(bar + kScDone + (~c & 1));
             }
             __syncwarp();
-            return true;
-        };
-        if (!STATE) ok = scores(0);
+            ahead.next();
+        }
+        // everything issued is done before tensor memory is given back
+        if (elect()) tc::commit(bar + kFinal);
+        mbar_wait_bounded(bar + kFinal, 0, kWaitFinal);
+    } else if (warp == 31 && !STATE) {
+        // ---------------------------------------------------------------- S Q and P V
+        constexpr uint32_t idO = tc::idesc(DT, 128, 64);
+        const uint64_t dq = sdesc(sb + C::sQ, 16), dv = sdesc(sb + C::sV, kTile), dp = sdesc(sb + C::oP, 16);
+        Ring<C::NST> ring;
         #pragma unroll 1
-        for (; ok && c < n; ++c) {
-            const int st = c % C::NST;
-            const uint32_t from = sb + st * C::STAGE;
-            if (!STATE && c + 1 < n && !(ok = scores(c + 1))) break;
-            ok = (!STATE || rest(bar + kFull + st, (c / C::NST) & 1, fail)) && rest(bar + kParts + (c & 1), (c >> 1) & 1, fail);
-            constexpr int NB = STATE ? 2 : 1;  // buffers of KV
-            if (ok && c >= NB) ok = rest(bar + kKvRead + ((c - NB) & 1), ((c - NB) >> 1) & 1, fail);
-            if (!ok) break;
-            tc::fence_after();
-            if (elect()) {
-                const uint64_t dk = sdesc(from + C::sK, kTile);
-                #pragma unroll 1
-                for (int q = 0; q < parts; ++q)
-                    #pragma unroll
-                    for (int t = 0; t < 64; t += 16)  // (w V)^T K
-                        tc::mma(tm + C::kv(STATE, c), tm + C::w(STATE, fine, c) + q * 32 + t / 2, adv(dk, t * 128), idS, q + t > 0);
-                tc::commit(bar + kKvDone + (c & 1));
-                if (STATE) tc::commit(bar + kFree + st);
-            }
-            if (STATE) continue;
-            ok = rest(bar + kSop, c & 1, fail);
+        for (; c < n; ++c, ring.next()) {
+            const uint32_t off = ring.st * C::STAGE;
+            ok = rest(bar + kFull + ring.st, ring.parity, fail) && rest(bar + kSop, c & 1, fail);
             if (ok && c >= 1) ok = rest(bar + kORead + (~c & 1), ((c - 1) >> 1) & 1, fail);
             if (!ok) break;
             tc::fence_after();
             if (elect()) {
-                const uint64_t dq = sdesc(from + C::sQ, 16);
                 #pragma unroll 1
                 for (int f = 0; f < C::KT; ++f)  // S^T Q^T
                     #pragma unroll
                     for (int t = 0; t < 4; ++t)
-                        tc::mma(tm + C::cOi, tm + C::cS + f * 32 + t * 8, adv(dq, f * kTile + t * 32), idO, f + t > 0);
+                        tc::mma(tm + C::cOi, tm + C::cS + f * 32 + t * 8, adv(dq, off + f * kTile + t * 32), idO, f + t > 0);
                 tc::commit(bar + kSqDone);
             }
             if (!(ok = rest(bar + kPReady + (c & 1), (c >> 1) & 1, fail))) break;
             tc::fence_after();
             if (elect()) {
-                const uint64_t dv = sdesc(from + C::sV, kTile), dp = sdesc(sb + C::oP + (c & 1) * kTile, 16);
                 #pragma unroll
                 for (int t = 0; t < 4; ++t)  // V^T P^T
-                    tc::mma_ss(tm + C::x(c), adv(dv, t * 2048), adv(dp, t * 32), idO | kMnA, t > 0);
-                tc::commit(bar + kPvDone);
-                tc::commit(bar + kFree + st);
+                    tc::mma_ss(tm + C::x(c), adv(dv, off + t * 2048), adv(dp, (c & 1) * kTile + t * 32), idO | kMnA, t > 0);
+                tc::commit(bar + kPvDone + (c & 1));
+                tc::commit(bar + kFree + ring.st);
             }
+            __syncwarp();
         }
-        // everything issued is done before tensor memory is given back
-        if (elect()) tc::commit(bar + kFinal);
-        mbar_wait_bounded(bar + kFinal, 0, kWaitFinal);
+        if (elect()) tc::commit(bar + kFinal + 1);
+        mbar_wait_bounded(bar + kFinal + 1, 0, kWaitFinal);
     } else if (warp == 30 && !STATE && !o32) {
         // ---------------------------------------------------------------- O -> global
         #pragma unroll 1
@@ -719,20 +788,24 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
 }
 
 // The states at the segments' ends, along a sequence in the walk's order: X_p =
-// l^(tokens of a segment) X_(p-1) + N_p, float32, in place of N_p.  All segments but
-// the walk's last are needed, all but its first are whole.  Four elements a thread,
-// four segments in flight.
+// l^(tokens of a segment) X_(p-1) + N_p, float32, in place of N_p; the walk's last one
+// is the sequence's final state, if that is wanted.  Four elements a thread, four
+// segments in flight.
 __global__ void __launch_bounds__(256) linattn_join_kernel(const __grid_constant__ Passes a, int size) {
     const Pass& x = a.p[blockIdx.z];
     const Walk& w = x.w;
     const int chunks = size / 1024, i = blockIdx.x / chunks, h = blockIdx.y;
     const Seq s = locate(w.offsets, w.T, i);
     const int64_t all = (s.len + kChunk - 1) / kChunk, nseg = (all + a.seg_chunks - 1) / a.seg_chunks;
-    if (nseg < 3) return;
+    if (nseg < (w.state_out ? 2 : 3)) return;
     const int64_t g0 = s.slot / a.seg_chunks + i, step = (w.reverse ? -1 : 1) * int64_t(w.H) * size;
     float4* at = reinterpret_cast<float4*>(x.seg_state + ((g0 + (w.reverse ? nseg - 1 : 0)) * w.H + h) * size +
                                            (blockIdx.x % chunks) * 1024 + threadIdx.x * 4);
-    const Decay l = decay_over(head_decay(w.decay, h), float(a.seg_chunks * kChunk));
+    const float g = head_decay(w.decay, h);
+    const Decay l = decay_over(g, float(a.seg_chunks * kChunk));
+    auto after = [](const Decay& d, const float4& x, const float4& y) {
+        return make_float4(decayed(d, x.x, y.x), decayed(d, x.y, y.y), decayed(d, x.z, y.z), decayed(d, x.w, y.w));
+    };
     float4 S = *at;
     for (int64_t p = 1; p + 1 < nseg; p += 4) {
         float4 N[4];
@@ -742,10 +815,15 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(const __grid_constant
         #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (p + j + 1 >= nseg) break;
-            S = make_float4(decayed(l, S.x, N[j].x), decayed(l, S.y, N[j].y), decayed(l, S.z, N[j].z), decayed(l, S.w, N[j].w));
+            S = after(l, S, N[j]);
             *(at + (p + j) * step / 4) = S;
         }
     }
+    if (!w.state_out) return;
+    float4* out = reinterpret_cast<float4*>(w.state_out + (int64_t(i) * w.H + h) * size + (blockIdx.x % chunks) * 1024 + threadIdx.x * 4);
+    // backwards in time the last segment is a sequence's first one, which is whole
+    const int64_t left = w.reverse ? a.seg_chunks * kChunk : s.len - (nseg - 1) * a.seg_chunks * kChunk;
+    *out = after(decay_over(g, float(left)), S, *out);
 }
 
 template <int DT, int DK, int DV>
@@ -753,7 +831,7 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
     static PerDevice c0, c1;
     constexpr size_t bytes = Cfg<DK, DV>::BYTES;
     static_assert(bytes <= 232448, "shared memory");
-    static_assert(kBars * 8 <= 240, "barriers");
+    static_assert(kBars * 8 <= 256, "barriers");
     cudaError_t e = opt_in(linattn_walk_kernel<DT, DK, DV, false>, bytes, c0);
     if (e == cudaSuccess) e = opt_in(linattn_walk_kernel<DT, DK, DV, true>, bytes, c1);
     if (e != cudaSuccess) return e;
@@ -771,16 +849,29 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
 }  // namespace
 
 // Segments.  A sequence's chunks follow one another, so few long sequences leave SMs
-// idle.  Cut into segments a walk costs another over K and V for the segments' end
-// states and a join.
+// idle.  Cut into m segments a walk costs another over K and V for the segments' end
+// states (0.6 of a walk's step for a chunk) and a join.  The rule counts waves of CTAs
+// over the SMs in steps of a walk, takes the two more launches as 8, and cuts when that
+// saves a tenth.  Packed rows are taken at their mean length, as the host does not know
+// their offsets.
 void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int sms) {
-    const int64_t slots = chunk_slots(B, T, nseq), rows = nseq * heads * walks;
+    const int64_t slots = chunk_slots(B, T, nseq), rows = nseq * heads;
     s->chunks = slots + 1;
     s->count = nseq;
-    if (rows == 0 || rows >= sms) return;
-    const int64_t L = (slots * heads * walks + sms - 1) / sms;
-    if (L * 2 > (slots + nseq - 1) / nseq) return;
-    s->chunks = L < 8 ? 8 : L;
+    if (rows == 0) return;
+    const int64_t n = (B * T / nseq + kChunk - 1) / kChunk;
+    auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
+    int64_t best = 1, cost = waves(rows * walks) * n * 9;
+    for (int64_t m = 2; m * 2 <= n && m * rows <= 2 * sms; ++m) {
+        const int64_t len = (n + m - 1) / m;
+        const int64_t c = (waves(m * rows * walks) * 10 + waves(m * rows * (walks > 1 ? 2 : 1)) * 6) * len + 80;
+        if (c < cost) {
+            cost = c;
+            best = m;
+        }
+    }
+    if (best == 1) return;
+    s->chunks = (n + best - 1) / best;
     s->count = slots / s->chunks + nseq;
 }
 
