@@ -30,6 +30,8 @@
 //   warp 29      issues KV and the next chunk's scores;  warp 31  S Q and P V
 #include "linattn_chunk.h"
 
+#include <type_traits>
+
 #include "chunk.cuh"
 
 namespace fftconv {
@@ -75,13 +77,13 @@ __device__ __forceinline__ bool poll(uint32_t addr, uint32_t parity) {
         : "=r"(over)
         : "r"(addr), "r"(parity), "r"(kWaitHintNs)
         : "memory");
-    return __all_sync(0xffffffffu, over);
+    return over;
 }
 
 __device__ __noinline__ bool rest_on(uint32_t addr, uint32_t parity, volatile int* fail) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 0; it < (1u << 20); ++it) {
-        if (poll(addr, parity)) return true;
+        if (__all_sync(0xffffffffu, poll(addr, parity))) return true;
         if (__any_sync(0xffffffffu, *fail || globaltimer_ns() - t0 > kWaitNs)) return false;
     }
     return false;
@@ -89,7 +91,8 @@ __device__ __noinline__ bool rest_on(uint32_t addr, uint32_t parity, volatile in
 
 __device__ __forceinline__ bool rest(uint64_t* bar, uint32_t parity, volatile int* fail) {
     const uint32_t addr = smem_u32(bar);
-    return poll(addr, parity) || rest_on(addr, parity, fail);
+    if (__builtin_expect(poll(addr, parity), 1)) return true;  // the same answer in every lane: one poll of one address
+    return rest_on(addr, parity, fail);
 }
 
 // Pairs of 16-bit values: products, fused products, a b - c, and the larger sizes.
@@ -135,9 +138,10 @@ struct Cfg {
     static constexpr uint32_t oP = NST * STAGE, oO = oP + 2 * kTile, oT = oO + (DV_ / 64) * kTile;
     // float tables: w and u for a whole chunk and for a last one; w of two tokens in two
     // 16-bit parts, packed [2][32][2]; the decays between a chunk's tokens (pairs); the
-    // scales of w V [4][128], S [2][128] and P [2][64]; the rows' sizes of S [2][4][128]
-    static constexpr uint32_t tW = 0, tU = 128, tH = 256, tD = 384, tV = 640, tS = 1152, tP = 1408, tM = 1536, TABLE = (1536 + 1024) * 4;
-    static constexpr uint32_t oBar = oT + TABLE, BYTES = oBar + 272;
+    // scales of w V [8][128] back, S [2][128] and P [2][64]; the rows' sizes of S
+    // [2][4][128]; the scales of w V
+    static constexpr uint32_t tW = 0, tU = 128, tH = 256, tD = 384, tV = 640, tS = 1664, tP = 1920, tM = 2048, tN = 3072, TABLE = (3072 + 512) * 4;
+    static constexpr uint32_t oBar = oT + TABLE, BYTES = oBar + 304;
     static constexpr int THREADS = 1024;
     // tensor memory columns: S; KV; S Q; scores and then P V, two buffers; w V: two buffers
     // of two parts, or one of three.  512 in all at Dk = 128.  Where only the states are
@@ -156,7 +160,8 @@ enum Bar {
     kKvDone = 6, kKvRead = 8, kParts = 10, kScDone = 12, kORead = 14, kPReady = 16, kPvDone = 18,  // by chunk parity
     kRaw = 20, kSop, kSqDone, kOReady, kOFree,
     kFinal,            // [2]
-    kMax = kFinal + 2, kBars = kMax + 4  // the four warps of 32 lanes of S
+    kSizes = kFinal + 2,  // [4]
+    kMax = kSizes + 4, kBars = kMax + 4  // the four warps of 32 lanes of S
 };
 
 // A stage of the loads and the parity of its barriers, step after step.
@@ -182,16 +187,16 @@ struct Part {
     bool first, last;  // in the walk's order
 };
 
-__device__ __forceinline__ bool find_part(const Walk& w, int64_t L, int64_t slot, Part* p) {
+__device__ __forceinline__ bool find_part(const Walk& w, uint32_t L, uint32_t slot, Part* p) {
     int lo = 0, hi = w.nseq - 1;
     while (lo < hi) {
         const int m = (lo + hi + 1) >> 1;
-        if (locate(w.offsets, w.T, m).slot / L + m <= slot) lo = m;
+        if (uint32_t(locate(w.offsets, w.T, m).slot) / L + m <= slot) lo = m;
         else hi = m - 1;
     }
     p->i = lo;
     p->s = locate(w.offsets, w.T, lo);
-    const int64_t seg = slot - (p->s.slot / L + lo), all = (p->s.len + kChunk - 1) / kChunk, from = seg * L;
+    const int64_t seg = int64_t(slot) - (uint32_t(p->s.slot) / L + lo), all = (p->s.len + kChunk - 1) / kChunk, from = seg * L;
     if (seg < 0 || (seg > 0 && from >= all)) return false;
     const bool low = seg == 0, high = from + L >= all;
     p->first = w.reverse ? high : low;
@@ -212,8 +217,8 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     const uint32_t sb = smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);
     // no static shared memory: the window starts 1024-byte aligned
-    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 256);
-    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 260);
+    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 288);
+    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 292);
     float* tab = reinterpret_cast<float*>(sm + C::oT);
     const Pass& x = a.p[blockIdx.z];
     const Walk& wk = x.w;
@@ -226,9 +231,22 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         if (threadIdx.x == 0) atomicExch(a.err, 7);
         return;
     }
+    // one warp looks for the part, the others take it from shared memory
     Part p;
-    if (!find_part(wk, a.seg_chunks, blockIdx.x, &p)) return;
-    if (STATE && p.last && !wk.state_out) return;
+    bool live;
+    {
+        Part* found = reinterpret_cast<Part*>(sm + C::oO);
+        bool* any = reinterpret_cast<bool*>(found + 1);
+        if (warp == 0) {
+            live = find_part(wk, uint32_t(a.seg_chunks), blockIdx.x, &p);
+            if (lane == 0) *found = p, *any = live;
+        }
+        __syncthreads();
+        p = *found;
+        live = *any;
+        __syncthreads();
+    }
+    if (!live || (STATE && p.last && !wk.state_out)) return;
     const int n = p.n;
     const int64_t hs = int64_t(p.i) * wk.H + h, gs = int64_t(blockIdx.x) * wk.H + h;
     const float* sin = wk.state_in ? wk.state_in + hs * DK * DV : nullptr;
@@ -236,14 +254,14 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     float* sout = p.last && wk.state_out ? wk.state_out + hs * DK * DV : nullptr;
     if (STATE && !p.last) sout = x.seg_state + gs * DK * DV;
     // w V in three parts (bf16) where the state at the end is wanted for itself
-    const bool fine = DT == 1 && sout;
+    const bool fine = DT == 1 && (STATE || sout);
     const int parts = fine ? 3 : 2;
 
     if (threadIdx.x == 0) {
         s_fail = 0;
         for (int i = 0; i < kBars; ++i) {
             uint32_t cnt = 1;  // else one arrival per warp of the role
-            if (i == kPReady || i == kPReady + 1 || i >= kMax) cnt = 4;
+            if (i == kPReady || i == kPReady + 1 || i >= kSizes) cnt = 4;
             if (i == kORead || i == kORead + 1 || i == kOReady) cnt = 8;
             if (i >= kFree && i < kFree + 3 && !STATE) cnt = 2;  // both warps that issue products
             if (i == kParts || i == kParts + 1) cnt = DT == 1 && (STATE || (p.last && wk.state_out)) ? 16 : 8;
@@ -324,7 +342,6 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                               ((((sp & 1) * 4 + hf * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) * 16);
         auto block = [&](int st, int b, uint32_t* v) { ldsm_t(v_at + st * C::STAGE + b * 2048, v[0], v[1], v[2], v[3]); };
         const uint32_t w_at = lanes + (uint32_t(16 * hf) << 16);
-        const float s_up = reverse ? wk.s_up * expf(g) : wk.s_up;  // fp16 (see the weights)
         Ring<C::NST> full;
         // Three parts: a warp half of the tokens of every step, as KV waits for it.
         auto weigh_fine = [&](int e) {
@@ -363,26 +380,11 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             const float* wt = tab + C::tH + (tokens(e) < kChunk ? 64 : 0) + 2 * (lane & 3);
             const uint32_t to = w_at + C::w(STATE, false, e);
             uint32_t sc[2] = {};
-            if constexpr (DT == 0) {  // the sizes of V's rows
-                uint32_t m[2] = {};
-                #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t v[4];
-                    block(full.st, b, v);
-                    #pragma unroll
-                    for (int i = 0; i < 4; ++i) m[i & 1] = Pair<DT>::larger(m[i & 1], v[i]);
-                }
-                #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    m[i] = Pair<DT>::larger(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
-                    m[i] = Pair<DT>::larger(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
-                    m[i] = max(m[i] & 0x7fffu, m[i] >> 16);
-                    // a power of two that takes the largest to [2^14, 2^15) (at most 2^15 itself)
-                    const uint32_t x = min(44u - (m[i] >> 10), 30u);
-                    sc[i] = x << 10 | x << 26;
-                    if ((lane & 3) == 0)
-                        tab[C::tV + (e & 3) * 128 + 32 * sp + 16 * hf + 8 * i + (lane >> 2)] = s_up * __uint_as_float((142u - x) << 23);
-                }
+            if constexpr (DT == 0) {
+                if (!rest(bar + kSizes + (e & 3), (e >> 2) & 1, fail)) return false;
+                const uint32_t* z = reinterpret_cast<const uint32_t*>(tab + C::tN) + (e & 3) * 128 + 32 * sp + 16 * hf + (lane >> 2);
+                sc[0] = z[0];
+                sc[1] = z[8];
             }
             #pragma unroll 1
             for (int b = 0; b < 4; b += 2) {
@@ -440,13 +442,14 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             return true;
         };
         // S += KV of step e
-        auto add = [&](int e) {
+        auto add = [&](int e, auto exact) {  // exact: S is an output, else it only feeds O
             if (!rest(bar + kKvDone + (e & 1), (e >> 1) & 1, fail)) return false;
             tc::fence_after();
             const Decay l = tokens(e) < kChunk ? last : whole;
             const float2 part = make_float2(l.part, l.part), keep = make_float2(l.keep, l.keep);
+            const float2 whole_l = make_float2(l.keep + l.part, l.keep + l.part);
             float inv = 1.0f;
-            if constexpr (DT == 0) inv = tab[C::tV + (e & 3) * 128 + row];
+            if constexpr (DT == 0) inv = tab[C::tV + (e & 7) * 128 + row];
             #pragma unroll
             for (int b = 0; b < NC; b += 16) {
                 uint32_t y[16];
@@ -456,8 +459,12 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                 for (int j = 0; j < 8; ++j) {
                     float2& s = S[b / 2 + j];
                     const float2 kv = pair(y[2 * j], y[2 * j + 1]);
-                    const float2 t = DT == 0 ? fma2(kv, make_float2(inv, inv), mul2(part, s)) : fma2(part, s, kv);
-                    s = fma2(keep, s, t);
+                    if constexpr (exact.value) {
+                        const float2 t = DT == 0 ? fma2(kv, make_float2(inv, inv), mul2(part, s)) : fma2(part, s, kv);
+                        s = fma2(keep, s, t);
+                    } else {
+                        s = fma2(whole_l, s, kv);
+                    }
                 }
             }
             tc::fence_before();
@@ -469,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             #pragma unroll 1
             for (; ok && c <= n; ++c) {
                 if (STATE && c < n) ok = weigh_fine(c);
-                if (ok && c > 0) ok = add(c - 1);
+                if (ok && c > 0) ok = add(c - 1, std::true_type());
                 if (!STATE && ok && c < n) ok = weigh_fine(c) && put(c);
             }
         } else {
@@ -480,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             else ok = weigh(0);
             #pragma unroll 1
             for (; ok && c <= n; ++c) {
-                if (c > 0) ok = add(c - 1);
+                if (c > 0) ok = add(c - 1, std::bool_constant<DT == 0>());
                 if (!STATE && ok && c < n) ok = put(c);
                 if (ok && c + 1 < n && ((c + 1) & 1) == side) ok = weigh(c + 1);
             }
@@ -497,8 +504,44 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         // rows i = 16 sp + q and i + 8, columns j = 8 b + 2 r and the next
         const int q = lane >> 2, r = lane & 3;
         const float2* dt = reinterpret_cast<const float2*>(tab + C::tD) + 64 + 16 * sp + q - 2 * r;
+        // fp16: the scales of V's rows, two chunks ahead.  A lane takes 8 of the warp's 32
+        // features, 8 tokens.  When chunk e has been loaded, chunk e - 3 has left its stage:
+        // its KV is over, so w V has used the scales of chunk e - 4, and S has added KV up to
+        // chunk e - 5 (places for 4 scales, and for 8 of their inverses).
+        const float s_up = reverse ? wk.s_up * expf(g) : wk.s_up;  // (see the weights)
+        Ring<C::NST> full;
+        auto sizes = [&](int e) {
+            if (!rest(bar + kFull + full.st, full.parity, fail)) return false;
+            const int f8 = lane & 3, t8 = lane >> 2;
+            const uint8_t* v = sm + full.st * C::STAGE + C::sV + (sp >> 1) * kTile + t8 * 1024;
+            uint32_t m[4] = {};
+            #pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const uint4 y = *reinterpret_cast<const uint4*>(v + t * 128 + ((((sp & 1) * 4 + f8) ^ t) * 16));
+                const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) m[i] = Pair<DT>::larger(m[i], z[i]);
+            }
+            #pragma unroll
+            for (int i = 0; i < 4; ++i)
+                #pragma unroll
+                for (int o = 4; o < 32; o <<= 1) m[i] = Pair<DT>::larger(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+            // feature 8 f8 + t8 is this lane's: a power of two that takes its largest to
+            // [2^14, 2^15) (at most 2^15 itself)
+            const uint32_t z = (t8 & 4 ? (t8 & 2 ? m[3] : m[2]) : (t8 & 2 ? m[1] : m[0])) >> (t8 & 1) * 16 & 0x7fffu;
+            const uint32_t x = min(44u - (z >> 10), 30u), at = (e & 3) * 128 + 32 * sp + 8 * f8 + t8;
+            reinterpret_cast<uint32_t*>(tab + C::tN)[at] = x << 10 | x << 26;
+            tab[C::tV + (e & 7) * 128 + (at & 127)] = s_up * __uint_as_float((142u - x) << 23);
+            full.next();
+            done(kSizes + (e & 3));
+            return true;
+        };
+        if (DT == 0) ok = sizes(0) && (n < 2 || sizes(1));
+        if (STATE && DT == 0)
+            #pragma unroll 1
+            for (c = 2; ok && c < n; ++c) ok = sizes(c);
         #pragma unroll 1
-        for (; !STATE && c < n; ++c) {
+        for (; !STATE && ok && c < n; ++c) {
             ok = rest(bar + kScDone + (c & 1), (c >> 1) & 1, fail);
             if (ok && c >= 2) ok = rest(bar + kPvDone + (c & 1), ((c - 2) >> 1) & 1, fail);  // the buffer's last P has been used
             if (!ok) break;
@@ -550,6 +593,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             tc::fence_proxy_async();
             tc::fence_before();
             done(kPReady + (c & 1));
+            if (DT == 0 && c + 2 < n) ok = sizes(c + 2);
         }
     } else if (warp < 28) {
         // ---------------------------------------------------------------- O
@@ -831,7 +875,7 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
     static PerDevice c0, c1;
     constexpr size_t bytes = Cfg<DK, DV>::BYTES;
     static_assert(bytes <= 232448, "shared memory");
-    static_assert(kBars * 8 <= 256, "barriers");
+    static_assert(kBars * 8 <= 288, "barriers");
     cudaError_t e = opt_in(linattn_walk_kernel<DT, DK, DV, false>, bytes, c0);
     if (e == cudaSuccess) e = opt_in(linattn_walk_kernel<DT, DK, DV, true>, bytes, c1);
     if (e != cudaSuccess) return e;
