@@ -9,15 +9,19 @@
 // bandwidth for whole batches and launch latency for single tokens.  Split: a row
 // belongs to G lanes that hold NV runs of 8 consecutive features (a 16-byte load
 // each): whole rows stay in registers, so nothing is read twice.  Up to 1024
-// features G is at most a warp and the row's sums are shuffles; wider rows take a
-// CTA, whose warps' sums meet in shared memory.  A group takes RB rows at a time:
-// their loads are in flight together and their sums share the barriers.
+// features G is at most a warp and the row's sums are shuffles; wider rows take half
+// of a CTA or all of it, whose warps' sums meet in shared memory.  Few lanes with two
+// runs each cost fewer shuffles and instructions than many with one (2097152 rows of
+// 32 features: 48 us, 62 us with four lanes of one run).  The grid is what the SMs
+// hold at once: the weights are read once a CTA and stay in registers, and the next
+// rows' loads are in flight while the current ones are worked (131072 rows of 768
+// features: forward 65 us, 6.2 TB/s; 95 us with a CTA for every 16 rows).
 #include "views.h"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "mma.cuh"
+#include "tile.cuh"
 
 namespace fftconv {
 namespace {
@@ -34,31 +38,41 @@ struct NormArgs {
     float* part;       // [parts][2][H][D] partial weight gradients, or null
 };
 
+using tile::fma2;
+using tile::mul2;
+using tile::sub2;
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return fma2(a, make_float2(1.0f, 1.0f), b); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Eight values as four pairs: the arithmetic is in packed float32 pairs, which halves
+// the instructions that a row costs.
 template <int DT>
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& u, float2 (&x)[4]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const cpx c = Op<DT>::unpack(w[i]);
-        x[2 * i] = c.r;
-        x[2 * i + 1] = c.i;
+        x[i] = make_float2(c.r, c.i);
     }
 }
 
 template <int DT>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(Op<DT>::pack(x[0], x[1]), Op<DT>::pack(x[2], x[3]), Op<DT>::pack(x[4], x[5]),
-                      Op<DT>::pack(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+    return make_uint4(Op<DT>::pack(x[0].x, x[0].y), Op<DT>::pack(x[1].x, x[1].y), Op<DT>::pack(x[2].x, x[2].y),
+                      Op<DT>::pack(x[3].x, x[3].y));
 }
 
-__device__ __forceinline__ void load8(const float* p, bool vec, float (&x)[8]) {
+__device__ __forceinline__ void load8(const float* p, bool vec, float2 (&x)[4]) {
     if (vec) {
         const float4 u = __ldg(reinterpret_cast<const float4*>(p)), v = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+        x[0] = make_float2(u.x, u.y);
+        x[1] = make_float2(u.z, u.w);
+        x[2] = make_float2(v.x, v.y);
+        x[3] = make_float2(v.z, v.w);
     } else {
         #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __ldg(p + j);
+        for (int j = 0; j < 4; ++j) x[j] = make_float2(__ldg(p + 2 * j), __ldg(p + 2 * j + 1));
     }
 }
 
@@ -70,7 +84,6 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[8]) {
         #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     if constexpr (G > 32) {
-        static_assert(G == kThreads, "a row takes the CTA");
         __syncthreads();  // the last sums have been read
         if (threadIdx.x % 32 == 0)
             #pragma unroll
@@ -78,121 +91,141 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[8]) {
         __syncthreads();
         #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float4 a = *reinterpret_cast<const float4*>(red[i]), b = *reinterpret_cast<const float4*>(red[i] + 4);
-            v[i] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+            const float* p = red[i] + threadIdx.x / G * (G / 32);
+            float4 a = *reinterpret_cast<const float4*>(p);
+            v[i] = (a.x + a.y) + (a.z + a.w);
+            if constexpr (G == 256) {
+                a = *reinterpret_cast<const float4*>(p + 4);
+                v[i] += (a.x + a.y) + (a.z + a.w);
+            }
         }
     }
 }
 
-template <int DT, int G, int NV, int RB, bool BWD>
-__global__ void __launch_bounds__(kThreads) layernorm_kernel(const NormArgs a) {
-    constexpr int NG = kThreads / G;
+// Rows that a group takes at a time, and CTAs that an SM holds: as many rows as the
+// registers of two CTAs hold.  The backward's two sums for each feature leave room
+// for one row of two runs, or for one CTA (131072 rows of 768 features in two CTAs
+// of one row: 178 us; in one of two rows 111 us).
+__host__ __device__ constexpr int rows_at_once(int G, int NV, bool bwd) { return bwd ? (G == 32 && NV == 3 ? 2 : 1) : (NV <= (G <= 32 ? 3 : 2) ? 2 : 1); }
+__host__ __device__ constexpr int ctas_per_sm(int NV, bool bwd) { return bwd && NV > 2 ? 1 : 2; }
+
+template <int DT, int G, int NV, bool BWD>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NV, BWD)) layernorm_kernel(const NormArgs a) {
+    constexpr int NG = kThreads / G, RB = rows_at_once(G, NV, BWD);
     __shared__ __align__(16) float red[G > 32 ? 2 * RB : 1][8];
     const int lane = threadIdx.x % G, grp = threadIdx.x / G;
     const int h = blockIdx.x % a.H, part = blockIdx.x / a.H;
     int f[NV];
     bool on[NV];
-    float w[NV][8], b[BWD ? 1 : NV][8];
+    float2 w[NV][4], b[BWD ? 1 : NV][4];
     #pragma unroll
     for (int v = 0; v < NV; ++v) {
         f[v] = (v * G + lane) * 8;
         on[v] = f[v] < a.D;
         #pragma unroll
-        for (int j = 0; j < 8; ++j) w[v][j] = 1.0f;
+        for (int j = 0; j < 4; ++j) w[v][j] = both(1.0f);
         if (a.w && on[v]) load8(a.w + int64_t(h) * a.D + f[v], a.vec, w[v]);
         if constexpr (!BWD) {
             #pragma unroll
-            for (int j = 0; j < 8; ++j) b[v][j] = 0.0f;
+            for (int j = 0; j < 4; ++j) b[v][j] = both(0.0f);
             if (a.b && on[v]) load8(a.b + int64_t(h) * a.D + f[v], a.vec, b[v]);
         }
     }
-    float aw[BWD ? NV : 1][8] = {}, ab[BWD ? NV : 1][8] = {};
-    for (uint32_t base = uint32_t(part) * (NG * RB); base < a.rows; base += uint32_t(a.parts) * (NG * RB)) {
-        uint4 ux[RB][NV], ud[BWD ? RB : 1][NV];
-        int64_t yo[RB];
-        bool live[RB];
+    float2 aw[BWD ? NV : 1][4] = {}, ab[BWD ? NV : 1][4] = {};
+    // where row r of this group starts in a view, in elements
+    auto at = [&](const View& v, uint32_t r) {
+        const uint32_t bi = r / a.T;
+        return bi * v.b + int64_t(r - bi * a.T) * v.t + h * v.h;
+    };
+    uint4 ux[RB][NV], ud[BWD ? RB : 1][NV];
+    auto fetch = [&](uint32_t base) {
         #pragma unroll
         for (int i = 0; i < RB; ++i) {
             const uint32_t r = base + i * NG + grp;
-            live[i] = r < a.rows;
-            const uint32_t bi = live[i] ? r / a.T : 0;
-            const int64_t t = live[i] ? r - bi * a.T : 0;
-            const uint16_t* px = reinterpret_cast<const uint16_t*>(a.x.p) + bi * a.x.b + t * a.x.t + h * a.x.h;
-            const uint16_t* pd = BWD ? reinterpret_cast<const uint16_t*>(a.dy.p) + bi * a.dy.b + t * a.dy.t + h * a.dy.h : nullptr;
-            yo[i] = bi * a.y.b + t * a.y.t + h * a.y.h;
+            const bool in = r < a.rows;
+            const uint16_t* px = reinterpret_cast<const uint16_t*>(a.x.p) + (in ? at(a.x, r) : 0);
+            const uint16_t* pd = BWD ? reinterpret_cast<const uint16_t*>(a.dy.p) + (in ? at(a.dy, r) : 0) : nullptr;
             #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                ux[i][v] = live[i] && on[v] ? *reinterpret_cast<const uint4*>(px + f[v]) : make_uint4(0, 0, 0, 0);
-                if constexpr (BWD) ud[i][v] = live[i] && on[v] ? *reinterpret_cast<const uint4*>(pd + f[v]) : make_uint4(0, 0, 0, 0);
+                ux[i][v] = in && on[v] ? *reinterpret_cast<const uint4*>(px + f[v]) : make_uint4(0, 0, 0, 0);
+                if constexpr (BWD) ud[i][v] = in && on[v] ? *reinterpret_cast<const uint4*>(pd + f[v]) : make_uint4(0, 0, 0, 0);
             }
         }
-        float s[BWD ? 2 * RB : RB] = {};
+    };
+    const uint32_t step = uint32_t(a.parts) * (NG * RB);
+    uint32_t base = uint32_t(part) * (NG * RB);
+    if (base < a.rows) fetch(base);
+    for (; base < a.rows; base += step) {
+        // the rows as float32; the next ones are fetched while these are worked
+        float2 x[RB][NV][4], d[BWD ? RB : 1][NV][4];
         #pragma unroll
-        for (int i = 0; i < RB; ++i) {
+        for (int i = 0; i < RB; ++i)
             #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                float x[8];
-                unpack8<DT>(ux[i][v], x);
-                #pragma unroll
-                for (int j = 0; j < 8; ++j) s[i] += x[j];
-                if constexpr (BWD) {
-                    unpack8<DT>(ud[i][v], x);
-                    #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[RB + i] = fmaf(x[j], w[v][j], s[RB + i]);
-                }
+                unpack8<DT>(ux[i][v], x[i][v]);
+                if constexpr (BWD) unpack8<DT>(ud[i][v], d[i][v]);
             }
+        if (base + step < a.rows) fetch(base + step);
+        float s[BWD ? 2 * RB : RB];
+        #pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            float2 p = both(0.0f), q = p;
+            #pragma unroll
+            for (int v = 0; v < NV; ++v)
+                #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    p = add2(p, x[i][v][j]);
+                    if constexpr (BWD) q = fma2(d[i][v][j], w[v][j], q);
+                }
+            s[i] = p.x + p.y;
+            if constexpr (BWD) s[RB + i] = q.x + q.y;
         }
         row_sums<G>(s, red);
-        float q[BWD ? 2 * RB : RB] = {}, m[RB], mz[RB];
+        float e[BWD ? 2 * RB : RB], mz[RB];
         #pragma unroll
         for (int i = 0; i < RB; ++i) {
-            m[i] = s[i] / float(a.D);  // exact for rows of equal values, as their sums are
+            const float m = s[i] / float(a.D);  // exact for rows of equal values, as their sums are
             if constexpr (BWD) mz[i] = s[RB + i] * a.c;
+            float2 p = both(0.0f), q = p;
             #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 if (!on[v]) continue;
-                float x[8];
-                unpack8<DT>(ux[i][v], x);
                 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[j] -= m[i];
-                    q[i] = fmaf(x[j], x[j], q[i]);
-                }
-                if constexpr (BWD) {
-                    float d[8];
-                    unpack8<DT>(ud[i][v], d);
-                    #pragma unroll
-                    for (int j = 0; j < 8; ++j) q[RB + i] = fmaf(d[j] * w[v][j], x[j], q[RB + i]);
+                for (int j = 0; j < 4; ++j) {
+                    float2& y = x[i][v][j];
+                    y = sub2(y, both(m));
+                    p = fma2(y, y, p);
+                    if constexpr (BWD) q = fma2(mul2(d[i][v][j], w[v][j]), y, q);
                 }
             }
+            e[i] = p.x + p.y;
+            if constexpr (BWD) e[RB + i] = q.x + q.y;
         }
-        row_sums<G>(q, red);
+        row_sums<G>(e, red);
         #pragma unroll
         for (int i = 0; i < RB; ++i) {
-            if (!live[i]) continue;
-            const float r = rsqrtf(fmaf(q[i], a.c, a.eps));
-            uint16_t* py = reinterpret_cast<uint16_t*>(a.y.p) + yo[i];
+            const uint32_t row = base + i * NG + grp;
+            if (row >= a.rows) continue;
+            const float r = rsqrtf(fmaf(e[i], a.c, a.eps));
+            uint16_t* py = reinterpret_cast<uint16_t*>(a.y.p) + at(a.y, row);
             #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 if (!on[v]) continue;
-                float x[8];
-                unpack8<DT>(ux[i][v], x);
+                float2 (&y)[4] = x[i][v];
                 if constexpr (!BWD) {
                     #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = fmaf((x[j] - m[i]) * r, w[v][j], b[v][j]);
+                    for (int j = 0; j < 4; ++j) y[j] = fma2(mul2(y[j], both(r)), w[v][j], b[v][j]);
                 } else {
-                    const float mh = q[RB + i] * a.c * r;  // mean of dz h
-                    float d[8];
-                    unpack8<DT>(ud[i][v], d);
+                    const float2 mh = both(-e[RB + i] * a.c * r * r), mr = both(-mz[i] * r);  // - mean(dz h) r, - mean(dz) r
                     #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float hh = (x[j] - m[i]) * r;
-                        aw[v][j] = fmaf(d[j], hh, aw[v][j]);
-                        ab[v][j] += d[j];
-                        x[j] = r * (fmaf(d[j], w[v][j], -mz[i]) - hh * mh);
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 hh = mul2(y[j], both(r)), z = d[i][v][j];
+                        aw[v][j] = fma2(z, hh, aw[v][j]);
+                        ab[v][j] = add2(ab[v][j], z);
+                        y[j] = fma2(hh, mh, fma2(mul2(z, w[v][j]), both(r), mr));
                     }
                 }
-                *reinterpret_cast<uint4*>(py + f[v]) = pack8<DT>(x);
+                *reinterpret_cast<uint4*>(py + f[v]) = pack8<DT>(y);
             }
         }
     }
@@ -205,9 +238,9 @@ __global__ void __launch_bounds__(kThreads) layernorm_kernel(const NormArgs a) {
             for (int v = 0; v < NV; ++v) {
                 if (!on[v]) continue;
                 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    out[f[v] + j] = aw[v][j];
-                    out[hd + f[v] + j] = ab[v][j];
+                for (int j = 0; j < 4; ++j) {
+                    *reinterpret_cast<float2*>(out + f[v] + 2 * j) = aw[v][j];
+                    *reinterpret_cast<float2*>(out + hd + f[v] + 2 * j) = ab[v][j];
                 }
             }
         } else {
@@ -219,7 +252,10 @@ __global__ void __launch_bounds__(kThreads) layernorm_kernel(const NormArgs a) {
                 #pragma unroll
                 for (int v = 0; v < NV; ++v)
                     #pragma unroll
-                    for (int j = 0; j < 8; ++j) sums[grp][f[v] + j] = k ? ab[v][j] : aw[v][j];
+                    for (int j = 0; j < 4; ++j) {
+                        sums[grp][f[v] + 2 * j] = k ? ab[v][j].x : aw[v][j].x;
+                        sums[grp][f[v] + 2 * j + 1] = k ? ab[v][j].y : aw[v][j].y;
+                    }
                 __syncthreads();
                 for (int i = threadIdx.x; i < a.D; i += kThreads) {
                     float v = 0.0f;
@@ -250,51 +286,45 @@ __global__ void __launch_bounds__(kThreads) layernorm_sum_kernel(const float* pa
     if (out) out[i < hd ? i : i - hd] = v;
 }
 
-// How a row of D features is held: G lanes of NV runs, RB rows at a time.
+// How a row of D features is held: G lanes of NV runs of 8.
 struct Shape {
-    int G, NV, RB;
+    int G, NV;
 };
 
 Shape shape_of(int D) {
     const int n = D / 8;
-    if (n <= 4) return {4, 1, 4};
-    if (n <= 8) return {8, 1, 4};
-    if (n <= 16) return {16, 1, 4};
-    if (n <= 128) return {32, (n + 31) / 32, n <= 32 ? 4 : (n <= 96 ? 2 : 1)};
-    return {kThreads, (n + kThreads - 1) / kThreads, n <= 512 ? 2 : 1};
+    for (int G = 2; G <= 32; G *= 2)
+        if (n <= 2 * G) return {G, 2};
+    if (n <= 128) return {32, (n + 31) / 32};
+    if (n <= 512) return {128, (n + 127) / 128};
+    return {256, (n + 255) / 256};
 }
 
-// CTAs that share a head in the backward, at most: each leaves a partial sum.
-constexpr int kMaxGrid = 152 * 2;
-
+// CTAs that share a head: what fills the SMs, or what the rows need.
 int parts_of(const fftconv_layernorm_args_t* p, bool backward) {
     const Shape s = shape_of(p->D);
-    const int64_t rows = p->B * p->T, per = int64_t(kThreads / s.G) * s.RB;
-    const int64_t need = (rows + per - 1) / per;
-    if (!backward) return int(need);
-    const int64_t most = (kMaxGrid + p->H - 1) / p->H;
-    return int(need < most ? need : most);
+    const int64_t per = int64_t(kThreads / s.G) * rows_at_once(s.G, s.NV, backward);
+    const int64_t need = (p->B * p->T + per - 1) / per, most = 152 * ctas_per_sm(s.NV, backward) / p->H;
+    return int(need < most ? need : (most > 0 ? most : 1));
 }
 
 template <int DT, bool BWD>
 void launch(const NormArgs& a, cudaStream_t st) {
     const Shape s = shape_of(a.D);
     const unsigned grid = unsigned(a.parts) * unsigned(a.H);
-    switch (s.G) {
-        case 4: layernorm_kernel<DT, 4, 1, 4, BWD><<<grid, kThreads, 0, st>>>(a); break;
-        case 8: layernorm_kernel<DT, 8, 1, 4, BWD><<<grid, kThreads, 0, st>>>(a); break;
-        case 16: layernorm_kernel<DT, 16, 1, 4, BWD><<<grid, kThreads, 0, st>>>(a); break;
-        case 32:
-            if (s.NV == 1) layernorm_kernel<DT, 32, 1, 4, BWD><<<grid, kThreads, 0, st>>>(a);
-            else if (s.NV == 2) layernorm_kernel<DT, 32, 2, 2, BWD><<<grid, kThreads, 0, st>>>(a);
-            else if (s.NV == 3) layernorm_kernel<DT, 32, 3, 2, BWD><<<grid, kThreads, 0, st>>>(a);
-            else layernorm_kernel<DT, 32, 4, 1, BWD><<<grid, kThreads, 0, st>>>(a);
-            break;
-        default:
-            if (s.NV == 1) layernorm_kernel<DT, kThreads, 1, 2, BWD><<<grid, kThreads, 0, st>>>(a);
-            else if (s.NV == 2) layernorm_kernel<DT, kThreads, 2, 2, BWD><<<grid, kThreads, 0, st>>>(a);
-            else if (s.NV == 3) layernorm_kernel<DT, kThreads, 3, 1, BWD><<<grid, kThreads, 0, st>>>(a);
-            else layernorm_kernel<DT, kThreads, 4, 1, BWD><<<grid, kThreads, 0, st>>>(a);
+    switch (s.G * 8 + s.NV) {
+        case 2 * 8 + 2: layernorm_kernel<DT, 2, 2, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 4 * 8 + 2: layernorm_kernel<DT, 4, 2, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 8 * 8 + 2: layernorm_kernel<DT, 8, 2, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 16 * 8 + 2: layernorm_kernel<DT, 16, 2, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 32 * 8 + 2: layernorm_kernel<DT, 32, 2, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 32 * 8 + 3: layernorm_kernel<DT, 32, 3, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 32 * 8 + 4: layernorm_kernel<DT, 32, 4, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 128 * 8 + 2: layernorm_kernel<DT, 128, 2, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 128 * 8 + 3: layernorm_kernel<DT, 128, 3, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 128 * 8 + 4: layernorm_kernel<DT, 128, 4, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        case 256 * 8 + 3: layernorm_kernel<DT, 256, 3, BWD><<<grid, kThreads, 0, st>>>(a); break;
+        default: layernorm_kernel<DT, 256, 4, BWD><<<grid, kThreads, 0, st>>>(a);
     }
 }
 
