@@ -280,10 +280,12 @@ bool encode(const fftconv_linattn_s* p, const Call& c, CUtensorMap* m, const Ten
     return encode_tokens_map(m, t.v, c.B, c.T, t.heads, t.D, p->dtype);
 }
 
-Passes passes_of(const fftconv_linattn_s* p, const Scratch& l) {
+Passes passes_of(const fftconv_linattn_s* p, const fftconv_linattn_args_t* x, const Scratch& l) {
     Passes a{};
     a.seg_chunks = l.seg.chunks;
     a.segments = l.seg.count;
+    a.join = l.seg.join;
+    a.longest_first = x->offsets && l.seg.count == x->nseq && x->nseq <= 32;
     a.err = p->dev_err;
     return a;
 }
@@ -395,7 +397,7 @@ extern "C" fftconv_status_t fftconv_linattn_forward(fftconv_linattn_t p, const f
                              : cudaMemsetAsync(state_out, 0, sb, st));
     }
     if (l.seg.count >= (int64_t(1) << 30) / c.Hv) return FFTCONV_ERR_UNSUPPORTED;
-    Passes a = passes_of(p, l);
+    Passes a = passes_of(p, args, l);
     Pass& x = a.p[0];
     x.w = walk_of(args, c, false);
     x.w.gq = x.w.gk = c.group;
@@ -411,6 +413,7 @@ extern "C" fftconv_status_t fftconv_linattn_forward(fftconv_linattn_t p, const f
     if (!c.nseq) return done(r);
     if (r == cudaSuccess && l.cut(c.nseq)) {
         r = launch_linattn(a, 1, true, p->dtype, p->Dk, p->Dv, st);
+        if (a.join) x.w.state_fin = state_out;
         x.w.state_out = nullptr;  // the segments' walk has written them
     }
     if (r == cudaSuccess) r = launch_linattn(a, 1, false, p->dtype, p->Dk, p->Dv, st);
@@ -467,7 +470,7 @@ extern "C" fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t p, const 
     float* dq32 = shared ? reinterpret_cast<float*>(at + l.q) : nullptr;
     float* dk32 = shared ? reinterpret_cast<float*>(at + l.k) : nullptr;
     // dQ and dK in tensors of Dv x Dk, dV of Dk x Dv: one launch where that is the same
-    Passes a = passes_of(p, l);
+    Passes a = passes_of(p, args, l);
     Pass &xq = a.p[0], &xk = a.p[1], &xv = a.p[2];
     xq.w = walk_of(args, c, false);
     xq.w.gv = c.group;
@@ -519,6 +522,7 @@ extern "C" fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t p, const 
         const bool same = p->Dk == p->Dv;
         if (r == cudaSuccess && l.cut(c.nseq)) {
             r = launch_linattn(b, 2, true, p->dtype, p->Dk, p->Dv, st);
+            if (a.join) xv.w.state_fin = only_dv.p[0].w.state_fin = d_state_in;
             xv.w.state_out = only_dv.p[0].w.state_out = nullptr;  // the segments' walk has written them
         }
         if (r == cudaSuccess) r = launch_linattn(a, same ? 3 : 2, false, p->dtype, p->Dv, p->Dk, st);

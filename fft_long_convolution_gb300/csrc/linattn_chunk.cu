@@ -184,7 +184,8 @@ struct Part {
     int64_t tok0;  // its first token in the row
     int64_t left;  // tokens from there to the sequence's end
     int n;         // chunks
-    bool first, last;  // in the walk's order
+    int before;        // segments before it in the walk's order
+    bool first, last;  // in that order
 };
 
 __device__ __forceinline__ bool find_part(const Walk& w, uint32_t L, uint32_t slot, Part* p) {
@@ -202,9 +203,26 @@ __device__ __forceinline__ bool find_part(const Walk& w, uint32_t L, uint32_t sl
     p->first = w.reverse ? high : low;
     p->last = w.reverse ? low : high;
     p->n = int(high ? all - from : L);
+    p->before = int(w.reverse ? (all + L - 1) / L - 1 - seg : seg);
     p->tok0 = p->s.start + from * kChunk;
     p->left = p->s.len - from * kChunk;
     return true;
+}
+
+// The sequence of a given rank by length, of up to 32: a lane for each.  All lanes of a
+// warp.  Sequences that are not cut start in this order, as the longest one ends the
+// launch: 24 sequences of 1 to 2000 tokens with 12 heads take 75 us, in the order of the
+// row 94.  More than 32 even out by themselves.
+__device__ __forceinline__ int by_length(const Walk& w, int rank) {
+    const int lane = threadIdx.x % 32;
+    const int len = lane < w.nseq ? int(locate(w.offsets, w.T, lane).len) : -1;
+    int longer = 0;
+    #pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+        const int y = __shfl_sync(0xffffffffu, len, i);
+        longer += y > len || (y == len && i < lane);
+    }
+    return __ffs(__ballot_sync(0xffffffffu, longer == rank)) - 1;
 }
 
 // STATE: only the state at the end of a segment (from zero, or from the initial state);
@@ -220,10 +238,17 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 288);
     volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 292);
     float* tab = reinterpret_cast<float*>(sm + C::oT);
-    const Pass& x = a.p[blockIdx.z];
+    int slot = blockIdx.x, h = blockIdx.y, z = blockIdx.z;
+    if (a.longest_first) {  // all heads of a sequence before the next sequence
+        slot += gridDim.x * (h + gridDim.y * z);
+        h = slot % gridDim.y;
+        slot /= gridDim.y;
+        z = slot % gridDim.z;
+        slot /= gridDim.z;
+    }
+    const Pass& x = a.p[z];
     const Walk& wk = x.w;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    const int h = blockIdx.y;
     // out of the indexed parameter once, not at every use
     const bool reverse = wk.reverse, packed = wk.offsets != nullptr;
     float* o32 = wk.o32;
@@ -238,7 +263,8 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         Part* found = reinterpret_cast<Part*>(sm + C::oO);
         bool* any = reinterpret_cast<bool*>(found + 1);
         if (warp == 0) {
-            live = find_part(wk, uint32_t(a.seg_chunks), blockIdx.x, &p);
+            if (a.longest_first) slot = by_length(wk, slot);
+            live = find_part(wk, uint32_t(a.seg_chunks), slot, &p);
             if (lane == 0) *found = p, *any = live;
         }
         __syncthreads();
@@ -248,9 +274,11 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     }
     if (!live || (STATE && p.last && !wk.state_out)) return;
     const int n = p.n;
-    const int64_t hs = int64_t(p.i) * wk.H + h, gs = int64_t(blockIdx.x) * wk.H + h;
+    const int64_t hs = int64_t(p.i) * wk.H + h, gs = int64_t(slot) * wk.H + h;
     const float* sin = wk.state_in ? wk.state_in + hs * DK * DV : nullptr;
-    if (!p.first) sin = STATE ? nullptr : x.seg_state + (gs + (reverse ? wk.H : -wk.H)) * DK * DV;
+    // what the walk's segment before left, and the way to those before it
+    const int64_t back = (reverse ? 1 : -1) * int64_t(wk.H) * DK * DV;
+    if (!p.first) sin = STATE ? nullptr : x.seg_state + gs * DK * DV + back;
     float* sout = p.last && wk.state_out ? wk.state_out + hs * DK * DV : nullptr;
     if (STATE && !p.last) sout = x.seg_state + gs * DK * DV;
     // w V in three parts (bf16) where the state at the end is wanted for itself
@@ -323,14 +351,30 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     } else if (warp < 16) {
         // ---------------------------------------------------------------- S
         const int dv = row % DV, quarter = warp >> 2, k0 = quarter * NC;
-        float2 S[NC / 2];
-        #pragma unroll
-        for (int j = 0; j < NC / 2; ++j) {
-            S[j] = make_float2(0.0f, 0.0f);
-            const int k = k0 + 2 * j;
-            if (sin)
-                S[j] = wk.turned ? *reinterpret_cast<const float2*>(sin + dv * DK + k)
-                                 : make_float2(sin[k * DV + dv], sin[(k + 1) * DV + dv]);
+        float2 S[NC / 2] = {};
+        // the state before: one that is given or joined, or the end states of all segments
+        // before, the first one first
+        const bool join = !STATE && !p.first && a.join;
+        const Decay over = decay_over(g, float(a.seg_chunks * kChunk));
+        #pragma unroll 1
+        for (int i = join ? p.before : 1; sin && i > 0; --i) {
+            const float* from = sin + (i - 1) * back;
+            #pragma unroll
+            for (int j = 0; j < NC / 2; ++j) {
+                const int k = k0 + 2 * j;
+                const float2 N = wk.turned ? *reinterpret_cast<const float2*>(from + dv * DK + k)
+                                           : make_float2(from[k * DV + dv], from[(k + 1) * DV + dv]);
+                S[j] = make_float2(decayed(over, S[j].x, N.x), decayed(over, S[j].y, N.y));
+            }
+        }
+        if (join && p.last && wk.state_fin && row < DV) {  // and the sequence's final state
+            float* out = wk.state_fin + hs * DK * DV + dv;
+            const Decay rest_of = decay_over(g, float(all));
+            #pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                float& y = out[(k0 + j) * DV];
+                y = decayed(rest_of, j & 1 ? S[j / 2].y : S[j / 2].x, y);
+            }
         }
         const Decay whole = decay_over(g, float(kChunk));
         const Decay last = decay_over(g, float(tokens(reverse ? 0 : n - 1)));
@@ -882,6 +926,7 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
     const dim3 grid(unsigned(a.segments), unsigned(a.p[0].w.H), unsigned(n));
     if (states) {
         linattn_walk_kernel<DT, DK, DV, true><<<grid, Cfg<DK, DV>::THREADS, bytes, st>>>(a);
+        if (a.join) return cudaGetLastError();
         constexpr int size = DK * DV;
         linattn_join_kernel<<<dim3(unsigned(a.p[0].w.nseq) * (size / 1024), grid.y, grid.z), 256, 0, st>>>(a, size);
     } else {
@@ -897,11 +942,15 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
 // states (0.6 of a walk's step for a chunk) and a join.  The rule counts waves of CTAs
 // over the SMs in steps of a walk, takes the two more launches as 8, and cuts when that
 // saves a tenth.  Packed rows are taken at their mean length, as the host does not know
-// their offsets.
+// their offsets.  The walks' CTAs join up to three segments themselves (8 rows of 4096,
+// 6 heads of 128, two segments: 99 us with the inputs from memory, against 107 with the
+// join's launch; four segments: 128 against 129; six: 121 against 105, as the reads of
+// the states before follow one another).
 void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int sms) {
     const int64_t slots = chunk_slots(B, T, nseq), rows = nseq * heads;
     s->chunks = slots + 1;
     s->count = nseq;
+    s->join = false;
     if (rows == 0) return;
     const int64_t n = (B * T / nseq + kChunk - 1) / kChunk;
     auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
@@ -917,6 +966,7 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
     if (best == 1) return;
     s->chunks = (n + best - 1) / best;
     s->count = slots / s->chunks + nseq;
+    s->join = best <= 3;
 }
 
 cudaError_t launch_linattn(const Passes& a, int n, bool states, int dt, int dk, int dv, cudaStream_t st) {
