@@ -325,6 +325,9 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     const int sp = warp & 3;
     const uint32_t lanes = tm + (uint32_t(32 * sp) << 16);  // this warp's tensor-memory lanes
     const int row = 32 * sp + lane;                         // this thread's lane
+    // 64 value features: nothing is written to the upper lanes and nothing read from them,
+    // as each lane's products are its own; their warps only keep step
+    const bool mine = 32 * sp < DV;
     // one arrival per warp, after every lane's work
     auto done = [&](int b) {
         __syncwarp();
@@ -350,14 +353,14 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             }
     } else if (warp < 16) {
         // ---------------------------------------------------------------- S
-        const int dv = row % DV, quarter = warp >> 2, k0 = quarter * NC;
+        const int dv = row, quarter = warp >> 2, k0 = quarter * NC;
         float2 S[NC / 2] = {};
         // the state before: one that is given or joined, or the end states of all segments
         // before, the first one first
         const bool join = !STATE && !p.first && a.join;
         const Decay over = decay_over(g, float(a.seg_chunks * kChunk));
         #pragma unroll 1
-        for (int i = join ? p.before : 1; sin && i > 0; --i) {
+        for (int i = join ? p.before : 1; mine && sin && i > 0; --i) {
             const float* from = sin + (i - 1) * back;
             #pragma unroll
             for (int j = 0; j < NC / 2; ++j) {
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                 S[j] = make_float2(decayed(over, S[j].x, N.x), decayed(over, S[j].y, N.y));
             }
         }
-        if (join && p.last && wk.state_fin && row < DV) {  // and the sequence's final state
+        if (join && p.last && wk.state_fin && mine) {  // and the sequence's final state
             float* out = wk.state_fin + hs * DK * DV + dv;
             const Decay rest_of = decay_over(g, float(all));
             #pragma unroll
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             const float* wt = tab + C::tW + (tokens(e) < kChunk ? 64 : 0) + 32 * side + 2 * (lane & 3);
             const uint32_t to = w_at + C::w(STATE, true, e) + 16 * side;
             #pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; mine && b < 2; ++b) {
                 uint32_t v[4], hi[4], lo[4], l2[4];
                 block(full.st, 2 * side + b, v);
                 #pragma unroll
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                 sc[1] = z[8];
             }
             #pragma unroll 1
-            for (int b = 0; b < 4; b += 2) {
+            for (int b = 0; mine && b < 4; b += 2) {
                 uint32_t v[8], hi[8], lo[8];
                 block(full.st, b, v);
                 block(full.st, b + 1, v + 4);
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         // S for step e, after S Q of the step before
         auto put = [&](int e) {
             float2 sc = make_float2(1.0f, 1.0f);
-            if constexpr (DT == 0) {
+            if (DT == 0 && mine) {
                 float m = 0.0f;
                 #pragma unroll
                 for (int j = 0; j < NC / 2; ++j) m = fmaxf(m, fmaxf(fabsf(S[j].x), fabsf(S[j].y)));
@@ -472,6 +475,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             if (DT == 0 && quarter == 0) tab[C::tS + (e & 1) * 128 + row] = sc.y;
             #pragma unroll
             for (int b = 0; b < NC; b += 16) {
+                if (!mine) break;
                 uint32_t y[8];
                 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -496,6 +500,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             if constexpr (DT == 0) inv = tab[C::tV + (e & 7) * 128 + row];
             #pragma unroll
             for (int b = 0; b < NC; b += 16) {
+                if (!mine) break;
                 uint32_t y[16];
                 ld16(lanes + C::kv(STATE, e) + k0 + b, y);
                 tc::wait_ld();
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                 if (ok && c + 1 < n && ((c + 1) & 1) == side) ok = weigh(c + 1);
             }
         }
-        if (ok && sout && row < DV) {
+        if (ok && sout && mine) {
             #pragma unroll
             for (int j = 0; j < NC / 2; ++j) {
                 sout[(k0 + 2 * j) * DV + dv] = S[j].x;
@@ -556,6 +561,11 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         Ring<C::NST> full;
         auto sizes = [&](int e) {
             if (!rest(bar + kFull + full.st, full.parity, fail)) return false;
+            if (!mine) {
+                full.next();
+                done(kSizes + (e & 3));
+                return true;
+            }
             const int f8 = lane & 3, t8 = lane >> 2;
             const uint8_t* v = sm + full.st * C::STAGE + C::sV + (sp >> 1) * kTile + t8 * 1024;
             uint32_t m[4] = {};
@@ -643,7 +653,6 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         // ---------------------------------------------------------------- O
         // 16 features a warp, 32 tokens at a time
         const int q = lane >> 2, r = lane & 3, hf = (warp >> 2) & 1, f = 32 * sp + 16 * hf + q;
-        const bool mine = 32 * sp < DV;
         const int piece = (sp & 1) * 4 + hf * 2 + ((lane >> 3) & 1);
         const uint32_t stage = sb + C::oO + (sp >> 1) * kTile + ((lane >> 4) * 8 + (lane & 7)) * 128 + ((piece ^ (lane & 7)) * 16);
         const int o32_token = wk.H * DV;
@@ -654,6 +663,11 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             if (ok && !o32 && c > 0) ok = rest(bar + kOFree, (c - 1) & 1, fail);  // the last O has left shared memory
             if (!ok) break;
             tc::fence_after();
+            if (!mine) {
+                done(kORead + (c & 1));
+                if (!o32) done(kOReady);
+                continue;
+            }
             const int m = tokens(c);
             const float* ut = tab + C::tU + (m < kChunk ? 64 : 0) + 2 * r;
             const float* pt = tab + C::tP + (c & 1) * 64 + 2 * r;
@@ -694,7 +708,6 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
                     tc::fence_before();
                     done(kORead + (c & 1));
                 }
-                if (!mine) continue;
                 if (o32) {
                     float* to = o32 + int64_t(chunk(c)) * kChunk * o32_token;
                     #pragma unroll
@@ -734,20 +747,20 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             if (c >= C::NST && !(ok = rest(bar + kFree + st, ring.parity ^ 1, fail))) break;
             uint64_t* full = tail ? bar + kRaw : bar + kFull + st;
             if (elect()) {
-                mbar_expect_tx(full, STATE ? C::STAGE - C::KT * kTile : C::STAGE);
+                mbar_expect_tx(full, C::STAGE - (STATE ? C::KT * kTile : 0) - (2 - DV / 64) * kTile);
                 #pragma unroll
                 for (int f = 0; f < C::KT; ++f) {
                     tma_load_4d(smem_u32(to) + C::sK + f * kTile, &x.mk, f * 64, h / wk.gk, t0, row0, full);
                     if (!STATE) tma_load_4d(smem_u32(to) + C::sQ + f * kTile, &x.mq, f * 64, h / wk.gq, t0, row0, full);
                 }
                 #pragma unroll
-                for (int f = 0; f < 2; ++f)
-                    tma_load_4d(smem_u32(to) + C::sV + f * kTile, &x.mv, DV == 128 ? f * 64 : 0, h / wk.gv, t0, row0, full);
+                for (int f = 0; f < DV / 64; ++f)
+                    tma_load_4d(smem_u32(to) + C::sV + f * kTile, &x.mv, f * 64, h / wk.gv, t0, row0, full);
             }
             __syncwarp();
             if (tail) {
                 if (!(ok = rest(bar + kRaw, 0, fail))) break;
-                for (int f = 0; f < 2 * C::KT + 2; ++f)
+                for (int f = 0; f < 2 * C::KT + DV / 64; ++f)
                     if (!STATE || f < C::KT || f >= 2 * C::KT) fix(to + f * kTile, m);
                 tc::fence_proxy_async();
                 __syncwarp();
