@@ -1,6 +1,7 @@
 // Gated delta rule: C entry points and the token-by-token kernels.
 #include "delta.h"
 #include "delta_chunk.h"
+#include "packed.cuh"
 
 #include <new>
 
@@ -129,33 +130,6 @@ __global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
     for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(a.sout + sbase + r * DV) = S[r];
 }
 
-// Zero the tokens of a packed row that belong to no sequence: those before the
-// first offset and from the last one on (offsets do not decrease); without
-// sequences, every token of every row.
-struct GapArgs {
-    View v[5];
-    int H[5], D[5];
-    int n;
-    const int32_t* offsets;
-    int nseq;
-    int64_t B, T;
-};
-
-__global__ void __launch_bounds__(256) gap_kernel(const GapArgs a) {
-    int64_t lo = a.nseq ? a.offsets[0] : a.T, hi = a.nseq ? a.offsets[a.nseq] : a.T;
-    lo = lo < 0 ? 0 : (lo > a.T ? a.T : lo);
-    hi = hi < lo ? lo : (hi > a.T ? a.T : hi);
-    const int64_t tokens = lo + a.T - hi;
-    for (int i = 0; i < a.n; ++i) {
-        const int64_t per = int64_t(a.H[i]) * a.D[i], row = tokens * per, n = a.B * row;
-        for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < n; e += int64_t(gridDim.x) * 256) {
-            const int64_t b = e / row, t = (e - b * row) / per, r = e - b * row - t * per;
-            reinterpret_cast<uint16_t*>(a.v[i].p)[b * a.v[i].b + (t < lo ? t : hi + t - lo) * a.v[i].t + r / a.D[i] * a.v[i].h +
-                                                  r % a.D[i]] = 0;
-        }
-    }
-}
-
 template <typename F>
 auto pick(int dt, int dk, int dv, F&& f) {
     if (dt == FFTCONV_F16) {
@@ -278,7 +252,7 @@ fftconv_status_t done(cudaError_t e) {
 }
 
 cudaError_t zero_gaps(const DeltaArgs& d, int n, const View* v, const int* H, const int* D, cudaStream_t st) {
-    GapArgs a{};
+    GapArgs<5> a{};
     for (int i = 0; i < n; ++i) {
         a.v[i] = v[i];
         a.H[i] = H[i];
@@ -289,7 +263,7 @@ cudaError_t zero_gaps(const DeltaArgs& d, int n, const View* v, const int* H, co
     a.nseq = d.nseq;
     a.B = d.B;
     a.T = d.T;
-    gap_kernel<<<64, 256, 0, st>>>(a);
+    gap_kernel<5><<<64, 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -28,6 +28,7 @@
 // 2.6 us a chunk however few rows there are (1 x 32768 tokens, 6 heads of 128: 1.22 ms
 // on 6 SMs of a training step of 1.67 ms).
 #include "chunk.cuh"
+#include "packed.cuh"
 
 namespace fftconv {
 namespace {
@@ -934,31 +935,6 @@ delta_grad_kernel(const __grid_constant__ GradArgs a) {
     tc::fence_after();
     if (w == 9) tc::dealloc(tm, C::COLS);
     if (p == 0 && s_fail) atomicExch(d.err, 7);
-}
-
-// dq, dk [token][Hk][DK] = the sum over a key head's value heads, 8 features a thread, in the
-// heads' order.  Bound: HBM (16 x 1000 tokens, 12 heads over 6 of 64: 123 MB in 22 us, 5.5 TB/s).
-template <int DT>
-__global__ void __launch_bounds__(256) head_sum_kernel(const float* xq, const float* xk, View yq, View yk, int64_t tokens,
-                                                       int64_t T, int Hk, int group, int DK) {
-    const int np = DK / 8;
-    const int64_t n = tokens * Hk * np * 2;
-    for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < n; e += int64_t(gridDim.x) * 256) {
-        const int64_t e2 = e >> 1;
-        const float* x = e & 1 ? xk : xq;
-        const View& y = e & 1 ? yk : yq;
-        const int r = int(e2 % np) * 8;
-        const int64_t hk = (e2 / np) % Hk, tok = e2 / np / Hk, b = tok / T, t = tok - b * T;
-        float4 u = make_float4(0, 0, 0, 0), v = u;
-        for (int j = 0; j < group; ++j) {
-            const float* q = x + ((tok * Hk + hk) * group + j) * DK + r;
-            const float4 s = *reinterpret_cast<const float4*>(q), z = *reinterpret_cast<const float4*>(q + 4);
-            u.x += s.x; u.y += s.y; u.z += s.z; u.w += s.w;
-            v.x += z.x; v.y += z.y; v.z += z.z; v.w += z.w;
-        }
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(y.p) + b * y.b + t * y.t + hk * y.h + r) =
-            make_uint4(Op<DT>::pack(u.x, u.y), Op<DT>::pack(u.z, u.w), Op<DT>::pack(v.x, v.y), Op<DT>::pack(v.z, v.w));
-    }
 }
 
 template <int DT, int DK, int DV>

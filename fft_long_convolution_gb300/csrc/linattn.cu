@@ -1,6 +1,7 @@
 // Linear attention with a fixed decay for each head: C entry points and the
 // token-by-token kernels.
 #include "linattn_chunk.h"
+#include "packed.cuh"
 
 #include <new>
 
@@ -103,58 +104,6 @@ __global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
     for (int r = 0; r < RP; ++r) *reinterpret_cast<float4*>(a.sout + sbase + r * DV) = S[r];
 }
 
-// dq, dk [token][Hk][DK] = the sum over a key head's value heads, 8 features a thread, in the
-// heads' order.
-template <int DT>
-__global__ void __launch_bounds__(256) group_sum_kernel(const float* xq, const float* xk, View yq, View yk, int64_t tokens,
-                                                        int64_t T, int Hk, int group, int DK) {
-    const int np = DK / 8;
-    const int64_t n = tokens * Hk * np * 2;
-    for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < n; e += int64_t(gridDim.x) * 256) {
-        const int64_t e2 = e >> 1;
-        const float* x = e & 1 ? xk : xq;
-        const View& y = e & 1 ? yk : yq;
-        const int r = int(e2 % np) * 8;
-        const int64_t hk = (e2 / np) % Hk, tok = e2 / np / Hk, b = tok / T, t = tok - b * T;
-        float4 u = make_float4(0, 0, 0, 0), v = u;
-        for (int j = 0; j < group; ++j) {
-            const float* q = x + ((tok * Hk + hk) * group + j) * DK + r;
-            const float4 s = *reinterpret_cast<const float4*>(q), z = *reinterpret_cast<const float4*>(q + 4);
-            u.x += s.x; u.y += s.y; u.z += s.z; u.w += s.w;
-            v.x += z.x; v.y += z.y; v.z += z.z; v.w += z.w;
-        }
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(y.p) + b * y.b + t * y.t + hk * y.h + r) =
-            make_uint4(Op<DT>::pack(u.x, u.y), Op<DT>::pack(u.z, u.w), Op<DT>::pack(v.x, v.y), Op<DT>::pack(v.z, v.w));
-    }
-}
-
-// Zero the tokens of a packed row that belong to no sequence: those before the
-// first offset and from the last one on (offsets do not decrease); without
-// sequences, every token of every row.
-struct GapArgs {
-    View v[3];
-    int H[3], D[3];
-    int n;
-    const int32_t* offsets;
-    int nseq;
-    int64_t B, T;
-};
-
-__global__ void __launch_bounds__(256) gap_kernel(const GapArgs a) {
-    int64_t lo = a.nseq ? a.offsets[0] : a.T, hi = a.nseq ? a.offsets[a.nseq] : a.T;
-    lo = lo < 0 ? 0 : (lo > a.T ? a.T : lo);
-    hi = hi < lo ? lo : (hi > a.T ? a.T : hi);
-    const int64_t tokens = lo + a.T - hi;
-    for (int i = 0; i < a.n; ++i) {
-        const int64_t per = int64_t(a.H[i]) * a.D[i], row = tokens * per, n = a.B * row;
-        for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < n; e += int64_t(gridDim.x) * 256) {
-            const int64_t b = e / row, t = (e - b * row) / per, r = e - b * row - t * per;
-            reinterpret_cast<uint16_t*>(a.v[i].p)[b * a.v[i].b + (t < lo ? t : hi + t - lo) * a.v[i].t + r / a.D[i] * a.v[i].h +
-                                                  r % a.D[i]] = 0;
-        }
-    }
-}
-
 template <typename F>
 cudaError_t pick(int dt, int dk, int dv, F&& f) {
     if (dt == FFTCONV_F16) {
@@ -205,7 +154,8 @@ fftconv_status_t take_args(const fftconv_linattn_s* p, const fftconv_linattn_arg
     if (x->offsets ? x->B != 1 : x->nseq != x->B) return FFTCONV_ERR_INVALID;
     if ((reinterpret_cast<uintptr_t>(x->offsets) | reinterpret_cast<uintptr_t>(x->decay)) & 3) return FFTCONV_ERR_ALIGN;
     const int64_t top = int64_t(1) << 31;
-    if (x->B >= top || x->T >= top || x->Hv > 65535 || x->nseq >= top) return FFTCONV_ERR_UNSUPPORTED;
+    if (x->B >= top || x->T >= top || x->Hv > 65535 || x->nseq >= top || chunk_slots(x->B, x->T, x->nseq) >= top)
+        return FFTCONV_ERR_UNSUPPORTED;
     *a = {};
     a->B = x->B;
     a->T = x->T;
@@ -242,7 +192,7 @@ struct Scratch {
     Segments seg;
     size_t s, r, q, k, total;  // byte offsets, and the size
     Scratch(const fftconv_linattn_s* p, int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t nseq, bool backward) {
-        plan_segments(&seg, B, T, nseq, Hv, backward ? 3 : 1, p->num_sms);
+        plan_segments(&seg, B, T, nseq, Hv, backward ? 3 : 1, p->dtype, p->num_sms);
         const size_t n = seg.count > nseq ? up256(state_bytes(p, seg.count, Hv)) : 0;
         const size_t h = backward && Hk < Hv ? up256(size_t(B) * T * Hv * p->Dk * 4) : 0;
         s = 0;
@@ -292,7 +242,7 @@ Passes passes_of(const fftconv_linattn_s* p, const fftconv_linattn_args_t* x, co
 
 cudaError_t zero_gaps(const fftconv_linattn_args_t* x, const Call& c, int n, const View* v, const int* H, const int* D,
                       cudaStream_t st) {
-    GapArgs a{};
+    GapArgs<3> a{};
     for (int i = 0; i < n; ++i) {
         a.v[i] = v[i];
         a.H[i] = H[i];
@@ -303,7 +253,7 @@ cudaError_t zero_gaps(const fftconv_linattn_args_t* x, const Call& c, int n, con
     a.nseq = x->offsets ? c.nseq : 0;
     a.B = c.B;
     a.T = c.T;
-    gap_kernel<<<64, 256, 0, st>>>(a);
+    gap_kernel<3><<<64, 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -530,7 +480,7 @@ extern "C" fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t p, const 
         if (r == cudaSuccess && shared) {
             const int64_t n = (c.B * c.T * c.Hk * (p->Dk / 8) * 2 + 255) / 256;
             const unsigned grid = unsigned(n < 152 * 32 ? n : 152 * 32);
-            auto f = p->dtype == FFTCONV_F16 ? group_sum_kernel<0> : group_sum_kernel<1>;
+            auto f = p->dtype == FFTCONV_F16 ? head_sum_kernel<0> : head_sum_kernel<1>;
             f<<<grid, 256, 0, st>>>(dq32, dk32, vdq, vdk, c.B * c.T, c.T, c.Hk, c.group, p->Dk);
             r = cudaGetLastError();
         }

@@ -952,25 +952,36 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
 
 // Segments.  A sequence's chunks follow one another, so few long sequences leave SMs
 // idle.  Cut into m segments a walk costs another over K and V for the segments' end
-// states (0.6 of a walk's step for a chunk) and a join.  The rule counts waves of CTAs
-// over the SMs in steps of a walk, takes the two more launches as 8, and cuts when that
-// saves a tenth.  Packed rows are taken at their mean length, as the host does not know
-// their offsets.  The walks' CTAs join up to three segments themselves (8 rows of 4096,
-// 6 heads of 128, two segments: 99 us with the inputs from memory, against 107 with the
-// join's launch; four segments: 128 against 129; six: 121 against 105, as the reads of
-// the states before follow one another).
-void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int sms) {
+// states, and a join.  The rule counts waves of CTAs over the SMs.  Its unit is 0.07 us:
+// a chunk's step of a walk 20 (26 in fp16, and uncut, where w V takes three parts; 22 if
+// that is one walk of a training step's three), of the segments' states 9 (13); a CTA's
+// start and end 106 and 100; the second launch 90, with the join's 160.  Fitted to 1024
+// to 16384 tokens with 6 to 150 rows, uncut and in 2 to 48 segments: 0.6 % above the
+// fastest of them on average, 12 % at most in calls of more than 47 us.
+//
+// bf16 128 x 128, 16384 tokens, forward: 6 rows uncut 496 us, in 24 segments 72; 24 rows
+// 495, in 6 145; 60 rows 497, in 5 312.  Training step's gradients: 16 rows 503, in 3
+// 232, in 8 257.  2048 tokens: 36 rows forward 79, in 3 61; gradients 83, in 2 108.
+// Packed rows are taken at their mean length, as the host does not know their offsets.
+//
+// The walks' CTAs join up to three segments themselves (8 rows of 4096, 6 heads of 128,
+// three segments: 99 us with the inputs from memory, against 107 with the join's launch;
+// four segments: 128 against 129; six: 121 against 105, as the reads of the states before
+// follow one another).
+void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int dt, int sms) {
     const int64_t slots = chunk_slots(B, T, nseq), rows = nseq * heads;
     s->chunks = slots + 1;
     s->count = nseq;
     s->join = false;
     if (rows == 0) return;
     const int64_t n = (B * T / nseq + kChunk - 1) / kChunk;
+    const bool f16 = dt == FFTCONV_F16;
     auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
-    int64_t best = 1, cost = waves(rows * walks) * n * 9;
+    int64_t best = 1, cost = waves(rows * walks) * (n * (f16 || walks == 1 ? 26 : 22) + 106);
     for (int64_t m = 2; m * 2 <= n && m * rows <= 2 * sms; ++m) {
         const int64_t len = (n + m - 1) / m;
-        const int64_t c = (waves(m * rows * walks) * 10 + waves(m * rows * (walks > 1 ? 2 : 1)) * 6) * len + 80;
+        const int64_t c = waves(m * rows * walks) * (len * (f16 ? 26 : 20) + 106) +
+                          waves(m * rows * (walks > 1 ? 2 : 1)) * (len * (f16 ? 13 : 9) + 100) + (m <= 3 ? 90 : 160);
         if (c < cost) {
             cost = c;
             best = m;

@@ -19,7 +19,7 @@ struct Passes {
     Pass p[3];
     int64_t seg_chunks;
     int64_t segments;
-    bool join;  // a walk's CTAs join the segments' states themselves
+    bool join;           // a walk's CTAs join the segments' states themselves
     bool longest_first;  // uncut packed sequences, in the order of their lengths
     int* err;
 };
@@ -31,7 +31,7 @@ struct Segments {
     int64_t chunks, count;
     bool join;
 };
-void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int sms);
+void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int dt, int sms);
 
 // states: the end states of all segments (of the walks' last where the final state is
 // wanted), joined along each sequence unless a.join.

@@ -56,3 +56,24 @@ def rel(got, ref):
     got, ref = got.double().cpu(), ref.double().cpu()
     d, n = float((got - ref).norm()), float(ref.norm())
     return 0.0 if d == 0 else d / max(n, 1e-300)
+
+
+def attention_chunks(q, k, v, decay, state=None, scale=1.0, C=50):
+    """linear_attention by chunks of C tokens, on the inputs' device, for rows too long to
+    take token by token."""
+    q, k, v = (x.double() for x in (q, k, v))
+    B, T, Hv, Dv = v.shape
+    g = decay.double().clamp(LOWEST, 0.0)
+    q, k = (x.repeat_interleave(Hv // x.shape[2], 2) for x in (q, k))
+    S = torch.zeros(B, Hv, q.shape[3], Dv, dtype=torch.float64, device=v.device) if state is None else state.double()
+    outs = []
+    for t in range(0, T, C):
+        x, y, z = (a[:, t:t + C] for a in (q, k, v))
+        m = x.shape[1]
+        i = torch.arange(m, device=v.device, dtype=torch.float64)
+        D = torch.where(i[:, None] >= i, (g[:, None, None] * (i[:, None] - i)).exp(), 0.0)
+        P = torch.einsum("bihd,bjhd->bhij", x, y) * D
+        o = torch.einsum("bihd,bhde->bihe", x * (g * (i[:, None] + 1)).exp()[..., None], S)
+        outs.append(scale * (o + torch.einsum("bhij,bjhe->bihe", P, z)))
+        S = (g * m).exp()[:, None, None] * S + torch.einsum("bjhd,bjhe->bhde", y * (g * (m - 1 - i)[:, None]).exp()[..., None], z)
+    return torch.cat(outs, 1), S
