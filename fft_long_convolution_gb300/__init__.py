@@ -214,11 +214,12 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, dev=None) -> Optional[int]:
+    """A call's stream: the current one of GPU dev (None: of the current GPU) by default."""
     if stream is not None:
         return stream.cuda_stream
-    from torch import _C  # torch.cuda.current_stream() takes 12 us
-    return _C._cuda_getCurrentRawStream(_current_device())
+    import torch  # torch.cuda.current_stream() takes 12 us
+    return torch._C._cuda_getCurrentRawStream(_current_device() if dev is None else dev)
 
 
 class Plan:
@@ -449,8 +450,8 @@ _LAYERNORM_ARGS = struct.Struct("=2if4x3q" + "Q3q" + "2Q")
 
 
 def _current_device() -> int:
-    from torch import _C
-    return _C._cuda_getDevice()
+    import torch
+    return torch._C._cuda_getDevice()
 
 
 def _device(t, what: str) -> int:
@@ -751,12 +752,13 @@ class LinearAttention:
                 return self.forward(q, k, v, decay, state, offsets, scale)
         a = self._args(q, k, v, decay, offsets, scale)
         shape = (a.nseq, a.Hv, self.Dk, self.Dv)
-        sin = _dense(state, "state", torch.float32, shape, q.get_device())
+        dev = q.get_device()
+        sin = _dense(state, "state", torch.float32, shape, dev)
         o, vo = _new(v)
         out = torch.empty(shape, dtype=torch.float32, device=v.device)
         scratch, n = self._scratch(a, 0, v.device)
         _check(lib().fftconv_linattn_forward(self._h, ctypes.byref(a), sin, vo, out.data_ptr(), _ptr(scratch), n,
-                                             _stream(None)), "fftconv_linattn_forward")
+                                             _stream(None, dev)), "fftconv_linattn_forward")
         return o, out
 
     def backward(self, do, q, k, v, decay, state=None, dstate=None, offsets=None, scale=None, stream=None):
@@ -778,7 +780,7 @@ class LinearAttention:
         dst = None if state is None else torch.empty(shape, dtype=torch.float32, device=v.device)
         scratch, n = self._scratch(a, 1, v.device)
         _check(lib().fftconv_linattn_backward(self._h, ctypes.byref(a), sin, vdo, dsin, oq, ok, ov, _ptr(dst),
-                                              _ptr(scratch), n, _stream(None)), "fftconv_linattn_backward")
+                                              _ptr(scratch), n, _stream(None, dev)), "fftconv_linattn_backward")
         return dq, dk, dv, dst
 
     def step(self, q, k, v, decay, state, state_out=None, slots=None, scale=None, stream=None):
@@ -795,7 +797,7 @@ class LinearAttention:
         sout = sin if state_out is None else _dense(state_out, "state_out", torch.float32, shape, dev)
         sl = _dense(slots, "slots", torch.int32, (q.shape[0],), dev)
         o, vo = _new(v)
-        _check(lib().fftconv_linattn_step(self._h, ctypes.byref(a), sin, sout, shape[0], sl, vo, _stream(None)),
+        _check(lib().fftconv_linattn_step(self._h, ctypes.byref(a), sin, sout, shape[0], sl, vo, _stream(None, dev)),
                "fftconv_linattn_step")
         return o
 
@@ -817,6 +819,12 @@ class LayerNorm:
     def __init__(self, D: int, dtype, eps: float = 1e-5):
         self.D, self.torch_dtype, self.eps = int(D), dtype, float(eps)
         self._code = _dtype_code(dtype)
+
+    def _new(self, x, a):
+        """An uninitialised contiguous tensor like x, and its view."""
+        import torch
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        return y, View(y.data_ptr(), a.T * a.H * self.D, a.H * self.D, self.D)
 
     def _view(self, t, what, shape, dev):
         """A tensor's address and its batch, token and head strides."""
@@ -843,15 +851,15 @@ class LayerNorm:
 
     def forward(self, x, w=None, b=None, y=None, stream=None):
         """The normed rows.  y: where to write (x itself is allowed)."""
-        import torch
         if stream is not None:
             with _on(stream):
                 return self.forward(x, w, b, y)
-        a = self._args(x, w, b)
+        a, dev = self._args(x, w, b), x.get_device()
         if y is None:
-            y = torch.empty_like(x, memory_format=torch.contiguous_format)
-        vy = View(*self._view(y, "y", x.shape, x.get_device()))
-        _check(lib().fftconv_layernorm_forward(ctypes.byref(a), vy, _stream(None)), "fftconv_layernorm_forward")
+            y, vy = self._new(x, a)
+        else:
+            vy = View(*self._view(y, "y", x.shape, dev))
+        _check(lib().fftconv_layernorm_forward(ctypes.byref(a), vy, _stream(None, dev)), "fftconv_layernorm_forward")
         return y
 
     def backward(self, dy, x, w=None, b=None, stream=None):
@@ -861,13 +869,12 @@ class LayerNorm:
         if stream is not None:
             with _on(stream):
                 return self.backward(dy, x, w, b)
-        a = self._args(x, w, b)
-        vdy = View(*self._view(dy, "dy", x.shape, x.get_device()))
-        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
-        vdx = View(*self._view(dx, "dx", x.shape, x.get_device()))
+        a, dev = self._args(x, w, b), x.get_device()
+        vdy = View(*self._view(dy, "dy", x.shape, dev))
+        dx, vdx = self._new(x, a)
         dw, db = (None if t is None else torch.empty_like(t) for t in (w, b))
         n = int(lib().fftconv_layernorm_scratch_bytes(ctypes.byref(a))) if (w is not None or b is not None) else 0
-        scratch = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+        scratch = x.new_empty(n, dtype=torch.uint8) if n else None
         _check(lib().fftconv_layernorm_backward(ctypes.byref(a), vdy, vdx, _ptr(dw), _ptr(db), _ptr(scratch), n,
-                                                _stream(None)), "fftconv_layernorm_backward")
+                                                _stream(None, dev)), "fftconv_layernorm_backward")
         return dx, dw, db
