@@ -26,7 +26,7 @@
 // over through mbarriers:
 //   warps 0-15   w V in parts -> tensor memory; S: float32 += KV, and in 16 bits for S Q
 //   warps 16-19  scores -> P;  warps 20-27  O -> shared memory
-//   warp 28      loads, three chunks deep;  warp 30  O -> global memory
+//   warp 28      loads, 3 to 5 chunks deep;  warp 30  O -> global memory
 //   warp 29      issues KV and the next chunk's scores;  warp 31  S Q and P V
 #include "linattn_chunk.h"
 
@@ -130,25 +130,32 @@ __device__ __forceinline__ float2 row_scale(float x) {
     return make_float2(__uint_as_float((268u - e) << 23), __uint_as_float((e - 14u) << 23));
 }
 
-template <int DK_, int DV_>
+constexpr int kThreads = 1024, kMaxStages = 5;
+
+// Shared memory: stages of K, Q (not where only the states are wanted) and V, P twice, O,
+// tables, barriers.  A stage is held for one and a half steps and takes another to load
+// again: as many as fit, up to 5 (three at 128 x 128; heads of 64 x 64 with three: XX).
+// Up to 4 where only the states are wanted, as the scales' places there rely on it.
+template <int DK_, int DV_, bool STATE>
 struct Cfg {
-    static constexpr int KT = DK_ / 64;  // tiles of K and of Q
-    static constexpr int NST = 3;
-    static constexpr uint32_t sK = 0, sQ = KT * kTile, sV = 2 * KT * kTile, STAGE = sV + 2 * kTile;  // V: M = 128 lanes
-    static constexpr uint32_t oP = NST * STAGE, oO = oP + 2 * kTile, oT = oO + (DV_ / 64) * kTile;
+    static constexpr int KT = DK_ / 64, VT = DV_ / 64;  // tiles of K and of Q, of V
+    static constexpr uint32_t sK = 0, sQ = KT * kTile, sV = (STATE ? 1 : 2) * KT * kTile, STAGE = sV + VT * kTile;
     // float tables: w and u for a whole chunk and for a last one; w of two tokens in two
     // 16-bit parts, packed [2][32][2]; the decays between a chunk's tokens (pairs); the
     // scales of w V [8][128] back, S [2][128] and P [2][64]; the rows' sizes of S
     // [2][4][128]; the scales of w V
     static constexpr uint32_t tW = 0, tU = 128, tH = 256, tD = 384, tV = 640, tS = 1664, tP = 1920, tM = 2048, tN = 3072, TABLE = (3072 + 512) * 4;
-    static constexpr uint32_t oBar = oT + TABLE, BYTES = oBar + 304;
-    static constexpr int THREADS = 1024;
+    static constexpr uint32_t kBarBytes = 336, kMost = 232448, kRest = (2 + VT) * kTile + TABLE + kBarBytes;
+    static constexpr int kFit = (kMost - kRest) / STAGE, kUse = STATE ? 4 : kMaxStages, NST = kFit < kUse ? kFit : kUse;
+    static_assert(NST >= 3, "stages");
+    static constexpr uint32_t oP = NST * STAGE, oO = oP + 2 * kTile, oT = oO + VT * kTile, oBar = oT + TABLE, BYTES = oBar + kBarBytes;
     // tensor memory columns: S; KV; S Q; scores and then P V, two buffers; w V: two buffers
     // of two parts, or one of three.  512 in all at Dk = 128.  Where only the states are
     // wanted: KV and w V of three parts, two buffers each.
-    static constexpr uint32_t cS = 0, cKV = DK_ / 2, cOi = cKV + DK_, cX = cOi + 64, cW = cX + 128;
+    static constexpr uint32_t cS = 0, cKV = DK_ / 2, cOi = cKV + 128, cX = cOi + 64, cW = cX + 128;
+    static constexpr bool kTwoKv = DK_ == 64;
     static_assert(cW + 128 <= 512 && 2 * DK_ + 192 <= 512, "tensor memory");
-    static __device__ __forceinline__ uint32_t kv(bool state, int c) { return state ? (c & 1) * DK_ : cKV; }
+    static __device__ __forceinline__ uint32_t kv(bool state, int c) { return state ? (c & 1) * DK_ : cKV + (kTwoKv ? (c & 1) * DK_ : 0); }
     static __device__ __forceinline__ uint32_t w(bool state, bool fine, int c) {
         return state ? 2 * DK_ + (c & 1) * 96 : cW + (fine ? 0 : (c & 1) * 64);
     }
@@ -156,9 +163,11 @@ struct Cfg {
 };
 
 enum Bar {
-    kFull = 0, kFree = 3,                                                        // by stage
-    kKvDone = 6, kKvRead = 8, kParts = 10, kScDone = 12, kORead = 14, kPReady = 16, kPvDone = 18,  // by chunk parity
-    kRaw = 20, kSop, kSqDone, kOReady, kOFree,
+    kFull = 0, kFree = kMaxStages,  // by stage
+    // by chunk parity
+    kKvDone = 2 * kMaxStages, kKvRead = kKvDone + 2, kParts = kKvRead + 2, kScDone = kParts + 2, kORead = kScDone + 2,
+    kPReady = kORead + 2, kPvDone = kPReady + 2,
+    kRaw = kPvDone + 2, kSop, kSqDone, kOReady, kOFree,
     kFinal,            // [2]
     kSizes = kFinal + 2,  // [4]
     kMax = kSizes + 4, kBars = kMax + 4  // the four warps of 32 lanes of S
@@ -228,15 +237,15 @@ __device__ __forceinline__ int by_length(const Walk& w, int rank) {
 // STATE: only the state at the end of a segment (from zero, or from the initial state);
 // a walk's last one, if the final state is wanted, to where that goes.
 template <int DT, int DK, int DV, bool STATE>
-__global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(const __grid_constant__ Passes a) {
-    using C = Cfg<DK, DV>;
+__global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_constant__ Passes a) {
+    using C = Cfg<DK, DV, STATE>;
     constexpr int NC = DK / 4;  // columns of S of a thread
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::oBar);
     // no static shared memory: the window starts 1024-byte aligned
-    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 288);
-    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 292);
+    uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + C::oBar + 320);
+    volatile int& s_fail = *reinterpret_cast<volatile int*>(sm + C::oBar + 324);
     float* tab = reinterpret_cast<float*>(sm + C::oT);
     int slot = blockIdx.x, h = blockIdx.y, z = blockIdx.z;
     if (a.longest_first) {  // all heads of a sequence before the next sequence
@@ -291,7 +300,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             uint32_t cnt = 1;  // else one arrival per warp of the role
             if (i == kPReady || i == kPReady + 1 || i >= kSizes) cnt = 4;
             if (i == kORead || i == kORead + 1 || i == kOReady) cnt = 8;
-            if (i >= kFree && i < kFree + 3 && !STATE) cnt = 2;  // both warps that issue products
+            if (i >= kFree && i < kFree + kMaxStages && !STATE) cnt = 2;  // both warps that issue products
             if (i == kParts || i == kParts + 1) cnt = DT == 1 && (STATE || (p.last && wk.state_out)) ? 16 : 8;
             if (i == kSop || i == kKvRead || i == kKvRead + 1) cnt = 16;
             mbar_init(bar + i, cnt);
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
     if (n == 0) {
         // an empty sequence: the state passes through
         if (sout)
-            for (int e = threadIdx.x; e < DK * DV; e += C::THREADS) {
+            for (int e = threadIdx.x; e < DK * DV; e += kThreads) {
                 float v = 0.0f;
                 if (sin) v = wk.turned ? sin[(e % DV) * DK + e / DV] : sin[e];
                 sout[e] = v;
@@ -554,9 +563,11 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         const int q = lane >> 2, r = lane & 3;
         const float2* dt = reinterpret_cast<const float2*>(tab + C::tD) + 64 + 16 * sp + q - 2 * r;
         // fp16: the scales of V's rows, two chunks ahead.  A lane takes 8 of the warp's 32
-        // features, 8 tokens.  When chunk e has been loaded, chunk e - 3 has left its stage:
-        // its KV is over, so w V has used the scales of chunk e - 4, and S has added KV up to
-        // chunk e - 5 (places for 4 scales, and for 8 of their inverses).
+        // features, 8 tokens.  There are places for the scales of 4 chunks and for 8 of their
+        // inverses.  When those of chunk e are written, w V has used the scales of chunk
+        // e - 4, and S has added KV up to chunk e - 6: P V of chunk e - 4 is over (P waits
+        // for it), before which all warps of S have put it, weighed V and added KV; where
+        // only the states are wanted, chunk e - 4 has left its stage, so its KV is over.
         const float s_up = reverse ? wk.s_up * expf(g) : wk.s_up;  // (see the weights)
         Ring<C::NST> full;
         auto sizes = [&](int e) {
@@ -747,7 +758,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             if (c >= C::NST && !(ok = rest(bar + kFree + st, ring.parity ^ 1, fail))) break;
             uint64_t* full = tail ? bar + kRaw : bar + kFull + st;
             if (elect()) {
-                mbar_expect_tx(full, C::STAGE - (STATE ? C::KT * kTile : 0) - (2 - DV / 64) * kTile);
+                mbar_expect_tx(full, C::STAGE);
                 #pragma unroll
                 for (int f = 0; f < C::KT; ++f) {
                     tma_load_4d(smem_u32(to) + C::sK + f * kTile, &x.mk, f * 64, h / wk.gk, t0, row0, full);
@@ -760,8 +771,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
             __syncwarp();
             if (tail) {
                 if (!(ok = rest(bar + kRaw, 0, fail))) break;
-                for (int f = 0; f < 2 * C::KT + DV / 64; ++f)
-                    if (!STATE || f < C::KT || f >= 2 * C::KT) fix(to + f * kTile, m);
+                for (int f = 0; f < int(C::STAGE / kTile); ++f) fix(to + f * kTile, m);
                 tc::fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) arrive(bar + kFull + st);
@@ -782,7 +792,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV>::THREADS, 1) linattn_walk_kernel(c
         for (int e = STATE ? 0 : -1; ok && e < n; ++e) {
             c = e;
             if (c >= 0) {
-                constexpr int NB = STATE ? 2 : 1;  // buffers of KV
+                constexpr int NB = STATE || C::kTwoKv ? 2 : 1;  // buffers of KV
                 if (STATE) ok = rest(bar + kFull + ring.st, ring.parity, fail);
                 ok = ok && rest(bar + kParts + (c & 1), (c >> 1) & 1, fail);
                 if (ok && c >= NB) ok = rest(bar + kKvRead + ((c - NB) & 1), ((c - NB) >> 1) & 1, fail);
@@ -930,20 +940,19 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(const __grid_constant
 template <int DT, int DK, int DV>
 cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
     static PerDevice c0, c1;
-    constexpr size_t bytes = Cfg<DK, DV>::BYTES;
-    static_assert(bytes <= 232448, "shared memory");
-    static_assert(kBars * 8 <= 288, "barriers");
-    cudaError_t e = opt_in(linattn_walk_kernel<DT, DK, DV, false>, bytes, c0);
-    if (e == cudaSuccess) e = opt_in(linattn_walk_kernel<DT, DK, DV, true>, bytes, c1);
+    constexpr size_t walk = Cfg<DK, DV, false>::BYTES, ends = Cfg<DK, DV, true>::BYTES;
+    static_assert(kBars * 8 <= 320, "barriers");
+    cudaError_t e = opt_in(linattn_walk_kernel<DT, DK, DV, false>, walk, c0);
+    if (e == cudaSuccess) e = opt_in(linattn_walk_kernel<DT, DK, DV, true>, ends, c1);
     if (e != cudaSuccess) return e;
     const dim3 grid(unsigned(a.segments), unsigned(a.p[0].w.H), unsigned(n));
     if (states) {
-        linattn_walk_kernel<DT, DK, DV, true><<<grid, Cfg<DK, DV>::THREADS, bytes, st>>>(a);
+        linattn_walk_kernel<DT, DK, DV, true><<<grid, kThreads, ends, st>>>(a);
         if (a.join) return cudaGetLastError();
         constexpr int size = DK * DV;
         linattn_join_kernel<<<dim3(unsigned(a.p[0].w.nseq) * (size / 1024), grid.y, grid.z), 256, 0, st>>>(a, size);
     } else {
-        linattn_walk_kernel<DT, DK, DV, false><<<grid, Cfg<DK, DV>::THREADS, bytes, st>>>(a);
+        linattn_walk_kernel<DT, DK, DV, false><<<grid, kThreads, walk, st>>>(a);
     }
     return cudaGetLastError();
 }

@@ -627,6 +627,18 @@ fftconv_status_t fftconv_qknorm_backward(const fftconv_qknorm_args_t *args, fftc
  * everything, -infinity only the token itself.  It is a constant of the layer
  * and has no gradient (fftconv_delta_* has decays for each token, with theirs).
  * Sequences and offsets as for the gated delta rule.
+ *
+ * Precision: states are float32, and what feeds one that is an output is taken to
+ * at least 22 bits (final states and the initial states' gradients: relative error
+ * about 1e-6).  In whole sequences the state and the scores enter the outputs, and
+ * their likes the gradients, as one value of the plan dtype each, scaled so that
+ * fp16 neither overflows nor loses small ones; with the result's own rounding an
+ * output is off by about sqrt(2) times that rounding alone.
+ * A NaN or an infinity in a token of a whole sequence may reach every output of its
+ * chunk (64 tokens, counted from the sequence's start), those before it included,
+ * and every later one of its sequence and head (gradients: every earlier one too);
+ * other sequences and heads are not reached.  So a batch that is padded behind its
+ * tokens holds finite values there, or is packed.
  */
 typedef struct fftconv_linattn_s *fftconv_linattn_t;
 
