@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(128) token_kernel(const TokenArgs a) {
     float4 S[RP];
     #pragma unroll
     for (int r = 0; r < RP; ++r) S[r] = *reinterpret_cast<const float4*>(a.sin + sbase + r * DV);
-    const Decay al = decay_over(head_decay(a.decay, h), 1.0f);
+    const Decay al = a.T ? decay_over(head_decay(a.decay, h), 1.0f) : Decay{};
     for (int64_t t = 0; t < a.T; ++t) {
         float k[RP], q[RP], v[4];
         #pragma unroll
@@ -495,15 +495,15 @@ extern "C" fftconv_status_t fftconv_linattn_step(fftconv_linattn_t p, const fftc
     fftconv_status_t e = take_args(p, args, &c);
     if (e != FFTCONV_OK) return e;
     if (args->offsets || nslots < 0 || (!slots && nslots < c.B)) return FFTCONV_ERR_INVALID;
-    if (!c.any) return FFTCONV_OK;
+    if (!c.B || !c.Hv || (!c.T && state_in == state_out)) return FFTCONV_OK;
     if (!state_in || !state_out) return FFTCONV_ERR_INVALID;
     if (off16(state_in) || off16(state_out) || (reinterpret_cast<uintptr_t>(slots) & 3)) return FFTCONV_ERR_ALIGN;
     TokenArgs a{};
-    if ((e = take_view(o, c.B, c.T, c.Hv, p->Dv, &a.o)) != FFTCONV_OK) return e;
+    if (c.any && (e = take_view(o, c.B, c.T, c.Hv, p->Dv, &a.o)) != FFTCONV_OK) return e;
     const size_t sb = state_bytes(p, nslots, c.Hv);
     Span in[5];
     input_spans(p, args, c, in);
-    const Span outs[2] = {span_of(a.o, c.B, c.T, c.Hv, p->Dv), span_of(state_out, sb)};
+    const Span outs[2] = {c.any ? span_of(a.o, c.B, c.T, c.Hv, p->Dv) : Span{}, span_of(state_out, sb)};
     const Span more[2] = {span_of(slots, size_t(c.B) * 4), state_in == state_out ? Span{} : span_of(state_in, sb)};
     if (any_meet(outs, in) || any_meet(outs, more) || meets(outs[0], outs[1]) || meets(outs[0], span_of(state_in, sb)))
         return FFTCONV_ERR_INVALID;

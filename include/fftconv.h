@@ -630,10 +630,12 @@ fftconv_status_t fftconv_qknorm_backward(const fftconv_qknorm_args_t *args, fftc
  *
  * Precision: states are float32, and what feeds one that is an output is taken to
  * at least 22 bits (final states and the initial states' gradients: relative error
- * about 1e-6).  In whole sequences the state and the scores enter the outputs, and
- * their likes the gradients, as one value of the plan dtype each, scaled so that
- * fp16 neither overflows nor loses small ones; with the result's own rounding an
- * output is off by about sqrt(2) times that rounding alone.
+ * about 1e-6).  In fp16 a token's weight in its chunk of 64, l^i with i tokens behind
+ * it there, is held to 2^-25: what is left of a token is off by that part of what it
+ * was, however much it has decayed since.  In whole sequences the state and the
+ * scores enter the outputs, and their likes the gradients, as one value of the plan
+ * dtype each, scaled so that fp16 neither overflows nor loses small ones; with the
+ * result's own rounding an output is off by about sqrt(2) times that rounding alone.
  * A NaN or an infinity in a token of a whole sequence may reach every output of its
  * chunk (64 tokens, counted from the sequence's start), those before it included,
  * and every later one of its sequence and head (gradients: every earlier one too);
@@ -702,8 +704,8 @@ fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t plan, const fftconv_
  * fftconv_delta_step: row b uses slot slots[b] (device int32 [B], distinct), or
  * slot b when slots is NULL; a row whose slot is negative or >= nslots gets zero
  * outputs and touches no state; state_out == state_in updates in place, other
- * overlaps are INVALID; slots that no row uses are not touched.  args->offsets
- * must be NULL.  Float32 throughout.  Returns OK, INVALID, UNSUPPORTED, ALIGN or
+ * overlaps are INVALID; slots that no row uses are not touched; with T = 0 the rows'
+ * states pass through.  args->offsets must be NULL.  Float32 throughout.  Returns OK, INVALID, UNSUPPORTED, ALIGN or
  * CUDA.
  */
 fftconv_status_t fftconv_linattn_step(fftconv_linattn_t plan, const fftconv_linattn_args_t *args,

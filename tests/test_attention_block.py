@@ -83,6 +83,54 @@ def test_queues_of_many_prompts(n):
     assert plan.device_status() == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [70, 2550])
+def test_gradients_of_final_states_without_initial_ones(T):
+    dt, B, Hk, Hv, Dk, Dv = torch.bfloat16, 2, 1, 2, 64, 128
+    ins = [x.cuda() for x in attention_inputs(B, T, Hk, Hv, Dk, Dv, dt, seed=21)]
+    do = attention_inputs(B, T, Hk, Hv, Dk, Dv, dt, seed=22)[2].cuda()
+    ds = states(B, Hv, Dk, Dv).cuda()
+    plan = F.LinearAttention(Dk, Dv, dt)
+    *got, none = plan.backward(do, *ins, dstate=ds)
+    xs = [x.double().requires_grad_() for x in ins[:3]]
+    o, s = attention_chunks(*xs, ins[3], None, Dk ** -0.5)
+    ref = torch.autograd.grad((o * do.double()).sum() + (s * ds.double()).sum(), xs)
+    assert none is None and all(rel(x, y) < U[dt] for x, y in zip(got, ref))
+    assert plan.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_step_of_no_tokens_passes_states_through():
+    dt = torch.bfloat16
+    plan = F.LinearAttention(64, 64, dt)
+    q, v = torch.empty(2, 0, 1, 64, dtype=dt, device="cuda"), torch.empty(2, 0, 2, 64, dtype=dt, device="cuda")
+    decay = torch.zeros(2, device="cuda")
+    pool = states(4, 2, 64, 64).cuda()
+    kept, out = pool.clone(), torch.full_like(pool, 7.0)
+    slots = torch.tensor([3, 1], dtype=torch.int32, device="cuda")
+    assert plan.step(q, q, v, decay, pool, slots=slots).shape == v.shape and torch.equal(pool, kept)
+    plan.step(q, q, v, decay, pool, state_out=out, slots=slots)
+    assert torch.equal(out[[1, 3]], kept[[1, 3]]) and bool((out[[0, 2]] == 7.0).all()) and torch.equal(pool, kept)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rate", [0.25, 0.5, 2.0])
+def test_fp16_states_of_tokens_long_gone(rate):
+    """Tokens with nothing behind them for the rest of their chunk.  A weight is within
+    2^-25 of l^i, and the parts within 2^-21 of the product: the error of the state is at
+    most (2^-25 + 2^-21 l^i) |k| |v| of each token, doubled for the sums."""
+    dt, T, n, D = torch.float16, 64, 24, 64
+    q, k, v, _ = attention_inputs(1, T, 1, 1, D, D, dt, seed=31)
+    k[:, n:], v[:, n:] = 0, 0
+    decay = torch.tensor([-rate])
+    _, ref = linear_attention(q, k, v, decay)
+    plan = F.LinearAttention(D, D, dt)
+    s = plan.forward(q.cuda(), k.cuda(), v.cuda(), decay.cuda())[1].cpu().double()
+    w = (-rate * (T - 1 - torch.arange(T, dtype=torch.float64))).exp()
+    size = torch.einsum("tk,tv,t->kv", k[0, :, 0].double().abs(), v[0, :, 0].double().abs(), 2.0 ** -25 + 2.0 ** -21 * w)
+    assert bool(((s - ref)[0, 0].abs() <= 2 * size).all())
+
+
 class Block:
     """x + heads normed (attention (projections of normed x)), with all its gradients."""
 
