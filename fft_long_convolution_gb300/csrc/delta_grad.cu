@@ -478,7 +478,7 @@ delta_dstate_kernel(const __grid_constant__ GradArgs a) {
 // thread.  Roles: warps 0-7 form X and H and the gradients' rows, warp 8 stores
 // them and forms the gates' gradients, warp 9 loads (a chunk ahead, each buffer as
 // soon as it has been read) and issues the products.  Bound: HBM, 181 kB read and
-// 33 kB written per chunk at Dk = Dv = 128 (8 x 4096 tokens, 6 heads, 3072 chunks:
+// 33 kB written per chunk at Dk = Dv = 128 (8 x 4096 tokens, 48 rows of 64 chunks:
 // 114 us, 5.8 TB/s; beta H as one 16-bit part, which dg does not stand, took 109).
 template <int DK, int DV>
 struct GradCfg {

@@ -28,6 +28,14 @@
 //   warps 16-19  scores -> P;  warps 20-27  O -> shared memory
 //   warp 28      loads, 3 to 5 chunks deep;  warp 30  O -> global memory
 //   warp 29      issues KV and the next chunk's scores;  warp 31  S Q and P V
+//
+// Bound: HBM where segments fill the SMs (262144 tokens, 6 heads of 128 x 128, bf16:
+// q, k, v read and o written in 250 us, 6.4 TB/s); else the chain of a chunk, 1.4 us in
+// bf16 and 1.9 us in fp16 or with three parts at 128 x 128, 1.0 to 1.6 us at 64 x 64 (8 x
+// 4096 tokens, 6 heads of 128: the three gradients' walks 92 us side by side).  Three
+// loops of that chain are equally long: S Q, P V and the read of O; scores, P, P V and
+// O; w V, KV and S.  The tensor pipe is active 40 % of the time, the schedulers issue in
+// 55 %.
 #include "linattn_chunk.h"
 
 #include <type_traits>
@@ -145,18 +153,22 @@ struct Cfg {
     // 16-bit parts, packed [2][32][2]; the decays between a chunk's tokens (pairs); the
     // scales of w V [8][128] back, S [2][128] and P [2][64]; the rows' sizes of S
     // [2][4][128]; the scales of w V
-    static constexpr uint32_t tW = 0, tU = 128, tH = 256, tD = 384, tV = 640, tS = 1664, tP = 1920, tM = 2048, tN = 3072, TABLE = (3072 + 512) * 4;
+    static constexpr uint32_t tW = 0, tU = 128, tH = 256, tD = 384, tV = 640, tS = tV + 1024, tP = tS + 256;
+    static constexpr uint32_t tM = tP + 128, tN = tM + 1024, TABLE = (tN + 512) * 4;
     static constexpr uint32_t kBarBytes = 336, kMost = 232448, kRest = (2 + VT) * kTile + TABLE + kBarBytes;
     static constexpr int kFit = (kMost - kRest) / STAGE, kUse = STATE ? 4 : kMaxStages, NST = kFit < kUse ? kFit : kUse;
     static_assert(NST >= 3, "stages");
     static constexpr uint32_t oP = NST * STAGE, oO = oP + 2 * kTile, oT = oO + VT * kTile, oBar = oT + TABLE, BYTES = oBar + kBarBytes;
-    // tensor memory columns: S; KV; S Q; scores and then P V, two buffers; w V: two buffers
-    // of two parts, or one of three.  512 in all at Dk = 128.  Where only the states are
-    // wanted: KV and w V of three parts, two buffers each.
+    // tensor memory columns: S; KV (two buffers at Dk = 64, where there is room: 2 % of a
+    // step in bf16); S Q; scores and then P V, two buffers; w V: two buffers of two parts,
+    // or one of three.  512 in all at Dk = 128.  Where only the states are wanted: KV and
+    // w V of three parts, two buffers each.
     static constexpr uint32_t cS = 0, cKV = DK_ / 2, cOi = cKV + 128, cX = cOi + 64, cW = cX + 128;
     static constexpr bool kTwoKv = DK_ == 64;
     static_assert(cW + 128 <= 512 && 2 * DK_ + 192 <= 512, "tensor memory");
-    static __device__ __forceinline__ uint32_t kv(bool state, int c) { return state ? (c & 1) * DK_ : cKV + (kTwoKv ? (c & 1) * DK_ : 0); }
+    static __device__ __forceinline__ uint32_t kv(bool state, int c) {
+        return (state ? 0 : cKV) + (state || kTwoKv ? (c & 1) * DK_ : 0);
+    }
     static __device__ __forceinline__ uint32_t w(bool state, bool fine, int c) {
         return state ? 2 * DK_ + (c & 1) * 96 : cW + (fine ? 0 : (c & 1) * 64);
     }
