@@ -159,20 +159,22 @@ struct Cfg {
     static constexpr int kFit = (kMost - kRest) / STAGE, kUse = STATE ? 4 : kMaxStages, NST = kFit < kUse ? kFit : kUse;
     static_assert(NST >= 3, "stages");
     static constexpr uint32_t oP = NST * STAGE, oO = oP + 2 * kTile, oT = oO + VT * kTile, oBar = oT + TABLE, BYTES = oBar + kBarBytes;
-    // tensor memory columns: S; KV (two buffers at Dk = 64, where there is room: 2 % of a
-    // step in bf16); S Q; scores and then P V, two buffers; w V: two buffers of two parts,
-    // or one of three.  512 in all at Dk = 128.  Where only the states are wanted: KV and
-    // w V of three parts, two buffers each.
-    static constexpr uint32_t cS = 0, cKV = DK_ / 2, cOi = cKV + 128, cX = cOi + 64, cW = cX + 128;
-    static constexpr bool kTwoKv = DK_ == 64;
-    static_assert(cW + 128 <= 512 && 2 * DK_ + 192 <= 512, "tensor memory");
-    static __device__ __forceinline__ uint32_t kv(bool state, int c) {
-        return (state ? 0 : cKV) + (state || kTwoKv ? (c & 1) * DK_ : 0);
+    // Tensor memory columns: S; S Q; scores and then P V; KV; w V, all 512 at Dk = 128.
+    // w V has two buffers.  With its two parts the scores have two and KV one, and two at
+    // Dk = 64, where there is room (2 % of a step in bf16).  With three parts (fine) KV has
+    // one, the scores one, and two at Dk = 64 (XXX).  Where only
+    // the states are wanted: KV and w V.
+    static __host__ __device__ constexpr int nx(bool fine) { return fine && DK_ == 128 ? 1 : 2; }
+    static __host__ __device__ constexpr int nkv(bool fine) { return STATE || (!fine && DK_ == 64) ? 2 : 1; }
+    static constexpr uint32_t cS = 0, cOi = DK_ / 2, cX = cOi + 64;
+    static __host__ __device__ constexpr uint32_t x(bool fine, int c) { return cX + (nx(fine) == 2 ? (c & 1) * 64 : 0); }
+    static __host__ __device__ constexpr uint32_t kv(bool fine, int c) {
+        return (STATE ? 0 : cX + nx(fine) * 64) + (nkv(fine) == 2 ? (c & 1) * DK_ : 0);
     }
-    static __device__ __forceinline__ uint32_t w(bool state, bool fine, int c) {
-        return state ? 2 * DK_ + (c & 1) * 96 : cW + (fine ? 0 : (c & 1) * 64);
+    static __host__ __device__ constexpr uint32_t w(bool fine, int c) {
+        return kv(fine, 0) + nkv(fine) * DK_ + (c & 1) * (fine ? 96 : 64);
     }
-    static __device__ __forceinline__ uint32_t x(int c) { return cX + (c & 1) * 64; }
+    static_assert(w(false, 1) + 64 <= 512 && w(true, 1) + 96 <= 512, "tensor memory");
 };
 
 enum Bar {
@@ -412,12 +414,12 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         auto block = [&](int st, int b, uint32_t* v) { ldsm_t(v_at + st * C::STAGE + b * 2048, v[0], v[1], v[2], v[3]); };
         const uint32_t w_at = lanes + (uint32_t(16 * hf) << 16);
         Ring<C::NST> full;
-        // Three parts: a warp half of the tokens of every step, as KV waits for it.
+        // Three parts: a warp half of the tokens of every step.
         auto weigh_fine = [&](int e) {
             if (!rest(bar + kFull + full.st, full.parity, fail)) return false;
             tc::fence_after();
             const float* wt = tab + C::tW + (tokens(e) < kChunk ? 64 : 0) + 32 * side + 2 * (lane & 3);
-            const uint32_t to = w_at + C::w(STATE, true, e) + 16 * side;
+            const uint32_t to = w_at + C::w(true, e) + 16 * side;
             #pragma unroll 1
             for (int b = 0; mine && b < 2; ++b) {
                 uint32_t v[4], hi[4], lo[4], l2[4];
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             if (!rest(bar + kFull + full.st, full.parity, fail)) return false;
             tc::fence_after();
             const float* wt = tab + C::tH + (tokens(e) < kChunk ? 64 : 0) + 2 * (lane & 3);
-            const uint32_t to = w_at + C::w(STATE, false, e);
+            const uint32_t to = w_at + C::w(false, e);
             uint32_t sc[2] = {};
             if constexpr (DT == 0) {
                 if (!rest(bar + kSizes + (e & 3), (e >> 2) & 1, fail)) return false;
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             for (int b = 0; b < NC; b += 16) {
                 if (!mine) break;
                 uint32_t y[16];
-                ld16(lanes + C::kv(STATE, e) + k0 + b, y);
+                ld16(lanes + C::kv(fine, e) + k0 + b, y);
                 tc::wait_ld();
                 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -543,12 +545,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             return true;
         };
         if (fine) {
-            // where only the states are wanted w V has two buffers, else KV has to be over
+            // w V of step c goes into the buffer of step c - 2, whose products add() has
+            // waited for, while KV of step c - 1 is formed
             #pragma unroll 1
             for (; ok && c <= n; ++c) {
-                if (STATE && c < n) ok = weigh_fine(c);
+                if (c < n) ok = weigh_fine(c);
                 if (ok && c > 0) ok = add(c - 1, std::true_type());
-                if (!STATE && ok && c < n) ok = weigh_fine(c) && put(c);
+                if (!STATE && ok && c < n) ok = put(c);
             }
         } else {
             // w V of step c goes into the buffer of step c - 2, whose products add() has
@@ -626,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             tc::fence_after();
             uint8_t* to = sm + C::oP + (c & 1) * kTile + (16 * sp + q) * 128 + r * 4;
             uint32_t y[32];
-            tc::ld16x256b_x8(lanes + C::x(c), y);
+            tc::ld16x256b_x8(lanes + C::x(fine, c), y);
             tc::wait_ld();
             float m0 = 0.0f, m1 = 0.0f;
             float2 z0 = make_float2(1.0f, 1.0f), z1 = z0;
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
                 uint32_t y[16], z[16];
                 const uint32_t from = lanes + (uint32_t(16 * hf) << 16) + t0;
                 tc::ld16x256b_x4(from + C::cOi, y);
-                tc::ld16x256b_x4(from + C::x(c), z);
+                tc::ld16x256b_x4(from + C::x(fine, c), z);
                 tc::wait_ld();
                 if (DT != 0 && t0) {  // the accumulators have been read
                     tc::fence_before();
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         for (int e = STATE ? 0 : -1; ok && e < n; ++e) {
             c = e;
             if (c >= 0) {
-                constexpr int NB = STATE || C::kTwoKv ? 2 : 1;  // buffers of KV
+                const int NB = C::nkv(fine);
                 if (STATE) ok = rest(bar + kFull + ring.st, ring.parity, fail);
                 ok = ok && rest(bar + kParts + (c & 1), (c >> 1) & 1, fail);
                 if (ok && c >= NB) ok = rest(bar + kKvRead + ((c - NB) & 1), ((c - NB) >> 1) & 1, fail);
@@ -808,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
                     for (int q = 0; q < parts; ++q)
                         #pragma unroll
                         for (int t = 0; t < 64; t += 16)  // (w V)^T K
-                            tc::mma(tm + C::kv(STATE, c), tm + C::w(STATE, fine, c) + q * 32 + t / 2, adv(d, t * 128), idS, q + t > 0);
+                            tc::mma(tm + C::kv(fine, c), tm + C::w(fine, c) + q * 32 + t / 2, adv(d, t * 128), idS, q + t > 0);
                     tc::commit(bar + kKvDone + (c & 1));
                     tc::commit(bar + kFree + ring.st);
                 }
@@ -817,7 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             }
             if (STATE || c + 1 >= n) continue;
             ok = rest(bar + kFull + ahead.st, ahead.parity, fail);
-            if (ok && c >= 1) ok = rest(bar + kORead + (~c & 1), ((c - 1) >> 1) & 1, fail);  // the buffer's last O has been read
+            const int before = c + 1 - C::nx(fine);  // whose O has to be read: the buffer's last
+            if (ok && before >= 0) ok = rest(bar + kORead + (before & 1), (before >> 1) & 1, fail);
             if (!ok) break;
             tc::fence_after();
             if (elect()) {
@@ -826,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
                 for (int f = 0; f < C::KT; ++f)
                     #pragma unroll
                     for (int t = 0; t < 128; t += 32)  // Q K^T
-                        tc::mma_ss(tm + C::x(c + 1), adv(dq, off + f * kTile + t), adv(dk, off + f * kTile + t), idX, f + t > 0);
+                        tc::mma_ss(tm + C::x(fine, c + 1), adv(dq, off + f * kTile + t), adv(dk, off + f * kTile + t), idX, f + t > 0);
                 tc::commit(bar + kScDone + (~c & 1));
             }
             __syncwarp();
@@ -860,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             if (elect()) {
                 #pragma unroll
                 for (int t = 0; t < 4; ++t)  // V^T P^T
-                    tc::mma_ss(tm + C::x(c), adv(dv, off + t * 2048), adv(dp, (c & 1) * kTile + t * 32), idO | kMnA, t > 0);
+                    tc::mma_ss(tm + C::x(fine, c), adv(dv, off + t * 2048), adv(dp, (c & 1) * kTile + t * 32), idO | kMnA, t > 0);
                 tc::commit(bar + kPvDone + (c & 1));
                 tc::commit(bar + kFree + ring.st);
             }
