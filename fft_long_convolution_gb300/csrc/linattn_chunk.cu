@@ -30,8 +30,8 @@
 //   warp 29      issues KV and the next chunk's scores;  warp 31  S Q and P V
 //
 // Bound: HBM where segments fill the SMs (262144 tokens, 6 heads of 128 x 128, bf16:
-// q, k, v read and o written in 250 us, 6.4 TB/s); else the chain of a chunk, 1.4 us in
-// bf16 and 1.9 us in fp16 or with three parts at 128 x 128, 1.0 to 1.6 us at 64 x 64 (8 x
+// q, k, v read and o written in 250 us, 6.4 TB/s); else the chain of a chunk, 1.3 us in
+// bf16 and 1.8 us in fp16 or with three parts at 128 x 128, 1.0 to 1.6 us at 64 x 64 (8 x
 // 4096 tokens, 6 heads of 128: the three gradients' walks 92 us side by side).  Three
 // loops of that chain are equally long: S Q, P V and the read of O; scores, P, P V and
 // O; w V, KV and S.  The tensor pipe is active 40 % of the time, the schedulers issue in
@@ -162,8 +162,9 @@ struct Cfg {
     // Tensor memory columns: S; S Q; scores and then P V; KV; w V, all 512 at Dk = 128.
     // w V has two buffers.  With its two parts the scores have two and KV one, and two at
     // Dk = 64, where there is room (2 % of a step in bf16).  With three parts (fine) KV has
-    // one, the scores one, and two at Dk = 64 (XXX).  Where only
-    // the states are wanted: KV and w V.
+    // one, the scores one, and two at Dk = 64 (150 rows of 4096 with final states: 82 us at
+    // 64 x 64, 124 at 128 x 128; with one buffer of w V and two of the scores 101 and 131).
+    // Where only the states are wanted: KV and w V.
     static __host__ __device__ constexpr int nx(bool fine) { return fine && DK_ == 128 ? 1 : 2; }
     static __host__ __device__ constexpr int nkv(bool fine) { return STATE || (!fine && DK_ == 64) ? 2 : 1; }
     static constexpr uint32_t cS = 0, cOi = DK_ / 2, cX = cOi + 64;
@@ -970,15 +971,15 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
 // Segments.  A sequence's chunks follow one another, so few long sequences leave SMs
 // idle.  Cut into m segments a walk costs another over K and V for the segments' end
 // states, and a join.  The rule counts waves of CTAs over the SMs.  Its unit is 0.07 us:
-// a chunk's step of a walk 20 (26 in fp16, and uncut, where w V takes three parts; 22 if
-// that is one walk of a training step's three), of the segments' states 9 (13); a CTA's
-// start and end 106 and 100; the second launch 90, with the join's 160.  Fitted to 1024
-// to 16384 tokens with 6 to 150 rows, uncut and in 2 to 48 segments: 0.6 % above the
-// fastest of them on average, 12 % at most in calls of more than 47 us.
+// a chunk's step of a walk 20 (22 uncut, where w V may take three parts; 26 in fp16), of
+// the segments' states 9 (13); a CTA's start and end 106 and 100; the second launch 90,
+// with the join's 160.  Fitted to 1024 to 16384 tokens with 6 to 150 rows, uncut and in
+// 2 to 48 segments: 0.9 % above the fastest of them on average, 15 % at most in calls of
+// more than 40 us.
 //
-// bf16 128 x 128, 16384 tokens, forward: 6 rows uncut 496 us, in 24 segments 72; 24 rows
-// 495, in 6 145; 60 rows 497, in 5 312.  Training step's gradients: 16 rows 503, in 3
-// 232, in 8 257.  2048 tokens: 36 rows forward 79, in 3 61; gradients 83, in 2 108.
+// bf16 128 x 128, 16384 tokens, forward: 6 rows uncut 457 us, in 24 segments 62; 24 rows
+// 459, in 6 134; 60 rows 461, in 5 298.  Training step's gradients: 16 rows 463, in 3
+// 224, in 8 244.  2048 tokens: 36 rows forward 71, in 3 51; gradients 83, in 2 100.
 // Packed rows are taken at their mean length, as the host does not know their offsets.
 //
 // The walks' CTAs join up to three segments themselves (8 rows of 4096, 6 heads of 128,
@@ -994,7 +995,7 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
     const int64_t n = (B * T / nseq + kChunk - 1) / kChunk;
     const bool f16 = dt == FFTCONV_F16;
     auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
-    int64_t best = 1, cost = waves(rows * walks) * (n * (f16 || walks == 1 ? 26 : 22) + 106);
+    int64_t best = 1, cost = waves(rows * walks) * (n * (f16 ? 26 : 22) + 106);
     for (int64_t m = 2; m * 2 <= n && m * rows <= 2 * sms; ++m) {
         const int64_t len = (n + m - 1) / m;
         const int64_t c = waves(m * rows * walks) * (len * (f16 ? 26 : 20) + 106) +
