@@ -236,7 +236,7 @@ Passes passes_of(const fftconv_linattn_s* p, const fftconv_linattn_args_t* x, co
     a.seg_chunks = l.seg.chunks;
     a.segments = l.seg.count;
     a.join = l.seg.join;
-    a.longest_first = x->offsets && l.seg.count == x->nseq && x->nseq <= 32;
+    a.longest_first = x->offsets && l.seg.by_length;
     a.err = p->dev_err;
     return a;
 }
@@ -362,11 +362,7 @@ extern "C" fftconv_status_t fftconv_linattn_forward(fftconv_linattn_t p, const f
     cudaError_t r = cudaSuccess;
     if (args->offsets) r = zero_gaps(args, c, 1, &vo, &c.Hv, &p->Dv, st);
     if (!c.nseq) return done(r);
-    if (r == cudaSuccess && l.cut(c.nseq)) {
-        r = launch_linattn(a, 1, true, p->dtype, p->Dk, p->Dv, st);
-        if (a.join) x.w.state_fin = state_out;
-        x.w.state_out = nullptr;  // the segments' walk has written them
-    }
+    if (r == cudaSuccess && l.cut(c.nseq)) r = launch_linattn(a, 1, true, p->dtype, p->Dk, p->Dv, st);
     if (r == cudaSuccess) r = launch_linattn(a, 1, false, p->dtype, p->Dk, p->Dv, st);
     return done(r);
 }
@@ -471,11 +467,7 @@ extern "C" fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t p, const 
     }
     if (c.nseq) {
         const bool same = p->Dk == p->Dv;
-        if (r == cudaSuccess && l.cut(c.nseq)) {
-            r = launch_linattn(b, 2, true, p->dtype, p->Dk, p->Dv, st);
-            if (a.join) xv.w.state_fin = only_dv.p[0].w.state_fin = d_state_in;
-            xv.w.state_out = only_dv.p[0].w.state_out = nullptr;  // the segments' walk has written them
-        }
+        if (r == cudaSuccess && l.cut(c.nseq)) r = launch_linattn(b, 2, true, p->dtype, p->Dk, p->Dv, st);
         if (r == cudaSuccess) r = launch_linattn(a, same ? 3 : 2, false, p->dtype, p->Dv, p->Dk, st);
         if (r == cudaSuccess && !same) r = launch_linattn(only_dv, 1, false, p->dtype, p->Dk, p->Dv, st);
         if (r == cudaSuccess && shared) {

@@ -31,7 +31,6 @@ struct Walk {
     const float* state_in;  // [nseq][H][DK][DV], or (turned) [nseq][H][DV][DK]; null: zero
     bool turned;
     float* state_out;  // [nseq][H][DK][DV], or null
-    float* state_fin;  // holds the last segments' end states, to become the final states; or null
 };
 
 // The log decay of a head, as the kernels take it.

@@ -206,6 +206,7 @@ struct Ring {
 struct Part {
     Seq s;
     int i;         // sequence
+    int64_t slot;  // segment slot
     int64_t tok0;  // its first token in the row
     int64_t left;  // tokens from there to the sequence's end
     int n;         // chunks
@@ -234,24 +235,43 @@ __device__ __forceinline__ bool find_part(const Walk& w, uint32_t L, uint32_t sl
     return true;
 }
 
-// The sequence of a given rank by length, of up to 32: a lane for each.  All lanes of a
-// warp.  Sequences that are not cut start in this order, as the longest one ends the
-// launch: 24 sequences of 1 to 2000 tokens with 12 heads take 75 us, in the order of the
-// row 94.  More than 32 even out by themselves.
-__device__ __forceinline__ int by_length(const Walk& w, int rank) {
+// The slot of the part of a given rank by length, of up to 32 sequences, a lane for each;
+// -1: there is none.  Whole segments come first, in the order of the row, then what is
+// left of each sequence (STATE: only of those that are cut).  All lanes of a warp.
+// Packed sequences start in this order, as the longest one ends the launch: 24 sequences
+// of 1 to 2000 tokens with 12 heads take 75 us, in the order of the row 94.  More than 32
+// even out by themselves.
+template <bool STATE>
+__device__ __forceinline__ int64_t by_length(const Walk& w, uint32_t L, int rank) {
     const int lane = threadIdx.x % 32;
-    const int len = lane < w.nseq ? int(locate(w.offsets, w.T, lane).len) : -1;
+    const bool real = lane < w.nseq;
+    const Seq s = locate(w.offsets, w.T, real ? lane : 0);
+    const uint32_t all = real ? uint32_t((s.len + kChunk - 1) / kChunk) : 0;
+    const int full = int(all / L), left = int(all - uint32_t(full) * L);
+    int upto = full;  // whole segments of this and the sequences before
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    const int whole = __shfl_sync(0xffffffffu, upto, 31);
+    const bool has = real && (STATE ? left > 0 && full > 0 : left > 0 || all == 0);
+    const int key = has ? left : -1;
     int longer = 0;
     #pragma unroll 1
     for (int i = 0; i < 32; ++i) {
-        const int y = __shfl_sync(0xffffffffu, len, i);
-        longer += y > len || (y == len && i < lane);
+        const int y = __shfl_sync(0xffffffffu, key, i);
+        longer += y > key || (y == key && i < lane);
     }
-    return __ffs(__ballot_sync(0xffffffffu, longer == rank)) - 1;
+    const bool mine = rank < whole ? upto > rank && upto - full <= rank : has && longer == rank - whole;
+    const uint32_t found = __ballot_sync(0xffffffffu, mine);
+    const int64_t slot = int64_t(uint32_t(s.slot) / L) + lane + (rank < whole ? rank - (upto - full) : full);
+    return found ? __shfl_sync(0xffffffffu, slot, __ffs(found) - 1) : -1;
 }
 
 // STATE: only the state at the end of a segment (from zero, or from the initial state);
-// a walk's last one, if the final state is wanted, to where that goes.
+// a walk's last one, if the final state is wanted, to where that goes.  Sequences of one
+// segment are left to the walk.
 template <int DT, int DK, int DV, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_constant__ Passes a) {
     using C = Cfg<DK, DV, STATE>;
@@ -288,8 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         Part* found = reinterpret_cast<Part*>(sm + C::oO);
         bool* any = reinterpret_cast<bool*>(found + 1);
         if (warp == 0) {
-            if (a.longest_first) slot = by_length(wk, slot);
-            live = find_part(wk, uint32_t(a.seg_chunks), slot, &p);
+            const int64_t at = a.longest_first ? by_length<STATE>(wk, uint32_t(a.seg_chunks), slot) : slot;
+            live = at >= 0 && find_part(wk, uint32_t(a.seg_chunks), uint32_t(at), &p);
+            p.slot = at;
             if (lane == 0) *found = p, *any = live;
         }
         __syncthreads();
@@ -297,15 +318,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         live = *any;
         __syncthreads();
     }
-    if (!live || (STATE && p.last && !wk.state_out)) return;
+    if (!live || (STATE && p.last && (p.first || !wk.state_out))) return;
     const int n = p.n;
-    const int64_t hs = int64_t(p.i) * wk.H + h, gs = int64_t(slot) * wk.H + h;
+    const int64_t hs = int64_t(p.i) * wk.H + h, gs = p.slot * wk.H + h;
     const float* sin = wk.state_in ? wk.state_in + hs * DK * DV : nullptr;
     // what the walk's segment before left, and the way to those before it
     const int64_t back = (reverse ? 1 : -1) * int64_t(wk.H) * DK * DV;
     if (!p.first) sin = STATE ? nullptr : x.seg_state + gs * DK * DV + back;
-    float* sout = p.last && wk.state_out ? wk.state_out + hs * DK * DV : nullptr;
-    if (STATE && !p.last) sout = x.seg_state + gs * DK * DV;
+    float* fin = p.last && wk.state_out ? wk.state_out + hs * DK * DV : nullptr;
+    float* sout = STATE ? (p.last ? fin : x.seg_state + gs * DK * DV) : p.first ? fin : nullptr;
     // w V in three parts (bf16) where the state at the end is wanted for itself
     const bool fine = DT == 1 && (STATE || sout);
     const int parts = fine ? 3 : 2;
@@ -317,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             if (i == kPReady || i == kPReady + 1 || i >= kSizes) cnt = 4;
             if (i == kORead || i == kORead + 1 || i == kOReady) cnt = 8;
             if (i >= kFree && i < kFree + kMaxStages && !STATE) cnt = 2;  // both warps that issue products
-            if (i == kParts || i == kParts + 1) cnt = DT == 1 && (STATE || (p.last && wk.state_out)) ? 16 : 8;
+            if (i == kParts || i == kParts + 1) cnt = fine ? 16 : 8;
             if (i == kSop || i == kKvRead || i == kKvRead + 1) cnt = 16;
             mbar_init(bar + i, cnt);
         }
@@ -395,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
                 S[j] = make_float2(decayed(over, S[j].x, N.x), decayed(over, S[j].y, N.y));
             }
         }
-        if (join && p.last && wk.state_fin && mine) {  // and the sequence's final state
-            float* out = wk.state_fin + hs * DK * DV + dv;
+        if (join && fin && mine) {  // and the sequence's final state
+            float* out = fin + dv;
             const Decay rest_of = decay_over(g, float(all));
             #pragma unroll
             for (int j = 0; j < NC; ++j) {
@@ -954,12 +975,16 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
     cudaError_t e = opt_in(linattn_walk_kernel<DT, DK, DV, false>, walk, c0);
     if (e == cudaSuccess) e = opt_in(linattn_walk_kernel<DT, DK, DV, true>, ends, c1);
     if (e != cudaSuccess) return e;
-    const dim3 grid(unsigned(a.segments), unsigned(a.p[0].w.H), unsigned(n));
+    const int64_t nseq = a.p[0].w.nseq;
+    dim3 grid(unsigned(a.segments), unsigned(a.p[0].w.H), unsigned(n));
     if (states) {
+        // by length, whole segments and what is left of cut sequences come first: at most
+        // one of the latter for one of the former
+        if (a.longest_first && 2 * (a.segments - nseq) < a.segments) grid.x = unsigned(2 * (a.segments - nseq));
         linattn_walk_kernel<DT, DK, DV, true><<<grid, kThreads, ends, st>>>(a);
         if (a.join) return cudaGetLastError();
         constexpr int size = DK * DV;
-        linattn_join_kernel<<<dim3(unsigned(a.p[0].w.nseq) * (size / 1024), grid.y, grid.z), 256, 0, st>>>(a, size);
+        linattn_join_kernel<<<dim3(unsigned(nseq) * (size / 1024), grid.y, grid.z), 256, 0, st>>>(a, size);
     } else {
         linattn_walk_kernel<DT, DK, DV, false><<<grid, kThreads, walk, st>>>(a);
     }
@@ -980,17 +1005,23 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
 // bf16 128 x 128, 16384 tokens, forward: 6 rows uncut 457 us, in 24 segments 62; 24 rows
 // 459, in 6 134; 60 rows 461, in 5 298.  Training step's gradients: 16 rows 463, in 3
 // 224, in 8 244.  2048 tokens: 36 rows forward 71, in 3 51; gradients 83, in 2 100.
-// Packed rows are taken at their mean length, as the host does not know their offsets.
+// Packed rows are taken at their mean length, as the host does not know their offsets; up
+// to 32 sequences that this leaves uncut are cut at four times that where the estimate is
+// above 140 us, which costs a launch of CTAs with nothing to do where none is as long: 12
+// heads of 128 x 128, bf16, 60000 tokens among 31 of 178: 324 us, uncut 1645; 32 of 2048:
+// 227, uncut 214.
 //
 // The walks' CTAs join up to three segments themselves (8 rows of 4096, 6 heads of 128,
 // three segments: 99 us with the inputs from memory, against 107 with the join's launch;
 // four segments: 128 against 129; six: 121 against 105, as the reads of the states before
-// follow one another).
+// follow one another), and the few long sequences of an uneven queue (up to nine segments),
+// where a launch would mostly find nothing to do.
 void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int dt, int sms) {
     const int64_t slots = chunk_slots(B, T, nseq), rows = nseq * heads;
     s->chunks = slots + 1;
     s->count = nseq;
     s->join = false;
+    s->by_length = nseq <= kSorted;
     if (rows == 0) return;
     const int64_t n = (B * T / nseq + kChunk - 1) / kChunk;
     const bool f16 = dt == FFTCONV_F16;
@@ -1005,10 +1036,12 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
             best = m;
         }
     }
-    if (best == 1) return;
-    s->chunks = (n + best - 1) / best;
+    const bool uneven = best == 1 && B == 1 && nseq > 1 && nseq <= kSorted && cost >= 2000;
+    if (best == 1 && !uneven) return;
+    s->chunks = uneven ? 4 * n : (n + best - 1) / best;
     s->count = slots / s->chunks + nseq;
     s->join = best <= 3;
+    s->by_length = best == 1 && nseq <= kSorted;
 }
 
 cudaError_t launch_linattn(const Passes& a, int n, bool states, int dt, int dk, int dv, cudaStream_t st) {

@@ -14,27 +14,29 @@ struct Pass {
     float* seg_state;
 };
 
+constexpr int kSorted = 32;
+
 // Up to three walks of the same sizes, side by side.
 struct Passes {
     Pass p[3];
     int64_t seg_chunks;
     int64_t segments;
     bool join;           // a walk's CTAs join the segments' states themselves
-    bool longest_first;  // uncut packed sequences, in the order of their lengths
+    bool longest_first;  // packed sequences (up to kSorted), in the order of their lengths
     int* err;
 };
 
 // Chunks of a segment, and how many segment slots there are (nseq: no sequence is cut),
 // for `walks` walks at once.  join: few enough for the walks' CTAs to add up the states
-// before theirs.
+// before theirs.  by_length: packed sequences in the order of their lengths.
 struct Segments {
     int64_t chunks, count;
-    bool join;
+    bool join, by_length;
 };
 void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int dt, int sms);
 
-// states: the end states of all segments (of the walks' last where the final state is
-// wanted), joined along each sequence unless a.join.
+// states: the end states of all segments of sequences that are cut (of a walk's last one
+// where the final state is wanted), joined along each sequence unless a.join.
 cudaError_t launch_linattn(const Passes& a, int n, bool states, int dt, int dk, int dv, cudaStream_t st);
 
 }  // namespace fftconv

@@ -84,6 +84,39 @@ def test_queues_of_many_prompts(n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 64)])
+def test_skewed_queue(Dk, Dv, dt):
+    """One prompt as long as all the others: 20 of 90 chunks on average, cut at 360 chunks.
+    Up to 938 chunks: (12 + 938) 2^-23 for the states."""
+    Hk, Hv = 2, 4
+    lens = [1, 0, 60000, 64, 23040, 23041, 5000] + [300] * 12
+    lens.append(20 * 90 * 64 - sum(lens))
+    n, T = len(lens), sum(lens)
+    ins = [x.cuda() for x in attention_inputs(1, T, Hk, Hv, Dk, Dv, dt, seed=71)]
+    do = attention_inputs(1, T, Hk, Hv, Dk, Dv, dt, seed=72)[2].cuda()
+    s0, ds = states(n, Hv, Dk, Dv).cuda(), states(n, Hv, Dk, Dv, seed=73).cuda()
+    off = torch.zeros(n + 1, dtype=torch.int32)
+    off[1:] = torch.cumsum(torch.tensor(lens), 0)
+    plan = F.LinearAttention(Dk, Dv, dt)
+    o, s = plan.forward(*ins, state=s0, offsets=off.cuda())
+    got = plan.backward(do, *ins, state=s0, dstate=ds, offsets=off.cuda())
+    for i, L in enumerate(lens):
+        if not L:
+            assert torch.equal(s[i], s0[i]) and torch.equal(got[3][i], ds[i])
+            continue
+        at = slice(int(off[i]), int(off[i]) + L)
+        xs = [x.double().requires_grad_() for x in (*[y[:, at] for y in ins[:3]], s0[i:i + 1])]
+        ro, rs = attention_chunks(*xs[:3], ins[3], xs[3], Dk ** -0.5)
+        assert rel(o[:, at], ro.detach()) < U[dt] and rel(s[i:i + 1], rs.detach()) < 1.2e-4, i
+        ref = torch.autograd.grad((ro * do[:, at].double()).sum() + (rs * ds[i:i + 1].double()).sum(), xs)
+        for name, x, y in zip(NAMES[:3], got, ref):
+            assert rel(x[:, at], y) < U[dt], (name, i)
+        assert rel(got[3][i:i + 1], ref[3]) < 1.2e-4, i
+    assert plan.device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [70, 2550])
 def test_gradients_of_final_states_without_initial_ones(T):
     dt, B, Hk, Hv, Dk, Dv = torch.bfloat16, 2, 1, 2, 64, 128
