@@ -1005,7 +1005,7 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
 // bf16 128 x 128, 16384 tokens, forward: 6 rows uncut 457 us, in 24 segments 62; 24 rows
 // 459, in 6 134; 60 rows 461, in 5 298.  Training step's gradients: 16 rows 463, in 3
 // 224, in 8 244.  2048 tokens: 36 rows forward 71, in 3 51; gradients 83, in 2 100.
-// Packed rows are taken at their mean length, as the host does not know their offsets; up
+// Packed rows are taken at their mean length, as the host does not know their offsets; 9
 // to 32 sequences that this leaves uncut are cut at four times that where the estimate is
 // above 140 us, which costs a launch of CTAs with nothing to do where none is as long: 12
 // heads of 128 x 128, bf16, 60000 tokens among 31 of 178: 324 us, uncut 1645; 32 of 2048:
@@ -1036,7 +1036,7 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
             best = m;
         }
     }
-    const bool uneven = best == 1 && B == 1 && nseq > 1 && nseq <= kSorted && cost >= 2000;
+    const bool uneven = best == 1 && B == 1 && nseq > 8 && nseq <= kSorted && cost >= 2000;
     if (best == 1 && !uneven) return;
     s->chunks = uneven ? 4 * n : (n + best - 1) / best;
     s->count = slots / s->chunks + nseq;
