@@ -1023,7 +1023,9 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
     s->join = false;
     s->by_length = nseq <= kSorted;
     if (rows == 0) return;
-    const int64_t n = (B * T / nseq + kChunk - 1) / kChunk;
+    // chunks of a sequence of mean length, at least one: there may be fewer tokens than sequences
+    const int64_t mean = (B * T / nseq + kChunk - 1) / kChunk, n = mean > 0 ? mean : 1;
+    const int64_t most = (T + kChunk - 1) / kChunk;  // chunks that one sequence may have
     const bool f16 = dt == FFTCONV_F16;
     auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
     int64_t best = 1, cost = waves(rows * walks) * (n * (f16 ? 26 : 22) + 106);
@@ -1036,7 +1038,7 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
             best = m;
         }
     }
-    const bool uneven = best == 1 && B == 1 && nseq > 8 && nseq <= kSorted && cost >= 2000;
+    const bool uneven = best == 1 && B == 1 && nseq > 8 && nseq <= kSorted && cost >= 2000 && most > 4 * n;
     if (best == 1 && !uneven) return;
     s->chunks = uneven ? 4 * n : (n + best - 1) / best;
     s->count = slots / s->chunks + nseq;

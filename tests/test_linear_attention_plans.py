@@ -1,0 +1,87 @@
+"""How the linear attention plans its calls: scratch sizes of rows of any shape, on the
+host, and the calls that such plans lead to."""
+import ctypes
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+import fft_long_convolution_gb300 as F
+from _attention import attention_grads, attention_inputs, linear_attention, rel, states
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+NAMES = ("dq", "dk", "dv", "dstate")
+
+
+class PlanOnHost(ctypes.Structure):
+    """What a plan holds, for the calls that need no device."""
+    _fields_ = [("Dk", ctypes.c_int), ("Dv", ctypes.c_int), ("dtype", ctypes.c_int), ("device", ctypes.c_int),
+                ("num_sms", ctypes.c_int), ("dev_err", ctypes.c_void_p)]
+
+
+def scratch_bytes(B, T, Hk, Hv, nseq, backward, Dk=64, Dv=64, dtype=1):
+    plan = PlanOnHost(Dk, Dv, dtype, 0, 152, None)
+    return int(F.lib().fftconv_linattn_scratch_bytes(ctypes.addressof(plan), B, T, Hk, Hv, nseq, backward))
+
+
+def sweep_of_short_rows():
+    """Packed rows of few tokens (at most one for each sequence): nothing to cut, no scratch."""
+    for nseq in range(1, 70):
+        for T in {0, 1, nseq - 1, nseq}:
+            for H in (1, 2, 7, 12, 16, 28, 29, 32, 48, 64, 85, 86, 96, 128, 300, 1000):
+                for dtype in (0, 1):
+                    for backward in (0, 1):
+                        n = scratch_bytes(1, T, H, H, nseq, backward, dtype=dtype)
+                        assert n == 0 or T > 64, (nseq, T, H, dtype, backward, n)
+
+
+def test_rows_of_fewer_tokens_than_sequences():
+    """In a process of its own: a division by zero ends it."""
+    r = subprocess.run([sys.executable, __file__], capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": os.pathsep.join(p for p in sys.path if p)})
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+
+
+def offsets_of(lens):
+    off = torch.zeros(len(lens) + 1, dtype=torch.int32)
+    off[1:] = torch.cumsum(torch.tensor(lens), 0)
+    return off
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", U)
+@pytest.mark.parametrize("lens", [[0] * 32, [1] * 20 + [0] * 11 + [0], [0] * 15 + [20] + [0] * 16, [2, 0, 3] + [0] * 9])
+def test_queues_of_mostly_empty_prompts(lens, dt):
+    """Fewer tokens than sequences over many heads.  Tolerances: o and the gradients have one
+    rounding at the end and one operand rounded in each term, u together; states are sums of
+    one chunk, 12 2^-23 and the parts' 2^-22."""
+    Hk, Hv, Dk, Dv, n, T = 48, 96, 64, 64, len(lens), sum(lens)
+    ins = attention_inputs(1, T, Hk, Hv, Dk, Dv, dt, seed=n)
+    do = attention_inputs(1, T, Hk, Hv, Dk, Dv, dt, seed=n + 1)[2]
+    s0, ds = states(n, Hv, Dk, Dv), states(n, Hv, Dk, Dv, seed=2)
+    off = offsets_of(lens).cuda()
+    plan = F.LinearAttention(Dk, Dv, dt)
+    dins = [x.cuda() for x in ins]
+    o, s = plan.forward(*dins, state=s0.cuda(), offsets=off)
+    got = plan.backward(do.cuda(), *dins, state=s0.cuda(), dstate=ds.cuda(), offsets=off)
+    assert o.shape == (1, T, Hv, Dv) and s.shape == s0.shape
+    at = 0
+    for i, L in enumerate(lens):
+        if L == 0:
+            assert torch.equal(s[i].cpu(), s0[i]) and torch.equal(got[3][i].cpu(), ds[i]), i
+            continue
+        part = [x[:, at:at + L] for x in ins[:3]] + [ins[3]]
+        ref, sref = linear_attention(*part, state=s0[i:i + 1], scale=Dk ** -0.5)
+        assert rel(o[:, at:at + L], ref) < U[dt] and rel(s[i:i + 1], sref) < 4e-6, i
+        r = attention_grads(*part, do[:, at:at + L], s0[i:i + 1], ds[i:i + 1], Dk ** -0.5)
+        for name, x, y in zip(NAMES[:3], got, r):
+            assert rel(x[:, at:at + L], y) < U[dt], (name, i)
+        assert rel(got[3][i:i + 1], r[3]) < 4e-6, i
+        at += L
+    assert plan.device_status() == 0
+
+
+if __name__ == "__main__":
+    sweep_of_short_rows()
