@@ -76,8 +76,10 @@ __device__ __forceinline__ void st16x128b_x4(uint32_t taddr, const uint32_t (&r)
 
 // Bounded wait of a whole warp that sleeps until the phase is over, so that the roles
 // that wait leave the issue slots to those that work.  Gives up after about a second,
-// or when another role has (*fail set).  The first poll nearly always suffices (it may
-// suspend the warp for kWaitHintNs); what follows it is kept out of the roles' loops.
+// or when another role has (*fail set).  Each lane gets an answer of its own from a poll,
+// so every one is voted on: the warp goes on as a whole, to instructions that ask for all
+// its lanes, or rests as a whole.  The first poll nearly always suffices (it may suspend
+// the warp for kWaitHintNs); what follows it is kept out of the roles' loops.
 __device__ __forceinline__ bool poll(uint32_t addr, uint32_t parity) {
     uint32_t over;
     asm volatile(
@@ -99,7 +101,7 @@ __device__ __noinline__ bool rest_on(uint32_t addr, uint32_t parity, volatile in
 
 __device__ __forceinline__ bool rest(uint64_t* bar, uint32_t parity, volatile int* fail) {
     const uint32_t addr = smem_u32(bar);
-    if (__builtin_expect(poll(addr, parity), 1)) return true;  // the same answer in every lane: one poll of one address
+    if (__builtin_expect(__all_sync(0xffffffffu, poll(addr, parity)), 1)) return true;
     return rest_on(addr, parity, fail);
 }
 
@@ -924,6 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    __syncwarp();
     if (warp == 29) tc::dealloc(tm, 512);
     if (threadIdx.x == 0 && s_fail) atomicExch(a.err, 7);
 }
