@@ -952,7 +952,7 @@ cudaError_t launch(const GradArgs& a, cudaStream_t st) {
     if (a.dqh) {
         const int64_t n = (a.d.B * a.d.T * a.d.Hk * (DK / 8) * 2 + 255) / 256;
         head_sum_kernel<DT><<<unsigned(n < 152 * 32 ? n : 152 * 32), 256, 0, st>>>(a.dqh, a.dkh, a.dq, a.dk, a.d.B * a.d.T,
-                                                                                  a.d.T, a.d.Hk, a.d.group, DK);
+                                                                                  a.d.T, a.d.Hk, a.d.group, DK, nullptr, 0);
     }
     return cudaGetLastError();
 }

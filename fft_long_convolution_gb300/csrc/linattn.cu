@@ -461,9 +461,7 @@ extern "C" fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t p, const 
     if (args->offsets) {
         const View zs[3] = {vdq, vdk, vdv};
         const int zh[3] = {c.Hk, c.Hk, c.Hv}, zd[3] = {p->Dk, p->Dk, p->Dv};
-        // with shared heads dq and dk are summed from float32 parts, zero in the gaps
-        if (shared) r = cudaMemsetAsync(at + l.q, 0, l.total - l.q, st);
-        if (r == cudaSuccess) r = zero_gaps(args, c, 3, zs, zh, zd, st);
+        r = zero_gaps(args, c, 3, zs, zh, zd, st);
     }
     if (c.nseq) {
         const bool same = p->Dk == p->Dv;
@@ -474,7 +472,8 @@ extern "C" fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t p, const 
             const int64_t n = (c.B * c.T * c.Hk * (p->Dk / 8) * 2 + 255) / 256;
             const unsigned grid = unsigned(n < 152 * 32 ? n : 152 * 32);
             auto f = p->dtype == FFTCONV_F16 ? head_sum_kernel<0> : head_sum_kernel<1>;
-            f<<<grid, 256, 0, st>>>(dq32, dk32, vdq, vdk, c.B * c.T, c.T, c.Hk, c.group, p->Dk);
+            f<<<grid, 256, 0, st>>>(dq32, dk32, vdq, vdk, c.B * c.T, c.T, c.Hk, c.group, p->Dk, args->offsets,
+                                    c.nseq);
             r = cudaGetLastError();
         }
     }

@@ -7,9 +7,21 @@
 namespace fftconv {
 namespace {
 
-// Zero the tokens of a packed row that belong to no sequence: those before the
-// first offset and from the last one on (offsets do not decrease); without
-// sequences, every token of every row.
+// The tokens of a packed row that belong to a sequence: from the first offset to the
+// last one (offsets do not decrease); none without sequences.
+struct Covered {
+    int64_t lo, hi;
+};
+
+__device__ __forceinline__ Covered covered(const int32_t* offsets, int nseq, int64_t T) {
+    int64_t lo = nseq ? offsets[0] : T, hi = nseq ? offsets[nseq] : T;
+    lo = lo < 0 ? 0 : (lo > T ? T : lo);
+    hi = hi < lo ? lo : (hi > T ? T : hi);
+    return {lo, hi};
+}
+
+// Zero the tokens of a packed row that belong to no sequence; without sequences,
+// every token of every row.
 template <int N>
 struct GapArgs {
     View v[N];
@@ -22,9 +34,7 @@ struct GapArgs {
 
 template <int N>
 __global__ void __launch_bounds__(256) gap_kernel(const GapArgs<N> a) {
-    int64_t lo = a.nseq ? a.offsets[0] : a.T, hi = a.nseq ? a.offsets[a.nseq] : a.T;
-    lo = lo < 0 ? 0 : (lo > a.T ? a.T : lo);
-    hi = hi < lo ? lo : (hi > a.T ? a.T : hi);
+    const auto [lo, hi] = covered(a.offsets, a.nseq, a.T);
     const int64_t tokens = lo + a.T - hi;
     for (int i = 0; i < a.n; ++i) {
         const int64_t per = int64_t(a.H[i]) * a.D[i], row = tokens * per, n = a.B * row;
@@ -37,10 +47,14 @@ __global__ void __launch_bounds__(256) gap_kernel(const GapArgs<N> a) {
 }
 
 // dq, dk [token][Hk][DK] = the sum over a key head's value heads, 8 features a thread, in the
-// heads' order.  Bound: HBM (16 x 1000 tokens, 12 heads over 6 of 64: 123 MB in 22 us, 5.5 TB/s).
+// heads' order.  With offsets the tokens of no sequence are left out: no part of theirs is
+// formed, and gap_kernel has zeroed them.  Bound: HBM (16 x 1000 tokens, 12 heads over 6
+// of 64: 123 MB in 22 us, 5.5 TB/s).
 template <int DT>
 __global__ void __launch_bounds__(256) head_sum_kernel(const float* xq, const float* xk, View yq, View yk, int64_t tokens,
-                                                       int64_t T, int Hk, int group, int DK) {
+                                                       int64_t T, int Hk, int group, int DK, const int32_t* offsets,
+                                                       int nseq) {
+    const Covered in = offsets ? covered(offsets, nseq, T) : Covered{0, T};
     const int np = DK / 8;
     const int64_t n = tokens * Hk * np * 2;
     for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < n; e += int64_t(gridDim.x) * 256) {
@@ -49,6 +63,7 @@ __global__ void __launch_bounds__(256) head_sum_kernel(const float* xq, const fl
         const View& y = e & 1 ? yk : yq;
         const int r = int(e2 % np) * 8;
         const int64_t hk = (e2 / np) % Hk, tok = e2 / np / Hk, b = tok / T, t = tok - b * T;
+        if (t < in.lo || t >= in.hi) continue;
         float4 u = make_float4(0, 0, 0, 0), v = u;
         for (int j = 0; j < group; ++j) {
             const float* q = x + ((tok * Hk + hk) * group + j) * DK + r;

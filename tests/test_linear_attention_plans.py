@@ -83,5 +83,31 @@ def test_queues_of_mostly_empty_prompts(lens, dt):
     assert plan.device_status() == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", U)
+@pytest.mark.parametrize("lens,before,behind", [([70, 0, 5, 130], 9, 11), ([64], 0, 0), ([3, 1], 0, 100), ([], 20, 0), ([0], 5, 5)])
+def test_parts_of_shared_heads_in_gaps(lens, before, behind, dt):
+    """Parts of dq and dk for each value head are formed and read for the sequences' tokens
+    alone: scratch of NaN leaves no trace, and stays NaN for the others."""
+    Hk, Hv, D, n, T = 2, 6, 64, len(lens), before + sum(lens) + behind
+    q, k, v, decay = (x.cuda() for x in attention_inputs(1, T, Hk, Hv, D, D, dt, seed=n))
+    do = attention_inputs(1, T, Hk, Hv, D, D, dt, seed=n + 1)[2].cuda()
+    off = (offsets_of(lens) + before).cuda()
+    plan = F.LinearAttention(D, D, dt)
+    want = plan.backward(do, q, k, v, decay, offsets=off)
+    L, a = F.lib(), plan._args(q, k, v, decay, off, None)
+    need = L.fftconv_linattn_scratch_bytes(plan._h, 1, T, Hk, Hv, n, 1)
+    assert need == 2 * T * Hv * D * 4  # the parts, and nothing else
+    scratch = torch.full((need // 4,), float("nan"), device="cuda")
+    got = [torch.full_like(x, 3.0) for x in (q, k, v)]
+    views = [F.View(*F._strides(x, "x", dt, x.shape)) for x in (do, *got)]
+    status = L.fftconv_linattn_backward(plan._h, ctypes.byref(a), None, views[0], None, *views[1:], None, scratch.data_ptr(),
+                                        need, torch.cuda.current_stream().cuda_stream)
+    assert status == 0 and plan.device_status() == 0
+    for x, y in zip(got, want):
+        assert torch.equal(x, y) and not bool(x[:, :before].any()) and not bool(x[:, T - behind:].any())
+    assert int(scratch.isnan().sum()) == 2 * (before + behind) * Hv * D
+
+
 if __name__ == "__main__":
     sweep_of_short_rows()
