@@ -212,7 +212,7 @@ struct Part {
     int64_t tok0;  // its first token in the row
     int64_t left;  // tokens from there to the sequence's end
     int n;         // chunks
-    int before;        // segments before it in the walk's order
+    int count, before;  // segments of the sequence, and those before this one in the walk's order
     bool first, last;  // in that order
 };
 
@@ -231,7 +231,8 @@ __device__ __forceinline__ bool find_part(const Walk& w, uint32_t L, uint32_t sl
     p->first = w.reverse ? high : low;
     p->last = w.reverse ? low : high;
     p->n = int(high ? all - from : L);
-    p->before = int(w.reverse ? (all + L - 1) / L - 1 - seg : seg);
+    p->count = int((all + L - 1) / L);
+    p->before = int(w.reverse ? p->count - 1 - seg : seg);
     p->tok0 = p->s.start + from * kChunk;
     p->left = p->s.len - from * kChunk;
     return true;
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         float2 S[NC / 2] = {};
         // the state before: one that is given or joined, or the end states of all segments
         // before, the first one first
-        const bool join = !STATE && !p.first && a.join;
+        const bool join = !STATE && !p.first && p.count <= a.join;
         const Decay over = decay_over(g, float(a.seg_chunks * kChunk));
         #pragma unroll 1
         for (int i = join ? p.before : 1; mine && sin && i > 0; --i) {
@@ -933,15 +934,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
 
 // The states at the segments' ends, along a sequence in the walk's order: X_p =
 // l^(tokens of a segment) X_(p-1) + N_p, float32, in place of N_p; the walk's last one
-// is the sequence's final state, if that is wanted.  Four elements a thread, four
-// segments in flight.
+// is the sequence's final state, if that is wanted.  Sequences of up to a.join segments
+// are left to the walks' CTAs.  Four elements a thread, four segments in flight.
 __global__ void __launch_bounds__(256) linattn_join_kernel(const __grid_constant__ Passes a, int size) {
     const Pass& x = a.p[blockIdx.z];
     const Walk& w = x.w;
     const int chunks = size / 1024, i = blockIdx.x / chunks, h = blockIdx.y;
     const Seq s = locate(w.offsets, w.T, i);
     const int64_t all = (s.len + kChunk - 1) / kChunk, nseg = (all + a.seg_chunks - 1) / a.seg_chunks;
-    if (nseg < (w.state_out ? 2 : 3)) return;
+    if (nseg <= a.join || nseg < (w.state_out ? 2 : 3)) return;
     const int64_t g0 = s.slot / a.seg_chunks + i, step = (w.reverse ? -1 : 1) * int64_t(w.H) * size;
     float4* at = reinterpret_cast<float4*>(x.seg_state + ((g0 + (w.reverse ? nseg - 1 : 0)) * w.H + h) * size +
                                            (blockIdx.x % chunks) * 1024 + threadIdx.x * 4);
@@ -985,7 +986,7 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
         // one of the latter for one of the former
         if (a.longest_first && 2 * (a.segments - nseq) < a.segments) grid.x = unsigned(2 * (a.segments - nseq));
         linattn_walk_kernel<DT, DK, DV, true><<<grid, kThreads, ends, st>>>(a);
-        if (a.join) return cudaGetLastError();
+        if (a.most <= a.join) return cudaGetLastError();
         constexpr int size = DK * DV;
         linattn_join_kernel<<<dim3(unsigned(nseq) * (size / 1024), grid.y, grid.z), 256, 0, st>>>(a, size);
     } else {
@@ -1018,12 +1019,16 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
 // three segments: 99 us with the inputs from memory, against 107 with the join's launch;
 // four segments: 128 against 129; six: 121 against 105, as the reads of the states before
 // follow one another), and the few long sequences of an uneven queue (up to nine segments),
-// where a launch would mostly find nothing to do.
+// where a launch would mostly find nothing to do.  A packed row that is cut by its mean
+// length may hold a sequence of many more segments: the launch joins those (one prompt of
+// 56226 tokens, 126 segments, among 49 of 190, one head of 128, bf16: 86 us, 196 with its
+// segments joined one after another; 50 of 1311: 65 us, 60 without the launch).
 void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int dt, int sms) {
     const int64_t slots = chunk_slots(B, T, nseq), rows = nseq * heads;
     s->chunks = slots + 1;
     s->count = nseq;
-    s->join = false;
+    s->join = 0;
+    s->most = 1;
     s->by_length = nseq <= kSorted;
     if (rows == 0) return;
     // chunks of a sequence of mean length, at least one: there may be fewer tokens than sequences
@@ -1045,7 +1050,8 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
     if (best == 1 && !uneven) return;
     s->chunks = uneven ? 4 * n : (n + best - 1) / best;
     s->count = slots / s->chunks + nseq;
-    s->join = best <= 3;
+    s->join = uneven ? 9 : best <= 3 ? 3 : 0;
+    s->most = (most + s->chunks - 1) / s->chunks;
     s->by_length = best == 1 && nseq <= kSorted;
 }
 

@@ -21,22 +21,25 @@ struct Passes {
     Pass p[3];
     int64_t seg_chunks;
     int64_t segments;
-    bool join;           // a walk's CTAs join the segments' states themselves
+    int join;            // a walk's CTAs join the states of sequences of up to so many segments themselves
+    int64_t most;        // segments that a sequence may have: past join, the join is launched
     bool longest_first;  // packed sequences (up to kSorted), in the order of their lengths
     int* err;
 };
 
 // Chunks of a segment, and how many segment slots there are (nseq: no sequence is cut),
-// for `walks` walks at once.  join: few enough for the walks' CTAs to add up the states
-// before theirs.  by_length: packed sequences in the order of their lengths.
+// for `walks` walks at once.  join: the most segments of a sequence whose states the
+// walks' CTAs add up themselves; most: segments that a sequence may have.  by_length:
+// packed sequences in the order of their lengths.
 struct Segments {
-    int64_t chunks, count;
-    bool join, by_length;
+    int64_t chunks, count, most;
+    int join;
+    bool by_length;
 };
 void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int dt, int sms);
 
 // states: the end states of all segments of sequences that are cut (of a walk's last one
-// where the final state is wanted), joined along each sequence unless a.join.
+// where the final state is wanted), joined along each sequence of more than a.join.
 cudaError_t launch_linattn(const Passes& a, int n, bool states, int dt, int dk, int dv, cudaStream_t st);
 
 }  // namespace fftconv

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import fft_long_convolution_gb300 as F
-from _attention import attention_grads, attention_inputs, linear_attention, rel, states
+from _attention import attention_chunks, attention_grads, attention_inputs, linear_attention, rel, states
 
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 NAMES = ("dq", "dk", "dv", "dstate")
@@ -107,6 +107,41 @@ def test_parts_of_shared_heads_in_gaps(lens, before, behind, dt):
     for x, y in zip(got, want):
         assert torch.equal(x, y) and not bool(x[:, :before].any()) and not bool(x[:, T - behind:].any())
     assert int(scratch.isnan().sum()) == 2 * (before + behind) * Hv * D
+
+
+def queue_against_definition(lens, Hk, Hv, D, dt, state_tol):
+    """A packed row's outputs, states and gradients against the 64-bit definition."""
+    n, T = len(lens), sum(lens)
+    ins = [x.cuda() for x in attention_inputs(1, T, Hk, Hv, D, D, dt, seed=n)]
+    do = attention_inputs(1, T, Hk, Hv, D, D, dt, seed=n + 1)[2].cuda()
+    s0, ds = states(n, Hv, D, D).cuda(), states(n, Hv, D, D, seed=3).cuda()
+    off = offsets_of(lens).cuda()
+    plan = F.LinearAttention(D, D, dt)
+    o, s = plan.forward(*ins, state=s0, offsets=off)
+    got = plan.backward(do, *ins, state=s0, dstate=ds, offsets=off)
+    for i, L in enumerate(lens):
+        if not L:
+            assert torch.equal(s[i], s0[i]) and torch.equal(got[3][i], ds[i])
+            continue
+        at = slice(int(off[i]), int(off[i]) + L)
+        xs = [x.double().requires_grad_() for x in (*[y[:, at] for y in ins[:3]], s0[i:i + 1])]
+        ro, rs = attention_chunks(*xs[:3], ins[3], xs[3], D ** -0.5, C=200)
+        assert rel(o[:, at], ro.detach()) < U[dt] and rel(s[i:i + 1], rs.detach()) < state_tol, i
+        ref = torch.autograd.grad((ro * do[:, at].double()).sum() + (rs * ds[i:i + 1].double()).sum(), xs)
+        for name, x, y in zip(NAMES[:3], got, ref):
+            assert rel(x[:, at], y) < U[dt], (name, i)
+        assert rel(got[3][i:i + 1], ref[3]) < state_tol, i
+    assert plan.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", U)
+@pytest.mark.parametrize("lens,Hk,Hv", [([190] * 25 + [56226] + [190] * 24, 1, 1), ([40000] + [0] * 3 + [64] * 12 + [24001] + [130] * 9, 1, 2),
+                                        ([1000, 25537] + [1000] * 6, 6, 6)])
+def test_rows_cut_by_their_mean_length_with_a_long_prompt(lens, Hk, Hv, dt):
+    """One prompt of a queue has most of the segments, dozens of them.  States: (12 + up to
+    880 chunks) 2^-23."""
+    queue_against_definition(lens, Hk, Hv, 64, dt, 1.1e-4)
 
 
 if __name__ == "__main__":
