@@ -237,6 +237,7 @@ Passes passes_of(const fftconv_linattn_s* p, const fftconv_linattn_args_t* x, co
     a.segments = l.seg.count;
     a.join = l.seg.join;
     a.most = l.seg.most;
+    a.few_cut = l.seg.few_cut;
     a.longest_first = x->offsets && l.seg.by_length;
     a.err = p->dev_err;
     return a;

@@ -38,6 +38,7 @@
 // 55 %.
 #include "linattn_chunk.h"
 
+#include <algorithm>
 #include <type_traits>
 
 #include "chunk.cuh"
@@ -240,11 +241,9 @@ __device__ __forceinline__ bool find_part(const Walk& w, uint32_t L, uint32_t sl
 
 // The slot of the part of a given rank by length, of up to 32 sequences, a lane for each;
 // -1: there is none.  Whole segments come first, in the order of the row, then what is
-// left of each sequence (STATE: only of those that are cut).  All lanes of a warp.
-// Packed sequences start in this order, as the longest one ends the launch: 24 sequences
-// of 1 to 2000 tokens with 12 heads take 75 us, in the order of the row 94.  More than 32
-// even out by themselves.
-template <bool STATE>
+// left of each sequence.  All lanes of a warp.  Packed sequences start in this order, as
+// the longest one ends the launch: 24 sequences of 1 to 2000 tokens with 12 heads take
+// 75 us, in the order of the row 94.  More than 32 start in the order of the row.
 __device__ __forceinline__ int64_t by_length(const Walk& w, uint32_t L, int rank) {
     const int lane = threadIdx.x % 32;
     const bool real = lane < w.nseq;
@@ -258,7 +257,7 @@ __device__ __forceinline__ int64_t by_length(const Walk& w, uint32_t L, int rank
         if (lane >= o) upto += y;
     }
     const int whole = __shfl_sync(0xffffffffu, upto, 31);
-    const bool has = real && (STATE ? left > 0 && full > 0 : left > 0 || all == 0);
+    const bool has = real && (left > 0 || all == 0);
     const int key = has ? left : -1;
     int longer = 0;
     #pragma unroll 1
@@ -270,6 +269,32 @@ __device__ __forceinline__ int64_t by_length(const Walk& w, uint32_t L, int rank
     const uint32_t found = __ballot_sync(0xffffffffu, mine);
     const int64_t slot = int64_t(uint32_t(s.slot) / L) + lane + (rank < whole ? rank - (upto - full) : full);
     return found ? __shfl_sync(0xffffffffu, slot, __ffs(found) - 1) : -1;
+}
+
+// The slot of the part of a given rank, in the order of the row, among those of sequences
+// that are cut; -1: there is none.  32 sequences at a time, a lane for each.  All lanes of
+// a warp.
+__device__ __forceinline__ int64_t cut_part(const Walk& w, uint32_t L, int rank) {
+    const int lane = threadIdx.x % 32;
+    #pragma unroll 1
+    for (int i0 = 0; i0 < w.nseq; i0 += 32) {
+        const bool real = i0 + lane < w.nseq;
+        const Seq s = locate(w.offsets, w.T, real ? i0 + lane : 0);
+        const uint32_t all = real ? uint32_t((s.len + kChunk - 1) / kChunk) : 0;
+        const int parts = all > L ? int((all + L - 1) / L) : 0;
+        int upto = parts;  // of this and the sequences before
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const int before = upto - parts;
+        const uint32_t found = __ballot_sync(0xffffffffu, upto > rank && before <= rank);
+        const int64_t slot = int64_t(uint32_t(s.slot) / L) + i0 + lane + (rank - before);
+        if (found) return __shfl_sync(0xffffffffu, slot, __ffs(found) - 1);
+        rank -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return -1;
 }
 
 // STATE: only the state at the end of a segment (from zero, or from the initial state);
@@ -311,7 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         Part* found = reinterpret_cast<Part*>(sm + C::oO);
         bool* any = reinterpret_cast<bool*>(found + 1);
         if (warp == 0) {
-            const int64_t at = a.longest_first ? by_length<STATE>(wk, uint32_t(a.seg_chunks), slot) : slot;
+            int64_t at = slot;
+            if (STATE ? a.few_cut : a.longest_first)
+                at = STATE ? cut_part(wk, uint32_t(a.seg_chunks), slot) : by_length(wk, uint32_t(a.seg_chunks), slot);
             live = at >= 0 && find_part(wk, uint32_t(a.seg_chunks), uint32_t(at), &p);
             p.slot = at;
             if (lane == 0) *found = p, *any = live;
@@ -982,9 +1009,9 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
     const int64_t nseq = a.p[0].w.nseq;
     dim3 grid(unsigned(a.segments), unsigned(a.p[0].w.H), unsigned(n));
     if (states) {
-        // by length, whole segments and what is left of cut sequences come first: at most
-        // one of the latter for one of the former
-        if (a.longest_first && 2 * (a.segments - nseq) < a.segments) grid.x = unsigned(2 * (a.segments - nseq));
+        // the parts of cut sequences alone: whole segments, and at most one that is shorter
+        // for each of these
+        if (a.few_cut && 2 * (a.segments - nseq) < a.segments) grid.x = unsigned(2 * (a.segments - nseq));
         linattn_walk_kernel<DT, DK, DV, true><<<grid, kThreads, ends, st>>>(a);
         if (a.most <= a.join) return cudaGetLastError();
         constexpr int size = DK * DV;
@@ -1009,11 +1036,20 @@ cudaError_t launch(const Passes& a, int n, bool states, cudaStream_t st) {
 // bf16 128 x 128, 16384 tokens, forward: 6 rows uncut 457 us, in 24 segments 62; 24 rows
 // 459, in 6 134; 60 rows 461, in 5 298.  Training step's gradients: 16 rows 463, in 3
 // 224, in 8 244.  2048 tokens: 36 rows forward 71, in 3 51; gradients 83, in 2 100.
-// Packed rows are taken at their mean length, as the host does not know their offsets; 9
-// to 32 sequences that this leaves uncut are cut at four times that where the estimate is
-// above 140 us, which costs a launch of CTAs with nothing to do where none is as long: 12
-// heads of 128 x 128, bf16, 60000 tokens among 31 of 178: 324 us, uncut 1645; 32 of 2048:
-// 227, uncut 214.
+// Packed rows are taken at their mean length, as the host does not know their offsets.
+// Where that leaves them uncut and the estimate is above 140 us, sequences of more than
+// twice the mean that would take longer by themselves than the estimate (its half for the
+// gradients' three walks) are cut into pieces of that length.  It costs a launch of CTAs
+// with nothing to do where no sequence is as long.  12 heads of 128 x 128, bf16, forward
+// (gradients), one prompt of 60000 tokens among others of 178:
+//   of 8 535 us (570), uncut 1644 (1650); 16 355 (570), with pieces of half the length 310;
+//   32 311 (610), half 350, uncut 1645 (1644); 33 357 (710), uncut 1671 (1764); 64 452
+//   (890), uncut 1706 (1885); 200 758 (1630), uncut 1859 (2403)
+// equal prompts: 8 of 8192 tokens 265 (508), uncut 258 (502); 33 of 2048 224 (489), uncut
+//   212 (478); 1000 of 178 1180 (3550), uncut 1148 (3545); 32 of uneven lengths up to 6000
+//   tokens 211 (463), half 272
+// Under 140 us such a launch weighs more (24 prompts in 16411 tokens take 61 us), and one
+// long prompt among short ones is one chain.
 //
 // The walks' CTAs join up to three segments themselves (8 rows of 4096, 6 heads of 128,
 // three segments: 99 us with the inputs from memory, against 107 with the join's launch;
@@ -1029,6 +1065,7 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
     s->count = nseq;
     s->join = 0;
     s->most = 1;
+    s->few_cut = false;
     s->by_length = nseq <= kSorted;
     if (rows == 0) return;
     // chunks of a sequence of mean length, at least one: there may be fewer tokens than sequences
@@ -1046,13 +1083,15 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
             best = m;
         }
     }
-    const bool uneven = best == 1 && B == 1 && nseq > 8 && nseq <= kSorted && cost >= 2000 && most > 4 * n;
-    if (best == 1 && !uneven) return;
-    s->chunks = uneven ? 4 * n : (n + best - 1) / best;
+    // an uneven queue's pieces: as long by themselves as the estimate, for several walks half
+    const int64_t piece = std::max(2 * n, cost / ((f16 ? 26 : 20) * (walks > 1 ? 2 : 1)));
+    s->few_cut = best == 1 && B == 1 && nseq > 1 && cost >= 2000 && most > piece;
+    if (best == 1 && !s->few_cut) return;
+    s->chunks = s->few_cut ? piece : (n + best - 1) / best;
     s->count = slots / s->chunks + nseq;
-    s->join = uneven ? 9 : best <= 3 ? 3 : 0;
+    s->join = s->few_cut ? 9 : best <= 3 ? 3 : 0;
     s->most = (most + s->chunks - 1) / s->chunks;
-    s->by_length = best == 1 && nseq <= kSorted;
+    s->by_length = s->few_cut && nseq <= kSorted;
 }
 
 cudaError_t launch_linattn(const Passes& a, int n, bool states, int dt, int dk, int dv, cudaStream_t st) {

@@ -23,18 +23,20 @@ struct Passes {
     int64_t segments;
     int join;            // a walk's CTAs join the states of sequences of up to so many segments themselves
     int64_t most;        // segments that a sequence may have: past join, the join is launched
+    bool few_cut;        // few sequences are cut: their end states' walk looks for those
     bool longest_first;  // packed sequences (up to kSorted), in the order of their lengths
     int* err;
 };
 
 // Chunks of a segment, and how many segment slots there are (nseq: no sequence is cut),
 // for `walks` walks at once.  join: the most segments of a sequence whose states the
-// walks' CTAs add up themselves; most: segments that a sequence may have.  by_length:
-// packed sequences in the order of their lengths.
+// walks' CTAs add up themselves; most: segments that a sequence may have.  few_cut: only
+// the long sequences of a packed row are.  by_length: packed sequences in the order of
+// their lengths.
 struct Segments {
     int64_t chunks, count, most;
     int join;
-    bool by_length;
+    bool few_cut, by_length;
 };
 void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t heads, int walks, int dt, int sms);
 

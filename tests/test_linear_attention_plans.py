@@ -44,6 +44,17 @@ def test_rows_of_fewer_tokens_than_sequences():
     assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("nseq", [5, 6, 7, 8, 9, 16, 31, 32, 33, 34, 64, 100, 200])
+def test_long_prompts_of_any_queue_are_cut(nseq, dtype):
+    """One prompt of 60000 tokens beside any number of short ones: pieces of it have states
+    in scratch, in both directions."""
+    for Dk, Dv in ((64, 64), (128, 64), (128, 128)):
+        for Hv in (12, 24):
+            for backward in (0, 1):
+                assert scratch_bytes(1, 60000 + 178 * (nseq - 1), Hv, Hv, nseq, backward, Dk, Dv, dtype) > 0, (Dk, Dv, Hv, backward)
+
+
 def offsets_of(lens):
     off = torch.zeros(len(lens) + 1, dtype=torch.int32)
     off[1:] = torch.cumsum(torch.tensor(lens), 0)
@@ -142,6 +153,15 @@ def test_rows_cut_by_their_mean_length_with_a_long_prompt(lens, Hk, Hv, dt):
     """One prompt of a queue has most of the segments, dozens of them.  States: (12 + up to
     880 chunks) 2^-23."""
     queue_against_definition(lens, Hk, Hv, 64, dt, 1.1e-4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", U)
+@pytest.mark.parametrize("lens", [[178] * 3 + [60000] + [100, 0, 178, 64], [178] * 30 + [0, 50000] + [77] * 3 + [15000],
+                                  [40] * 31 + [0] * 33 + [35000] + [8192] * 2 + [200] * 20])
+def test_queues_with_long_prompts(lens, dt):
+    """8, 36 and 87 prompts, the long ones cut.  States: (12 + up to 938 chunks) 2^-23."""
+    queue_against_definition(lens, 6, 12, 64, dt, 1.2e-4)
 
 
 if __name__ == "__main__":
