@@ -492,6 +492,13 @@ def _dense(t, what: str, dtype, shape, dev=None) -> int:
     return t.data_ptr()
 
 
+def _slots_of(state) -> int:
+    """How many states a step's pool holds."""
+    if state is None or state.dim() != 4:
+        raise ValueError("state must be float32 [slots, Hv, Dk, Dv]")
+    return state.shape[0]
+
+
 def _on(stream):
     """Allocations made inside belong to the stream that the call runs on."""
     import torch
@@ -604,7 +611,7 @@ class DeltaRule:
             with _on(stream):
                 return self.step(q, k, v, g, beta, state, state_out, slots, scale)
         a = self._args(q, k, v, g, beta, None, scale)
-        shape = (state.shape[0], v.shape[2], self.Dk, self.Dv)
+        shape = (_slots_of(state), v.shape[2], self.Dk, self.Dv)
         sin = _dense(state, "state", torch.float32, shape, q.get_device())
         sout = sin if state_out is None else _dense(state_out, "state_out", torch.float32, shape, q.get_device())
         sl = _dense(slots, "slots", torch.int32, (q.shape[0],), q.get_device())
@@ -792,7 +799,7 @@ class LinearAttention:
             with _on(stream):
                 return self.step(q, k, v, decay, state, state_out, slots, scale)
         a = self._args(q, k, v, decay, None, scale)
-        shape, dev = (state.shape[0], v.shape[2], self.Dk, self.Dv), q.get_device()
+        shape, dev = (_slots_of(state), v.shape[2], self.Dk, self.Dv), q.get_device()
         sin = _dense(state, "state", torch.float32, shape, dev)
         sout = sin if state_out is None else _dense(state_out, "state_out", torch.float32, shape, dev)
         sl = _dense(slots, "slots", torch.int32, (q.shape[0],), dev)
