@@ -951,8 +951,9 @@ cudaError_t launch(const GradArgs& a, cudaStream_t st) {
     delta_grad_kernel<DT, DK, DV><<<unsigned(items < most ? items : most), GradCfg<DK, DV>::THREADS, sg, st>>>(a);
     if (a.dqh) {
         const int64_t n = (a.d.B * a.d.T * a.d.Hk * (DK / 8) * 2 + 255) / 256;
-        head_sum_kernel<DT><<<unsigned(n < 152 * 32 ? n : 152 * 32), 256, 0, st>>>(a.dqh, a.dkh, a.dq, a.dk, a.d.B * a.d.T,
-                                                                                  a.d.T, a.d.Hk, a.d.group, DK, nullptr, 0);
+        const int64_t grid = int64_t(a.sms) * 32;
+        head_sum_kernel<DT><<<unsigned(n < grid ? n : grid), 256, 0, st>>>(a.dqh, a.dkh, a.dq, a.dk, a.d.B * a.d.T, a.d.T,
+                                                                           a.d.Hk, a.d.group, DK, nullptr, 0);
     }
     return cudaGetLastError();
 }

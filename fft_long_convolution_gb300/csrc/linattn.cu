@@ -471,8 +471,8 @@ extern "C" fftconv_status_t fftconv_linattn_backward(fftconv_linattn_t p, const 
         if (r == cudaSuccess) r = launch_linattn(a, same ? 3 : 2, false, p->dtype, p->Dv, p->Dk, st);
         if (r == cudaSuccess && !same) r = launch_linattn(only_dv, 1, false, p->dtype, p->Dk, p->Dv, st);
         if (r == cudaSuccess && shared) {
-            const int64_t n = (c.B * c.T * c.Hk * (p->Dk / 8) * 2 + 255) / 256;
-            const unsigned grid = unsigned(n < 152 * 32 ? n : 152 * 32);
+            const int64_t n = (c.B * c.T * c.Hk * (p->Dk / 8) * 2 + 255) / 256, most = int64_t(p->num_sms) * 32;
+            const unsigned grid = unsigned(n < most ? n : most);
             auto f = p->dtype == FFTCONV_F16 ? head_sum_kernel<0> : head_sum_kernel<1>;
             f<<<grid, 256, 0, st>>>(dq32, dk32, vdq, vdk, c.B * c.T, c.T, c.Hk, c.group, p->Dk, args->offsets,
                                     c.nseq);
