@@ -15,12 +15,13 @@
 // w V, is taken in 16-bit parts: three for bf16 (24 bits) and two for fp16 (22 bits)
 // where the state at the end of the walk is an output, so that it keeps float32's
 // digits; two for bf16 (17 bits) where S only feeds O.  S and P enter O as one 16-bit
-// value each: their roundings are as large as O's own and fall on the two terms of its
-// sum, so that O is off by about sqrt(2) times its rounding alone at most (two parts
-// each, built and measured, gave the rounding alone and took 1.3 times as long).  In
-// fp16 a row of each of them is first scaled by a power of two to a largest value in
-// [2^14, 2^15), and the accumulator scaled back: neither small values nor large states
-// leave fp16's range.
+// value each: their roundings fall on the two terms of O's sum, by half a step of each
+// factor's size.  Where the terms do not cancel O is off by about sqrt(2) times its own
+// rounding alone; what is left of terms that do is off by their roundings all the same
+// (two parts each, built and measured, gave O's rounding alone and took 1.3 times as
+// long).  In fp16 a row of each of them is first scaled by a power of two to a largest
+// value in [2^14, 2^15), and the accumulator scaled back: neither small values nor large
+// states leave fp16's range.
 //
 // One CTA per sequence (or segment of one) and value head, roles by warp, handing
 // over through mbarriers:

@@ -632,10 +632,19 @@ fftconv_status_t fftconv_qknorm_backward(const fftconv_qknorm_args_t *args, fftc
  * at least 22 bits (final states and the initial states' gradients: relative error
  * about 1e-6).  In fp16 a token's weight in its chunk of 64, l^i with i tokens behind
  * it there, is held to 2^-25: what is left of a token is off by that part of what it
- * was, however much it has decayed since.  In whole sequences the state and the
- * scores enter the outputs, and their likes the gradients, as one value of the plan
- * dtype each, scaled so that fp16 neither overflows nor loses small ones; with the
- * result's own rounding an output is off by about sqrt(2) times that rounding alone.
+ * was, however much it has decayed since; a feature of V (of d_o, for the initial
+ * states' gradients) all of whose values in a chunk are below 2^-17 feeds a state to
+ * 2^-39 a token.  In bf16 a state that only feeds outputs takes 17 bits of what feeds it.
+ * In whole sequences the state and the scores P_ij = l^(i-j) q_i.k_j enter the outputs,
+ * and their likes the gradients, as one value of the plan dtype each, scaled so that fp16
+ * neither overflows nor loses small ones.  With u = 2^-8 (bf16) or 2^-11 (fp16), half a
+ * step, and S the state before the token's chunk (whose first token is s), o_i is off by up to
+ *   u (|o_i| + scale l^(i-s+1) sum |S| |q_i| + scale sum_j |P_ij| |v_j|)
+ * and little more.  Where these terms do not cancel that is about sqrt(2) times the last
+ * rounding alone in root mean square.  Where they do it is more of what is left: a token
+ * that overwrites what the state holds under its key, so that o is 1/100 of either term,
+ * may be off by a quarter of itself in bf16.  The recurrent form has the last rounding
+ * alone.
  * A NaN or an infinity in a token of a whole sequence may reach every output of its
  * chunk (64 tokens, counted from the sequence's start), those before it included,
  * and every later one of its sequence and head (gradients: every earlier one too);
