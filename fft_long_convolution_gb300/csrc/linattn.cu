@@ -194,7 +194,7 @@ struct Scratch {
     size_t s, r, q, k, total;  // byte offsets, and the size
     Scratch(const fftconv_linattn_s* p, int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t nseq, bool backward) {
         plan_segments(&seg, B, T, nseq, Hv, backward ? 3 : 1, p->dtype, p->num_sms);
-        const size_t n = seg.count > nseq ? up256(state_bytes(p, seg.count, Hv)) : 0;
+        const size_t n = up256(state_bytes(p, seg.states, Hv));
         const size_t h = backward && Hk < Hv ? up256(size_t(B) * T * Hv * p->Dk * 4) : 0;
         s = 0;
         r = n;

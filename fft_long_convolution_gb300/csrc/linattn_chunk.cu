@@ -210,7 +210,7 @@ struct Ring {
 struct Part {
     Seq s;
     int i;         // sequence
-    int64_t slot;  // segment slot
+    int64_t state;  // where the state at its end is, unless it is the walk's last one
     int64_t tok0;  // its first token in the row
     int64_t left;  // tokens from there to the sequence's end
     int n;         // chunks
@@ -235,6 +235,7 @@ __device__ __forceinline__ bool find_part(const Walk& w, uint32_t L, uint32_t sl
     p->n = int(high ? all - from : L);
     p->count = int((all + L - 1) / L);
     p->before = int(w.reverse ? p->count - 1 - seg : seg);
+    p->state = int64_t(uint32_t(p->s.slot) / L) + seg - (w.reverse ? 1 : 0);
     p->tok0 = p->s.start + from * kChunk;
     p->left = p->s.len - from * kChunk;
     return true;
@@ -341,7 +342,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             if (STATE ? a.few_cut : a.longest_first)
                 at = STATE ? cut_part(wk, uint32_t(a.seg_chunks), slot) : by_length(wk, uint32_t(a.seg_chunks), slot);
             live = at >= 0 && find_part(wk, uint32_t(a.seg_chunks), uint32_t(at), &p);
-            p.slot = at;
             if (lane == 0) *found = p, *any = live;
         }
         __syncthreads();
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
     }
     if (!live || (STATE && p.last && (p.first || !wk.state_out))) return;
     const int n = p.n;
-    const int64_t hs = int64_t(p.i) * wk.H + h, gs = p.slot * wk.H + h;
+    const int64_t hs = int64_t(p.i) * wk.H + h, gs = p.state * wk.H + h;
     const float* sin = wk.state_in ? wk.state_in + hs * DK * DV : nullptr;
     // what the walk's segment before left, and the way to those before it
     const int64_t back = (reverse ? 1 : -1) * int64_t(wk.H) * DK * DV;
@@ -971,8 +971,8 @@ __global__ void __launch_bounds__(256) linattn_join_kernel(const __grid_constant
     const Seq s = locate(w.offsets, w.T, i);
     const int64_t all = (s.len + kChunk - 1) / kChunk, nseg = (all + a.seg_chunks - 1) / a.seg_chunks;
     if (nseg <= a.join || nseg < (w.state_out ? 2 : 3)) return;
-    const int64_t g0 = s.slot / a.seg_chunks + i, step = (w.reverse ? -1 : 1) * int64_t(w.H) * size;
-    float4* at = reinterpret_cast<float4*>(x.seg_state + ((g0 + (w.reverse ? nseg - 1 : 0)) * w.H + h) * size +
+    const int64_t g0 = s.slot / a.seg_chunks, step = (w.reverse ? -1 : 1) * int64_t(w.H) * size;
+    float4* at = reinterpret_cast<float4*>(x.seg_state + ((g0 + (w.reverse ? nseg - 2 : 0)) * w.H + h) * size +
                                            (blockIdx.x % chunks) * 1024 + threadIdx.x * 4);
     const float g = head_decay(w.decay, h);
     const Decay l = decay_over(g, float(a.seg_chunks * kChunk));
@@ -1064,6 +1064,7 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
     const int64_t slots = chunk_slots(B, T, nseq), rows = nseq * heads;
     s->chunks = slots + 1;
     s->count = nseq;
+    s->states = 0;
     s->join = 0;
     s->most = 1;
     s->few_cut = false;
@@ -1089,7 +1090,8 @@ void plan_segments(Segments* s, int64_t B, int64_t T, int64_t nseq, int64_t head
     s->few_cut = best == 1 && B == 1 && nseq > 1 && cost >= 2000 && most > piece;
     if (best == 1 && !s->few_cut) return;
     s->chunks = s->few_cut ? piece : (n + best - 1) / best;
-    s->count = slots / s->chunks + nseq;
+    s->states = slots / s->chunks;
+    s->count = s->states + nseq;
     s->join = s->few_cut ? 9 : best <= 3 ? 3 : 0;
     s->most = (most + s->chunks - 1) / s->chunks;
     s->by_length = s->few_cut && nseq <= kSorted;

@@ -6,8 +6,10 @@
 namespace fftconv {
 
 // A walk over sequences (linattn.h), its tensors as boxes of 64 tokens x 64 features,
-// and where the segments' states are: float32 [segment slot][H][DK][DV] of the walk
-// that formed them; they are read as w.turned says.
+// and where the segments' states are: float32 [state][H][DK][DV] of the walk that formed
+// them; they are read as w.turned says.  A sequence of n segments has n - 1 of them, in
+// the order of time, from its first chunk slot / seg_chunks on: as sequences' chunk slots
+// do not meet, neither do these.
 struct Pass {
     CUtensorMap mq, mk, mv, mo;
     Walk w;
@@ -28,13 +30,13 @@ struct Passes {
     int* err;
 };
 
-// Chunks of a segment, and how many segment slots there are (nseq: no sequence is cut),
-// for `walks` walks at once.  join: the most segments of a sequence whose states the
+// Chunks of a segment, how many segment slots there are (nseq: no sequence is cut) and
+// states at segments' ends, for `walks` walks at once.  join: the most segments of a sequence whose states the
 // walks' CTAs add up themselves; most: segments that a sequence may have.  few_cut: only
 // the long sequences of a packed row are.  by_length: packed sequences in the order of
 // their lengths.
 struct Segments {
-    int64_t chunks, count, most;
+    int64_t chunks, count, states, most;
     int join;
     bool few_cut, by_length;
 };

@@ -55,6 +55,14 @@ def test_long_prompts_of_any_queue_are_cut(nseq, dtype):
                 assert scratch_bytes(1, 60000 + 178 * (nseq - 1), Hv, Hv, nseq, backward, Dk, Dv, dtype) > 0, (Dk, Dv, Hv, backward)
 
 
+@pytest.mark.parametrize("nseq", [33, 200, 1000, 10000])
+def test_scratch_is_for_the_long_prompts(nseq):
+    """Pieces' states, not states of every sequence."""
+    state = 12 * 128 * 128 * 4
+    for backward in (0, 1):
+        assert 0 < scratch_bytes(1, 60000 + 178 * (nseq - 1), 12, 12, nseq, backward, 128, 128) < 2 * 24 * state
+
+
 def offsets_of(lens):
     off = torch.zeros(len(lens) + 1, dtype=torch.int32)
     off[1:] = torch.cumsum(torch.tensor(lens), 0)
@@ -153,6 +161,37 @@ def test_rows_cut_by_their_mean_length_with_a_long_prompt(lens, Hk, Hv, dt):
     """One prompt of a queue has most of the segments, dozens of them.  States: (12 + up to
     880 chunks) 2^-23."""
     queue_against_definition(lens, Hk, Hv, 64, dt, 1.1e-4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,B,Hv,D", [(None, 2, 2, 64), (None, 1, 6, 128), ([64] * 5 + [9000, 0, 6000], 1, 1, 128), ([6400], 1, 2, 64),
+                                         ([178] * 3 + [60000] + [100, 0, 178, 64], 1, 12, 64), ([128] * 40 + [64000], 1, 12, 128),
+                                         ([25600] + [64] * 40, 1, 12, 128)])
+def test_scratch_is_not_left(lens, B, Hv, D):
+    """Rows and queues that are cut: nothing before and behind the scratch is written."""
+    dt = torch.bfloat16
+    T, n, off = (sum(lens), len(lens), offsets_of(lens).cuda()) if lens else (6401, B, None)
+    q, k, v, decay = (x.cuda() for x in attention_inputs(B, T, Hv, Hv, D, D, dt, seed=n))
+    plan = F.LinearAttention(D, D, dt)
+    want = [*plan.forward(q, k, v, decay, offsets=off), *plan.backward(v, q, k, v, decay, offsets=off)[:3]]
+    L, a = F.lib(), plan._args(q, k, v, decay, off, None)
+    got = [torch.empty_like(x) for x in want]
+    vo, _, *vg = (F.View(*F._strides(x, "x", dt, x.shape)) if x.dtype == dt else None for x in got)
+    vv = F.View(*F._strides(v, "v", dt, v.shape))
+    stream = torch.cuda.current_stream().cuda_stream
+    needs = [L.fftconv_linattn_scratch_bytes(plan._h, B, T, Hv, Hv, n, backward) for backward in (0, 1)]
+    assert max(needs) > 0
+    for backward, need in enumerate(needs):
+        hold = torch.full((need + 2 * 65536,), 7, dtype=torch.uint8, device="cuda")
+        at = hold.data_ptr() + 65536
+        if backward:
+            status = L.fftconv_linattn_backward(plan._h, ctypes.byref(a), None, vv, None, *vg, None, at, need, stream)
+        else:
+            status = L.fftconv_linattn_forward(plan._h, ctypes.byref(a), None, vo, got[1].data_ptr(), at, need, stream)
+        assert status == 0
+        assert bool((hold[:65536] == 7).all()) and bool((hold[65536 + need:] == 7).all())
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert plan.device_status() == 0
 
 
 @pytest.mark.gpu
