@@ -80,8 +80,10 @@ __device__ __forceinline__ void st16x128b_x4(uint32_t taddr, const uint32_t (&r)
 // that wait leave the issue slots to those that work.  Gives up after about a second,
 // or when another role has (*fail set).  Each lane gets an answer of its own from a poll,
 // so every one is voted on: the warp goes on as a whole, to instructions that ask for all
-// its lanes, or rests as a whole.  The first poll nearly always suffices (it may suspend
-// the warp for kWaitHintNs); what follows it is kept out of the roles' loops.
+// its lanes, or rests as a whole.  Barriers that are waited for together share a vote
+// (each by itself, prompts of uneven length in fp16 took 2 to 4 % longer).  The first poll
+// nearly always suffices (it may suspend the warp for kWaitHintNs); what follows it is kept
+// out of the roles' loops.
 __device__ __forceinline__ bool poll(uint32_t addr, uint32_t parity) {
     uint32_t over;
     asm volatile(
@@ -101,10 +103,27 @@ __device__ __noinline__ bool rest_on(uint32_t addr, uint32_t parity, volatile in
     return false;
 }
 
-__device__ __forceinline__ bool rest(uint64_t* bar, uint32_t parity, volatile int* fail) {
-    const uint32_t addr = smem_u32(bar);
-    if (__builtin_expect(__all_sync(0xffffffffu, poll(addr, parity)), 1)) return true;
-    return rest_on(addr, parity, fail);
+struct Phase {
+    uint64_t* bar;
+    uint32_t parity;  // of the phase; that before a barrier's first phase counts as over
+    __device__ __forceinline__ uint32_t addr() const { return smem_u32(bar); }
+};
+
+__device__ __forceinline__ bool rest(volatile int* fail, const Phase& a) {
+    if (__builtin_expect(__all_sync(0xffffffffu, poll(a.addr(), a.parity)), 1)) return true;
+    return rest_on(a.addr(), a.parity, fail);
+}
+
+__device__ __forceinline__ bool rest(volatile int* fail, const Phase& a, const Phase& b) {
+    const bool x = poll(a.addr(), a.parity), y = poll(b.addr(), b.parity);
+    if (__builtin_expect(__all_sync(0xffffffffu, x && y), 1)) return true;
+    return rest_on(a.addr(), a.parity, fail) && rest_on(b.addr(), b.parity, fail);
+}
+
+__device__ __forceinline__ bool rest(volatile int* fail, const Phase& a, const Phase& b, const Phase& c) {
+    const bool x = poll(a.addr(), a.parity), y = poll(b.addr(), b.parity), z = poll(c.addr(), c.parity);
+    if (__builtin_expect(__all_sync(0xffffffffu, x && y && z), 1)) return true;
+    return rest_on(a.addr(), a.parity, fail) && rest_on(b.addr(), b.parity, fail) && rest_on(c.addr(), c.parity, fail);
 }
 
 // Pairs of 16-bit values: products, fused products, a b - c, and the larger sizes.
@@ -410,6 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         __syncwarp();
         if (lane == 0) arrive(bar + b);
     };
+    // a barrier's phases from 0 on; the one before them is over from the start
+    auto at = [&](int b, uint32_t phase) { return Phase{bar + b, phase & 1}; };
+    auto wait = [&](const auto&... phases) { return rest(fail, phases...); };
     // step c's chunk, and its tokens
     auto chunk = [&](int c) { return reverse ? n - 1 - c : c; };
     const int all = int(p.left < int64_t(n) * kChunk ? p.left : int64_t(n) * kChunk);
@@ -469,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         Ring<C::NST> full;
         // Three parts: a warp half of the tokens of every step.
         auto weigh_fine = [&](int e) {
-            if (!rest(bar + kFull + full.st, full.parity, fail)) return false;
+            if (!wait(at(kFull + full.st, full.parity))) return false;
             tc::fence_after();
             const float* wt = tab + C::tW + (tokens(e) < kChunk ? 64 : 0) + 32 * side + 2 * (lane & 3);
             const uint32_t to = w_at + C::w(true, e) + 16 * side;
@@ -499,13 +521,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         // and leaves an error that 16 bits hold exactly, which a fused multiply-add gives:
         // lo = v wm + (v wh - hi).  A warp all tokens of every other step, a step ahead.
         auto weigh = [&](int e) {
-            if (!rest(bar + kFull + full.st, full.parity, fail)) return false;
+            const Phase loaded = at(kFull + full.st, full.parity);
+            if (!(DT == 0 ? wait(loaded, at(kSizes + (e & 3), e >> 2)) : wait(loaded))) return false;
             tc::fence_after();
             const float* wt = tab + C::tH + (tokens(e) < kChunk ? 64 : 0) + 2 * (lane & 3);
             const uint32_t to = w_at + C::w(false, e);
             uint32_t sc[2] = {};
             if constexpr (DT == 0) {
-                if (!rest(bar + kSizes + (e & 3), (e >> 2) & 1, fail)) return false;
                 const uint32_t* z = reinterpret_cast<const uint32_t*>(tab + C::tN) + (e & 3) * 128 + 32 * sp + 16 * hf + (lane >> 2);
                 sc[0] = z[0];
                 sc[1] = z[8];
@@ -542,12 +564,12 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
                 float* size = tab + C::tM + (e & 1) * 512 + row;
                 size[quarter * 128] = m;
                 done(kMax + sp);
-                if (!rest(bar + kMax + sp, e & 1, fail)) return false;
+                if (!wait(at(kMax + sp, e))) return false;
                 #pragma unroll
                 for (int j = 1; j < 4; ++j) m = fmaxf(m, size[((quarter + j) & 3) * 128]);
                 sc = row_scale(m);
             }
-            if (e > 0 && !rest(bar + kSqDone, (e - 1) & 1, fail)) return false;
+            if (!wait(at(kSqDone, e - 1))) return false;
             tc::fence_after();
             if (DT == 0 && quarter == 0) tab[C::tS + (e & 1) * 128 + row] = sc.y;
             #pragma unroll
@@ -568,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         };
         // S += KV of step e
         auto add = [&](int e, auto exact) {  // exact: S is an output, else it only feeds O
-            if (!rest(bar + kKvDone + (e & 1), (e >> 1) & 1, fail)) return false;
+            if (!wait(at(kKvDone + (e & 1), e >> 1))) return false;
             tc::fence_after();
             const Decay l = tokens(e) < kChunk ? last : whole;
             const float2 part = make_float2(l.part, l.part), keep = make_float2(l.keep, l.keep);
@@ -640,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         const float s_up = reverse ? wk.s_up * expf(g) : wk.s_up;  // (see the weights)
         Ring<C::NST> full;
         auto sizes = [&](int e) {
-            if (!rest(bar + kFull + full.st, full.parity, fail)) return false;
+            if (!wait(at(kFull + full.st, full.parity))) return false;
             if (!mine) {
                 full.next();
                 done(kSizes + (e & 3));
@@ -676,8 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             for (c = 2; ok && c < n; ++c) ok = sizes(c);
         #pragma unroll 1
         for (; !STATE && ok && c < n; ++c) {
-            ok = rest(bar + kScDone + (c & 1), (c >> 1) & 1, fail);
-            if (ok && c >= 2) ok = rest(bar + kPvDone + (c & 1), ((c - 2) >> 1) & 1, fail);  // the buffer's last P has been used
+            // the scores are there, and the buffer's last P has been used
+            ok = wait(at(kScDone + (c & 1), c >> 1), at(kPvDone + (c & 1), (c - 2) >> 1));
             if (!ok) break;
             tc::fence_after();
             uint8_t* to = sm + C::oP + (c & 1) * kTile + (16 * sp + q) * 128 + r * 4;
@@ -730,8 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         if (o32) o32 += (p.s.row * wk.T + p.tok0) * o32_token + h * DV + f;
         #pragma unroll 1
         for (; !STATE && c < n; ++c) {
-            ok = rest(bar + kPvDone + (c & 1), (c >> 1) & 1, fail);
-            if (ok && !o32 && c > 0) ok = rest(bar + kOFree, (c - 1) & 1, fail);  // the last O has left shared memory
+            const Phase formed = at(kPvDone + (c & 1), c >> 1);
+            ok = o32 ? wait(formed) : wait(formed, at(kOFree, c - 1));  // the last O has left shared memory
             if (!ok) break;
             tc::fence_after();
             if (!mine) {
@@ -815,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             // end; in a packed row they are the next sequence's and are zeroed here
             const bool tail = packed && m < kChunk;  // one chunk at most
             uint8_t* to = sm + st * C::STAGE;
-            if (c >= C::NST && !(ok = rest(bar + kFree + st, ring.parity ^ 1, fail))) break;
+            if (c >= C::NST && !(ok = wait(at(kFree + st, ring.parity ^ 1)))) break;
             uint64_t* full = tail ? bar + kRaw : bar + kFull + st;
             if (elect()) {
                 mbar_expect_tx(full, C::STAGE);
@@ -830,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             }
             __syncwarp();
             if (tail) {
-                if (!(ok = rest(bar + kRaw, 0, fail))) break;
+                if (!(ok = wait(at(kRaw, 0)))) break;
                 for (int f = 0; f < int(C::STAGE / kTile); ++f) fix(to + f * kTile, m);
                 tc::fence_proxy_async();
                 __syncwarp();
@@ -853,9 +875,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
             c = e;
             if (c >= 0) {
                 const int NB = C::nkv(fine);
-                if (STATE) ok = rest(bar + kFull + ring.st, ring.parity, fail);
-                ok = ok && rest(bar + kParts + (c & 1), (c >> 1) & 1, fail);
-                if (ok && c >= NB) ok = rest(bar + kKvRead + ((c - NB) & 1), ((c - NB) >> 1) & 1, fail);
+                const Phase ready = at(kParts + (c & 1), c >> 1), read = at(kKvRead + ((c - NB) & 1), (c - NB) >> 1);
+                ok = STATE ? wait(at(kFull + ring.st, ring.parity), ready, read) : wait(ready, read);
                 if (!ok) break;
                 tc::fence_after();
                 if (elect()) {
@@ -872,9 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
                 ring.next();
             }
             if (STATE || c + 1 >= n) continue;
-            ok = rest(bar + kFull + ahead.st, ahead.parity, fail);
             const int before = c + 1 - C::nx(fine);  // whose O has to be read: the buffer's last
-            if (ok && before >= 0) ok = rest(bar + kORead + (before & 1), (before >> 1) & 1, fail);
+            ok = wait(at(kFull + ahead.st, ahead.parity), at(kORead + (before & 1), before >> 1));
             if (!ok) break;
             tc::fence_after();
             if (elect()) {
@@ -900,8 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         #pragma unroll 1
         for (; c < n; ++c, ring.next()) {
             const uint32_t off = ring.st * C::STAGE;
-            ok = rest(bar + kFull + ring.st, ring.parity, fail) && rest(bar + kSop, c & 1, fail);
-            if (ok && c >= 1) ok = rest(bar + kORead + (~c & 1), ((c - 1) >> 1) & 1, fail);
+            ok = wait(at(kFull + ring.st, ring.parity), at(kSop, c), at(kORead + (~c & 1), (c - 1) >> 1));
             if (!ok) break;
             tc::fence_after();
             if (elect()) {
@@ -912,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
                         tc::mma(tm + C::cOi, tm + C::cS + f * 32 + t * 8, adv(dq, off + f * kTile + t * 32), idO, f + t > 0);
                 tc::commit(bar + kSqDone);
             }
-            if (!(ok = rest(bar + kPReady + (c & 1), (c >> 1) & 1, fail))) break;
+            if (!(ok = wait(at(kPReady + (c & 1), c >> 1)))) break;
             tc::fence_after();
             if (elect()) {
                 #pragma unroll
@@ -929,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_walk_kernel(const __grid_
         // ---------------------------------------------------------------- O -> global
         #pragma unroll 1
         for (; c < n; ++c) {
-            if (!(ok = rest(bar + kOReady, c & 1, fail))) break;
+            if (!(ok = wait(at(kOReady, c)))) break;
             const int m = tokens(c);
             const int64_t t0 = p.tok0 + int64_t(chunk(c)) * kChunk;
             if (!(packed && m < kChunk)) {  // tokens past the tensor's end are not written

@@ -17,10 +17,14 @@ def test_polls_are_voted_on():
     """mbarrier.try_wait answers each lane by itself; .sync.aligned instructions follow."""
     with open(os.path.join(CSRC, "linattn_chunk.cu")) as f:
         text = re.sub(r"//[^\n]*", "", f.read())
-    uses = [m.start() for m in re.finditer(r"(?<!bool )\bpoll\(", text)]
-    assert uses and text.count("try_wait") == 1
-    for at in uses:
-        assert text[:at].endswith("__all_sync(0xffffffffu, "), text[at - 40:at + 40]
+    assert text.count("try_wait") == 1
+    lines = text.split("\n")
+    uses = [i for i, line in enumerate(lines) if re.search(r"(?<!bool )\bpoll\(", line)]
+    assert uses
+    for i in uses:  # voted on at once, or all of a line's answers on the next line
+        names = re.findall(r"(\w+) = poll\(", lines[i])
+        vote = f"__all_sync(0xffffffffu, {' && '.join(names)})" if names else "__all_sync(0xffffffffu, poll("
+        assert vote in lines[i + 1 if names else i], lines[i]
 
 
 @pytest.mark.gpu
