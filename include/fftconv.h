@@ -643,8 +643,8 @@ fftconv_status_t fftconv_qknorm_backward(const fftconv_qknorm_args_t *args, fftc
  * and little more.  Where these terms do not cancel that is about sqrt(2) times the last
  * rounding alone in root mean square.  Where they do it is more of what is left: a token
  * that overwrites what the state holds under its key, so that o is 1/100 of either term,
- * may be off by a quarter of itself in bf16.  The recurrent form has the last rounding
- * alone.
+ * may be off by a quarter of itself in bf16; so may dq and dk where the value heads that
+ * share a key head cancel.  The recurrent form has the last rounding alone.
  * A NaN or an infinity in a token of a whole sequence may reach every output of its
  * chunk (64 tokens, counted from the sequence's start), those before it included,
  * and every later one of its sequence and head (gradients: every earlier one too);
