@@ -203,5 +203,36 @@ def test_queues_with_long_prompts(lens, dt):
     queue_against_definition(lens, 6, 12, 64, dt, 1.2e-4)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hk,Hv,n", [(1, 1, 6), (6, 12, 40)])
+def test_captured_queues_replay_on_other_offsets(Hk, Hv, n):
+    """Segments are planned from the row's size; which prompts are cut is seen on the device."""
+    dt, D, T = torch.bfloat16, 64, 40000
+    q, k, v, decay = (x.cuda() for x in attention_inputs(1, T, Hk, Hv, D, D, dt, seed=n))
+    s0 = states(n, Hv, D, D).cuda()
+    plan = F.LinearAttention(D, D, dt)
+    rest = T - 30000
+    queues = [[T // n] * n, [0] * (n - 1) + [T], [30000] + [rest // (n - 1)] * (n - 1), [rest // (n - 1)] * (n - 1) + [30000], [0] * n]
+    off = offsets_of(queues[0]).cuda()
+
+    def work():
+        o, s = plan.forward(q, k, v, decay, state=s0, offsets=off)
+        return [o, s, *plan.backward(v, q, k, v, decay, state=s0, dstate=s0, offsets=off)]
+
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = work()
+    for lens in queues:
+        off.copy_(offsets_of(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(kept, work()))
+        for x in (kept[0], *kept[2:5]):
+            assert not bool(x[:, sum(lens):].any())
+    assert torch.equal(kept[1], s0) and torch.equal(kept[5], s0) and plan.device_status() == 0
+
+
 if __name__ == "__main__":
     sweep_of_short_rows()
