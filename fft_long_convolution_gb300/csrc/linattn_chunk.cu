@@ -228,13 +228,13 @@ struct Ring {
 // Where a CTA's part of a sequence is.
 struct Part {
     Seq s;
-    int i;         // sequence
-    int64_t state;  // where the state at its end is, unless it is the walk's last one
-    int64_t tok0;  // its first token in the row
-    int64_t left;  // tokens from there to the sequence's end
-    int n;         // chunks
+    int i;              // sequence
+    int64_t state;      // where the state at its end is, unless it is the walk's last one
+    int64_t tok0;       // its first token in the row
+    int64_t left;       // tokens from there to the sequence's end
+    int n;              // chunks
     int count, before;  // segments of the sequence, and those before this one in the walk's order
-    bool first, last;  // in that order
+    bool first, last;   // in that order
 };
 
 __device__ __forceinline__ bool find_part(const Walk& w, uint32_t L, uint32_t slot, Part* p) {
@@ -252,7 +252,7 @@ __device__ __forceinline__ bool find_part(const Walk& w, uint32_t L, uint32_t sl
     p->first = w.reverse ? high : low;
     p->last = w.reverse ? low : high;
     p->n = int(high ? all - from : L);
-    p->count = int((all + L - 1) / L);
+    p->count = int((uint32_t(all) + L - 1) / L);
     p->before = int(w.reverse ? p->count - 1 - seg : seg);
     p->state = int64_t(uint32_t(p->s.slot) / L) + seg - (w.reverse ? 1 : 0);
     p->tok0 = p->s.start + from * kChunk;
